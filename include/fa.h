@@ -152,6 +152,34 @@ FA_API fa_status fa_backward_noalloc(const fa_dims* dims, const void* Q, const v
                                      const void* O, const void* dO, const float* L, void* dQ, void* dK, void* dV,
                                      void* stream);
 
+/* Rotary positions of Q and K, the step before the attention, with one to four
+ * position axes (one for text; time, height and width for images and video).
+ *   bf16 Q, Qo [B, Hq, T, d] and K, Ko [B, Hk, T, d] with the given strides (in
+ *   elements; batch, head, token; channels contiguous).  The inputs may be
+ *   views of a packed projection.  Qo / Ko may be Q / K themselves (same
+ *   strides), and otherwise must not overlap them.
+ *   positions: int32 or int64 (pos_bytes 4 or 8), entry (a, b, t) at
+ *   a * pos_axis_stride + b * pos_batch_stride + t; any value, also negative.
+ *   inv_freq: fp32 [rot / 2], radians per position step, |inv_freq| <= 1 for
+ *   full accuracy (each further factor of two costs one bit of the angle's 64).
+ * Frequency f belongs to the axis whose section holds it (section[0] frequencies
+ * of axis 0, then section[1] of axis 1, ...; the sections add up to rot / 2)
+ * and turns its channel pair by positions[axis][b][t] * inv_freq[f]:
+ *   (x, y) -> (x cos - y sin, y cos + x sin).
+ * Pair f is channels (f, f + rot / 2), or (2 f, 2 f + 1) with interleaved = 1;
+ * channels rot .. d-1 are copied.  inverse = 1 turns back, which is the gradient:
+ * it takes dQo, dKo to dQ, dK.  d is 64 or 128, rot a multiple of 16 up to d.
+ * Pointers are 16-byte aligned and strides multiples of 8 elements.  Hk = 0 (or
+ * Hq = 0) leaves K (or Q) out. */
+typedef struct {
+  int B, Hq, Hk, T, d, rot, axes, interleaved, pos_bytes;
+  int section[4];
+  long long q_stride[3], k_stride[3], qo_stride[3], ko_stride[3];
+  long long pos_axis_stride, pos_batch_stride;
+} fa_rotary_dims;
+FA_API fa_status fa_rotary(const fa_rotary_dims* dims, const void* Q, const void* K, const void* positions,
+                           const float* inv_freq, void* Qo, void* Ko, int inverse, void* stream);
+
 /* Static description of a status code. */
 FA_API const char* fa_status_string(fa_status s);
 

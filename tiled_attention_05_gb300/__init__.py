@@ -9,10 +9,14 @@ Entry points mirror the C ABI:
     fa_backward(Q, K, V, O, dO, L, causal, scale=None, window=0)  -> (dQ, dK, dV)
     fa_backward_workspace_bytes(...), fa_backward_workspace_min_bytes(...), fa_status_string(code),
     fa_last_device_status()
+    fa_rotary(Q, K, positions, inv_freq, ...)                     -> (Qr, Kr)
+    fa_rotary_backward(dQr, dKr, positions, inv_freq, ...)        -> (dQ, dK)
 plus ``FlashAttention`` (a torch.autograd.Function that keeps only Q, K, V, O
-and L for the backward pass) and ``attention`` (its functional form).
+and L for the backward pass) and ``attention`` (its functional form), and
+``rotary`` (multi-axis rotary positions of Q and K, differentiable).
 
-Tensors are CUDA bf16, contiguous, [B, H, T, d]; L is fp32 [B, Hq, Tq].
+Tensors are CUDA bf16, contiguous, [B, H, T, d]; L is fp32 [B, Hq, Tq].  The
+rotary calls also take strided Q and K (views of a packed projection).
 """
 from __future__ import annotations
 
@@ -28,7 +32,7 @@ FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = ran
 
 EXPORTED_SYMBOLS = ("fa_forward", "fa_backward", "fa_backward_stages", "fa_backward_workspace_bytes",
                     "fa_backward_workspace_min_bytes", "fa_backward_noalloc", "fa_status_string",
-                    "fa_last_device_status", "fa_last_launch_count")
+                    "fa_last_device_status", "fa_last_launch_count", "fa_rotary")
 FA_ERR_SCRATCH_TOO_SMALL = 5
 FA_NOALLOC_SCRATCH_BYTES = 32 << 20
 FA_BWD_PRE, FA_BWD_MAIN, FA_BWD_CAST, FA_BWD_ALL = 1, 2, 4, 7
@@ -44,6 +48,13 @@ class FaDims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("Tq", ctypes.c_int),
                 ("Tk", ctypes.c_int), ("d", ctypes.c_int), ("dv", ctypes.c_int), ("causal", ctypes.c_int),
                 ("scale", ctypes.c_float), ("window", ctypes.c_int)]
+
+
+class FaRotaryDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "Hq", "Hk", "T", "d", "rot", "axes", "interleaved", "pos_bytes")] + \
+        [("section", ctypes.c_int * 4)] + \
+        [(n, ctypes.c_longlong * 3) for n in ("q_stride", "k_stride", "qo_stride", "ko_stride")] + \
+        [("pos_axis_stride", ctypes.c_longlong), ("pos_batch_stride", ctypes.c_longlong)]
 
 
 _lock = threading.Lock()
@@ -83,6 +94,8 @@ def load(path: str | None = None):
             lib.fa_last_device_status.restype = ctypes.c_int
             lib.fa_last_launch_count.argtypes = []
             lib.fa_last_launch_count.restype = ctypes.c_int
+            lib.fa_rotary.argtypes = [ctypes.POINTER(FaRotaryDims), vp, vp, vp, vp, vp, vp, ctypes.c_int, vp]
+            lib.fa_rotary.restype = ctypes.c_int
             _lib = lib
     return _lib
 
@@ -260,3 +273,6 @@ class FlashAttention(torch.autograd.Function):
 
 def attention(Q, K, V, causal=False, scale=None, window=0):
     return FlashAttention.apply(Q, K, V, causal, scale, window)
+
+
+from .rotary import fa_rotary, fa_rotary_backward, rotary  # noqa: E402

@@ -218,7 +218,8 @@ const char* fa_status_string(fa_status s) {
       return "invalid argument (null or misaligned pointer, negative size, Hq not a multiple of Hkv, "
              "bad causal flag, window or scale, or workspace too small)";
     case FA_ERR_UNSUPPORTED:
-      return "unsupported shape (d and dv must each be 64 or 128; sizes within the grid limits)";
+      return "unsupported shape (d and dv must each be 64 or 128, rotary channels a multiple of 16; sizes within the "
+             "grid limits)";
     case FA_ERR_CUDA:
       return "CUDA error while encoding tensor maps or launching kernels";
     case FA_ERR_TIMEOUT:
