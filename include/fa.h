@@ -152,6 +152,50 @@ FA_API fa_status fa_backward_noalloc(const fa_dims* dims, const void* Q, const v
                                      const void* O, const void* dO, const float* L, void* dQ, void* dK, void* dV,
                                      void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention with modified scores.  Between the scaled product and the softmax
+ *   x_ij = scale * q_i . k_j
+ *   x_ij = softcap * tanh(x_ij / softcap)            softcap > 0
+ *   x_ij = x_ij - slopes[h] * |i + (Tk - Tq) - j|    slopes given (fp32 [Hq])
+ * in this order; L is the logsumexp of the modified scores.  The masks are those
+ * above (causal, window, ragged ends), or those of a mask plan.  The gradients
+ * go through the cap; the slopes are constants and have none.
+ *
+ * softcap is 0 (none) or between 2^-10 and 2^20.  Slopes may have any sign.  With
+ * slopes, Tq and Tk are at most 2^24 (distances stay exact in fp32).  Everything
+ * else is as for fa_forward / fa_backward: layouts, head sizes, empty rows,
+ * workspace, errors.  Values of K and V at masked places have to be finite (a
+ * masked pair has weight 0, and 0 * NaN is NaN). */
+typedef struct {
+  float softcap;
+  const float* slopes; /* device, [Hq], or NULL */
+  const void* plan;    /* device, written by fa_mask_plan for the same B, Tq, Tk, causal and window; or NULL */
+} fa_scores;
+
+/* A mask plan holds, for one batch of sequences, which keys each row sees, in
+ * the form the kernels walk (per-row key intervals and per-tile ranges).  It
+ * serves every layer, head and direction that has the same B, Tq, Tk, causal
+ * and window; other fields of dims do not matter to it.
+ *   doc_q int32 [B, Tq], doc_k int32 [B, Tk] (both or neither): row i sees key j
+ *     only if doc_q[i] == doc_k[j]; negative ids (and 2^31 - 1) are padding, which
+ *     sees nothing and is not seen.  Any order is served; key documents in
+ *     ascending order (packed rows, padding last) are the fast case.
+ *   prefix int32 [B], or [B, Tq] with prefix_per_row = 1; needs causal and no window: row i
+ *     also sees the keys j < prefix, those after it among them.
+ * With both, a key has to be in the row's document and causal or in the prefix.
+ * The plan buffer has fa_mask_plan_bytes(dims) bytes, 16-byte aligned. */
+FA_API size_t fa_mask_plan_bytes(const fa_dims* dims);
+FA_API fa_status fa_mask_plan(const fa_dims* dims, const int* doc_q, const int* doc_k, const int* prefix,
+                              int prefix_per_row, void* plan, size_t plan_bytes, void* stream);
+
+/* fa_forward and fa_backward_stages with modified scores (scores NULL or all
+ * zero: the same as those calls). */
+FA_API fa_status fa_forward_scored(const fa_dims* dims, const fa_scores* scores, const void* Q, const void* K,
+                                   const void* V, void* O, float* L, void* stream);
+FA_API fa_status fa_backward_scored(const fa_dims* dims, const fa_scores* scores, const void* Q, const void* K,
+                                    const void* V, const void* O, const void* dO, const float* L, void* dQ, void* dK,
+                                    void* dV, void* workspace, size_t workspace_bytes, int stages, void* stream);
+
 /* Rotary positions of Q and K, the step before the attention, with one to four
  * position axes (one for text; time, height and width for images and video).
  *   bf16 Q, Qo [B, Hq, T, d] and K, Ko [B, Hk, T, d] with the given strides (in

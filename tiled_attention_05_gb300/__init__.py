@@ -7,6 +7,8 @@ library cannot be loaded, every entry point raises.
 Entry points mirror the C ABI:
     fa_forward(Q, K, V, causal, scale=None, window=0)            -> (O, L)
     fa_backward(Q, K, V, O, dO, L, causal, scale=None, window=0)  -> (dQ, dK, dV)
+        both also with softcap=, slopes= (score modifications) and mask= (a plan)
+    fa_mask_plan(B, Tq, Tk, causal, doc_q, doc_k, prefix)         -> MaskPlan
     fa_backward_workspace_bytes(...), fa_backward_workspace_min_bytes(...), fa_status_string(code),
     fa_last_device_status()
     fa_rotary(Q, K, positions, inv_freq, ...)                     -> (Qr, Kr)
@@ -20,6 +22,7 @@ rotary calls also take strided Q and K (views of a packed projection).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -32,7 +35,8 @@ FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = ran
 
 EXPORTED_SYMBOLS = ("fa_forward", "fa_backward", "fa_backward_stages", "fa_backward_workspace_bytes",
                     "fa_backward_workspace_min_bytes", "fa_backward_noalloc", "fa_status_string",
-                    "fa_last_device_status", "fa_last_launch_count", "fa_rotary")
+                    "fa_last_device_status", "fa_last_launch_count", "fa_rotary", "fa_mask_plan_bytes", "fa_mask_plan",
+                    "fa_forward_scored", "fa_backward_scored")
 FA_ERR_SCRATCH_TOO_SMALL = 5
 FA_NOALLOC_SCRATCH_BYTES = 32 << 20
 FA_BWD_PRE, FA_BWD_MAIN, FA_BWD_CAST, FA_BWD_ALL = 1, 2, 4, 7
@@ -50,6 +54,10 @@ class FaDims(ctypes.Structure):
                 ("scale", ctypes.c_float), ("window", ctypes.c_int)]
 
 
+class FaScores(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("plan", ctypes.c_void_p)]
+
+
 class FaRotaryDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("B", "Hq", "Hk", "T", "d", "rot", "axes", "interleaved", "pos_bytes")] + \
         [("section", ctypes.c_int * 4)] + \
@@ -57,6 +65,7 @@ class FaRotaryDims(ctypes.Structure):
         [("pos_axis_stride", ctypes.c_longlong), ("pos_batch_stride", ctypes.c_longlong)]
 
 
+_HERE = contextlib.nullcontext()
 _lock = threading.Lock()
 _lib = None
 
@@ -94,6 +103,16 @@ def load(path: str | None = None):
             lib.fa_last_device_status.restype = ctypes.c_int
             lib.fa_last_launch_count.argtypes = []
             lib.fa_last_launch_count.restype = ctypes.c_int
+            sp = ctypes.POINTER(FaScores)
+            lib.fa_mask_plan_bytes.argtypes = [dp]
+            lib.fa_mask_plan_bytes.restype = ctypes.c_size_t
+            lib.fa_mask_plan.argtypes = [dp, vp, vp, vp, ctypes.c_int, vp, ctypes.c_size_t, vp]
+            lib.fa_mask_plan.restype = ctypes.c_int
+            lib.fa_forward_scored.argtypes = [dp, sp, vp, vp, vp, vp, vp, vp]
+            lib.fa_forward_scored.restype = ctypes.c_int
+            lib.fa_backward_scored.argtypes = [dp, sp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t,
+                                               ctypes.c_int, vp]
+            lib.fa_backward_scored.restype = ctypes.c_int
             lib.fa_rotary.argtypes = [ctypes.POINTER(FaRotaryDims), vp, vp, vp, vp, vp, vp, ctypes.c_int, vp]
             lib.fa_rotary.restype = ctypes.c_int
             _lib = lib
@@ -149,6 +168,11 @@ def _stream_ptr(stream=None, device=None) -> int:
     return s.cuda_stream
 
 
+def _on(device):
+    """Makes ``device`` current for a call (nothing to do where it already is)."""
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
 def _raise(code: int, where: str):
     if code != FA_OK:
         raise FAError(code, where)
@@ -164,9 +188,85 @@ def fa_backward_workspace_min_bytes(dims: FaDims) -> int:
     return int(load().fa_backward_workspace_min_bytes(ctypes.byref(dims)))
 
 
-def fa_forward(Q, K, V, causal: bool, scale: float | None = None, O=None, L=None, stream=None, window: int = 0):
+class MaskPlan:
+    """Which keys each row sees, for one batch of sequences (see fa_mask_plan)."""
+
+    def __init__(self, key, buffer):
+        self.key, self.buffer = key, buffer  # (B, Tq, Tk, causal, window), int32 device array
+
+
+def fa_mask_plan(B, Tq, Tk, causal: bool, window: int = 0, doc_q=None, doc_k=None, prefix=None, stream=None) -> MaskPlan:
+    """The mask plan of a batch of sequences, for ``mask=`` of fa_forward,
+    fa_backward and attention; built on the GPU by one small kernel.
+
+    doc_q [B, Tq], doc_k [B, Tk]: int32 document ids; a row sees the keys of its
+    own document.  Negative ids are padding.  prefix: int32 [B] or [B, Tq]; a row
+    also sees the first ``prefix`` keys (causal, without a window).  The plan is
+    valid for any heads, head sizes and scores with the same B, Tq, Tk, causal
+    and window, as long as the ids it was built from hold."""
+    dims = make_dims(B, 1, 1, Tq, Tk, 64, 64, causal, None, window)
+    if (doc_q is None) != (doc_k is None):
+        raise ValueError("doc_q and doc_k go together")
+    if doc_q is None and prefix is None:
+        raise ValueError("a mask plan needs documents or a prefix")
+    if prefix is not None and prefix.dim() not in (1, 2):
+        raise ValueError(f"prefix has shape {tuple(prefix.shape)}, expected ({B},) or ({B}, {Tq})")
+    specs = [] if doc_q is None else [(doc_q, "doc_q", (B, Tq), torch.int32), (doc_k, "doc_k", (B, Tk), torch.int32)]
+    if prefix is not None:
+        specs.append((prefix, "prefix", (B,) if prefix.dim() == 1 else (B, Tq), torch.int32))
+    device = specs[0][0].device
+    _check_all(device, specs)
+    lib = load()
+    nbytes = int(lib.fa_mask_plan_bytes(ctypes.byref(dims)))
+    buffer = torch.empty(max(nbytes // 4, 4), dtype=torch.int32, device=device)
+    if stream is not None:
+        buffer.record_stream(stream)
+    with _on(device):
+        code = lib.fa_mask_plan(ctypes.byref(dims), _ptr(doc_q), _ptr(doc_k), _ptr(prefix),
+                                int(prefix is not None and prefix.dim() == 2), buffer.data_ptr(), nbytes,
+                                _stream_ptr(stream, device))
+    _raise(code, "fa_mask_plan")
+    return MaskPlan(_plan_key(dims), buffer)
+
+
+def _plan_key(dims: FaDims):
+    return (dims.B, dims.Tq, dims.Tk, dims.causal, dims.window)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scores(dims: FaDims, device, softcap, slopes, mask, stream):
+    """The fa_scores of a call (None for an unmodified one), checked."""
+    if slopes is None and mask is None and not softcap:
+        return None
+    if slopes is not None:
+        if slopes.requires_grad:
+            raise ValueError("slopes have no gradient here; detach them")
+        _check_all(device, [(slopes, "slopes", (dims.Hq,), torch.float32)])
+    if mask is not None:
+        if not isinstance(mask, MaskPlan):
+            raise ValueError("mask must be a MaskPlan (see fa_mask_plan)")
+        if mask.key != _plan_key(dims):
+            raise ValueError(f"mask was planned for (B, Tq, Tk, causal, window) = {mask.key}, the call has "
+                             f"{_plan_key(dims)}")
+        if mask.buffer.device != device:
+            raise ValueError(f"mask is on {mask.buffer.device}, expected {device} (all tensors on one GPU)")
+        if stream is not None:
+            mask.buffer.record_stream(stream)
+    return FaScores(float(softcap), _ptr(slopes), None if mask is None else mask.buffer.data_ptr())
+
+
+def fa_forward(Q, K, V, causal: bool, scale: float | None = None, O=None, L=None, stream=None, window: int = 0,
+               softcap: float = 0.0, slopes=None, mask: MaskPlan | None = None):
     """O, L = attention forward.  Optional preallocated O / L are written in place.
-    ``window=W`` (causal only) lets each row see at most its last W keys."""
+    ``window=W`` (causal only) lets each row see at most its last W keys.
+
+    ``softcap=c`` replaces each scaled score x by c tanh(x / c); ``slopes`` (fp32
+    [Hq]) then subtracts slopes[h] |i + Tk - Tq - j|; ``mask`` (a MaskPlan of the
+    same sizes, causal and window) hides other documents' keys and shows a
+    prefix.  The backward takes the same three."""
     dims = _dims_of(Q, K, V, causal, scale, window)
     bf, f32 = torch.bfloat16, torch.float32
     specs = [(Q, "Q", Q.shape, bf), (K, "K", K.shape, bf), (V, "V", V.shape, bf)]
@@ -180,16 +280,19 @@ def fa_forward(Q, K, V, causal: bool, scale: float | None = None, O=None, L=None
     if L is None:
         L = torch.empty(dims.B, dims.Hq, dims.Tq, dtype=f32, device=Q.device)
     lib = load()
-    with torch.cuda.device(Q.device):
-        code = lib.fa_forward(ctypes.byref(dims), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
-                              L.data_ptr(), _stream_ptr(stream, Q.device))
+    scores = _scores(dims, Q.device, softcap, slopes, mask, stream)
+    with _on(Q.device):
+        code = lib.fa_forward_scored(ctypes.byref(dims), scores, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+                                     O.data_ptr(), L.data_ptr(), _stream_ptr(stream, Q.device))
     _raise(code, "fa_forward")
     return O, L
 
 
 def fa_backward(Q, K, V, O, dO, L, causal: bool, scale: float | None = None, dQ=None, dK=None, dV=None,
-                workspace=None, stream=None, stages: int = FA_BWD_ALL, window: int = 0):
-    """dQ, dK, dV = attention backward from the saved O and L.
+                workspace=None, stream=None, stages: int = FA_BWD_ALL, window: int = 0, softcap: float = 0.0,
+                slopes=None, mask: MaskPlan | None = None):
+    """dQ, dK, dV = attention backward from the saved O and L (``softcap``,
+    ``slopes`` and ``mask`` as in the forward).
 
     ``stages`` selects which of the three backward kernels to launch (see
     fa_backward_stages in include/fa.h); the default runs all of them.
@@ -199,16 +302,17 @@ def fa_backward(Q, K, V, O, dO, L, causal: bool, scale: float | None = None, dQ=
     need = fa_backward_workspace_bytes(dims)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=Q.device)
+        if stream is not None:  # freed on return, while the other stream still uses it
+            workspace.record_stream(stream)
     elif not workspace.is_cuda or workspace.device != Q.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous CUDA tensor on {Q.device}")
     nbytes = workspace.numel() * workspace.element_size()
-    args = (ctypes.byref(dims), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(),
-            L.data_ptr(), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), workspace.data_ptr(), nbytes)
-    with torch.cuda.device(Q.device):
-        if stages == FA_BWD_ALL:
-            code = lib.fa_backward(*args, _stream_ptr(stream, Q.device))
-        else:
-            code = lib.fa_backward_stages(*args, int(stages), _stream_ptr(stream, Q.device))
+    scores = _scores(dims, Q.device, softcap, slopes, mask, stream)
+    with _on(Q.device):
+        code = lib.fa_backward_scored(ctypes.byref(dims), scores, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+                                      O.data_ptr(), dO.data_ptr(), L.data_ptr(), dQ.data_ptr(), dK.data_ptr(),
+                                      dV.data_ptr(), workspace.data_ptr(), nbytes, int(stages),
+                                      _stream_ptr(stream, Q.device))
     _raise(code, "fa_backward")
     return dQ, dK, dV
 
@@ -255,24 +359,42 @@ def last_launch_count() -> int:
 
 
 class FlashAttention(torch.autograd.Function):
-    """Autograd wrapper: saves Q, K, V (inputs) plus O and L -- nothing quadratic."""
+    """Autograd wrapper: saves Q, K, V (inputs) plus O and L -- nothing quadratic
+    (and with modified scores the slopes and the mask plan)."""
 
     @staticmethod
-    def forward(ctx, Q, K, V, causal=False, scale=None, window=0):
-        O, L = fa_forward(Q, K, V, causal, scale, window=window)
-        ctx.save_for_backward(Q, K, V, O, L)
-        ctx.causal, ctx.scale, ctx.window = causal, scale, window
+    def forward(ctx, Q, K, V, causal=False, scale=None, window=0, softcap=0.0, slopes=None, mask=None):
+        O, L = fa_forward(Q, K, V, causal, scale, window=window, softcap=softcap, slopes=slopes, mask=mask)
+        plan = None if mask is None else mask.buffer
+        ctx.save_for_backward(*(t for t in (Q, K, V, O, L, slopes, plan) if t is not None))
+        ctx.causal, ctx.scale, ctx.window, ctx.softcap = causal, scale, window, softcap
+        ctx.has_slopes, ctx.plan_key = slopes is not None, None if mask is None else mask.key
         return O
 
     @staticmethod
     def backward(ctx, dO):
-        Q, K, V, O, L = ctx.saved_tensors
-        dQ, dK, dV = fa_backward(Q, K, V, O, dO.contiguous(), L, ctx.causal, ctx.scale, window=ctx.window)
-        return dQ, dK, dV, None, None, None
+        Q, K, V, O, L, *more = ctx.saved_tensors
+        slopes = more.pop(0) if ctx.has_slopes else None
+        mask = None if ctx.plan_key is None else MaskPlan(ctx.plan_key, more[0])
+        dQ, dK, dV = fa_backward(Q, K, V, O, dO.contiguous(), L, ctx.causal, ctx.scale, window=ctx.window,
+                                 softcap=ctx.softcap, slopes=slopes, mask=mask)
+        return dQ, dK, dV, None, None, None, None, None, None
 
 
-def attention(Q, K, V, causal=False, scale=None, window=0):
-    return FlashAttention.apply(Q, K, V, causal, scale, window)
+def attention(Q, K, V, causal=False, scale=None, window=0, softcap=0.0, slopes=None, mask=None, docs=None,
+              prefix=None):
+    """Differentiable attention; ``softcap``, ``slopes`` and ``mask`` as in
+    fa_forward.  ``docs`` (int32 ids [B, T] of rows and keys, or a pair for
+    each) and ``prefix`` plan the mask here, for this call and its backward;
+    a program with several layers plans once (fa_mask_plan) and passes ``mask``."""
+    if docs is not None or prefix is not None:
+        if mask is not None:
+            raise ValueError("mask is a plan already: give docs and prefix to fa_mask_plan")
+        if Q.dim() != 4 or K.dim() != 4:
+            raise ValueError("Q, K, V must be [B, H, T, d]")
+        doc_q, doc_k = docs if isinstance(docs, (tuple, list)) else (docs, docs)
+        mask = fa_mask_plan(Q.shape[0], Q.shape[2], K.shape[2], causal, window, doc_q, doc_k, prefix)
+    return FlashAttention.apply(Q, K, V, causal, scale, window, softcap, slopes, mask)
 
 
 from .rotary import fa_rotary, fa_rotary_backward, rotary  # noqa: E402

@@ -84,6 +84,18 @@ fa_status check_ptr(const void* p, long long elems) {
   return FA_OK;
 }
 
+fa_status check_scores(const fa::Problem& pr, const fa_scores* sc, fa::ScoreMods* m) {
+  if (!sc) return FA_OK;
+  if (sc->softcap != 0.f && !(sc->softcap >= 0x1p-10f && sc->softcap <= 0x1p20f)) return FA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(sc->slopes) & 3u) return FA_ERR_INVALID_ARG;
+  if (!aligned16(sc->plan)) return FA_ERR_INVALID_ARG;
+  if (sc->slopes && (pr.Tq > (1 << 24) || pr.Tk > (1 << 24))) return FA_ERR_UNSUPPORTED;
+  m->softcap = sc->softcap;
+  m->slopes = sc->slopes;
+  m->plan = sc->plan;
+  return FA_OK;
+}
+
 }  // namespace
 
 namespace fa {
@@ -147,9 +159,16 @@ extern "C" {
 
 fa_status fa_forward(const fa_dims* dims, const void* Q, const void* K, const void* V, void* O, float* L,
                      void* stream) {
+  return fa_forward_scored(dims, nullptr, Q, K, V, O, L, stream);
+}
+
+fa_status fa_forward_scored(const fa_dims* dims, const fa_scores* scores, const void* Q, const void* K, const void* V,
+                            void* O, float* L, void* stream) {
   t_last_launches = 0;
   fa::Problem pr;
+  fa::ScoreMods mods;
   fa_status s = check_dims(dims, &pr);
+  if (s == FA_OK) s = check_scores(pr, scores, &mods);
   if (s != FA_OK) return s;
   const long long nq = (long long)pr.B * pr.Hq * pr.Tq * pr.d, nqv = (long long)pr.B * pr.Hq * pr.Tq * pr.dv;
   const long long nk = (long long)pr.B * pr.Hkv * pr.Tk * pr.d, nkv = (long long)pr.B * pr.Hkv * pr.Tk * pr.dv;
@@ -159,7 +178,7 @@ fa_status fa_forward(const fa_dims* dims, const void* Q, const void* K, const vo
   if (nq == 0) return FA_OK;
   if (!fa::device_status_word()) return FA_ERR_CUDA;
   int launches = 0;
-  cudaError_t e = fa::launch_forward(pr, Q, K, V, O, L, static_cast<cudaStream_t>(stream), &launches);
+  cudaError_t e = fa::launch_forward(pr, mods, Q, K, V, O, L, static_cast<cudaStream_t>(stream), &launches);
   t_last_launches = launches;
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
@@ -179,9 +198,17 @@ size_t fa_backward_workspace_min_bytes(const fa_dims* dims) {
 fa_status fa_backward_stages(const fa_dims* dims, const void* Q, const void* K, const void* V, const void* O,
                              const void* dO, const float* L, void* dQ, void* dK, void* dV, void* workspace,
                              size_t workspace_bytes, int stages, void* stream) {
+  return fa_backward_scored(dims, nullptr, Q, K, V, O, dO, L, dQ, dK, dV, workspace, workspace_bytes, stages, stream);
+}
+
+fa_status fa_backward_scored(const fa_dims* dims, const fa_scores* scores, const void* Q, const void* K,
+                             const void* V, const void* O, const void* dO, const float* L, void* dQ, void* dK,
+                             void* dV, void* workspace, size_t workspace_bytes, int stages, void* stream) {
   t_last_launches = 0;
   fa::Problem pr;
+  fa::ScoreMods mods;
   fa_status s = check_dims(dims, &pr);
+  if (s == FA_OK) s = check_scores(pr, scores, &mods);
   if (s != FA_OK) return s;
   if (stages < 0 || stages > FA_BWD_ALL) return FA_ERR_INVALID_ARG;
   const long long nq = (long long)pr.B * pr.Hq * pr.Tq * pr.d, nqv = (long long)pr.B * pr.Hq * pr.Tq * pr.dv;
@@ -198,7 +225,7 @@ fa_status fa_backward_stages(const fa_dims* dims, const void* Q, const void* K, 
   }
   if (!fa::device_status_word()) return FA_ERR_CUDA;
   int launches = 0;
-  cudaError_t e = fa::launch_backward(pr, Q, K, V, O, dO, L, dQ, dK, dV, workspace, workspace_bytes, stages,
+  cudaError_t e = fa::launch_backward(pr, mods, Q, K, V, O, dO, L, dQ, dK, dV, workspace, workspace_bytes, stages,
                                       static_cast<cudaStream_t>(stream), &launches);
   t_last_launches = launches;
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
@@ -210,13 +237,39 @@ fa_status fa_backward(const fa_dims* dims, const void* Q, const void* K, const v
   return fa_backward_stages(dims, Q, K, V, O, dO, L, dQ, dK, dV, workspace, workspace_bytes, FA_BWD_ALL, stream);
 }
 
+size_t fa_mask_plan_bytes(const fa_dims* dims) {
+  fa::Problem pr;
+  if (check_dims(dims, &pr) != FA_OK) return 0;
+  return (size_t)fa::plan_layout(pr).total * sizeof(int);
+}
+
+fa_status fa_mask_plan(const fa_dims* dims, const int* doc_q, const int* doc_k, const int* prefix, int prefix_per_row,
+                       void* plan, size_t plan_bytes, void* stream) {
+  t_last_launches = 0;
+  fa::Problem pr;
+  const fa_status s = check_dims(dims, &pr);
+  if (s != FA_OK) return s;
+  if ((prefix_per_row != 0 && prefix_per_row != 1) || (prefix && (!pr.causal || pr.window))) return FA_ERR_INVALID_ARG;
+  if ((pr.Tq > 0 && pr.Tk > 0 && !doc_q != !doc_k) || ((reinterpret_cast<uintptr_t>(doc_q) |
+      reinterpret_cast<uintptr_t>(doc_k) | reinterpret_cast<uintptr_t>(prefix)) & 3u))
+    return FA_ERR_INVALID_ARG;
+  const size_t need = (size_t)fa::plan_layout(pr).total * sizeof(int);
+  if (need == 0) return FA_OK;
+  if (!plan || !aligned16(plan) || plan_bytes < need) return FA_ERR_INVALID_ARG;
+  if ((long long)pr.B * fa::kPlanCtas > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  const cudaError_t e = fa::launch_mask_plan(pr, {doc_q, doc_k, prefix, prefix_per_row}, plan,
+                                             static_cast<cudaStream_t>(stream));
+  t_last_launches = e == cudaSuccess;
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 const char* fa_status_string(fa_status s) {
   switch (s) {
     case FA_OK:
       return "ok";
     case FA_ERR_INVALID_ARG:
       return "invalid argument (null or misaligned pointer, negative size, Hq not a multiple of Hkv, "
-             "bad causal flag, window or scale, or workspace too small)";
+             "bad causal flag, window, scale, cap or prefix, or workspace too small)";
     case FA_ERR_UNSUPPORTED:
       return "unsupported shape (d and dv must each be 64 or 128, rotary channels a multiple of 16; sizes within the "
              "grid limits)";

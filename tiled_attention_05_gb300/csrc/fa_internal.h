@@ -48,12 +48,156 @@ int* device_status_word();
 // pair; safe to call from several host threads.
 cudaError_t allow_dynamic_smem(const void* kernel, int bytes);
 
+// ---------------------------------------------------------------- score modifications
+// Bits of the kernels' SCORE template argument; kPlain compiles none of it.
+enum ScoreBits : int { kPlain = -1, kCap = 1, kSlopes = 2 };
+
+struct ScoreMods {
+  float softcap = 0.f;            // c > 0: x = c tanh(x / c)
+  const float* slopes = nullptr;  // [Hq]: x -= slope |i + Tk - Tq - j|
+  const void* plan = nullptr;     // mask plan (documents, prefixes) for the same dims
+  bool any() const { return softcap > 0.f || slopes || plan; }
+  int bits() const { return (softcap > 0.f ? kCap : 0) | (slopes ? kSlopes : 0); }
+};
+
+// Without a plan, row i sees keys [i + lo_off, i + hi_off) within [0, Tk);
+// kFar stands for "no limit" and keeps the sums inside 32 bits.
+constexpr int kFar = 1 << 30;
+inline int row_hi_off(const Problem& p) { return p.causal ? p.Tk - p.Tq + 1 : kFar; }
+inline int row_lo_off(const Problem& p) { return p.causal && p.window ? p.Tk - p.Tq - p.window + 1 : -kFar; }
+
+// The cap's derivative is 4 r (1 - r); the kernels leave the 4 to this factor.
+inline float scale_grad(const Problem& p, const ScoreMods& m) { return m.softcap > 0.f ? 4.f * p.scale : p.scale; }
+
+// Mask plan: what fa_mask_plan wrote for one set of dims, as int32 arrays.
+// Rows and keys are padded to whole tiles per batch entry.
+constexpr int kPlanCtas = 8;  // CTAs that plan one batch entry, each with a flag of its own
+struct PlanView {
+  // row i sees keys [row_lo, row_hi) (empty where row_hi <= row_lo); with the
+  // flag by_key only those of its own document
+  const int *row_lo, *row_hi, *q_doc, *k_doc;
+  const int *kv_beg, *kv_end;          // key tiles a query tile visits
+  const int *key_from, *key_to;        // key j is seen by rows [key_from, key_to), unless the flag by_row
+  const int *m_beg, *m_end;            // query tiles a key tile visits
+  const int *tile_doc_lo, *tile_doc_hi;  // least and greatest document of a key tile
+  const int *by_key, *by_row;          // [B][kPlanCtas], any nonzero: set
+};
+struct PlanLayout {
+  long long row_lo, row_hi, q_doc, k_doc, kv_beg, kv_end, key_from, key_to, m_beg, m_end, tile_doc_lo, tile_doc_hi,
+      by_key, by_row, total;  // offsets in ints
+};
+inline PlanLayout plan_layout(const Problem& p) {
+  const long long qt = (long long)p.B * p.q_tiles(), kt = (long long)p.B * p.kv_tiles();
+  long long at = 0;
+  auto take = [&at](long long n) {
+    const long long o = at;
+    at += (n + 3) / 4 * 4;
+    return o;
+  };
+  PlanLayout l;
+  l.row_lo = take(qt * kTile);
+  l.row_hi = take(qt * kTile);
+  l.q_doc = take(qt * kTile);
+  l.k_doc = take(kt * kTile);
+  l.key_from = take(kt * kTile);
+  l.key_to = take(kt * kTile);
+  l.kv_beg = take(qt);
+  l.kv_end = take(qt);
+  l.m_beg = take(kt);
+  l.m_end = take(kt);
+  l.tile_doc_lo = take(kt);
+  l.tile_doc_hi = take(kt);
+  l.by_key = take((long long)p.B * kPlanCtas);
+  l.by_row = take((long long)p.B * kPlanCtas);
+  l.total = at;
+  return l;
+}
+inline PlanView plan_view(const Problem& p, const void* plan) {
+  PlanView v = {};
+  if (!plan) return v;
+  const int* a = static_cast<const int*>(plan);
+  const PlanLayout l = plan_layout(p);
+  v.row_lo = a + l.row_lo;
+  v.row_hi = a + l.row_hi;
+  v.q_doc = a + l.q_doc;
+  v.k_doc = a + l.k_doc;
+  v.kv_beg = a + l.kv_beg;
+  v.kv_end = a + l.kv_end;
+  v.key_from = a + l.key_from;
+  v.key_to = a + l.key_to;
+  v.m_beg = a + l.m_beg;
+  v.m_end = a + l.m_end;
+  v.tile_doc_lo = a + l.tile_doc_lo;
+  v.tile_doc_hi = a + l.tile_doc_hi;
+  v.by_key = a + l.by_key;
+  v.by_row = a + l.by_row;
+  return v;
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ bool plan_flag(const int* flags, int batch) {
+  const int4* f = reinterpret_cast<const int4*>(flags) + (size_t)batch * (kPlanCtas / 4);
+  int any = 0;
+#pragma unroll
+  for (int c = 0; c < kPlanCtas / 4; ++c) {
+    const int4 v = __ldg(f + c);
+    any |= v.x | v.y | v.z | v.w;
+  }
+  return any != 0;
+}
+#endif
+
+// Documents and prefixes of a mask plan (device arrays, any of them null).
+struct MaskInputs {
+  const int *doc_q, *doc_k;  // [B, Tq], [B, Tk]
+  const int* prefix;         // [B], or [B, Tq] with prefix_per_row
+  int prefix_per_row;
+};
+cudaError_t launch_mask_plan(const Problem& p, const MaskInputs& in, void* plan, cudaStream_t stream);
+
+// Parameters of the backward main kernel.
+struct BwdParams {
+  const float* lse2;
+  const float* delta;
+  int* status;
+  int Hq, Hkv, G, Tq, Tk, causal_off, q_tiles, kv_tiles;
+  int sb_groups;  // (batch, kv head) groups per super-batch of the grid order; divides B * Hkv
+  int window;     // causal sliding window in keys, 0 = none
+  long long Tq_pad;
+  float scale_log2;
+  float scale_grad;  // of dK (scale, times 4 with a cap: see scale_grad())
+  int test_withhold_do;  // test build only: never issue the dO loads (the CTA's waits then time out)
+  // Split items: the last n_split items of the grid order run as two CTAs
+  // each (CTAs n_whole + 2 s and n_whole + 2 s + 1 for item n_whole + s),
+  // each walking half of the item's query tiles; the halves' fp32 dK / dV
+  // meet in `part`, and whichever half finishes second adds the other's and
+  // stores them (split_counters, zeroed by fa_bwd_pre, tell them apart).
+  int n_whole, n_split;
+  // Score-modified instances only (see ScoreMods):
+  float cap_log2, cap_in;  // c * log2(e), 2 * scale * log2(e) / c
+  const float* slopes;     // [Hq]
+  int hi_off, lo_off;      // row i sees keys [i + lo_off, i + hi_off) (no plan)
+  PlanView plan;
+  float* part;                    // [n_split][2 halves][128 key rows][d + dv]
+  unsigned int* split_counters;   // [n_split]
+};
+
+// The score-modified instances, by head size of Q and K (one translation unit
+// and direction each).
+cudaError_t launch_fwd_scored_64(const Problem& p, const ScoreMods& m, const CUtensorMap& mq, const CUtensorMap& mk,
+                                 const CUtensorMap& mv, void* O, float* L, cudaStream_t stream);
+cudaError_t launch_fwd_scored_128(const Problem& p, const ScoreMods& m, const CUtensorMap& mq, const CUtensorMap& mk,
+                                  const CUtensorMap& mv, void* O, float* L, cudaStream_t stream);
+cudaError_t launch_bwd_scored_64(const Problem& p, const ScoreMods& m, const CUtensorMap* maps, const BwdParams& bp,
+                                 cudaStream_t stream);
+cudaError_t launch_bwd_scored_128(const Problem& p, const ScoreMods& m, const CUtensorMap* maps, const BwdParams& bp,
+                                  cudaStream_t stream);
+
 // Launchers.  Each returns the first CUDA error it met and adds the number
 // of kernels it enqueued to *launches.
-cudaError_t launch_forward(const Problem& p, const void* Q, const void* K, const void* V, void* O, float* L,
-                           cudaStream_t stream, int* launches);
+cudaError_t launch_forward(const Problem& p, const ScoreMods& m, const void* Q, const void* K, const void* V, void* O,
+                           float* L, cudaStream_t stream, int* launches);
 // `workspace_bytes` decides whether the split-item area fits (see BwdWorkspace).
-cudaError_t launch_backward(const Problem& p, const void* Q, const void* K, const void* V, const void* O,
+cudaError_t launch_backward(const Problem& p, const ScoreMods& m, const void* Q, const void* K, const void* V, const void* O,
                             const void* dO, const float* L, void* dQ, void* dK, void* dV, void* workspace,
                             size_t workspace_bytes, int stages, cudaStream_t stream, int* launches);
 
