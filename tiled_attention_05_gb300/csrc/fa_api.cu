@@ -86,7 +86,7 @@ fa_status check_ptr(const void* p, long long elems) {
 
 fa_status check_scores(const fa::Problem& pr, const fa_scores* sc, fa::ScoreMods* m) {
   if (!sc) return FA_OK;
-  if (sc->softcap != 0.f && !(sc->softcap >= 0x1p-10f && sc->softcap <= 0x1p20f)) return FA_ERR_INVALID_ARG;
+  if (sc->softcap != 0.f && !(sc->softcap >= 0x1p-10f && sc->softcap <= 0x1p10f)) return FA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(sc->slopes) & 3u) return FA_ERR_INVALID_ARG;
   if (!aligned16(sc->plan)) return FA_ERR_INVALID_ARG;
   if (sc->slopes && (pr.Tq > (1 << 24) || pr.Tk > (1 << 24))) return FA_ERR_UNSUPPORTED;

@@ -235,7 +235,7 @@ cudaError_t launch_backward(const Problem& pr, const ScoreMods& mods, const void
       !encode_rows_bf16(&maps[5], dV, pr.dv, pr.Tk, (long long)pr.B * pr.Hkv) ||
       !encode_acc_f32(&maps[6], dq_acc, pr.d, pr.Tq_pad(), (long long)pr.B * pr.Hq, 32))
     return cudaErrorInvalidValue;
-  BwdParams bp;
+  ScoredBwdParams bp;
   bp.lse2 = lse2;
   bp.delta = delta;
   bp.status = device_status_word();
@@ -259,6 +259,7 @@ cudaError_t launch_backward(const Problem& pr, const ScoreMods& mods, const void
   bp.slopes = mods.slopes;
   bp.hi_off = row_hi_off(pr);
   bp.lo_off = row_lo_off(pr);
+  bp.two_sided = !pr.causal || mods.plan;
   bp.plan = plan_view(pr, mods.plan);
   bp.n_split = mods.plan ? 0 : backward_split_items(pr, split_cap);  // a plan's items differ in work
   bp.n_whole = (int)((long long)pr.B * pr.Hkv * pr.kv_tiles()) - bp.n_split;

@@ -70,6 +70,7 @@
 // intervals are not in order is looked up row by row instead.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "sm103_ptx.cuh"
@@ -195,33 +196,87 @@ __device__ __forceinline__ void write_partial(uint32_t src, float* dst, bool hav
 }
 
 using fa::BwdParams;
+using fa::ScoredBwdParams;
+template <int SCORE>
+using BwdParamsOf = std::conditional_t<SCORE >= 0, ScoredBwdParams, BwdParams>;
 
-// Two neighbouring queries' scores of one key: raw q.k -> the exponent of P
-// (log2 units, minus the rows' log2 statistics l2), and with a cap a quarter of
-// its derivative.  rel: position of the first of the two queries minus the key's.
-template <bool CAP, bool SLOPES>
-__device__ __forceinline__ void modified_pair(const BwdParams& p, uint64_t s, uint64_t l2, float rel, float slope2,
-                                              uint64_t& x, uint64_t& w) {
-  if (CAP) {
-    const uint64_t z = f2_mul(s, f2_pack(p.cap_in, p.cap_in));
-    const uint64_t d = f2_add(f2_pack(ex2(f2_lo(z)), ex2(f2_hi(z))), f2_pack(1.f, 1.f));
-    const uint64_t r = f2_pack(rcp(f2_lo(d)), rcp(f2_hi(d)));
-    x = f2_fma(r, f2_pack(-2.f * p.cap_log2, -2.f * p.cap_log2), f2_sub(f2_pack(p.cap_log2, p.cap_log2), l2));
-    w = f2_fma(f2_neg(r), r, r);
-  } else {
-    x = f2_fma(s, f2_pack(p.scale_log2, p.scale_log2), f2_neg(l2));
+// The exponentials of 32 queries' scores of one key: raw q.k in sr -> fp32 weights
+// for dS in pr (with a cap times a quarter of its derivative) and P as packed
+// bf16.  lse: the queries' row statistics (log2 units); rel0: position of the
+// first query minus the key's; vis: the queries that see the key (MASKED).
+// BOTH: queries on both sides of the key may see it, else the bias is a line.
+template <bool CAP, bool SLOPES, bool MASKED, bool BOTH>
+__device__ __forceinline__ void modified_chunk(const ScoredBwdParams& p, const uint32_t (&sr)[32], const float4* lse,
+                                               int rel0, float slope2, uint32_t vis, float* pr, uint32_t (&pk)[16]) {
+  const float in = CAP ? p.cap_in : p.scale_log2;
+  const uint64_t in2 = f2_pack(in, in), m2cap2 = f2_pack(-2.f * p.cap_log2, -2.f * p.cap_log2);
+  const float side = rel0 + 31 <= 0 ? slope2 : -slope2;  // bias per step of the query
+  uint64_t step[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) step[k] = f2_pack((float)(2 * k) * side, (float)(2 * k + 1) * side);
+  const float rel = (float)rel0;
+#pragma unroll
+  for (int c = 0; c < 32; c += 4) {
+    const float4 l4 = ld_shared_f4(lse + (c >> 2));  // 16-byte broadcast: 4 columns
+    const uint64_t l[2] = {f2_pack(l4.x, l4.y), f2_pack(l4.z, l4.w)};
+    uint64_t x[2] = {f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
+                     f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]))};
+    uint64_t r[2], e[2];
+    if (CAP) cap_quad(f2_mul(x[0], in2), f2_mul(x[1], in2), r[0], r[1], e[0], e[1]);
+    const float gb = fmaf(rel + (float)c, side, CAP ? p.cap_log2 : 0.f);  // (the sum is exact)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint64_t bias;  // (cap +) distance bias - row statistic
+      if (SLOPES && BOTH) {
+        const float d0 = (float)(rel0 + c + 2 * h), d1 = (float)(rel0 + c + 2 * h + 1);
+        bias = f2_sub(f2_pack(fmaf(fabsf(d0), -slope2, CAP ? p.cap_log2 : 0.f),
+                              fmaf(fabsf(d1), -slope2, CAP ? p.cap_log2 : 0.f)), l[h]);
+      } else if (SLOPES) {
+        bias = f2_sub(f2_add(step[h], f2_pack(gb, gb)), l[h]);
+      } else if (CAP) {
+        bias = f2_sub(f2_pack(p.cap_log2, p.cap_log2), l[h]);
+      } else {
+        bias = f2_neg(l[h]);
+      }
+      x[h] = CAP ? f2_fma(r[h], m2cap2, bias) : f2_fma(x[h], in2, bias);
+      float v0 = ex2(f2_lo(x[h])), v1 = ex2(f2_hi(x[h]));
+      if (MASKED) {
+        if (!((vis >> (c + 2 * h)) & 1u)) v0 = 0.f;
+        if (!((vis >> (c + 2 * h + 1)) & 1u)) v1 = 0.f;
+      }
+      pk[c / 2 + h] = pack_bf16x2(v0, v1);
+      uint64_t w = f2_pack(v0, v1);
+      if (CAP) w = f2_mul(w, f2_mul(f2_mul(e[h], r[h]), r[h]));
+      pr[c + 2 * h] = f2_lo(w);
+      pr[c + 2 * h + 1] = f2_hi(w);
+    }
   }
-  if (SLOPES) x = f2_fma(f2_abs(f2_pack(rel, rel + 1.f)), f2_pack(-slope2, -slope2), x);
+}
+
+// Bits [from, to] of 64.
+__device__ __forceinline__ void interval_bits(int from, int to, uint32_t (&vis)[2]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int lo = min(max(from - 32 * k, 0), 32), hi = min(max(to + 1 - 32 * k, 0), 32);
+    vis[k] = (uint32_t)(((1ull << hi) - 1) & ~((1ull << lo) - 1));
+  }
 }
 
 // Whether query row q sees key j by the plan's row intervals (and, where they
 // are compared key by key, documents).
-__device__ __forceinline__ bool row_sees(const BwdParams& p, int b, int q, int j) {
+__device__ __forceinline__ bool row_sees(const ScoredBwdParams& p, int b, int q, int j) {
   const size_t at = (size_t)b * p.q_tiles * BM + q;
   bool see = j >= __ldg(p.plan.row_lo + at) && j < __ldg(p.plan.row_hi + at);
   if (see && fa::plan_flag(p.plan.by_key, b))
     see = __ldg(p.plan.q_doc + at) == __ldg(p.plan.k_doc + (size_t)b * p.kv_tiles * BN + j);
   return see;
+}
+__device__ __noinline__ void rows_that_see(const ScoredBwdParams& p, int b, int q0, int j, uint32_t (&vis)[2]) {
+  for (int k = 0; k < 2; ++k) {
+    uint32_t bits = 0u;
+    for (int c = 0; c < 32; ++c) bits |= (uint32_t)row_sees(p, b, q0 + 32 * k + c, j) << c;
+    vis[k] = bits;
+  }
 }
 
 // WINDOW (causal only): the sliding-window terms are compiled in only where
@@ -232,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fa_bwd_main(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                 const __grid_constant__ CUtensorMap tmdK, const __grid_constant__ CUtensorMap tmdV,
-                const __grid_constant__ CUtensorMap tmAcc, const BwdParams p) {
+                const __grid_constant__ CUtensorMap tmAcc, const BwdParamsOf<SCORE> p) {
   using C = BwdCfg<HD, HDV>;
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int NQ = C::NQ, NDO = C::NDO;
@@ -527,73 +582,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The packed bf16 P of chunk c is stored over S columns this thread has
       // already read (each thread only touches its own TMEM lane); the fp32 P
       // stays in registers for dS.
-      bool need_mask;
-      int vis_from, vis_to;
-      float slope2 = 0.f;
-      if constexpr (MODS) {
-        vis_from = row_from - q0;
-        vis_to = row_to - q0;
-        need_mask = __any_sync(0xffffffffu, vis_from > wg * 64 || vis_to < wg * 64 + 63) && !by_row;
-        if (SLOPES) slope2 = p.slopes[hk * p.G + g] * 1.4426950408889634f;
-      } else {
-        need_mask = !key_valid || (CAUSAL && k0 + BN - 1 > q0 + p.causal_off) ||
-                               (WINDOW && q0 + BM - 1 + p.causal_off - p.window + 1 > k0);
-        // key row `key` is visible to query q0 + c iff vis_from <= c <= vis_to:
-        // key <= q0 + c + off, and with a window also key > q0 + c + off - W
-        vis_from = key_valid ? (CAUSAL ? key - p.causal_off - q0 : -0x40000000) : 0x40000000;
-        vis_to = WINDOW ? key - p.causal_off - q0 + p.window - 1 : 0x40000000;
-      }
       const float4* lse4 = reinterpret_cast<const float4*>(lse_s + wg * 64);
       const uint64_t sl2x2 = f2_pack(sl2, sl2);
       float pr[64];
-#pragma unroll
-      for (int ch = 0; ch < 2; ++ch) {
-        uint32_t sr[32];
-        tmem_ld32(T_S + lane_base + wg * 64 + ch * 32, sr);
-        tmem_wait_ld();
-        uint32_t pk[16];
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 l4 = ld_shared_f4(lse4 + ((ch * 32 + c) >> 2));  // 16-byte broadcast: 4 columns
-          uint64_t x01, x23, w01 = 0ull, w23 = 0ull;  // w: a quarter of the cap's derivative
-          if constexpr (CAP || SLOPES) {
-            // column c of this chunk is query q0 + wg * 64 + ch * 32 + c
-            const float rel0 = (float)(q0 + wg * 64 + ch * 32 + p.causal_off - key);
-            modified_pair<CAP, SLOPES>(p, f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
-                                       f2_pack(l4.x, l4.y), rel0 + (float)c, slope2, x01, w01);
-            modified_pair<CAP, SLOPES>(p, f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])),
-                                       f2_pack(l4.z, l4.w), rel0 + (float)(c + 2), slope2, x23, w23);
-          } else {
-            x01 = f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl2x2, f2_pack(-l4.x, -l4.y));
-            x23 = f2_fma(f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl2x2,
-                         f2_pack(-l4.z, -l4.w));
-          }
-          float v0 = ex2(f2_lo(x01)), v1 = ex2(f2_hi(x01)), v2 = ex2(f2_lo(x23)), v3 = ex2(f2_hi(x23));
-          if constexpr (MODS) {
-            if (by_row) {
-              const int qc = q0 + wg * 64 + ch * 32 + c;
-              if (!row_sees(p, b, qc, key)) v0 = 0.f;
-              if (!row_sees(p, b, qc + 1, key)) v1 = 0.f;
-              if (!row_sees(p, b, qc + 2, key)) v2 = 0.f;
-              if (!row_sees(p, b, qc + 3, key)) v3 = 0.f;
-            }
-          }
-          if (need_mask) {
-            const int qc = wg * 64 + ch * 32 + c;
-            constexpr bool UPPER = WINDOW || MODS;
-            if (qc < vis_from || (UPPER && qc > vis_to)) v0 = 0.f;
-            if (qc + 1 < vis_from || (UPPER && qc + 1 > vis_to)) v1 = 0.f;
-            if (qc + 2 < vis_from || (UPPER && qc + 2 > vis_to)) v2 = 0.f;
-            if (qc + 3 < vis_from || (UPPER && qc + 3 > vis_to)) v3 = 0.f;
-          }
-          pr[ch * 32 + c] = CAP ? v0 * f2_lo(w01) : v0;
-          pr[ch * 32 + c + 1] = CAP ? v1 * f2_hi(w01) : v1;
-          pr[ch * 32 + c + 2] = CAP ? v2 * f2_lo(w23) : v2;
-          pr[ch * 32 + c + 3] = CAP ? v3 * f2_hi(w23) : v3;
-          pk[c / 2] = pack_bf16x2(v0, v1);
-          pk[c / 2 + 1] = pack_bf16x2(v2, v3);
+      if constexpr (MODS) {
+        // which of this warpgroup's 64 queries see this thread's key, by bits
+        const int c0 = q0 + wg * 64;  // first of them
+        uint32_t vis[2] = {~0u, ~0u};
+        const bool masked = by_row || __any_sync(0xffffffffu, row_from > c0 || row_to < c0 + 63);
+        if (masked) {
+          if (by_row)
+            rows_that_see(p, b, c0, key, vis);
+          else
+            interval_bits(row_from - c0, row_to - c0, vis);
         }
-        tmem_st16(T_S + lane_base + wg * 64 + ch * 16, pk);
+        float slope2 = 0.f;
+        if (SLOPES) slope2 = p.slopes[hk * p.G + g] * 1.4426950408889634f;
+        const int rel0 = c0 + p.causal_off - key;  // of query c0 to the key
+        auto chunk = [&](auto ch_, auto masked_, auto both_) {
+          constexpr int ch = decltype(ch_)::value;
+          uint32_t sr[32], pk[16];
+          tmem_ld32(T_S + lane_base + wg * 64 + ch * 32, sr);
+          tmem_wait_ld();
+          modified_chunk<CAP, SLOPES, decltype(masked_)::value, decltype(both_)::value>(
+              p, sr, lse4 + ch * 8, rel0 + ch * 32, slope2, vis[ch], pr + ch * 32, pk);
+          tmem_st16(T_S + lane_base + wg * 64 + ch * 16, pk);
+        };
+        using zero = std::integral_constant<int, 0>;
+        using one = std::integral_constant<int, 1>;
+        if (!masked) {
+          if (SLOPES && p.two_sided && __any_sync(0xffffffffu, rel0 < 0 && rel0 + 64 > 1)) {
+            chunk(zero{}, std::false_type{}, std::bool_constant<SLOPES>{});
+            chunk(one{}, std::false_type{}, std::bool_constant<SLOPES>{});
+          } else {
+            chunk(zero{}, std::false_type{}, std::false_type{});
+            chunk(one{}, std::false_type{}, std::false_type{});
+          }
+        } else {  // (rare enough to take the two-sided form at once)
+          chunk(zero{}, std::true_type{}, std::bool_constant<SLOPES>{});
+          chunk(one{}, std::true_type{}, std::bool_constant<SLOPES>{});
+        }
+      } else {
+        const bool need_mask = !key_valid || (CAUSAL && k0 + BN - 1 > q0 + p.causal_off) ||
+                               (WINDOW && q0 + BM - 1 + p.causal_off - p.window + 1 > k0);
+        // key row `key` is visible to query q0 + c iff vis_from <= c <= vis_to:
+        // key <= q0 + c + off, and with a window also key > q0 + c + off - W
+        const int vis_from = key_valid ? (CAUSAL ? key - p.causal_off - q0 : -0x40000000) : 0x40000000;
+        const int vis_to = WINDOW ? key - p.causal_off - q0 + p.window - 1 : 0x40000000;
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          uint32_t sr[32];
+          tmem_ld32(T_S + lane_base + wg * 64 + ch * 32, sr);
+          tmem_wait_ld();
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 l4 = ld_shared_f4(lse4 + ((ch * 32 + c) >> 2));  // 16-byte broadcast: 4 columns
+            const uint64_t x01 = f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl2x2,
+                                        f2_pack(-l4.x, -l4.y));
+            const uint64_t x23 = f2_fma(f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl2x2,
+                                        f2_pack(-l4.z, -l4.w));
+            float v0 = ex2(f2_lo(x01)), v1 = ex2(f2_hi(x01)), v2 = ex2(f2_lo(x23)), v3 = ex2(f2_hi(x23));
+            if (need_mask) {
+              const int qc = wg * 64 + ch * 32 + c;
+              if (qc < vis_from || (WINDOW && qc > vis_to)) v0 = 0.f;
+              if (qc + 1 < vis_from || (WINDOW && qc + 1 > vis_to)) v1 = 0.f;
+              if (qc + 2 < vis_from || (WINDOW && qc + 2 > vis_to)) v2 = 0.f;
+              if (qc + 3 < vis_from || (WINDOW && qc + 3 > vis_to)) v3 = 0.f;
+            }
+            pr[ch * 32 + c] = v0;
+            pr[ch * 32 + c + 1] = v1;
+            pr[ch * 32 + c + 2] = v2;
+            pr[ch * 32 + c + 3] = v3;
+            pk[c / 2] = pack_bf16x2(v0, v1);
+            pk[c / 2 + 1] = pack_bf16x2(v2, v3);
+          }
+          tmem_st16(T_S + lane_base + wg * 64 + ch * 16, pk);
+        }
       }
       tmem_wait_st();
       tc_fence_before();
@@ -753,7 +818,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int HD, int HDV, bool CAUSAL, bool WINDOW, int SCORE>
-cudaError_t launch_main_t(const fa::Problem& pr, const CUtensorMap* maps, const BwdParams& bp, cudaStream_t stream) {
+cudaError_t launch_main_t(const fa::Problem& pr, const CUtensorMap* maps, const BwdParamsOf<SCORE>& bp,
+                          cudaStream_t stream) {
   using C = BwdCfg<HD, HDV>;
   const void* fn = reinterpret_cast<const void*>(fa_bwd_main<HD, HDV, CAUSAL, WINDOW, SCORE>);
   cudaError_t e = fa::allow_dynamic_smem(fn, C::SMEM);

@@ -65,6 +65,7 @@
 // masks a tile only where one of its rows does not see all of it.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "sm103_ptx.cuh"
@@ -154,19 +155,25 @@ struct FwdParams {
   long long n_full;    // work items that are pairs of query tiles
   long long n_items;   // all work items: n_full pairs, then single query tiles
   float scale_log2;  // scale * log2(e)
-  // Score-modified instances only (see fa::ScoreMods):
-  float cap_log2;      // c * log2(e)
-  float cap_in;        // 2 * scale * log2(e) / c
-  const float* slopes;  // [Hq]
-  int hi_off, lo_off;  // row i sees keys [i + lo_off, i + hi_off) (no plan)
-  int q_tiles;
-  fa::PlanView plan;
   int test_withhold_q;  // test build only: never issue the Q loads (every wait then times out)
 };
 
+// What the score-modified instances need besides (see fa::ScoreMods).
+struct ScoredFwdParams : FwdParams {
+  float cap_log2;       // c * log2(e)
+  float cap_in;         // 2 * scale * log2(e) / c
+  const float* slopes;  // [Hq]
+  int hi_off, lo_off;   // row i sees keys [i + lo_off, i + hi_off) (no plan)
+  int q_tiles;
+  int two_sided;        // a row may see keys on both sides of its own position
+  fa::PlanView plan;
+};
+template <int SCORE>
+using FwdParamsOf = std::conditional_t<SCORE >= 0, ScoredFwdParams, FwdParams>;
+
 // Key tiles [*beg, *end) that query rows [qa, qa+128) must visit (empty: 0, 0).
 template <bool CAUSAL, bool WINDOW, int SCORE>
-__device__ __forceinline__ void kv_range_for(const FwdParams& p, int b, int qa, int* beg, int* end) {
+__device__ __forceinline__ void kv_range_for(const FwdParamsOf<SCORE>& p, int b, int qa, int* beg, int* end) {
   *beg = *end = 0;
   if (qa >= p.Tq) return;
   if constexpr (SCORE >= 0) {
@@ -221,7 +228,7 @@ struct FwdItem {
 // which spreads a short last round of equal-weight items over twice as many
 // CTAs.
 template <bool CAUSAL, bool WINDOW, int SCORE>
-__device__ __forceinline__ bool fwd_item(const FwdParams& p, int n, FwdItem* it) {
+__device__ __forceinline__ bool fwd_item(const FwdParamsOf<SCORE>& p, int n, FwdItem* it) {
   const long long G = gridDim.x, c = blockIdx.x;
   const long long k = n * G + ((n & 1) ? G - 1 - c : c);
   if (k >= p.n_items) return false;
@@ -259,34 +266,56 @@ __device__ __forceinline__ bool fwd_item(const FwdParams& p, int n, FwdItem* it)
 
 // Scores of one row and key tile, in place: raw q.k -> log2 units with the cap
 // and the distance bias.  rel0: key of column 0 minus the row's own position.
-template <bool CAP, bool SLOPES>
-__device__ __forceinline__ void modify_scores(uint32_t (&sr)[BN], const FwdParams& p, int rel0, float slope2) {
+// BOTH: the row's own position may lie inside the tile with keys visible on
+// both sides of it; otherwise all visible keys are on one side and the bias is
+// a line in the column, built from eight slopes and one base per eight columns.
+template <bool CAP, bool SLOPES, bool BOTH>
+__device__ __forceinline__ void modify_scores(uint32_t (&sr)[BN], const ScoredFwdParams& p, int rel0, float slope2) {
   if constexpr (CAP || SLOPES) {
-    const uint64_t rel2 = f2_pack((float)rel0, (float)rel0), ns2 = f2_pack(-slope2, -slope2);
-    const uint64_t in2 = f2_pack(p.cap_in, p.cap_in), one2 = f2_pack(1.f, 1.f);
+    const uint64_t in2 = CAP ? f2_pack(p.cap_in, p.cap_in) : f2_pack(p.scale_log2, p.scale_log2);
     const uint64_t cap2 = f2_pack(p.cap_log2, p.cap_log2), m2cap2 = f2_pack(-2.f * p.cap_log2, -2.f * p.cap_log2);
-    const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+    const float s2 = rel0 >= 0 ? -slope2 : slope2;
+    const float rel = (float)rel0;
+    uint64_t step[4];
 #pragma unroll
-    for (int c = 0; c < BN; c += 2) {
-      const uint64_t s = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-      uint64_t x;
-      if (CAP) {
-        const uint64_t z = f2_mul(s, in2);
-        const uint64_t d = f2_add(f2_pack(ex2(f2_lo(z)), ex2(f2_hi(z))), one2);
-        x = f2_fma(f2_pack(rcp(f2_lo(d)), rcp(f2_hi(d))), m2cap2, cap2);
-      } else {
-        x = f2_mul(s, sc2);
+    for (int k = 0; k < 4; ++k) step[k] = f2_pack((float)(2 * k) * s2, (float)(2 * k + 1) * s2);
+#pragma unroll
+    for (int g = 0; g < BN; g += 8) {
+      // (rel + g is exact: a key near the row is biased by few steps, so that
+      // nothing large cancels there)
+      const float gb = fmaf(rel + (float)g, s2, CAP ? p.cap_log2 : 0.f);
+      const uint64_t base2 = f2_pack(gb, gb);
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        const int c = g + 2 * k;
+        uint64_t x[2] = {f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
+                         f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]))};
+        uint64_t r[2], e[2];
+        if (CAP) cap_quad(f2_mul(x[0], in2), f2_mul(x[1], in2), r[0], r[1], e[0], e[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (SLOPES && BOTH) {
+            const float d0 = (float)(rel0 + c + 2 * h), d1 = (float)(rel0 + c + 2 * h + 1);
+            const uint64_t bias = f2_pack(fmaf(fabsf(d0), -slope2, CAP ? p.cap_log2 : 0.f),
+                                          fmaf(fabsf(d1), -slope2, CAP ? p.cap_log2 : 0.f));
+            x[h] = CAP ? f2_fma(r[h], m2cap2, bias) : f2_fma(x[h], in2, bias);
+          } else if (SLOPES) {
+            const uint64_t bias = f2_add(step[k + h], base2);
+            x[h] = CAP ? f2_fma(r[h], m2cap2, bias) : f2_fma(x[h], in2, bias);
+          } else {
+            x[h] = f2_fma(r[h], m2cap2, cap2);
+          }
+          sr[c + 2 * h] = __float_as_uint(f2_lo(x[h]));
+          sr[c + 2 * h + 1] = __float_as_uint(f2_hi(x[h]));
+        }
       }
-      if (SLOPES) x = f2_fma(f2_abs(f2_add(f2_pack((float)c, (float)(c + 1)), rel2)), ns2, x);
-      sr[c] = __float_as_uint(f2_lo(x));
-      sr[c + 1] = __float_as_uint(f2_hi(x));
     }
   }
 }
 
 // Plans whose documents are not in order: hides the keys of other documents one
 // by one, unless every row of the warp has the document of the whole key tile.
-__device__ __forceinline__ void mask_documents(uint32_t (&sr)[BN], const FwdParams& p, int batch, int kv0, int my_doc) {
+__device__ __forceinline__ void mask_documents(uint32_t (&sr)[BN], const ScoredFwdParams& p, int batch, int kv0, int my_doc) {
   const size_t tile = (size_t)batch * p.kv_tiles + kv0 / BN;
   const int lo = p.plan.tile_doc_lo[tile], hi = p.plan.tile_doc_hi[tile];
   if (__all_sync(0xffffffffu, lo == my_doc && hi == my_doc)) return;
@@ -308,7 +337,7 @@ __device__ __forceinline__ void mask_documents(uint32_t (&sr)[BN], const FwdPara
 template <int HD, int HDV, bool CAUSAL, bool WINDOW, int SCORE>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                  const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
+                  const __grid_constant__ CUtensorMap tmV, const FwdParamsOf<SCORE> p) {
   using C = FwdCfg<HD, HDV>;
   constexpr int NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -569,8 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int my_doc = 0;              // its document, where the plan wants documents compared key by key
       bool by_key = false;
       float slope2 = 0.f;
-      const int batch = it.bh / p.Hq;
+      int batch = 0;
       if constexpr (SCORE >= 0) {
+        batch = it.bh / p.Hq;
         if (p.plan.kv_beg) {
           const size_t at = (size_t)batch * p.q_tiles * BM + (i < p.q_tiles * BM ? i : 0);
           row_lo = p.plan.row_lo[at];
@@ -596,8 +626,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         const int kv0 = (kbx + jx) * BN;
         if constexpr (SCORE >= 0) {
-          modify_scores<CAP, SLOPES>(sr, p, kv0 - p.causal_off - i, slope2);
           const int lim = row_hi - kv0, lo = row_lo - kv0;  // columns [lo, lim) are visible to row i
+          const int rel0 = kv0 - p.causal_off - i;
+          if (SLOPES && p.two_sided && __any_sync(0xffffffffu, rel0 < 0 && rel0 + BN > 1))
+            modify_scores<CAP, SLOPES, SLOPES>(sr, p, rel0, slope2);
+          else
+            modify_scores<CAP, SLOPES, false>(sr, p, rel0, slope2);
           if (__any_sync(0xffffffffu, lim < BN || lo > 0)) {
 #pragma unroll
             for (int c = 0; c < BN; ++c)
@@ -622,9 +656,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k) pm[k] = __uint_as_float(sr[k]);
 #pragma unroll
-        for (int c = 8; c < BN; c += 16)
+        for (int c = 8; c + 16 <= BN; c += 16)
 #pragma unroll
           for (int k = 0; k < 8; ++k) pm[k] = fmax3(pm[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], __uint_as_float(sr[BN - 8 + k]));
         const float mt = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
         const float mt2 = mt * sl2;
         float m_new = m_ref;
@@ -753,7 +789,7 @@ cudaError_t launch_fwd_t(const fa::Problem& pr, const fa::ScoreMods& mods, const
   if (fa_attr.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  FwdParams p;
+  FwdParamsOf<SCORE> p;
   p.O = static_cast<uint16_t*>(O);
   p.L = L;
   p.status = fa::device_status_word();
@@ -775,13 +811,16 @@ cudaError_t launch_fwd_t(const fa::Problem& pr, const fa::ScoreMods& mods, const
   p.n_full = (!pr.causal && !mods.plan && r > 0 && 2 * r <= sms) ? n_pair_items - r : n_pair_items;
   p.n_items = p.n_full + 2 * (n_pair_items - p.n_full);
   p.scale_log2 = pr.scale * 1.4426950408889634f;
-  p.cap_log2 = mods.softcap * 1.4426950408889634f;
-  p.cap_in = mods.softcap > 0.f ? 2.f * p.scale_log2 / mods.softcap : 0.f;
-  p.slopes = mods.slopes;
-  p.hi_off = fa::row_hi_off(pr);
-  p.lo_off = fa::row_lo_off(pr);
-  p.q_tiles = pr.q_tiles();
-  p.plan = fa::plan_view(pr, mods.plan);
+  if constexpr (SCORE >= 0) {
+    p.cap_log2 = mods.softcap * 1.4426950408889634f;
+    p.cap_in = mods.softcap > 0.f ? 2.f * p.scale_log2 / mods.softcap : 0.f;
+    p.slopes = mods.slopes;
+    p.hi_off = fa::row_hi_off(pr);
+    p.lo_off = fa::row_lo_off(pr);
+    p.q_tiles = pr.q_tiles();
+    p.two_sided = !pr.causal || mods.plan;
+    p.plan = fa::plan_view(pr, mods.plan);
+  }
   p.test_withhold_q = fa::test_withhold() == fa::kWithholdFwdQ;
   const int grid = (int)(p.n_items < sms ? p.n_items : sms);
   fa_fwd_kernel<HD, HDV, CAUSAL, WINDOW, SCORE><<<grid, kThreads, C::SMEM, stream>>>(mq, mk, mv, p);

@@ -163,8 +163,7 @@ struct BwdParams {
   int sb_groups;  // (batch, kv head) groups per super-batch of the grid order; divides B * Hkv
   int window;     // causal sliding window in keys, 0 = none
   long long Tq_pad;
-  float scale_log2;
-  float scale_grad;  // of dK (scale, times 4 with a cap: see scale_grad())
+  float scale_log2, scale_grad;  // scale_grad: of dK (scale, times 4 with a cap)
   int test_withhold_do;  // test build only: never issue the dO loads (the CTA's waits then time out)
   // Split items: the last n_split items of the grid order run as two CTAs
   // each (CTAs n_whole + 2 s and n_whole + 2 s + 1 for item n_whole + s),
@@ -172,13 +171,16 @@ struct BwdParams {
   // meet in `part`, and whichever half finishes second adds the other's and
   // stores them (split_counters, zeroed by fa_bwd_pre, tell them apart).
   int n_whole, n_split;
-  // Score-modified instances only (see ScoreMods):
+  float* part;                    // [n_split][2 halves][128 key rows][d + dv]
+  unsigned int* split_counters;   // [n_split]
+};
+// What the score-modified instances need besides (see ScoreMods).
+struct ScoredBwdParams : BwdParams {
   float cap_log2, cap_in;  // c * log2(e), 2 * scale * log2(e) / c
   const float* slopes;     // [Hq]
   int hi_off, lo_off;      // row i sees keys [i + lo_off, i + hi_off) (no plan)
+  int two_sided;           // a row may see keys on both sides of its own position
   PlanView plan;
-  float* part;                    // [n_split][2 halves][128 key rows][d + dv]
-  unsigned int* split_counters;   // [n_split]
 };
 
 // The score-modified instances, by head size of Q and K (one translation unit
@@ -187,9 +189,9 @@ cudaError_t launch_fwd_scored_64(const Problem& p, const ScoreMods& m, const CUt
                                  const CUtensorMap& mv, void* O, float* L, cudaStream_t stream);
 cudaError_t launch_fwd_scored_128(const Problem& p, const ScoreMods& m, const CUtensorMap& mq, const CUtensorMap& mk,
                                   const CUtensorMap& mv, void* O, float* L, cudaStream_t stream);
-cudaError_t launch_bwd_scored_64(const Problem& p, const ScoreMods& m, const CUtensorMap* maps, const BwdParams& bp,
+cudaError_t launch_bwd_scored_64(const Problem& p, const ScoreMods& m, const CUtensorMap* maps, const ScoredBwdParams& bp,
                                  cudaStream_t stream);
-cudaError_t launch_bwd_scored_128(const Problem& p, const ScoreMods& m, const CUtensorMap* maps, const BwdParams& bp,
+cudaError_t launch_bwd_scored_128(const Problem& p, const ScoreMods& m, const CUtensorMap* maps, const ScoredBwdParams& bp,
                                   cudaStream_t stream);
 
 // Launchers.  Each returns the first CUDA error it met and adds the number

@@ -4,7 +4,7 @@
 namespace {
 
 template <int HDV>
-cudaError_t launch_dims(const fa::Problem& p, const fa::ScoreMods& m, const CUtensorMap* maps, const BwdParams& bp,
+cudaError_t launch_dims(const fa::Problem& p, const fa::ScoreMods& m, const CUtensorMap* maps, const ScoredBwdParams& bp,
                         cudaStream_t stream) {
   switch (m.bits()) {
     case 0:
@@ -19,7 +19,7 @@ cudaError_t launch_dims(const fa::Problem& p, const fa::ScoreMods& m, const CUte
 
 }  // namespace
 
-cudaError_t fa::launch_bwd_scored_128(const Problem& p, const ScoreMods& m, const CUtensorMap* maps, const BwdParams& bp,
+cudaError_t fa::launch_bwd_scored_128(const Problem& p, const ScoreMods& m, const CUtensorMap* maps, const ScoredBwdParams& bp,
                                      cudaStream_t stream) {
   return p.dv == 64 ? launch_dims<64>(p, m, maps, bp, stream) : launch_dims<128>(p, m, maps, bp, stream);
 }

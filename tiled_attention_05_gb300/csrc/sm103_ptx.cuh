@@ -317,15 +317,40 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t f2_abs(uint64_t v) { return v & 0x7fffffff7fffffffull; }
 __device__ __forceinline__ uint64_t f2_neg(uint64_t v) { return v ^ 0x8000000080000000ull; }
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// min that keeps NaN (fminf would replace it)
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+// The tanh cap of four scores: with e = exp2(z), z = 2 x log2(e) / c,
+//   tanh(x / c) = 1 - 2 r,  r = 1 / (1 + e),
+// and the derivative 1 - tanh^2 = 4 e r^2.  One reciprocal serves all four: the
+// product of the four sums stays below 2^121 because z is held at 30, where
+// tanh is 1 to 2^-29.  (A reciprocal for each is the slower part: the special
+// function unit gives 16 a clock and SM, against 32 of ex2.)
+__device__ __forceinline__ void cap_quad(uint64_t z01, uint64_t z23, uint64_t& r01, uint64_t& r23, uint64_t& e01,
+                                         uint64_t& e23) {
+  constexpr float kTop = 30.f;
+  e01 = f2_pack(ex2(min_nan(f2_lo(z01), kTop)), ex2(min_nan(f2_hi(z01), kTop)));
+  e23 = f2_pack(ex2(min_nan(f2_lo(z23), kTop)), ex2(min_nan(f2_hi(z23), kTop)));
+  const uint64_t one = f2_pack(1.f, 1.f);
+  const uint64_t d01 = f2_add(e01, one), d23 = f2_add(e23, one);
+  const uint64_t d02_13 = f2_mul(d01, d23);                 // (d0 d2, d1 d3)
+  const float all = rcp(f2_lo(d02_13) * f2_hi(d02_13));     // 1 / (d0 d1 d2 d3)
+  const uint64_t i02_13 = f2_mul(f2_pack(f2_hi(d02_13), f2_lo(d02_13)), f2_pack(all, all));  // (1/(d0 d2), 1/(d1 d3))
+  r01 = f2_mul(i02_13, d23);
+  r23 = f2_mul(i02_13, d01);
+}
 // max of three (sm_100+ three-input form)
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 // Two fp32 -> packed bf16x2 (round to nearest even); `lo` lands in the low half.
