@@ -254,8 +254,7 @@ cudaError_t launch_backward(const Problem& pr, const ScoreMods& mods, const void
   bp.scale_grad = scale_grad(pr, mods);
   bp.scale_log2 = pr.scale * 1.4426950408889634f;
   bp.test_withhold_do = fa::test_withhold() == fa::kWithholdBwdDO;
-  bp.cap_log2 = mods.softcap * 1.4426950408889634f;
-  bp.cap_in = mods.softcap > 0.f ? 2.f * bp.scale_log2 / mods.softcap : 0.f;
+  bp.cap = cap_params(mods.softcap, pr.scale);
   bp.slopes = mods.slopes;
   bp.hi_off = row_hi_off(pr);
   bp.lo_off = row_lo_off(pr);

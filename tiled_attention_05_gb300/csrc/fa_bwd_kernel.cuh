@@ -208,8 +208,8 @@ using BwdParamsOf = std::conditional_t<SCORE >= 0, ScoredBwdParams, BwdParams>;
 template <bool CAP, bool SLOPES, bool MASKED, bool BOTH>
 __device__ __forceinline__ void modified_chunk(const ScoredBwdParams& p, const uint32_t (&sr)[32], const float4* lse,
                                                int rel0, float slope2, uint32_t vis, float* pr, uint32_t (&pk)[16]) {
-  const float in = CAP ? p.cap_in : p.scale_log2;
-  const uint64_t in2 = f2_pack(in, in), m2cap2 = f2_pack(-2.f * p.cap_log2, -2.f * p.cap_log2);
+  const float in = CAP ? p.cap.in : p.scale_log2;
+  const uint64_t in2 = f2_pack(in, in), m2cap2 = f2_pack(-2.f * p.cap.log2c, -2.f * p.cap.log2c);
   const float side = rel0 + 31 <= 0 ? slope2 : -slope2;  // bias per step of the query
   uint64_t step[2];
 #pragma unroll
@@ -223,18 +223,18 @@ __device__ __forceinline__ void modified_chunk(const ScoredBwdParams& p, const u
                      f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]))};
     uint64_t r[2], e[2];
     if (CAP) cap_quad(f2_mul(x[0], in2), f2_mul(x[1], in2), r[0], r[1], e[0], e[1]);
-    const float gb = fmaf(rel + (float)c, side, CAP ? p.cap_log2 : 0.f);  // (the sum is exact)
+    const float gb = fmaf(rel + (float)c, side, CAP ? p.cap.log2c : 0.f);  // (the sum is exact)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint64_t bias;  // (cap +) distance bias - row statistic
       if (SLOPES && BOTH) {
         const float d0 = (float)(rel0 + c + 2 * h), d1 = (float)(rel0 + c + 2 * h + 1);
-        bias = f2_sub(f2_pack(fmaf(fabsf(d0), -slope2, CAP ? p.cap_log2 : 0.f),
-                              fmaf(fabsf(d1), -slope2, CAP ? p.cap_log2 : 0.f)), l[h]);
+        bias = f2_sub(f2_pack(fmaf(fabsf(d0), -slope2, CAP ? p.cap.log2c : 0.f),
+                              fmaf(fabsf(d1), -slope2, CAP ? p.cap.log2c : 0.f)), l[h]);
       } else if (SLOPES) {
         bias = f2_sub(f2_add(step[h], f2_pack(gb, gb)), l[h]);
       } else if (CAP) {
-        bias = f2_sub(f2_pack(p.cap_log2, p.cap_log2), l[h]);
+        bias = f2_sub(f2_pack(p.cap.log2c, p.cap.log2c), l[h]);
       } else {
         bias = f2_neg(l[h]);
       }

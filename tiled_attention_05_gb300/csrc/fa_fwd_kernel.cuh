@@ -160,8 +160,7 @@ struct FwdParams {
 
 // What the score-modified instances need besides (see fa::ScoreMods).
 struct ScoredFwdParams : FwdParams {
-  float cap_log2;       // c * log2(e)
-  float cap_in;         // 2 * scale * log2(e) / c
+  fa::CapParams cap;
   const float* slopes;  // [Hq]
   int hi_off, lo_off;   // row i sees keys [i + lo_off, i + hi_off) (no plan)
   int q_tiles;
@@ -264,53 +263,259 @@ __device__ __forceinline__ bool fwd_item(const FwdParamsOf<SCORE>& p, int n, Fwd
   return true;
 }
 
-// Scores of one row and key tile, in place: raw q.k -> log2 units with the cap
-// and the distance bias.  rel0: key of column 0 minus the row's own position.
-// BOTH: the row's own position may lie inside the tile with keys visible on
-// both sides of it; otherwise all visible keys are on one side and the bias is
-// a line in the column, built from eight slopes and one base per eight columns.
-template <bool CAP, bool SLOPES, bool BOTH>
-__device__ __forceinline__ void modify_scores(uint32_t (&sr)[BN], const ScoredFwdParams& p, int rel0, float slope2) {
-  if constexpr (CAP || SLOPES) {
-    const uint64_t in2 = CAP ? f2_pack(p.cap_in, p.cap_in) : f2_pack(p.scale_log2, p.scale_log2);
-    const uint64_t cap2 = f2_pack(p.cap_log2, p.cap_log2), m2cap2 = f2_pack(-2.f * p.cap_log2, -2.f * p.cap_log2);
-    const float s2 = rel0 >= 0 ? -slope2 : slope2;
-    const float rel = (float)rel0;
-    uint64_t step[4];
+// The polynomial of fa::CapParams without its leading factor s, of u = s^2.
+__device__ __forceinline__ uint64_t cap_poly(const fa::CapParams& c, uint64_t u) {
+  uint64_t t = f2_fma(u, f2_pack(c.a[3], c.a[3]), f2_pack(c.a[2], c.a[2]));
+  t = f2_fma(u, t, f2_pack(c.a[1], c.a[1]));
+  return f2_fma(u, t, f2_pack(c.a[0], c.a[0]));
+}
+
+// Bits of the columns [lo, lim).
+__device__ __forceinline__ void interval_bits(int lo, int lim, uint32_t (&vis)[BN / 32]) {
+#pragma unroll
+  for (int k = 0; k < BN / 32; ++k) {
+    const int from = min(max(lo - 32 * k, 0), 32), to = min(max(lim - 32 * k, 0), 32);
+    vis[k] = (uint32_t)(((1ull << to) - 1) & ~((1ull << from) - 1));
+  }
+}
+
+// Plans whose documents are not in order: takes the keys of other documents out
+// of vis, unless every row of the warp has the document of the whole key tile
+// (then false).
+__device__ __noinline__ bool document_bits(uint32_t (&vis)[BN / 32], const ScoredFwdParams& p, int batch, int kv0,
+                                           int my_doc) {
+  const size_t tile = (size_t)batch * p.kv_tiles + kv0 / BN;
+  const int lo = p.plan.tile_doc_lo[tile], hi = p.plan.tile_doc_hi[tile];
+  if (__all_sync(0xffffffffu, lo == my_doc && hi == my_doc)) return false;
+  const int* doc = p.plan.k_doc + tile * BN;
+  for (int k = 0; k < BN / 32; ++k) {
+    uint32_t bits = 0u;
+    for (int c = 0; c < 32; ++c) bits |= (uint32_t)(__ldg(doc + 32 * k + c) == my_doc) << c;
+    vis[k] &= bits;
+  }
+  return true;
+}
+
+// The distance bias of one row and key tile is a line in the column: it rises up to
+// the row's own position and falls from there on (or all the way, where the tile
+// starts there).  slope2: bias per step of the distance (log2 units); rel0: key of
+// column 0 minus the row's position.
+struct BiasLine {
+  float s2, rel;     // per column; rel0
+  uint64_t step[4];  // s2 * (0, 1), (2, 3), (4, 5), (6, 7)
+  __device__ __forceinline__ BiasLine(int rel0, float slope2) : s2(rel0 >= 0 ? -slope2 : slope2), rel((float)rel0) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) step[k] = f2_pack((float)(2 * k) * s2, (float)(2 * k + 1) * s2);
+  }
+  // Bias of column g (a multiple of 8) plus `more`.  rel + g is exact: a key near
+  // the row is biased by few steps, so nothing large cancels there.
+  __device__ __forceinline__ float at(int g, float more) const { return fmaf(rel + (float)g, s2, more); }
+};
+
+// One key tile of a capped row whose cap bounds every score (kBounded).  P = 2^x,
+// with slopes 2^(x + bias - m_ref), needs no running maximum: m_ref is the
+// greatest bias of a key the row sees.  So the scores stream through 32 columns
+// at a time, each written back as bf16 P over scores already read.  The cap is
+// taken by its polynomial; from the first score beyond it on (in any row of the
+// warp), the rest of the tile goes by the form that holds everywhere (the scores
+// are still in TMEM).  Returns the row's sum of P.
+// MASKED: only the columns in vis4 count, and the row's position may be inside
+// the tile with visible keys on both sides.
+// The loop stays rolled: unrolled, its instructions crowd the MMA thread's out of
+// the instruction cache (T 8192, d 128: 925 us rolled, 1005 unrolled; two
+// warpgroups of 64 columns each per tile: 980 and 1025).
+template <bool SLOPES, bool MASKED>
+__device__ __forceinline__ float bounded_tile(uint32_t tS, const ScoredFwdParams& p, const uint32_t (&vis4)[BN / 32],
+                                              int rel0, float slope2, float m_ref) {
+  uint64_t rs[2] = {0ull, 0ull};
+  bool small = true;
+  BiasLine line(rel0, slope2);
+#pragma unroll 1
+  for (int ch = 0; ch < BN / 32; ++ch) {
+    const uint32_t vis = MASKED ? (ch < 2 ? (ch == 0 ? vis4[0] : vis4[1]) : (ch == 2 ? vis4[2] : vis4[3])) : 0u;
+    const float relc = line.rel + (float)(32 * ch);
+    uint32_t s[32], pk[16];
+    uint64_t part[2] = {0ull, 0ull};
+    auto take = [&](int c, uint64_t x01, uint64_t x23) {  // four capped scores -> P and the sums
+      float v0 = ex2(f2_lo(x01)), v1 = ex2(f2_hi(x01)), v2 = ex2(f2_lo(x23)), v3 = ex2(f2_hi(x23));
+      if (MASKED) {
+        if (!((vis >> c) & 1u)) v0 = 0.f;
+        if (!((vis >> (c + 1)) & 1u)) v1 = 0.f;
+        if (!((vis >> (c + 2)) & 1u)) v2 = 0.f;
+        if (!((vis >> (c + 3)) & 1u)) v3 = 0.f;
+      }
+      part[0] = f2_add(part[0], f2_pack(v0, v1));
+      part[1] = f2_add(part[1], f2_pack(v2, v3));
+      pk[c / 2] = pack_bf16x2(v0, v1);
+      pk[c / 2 + 1] = pack_bf16x2(v2, v3);
+    };
+    auto pair = [&](int c) { return f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])); };
+    // the bias of columns c, c + 1 of this chunk plus `more`
+    auto bias = [&](int c, float more) -> uint64_t {
+      if (!SLOPES) return f2_pack(more, more);
+      if (MASKED) {
+        const float far0 = fabsf(relc + (float)c), far1 = fabsf(relc + (float)(c + 1));
+        return f2_pack(fmaf(far0, -slope2, more - m_ref), fmaf(far1, -slope2, more - m_ref));
+      }
+      const float g = fmaf(relc + (float)(c & ~7), line.s2, more - m_ref);
+      return f2_add(line.step[(c & 7) / 2], f2_pack(g, g));
+    };
+    if (small) {
+      tmem_ld32(tS + ch * 32, s);
+      tmem_wait_ld();
+      float top = 0.f;  // greatest s^2
 #pragma unroll
-    for (int g = 0; g < BN; g += 8) {
-      // (rel + g is exact: a key near the row is biased by few steps, so that
-      // nothing large cancels there)
-      const float gb = fmaf(rel + (float)g, s2, CAP ? p.cap_log2 : 0.f);
-      const uint64_t base2 = f2_pack(gb, gb);
+      for (int c = 0; c < 32; c += 4) {
+        const uint64_t u01 = f2_mul(pair(c), pair(c)), u23 = f2_mul(pair(c + 2), pair(c + 2));
+        top = fmax3(fmax3(top, f2_lo(u01), f2_hi(u01)), f2_lo(u23), f2_hi(u23));
+        const uint64_t t01 = cap_poly(p.cap, u01), t23 = cap_poly(p.cap, u23);
+        if (SLOPES)
+          take(c, f2_fma(pair(c), t01, bias(c, 0.f)), f2_fma(pair(c + 2), t23, bias(c + 2, 0.f)));
+        else
+          take(c, f2_mul(pair(c), t01), f2_mul(pair(c + 2), t23));
+      }
+      small = !__any_sync(0xffffffffu, top > p.cap.small2);
+    }
+    if (!small) {
+      const uint64_t in2 = f2_pack(p.cap.in, p.cap.in), m2cap2 = f2_pack(-2.f * p.cap.log2c, -2.f * p.cap.log2c);
+      part[0] = part[1] = 0ull;
+      tmem_ld32(tS + ch * 32, s);
+      tmem_wait_ld();
 #pragma unroll
-      for (int k = 0; k < 4; k += 2) {
-        const int c = g + 2 * k;
-        uint64_t x[2] = {f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
-                         f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]))};
-        uint64_t r[2], e[2];
-        if (CAP) cap_quad(f2_mul(x[0], in2), f2_mul(x[1], in2), r[0], r[1], e[0], e[1]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (SLOPES && BOTH) {
-            const float d0 = (float)(rel0 + c + 2 * h), d1 = (float)(rel0 + c + 2 * h + 1);
-            const uint64_t bias = f2_pack(fmaf(fabsf(d0), -slope2, CAP ? p.cap_log2 : 0.f),
-                                          fmaf(fabsf(d1), -slope2, CAP ? p.cap_log2 : 0.f));
-            x[h] = CAP ? f2_fma(r[h], m2cap2, bias) : f2_fma(x[h], in2, bias);
-          } else if (SLOPES) {
-            const uint64_t bias = f2_add(step[k + h], base2);
-            x[h] = CAP ? f2_fma(r[h], m2cap2, bias) : f2_fma(x[h], in2, bias);
-          } else {
-            x[h] = f2_fma(r[h], m2cap2, cap2);
-          }
-          sr[c + 2 * h] = __float_as_uint(f2_lo(x[h]));
-          sr[c + 2 * h + 1] = __float_as_uint(f2_hi(x[h]));
-        }
+      for (int c = 0; c < 32; c += 4) {
+        uint64_t r01, r23, e01, e23;
+        cap_quad(f2_mul(pair(c), in2), f2_mul(pair(c + 2), in2), r01, r23, e01, e23);
+        take(c, f2_fma(r01, m2cap2, bias(c, p.cap.log2c)), f2_fma(r23, m2cap2, bias(c + 2, p.cap.log2c)));
       }
     }
+    rs[0] = f2_add(rs[0], part[0]);
+    rs[1] = f2_add(rs[1], part[1]);
+    tmem_st16(tS + 16 * ch, pk);
   }
+  const uint64_t rs2 = f2_add(rs[0], rs[1]);
+  return f2_lo(rs2) + f2_hi(rs2);
+}
+
+// Slopes without a cap: two passes over the scores in TMEM, which keep few
+// registers and little code (see bounded_tile on code; one pass over a row held in
+// registers: 76 us against 65 at T 2048, d 64).
+//
+// First pass: the greatest score with its bias in one row and key tile (log2 units),
+// or a little more: of eight columns, the greatest score with the greatest bias,
+// which is over by at most seven steps of the slope.  Any reference near the
+// maximum serves the softmax.  MASKED: every visible column by itself (also where
+// seven steps of the slope are many).
+template <bool MASKED>
+__device__ __forceinline__ float line_max(uint32_t tS, float scale, const uint32_t (&vis4)[BN / 32], int rel0,
+                                          float slope2) {
+  float top[2] = {-__int_as_float(0x7f800000), -__int_as_float(0x7f800000)};
+  const BiasLine line(rel0, slope2);
+  if (MASKED) {
+#pragma unroll 1
+    for (int ch = 0; ch < BN / 32; ++ch) {
+      const uint32_t vis = ch < 2 ? (ch == 0 ? vis4[0] : vis4[1]) : (ch == 2 ? vis4[2] : vis4[3]);
+      const float relc = line.rel + (float)(32 * ch);
+      uint32_t s[32];
+      tmem_ld32(tS + ch * 32, s);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float x = fmaf(__uint_as_float(s[c]), scale, -slope2 * fabsf(relc + (float)c));
+        if ((vis >> c) & 1u) top[c & 1] = fmaxf(top[c & 1], x);
+      }
+    }
+  } else {
+    uint32_t s[BN];
+#pragma unroll
+    for (int ch = 0; ch < BN / 32; ++ch) tmem_ld32(tS + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[ch * 32]));
+    tmem_wait_ld();
+    const float more = fmaxf(0.f, 7.f * line.s2);
+#pragma unroll
+    for (int g = 0; g < BN; g += 8) {
+      auto f = [&](int c) { return __uint_as_float(s[g + c]); };
+      const float m = fmax3(fmax3(f(0), f(1), f(2)), fmax3(f(3), f(4), f(5)), fmaxf(f(6), f(7)));
+      top[(g >> 3) & 1] = fmaxf(top[(g >> 3) & 1], fmaf(m, scale, line.at(g, more)));
+    }
+  }
+  return fmaxf(top[0], top[1]);
+}
+// Second pass: P = 2^(score + bias - base) as bf16 over the scores; returns the row's
+// sum of P.
+template <bool MASKED>
+__device__ __forceinline__ float line_exp(uint32_t tS, float scale, const uint32_t (&vis4)[BN / 32], int rel0,
+                                          float slope2, float base) {
+  uint64_t rs[2] = {0ull, 0ull};
+  const BiasLine line(rel0, slope2);
+  const uint64_t scale2 = f2_pack(scale, scale);
+#pragma unroll 1
+  for (int ch = 0; ch < BN / 32; ++ch) {
+    const uint32_t vis = MASKED ? (ch < 2 ? (ch == 0 ? vis4[0] : vis4[1]) : (ch == 2 ? vis4[2] : vis4[3])) : 0u;
+    const float relc = line.rel + (float)(32 * ch);
+    uint32_t s[32], pk[16];
+    tmem_ld32(tS + ch * 32, s);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      uint64_t bias;
+      if (MASKED) {
+        bias = f2_pack(fmaf(fabsf(relc + (float)c), -slope2, -base), fmaf(fabsf(relc + (float)(c + 1)), -slope2, -base));
+      } else {
+        const float g = fmaf(relc + (float)(c & ~7), line.s2, -base);
+        bias = f2_add(line.step[(c & 7) / 2], f2_pack(g, g));
+      }
+      const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, bias);
+      float v0 = ex2(f2_lo(x)), v1 = ex2(f2_hi(x));
+      if (MASKED) {
+        if (!((vis >> c) & 1u)) v0 = 0.f;
+        if (!((vis >> (c + 1)) & 1u)) v1 = 0.f;
+      }
+      rs[(c >> 1) & 1] = f2_add(rs[(c >> 1) & 1], f2_pack(v0, v1));
+      pk[c / 2] = pack_bf16x2(v0, v1);
+    }
+    tmem_st16(tS + 16 * ch, pk);
+  }
+  const uint64_t rs2 = f2_add(rs[0], rs[1]);
+  return f2_lo(rs2) + f2_hi(rs2);
+}
+
+// Adds per_step * (key - position) to the scores of keys past the row's position.
+__device__ __forceinline__ void turn_over(uint32_t (&sr)[BN], int rel0, float per_step) {
+#pragma unroll
+  for (int c = 0; c < BN; ++c)
+    if (rel0 + c > 0 && rel0 < 0)
+      sr[c] = __float_as_uint(fmaf((float)(rel0 + c), per_step, __uint_as_float(sr[c])));
+}
+
+// Capped scores of one row and key tile, in place: raw q.k -> log2 units with the
+// cap and the distance bias (caps too wide for the bounded form, and plans that
+// compare documents key by key).  crossing: keys on both sides of the row's
+// position may be visible; the rising line is then turned over past it.  (Two
+// forms of the whole, each in a branch of its own, cost a move per score where
+// the branches meet: 1870 against 2550 cycles a tile with slopes alone.)
+template <bool SLOPES>
+__device__ __forceinline__ void cap_scores(uint32_t (&sr)[BN], const ScoredFwdParams& p, int rel0, float slope2,
+                                           bool crossing) {
+  const uint64_t in2 = f2_pack(p.cap.in, p.cap.in), cap2 = f2_pack(p.cap.log2c, p.cap.log2c);
+  const uint64_t m2cap2 = f2_pack(-2.f * p.cap.log2c, -2.f * p.cap.log2c);
+  const BiasLine line(rel0, slope2);
+#pragma unroll
+  for (int c = 0; c < BN; c += 4) {
+    const uint64_t s01 = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+    const uint64_t s23 = f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+    uint64_t r01, r23, e01, e23, b01 = cap2, b23 = cap2;
+    cap_quad(f2_mul(s01, in2), f2_mul(s23, in2), r01, r23, e01, e23);
+    if (SLOPES) {
+      const float g = line.at(c & ~7, p.cap.log2c);
+      b01 = f2_add(line.step[(c & 7) / 2], f2_pack(g, g));
+      b23 = f2_add(line.step[(c & 7) / 2 + 1], f2_pack(g, g));
+    }
+    const uint64_t x01 = f2_fma(r01, m2cap2, b01), x23 = f2_fma(r23, m2cap2, b23);
+    sr[c] = __float_as_uint(f2_lo(x01));
+    sr[c + 1] = __float_as_uint(f2_hi(x01));
+    sr[c + 2] = __float_as_uint(f2_lo(x23));
+    sr[c + 3] = __float_as_uint(f2_hi(x23));
+  }
+  if (SLOPES && crossing) turn_over(sr, rel0, -2.f * slope2);
 }
 
 // Plans whose documents are not in order: hides the keys of other documents one
@@ -511,12 +716,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (wait_kv && !fwd_wait(&kv_full[s], (pos / NS) & 1, abort_flag)) return false;
             tc_fence_after();
-            const uint32_t q_base = q_buf + x * C::Q_BYTES;
+            const uint64_t a0 = desc_kmajor(q_buf + x * C::Q_BYTES), b0 = desc_kmajor(k_base + s * C::K_BYTES);
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k) {
-              const uint64_t a = desc_kmajor(q_base + (k >> 2) * (BM * 128) + (k & 3) * 32);
-              const uint64_t bd = desc_kmajor(k_base + s * C::K_BYTES + (k >> 2) * (BN * 128) + (k & 3) * 32);
-              mma_ss(tmem + x * 128, a, bd, idS, k > 0 ? 1u : 0u);
+              const uint32_t step = (k >> 2) * (BM * 128) + (k & 3) * 32;
+              mma_ss(tmem + x * 128, desc_at(a0, step), desc_at(b0, step), idS, k > 0 ? 1u : 0u);
             }
             mma_commit(&s_full[x]);
             if (j == it.ke[x] - 1) mma_commit(&q_empty[x]);  // last reader of Q_X in this item
@@ -529,9 +733,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!fwd_wait(&p_full[x], np[x] & 1, abort_flag)) return false;
             ++np[x];
             tc_fence_after();
+            const uint64_t v0 = desc_mnmajor(v_base + s * C::V_BYTES, BN * 128);
 #pragma unroll
             for (int k = 0; k < BN / 16; ++k) {
-              const uint64_t bd = desc_mnmajor(v_base + s * C::V_BYTES + k * 2048, BN * 128);
+              const uint64_t bd = desc_at(v0, k * 2048);
               mma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, bd, idPV, (j > it.kb[x] || k > 0) ? 1u : 0u);
             }
             return true;
@@ -581,7 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + x * 128 + lane_base;
     const uint32_t tO = tmem + 256 + x * 128 + lane_base;
     constexpr bool CAP = SCORE >= 0 && (SCORE & fa::kCap), SLOPES = SCORE >= 0 && (SCORE & fa::kSlopes);
-    const float sl2 = (CAP || SLOPES) ? 1.f : p.scale_log2;  // what brings the (modified) scores to log2 units
+    constexpr bool BOUNDED = SCORE >= 0 && (SCORE & fa::kBounded);
+    const float sl2 = CAP ? 1.f : p.scale_log2;  // what brings the (capped) scores to log2 units
     const float NEG_INF = -__int_as_float(0x7f800000);
     int ns = 0, no = 0;  // s_full / o_done phases waited for
     int base = 0;        // ring position of the current item's first key tile
@@ -613,100 +819,144 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (SLOPES) slope2 = p.slopes[it.bh - batch * p.Hq] * 1.4426950408889634f;
       }
-      float m_ref = NEG_INF;  // reference max (log2 units) the P values are taken against
+      // reference max (log2 units) the P values are taken against
+      float m_ref = NEG_INF;
+      if (BOUNDED && !(SLOPES && by_key)) {
+        m_ref = 0.f;
+        if (SLOPES) {  // the greatest bias: of the nearest key the row sees, or the farthest (negative slopes)
+          const int to_lo = i + p.causal_off - row_lo, to_hi = i + p.causal_off - (row_hi - 1);
+          const int near = to_lo >= 0 && to_hi <= 0 ? 0 : min(abs(to_lo), abs(to_hi));
+          m_ref = -slope2 * (float)(slope2 >= 0.f ? near : max(abs(to_lo), abs(to_hi)));
+        }
+      }
       float l = 0.f;
       for (int jx = 0; ok && jx < nkv; ++jx) {  // jx-th key tile of this tile's range
         // the warp agrees on the outcome before its collective TMEM loads
         if (!__all_sync(0xffffffffu, fwd_wait(&s_full[x], ns & 1, abort_flag))) { ok = false; break; }
         ++ns;
         tc_fence_after();
-        uint32_t sr[BN];
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-        tmem_wait_ld();
         const int kv0 = (kbx + jx) * BN;
+        int lim = 0, lo = 0, rel0 = 0;  // (SCORE >= 0) columns [lo, lim) are visible to row i; column 0 minus its position
+        bool crossing = false;          // some row of the warp may see keys on both sides of its position in this tile
         if constexpr (SCORE >= 0) {
-          const int lim = row_hi - kv0, lo = row_lo - kv0;  // columns [lo, lim) are visible to row i
-          const int rel0 = kv0 - p.causal_off - i;
-          if (SLOPES && p.two_sided && __any_sync(0xffffffffu, rel0 < 0 && rel0 + BN > 1))
-            modify_scores<CAP, SLOPES, SLOPES>(sr, p, rel0, slope2);
-          else
-            modify_scores<CAP, SLOPES, false>(sr, p, rel0, slope2);
-          if (__any_sync(0xffffffffu, lim < BN || lo > 0)) {
-#pragma unroll
-            for (int c = 0; c < BN; ++c)
-              if (c >= lim || c < lo) sr[c] = __float_as_uint(NEG_INF);
+          lim = row_hi - kv0;
+          lo = row_lo - kv0;
+          rel0 = kv0 - p.causal_off - i;
+          if (SLOPES) crossing = p.two_sided && __any_sync(0xffffffffu, rel0 < 0 && rel0 + BN > 1);
+        }
+        if (BOUNDED && !(SLOPES && by_key)) {
+          if constexpr (BOUNDED) {
+            uint32_t vis[BN / 32];
+            bool masked = crossing || __any_sync(0xffffffffu, lim < BN || lo > 0);
+            if (masked || by_key) {
+              interval_bits(lo, lim, vis);
+              if (by_key) masked = document_bits(vis, p, batch, kv0, my_doc) || masked;
+            }
+            l += masked ? bounded_tile<SLOPES, true>(tS, p, vis, rel0, slope2, m_ref)
+                        : bounded_tile<SLOPES, false>(tS, p, vis, rel0, slope2, m_ref);
           }
-          if (by_key) mask_documents(sr, p, batch, kv0, my_doc);
         } else {
-          // window: the tile's last row starts its window past this key tile's start
-          const bool win_mask = WINDOW && qx0 + BM - 1 + p.causal_off - p.window + 1 > kv0;
-          const bool need_mask = (kv0 + BN > p.Tk) || (CAUSAL && kv0 + BN - 1 > qx0 + p.causal_off) || win_mask;
-          if (need_mask) {
-            int lim = p.Tk - kv0;  // columns [lo, lim) are visible to row i
-            if (CAUSAL) lim = min(lim, i + p.causal_off + 1 - kv0);
-            const int lo = win_mask ? i + p.causal_off - p.window + 1 - kv0 : -BN;
+          constexpr bool LINE = SLOPES && !CAP;  // two passes over the scores in TMEM
+          uint32_t sr[BN], vis[BN / 32];         // the scores (in registers), or which columns count (LINE)
+          bool masked = false;
+          float mt2;  // row max, in log2 units
+          if constexpr (LINE) {
+            masked = crossing || __any_sync(0xffffffffu, lim < BN || lo > 0);
+            if (masked || by_key || fabsf(slope2) > 8.f) {
+              interval_bits(lo, lim, vis);
+              if (by_key) masked = document_bits(vis, p, batch, kv0, my_doc) || masked;
+              masked = masked || fabsf(slope2) > 8.f;
+            }
+            mt2 = masked ? line_max<true>(tS, sl2, vis, rel0, slope2) : line_max<false>(tS, sl2, vis, rel0, slope2);
+          } else {
 #pragma unroll
-            for (int c = 0; c < BN; ++c)
-              if (c >= lim || c < lo) sr[c] = __float_as_uint(NEG_INF);
+          for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+          tmem_wait_ld();
+          if constexpr (SCORE >= 0) {
+            if constexpr (CAP) cap_scores<SLOPES>(sr, p, rel0, slope2, crossing);
+            if (__any_sync(0xffffffffu, lim < BN || lo > 0)) {
+#pragma unroll
+              for (int c = 0; c < BN; ++c)
+                if (c >= lim || c < lo) sr[c] = __float_as_uint(NEG_INF);
+            }
+            if (by_key) mask_documents(sr, p, batch, kv0, my_doc);
+          } else {
+            // window: the tile's last row starts its window past this key tile's start
+            const bool win_mask = WINDOW && qx0 + BM - 1 + p.causal_off - p.window + 1 > kv0;
+            const bool need_mask = (kv0 + BN > p.Tk) || (CAUSAL && kv0 + BN - 1 > qx0 + p.causal_off) || win_mask;
+            if (need_mask) {
+              int lim = p.Tk - kv0;  // columns [lo, lim) are visible to row i
+              if (CAUSAL) lim = min(lim, i + p.causal_off + 1 - kv0);
+              const int lo = win_mask ? i + p.causal_off - p.window + 1 - kv0 : -BN;
+#pragma unroll
+              for (int c = 0; c < BN; ++c)
+                if (c >= lim || c < lo) sr[c] = __float_as_uint(NEG_INF);
+            }
           }
-        }
-        // row max: eight independent three-input max chains (short dependency depth)
-        float pm[8];
+          // row max: eight independent three-input max chains (short dependency depth)
+          float pm[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) pm[k] = __uint_as_float(sr[k]);
+          for (int k = 0; k < 8; ++k) pm[k] = __uint_as_float(sr[k]);
 #pragma unroll
-        for (int c = 8; c + 16 <= BN; c += 16)
+          for (int c = 8; c + 16 <= BN; c += 16)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) pm[k] = fmax3(pm[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
+            for (int k = 0; k < 8; ++k) pm[k] = fmax3(pm[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], __uint_as_float(sr[BN - 8 + k]));
-        const float mt = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
-        const float mt2 = mt * sl2;
-        float m_new = m_ref;
-        if (mt2 > m_ref + kRescaleThreshold) m_new = mt2;  // also taken when m_ref == -inf
-        // Does this row's O need rescaling, and does any row of the warp's?  (The
-        // vote is taken here, where fewer registers are live than after exp2.)
-        const bool rescale = jx > 0 && m_new != m_ref && m_ref != NEG_INF;
-        const bool warp_rescale = __any_sync(0xffffffffu, rescale);
-        const float base = (m_new == NEG_INF) ? 0.f : m_new;
-        const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(-base, -base);
-        // exponentials (argument and row sum on packed pairs); P (packed bf16)
-        // goes over the already-loaded scores in TMEM 16 columns at a time
-        uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t xv = f2_fma(
-                f2_pack(__uint_as_float(sr[32 * c + 2 * e]), __uint_as_float(sr[32 * c + 2 * e + 1])), sl2x2, nbase2);
-            const float e0 = ex2(f2_lo(xv)), e1 = ex2(f2_hi(xv));
-            rs[e & 3] = f2_add(rs[e & 3], f2_pack(e0, e1));
-            pk[e] = pack_bf16x2(e0, e1);
+          for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], __uint_as_float(sr[BN - 8 + k]));
+          const float mt = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+          mt2 = mt * sl2;
           }
-          tmem_st16(tS + 16 * c, pk);
-        }
-        const uint64_t rs2 = f2_add(f2_add(rs[0], rs[1]), f2_add(rs[2], rs[3]));
-        const float rowsum = f2_lo(rs2) + f2_hi(rs2);
-        // O_X is idle here: the P.V of tile j-1 completed before S_X(j) did.
-        const float alpha = (m_new == m_ref) ? 1.f : (m_ref == NEG_INF ? 0.f : ex2(m_ref - m_new));
-        l = l * alpha + rowsum;
-        // TMEM loads and stores are warp-collective: when any row of the warp
-        // must rescale its O row, every lane takes part (factor 1 where not).
-        if (warp_rescale) {
-          const float a = rescale ? alpha : 1.f;
+          float m_new = m_ref;
+          if (mt2 > m_ref + kRescaleThreshold) m_new = mt2;  // also taken when m_ref == -inf
+          // Does this row's O need rescaling, and does any row of the warp's?  (The
+          // vote is taken here, where fewer registers are live than after exp2.)
+          const bool rescale = jx > 0 && m_new != m_ref && m_ref != NEG_INF;
+          const bool warp_rescale = __any_sync(0xffffffffu, rescale);
+          const float base = (m_new == NEG_INF) ? 0.f : m_new;
+          float rowsum;
+          if constexpr (LINE) {
+            rowsum = masked ? line_exp<true>(tS, sl2, vis, rel0, slope2, base)
+                            : line_exp<false>(tS, sl2, vis, rel0, slope2, base);
+          } else {
+          const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(-base, -base);
+          // exponentials (argument and row sum on packed pairs); P (packed bf16)
+          // goes over the already-loaded scores in TMEM 16 columns at a time
+          uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-          for (int c = 0; c < HDV / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + c * 32, o);
-            tmem_wait_ld();
+          for (int c = 0; c < BN / 32; ++c) {
+            uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-            tmem_st32(tO + c * 32, o);
+            for (int e = 0; e < 16; ++e) {
+              const uint64_t xv = f2_fma(
+                  f2_pack(__uint_as_float(sr[32 * c + 2 * e]), __uint_as_float(sr[32 * c + 2 * e + 1])), sl2x2, nbase2);
+              const float e0 = ex2(f2_lo(xv)), e1 = ex2(f2_hi(xv));
+              rs[e & 3] = f2_add(rs[e & 3], f2_pack(e0, e1));
+              pk[e] = pack_bf16x2(e0, e1);
+            }
+            tmem_st16(tS + 16 * c, pk);
           }
+          const uint64_t rs2 = f2_add(f2_add(rs[0], rs[1]), f2_add(rs[2], rs[3]));
+          rowsum = f2_lo(rs2) + f2_hi(rs2);
+          }
+          // O_X is idle here: the P.V of tile j-1 completed before S_X(j) did.
+          const float alpha = (m_new == m_ref) ? 1.f : (m_ref == NEG_INF ? 0.f : ex2(m_ref - m_new));
+          l = l * alpha + rowsum;
+          // TMEM loads and stores are warp-collective: when any row of the warp
+          // must rescale its O row, every lane takes part (factor 1 where not).
+          if (warp_rescale) {
+            const float a = rescale ? alpha : 1.f;
+#pragma unroll
+            for (int c = 0; c < HDV / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+              tmem_st32(tO + c * 32, o);
+            }
+          }
+          m_ref = m_new;
         }
-        m_ref = m_new;
         tmem_wait_st();
         tc_fence_before();
         // The MMA thread takes this barrier as word that K / V of this tile's
@@ -812,8 +1062,7 @@ cudaError_t launch_fwd_t(const fa::Problem& pr, const fa::ScoreMods& mods, const
   p.n_items = p.n_full + 2 * (n_pair_items - p.n_full);
   p.scale_log2 = pr.scale * 1.4426950408889634f;
   if constexpr (SCORE >= 0) {
-    p.cap_log2 = mods.softcap * 1.4426950408889634f;
-    p.cap_in = mods.softcap > 0.f ? 2.f * p.scale_log2 / mods.softcap : 0.f;
+    p.cap = fa::cap_params(mods.softcap, pr.scale);
     p.slopes = mods.slopes;
     p.hi_off = fa::row_hi_off(pr);
     p.lo_off = fa::row_lo_off(pr);

@@ -50,7 +50,14 @@ cudaError_t allow_dynamic_smem(const void* kernel, int bytes);
 
 // ---------------------------------------------------------------- score modifications
 // Bits of the kernels' SCORE template argument; kPlain compiles none of it.
-enum ScoreBits : int { kPlain = -1, kCap = 1, kSlopes = 2 };
+// kBounded (forward, with kCap): the cap keeps 2^score inside fp32, so the
+// softmax needs no running maximum.
+enum ScoreBits : int { kPlain = -1, kCap = 1, kSlopes = 2, kBounded = 4 };
+
+// Largest cap (log2 units) of the bounded form: 2^-90 <= P <= 2^90, so that P, its
+// sums over 2^30 keys and its products with values down to 2^-36 are normal
+// numbers of bf16 and fp32.  In natural units a cap of 62.
+constexpr float kBoundedCapLog2 = 90.f;
 
 struct ScoreMods {
   float softcap = 0.f;            // c > 0: x = c tanh(x / c)
@@ -58,6 +65,9 @@ struct ScoreMods {
   const void* plan = nullptr;     // mask plan (documents, prefixes) for the same dims
   bool any() const { return softcap > 0.f || slopes || plan; }
   int bits() const { return (softcap > 0.f ? kCap : 0) | (slopes ? kSlopes : 0); }
+  int fwd_bits() const {
+    return softcap > 0.f && softcap * 1.4426950408889634f <= kBoundedCapLog2 ? bits() | kBounded : bits();
+  }
 };
 
 // Without a plan, row i sees keys [i + lo_off, i + hi_off) within [0, Tk);
@@ -65,6 +75,31 @@ struct ScoreMods {
 constexpr int kFar = 1 << 30;
 inline int row_hi_off(const Problem& p) { return p.causal ? p.Tk - p.Tq + 1 : kFar; }
 inline int row_lo_off(const Problem& p) { return p.causal && p.window ? p.Tk - p.Tq - p.window + 1 : -kFar; }
+
+// The cap, for the kernels.  c * tanh(s * scale / c) in log2 units of a raw score s:
+//   everywhere  log2c - 2 log2c / (1 + exp2(in * s));
+//   for s^2 <= small2, i.e. arguments y = s * scale / c up to 1/2, where scores
+//   mostly are (a cap of 50 and scores up to 25):  s * (a0 + u (a1 + u (a2 + u a3))),
+//   u = s^2.  The odd polynomial of degree 7 has the least greatest error there,
+//   1.3e-7 of c (fitted to tanh(y) / y in y^2 by reweighted least squares); in fp32
+//   1.6e-7.  It needs no special function, of which the other form takes 1 1/4.
+struct CapParams {
+  float log2c, in, small2, a[4];
+};
+inline CapParams cap_params(float softcap, float scale) {
+  CapParams c = {};
+  if (!(softcap > 0.f)) return c;
+  const double b[4] = {0.9999976761926945, -0.33320655218172035, 0.13145145656354004, -0.04337248367772688};
+  const double log2e = 1.4426950408889634, k = (double)scale / softcap;
+  c.log2c = (float)(softcap * log2e);
+  c.in = (float)(2.0 * scale * log2e / softcap);
+  // (past k = 1000 the coefficients could leave fp32: the first form then serves all)
+  const bool fits = k < 1000.0;
+  c.small2 = fits ? (float)(0.25 / (k * k)) : -1.f;
+  double f = scale * log2e;
+  for (int i = 0; i < 4; ++i, f *= k * k) c.a[i] = fits ? (float)(b[i] * f) : 0.f;
+  return c;
+}
 
 // The cap's derivative is 4 r (1 - r); the kernels leave the 4 to this factor.
 inline float scale_grad(const Problem& p, const ScoreMods& m) { return m.softcap > 0.f ? 4.f * p.scale : p.scale; }
@@ -176,7 +211,7 @@ struct BwdParams {
 };
 // What the score-modified instances need besides (see ScoreMods).
 struct ScoredBwdParams : BwdParams {
-  float cap_log2, cap_in;  // c * log2(e), 2 * scale * log2(e) / c
+  CapParams cap;
   const float* slopes;     // [Hq]
   int hi_off, lo_off;      // row i sees keys [i + lo_off, i + hi_off) (no plan)
   int two_sided;           // a row may see keys on both sides of its own position

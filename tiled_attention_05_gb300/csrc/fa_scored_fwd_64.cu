@@ -6,11 +6,15 @@ namespace {
 template <int HDV>
 cudaError_t launch_dims(const fa::Problem& p, const fa::ScoreMods& m, const CUtensorMap& mq, const CUtensorMap& mk,
                         const CUtensorMap& mv, void* O, float* L, cudaStream_t stream) {
-  switch (m.bits()) {
+  switch (m.fwd_bits()) {
     case 0:
       return launch_fwd_t<64, HDV, false, false, 0>(p, m, mq, mk, mv, O, L, stream);
     case fa::kCap:
       return launch_fwd_t<64, HDV, false, false, fa::kCap>(p, m, mq, mk, mv, O, L, stream);
+    case fa::kCap | fa::kBounded:
+      return launch_fwd_t<64, HDV, false, false, fa::kCap | fa::kBounded>(p, m, mq, mk, mv, O, L, stream);
+    case fa::kCap | fa::kSlopes | fa::kBounded:
+      return launch_fwd_t<64, HDV, false, false, fa::kCap | fa::kSlopes | fa::kBounded>(p, m, mq, mk, mv, O, L, stream);
     case fa::kSlopes:
       return launch_fwd_t<64, HDV, false, false, fa::kSlopes>(p, m, mq, mk, mv, O, L, stream);
   }

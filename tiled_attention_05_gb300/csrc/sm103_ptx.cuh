@@ -154,6 +154,12 @@ __device__ __forceinline__ uint64_t desc_mnmajor(uint32_t saddr, uint32_t mn_blo
   return smem_desc_sw128(saddr, mn_block_bytes, 1024);
 }
 
+// The descriptor `bytes` further on (inside the 18-bit shared-memory window):
+// only the low word's address field changes.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
+  return (desc & 0xffffffff00000000ull) | (uint32_t)((uint32_t)desc + (bytes >> 4));
+}
+
 // Instruction descriptor, kind::f16 with bf16 A/B and fp32 D.
 // a_mn / b_mn: operand is MN-major (1) or K-major (0).
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
