@@ -15,9 +15,11 @@
 //   empty interval in its place of the order; the backward gives such a row no
 //   weight anyway (its L is -inf).
 //
-// Small and bound by latency: a cluster of 8 CTAs per batch entry, three
-// phases over keys, rows and keys again, with cluster barriers between them;
-// the arrays stay in L2.
+// Small and bound by latency, of which the first fetch of its instructions is the
+// larger part: a cluster of 8 CTAs per batch entry, three phases over keys, rows
+// and keys again with cluster barriers between them (0.3 us each), and as little
+// code as will do.  (T 8192: 16.3 us with four rows' searches a lane unrolled side
+// by side, 14.4 us rolled, with the searches in global memory.)
 #include <climits>
 #include <cooperative_groups.h>
 #include <cstdint>
@@ -28,8 +30,10 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
+constexpr int kGroup = kThreads / fa::kTile;  // tiles a CTA takes at a time
 constexpr int kCtas = fa::kPlanCtas;
+constexpr int kMaxSmem = 200 << 10;
 constexpr int kNoKeyDoc = INT_MAX, kNoRowDoc = -1;  // unlike each other and every document
 constexpr int T = fa::kTile;
 
@@ -38,23 +42,29 @@ struct PlanParams {
   int *row_lo, *row_hi, *q_doc, *k_doc, *kv_beg, *kv_end, *key_from, *key_to, *m_beg, *m_end, *tile_doc_lo,
       *tile_doc_hi, *by_key, *by_row;
   int Tq, Tk, q_tiles, kv_tiles, causal, window, prefix_per_row;
+  int room;  // ints of dynamic shared memory
 };
 
 __device__ __forceinline__ bool is_doc(int id) { return id >= 0 && id != INT_MAX; }
 
-// First index in [0, n) with a[index] > v (upper) or >= v; n if there is none.
-template <bool UPPER>
-__device__ __forceinline__ int search(const int* a, int n, int v) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = (int)(((unsigned)lo + (unsigned)hi) >> 1);
-    const int x = a[mid];
-    if (UPPER ? x > v : x >= v)
-      hi = mid;
-    else
-      lo = mid + 1;
+// How many entries of the ascending arrays a0, a1 (n each) are <= v0, v1.
+__device__ __noinline__ int2 search(const int* a0, const int* a1, int n, int v0, int v1) {
+  int c0 = 0, c1 = 0;
+#pragma unroll 1
+  for (int step = n > 0 ? 1 << (31 - __clz(n)) : 0; step > 0; step >>= 1) {
+    if (c0 + step <= n && a0[c0 + step - 1] <= v0) c0 += step;
+    if (c1 + step <= n && a1[c1 + step - 1] <= v1) c1 += step;
   }
-  return lo;
+  return make_int2(c0, c1);
+}
+
+// An array of n entries as the search reads it: copied to shared memory where it
+// fits (`room` entries), since every step of a search in global memory is a miss
+// of ~0.3 us.
+__device__ __forceinline__ const int* staged(const int* a, int n, int* buf, int room) {
+  if (n > room) return a;
+  for (int k = threadIdx.x; k < n; k += kThreads) buf[k] = a[k];
+  return buf;
 }
 
 __device__ __forceinline__ bool any_flag(const int* flags) {
@@ -65,6 +75,7 @@ __device__ __forceinline__ bool any_flag(const int* flags) {
 }
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) fa_mask_plan_kernel(const PlanParams p) {
+  extern __shared__ int buf[];
   cg::cluster_group cluster = cg::this_cluster();
   const int b = blockIdx.x / kCtas, cta = blockIdx.x % kCtas;
   const int lane = threadIdx.x & 31;
@@ -79,10 +90,11 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) fa_mas
 
   // ---- keys: documents without the padding's ids, their order, each tile's span
   int bad = 0;
+#pragma unroll 1
   for (int n = warp; n < p.kv_tiles; n += warps) {
     int lo = INT_MAX, hi = -1;
     bool none = false;
-#pragma unroll
+#pragma unroll 1
     for (int e = 0; e < T / 32; ++e) {
       const int j = n * T + e * 32 + lane;
       int d = kNoKeyDoc;
@@ -109,96 +121,104 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) fa_mas
   }
   bad = __syncthreads_or(bad);
   if (threadIdx.x == 0) p.by_key[b * kCtas + cta] = bad;
-  __threadfence();
   cluster.sync();
 
-  // ---- rows: intervals, and the key tiles of each query tile
+  // ---- rows: intervals, and the key tiles of each query tile (one row a thread)
+  __shared__ int w_beg[kThreads / 32], w_end[kThreads / 32], w_dmin[kThreads / 32], w_dmax[kThreads / 32];
   const bool by_key = any_flag(p.by_key + b * kCtas);
-  for (int m = warp; m < p.q_tiles; m += warps) {
-    int beg = INT_MAX, end = 0, dmin = INT_MAX, dmax = -1;
-#pragma unroll
-    for (int e = 0; e < T / 32; ++e) {
-      const int i = m * T + e * 32 + lane;
-      int lo = p.Tk, hi = p.Tk, d = kNoRowDoc;  // rows past the last: empty, last in order
-      if (i < p.Tq) {
-        const int id = doc_q ? doc_q[i] : 0;
-        const bool has = is_doc(id);
-        if (has) d = id;
-        lo = 0;
-        hi = p.Tk;
-        if (doc_q && !by_key) {
-          lo = search<false>(k_doc, p.Tk, has ? id : kNoKeyDoc);
-          hi = has ? search<true>(k_doc, p.Tk, id) : lo;
-        } else if (!has) {
-          hi = 0;
-        }
-        if (p.causal) {
-          int seen = i + off + 1;
-          if (p.in.prefix)
-            seen = max(seen, p.in.prefix[p.prefix_per_row ? (long long)b * p.Tq + i : (long long)b]);
-          hi = min(hi, max(seen, 0));
-        }
-        if (p.window) lo = max(lo, min(i + off - p.window + 1, p.Tk));
-        hi = max(hi, lo);
-        if (lo < hi) {
-          beg = min(beg, lo);
-          end = max(end, hi);
-          dmin = min(dmin, d);
-          dmax = max(dmax, d);
-        }
+  const int* sorted = doc_q && !by_key ? staged(k_doc, p.Tk, buf, p.room) : k_doc;
+  __syncthreads();
+#pragma unroll 1
+  for (int m0 = cta * kGroup; m0 < p.q_tiles; m0 += kCtas * kGroup) {
+    const int i = m0 * T + threadIdx.x, wid = threadIdx.x >> 5;
+    int lo = p.Tk, hi = p.Tk, d = kNoRowDoc;  // rows past the last: empty, last in order
+    if (i < p.Tq) {
+      const int id = doc_q ? doc_q[i] : 0;
+      const bool has = is_doc(id);
+      lo = 0;
+      hi = by_key && !has ? 0 : p.Tk;
+      if (doc_q && !by_key) {  // (padding rows: both ends where the keys' padding starts)
+        const int v = has ? id : kNoKeyDoc - 1;
+        const int2 ends = search(sorted, sorted, p.Tk, has ? v - 1 : v, v);
+        lo = ends.x;
+        hi = ends.y;
       }
+      if (has) d = id;
+      if (p.causal) {
+        int seen = i + off + 1;
+        if (p.in.prefix) seen = max(seen, p.in.prefix[p.prefix_per_row ? (long long)b * p.Tq + i : (long long)b]);
+        hi = min(hi, max(seen, 0));
+      }
+      if (p.window) lo = max(lo, min(i + off - p.window + 1, p.Tk));
+      hi = max(hi, lo);
+    }
+    if (i < p.q_tiles * T) {
       row_lo[i] = lo;
       row_hi[i] = hi;
       p.q_doc[qp + i] = d;
     }
-    beg = __reduce_min_sync(0xffffffffu, beg);
-    end = __reduce_max_sync(0xffffffffu, end);
-    int tb = 0, te = 0;
-    if (beg < end) {
-      tb = beg / T;
-      te = (end + T - 1) / T;
-      if (by_key) {  // only as far as tiles that can hold the rows' documents
-        dmin = __reduce_min_sync(0xffffffffu, dmin);
-        dmax = __reduce_max_sync(0xffffffffu, dmax);
-        int first = INT_MAX, last = -1;
-        for (int n = tb + lane; n < te; n += 32) {
-          const long long at = (long long)b * p.kv_tiles + n;
-          if (p.tile_doc_lo[at] <= dmax && p.tile_doc_hi[at] >= dmin) {
-            first = min(first, n);
-            last = max(last, n);
+    const bool sees = lo < hi;
+    const int beg = __reduce_min_sync(0xffffffffu, sees ? lo : INT_MAX), end = __reduce_max_sync(0xffffffffu, sees ? hi : 0);
+    const int dmin = __reduce_min_sync(0xffffffffu, sees ? d : INT_MAX), dmax = __reduce_max_sync(0xffffffffu, sees ? d : -1);
+    if (lane == 0) {
+      w_beg[wid] = beg;
+      w_end[wid] = end;
+      w_dmin[wid] = dmin;
+      w_dmax[wid] = dmax;
+    }
+    __syncthreads();
+    const int m = m0 + wid;
+    if (wid < kGroup && m < p.q_tiles) {  // one warp a tile
+      const int from = wid * (T / 32) + lane % (T / 32);
+      const int tbeg = __reduce_min_sync(0xffffffffu, w_beg[from]), tend = __reduce_max_sync(0xffffffffu, w_end[from]);
+      int tb = 0, te = 0;
+      if (tbeg < tend) {
+        tb = tbeg / T;
+        te = (tend + T - 1) / T;
+        if (by_key) {  // only as far as tiles that can hold the rows' documents
+          const int tmin = __reduce_min_sync(0xffffffffu, w_dmin[from]), tmax = __reduce_max_sync(0xffffffffu, w_dmax[from]);
+          int first = INT_MAX, last = -1;
+#pragma unroll 1
+          for (int n = tb + lane; n < te; n += 32) {
+            const long long at = (long long)b * p.kv_tiles + n;
+            if (p.tile_doc_lo[at] <= tmax && p.tile_doc_hi[at] >= tmin) {
+              first = min(first, n);
+              last = max(last, n);
+            }
           }
+          tb = __reduce_min_sync(0xffffffffu, first);
+          te = __reduce_max_sync(0xffffffffu, last) + 1;
+          if (te == 0) tb = 0;
         }
-        first = __reduce_min_sync(0xffffffffu, first);
-        last = __reduce_max_sync(0xffffffffu, last);
-        tb = last >= 0 ? first : 0;
-        te = last + 1;
+      }
+      if (lane == 0) {
+        p.kv_beg[(long long)b * p.q_tiles + m] = tb;
+        p.kv_end[(long long)b * p.q_tiles + m] = te;
       }
     }
-    if (lane == 0) {
-      p.kv_beg[(long long)b * p.q_tiles + m] = tb;
-      p.kv_end[(long long)b * p.q_tiles + m] = te;
-    }
+    __syncthreads();
   }
-  __threadfence();
   cluster.sync();
 
   // ---- keys again: the rows that see each, and the query tiles of each key tile
   bad = by_key;
-  for (int i = cta * kThreads + threadIdx.x; i < p.Tq; i += kCtas * kThreads)
-    if (i > 0) bad |= row_lo[i] < row_lo[i - 1] || row_hi[i] < row_hi[i - 1];
-  for (int n = warp; n < p.kv_tiles; n += warps) {
-#pragma unroll
-    for (int e = 0; e < T / 32; ++e) {
-      const int j = n * T + e * 32 + lane;
-      int from = 1 << 30, to = 0;
-      if (j < p.Tk) {
-        from = search<true>(row_hi, p.Tq, j);
-        to = search<true>(row_lo, p.Tq, j);
-      }
-      p.key_from[kp + j] = from;
-      p.key_to[kp + j] = to;
+  const int* his = staged(row_hi, p.Tq, buf, p.room / 2);
+  const int* los = staged(row_lo, p.Tq, buf + p.room / 2, p.room / 2);
+  __syncthreads();
+#pragma unroll 1
+  for (int t = cta * kThreads + threadIdx.x; t < max(p.Tq, p.kv_tiles * T); t += kCtas * kThreads) {
+    if (t > 0 && t < p.Tq) bad |= los[t] < los[t - 1] || his[t] < his[t - 1];
+    if (t < p.kv_tiles * T) {
+      int2 rows = make_int2(1 << 30, 0);
+      if (t < p.Tk) rows = search(his, los, p.Tq, t, t);
+      p.key_from[kp + t] = rows.x;
+      p.key_to[kp + t] = rows.y;
     }
+  }
+#pragma unroll 1
+  for (int n = warp; n < p.kv_tiles; n += warps) {
     int first = INT_MAX, last = -1;
+#pragma unroll 1
     for (int m = lane; m < p.q_tiles; m += 32) {
       const long long at = (long long)b * p.q_tiles + m;
       if (p.kv_beg[at] <= n && n < p.kv_end[at]) {
@@ -248,7 +268,13 @@ cudaError_t launch_mask_plan(const Problem& pr, const MaskInputs& in, void* plan
   p.causal = pr.causal;
   p.window = pr.window;
   p.prefix_per_row = in.prefix_per_row;
-  fa_mask_plan_kernel<<<(unsigned)pr.B * kCtas, kThreads, 0, stream>>>(p);
+  // room for the keys' documents, then for the rows' two ends
+  const long long want = 4 * (pr.Tk > 2LL * pr.Tq ? (long long)pr.Tk : 2LL * pr.Tq);
+  const int smem = (int)(want < kMaxSmem ? want : kMaxSmem);
+  p.room = smem / 4;
+  const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(fa_mask_plan_kernel), kMaxSmem);
+  if (e != cudaSuccess) return e;
+  fa_mask_plan_kernel<<<(unsigned)pr.B * kCtas, kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
