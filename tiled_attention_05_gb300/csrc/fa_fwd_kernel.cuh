@@ -234,10 +234,14 @@ __device__ __forceinline__ bool fwd_item(const FwdParamsOf<SCORE>& p, int n, Fwd
   const bool single = k >= p.n_full;
   it->single = single;
   const long long kp = single ? p.n_full + ((k - p.n_full) >> 1) : k;  // the pair
-  const int y = (int)(kp / p.n_bh);
+  int y = (int)(kp / p.n_bh);
   it->bh = (int)(kp - (long long)y * p.n_bh);
   const int b = it->bh / p.Hq, h = it->bh - b * p.Hq;
-  it->q0 = (p.n_pairs - 1 - y) * (2 * BM) + (single ? (int)((k - p.n_full) & 1) * BM : 0);
+  y = p.n_pairs - 1 - y;
+  if constexpr (SCORE >= 0) {  // a plan's heaviest pairs first
+    if (p.plan.kv_beg) y = min(max(p.plan.pair_order[(size_t)b * p.n_pairs + p.n_pairs - 1 - y], 0), p.n_pairs - 1);
+  }
+  it->q0 = y * (2 * BM) + (single ? (int)((k - p.n_full) & 1) * BM : 0);
   it->bkv = b * p.Hkv + h / p.G;
   kv_range_for<CAUSAL, WINDOW, SCORE>(p, b, it->q0, &it->kb[0], &it->ke[0]);
   if (single) {

@@ -114,12 +114,13 @@ struct PlanView {
   const int *kv_beg, *kv_end;          // key tiles a query tile visits
   const int *key_from, *key_to;        // key j is seen by rows [key_from, key_to), unless the flag by_row
   const int *m_beg, *m_end;            // query tiles a key tile visits
+  const int* pair_order;               // pairs of query tiles of a batch entry, most work first
   const int *tile_doc_lo, *tile_doc_hi;  // least and greatest document of a key tile
   const int *by_key, *by_row;          // [B][kPlanCtas], any nonzero: set
 };
 struct PlanLayout {
   long long row_lo, row_hi, q_doc, k_doc, kv_beg, kv_end, key_from, key_to, m_beg, m_end, tile_doc_lo, tile_doc_hi,
-      by_key, by_row, total;  // offsets in ints
+      pair_order, by_key, by_row, total;  // offsets in ints
 };
 inline PlanLayout plan_layout(const Problem& p) {
   const long long qt = (long long)p.B * p.q_tiles(), kt = (long long)p.B * p.kv_tiles();
@@ -142,6 +143,7 @@ inline PlanLayout plan_layout(const Problem& p) {
   l.m_end = take(kt);
   l.tile_doc_lo = take(kt);
   l.tile_doc_hi = take(kt);
+  l.pair_order = take((long long)p.B * ((p.q_tiles() + 1) / 2));
   l.by_key = take((long long)p.B * kPlanCtas);
   l.by_row = take((long long)p.B * kPlanCtas);
   l.total = at;
@@ -162,6 +164,7 @@ inline PlanView plan_view(const Problem& p, const void* plan) {
   v.key_to = a + l.key_to;
   v.m_beg = a + l.m_beg;
   v.m_end = a + l.m_end;
+  v.pair_order = a + l.pair_order;
   v.tile_doc_lo = a + l.tile_doc_lo;
   v.tile_doc_hi = a + l.tile_doc_hi;
   v.by_key = a + l.by_key;

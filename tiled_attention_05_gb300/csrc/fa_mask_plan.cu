@@ -40,7 +40,7 @@ constexpr int T = fa::kTile;
 struct PlanParams {
   fa::MaskInputs in;
   int *row_lo, *row_hi, *q_doc, *k_doc, *kv_beg, *kv_end, *key_from, *key_to, *m_beg, *m_end, *tile_doc_lo,
-      *tile_doc_hi, *by_key, *by_row;
+      *tile_doc_hi, *pair_order, *by_key, *by_row;
   int Tq, Tk, q_tiles, kv_tiles, causal, window, prefix_per_row;
   int room;  // ints of dynamic shared memory
 };
@@ -215,6 +215,26 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) fa_mas
       p.key_to[kp + t] = rows.y;
     }
   }
+  // pairs of query tiles by work (a step with both tiles costs 1.5 of one with a
+  // single tile): one warp a pair, which counts those before it
+  const int pairs = (p.q_tiles + 1) / 2;
+  const int *kv_beg = p.kv_beg + (long long)b * p.q_tiles, *kv_end = p.kv_end + (long long)b * p.q_tiles;
+  auto work = [&](int y) {
+    const int a = kv_end[2 * y] - kv_beg[2 * y], c = 2 * y + 1 < p.q_tiles ? kv_end[2 * y + 1] - kv_beg[2 * y + 1] : 0;
+    return 2 * max(a, c) + min(a, c);
+  };
+#pragma unroll 1
+  for (int y = warp; y < pairs; y += warps) {
+    const int w = work(y);
+    int before = 0;
+#pragma unroll 1
+    for (int z = lane; z < pairs; z += 32) {
+      const int v = work(z);
+      before += v > w || (v == w && z > y);  // (equal work: the later rows first)
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (lane == 0) p.pair_order[(long long)b * pairs + before] = y;
+  }
 #pragma unroll 1
   for (int n = warp; n < p.kv_tiles; n += warps) {
     int first = INT_MAX, last = -1;
@@ -259,6 +279,7 @@ cudaError_t launch_mask_plan(const Problem& pr, const MaskInputs& in, void* plan
   p.m_end = a + l.m_end;
   p.tile_doc_lo = a + l.tile_doc_lo;
   p.tile_doc_hi = a + l.tile_doc_hi;
+  p.pair_order = a + l.pair_order;
   p.by_key = a + l.by_key;
   p.by_row = a + l.by_row;
   p.Tq = pr.Tq;
