@@ -77,6 +77,8 @@ def lib_path() -> str:
 def load(path: str | None = None):
     """Load (building first if needed) the shared library; raises if that fails."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or _build.build()
@@ -152,6 +154,12 @@ def _check_all(device, specs):
     here: each (tensor, name, shape, dtype) must have exactly that shape, be a
     contiguous CUDA tensor of that dtype and live on ``device``.  Shapes are
     checked first so a mismatch is reported as such on any device."""
+    index = device.index if device.type == "cuda" else -2
+    for t, _, shape, dtype in specs:  # (a call's host time is mostly such checks: first without words)
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+            break
+    else:
+        return
     for t, name, shape, _ in specs:
         if tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -161,16 +169,26 @@ def _check_all(device, specs):
             raise ValueError(f"{name} is on {t.device}, expected {device} (all tensors on one GPU)")
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the current stream's handle, without an object
+
+
 def _stream_ptr(stream=None, device=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if device is not None and s.device != device:
-        raise ValueError(f"stream belongs to {s.device}, the tensors to {device}")
-    return s.cuda_stream
+    if stream is None:
+        if device is not None and _raw_stream is not None:
+            return _raw_stream(device.index)
+        stream = torch.cuda.current_stream(device)
+    if device is not None and stream.device != device:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+    return stream.cuda_stream
+
+
+def _current_device() -> int:
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
 
 
 def _on(device):
     """Makes ``device`` current for a call (nothing to do where it already is)."""
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if device.index == _current_device() else torch.cuda.device(device)
 
 
 def _raise(code: int, where: str):
@@ -275,15 +293,17 @@ def fa_forward(Q, K, V, causal: bool, scale: float | None = None, O=None, L=None
     if L is not None:
         specs.append((L, "L", (dims.B, dims.Hq, dims.Tq), f32))
     _check_all(Q.device, specs)
+    device = Q.device
     if O is None:
-        O = torch.empty(dims.B, dims.Hq, dims.Tq, dims.dv, dtype=bf, device=Q.device)
+        O = torch.empty_like(Q) if dims.dv == dims.d else torch.empty(dims.B, dims.Hq, dims.Tq, dims.dv, dtype=bf,
+                                                                      device=device)
     if L is None:
-        L = torch.empty(dims.B, dims.Hq, dims.Tq, dtype=f32, device=Q.device)
+        L = torch.empty((dims.B, dims.Hq, dims.Tq), dtype=f32, device=device)
     lib = load()
-    scores = _scores(dims, Q.device, softcap, slopes, mask, stream)
-    with _on(Q.device):
+    scores = _scores(dims, device, softcap, slopes, mask, stream)
+    with _on(device):
         code = lib.fa_forward_scored(ctypes.byref(dims), scores, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
-                                     O.data_ptr(), L.data_ptr(), _stream_ptr(stream, Q.device))
+                                     O.data_ptr(), L.data_ptr(), _stream_ptr(stream, device))
     _raise(code, "fa_forward")
     return O, L
 

@@ -25,68 +25,79 @@ import tiled_attention_05_gb300 as _fa
 
 
 def _heads(x, name, B, T, d, device):
-    if x.dim() != 4 or x.shape[0] != B or x.shape[2] != T or x.shape[3] != d:
+    """Strides (batch, head, token) of a [B, H, T, d] operand, checked."""
+    if x.dim() != 4:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected [{B}, H, {T}, {d}]")
+    xB, _, xT, xd = x.shape
+    if xB != B or xT != T or xd != d:
         raise ValueError(f"{name} has shape {tuple(x.shape)}, expected [{B}, H, {T}, {d}]")
     if not x.is_cuda or x.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be a CUDA {torch.bfloat16} tensor")
-    if x.device != device:
+    if x.get_device() != device.index:
         raise ValueError(f"{name} is on {x.device}, expected {device} (all tensors on one GPU)")
-    if x.numel() and (x.stride(3) != 1 or any(s % 8 for s in x.stride()[:3]) or x.data_ptr() % 16):
+    sb, sh, st, sd = x.stride()
+    if (sd != 1 or (sb | sh | st) & 7 or x.data_ptr() & 15) and x.numel():
         raise ValueError(f"{name} needs contiguous channels, strides of a multiple of 8 elements and 16-byte alignment")
+    return sb, sh, st
 
 
 def _rows_positions(positions, axes, B, T, device):
-    """positions as a view [axes, B, T] (stride 0 over what is shared)."""
+    """positions (or a copy with contiguous tokens), and its strides over axes
+    and batch rows (0 over what is shared)."""
     p = positions
-    if p.dtype not in (torch.int32, torch.int64):
+    if p.dtype != torch.int32 and p.dtype != torch.int64:
         raise ValueError("positions must be int32 or int64")
-    if p.dim() == 1 and axes == 1:
-        p = p.view(1, 1, -1)
-    elif p.dim() == 2:
-        p = p.unsqueeze(0) if axes == 1 else p.unsqueeze(1)
-    if p.dim() != 3 or p.shape[0] != axes or p.shape[1] not in (1, B) or p.shape[2] != T:
-        raise ValueError(f"positions has shape {tuple(positions.shape)}, expected [{axes}, {B}, {T}] or [{axes}, {T}]")
-    if not p.is_cuda or p.device != device:
+    shape = tuple(p.shape)
+    full = shape if len(shape) == 3 else (1,) + shape if len(shape) == 2 and axes == 1 else \
+        (axes, 1, shape[1]) if len(shape) == 2 and shape[0] == axes else (1, 1) + shape if axes == 1 else shape
+    if len(full) != 3 or full[0] != axes or full[1] not in (1, B) or full[2] != T:
+        raise ValueError(f"positions has shape {shape}, expected [{axes}, {B}, {T}] or [{axes}, {T}]")
+    if not p.is_cuda or p.get_device() != device.index:
         raise ValueError(f"positions is on {p.device}, expected {device} (all tensors on one GPU)")
-    p = p.expand(axes, B, T)
-    return p if T <= 1 or p.stride(2) == 1 else p.contiguous()
+    if T > 1 and p.stride(-1) != 1:
+        p = p.contiguous()
+    st = p.stride()
+    if len(shape) == 3:
+        return p, st[0], st[1] if full[1] == B else 0
+    if len(shape) == 2:
+        return (p, 0, st[0] if full[1] == B else 0) if axes == 1 else (p, st[0], 0)
+    return p, 0, 0
 
 
 def _call(Q, K, positions, inv_freq, sections, interleaved, inverse, Qo, Ko, stream, where):
     if Q.dim() != 4:
         raise ValueError("Q, K must be [B, H, T, d]")
     B, Hq, T, d = Q.shape
-    if inv_freq.dim() != 1 or 2 * inv_freq.numel() > d:
+    half = inv_freq.numel()
+    if inv_freq.dim() != 1 or 2 * half > d:
         raise ValueError(f"inv_freq has shape {tuple(inv_freq.shape)}, expected [rot / 2] with rot <= {d}")
-    rot = 2 * inv_freq.numel()
-    sections = [rot // 2] if sections is None else [int(n) for n in sections]
-    if not 1 <= len(sections) <= 4 or min(sections) < 0 or 2 * sum(sections) != rot:
-        raise ValueError(f"sections {sections}: one to four axes whose frequencies add up to {rot // 2}")
-    _heads(Q, "Q", B, T, d, Q.device)
-    _heads(K, "K", B, T, d, Q.device)
-    if not inv_freq.is_cuda or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous() or \
-            inv_freq.device != Q.device:
-        raise ValueError(f"inv_freq must be a contiguous CUDA {torch.float32} tensor on {Q.device}")
-    pos = _rows_positions(positions, len(sections), B, T, Q.device)
+    sections = (half,) if sections is None else tuple(sections)
+    axes = len(sections)
+    if not 1 <= axes <= 4 or min(sections) < 0 or sum(sections) != half:
+        raise ValueError(f"sections {list(sections)}: one to four axes whose frequencies add up to {half}")
+    device = Q.device
+    q_strides = _heads(Q, "Q", B, T, d, device)
+    k_strides = _heads(K, "K", B, T, d, device)
+    if inv_freq.dtype != torch.float32 or inv_freq.get_device() != device.index or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be a contiguous CUDA {torch.float32} tensor on {device}")
+    pos, pos_axis, pos_batch = _rows_positions(positions, axes, B, T, device)
     if pos is not positions and stream is not None:
         pos.record_stream(stream)
-    outs = []
-    for x, o, name in ((Q, Qo, "Qo"), (K, Ko, "Ko")):
-        if o is None:
-            o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _fa._check_all(Q.device, [(o, name, x.shape, torch.bfloat16)])
-        outs.append(o)
-    (Qo, Ko), Hk = outs, K.shape[1]
-    c = ctypes.c_int * 4
-    s3 = ctypes.c_longlong * 3
-    dims = _fa.FaRotaryDims(B, Hq, Hk, T, d, rot, len(sections), int(bool(interleaved)), pos.element_size(),
-                            c(*sections), s3(*Q.stride()[:3]), s3(*K.stride()[:3]), s3(*Qo.stride()[:3]),
-                            s3(*Ko.stride()[:3]), pos.stride(0), pos.stride(1))
+    Hk = K.shape[1]
+    if Qo is None:
+        Qo = torch.empty((B, Hq, T, d), dtype=torch.bfloat16, device=device)
+    else:
+        _fa._check_all(device, [(Qo, "Qo", Q.shape, torch.bfloat16)])
+    if Ko is None:
+        Ko = torch.empty((B, Hk, T, d), dtype=torch.bfloat16, device=device)
+    else:
+        _fa._check_all(device, [(Ko, "Ko", K.shape, torch.bfloat16)])
+    dims = _fa.FaRotaryDims(B, Hq, Hk, T, d, 2 * half, axes, 1 if interleaved else 0, pos.element_size(), sections,
+                            q_strides, k_strides, (Hq * T * d, T * d, d), (Hk * T * d, T * d, d), pos_axis, pos_batch)
     lib = _fa.load()
-    with torch.cuda.device(Q.device):
+    with _fa._on(device):
         code = lib.fa_rotary(ctypes.byref(dims), Q.data_ptr(), K.data_ptr(), pos.data_ptr(), inv_freq.data_ptr(),
-                             Qo.data_ptr(), Ko.data_ptr(), inverse, _fa._stream_ptr(stream, Q.device))
+                             Qo.data_ptr(), Ko.data_ptr(), inverse, _fa._stream_ptr(stream, device))
     _fa._raise(code, where)
     return Qo, Ko
 
