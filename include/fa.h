@@ -191,9 +191,16 @@ FA_API fa_status fa_mask_plan(const fa_dims* dims, const int* doc_q, const int* 
                               int prefix_per_row, void* plan, size_t plan_bytes, void* stream);
 
 /* fa_forward and fa_backward_stages with modified scores (scores NULL or all
- * zero: the same as those calls). */
+ * zero: the same as those calls).
+ * A forward of few query rows over many keys splits the keys over the SMs where it
+ * is given a workspace (256-byte aligned, contents ignored) of at least
+ * fa_forward_scored_workspace_bytes (0 where nothing is split; it asks the current
+ * device for its SMs); with less, or NULL, it runs unsplit: same results up to
+ * rounding, slower. */
+FA_API size_t fa_forward_scored_workspace_bytes(const fa_dims* dims, const fa_scores* scores);
 FA_API fa_status fa_forward_scored(const fa_dims* dims, const fa_scores* scores, const void* Q, const void* K,
-                                   const void* V, void* O, float* L, void* stream);
+                                   const void* V, void* O, float* L, void* workspace, size_t workspace_bytes,
+                                   void* stream);
 FA_API fa_status fa_backward_scored(const fa_dims* dims, const fa_scores* scores, const void* Q, const void* K,
                                     const void* V, const void* O, const void* dO, const float* L, void* dQ, void* dK,
                                     void* dV, void* workspace, size_t workspace_bytes, int stages, void* stream);

@@ -36,7 +36,7 @@ FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = ran
 EXPORTED_SYMBOLS = ("fa_forward", "fa_backward", "fa_backward_stages", "fa_backward_workspace_bytes",
                     "fa_backward_workspace_min_bytes", "fa_backward_noalloc", "fa_status_string",
                     "fa_last_device_status", "fa_last_launch_count", "fa_rotary", "fa_mask_plan_bytes", "fa_mask_plan",
-                    "fa_forward_scored", "fa_backward_scored")
+                    "fa_forward_scored", "fa_backward_scored", "fa_forward_scored_workspace_bytes")
 FA_ERR_SCRATCH_TOO_SMALL = 5
 FA_NOALLOC_SCRATCH_BYTES = 32 << 20
 FA_BWD_PRE, FA_BWD_MAIN, FA_BWD_CAST, FA_BWD_ALL = 1, 2, 4, 7
@@ -110,7 +110,9 @@ def load(path: str | None = None):
             lib.fa_mask_plan_bytes.restype = ctypes.c_size_t
             lib.fa_mask_plan.argtypes = [dp, vp, vp, vp, ctypes.c_int, vp, ctypes.c_size_t, vp]
             lib.fa_mask_plan.restype = ctypes.c_int
-            lib.fa_forward_scored.argtypes = [dp, sp, vp, vp, vp, vp, vp, vp]
+            lib.fa_forward_scored_workspace_bytes.argtypes = [dp, sp]
+            lib.fa_forward_scored_workspace_bytes.restype = ctypes.c_size_t
+            lib.fa_forward_scored.argtypes = [dp, sp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
             lib.fa_forward_scored.restype = ctypes.c_int
             lib.fa_backward_scored.argtypes = [dp, sp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t,
                                                ctypes.c_int, vp]
@@ -301,9 +303,14 @@ def fa_forward(Q, K, V, causal: bool, scale: float | None = None, O=None, L=None
         L = torch.empty((dims.B, dims.Hq, dims.Tq), dtype=f32, device=device)
     lib = load()
     scores = _scores(dims, device, softcap, slopes, mask, stream)
+    ref = ctypes.byref(dims)
     with _on(device):
-        code = lib.fa_forward_scored(ctypes.byref(dims), scores, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
-                                     O.data_ptr(), L.data_ptr(), _stream_ptr(stream, device))
+        nbytes = lib.fa_forward_scored_workspace_bytes(ref, scores) if scores is not None else 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+        if stream is not None and workspace is not None:  # freed on return, while the other stream still uses it
+            workspace.record_stream(stream)
+        code = lib.fa_forward_scored(ref, scores, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
+                                     L.data_ptr(), _ptr(workspace), nbytes, _stream_ptr(stream, device))
     _raise(code, "fa_forward")
     return O, L
 

@@ -140,6 +140,14 @@ int* device_status_word() {
   return g_status_ptr[dev];
 }
 
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
 cudaError_t allow_dynamic_smem(const void* kernel, int bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -159,11 +167,11 @@ extern "C" {
 
 fa_status fa_forward(const fa_dims* dims, const void* Q, const void* K, const void* V, void* O, float* L,
                      void* stream) {
-  return fa_forward_scored(dims, nullptr, Q, K, V, O, L, stream);
+  return fa_forward_scored(dims, nullptr, Q, K, V, O, L, nullptr, 0, stream);
 }
 
 fa_status fa_forward_scored(const fa_dims* dims, const fa_scores* scores, const void* Q, const void* K, const void* V,
-                            void* O, float* L, void* stream) {
+                            void* O, float* L, void* workspace, size_t workspace_bytes, void* stream) {
   t_last_launches = 0;
   fa::Problem pr;
   fa::ScoreMods mods;
@@ -175,12 +183,21 @@ fa_status fa_forward_scored(const fa_dims* dims, const fa_scores* scores, const 
   if ((s = check_ptr(Q, nq)) || (s = check_ptr(K, nk)) || (s = check_ptr(V, nkv)) || (s = check_ptr(O, nqv)) ||
       (s = check_ptr(L, (long long)pr.B * pr.Hq * pr.Tq)))
     return s;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return FA_ERR_INVALID_ARG;
   if (nq == 0) return FA_OK;
   if (!fa::device_status_word()) return FA_ERR_CUDA;
   int launches = 0;
-  cudaError_t e = fa::launch_forward(pr, mods, Q, K, V, O, L, static_cast<cudaStream_t>(stream), &launches);
+  cudaError_t e = fa::launch_forward(pr, mods, Q, K, V, O, L, workspace, workspace_bytes,
+                                     static_cast<cudaStream_t>(stream), &launches);
   t_last_launches = launches;
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_forward_scored_workspace_bytes(const fa_dims* dims, const fa_scores* scores) {
+  fa::Problem pr;
+  fa::ScoreMods mods;
+  if (check_dims(dims, &pr) != FA_OK || check_scores(pr, scores, &mods) != FA_OK || pr.Tk == 0 || pr.Tq == 0) return 0;
+  return fa::fwd_workspace_bytes(pr, fa::fwd_shape(pr, mods, fa::sm_count()));
 }
 
 size_t fa_backward_workspace_bytes(const fa_dims* dims) {

@@ -165,8 +165,13 @@ struct ScoredFwdParams : FwdParams {
   int hi_off, lo_off;   // row i sees keys [i + lo_off, i + hi_off) (no plan)
   int q_tiles;
   int two_sided;        // a row may see keys on both sides of its own position
+  int row_mod, group;   // packed heads (fa::FwdShape)
+  int split;            // CTAs per item
+  float* part;          // [items][split][256 rows][dv], then as many (m, l) pairs
   fa::PlanView plan;
 };
+template <int SCORE>
+constexpr bool kIsFew = SCORE >= 0 && (SCORE & fa::kFew) != 0;
 template <int SCORE>
 using FwdParamsOf = std::conditional_t<SCORE >= 0, ScoredFwdParams, FwdParams>;
 
@@ -178,12 +183,14 @@ __device__ __forceinline__ void kv_range_for(const FwdParamsOf<SCORE>& p, int b,
   if constexpr (SCORE >= 0) {
     int bg, e;
     if (p.plan.kv_beg) {
-      const size_t at = (size_t)b * p.q_tiles + qa / BM;
+      const size_t at = (size_t)b * p.q_tiles + (kIsFew<SCORE> && p.row_mod ? 0 : qa / BM);
       bg = max(0, p.plan.kv_beg[at]);
       e = min(p.kv_tiles, p.plan.kv_end[at]);
     } else {
-      const int hi = min(p.Tk, min(qa + BM, p.Tq) - 1 + p.hi_off);  // keys the last row sees end here
-      bg = max(0, qa + p.lo_off) / BN;
+      const bool packed = kIsFew<SCORE> && p.row_mod;
+      const int first = packed ? 0 : qa, last = packed ? p.row_mod - 1 : min(qa + BM, p.Tq) - 1;  // positions
+      const int hi = min(p.Tk, last + p.hi_off);  // keys the last row sees end here
+      bg = max(0, first + p.lo_off) / BN;
       e = hi > 0 ? (hi + BN - 1) / BN : 0;
     }
     if (bg < e) {
@@ -219,6 +226,12 @@ struct FwdItem {
   bool single;       // tile B is not part of the item (its rows belong to another item)
 };
 
+// Index of the n-th item of this CTA (see fwd_item).
+__device__ __forceinline__ long long fwd_index(int n) {
+  const long long G = gridDim.x, c = blockIdx.x;
+  return n * G + ((n & 1) ? G - 1 - c : c);
+}
+
 // The n-th item of this CTA, or false past its last.  Items are numbered
 // heaviest causal rows first (the pair index slowest); round n of the grid
 // takes items [n * G, n * G + G), CTA c the c-th of them in even rounds and
@@ -228,9 +241,15 @@ struct FwdItem {
 // CTAs.
 template <bool CAUSAL, bool WINDOW, int SCORE>
 __device__ __forceinline__ bool fwd_item(const FwdParamsOf<SCORE>& p, int n, FwdItem* it) {
-  const long long G = gridDim.x, c = blockIdx.x;
-  const long long k = n * G + ((n & 1) ? G - 1 - c : c);
+  long long k = fwd_index(n);
   if (k >= p.n_items) return false;
+  int share = 0;
+  if constexpr (kIsFew<SCORE>) {
+    if (p.split > 1) {
+      share = (int)(k % p.split);
+      k /= p.split;
+    }
+  }
   const bool single = k >= p.n_full;
   it->single = single;
   const long long kp = single ? p.n_full + ((k - p.n_full) >> 1) : k;  // the pair
@@ -238,8 +257,9 @@ __device__ __forceinline__ bool fwd_item(const FwdParamsOf<SCORE>& p, int n, Fwd
   it->bh = (int)(kp - (long long)y * p.n_bh);
   const int b = it->bh / p.Hq, h = it->bh - b * p.Hq;
   y = p.n_pairs - 1 - y;
-  if constexpr (SCORE >= 0) {  // a plan's heaviest pairs first
-    if (p.plan.kv_beg) y = min(max(p.plan.pair_order[(size_t)b * p.n_pairs + p.n_pairs - 1 - y], 0), p.n_pairs - 1);
+  if constexpr (SCORE >= 0) {  // a plan's heaviest pairs first (the parts of split items go by position)
+    if (p.plan.kv_beg && (!kIsFew<SCORE> || (!p.row_mod && p.split == 1)))
+      y = min(max(p.plan.pair_order[(size_t)b * p.n_pairs + p.n_pairs - 1 - y], 0), p.n_pairs - 1);
   }
   it->q0 = y * (2 * BM) + (single ? (int)((k - p.n_full) & 1) * BM : 0);
   it->bkv = b * p.Hkv + h / p.G;
@@ -262,6 +282,18 @@ __device__ __forceinline__ bool fwd_item(const FwdParamsOf<SCORE>& p, int n, Fwd
       if (it->ke[0] < it->kb[1]) it->ke[0] = it->kb[1];
       if (it->ke[1] < it->kb[0]) it->ke[1] = it->kb[0];
       it->ub = min(it->kb[0], it->kb[1]);
+    }
+    if (kIsFew<SCORE> && p.split > 1) {  // this CTA's share of the key tiles
+      const int len = (it->ue - it->ub + p.split - 1) / p.split;
+      const int from = min(it->ub + share * len, it->ue), to = min(from + len, it->ue);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        it->kb[x] = max(it->kb[x], from);
+        it->ke[x] = min(it->ke[x], to);
+        if (it->ke[x] <= it->kb[x]) it->kb[x] = it->ke[x] = 0;
+      }
+      it->ub = from;
+      it->ue = to;
     }
   }
   return true;
@@ -808,27 +840,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       int my_doc = 0;              // its document, where the plan wants documents compared key by key
       bool by_key = false;
       float slope2 = 0.f;
-      int batch = 0;
+      int batch = 0, pos = i;  // the row's position among Tq
       if constexpr (SCORE >= 0) {
         batch = it.bh / p.Hq;
+        // (packed heads: the row's position, and its head, within the group)
+        int head = 0;
+        if (kIsFew<SCORE> && p.row_mod) {
+          const int row = min(i, p.Tq - 1);
+          head = row / p.row_mod;
+          pos = row - head * p.row_mod;
+        }
         if (p.plan.kv_beg) {
-          const size_t at = (size_t)batch * p.q_tiles * BM + (i < p.q_tiles * BM ? i : 0);
+          const size_t at = (size_t)batch * p.q_tiles * BM + (i < p.Tq ? pos : 0);
           row_lo = p.plan.row_lo[at];
           row_hi = i < p.Tq ? min(p.plan.row_hi[at], p.Tk) : 0;
           by_key = fa::plan_flag(p.plan.by_key, batch);
           if (by_key) my_doc = p.plan.q_doc[at];
         } else {
-          row_lo = max(0, i + p.lo_off);
-          row_hi = min(p.Tk, i + p.hi_off);
+          row_lo = max(0, pos + p.lo_off);
+          row_hi = min(p.Tk, pos + p.hi_off);
         }
-        if (SLOPES) slope2 = p.slopes[it.bh - batch * p.Hq] * 1.4426950408889634f;
+        if (SLOPES) slope2 = p.slopes[(it.bh - batch * p.Hq) * (kIsFew<SCORE> ? p.group : 1) + head] * 1.4426950408889634f;
       }
-      // reference max (log2 units) the P values are taken against
       float m_ref = NEG_INF;
       if (BOUNDED && !(SLOPES && by_key)) {
         m_ref = 0.f;
         if (SLOPES) {  // the greatest bias: of the nearest key the row sees, or the farthest (negative slopes)
-          const int to_lo = i + p.causal_off - row_lo, to_hi = i + p.causal_off - (row_hi - 1);
+          const int to_lo = pos + p.causal_off - row_lo, to_hi = pos + p.causal_off - (row_hi - 1);
           const int near = to_lo >= 0 && to_hi <= 0 ? 0 : min(abs(to_lo), abs(to_hi));
           m_ref = -slope2 * (float)(slope2 >= 0.f ? near : max(abs(to_lo), abs(to_hi)));
         }
@@ -845,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (SCORE >= 0) {
           lim = row_hi - kv0;
           lo = row_lo - kv0;
-          rel0 = kv0 - p.causal_off - i;
+          rel0 = kv0 - p.causal_off - pos;
           if (SLOPES) crossing = p.two_sided && __any_sync(0xffffffffu, rel0 < 0 && rel0 + BN > 1);
         }
         if (BOUNDED && !(SLOPES && by_key)) {
@@ -982,6 +1020,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (a tile past the last row, or tile B of a single-tile item, has nothing to write)
       if (!ok || qx0 >= p.Tq || (x == 1 && it.single)) continue;
       const bool row_ok = i < p.Tq;
+      if constexpr (kIsFew<SCORE>) {
+        if (p.split > 1) {  // the unnormalised row, its reference and sum, for fa_fwd_join
+          const size_t row = ((size_t)fwd_index(n) * 2 + x) * BM + r;
+          if (row_ok)
+            reinterpret_cast<float2*>(p.part + (size_t)p.n_items * 2 * BM * HDV)[row] = make_float2(m_ref, l);
+          float4* out = reinterpret_cast<float4*>(p.part + row * HDV);
+          if (nkv > 0) {
+#pragma unroll
+            for (int c = 0; c < HDV / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_wait_ld();
+              if (row_ok) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                  out[c * 8 + q] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                               __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+              }
+            }
+          }
+          continue;
+        }
+      }
       if (row_ok) p.L[(size_t)it.bh * p.Tq + i] = l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : NEG_INF;
       const float inv_l = l > 0.f ? 1.f / l : 0.f;
       uint4* orow = reinterpret_cast<uint4*>(p.O + ((size_t)it.bh * p.Tq + (row_ok ? i : 0)) * HDV);
@@ -1018,18 +1079,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && *abort_flag) atomicExch(p.status, DEV_TIMEOUT);
 }
 
-// SM count of the current device (the persistent grid's size); 0 if unknown.
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) !=
-                                                 cudaSuccess)
-    return 0;
-  return sms;
-}
-
 template <int HD, int HDV, bool CAUSAL, bool WINDOW, int SCORE>
-cudaError_t launch_fwd_t(const fa::Problem& pr, const fa::ScoreMods& mods, const CUtensorMap& mq,
-                         const CUtensorMap& mk, const CUtensorMap& mv, void* O, float* L, cudaStream_t stream) {
+cudaError_t launch_fwd_t(const fa::Problem& pr, const fa::ScoreMods& mods, const fa::FwdShape& shape,
+                         const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, void* O, float* L,
+                         float* part, cudaStream_t stream) {
   using C = FwdCfg<HD, HDV>;
   const void* fn = reinterpret_cast<const void*>(fa_fwd_kernel<HD, HDV, CAUSAL, WINDOW, SCORE>);
   cudaError_t e = fa::allow_dynamic_smem(fn, C::SMEM);
@@ -1041,22 +1094,22 @@ cudaError_t launch_fwd_t(const fa::Problem& pr, const fa::ScoreMods& mods, const
   e = cudaFuncGetAttributes(&fa_attr, fn);
   if (e != cudaSuccess) return e;
   if (fa_attr.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-  const int sms = sm_count();
+  const int sms = fa::sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   FwdParamsOf<SCORE> p;
   p.O = static_cast<uint16_t*>(O);
   p.L = L;
   p.status = fa::device_status_word();
-  p.Hq = pr.Hq;
+  p.Hq = shape.heads;
   p.Hkv = pr.Hkv;
-  p.G = pr.G();
-  p.Tq = pr.Tq;
+  p.G = shape.heads / pr.Hkv;
+  p.Tq = shape.rows;
   p.Tk = pr.Tk;
   p.causal_off = pr.Tk - pr.Tq;
   p.window = pr.causal ? pr.window : 0;
   p.kv_tiles = pr.kv_tiles();
-  p.n_bh = pr.B * pr.Hq;
-  p.n_pairs = (pr.q_tiles() + 1) / 2;
+  p.n_bh = pr.B * shape.heads;
+  p.n_pairs = (shape.rows + 2 * BM - 1) / (2 * BM);
   const long long n_pair_items = (long long)p.n_bh * p.n_pairs;
   // Without a causal mask every item has the same work.  A last round with at
   // most half as many items as SMs then runs them as single tiles on twice
@@ -1064,6 +1117,10 @@ cudaError_t launch_fwd_t(const fa::Problem& pr, const fa::ScoreMods& mods, const
   const long long r = n_pair_items % sms;
   p.n_full = (!pr.causal && !mods.plan && r > 0 && 2 * r <= sms) ? n_pair_items - r : n_pair_items;
   p.n_items = p.n_full + 2 * (n_pair_items - p.n_full);
+  if (shape.split > 1) {
+    p.n_full = n_pair_items;
+    p.n_items = n_pair_items * shape.split;
+  }
   p.scale_log2 = pr.scale * 1.4426950408889634f;
   if constexpr (SCORE >= 0) {
     p.cap = fa::cap_params(mods.softcap, pr.scale);
@@ -1072,6 +1129,10 @@ cudaError_t launch_fwd_t(const fa::Problem& pr, const fa::ScoreMods& mods, const
     p.lo_off = fa::row_lo_off(pr);
     p.q_tiles = pr.q_tiles();
     p.two_sided = !pr.causal || mods.plan;
+    p.row_mod = shape.row_mod;
+    p.group = shape.group;
+    p.split = shape.split;
+    p.part = part;
     p.plan = fa::plan_view(pr, mods.plan);
   }
   p.test_withhold_q = fa::test_withhold() == fa::kWithholdFwdQ;

@@ -48,11 +48,16 @@ int* device_status_word();
 // pair; safe to call from several host threads.
 cudaError_t allow_dynamic_smem(const void* kernel, int bytes);
 
+// SM count of the current device; 0 if it cannot be read.
+int sm_count();
+
 // ---------------------------------------------------------------- score modifications
 // Bits of the kernels' SCORE template argument; kPlain compiles none of it.
 // kBounded (forward, with kCap): the cap keeps 2^score inside fp32, so the
 // softmax needs no running maximum.
-enum ScoreBits : int { kPlain = -1, kCap = 1, kSlopes = 2, kBounded = 4 };
+// kFew (forward): packed heads and split items (FwdShape).  (In every instance their
+// bookkeeping cost the large calls 4%: T 8192, cap 50, 938 -> 978 us.)
+enum ScoreBits : int { kPlain = -1, kCap = 1, kSlopes = 2, kBounded = 4, kFew = 8 };
 
 // Largest cap (log2 units) of the bounded form: 2^-90 <= P <= 2^90, so that P, its
 // sums over 2^30 keys and its products with values down to 2^-36 are normal
@@ -103,6 +108,48 @@ inline CapParams cap_params(float softcap, float scale) {
 
 // The cap's derivative is 4 r (1 - r); the kernels leave the 4 to this factor.
 inline float scale_grad(const Problem& p, const ScoreMods& m) { return m.softcap > 0.f ? 4.f * p.scale : p.scale; }
+
+// Few query rows over many keys (score-modified forward).
+// Packing: the G query heads of a key/value head are G * Tq consecutive rows of Q, O
+// and L, so a call of at most 64 query rows runs them as one head's rows: K and V
+// are walked once for the group, in tiles that are at least as full.
+// Splitting: where the work items fill at most half of the SMs, each item's key
+// tiles are dealt to `split` CTAs.  Each leaves its unnormalised O, reference and
+// sum (fp32) in the workspace, and a second kernel joins them.
+constexpr int kPackRows = 64;
+struct FwdShape {
+  int heads, rows;  // per batch entry, rows per head
+  int row_mod;      // packed: Tq, the period of the rows' positions; else 0
+  int group;        // packed: G; else 1
+  long long items;  // pairs of query tiles
+  int split;        // CTAs per item
+  bool few() const { return row_mod || split > 1; }
+};
+inline FwdShape fwd_shape(const Problem& p, const ScoreMods& m, int sms) {
+  FwdShape s = {p.Hq, p.Tq, 0, 1, 0, 1};
+  if (m.any() && p.G() > 1 && p.Tq <= kPackRows && (long long)p.G() * p.Tq <= (1 << 24)) {
+    s.heads = p.Hkv;
+    s.rows = p.G() * p.Tq;
+    s.row_mod = p.Tq;
+    s.group = p.G();
+  }
+  s.items = (long long)p.B * s.heads * ((s.rows + 2 * kTile - 1) / (2 * kTile));
+  if (m.any() && s.items > 0 && 2 * s.items <= sms) {
+    // Key tiles an item can see.  A tile takes ~1.5 us, the parts and their joining
+    // 5 to 6: four tiles and more a part, of twelve at least.  (Tq 777, window 200,
+    // at most 4 tiles: 15.8 us whole, 20.0 in three parts; Tq 32, Tk 8032: 124 us
+    // whole, 23 in parts and packed.)
+    const long long seen = p.window ? ((long long)p.window + 2 * kTile - 1) / kTile + 1 : p.kv_tiles();
+    const long long tiles = seen < p.kv_tiles() ? seen : p.kv_tiles();
+    const long long most = tiles >= 12 ? tiles / 4 : 1, want = sms / s.items;
+    s.split = (int)(want < most ? want : most);
+  }
+  return s;
+}
+// fp32 workspace of a split forward: per item, part and row the O row, m and l.
+inline size_t fwd_workspace_bytes(const Problem& p, const FwdShape& s) {
+  return s.split > 1 ? (size_t)s.items * s.split * 2 * kTile * (p.dv + 2) * sizeof(float) : 0;
+}
 
 // Mask plan: what fa_mask_plan wrote for one set of dims, as int32 arrays.
 // Rows and keys are padded to whole tiles per batch entry.
@@ -223,10 +270,14 @@ struct ScoredBwdParams : BwdParams {
 
 // The score-modified instances, by head size of Q and K (one translation unit
 // and direction each).
-cudaError_t launch_fwd_scored_64(const Problem& p, const ScoreMods& m, const CUtensorMap& mq, const CUtensorMap& mk,
-                                 const CUtensorMap& mv, void* O, float* L, cudaStream_t stream);
-cudaError_t launch_fwd_scored_128(const Problem& p, const ScoreMods& m, const CUtensorMap& mq, const CUtensorMap& mk,
-                                  const CUtensorMap& mv, void* O, float* L, cudaStream_t stream);
+using FwdLauncher = cudaError_t (*)(const Problem& p, const ScoreMods& m, const FwdShape& s, const CUtensorMap& mq,
+                                    const CUtensorMap& mk, const CUtensorMap& mv, void* O, float* L, float* part,
+                                    cudaStream_t stream);
+// For the problem's modifications and value head size; _few: with kFew.
+FwdLauncher fwd_scored_64(const Problem& p, const ScoreMods& m);
+FwdLauncher fwd_scored_128(const Problem& p, const ScoreMods& m);
+FwdLauncher fwd_scored_few_64(const Problem& p, const ScoreMods& m);
+FwdLauncher fwd_scored_few_128(const Problem& p, const ScoreMods& m);
 cudaError_t launch_bwd_scored_64(const Problem& p, const ScoreMods& m, const CUtensorMap* maps, const ScoredBwdParams& bp,
                                  cudaStream_t stream);
 cudaError_t launch_bwd_scored_128(const Problem& p, const ScoreMods& m, const CUtensorMap* maps, const ScoredBwdParams& bp,
@@ -235,7 +286,7 @@ cudaError_t launch_bwd_scored_128(const Problem& p, const ScoreMods& m, const CU
 // Launchers.  Each returns the first CUDA error it met and adds the number
 // of kernels it enqueued to *launches.
 cudaError_t launch_forward(const Problem& p, const ScoreMods& m, const void* Q, const void* K, const void* V, void* O,
-                           float* L, cudaStream_t stream, int* launches);
+                           float* L, void* workspace, size_t workspace_bytes, cudaStream_t stream, int* launches);
 // `workspace_bytes` decides whether the split-item area fits (see BwdWorkspace).
 cudaError_t launch_backward(const Problem& p, const ScoreMods& m, const void* Q, const void* K, const void* V, const void* O,
                             const void* dO, const float* L, void* dQ, void* dK, void* dV, void* workspace,
