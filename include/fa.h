@@ -201,6 +201,10 @@ FA_API size_t fa_forward_scored_workspace_bytes(const fa_dims* dims, const fa_sc
 FA_API fa_status fa_forward_scored(const fa_dims* dims, const fa_scores* scores, const void* Q, const void* K,
                                    const void* V, void* O, float* L, void* workspace, size_t workspace_bytes,
                                    void* stream);
+/* Workspace for fa_backward_scored's fastest schedule on the current device (room
+ * for the partial sums of split work items); the least that it accepts is
+ * fa_backward_workspace_min_bytes(dims).  0 for invalid arguments. */
+FA_API size_t fa_backward_scored_workspace_bytes(const fa_dims* dims, const fa_scores* scores);
 FA_API fa_status fa_backward_scored(const fa_dims* dims, const fa_scores* scores, const void* Q, const void* K,
                                     const void* V, const void* O, const void* dO, const float* L, void* dQ, void* dK,
                                     void* dV, void* workspace, size_t workspace_bytes, int stages, void* stream);

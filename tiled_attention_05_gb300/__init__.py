@@ -36,7 +36,8 @@ FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = ran
 EXPORTED_SYMBOLS = ("fa_forward", "fa_backward", "fa_backward_stages", "fa_backward_workspace_bytes",
                     "fa_backward_workspace_min_bytes", "fa_backward_noalloc", "fa_status_string",
                     "fa_last_device_status", "fa_last_launch_count", "fa_rotary", "fa_mask_plan_bytes", "fa_mask_plan",
-                    "fa_forward_scored", "fa_backward_scored", "fa_forward_scored_workspace_bytes")
+                    "fa_forward_scored", "fa_backward_scored", "fa_forward_scored_workspace_bytes",
+                    "fa_backward_scored_workspace_bytes")
 FA_ERR_SCRATCH_TOO_SMALL = 5
 FA_NOALLOC_SCRATCH_BYTES = 32 << 20
 FA_BWD_PRE, FA_BWD_MAIN, FA_BWD_CAST, FA_BWD_ALL = 1, 2, 4, 7
@@ -110,6 +111,8 @@ def load(path: str | None = None):
             lib.fa_mask_plan_bytes.restype = ctypes.c_size_t
             lib.fa_mask_plan.argtypes = [dp, vp, vp, vp, ctypes.c_int, vp, ctypes.c_size_t, vp]
             lib.fa_mask_plan.restype = ctypes.c_int
+            lib.fa_backward_scored_workspace_bytes.argtypes = [dp, sp]
+            lib.fa_backward_scored_workspace_bytes.restype = ctypes.c_size_t
             lib.fa_forward_scored_workspace_bytes.argtypes = [dp, sp]
             lib.fa_forward_scored_workspace_bytes.restype = ctypes.c_size_t
             lib.fa_forward_scored.argtypes = [dp, sp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
@@ -325,21 +328,21 @@ def fa_backward(Q, K, V, O, dO, L, causal: bool, scale: float | None = None, dQ=
     fa_backward_stages in include/fa.h); the default runs all of them.
     """
     dims, dQ, dK, dV = _backward_operands(Q, K, V, O, dO, L, causal, scale, window, dQ, dK, dV)
-    lib = load()
-    need = fa_backward_workspace_bytes(dims)
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=Q.device)
-        if stream is not None:  # freed on return, while the other stream still uses it
-            workspace.record_stream(stream)
-    elif not workspace.is_cuda or workspace.device != Q.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {Q.device}")
-    nbytes = workspace.numel() * workspace.element_size()
-    scores = _scores(dims, Q.device, softcap, slopes, mask, stream)
-    with _on(Q.device):
-        code = lib.fa_backward_scored(ctypes.byref(dims), scores, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+    lib, device, ref = load(), Q.device, ctypes.byref(dims)
+    scores = _scores(dims, device, softcap, slopes, mask, stream)
+    with _on(device):
+        if workspace is None:
+            need = lib.fa_backward_scored_workspace_bytes(ref, scores)
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+            if stream is not None:  # freed on return, while the other stream still uses it
+                workspace.record_stream(stream)
+        elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+        nbytes = workspace.numel() * workspace.element_size()
+        code = lib.fa_backward_scored(ref, scores, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
                                       O.data_ptr(), dO.data_ptr(), L.data_ptr(), dQ.data_ptr(), dK.data_ptr(),
                                       dV.data_ptr(), workspace.data_ptr(), nbytes, int(stages),
-                                      _stream_ptr(stream, Q.device))
+                                      _stream_ptr(stream, device))
     _raise(code, "fa_backward")
     return dQ, dK, dV
 

@@ -206,6 +206,16 @@ size_t fa_backward_workspace_bytes(const fa_dims* dims) {
   return fa::backward_workspace_layout(pr).total;
 }
 
+size_t fa_backward_scored_workspace_bytes(const fa_dims* dims, const fa_scores* scores) {
+  fa::Problem pr;
+  fa::ScoreMods mods;
+  if (check_dims(dims, &pr) != FA_OK || check_scores(pr, scores, &mods) != FA_OK) return 0;
+  const fa::ScoredSplit parts = mods.any() ? fa::scored_split(pr, fa::sm_count()) : fa::ScoredSplit{0, 1};
+  if (parts.items)
+    return fa::backward_workspace_layout(pr, (long long)parts.items * parts.parts, parts.items).total;
+  return fa::backward_workspace_layout(pr).total;
+}
+
 size_t fa_backward_workspace_min_bytes(const fa_dims* dims) {
   fa::Problem pr;
   if (check_dims(dims, &pr) != FA_OK) return 0;

@@ -144,7 +144,7 @@ inline int grid_for(long long work, int per_block) {
 
 namespace fa {
 
-BwdWorkspace backward_workspace_layout(const Problem& p) {
+BwdWorkspace backward_workspace_layout(const Problem& p, long long slots, int items) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   const size_t rows = (size_t)p.B * p.Hq * (size_t)p.Tq_pad();
   BwdWorkspace w;
@@ -158,7 +158,9 @@ BwdWorkspace backward_workspace_layout(const Problem& p) {
   // tiles of each head are lighter, and splitting did not pay.)
   const long long n_items = (long long)p.B * p.Hkv * p.kv_tiles();
   w.split_cap = !p.causal ? (int)(n_items < kMaxSplitItems ? n_items : kMaxSplitItems) : 0;
-  w.counters = up(w.part + (size_t)w.split_cap * 2 * kTile * (p.d + p.dv) * sizeof(float));
+  if (slots >= 0) w.split_cap = items;
+  if (slots < 0) slots = 2LL * w.split_cap;
+  w.counters = up(w.part + (size_t)slots * kTile * (p.d + p.dv) * sizeof(float));
   w.total = up(w.counters + (size_t)w.split_cap * sizeof(unsigned int));
   return w;
 }
@@ -200,7 +202,10 @@ cudaError_t launch_backward(const Problem& pr, const ScoreMods& mods, const void
     }
     return cudaGetLastError();
   }
-  const BwdWorkspace w = backward_workspace_layout(pr);
+  // (modified scores: unequal items in parts where there are few, else the plain rule)
+  const ScoredSplit parts = mods.any() ? scored_split(pr, sm_count()) : ScoredSplit{0, 1};
+  const BwdWorkspace w = parts.items ? backward_workspace_layout(pr, (long long)parts.items * parts.parts, parts.items)
+                                     : backward_workspace_layout(pr);
   // the split items' area is used only where the caller's workspace holds it
   const int split_cap = workspace_bytes >= w.total ? w.split_cap : 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -248,7 +253,8 @@ cudaError_t launch_backward(const Problem& pr, const ScoreMods& mods, const void
   bp.window = pr.causal ? pr.window : 0;
   bp.q_tiles = pr.q_tiles();
   bp.kv_tiles = pr.kv_tiles();
-  bp.sb_groups = backward_super_batch(pr.B * pr.Hkv, pr.kv_tiles());
+  // (items in parts: one super-batch, so that the heaviest items are the order's first)
+  bp.sb_groups = parts.items ? pr.B * pr.Hkv : backward_super_batch(pr.B * pr.Hkv, pr.kv_tiles());
   if (bp.sb_groups < 1) return cudaErrorInvalidValue;
   bp.Tq_pad = pr.Tq_pad();
   bp.scale_grad = scale_grad(pr, mods);
@@ -260,7 +266,9 @@ cudaError_t launch_backward(const Problem& pr, const ScoreMods& mods, const void
   bp.lo_off = row_lo_off(pr);
   bp.two_sided = !pr.causal || mods.plan;
   bp.plan = plan_view(pr, mods.plan);
-  bp.n_split = mods.plan ? 0 : backward_split_items(pr, split_cap);  // a plan's items differ in work
+  bp.parts = parts.items ? parts.parts : 2;
+  bp.split_first = parts.items != 0;
+  bp.n_split = parts.items ? split_cap : mods.plan ? 0 : backward_split_items(pr, split_cap);
   bp.n_whole = (int)((long long)pr.B * pr.Hkv * pr.kv_tiles()) - bp.n_split;
   bp.part = part;
   bp.split_counters = split_counters;

@@ -132,10 +132,12 @@ struct BwdCfg {
 // as bf16 into a 128-row, 128B-swizzled staging tile for the TMA store.
 // `have` is false when the CTA saw no query tile: the rows are zero.
 // `add` (optional): the same row's partial sums from the other half of a
-// split item, this warpgroup's columns, added before the scaling.
+// split item, this warpgroup's columns, added before the scaling; or those of
+// n_add parts, add_stride floats apart, of which the skip-th is the CTA's own.
 template <int W>
 __device__ __forceinline__ void stage_rows_bf16(uint32_t src, uint8_t* stage, int r, int wg, float mul, bool have,
-                                                const float* add = nullptr) {
+                                                const float* add = nullptr, int n_add = 1, size_t add_stride = 0,
+                                                int skip = -1) {
   constexpr int HALF = W / 2;
 #pragma unroll
   for (int c = 0; c < HALF / 32; ++c) {
@@ -147,10 +149,11 @@ __device__ __forceinline__ void stage_rows_bf16(uint32_t src, uint8_t* stage, in
 #pragma unroll
       for (int e = 0; e < 32; ++e) v[e] = 0u;
     }
-    if (add) {
+    for (int n = 0; add && n < n_add; ++n) {
+      if (n == skip) continue;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(add + c * 32) + q);
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(add + n * add_stride + c * 32) + q);
         v[4 * q] = __float_as_uint(__uint_as_float(v[4 * q]) + a.x);
         v[4 * q + 1] = __float_as_uint(__uint_as_float(v[4 * q + 1]) + a.y);
         v[4 * q + 2] = __float_as_uint(__uint_as_float(v[4 * q + 2]) + a.z);
@@ -197,6 +200,8 @@ __device__ __forceinline__ void write_partial(uint32_t src, float* dst, bool hav
 
 using fa::BwdParams;
 using fa::ScoredBwdParams;
+__device__ __forceinline__ bool parts_first(const BwdParams&) { return false; }
+__device__ __forceinline__ bool parts_first(const ScoredBwdParams& p) { return p.split_first != 0; }
 template <int SCORE>
 using BwdParamsOf = std::conditional_t<SCORE >= 0, ScoredBwdParams, BwdParams>;
 
@@ -205,16 +210,18 @@ using BwdParamsOf = std::conditional_t<SCORE >= 0, ScoredBwdParams, BwdParams>;
 // bf16.  lse: the queries' row statistics (log2 units); rel0: position of the
 // first query minus the key's; vis: the queries that see the key (MASKED).
 // BOTH: queries on both sides of the key may see it, else the bias is a line.
-template <bool CAP, bool SLOPES, bool MASKED, bool BOTH>
-__device__ __forceinline__ void modified_chunk(const ScoredBwdParams& p, const uint32_t (&sr)[32], const float4* lse,
+// SMALL: the cap by its polynomial; then returns whether every score was inside it.
+template <bool CAP, bool SLOPES, bool MASKED, bool BOTH, bool SMALL>
+__device__ __forceinline__ bool modified_chunk(const ScoredBwdParams& p, const uint32_t (&sr)[32], const float4* lse,
                                                int rel0, float slope2, uint32_t vis, float* pr, uint32_t (&pk)[16]) {
-  const float in = CAP ? p.cap.in : p.scale_log2;
+  const float in = CAP ? p.cap.in : p.scale_log2, log2c = CAP && !SMALL ? p.cap.log2c : 0.f;
   const uint64_t in2 = f2_pack(in, in), m2cap2 = f2_pack(-2.f * p.cap.log2c, -2.f * p.cap.log2c);
   const float side = rel0 + 31 <= 0 ? slope2 : -slope2;  // bias per step of the query
   uint64_t step[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) step[k] = f2_pack((float)(2 * k) * side, (float)(2 * k + 1) * side);
   const float rel = (float)rel0;
+  float top = 0.f;  // greatest s^2
 #pragma unroll
   for (int c = 0; c < 32; c += 4) {
     const float4 l4 = ld_shared_f4(lse + (c >> 2));  // 16-byte broadcast: 4 columns
@@ -222,35 +229,48 @@ __device__ __forceinline__ void modified_chunk(const ScoredBwdParams& p, const u
     uint64_t x[2] = {f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
                      f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]))};
     uint64_t r[2], e[2];
-    if (CAP) cap_quad(f2_mul(x[0], in2), f2_mul(x[1], in2), r[0], r[1], e[0], e[1]);
-    const float gb = fmaf(rel + (float)c, side, CAP ? p.cap.log2c : 0.f);  // (the sum is exact)
+    if (CAP && !SMALL) cap_quad(f2_mul(x[0], in2), f2_mul(x[1], in2), r[0], r[1], e[0], e[1]);
+    const float gb = fmaf(rel + (float)c, side, log2c);  // (the sum is exact)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint64_t bias;  // (cap +) distance bias - row statistic
       if (SLOPES && BOTH) {
         const float d0 = (float)(rel0 + c + 2 * h), d1 = (float)(rel0 + c + 2 * h + 1);
-        bias = f2_sub(f2_pack(fmaf(fabsf(d0), -slope2, CAP ? p.cap.log2c : 0.f),
-                              fmaf(fabsf(d1), -slope2, CAP ? p.cap.log2c : 0.f)), l[h]);
+        bias = f2_sub(f2_pack(fmaf(fabsf(d0), -slope2, log2c), fmaf(fabsf(d1), -slope2, log2c)), l[h]);
       } else if (SLOPES) {
         bias = f2_sub(f2_add(step[h], f2_pack(gb, gb)), l[h]);
-      } else if (CAP) {
-        bias = f2_sub(f2_pack(p.cap.log2c, p.cap.log2c), l[h]);
+      } else if (CAP && !SMALL) {
+        bias = f2_sub(f2_pack(log2c, log2c), l[h]);
       } else {
         bias = f2_neg(l[h]);
       }
-      x[h] = CAP ? f2_fma(r[h], m2cap2, bias) : f2_fma(x[h], in2, bias);
+      uint64_t w = 0ull;  // a quarter of the cap's derivative
+      if (CAP && SMALL) {
+        const uint64_t u = f2_mul(x[h], x[h]);
+        top = fmax3(top, f2_lo(u), f2_hi(u));
+        uint64_t t = f2_fma(u, f2_pack(p.cap.a[3], p.cap.a[3]), f2_pack(p.cap.a[2], p.cap.a[2]));
+        t = f2_fma(u, t, f2_pack(p.cap.a[1], p.cap.a[1]));
+        t = f2_mul(x[h], f2_fma(u, t, f2_pack(p.cap.a[0], p.cap.a[0])));
+        w = f2_fma(f2_mul(t, t), f2_pack(p.cap.slope, p.cap.slope), f2_pack(0.25f, 0.25f));
+        x[h] = f2_add(t, bias);
+      } else if (CAP) {
+        x[h] = f2_fma(r[h], m2cap2, bias);
+        w = f2_mul(f2_mul(e[h], r[h]), r[h]);
+      } else {
+        x[h] = f2_fma(x[h], in2, bias);
+      }
       float v0 = ex2(f2_lo(x[h])), v1 = ex2(f2_hi(x[h]));
       if (MASKED) {
         if (!((vis >> (c + 2 * h)) & 1u)) v0 = 0.f;
         if (!((vis >> (c + 2 * h + 1)) & 1u)) v1 = 0.f;
       }
       pk[c / 2 + h] = pack_bf16x2(v0, v1);
-      uint64_t w = f2_pack(v0, v1);
-      if (CAP) w = f2_mul(w, f2_mul(f2_mul(e[h], r[h]), r[h]));
+      w = CAP ? f2_mul(f2_pack(v0, v1), w) : f2_pack(v0, v1);
       pr[c + 2 * h] = f2_lo(w);
       pr[c + 2 * h + 1] = f2_hi(w);
     }
   }
+  return !CAP || !SMALL || !__any_sync(0xffffffffu, top > p.cap.small2);
 }
 
 // Bits [from, to] of 64.
@@ -323,7 +343,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool MODS = SCORE >= 0, CAP = MODS && (SCORE & fa::kCap), SLOPES = MODS && (SCORE & fa::kSlopes);
   constexpr bool SPLIT = MODS || !CAUSAL;
   int item = blockIdx.x, split = -1, half = 0;
-  if (SPLIT && item >= p.n_whole) {
+  int parts = 2;
+  if constexpr (MODS) parts = p.parts;
+  if (MODS && parts_first(p)) {
+    // (unequal work: the first items of the order in `parts` parts each, launched first)
+    if (item < p.n_split * parts) {
+      split = item / parts;
+      half = item - split * parts;
+      item = split;
+    } else {
+      item -= p.n_split * (parts - 1);
+    }
+  } else if (SPLIT && item >= p.n_whole) {
     split = (item - p.n_whole) >> 1;
     half = (item - p.n_whole) & 1;
     item = p.n_whole + split;
@@ -358,8 +389,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_m = max(0, m_end - m_begin);
   const int T_item = p.G * n_m;  // the item's tiles
   // this CTA's tiles: [t0, t0 + T) of the item's
-  const int t0 = split >= 0 && half ? T_item / 2 : 0;
-  const int T = split >= 0 ? (half ? T_item - T_item / 2 : T_item / 2) : T_item;
+  int t0 = split >= 0 && half ? T_item / 2 : 0;
+  int T = split >= 0 ? (half ? T_item - T_item / 2 : T_item / 2) : T_item;
+  if constexpr (MODS) {
+    if (split >= 0) {
+      t0 = (int)((long long)T_item * half / parts);
+      T = (int)((long long)T_item * (half + 1) / parts) - t0;
+    }
+  }
 
   if (threadIdx.x == 0) {
     *abort_flag = (smem_u32(smem) & 1023u) ? 1 : 0;
@@ -604,8 +641,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t sr[32], pk[16];
           tmem_ld32(T_S + lane_base + wg * 64 + ch * 32, sr);
           tmem_wait_ld();
-          modified_chunk<CAP, SLOPES, decltype(masked_)::value, decltype(both_)::value>(
-              p, sr, lse4 + ch * 8, rel0 + ch * 32, slope2, vis[ch], pr + ch * 32, pk);
+          constexpr bool M = decltype(masked_)::value, B = decltype(both_)::value;
+          if (!modified_chunk<CAP, SLOPES, M, B, CAP>(p, sr, lse4 + ch * 8, rel0 + ch * 32, slope2, vis[ch],
+                                                      pr + ch * 32, pk)) {
+            // a score past the polynomial: the whole chunk again (its scores are still in TMEM)
+            tmem_ld32(T_S + lane_base + wg * 64 + ch * 32, sr);
+            tmem_wait_ld();
+            modified_chunk<CAP, SLOPES, M, B, false>(p, sr, lse4 + ch * 8, rel0 + ch * 32, slope2, vis[ch],
+                                                     pr + ch * 32, pk);
+          }
           tmem_st16(T_S + lane_base + wg * 64 + ch * 16, pk);
         };
         using zero = std::integral_constant<int, 0>;
@@ -719,24 +763,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* other = nullptr;
       bool finish = true;
       if (split >= 0) {
-        float* own = p.part + (((size_t)split * 2 + half) * BN + r) * (HD + HDV);
+        float* own = p.part + (((size_t)split * parts + half) * BN + r) * (HD + HDV);
         write_partial<HDV>(T_DV + lane_base + wg * (HDV / 2), own + wg * (HDV / 2), T > 0);
         write_partial<HD>(T_DK + lane_base + wg * (HD / 2), own + HDV + wg * (HD / 2), T > 0);
         __threadfence();
         named_bar_sync(3, 256);
         if (warp == 4 && lane == 0) *split_seen = atomicAdd(&p.split_counters[split], 1u);
         named_bar_sync(3, 256);
-        finish = *split_seen == 1u;
+        finish = *split_seen == (unsigned)parts - 1u;
         if (finish) {
           __threadfence();
-          other = p.part + (((size_t)split * 2 + (half ^ 1)) * BN + r) * (HD + HDV);
+          other = p.part + ((size_t)split * parts * BN + r) * (HD + HDV);
+          if (!MODS) other += (size_t)(half ^ 1) * BN * (HD + HDV);
         }
       }
+      const int n_other = MODS ? parts : 1, skip = MODS ? half : -1;
+      constexpr size_t kPartStride = (size_t)BN * (HD + HDV);
       if (!finish) goto epilogue_done;
       stage_rows_bf16<HDV>(T_DV + lane_base + wg * (HDV / 2), smem + C::OFF_DV_STAGE, r, wg, 1.f, T > 0,
-                           other ? other + wg * (HDV / 2) : nullptr);
+                           other ? other + wg * (HDV / 2) : nullptr, n_other, kPartStride, skip);
       stage_rows_bf16<HD>(T_DK + lane_base + wg * (HD / 2), smem + C::OFF_DK_STAGE, r, wg, p.scale_grad, T > 0,
-                          other ? other + HDV + wg * (HD / 2) : nullptr);
+                          other ? other + HDV + wg * (HD / 2) : nullptr, n_other, kPartStride, skip);
       fence_async_smem();
       named_bar_sync(2, 256);
       if (warp == 4 && lane == 0) {
@@ -833,8 +880,10 @@ cudaError_t launch_main_t(const fa::Problem& pr, const CUtensorMap* maps, const 
     if (e != cudaSuccess) return e;
     if (fa_attr.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
   }
-  // one CTA per item, two per split item (within int range: checked by the API, n_split <= kMaxSplitItems)
-  dim3 grid((unsigned)(bp.n_whole + 2 * bp.n_split));
+  // one CTA per item, two (or `parts`) per split item (within int range: checked by the API, n_split <= kMaxSplitItems)
+  int parts = 2;
+  if constexpr (SCORE >= 0) parts = bp.parts;
+  dim3 grid((unsigned)(bp.n_whole + parts * bp.n_split));
   fa_bwd_main<HD, HDV, CAUSAL, WINDOW, SCORE><<<grid, kThreads, C::SMEM, stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4], maps[5],
                                                                maps[6], bp);
   return cudaGetLastError();

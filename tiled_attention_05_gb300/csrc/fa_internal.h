@@ -88,8 +88,10 @@ inline int row_lo_off(const Problem& p) { return p.causal && p.window ? p.Tk - p
 //   u = s^2.  The odd polynomial of degree 7 has the least greatest error there,
 //   1.3e-7 of c (fitted to tanh(y) / y in y^2 by reweighted least squares); in fp32
 //   1.6e-7.  It needs no special function, of which the other form takes 1 1/4.
+// slope: with the polynomial's x (log2 units), a quarter of the derivative
+// 1 - (x / log2c)^2 is 1/4 + slope x^2.
 struct CapParams {
-  float log2c, in, small2, a[4];
+  float log2c, in, small2, a[4], slope;
 };
 inline CapParams cap_params(float softcap, float scale) {
   CapParams c = {};
@@ -98,6 +100,7 @@ inline CapParams cap_params(float softcap, float scale) {
   const double log2e = 1.4426950408889634, k = (double)scale / softcap;
   c.log2c = (float)(softcap * log2e);
   c.in = (float)(2.0 * scale * log2e / softcap);
+  c.slope = (float)(-0.25 / ((double)softcap * log2e * softcap * log2e));
   // (past k = 1000 the coefficients could leave fp32: the first form then serves all)
   const bool fits = k < 1000.0;
   c.small2 = fits ? (float)(0.25 / (k * k)) : -1.f;
@@ -265,6 +268,7 @@ struct ScoredBwdParams : BwdParams {
   const float* slopes;     // [Hq]
   int hi_off, lo_off;      // row i sees keys [i + lo_off, i + hi_off) (no plan)
   int two_sided;           // a row may see keys on both sides of its own position
+  int parts, split_first;  // CTAs per split item; the split items are the order's first (see scored_split)
   PlanView plan;
 };
 
@@ -317,6 +321,44 @@ struct BwdWorkspace {
   size_t dq_acc, lse2, delta, part, counters, total_min, total;
   int split_cap;  // items the partial area has room for
 };
-BwdWorkspace backward_workspace_layout(const Problem& p);
+// slots: rows of 128 keys in the partial area (items * parts); -1: the plain rule.
+BwdWorkspace backward_workspace_layout(const Problem& p, long long slots = -1, int items = 0);
+
+// Split items of the score-modified backward.  A key tile's work is the query tiles
+// that see it, so where there are few items the heaviest alone can outlast the
+// rest (a causal call with one item per SM runs twice its mean).  Then the items
+// above the mean per SM, the first of the order, run in parts; four tiles are
+// left to a part, whose set-up and fp32 partial sums cost about as much as two.
+// (B 2, 16 / 4 heads of 128, T 2001, causal: 142 us whole, 114 with every item in
+// four parts.)  A plan's documents are not known here: its items count as without
+// it.  With more than two items per SM the plain rule holds (equal work: a short
+// last round in halves).
+struct ScoredSplit {
+  int items, parts;  // 0: none
+};
+inline ScoredSplit scored_split(const Problem& p, int sms) {
+  const long long groups = (long long)p.B * p.Hkv, n = groups * p.kv_tiles();
+  if (n < 1 || sms < 1 || n > 2LL * sms || p.q_tiles() < 1) return {0, 1};
+  const int hi = row_hi_off(p), lo = row_lo_off(p);
+  auto work = [&](int k) {  // query tiles of key tile k, all heads of a group
+    const int k0 = k * kTile, last_key = (k0 + kTile < p.Tk ? k0 + kTile : p.Tk) - 1;
+    const int first = k0 - hi + 1 > 0 ? (k0 - hi + 1) / kTile : 0, last_row = last_key - lo;
+    const int end = last_row < 0 ? 0 : last_row / kTile + 1 < p.q_tiles() ? last_row / kTile + 1 : p.q_tiles();
+    return end > first ? (long long)p.G() * (end - first) : 0LL;
+  };
+  long long total = 0, most = 0;
+  for (int k = 0; k < p.kv_tiles(); ++k) {
+    const long long w = work(k);
+    total += w * groups;
+    if (w > most) most = w;
+  }
+  const double mean = (double)total / sms, target = mean > 4.0 ? mean : 4.0;
+  int parts = (int)(most / (1.2 * target)) + (most > 1.2 * target);
+  if (parts > 8) parts = 8;
+  long long items = 0;
+  for (int k = 0; k < p.kv_tiles() && (double)work(k) > target; ++k) items += groups;
+  if (items > kMaxSplitItems) items = kMaxSplitItems;
+  return parts < 2 || items < 1 ? ScoredSplit{0, 1} : ScoredSplit{(int)items, parts};
+}
 
 }  // namespace fa
