@@ -395,6 +395,21 @@ def test_one_document_is_the_plain_call():
 
 
 @gpu
+@pytest.mark.parametrize("score", [("mask", 0.0, False)] + SCORES, ids=lambda s: s[0])
+def test_a_row_of_one_key_returns_its_value(score):
+    _, cap, slopes = score
+    B, H, T, d = 1, 4, 900, 64
+    Q, K, V, dO = inputs(B, H, H, T, T, d, d, seed=5)
+    ids = torch.arange(T, dtype=torch.int32, device="cuda")[None]
+    mask = fa.fa_mask_plan(B, T, T, True, 0, ids, ids)  # every token a document
+    O, L = fa.fa_forward(Q, K, V, True, softcap=cap, slopes=alibi(H) if slopes else None, mask=mask)
+    assert torch.equal(O, V)
+    O, L = fa.fa_forward(Q[:, :, :1].contiguous(), K[:, :, :1].contiguous(), V[:, :, :1].contiguous(), True,
+                         softcap=cap or 9.0, slopes=alibi(H) if slopes else None)
+    assert torch.equal(O, V[:, :, :1])
+
+
+@gpu
 def test_empty_sizes():
     z = lambda *s: torch.zeros(*s, device="cuda", dtype=bf)  # noqa: E731
     ids = lambda T: torch.zeros(1, T, device="cuda", dtype=torch.int32)  # noqa: E731

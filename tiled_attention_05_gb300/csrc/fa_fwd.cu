@@ -15,8 +15,8 @@ cudaError_t launch_fwd_dims(const fa::Problem& pr, const fa::FwdShape& shape, co
 }
 
 // Joins the parts of a split forward: with reference m_s and sum l_s of part s and
-// M = max m_s, O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s and L = ln2 (M + log2 of
-// that sum).  A part that saw no key has l = 0 and no O.  One warp a row, HDV / 32
+// M = max m_s, O = sum 2^(m_s - M) O_s over the same sum of what each O is divided by,
+// and L = ln2 (M + log2 sum 2^(m_s - M) l_s).  A part that saw no key has l = 0 and no O.  One warp a row, HDV / 32
 // columns a lane.  Bound by HBM / L2 (the parts, fp32) and by its launch.
 template <int HDV>
 __global__ void __launch_bounds__(256) fa_fwd_join(const float* __restrict__ part, uint16_t* __restrict__ O,
@@ -31,28 +31,29 @@ __global__ void __launch_bounds__(256) fa_fwd_join(const float* __restrict__ par
   const int pair = pairs - 1 - i / (2 * BM);  // (items take the last pair first, heads fastest)
   const long long first = ((long long)pair * n_bh + bh) * split;  // the item's first part
   const int at = i % (2 * BM);
-  const float2* ml = reinterpret_cast<const float2*>(part + n_parts * 2 * BM * HDV);
+  const float4* ml = reinterpret_cast<const float4*>(part + n_parts * 2 * BM * HDV);
   float top = -__int_as_float(0x7f800000);
   for (int s = lane; s < split; s += 32) {
-    const float2 v = ml[(first + s) * 2 * BM + at];
+    const float4 v = ml[(first + s) * 2 * BM + at];
     if (v.y > 0.f) top = fmaxf(top, v.x);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  float sum = 0.f, acc[W];
+  float sum = 0.f, sum_o = 0.f, acc[W];
 #pragma unroll
   for (int e = 0; e < W; ++e) acc[e] = 0.f;
 #pragma unroll 4
   for (int s = 0; s < split; ++s) {
-    const float2 v = ml[(first + s) * 2 * BM + at];
+    const float4 v = ml[(first + s) * 2 * BM + at];
     if (!(v.y > 0.f)) continue;
     const float w = exp2f(v.x - top);
     const float* o = part + ((first + s) * 2 * BM + at) * HDV + lane * W;
     sum += w * v.y;
+    sum_o += w * v.z;
 #pragma unroll
     for (int e = 0; e < W; ++e) acc[e] += w * o[e];
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum > 0.f ? 1.f / sum_o : 0.f;
   uint32_t* out = reinterpret_cast<uint32_t*>(O + row * HDV + lane * W);
 #pragma unroll
   for (int e = 0; e < W; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);

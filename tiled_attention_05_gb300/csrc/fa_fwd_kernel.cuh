@@ -167,7 +167,7 @@ struct ScoredFwdParams : FwdParams {
   int two_sided;        // a row may see keys on both sides of its own position
   int row_mod, group;   // packed heads (fa::FwdShape)
   int split;            // CTAs per item
-  float* part;          // [items][split][256 rows][dv], then as many (m, l) pairs
+  float* part;          // [items][split][256 rows][dv], then as many (m, l, l of O, 0)
   fa::PlanView plan;
 };
 template <int SCORE>
@@ -354,16 +354,20 @@ struct BiasLine {
 // at a time, each written back as bf16 P over scores already read.  The cap is
 // taken by its polynomial; from the first score beyond it on (in any row of the
 // warp), the rest of the tile goes by the form that holds everywhere (the scores
-// are still in TMEM).  Returns the row's sum of P.
+// are still in TMEM).  Returns the row's sum of P, for L, and the sum that its O is
+// divided by.
 // MASKED: only the columns in vis4 count, and the row's position may be inside
-// the tile with visible keys on both sides.
+// the tile with visible keys on both sides.  Here the second sum is of P as rounded
+// to bf16, so that a row of few keys is divided by the weights that its O was made
+// of (with one key O is V exactly, as where a maximum makes its P 1).  In other
+// tiles the roundings of 128 keys and more even out, and the two sums are one.
 // The loop stays rolled: unrolled, its instructions crowd the MMA thread's out of
 // the instruction cache (T 8192, d 128: 925 us rolled, 1005 unrolled; two
 // warpgroups of 64 columns each per tile: 980 and 1025).
 template <bool SLOPES, bool MASKED>
-__device__ __forceinline__ float bounded_tile(uint32_t tS, const ScoredFwdParams& p, const uint32_t (&vis4)[BN / 32],
-                                              int rel0, float slope2, float m_ref) {
-  uint64_t rs[2] = {0ull, 0ull};
+__device__ __forceinline__ float2 bounded_tile(uint32_t tS, const ScoredFwdParams& p, const uint32_t (&vis4)[BN / 32],
+                                               int rel0, float slope2, float m_ref) {
+  uint64_t rs[2] = {0ull, 0ull}, rounded = 0ull;
   bool small = true;
   BiasLine line(rel0, slope2);
 #pragma unroll 1
@@ -426,10 +430,16 @@ __device__ __forceinline__ float bounded_tile(uint32_t tS, const ScoredFwdParams
     }
     rs[0] = f2_add(rs[0], part[0]);
     rs[1] = f2_add(rs[1], part[1]);
+    if (MASKED) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        rounded = f2_add(rounded, f2_pack(__uint_as_float(pk[c] << 16), __uint_as_float(pk[c] & 0xffff0000u)));
+    }
     tmem_st16(tS + 16 * ch, pk);
   }
   const uint64_t rs2 = f2_add(rs[0], rs[1]);
-  return f2_lo(rs2) + f2_hi(rs2);
+  const float sum = f2_lo(rs2) + f2_hi(rs2);
+  return make_float2(sum, MASKED ? f2_lo(rounded) + f2_hi(rounded) : sum);
 }
 
 // Slopes without a cap: two passes over the scores in TMEM, which keep few
@@ -871,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_ref = -slope2 * (float)(slope2 >= 0.f ? near : max(abs(to_lo), abs(to_hi)));
         }
       }
-      float l = 0.f;
+      float l = 0.f, l_o = 0.f;  // sum of P; (BOUNDED) the sum that O is divided by
       for (int jx = 0; ok && jx < nkv; ++jx) {  // jx-th key tile of this tile's range
         // the warp agrees on the outcome before its collective TMEM loads
         if (!__all_sync(0xffffffffu, fwd_wait(&s_full[x], ns & 1, abort_flag))) { ok = false; break; }
@@ -894,8 +904,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               interval_bits(lo, lim, vis);
               if (by_key) masked = document_bits(vis, p, batch, kv0, my_doc) || masked;
             }
-            l += masked ? bounded_tile<SLOPES, true>(tS, p, vis, rel0, slope2, m_ref)
-                        : bounded_tile<SLOPES, false>(tS, p, vis, rel0, slope2, m_ref);
+            const float2 sums = masked ? bounded_tile<SLOPES, true>(tS, p, vis, rel0, slope2, m_ref)
+                                       : bounded_tile<SLOPES, false>(tS, p, vis, rel0, slope2, m_ref);
+            l += sums.x;
+            l_o += sums.y;
           }
         } else {
           constexpr bool LINE = SLOPES && !CAP;  // two passes over the scores in TMEM
@@ -1017,6 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++no;
         tc_fence_after();
       }
+      if (!BOUNDED || (SLOPES && by_key)) l_o = l;
       // (a tile past the last row, or tile B of a single-tile item, has nothing to write)
       if (!ok || qx0 >= p.Tq || (x == 1 && it.single)) continue;
       const bool row_ok = i < p.Tq;
@@ -1024,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.split > 1) {  // the unnormalised row, its reference and sum, for fa_fwd_join
           const size_t row = ((size_t)fwd_index(n) * 2 + x) * BM + r;
           if (row_ok)
-            reinterpret_cast<float2*>(p.part + (size_t)p.n_items * 2 * BM * HDV)[row] = make_float2(m_ref, l);
+            reinterpret_cast<float4*>(p.part + (size_t)p.n_items * 2 * BM * HDV)[row] = make_float4(m_ref, l, l_o, 0.f);
           float4* out = reinterpret_cast<float4*>(p.part + row * HDV);
           if (nkv > 0) {
 #pragma unroll
@@ -1044,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (row_ok) p.L[(size_t)it.bh * p.Tq + i] = l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : NEG_INF;
-      const float inv_l = l > 0.f ? 1.f / l : 0.f;
+      const float inv_l = l > 0.f ? 1.f / l_o : 0.f;
       uint4* orow = reinterpret_cast<uint4*>(p.O + ((size_t)it.bh * p.Tq + (row_ok ? i : 0)) * HDV);
 #pragma unroll
       for (int c = 0; c < HDV / 32; ++c) {
