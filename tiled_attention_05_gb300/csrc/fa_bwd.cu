@@ -1,6 +1,6 @@
 // Backward pass: the preprocess and cast kernels, the plain instances of the
 // main kernel (fa_bwd_kernel.cuh) and the launcher that picks an instance (the
-// score-modified ones are compiled in fa_scored_64.cu and fa_scored_128.cu).
+// score-modified ones are compiled in fa_scored_bwd_*.cu).
 #include "fa_bwd_kernel.cuh"
 
 namespace {

@@ -1,6 +1,6 @@
 // Backward main kernel of tiled exact attention on sm_103a (the plain instances
 // and the other two kernels are in fa_bwd.cu, the score-modified instances in
-// fa_scored_*.cu).
+// fa_scored_bwd_*.cu).
 //
 // Method ("What Ordinary Autograd Saves", section "Why this is
 // FlashAttention's second idea"; "Backward Pass Implementation", section "The
@@ -62,12 +62,16 @@
 //
 // Score-modified instances (SCORE >= 0) rebuild the modified scores as the
 // forward does (fa_fwd_kernel.cuh).  The cap's derivative is 1 - tanh^2 =
-// 4 r (1 - r) with the r = 1 / (1 + exp(2 s / c)) already at hand, so the fp32
-// P kept for dS is P r (1 - r) and the factor 4 joins the scale of dK and dQ:
-// no further registers.  The distance bias has no gradient (its slopes are
-// constants).  Masks: query rows [from, to] see this thread's key, from the
-// mask plan or from the two lines of causal mask and window; a plan whose
-// intervals are not in order is looked up row by row instead.
+// 4 e r^2 with the e = exp(2 s / c) and r = 1 / (1 + e) already at hand (with the
+// polynomial 1 - (x / c)^2), so the fp32 P kept for dS is P times a quarter of it
+// and the factor 4 joins the scale of dK and dQ: no further registers.  The
+// distance bias has no gradient (its slopes are constants).  Masks: query rows
+// [from, to] see this thread's key, from the mask plan or from the two lines of
+// causal mask and window; a plan whose intervals are not in order is looked up
+// row by row instead.  Where there are few key tiles of unequal work, the
+// heaviest run in parts (fa::scored_split).  Bounded as the plain form is, with
+// a longer elementwise phase: 32 / 8 heads of 128, T 8192, causal, 990 us plain,
+// 1030 with slopes, 1185 with a cap, 1283 with both.
 #pragma once
 #include <cstdint>
 #include <type_traits>

@@ -1,5 +1,5 @@
 // Forward kernel of tiled exact attention on sm_103a (the plain instances are
-// in fa_fwd.cu, the score-modified ones in fa_scored_*.cu).
+// in fa_fwd.cu, the score-modified ones in fa_scored_fwd_*.cu).
 //
 // Method ("What Ordinary Autograd Saves: Tiling the Forward Pass Is Only Half
 // the Algorithm", section "The implementation under test"): for one block of
@@ -51,18 +51,26 @@
 // MMAs and softmax.  Every barrier phase (and ring position) is counted from
 // the start of the CTA, not of the item.
 //
-// Score-modified instances (SCORE >= 0, bits kCap and kSlopes) work on the
-// scores between the TMEM load and the row maximum, in log2 units:
-//   cap     x = c tanh(s / c) = c - 2 c / (1 + exp(2 s / c)): one ex2, one
-//           reciprocal and one FMA per element, exact to a few 2^-24 of c (the
-//           single-instruction tanh is good to 2^-11 only, which would put
-//           0.02 on a score near a cap of 50);
-//   slopes  x -= slope_h |i + Tk - Tq - j|, one packed FMA on exact integer
-//           distances.
+// Score-modified instances (SCORE >= 0; bits in fa::ScoreBits) change the scores
+// between their TMEM load and the exponential, in log2 units:
+//   cap     x = c tanh(s / c) = c - 2 c / (1 + exp(2 s / c)): one ex2, a quarter of a
+//           reciprocal (cap_quad) and one FMA per element, off by at most 2^-20 of c
+//           (the single-instruction tanh is good to 2^-11 only, which would put
+//           0.02 on a score near a cap of 50); an odd polynomial where |s| <= c / 2.
+//   slopes  x -= slope_h |i + Tk - Tq - j|: a line in the column on either side of
+//           the row's position, which joins the exponent.
+// kBounded: a capped score is bounded, so no maximum is looked for and O is never
+// rescaled (bounded_tile).  kSlopes alone: two passes over the scores in TMEM
+// (line_max, line_exp).  The rest holds a row in registers as the plain form does.
 // Their masks are one interval of keys per row, [lo, hi): causal, window and
 // tail are lines in i, documents and prefixes come from a mask plan (see
 // fa_mask_plan.cu), which also holds each query tile's key-tile range.  A warp
 // masks a tile only where one of its rows does not see all of it.
+// What bounds them is the MMA-issuing thread, as in the plain form, and beside it
+// the softmax: the more its warps issue, the longer each group of MMAs takes to
+// issue (PV 602 cycles a group plain, 731 with a cap, 774 with both; the softmax
+// 1050, 1800 and 2100 cycles a tile).  B 2, 32 / 8 heads of 128, T 8192, causal:
+// 758 us plain, 950 with a cap of 50, 994 with slopes, 1115 with both.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -927,48 +935,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             mt2 = masked ? line_max<true>(tS, sl2, vis, rel0, slope2) : line_max<false>(tS, sl2, vis, rel0, slope2);
           } else {
 #pragma unroll
-          for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-          tmem_wait_ld();
-          if constexpr (SCORE >= 0) {
-            if constexpr (CAP) cap_scores<SLOPES>(sr, p, rel0, slope2, crossing);
-            // (one end at a time: a tile seldom has both, and a loop over both is half
-            // as long again; packed documents 154 -> 141 us)
-            if (__any_sync(0xffffffffu, lim < BN)) {
+            for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+            tmem_wait_ld();
+            if constexpr (SCORE >= 0) {
+              if constexpr (CAP) cap_scores<SLOPES>(sr, p, rel0, slope2, crossing);
+              // (one end at a time: a tile seldom has both, and a loop over both is half
+              // as long again; packed documents 154 -> 141 us)
+              if (__any_sync(0xffffffffu, lim < BN)) {
 #pragma unroll
-              for (int c = 0; c < BN; ++c)
-                if (c >= lim) sr[c] = __float_as_uint(NEG_INF);
+                for (int c = 0; c < BN; ++c)
+                  if (c >= lim) sr[c] = __float_as_uint(NEG_INF);
+              }
+              if (__any_sync(0xffffffffu, lo > 0)) {
+#pragma unroll
+                for (int c = 0; c < BN; ++c)
+                  if (c < lo) sr[c] = __float_as_uint(NEG_INF);
+              }
+              if (by_key) mask_documents(sr, p, batch, kv0, my_doc);
+            } else {
+              // window: the tile's last row starts its window past this key tile's start
+              const bool win_mask = WINDOW && qx0 + BM - 1 + p.causal_off - p.window + 1 > kv0;
+              const bool need_mask = (kv0 + BN > p.Tk) || (CAUSAL && kv0 + BN - 1 > qx0 + p.causal_off) || win_mask;
+              if (need_mask) {
+                int lim = p.Tk - kv0;  // columns [lo, lim) are visible to row i
+                if (CAUSAL) lim = min(lim, i + p.causal_off + 1 - kv0);
+                const int lo = win_mask ? i + p.causal_off - p.window + 1 - kv0 : -BN;
+#pragma unroll
+                for (int c = 0; c < BN; ++c)
+                  if (c >= lim || c < lo) sr[c] = __float_as_uint(NEG_INF);
+              }
             }
-            if (__any_sync(0xffffffffu, lo > 0)) {
+            // row max: eight independent three-input max chains (short dependency depth)
+            float pm[8];
 #pragma unroll
-              for (int c = 0; c < BN; ++c)
-                if (c < lo) sr[c] = __float_as_uint(NEG_INF);
-            }
-            if (by_key) mask_documents(sr, p, batch, kv0, my_doc);
-          } else {
-            // window: the tile's last row starts its window past this key tile's start
-            const bool win_mask = WINDOW && qx0 + BM - 1 + p.causal_off - p.window + 1 > kv0;
-            const bool need_mask = (kv0 + BN > p.Tk) || (CAUSAL && kv0 + BN - 1 > qx0 + p.causal_off) || win_mask;
-            if (need_mask) {
-              int lim = p.Tk - kv0;  // columns [lo, lim) are visible to row i
-              if (CAUSAL) lim = min(lim, i + p.causal_off + 1 - kv0);
-              const int lo = win_mask ? i + p.causal_off - p.window + 1 - kv0 : -BN;
+            for (int k = 0; k < 8; ++k) pm[k] = __uint_as_float(sr[k]);
 #pragma unroll
-              for (int c = 0; c < BN; ++c)
-                if (c >= lim || c < lo) sr[c] = __float_as_uint(NEG_INF);
-            }
-          }
-          // row max: eight independent three-input max chains (short dependency depth)
-          float pm[8];
+            for (int c = 8; c + 16 <= BN; c += 16)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) pm[k] = __uint_as_float(sr[k]);
+              for (int k = 0; k < 8; ++k) pm[k] = fmax3(pm[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
 #pragma unroll
-          for (int c = 8; c + 16 <= BN; c += 16)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) pm[k] = fmax3(pm[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
-#pragma unroll
-          for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], __uint_as_float(sr[BN - 8 + k]));
-          const float mt = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
-          mt2 = mt * sl2;
+            for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], __uint_as_float(sr[BN - 8 + k]));
+            const float mt = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+            mt2 = mt * sl2;
           }
           float m_new = m_ref;
           if (mt2 > m_ref + kRescaleThreshold) m_new = mt2;  // also taken when m_ref == -inf
@@ -982,25 +990,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             rowsum = masked ? line_exp<true>(tS, sl2, vis, rel0, slope2, base)
                             : line_exp<false>(tS, sl2, vis, rel0, slope2, base);
           } else {
-          const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(-base, -base);
-          // exponentials (argument and row sum on packed pairs); P (packed bf16)
-          // goes over the already-loaded scores in TMEM 16 columns at a time
-          uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
+            const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(-base, -base);
+            // exponentials (argument and row sum on packed pairs); P (packed bf16)
+            // goes over the already-loaded scores in TMEM 16 columns at a time
+            uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-          for (int c = 0; c < BN / 32; ++c) {
-            uint32_t pk[16];
+            for (int c = 0; c < BN / 32; ++c) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const uint64_t xv = f2_fma(
+              for (int e = 0; e < 16; ++e) {
+                const uint64_t xv = f2_fma(
                   f2_pack(__uint_as_float(sr[32 * c + 2 * e]), __uint_as_float(sr[32 * c + 2 * e + 1])), sl2x2, nbase2);
-              const float e0 = ex2(f2_lo(xv)), e1 = ex2(f2_hi(xv));
-              rs[e & 3] = f2_add(rs[e & 3], f2_pack(e0, e1));
-              pk[e] = pack_bf16x2(e0, e1);
+                const float e0 = ex2(f2_lo(xv)), e1 = ex2(f2_hi(xv));
+                rs[e & 3] = f2_add(rs[e & 3], f2_pack(e0, e1));
+                pk[e] = pack_bf16x2(e0, e1);
+              }
+              tmem_st16(tS + 16 * c, pk);
             }
-            tmem_st16(tS + 16 * c, pk);
-          }
-          const uint64_t rs2 = f2_add(f2_add(rs[0], rs[1]), f2_add(rs[2], rs[3]));
-          rowsum = f2_lo(rs2) + f2_hi(rs2);
+            const uint64_t rs2 = f2_add(f2_add(rs[0], rs[1]), f2_add(rs[2], rs[3]));
+            rowsum = f2_lo(rs2) + f2_hi(rs2);
           }
           // O_X is idle here: the P.V of tile j-1 completed before S_X(j) did.
           const float alpha = (m_new == m_ref) ? 1.f : (m_ref == NEG_INF ? 0.f : ex2(m_ref - m_new));

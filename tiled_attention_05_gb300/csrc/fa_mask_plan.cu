@@ -15,11 +15,12 @@
 //   empty interval in its place of the order; the backward gives such a row no
 //   weight anyway (its L is -inf).
 //
-// Small and bound by latency, of which the first fetch of its instructions is the
-// larger part: a cluster of 8 CTAs per batch entry, three phases over keys, rows
+// Small and bound by latency, of which the first fetch of its instructions is a
+// large part: a cluster of 8 CTAs per batch entry, three phases over keys, rows
 // and keys again with cluster barriers between them (0.3 us each), and as little
-// code as will do.  (T 8192: 16.3 us with four rows' searches a lane unrolled side
-// by side, 14.4 us rolled, with the searches in global memory.)
+// code as will do.  T 8192: 24 us with each row's searches one after the other in
+// global memory, 16.3 with four rows' side by side, unrolled, 14.4 rolled, 12.3 in
+// shared memory; T 777, B 2: 9.
 #include <climits>
 #include <cooperative_groups.h>
 #include <cstdint>
