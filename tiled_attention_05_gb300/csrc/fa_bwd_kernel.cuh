@@ -366,9 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per_sb = p.sb_groups * p.kv_tiles;
   const int sb = item / per_sb;
   const int in_sb = item - sb * per_sb;
-  const int n = in_sb / p.sb_groups;  // key tile
+  int n = in_sb / p.sb_groups;  // key tile
   const int bkv = sb * p.sb_groups + (in_sb - n * p.sb_groups);
   const int b = bkv / p.Hkv, hk = bkv - b * p.Hkv;
+  if constexpr (MODS) {  // a plan's heaviest key tiles first
+    if (p.plan.m_beg) n = min(max(p.plan.key_order[(size_t)b * p.kv_tiles + n], 0), p.kv_tiles - 1);
+  }
   const int k0 = n * BN;
 
   int m_begin = 0, m_end = p.q_tiles;

@@ -165,13 +165,13 @@ struct PlanView {
   const int *kv_beg, *kv_end;          // key tiles a query tile visits
   const int *key_from, *key_to;        // key j is seen by rows [key_from, key_to), unless the flag by_row
   const int *m_beg, *m_end;            // query tiles a key tile visits
-  const int* pair_order;               // pairs of query tiles of a batch entry, most work first
+  const int *pair_order, *key_order;   // pairs of query tiles, and key tiles, of a batch entry: most work first
   const int *tile_doc_lo, *tile_doc_hi;  // least and greatest document of a key tile
   const int *by_key, *by_row;          // [B][kPlanCtas], any nonzero: set
 };
 struct PlanLayout {
   long long row_lo, row_hi, q_doc, k_doc, kv_beg, kv_end, key_from, key_to, m_beg, m_end, tile_doc_lo, tile_doc_hi,
-      pair_order, by_key, by_row, total;  // offsets in ints
+      pair_order, key_order, by_key, by_row, total;  // offsets in ints
 };
 inline PlanLayout plan_layout(const Problem& p) {
   const long long qt = (long long)p.B * p.q_tiles(), kt = (long long)p.B * p.kv_tiles();
@@ -195,6 +195,7 @@ inline PlanLayout plan_layout(const Problem& p) {
   l.tile_doc_lo = take(kt);
   l.tile_doc_hi = take(kt);
   l.pair_order = take((long long)p.B * ((p.q_tiles() + 1) / 2));
+  l.key_order = take(kt);
   l.by_key = take((long long)p.B * kPlanCtas);
   l.by_row = take((long long)p.B * kPlanCtas);
   l.total = at;
@@ -216,6 +217,7 @@ inline PlanView plan_view(const Problem& p, const void* plan) {
   v.m_beg = a + l.m_beg;
   v.m_end = a + l.m_end;
   v.pair_order = a + l.pair_order;
+  v.key_order = a + l.key_order;
   v.tile_doc_lo = a + l.tile_doc_lo;
   v.tile_doc_hi = a + l.tile_doc_hi;
   v.by_key = a + l.by_key;
@@ -330,8 +332,8 @@ BwdWorkspace backward_workspace_layout(const Problem& p, long long slots = -1, i
 // rest (a causal call with one item per SM runs twice its mean).  Then the items
 // above the mean per SM, the first of the order, run in parts; four tiles are
 // left to a part, whose set-up and fp32 partial sums cost about as much as two.
-// (B 2, 16 / 4 heads of 128, T 2001, causal: 142 us whole, 114 with every item in
-// four parts.)  A plan's documents are not known here: its items count as without
+// (B 2, 16 / 4 heads of 128, T 2001, prefixes: 142 us whole, 114 with every item in
+// four parts, 105 with the heavier half of the items in two.)  A plan's documents are not known here: its items count as without
 // it.  With more than two items per SM the plain rule holds (equal work: a short
 // last round in halves).
 struct ScoredSplit {
@@ -358,6 +360,8 @@ inline ScoredSplit scored_split(const Problem& p, int sms) {
   if (parts > 8) parts = 8;
   long long items = 0;
   for (int k = 0; k < p.kv_tiles() && (double)work(k) > target; ++k) items += groups;
+  // (few enough: all of them, so that no whole item starts after the others' parts)
+  if (items > 0 && n <= kMaxSplitItems) items = n;
   if (items > kMaxSplitItems) items = kMaxSplitItems;
   return parts < 2 || items < 1 ? ScoredSplit{0, 1} : ScoredSplit{(int)items, parts};
 }

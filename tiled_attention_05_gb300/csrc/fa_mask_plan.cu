@@ -41,7 +41,7 @@ constexpr int T = fa::kTile;
 struct PlanParams {
   fa::MaskInputs in;
   int *row_lo, *row_hi, *q_doc, *k_doc, *kv_beg, *kv_end, *key_from, *key_to, *m_beg, *m_end, *tile_doc_lo,
-      *tile_doc_hi, *pair_order, *by_key, *by_row;
+      *tile_doc_hi, *pair_order, *key_order, *by_key, *by_row;
   int Tq, Tk, q_tiles, kv_tiles, causal, window, prefix_per_row;
   int room;  // ints of dynamic shared memory
 };
@@ -256,6 +256,22 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) fa_mas
   }
   bad = __syncthreads_or(bad);
   if (threadIdx.x == 0) p.by_row[b * kCtas + cta] = bad;
+  cluster.sync();
+
+  // ---- key tiles by work
+  const int *m_beg = p.m_beg + (long long)b * p.kv_tiles, *m_end = p.m_end + (long long)b * p.kv_tiles;
+#pragma unroll 1
+  for (int n = warp; n < p.kv_tiles; n += warps) {
+    const int w = m_end[n] - m_beg[n];
+    int before = 0;
+#pragma unroll 1
+    for (int z = lane; z < p.kv_tiles; z += 32) {
+      const int v = m_end[z] - m_beg[z];
+      before += v > w || (v == w && z < n);
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (lane == 0) p.key_order[(long long)b * p.kv_tiles + before] = n;
+  }
 }
 
 }  // namespace
@@ -281,6 +297,7 @@ cudaError_t launch_mask_plan(const Problem& pr, const MaskInputs& in, void* plan
   p.tile_doc_lo = a + l.tile_doc_lo;
   p.tile_doc_hi = a + l.tile_doc_hi;
   p.pair_order = a + l.pair_order;
+  p.key_order = a + l.key_order;
   p.by_key = a + l.by_key;
   p.by_row = a + l.by_row;
   p.Tq = pr.Tq;
