@@ -5,7 +5,8 @@ on the CPU over random interleavings.
 As for the two halves of test_bwd_split_handoff.py, with S parts: each part's
 threads write their fp32 rows, fence, meet on a barrier, and one takes a ticket;
 the part that draws ticket S - 1 fences and adds the other S - 1 parts' rows to
-its own.  No part waits for another.  Stores drain to memory at random moments;
+its own.  A part that finds the other S - 1 counted in before it writes is the last
+one: it writes no rows and takes no ticket.  No part waits for another.  Stores drain to memory at random moments;
 the partial area starts with the previous call's rows."""
 import random
 
@@ -28,7 +29,8 @@ def run(seed, S, mutation=None):
         out = {}
         own = {(h, r): float(100 * call + 10 * h + r + 1) for h in range(S) for r in range(ROWS)}
         buf = {k: [] for k in own}
-        arrived = {(h, b): 0 for h in range(S) for b in (1, 2)}
+        arrived = {(h, b): 0 for h in range(S) for b in (0, 1, 2)}
+        peeked = {}
         ticket = {}
 
         def drain(key):
@@ -37,6 +39,15 @@ def run(seed, S, mutation=None):
                 mem[addr] = val
 
         def thread(h, r):
+            if r == 0:
+                peeked[h] = mem["cnt"] >= (S - 2 if mutation == "peeks-one-early" else S - 1)
+            arrived[(h, 0)] += 1
+            while arrived[(h, 0)] < ROWS:
+                yield
+            if peeked[h]:
+                ticket[h] = S - 1
+                yield from finish(h, r)
+                return
             buf[(h, r)].append((("part", h, r), (call, own[(h, r)])))
             yield
             if mutation != "no-writer-fence":
@@ -50,11 +61,16 @@ def run(seed, S, mutation=None):
             arrived[(h, 2)] += 1
             while arrived[(h, 2)] < ROWS:
                 yield
-            if ticket[h] != (1 if mutation == "second-finishes" else S - 1):
-                return
+            if ticket[h] == (1 if mutation == "second-finishes" else S - 1):
+                yield from finish(h, r)
+
+        def finish(h, r):
+            yield
             total = own[(h, r)]
             for other in range(S):
-                if other == h and mutation != "own-part-twice":
+                if other == h:
+                    if mutation == "own-part-twice":
+                        total += own[(h, r)]
                     continue
                 got = mem[("part", other, r)]
                 if got[0] != call:
@@ -85,7 +101,7 @@ def test_the_last_part_stores_the_sum(S):
         run(seed, S)
 
 
-@pytest.mark.parametrize("mutation", ["no-writer-fence", "second-finishes", "counter-not-zeroed", "own-part-twice"])
+@pytest.mark.parametrize("mutation", ["no-writer-fence", "second-finishes", "counter-not-zeroed", "own-part-twice", "peeks-one-early"])
 def test_planted_mistakes_are_caught(mutation):
     caught = 0
     for seed in range(400):

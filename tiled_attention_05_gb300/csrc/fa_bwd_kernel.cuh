@@ -252,7 +252,8 @@ __device__ __forceinline__ bool modified_chunk(const ScoredBwdParams& p, const u
       if (CAP && SMALL) {
         const uint64_t u = f2_mul(x[h], x[h]);
         top = fmax3(top, f2_lo(u), f2_hi(u));
-        uint64_t t = f2_fma(u, f2_pack(p.cap.a[3], p.cap.a[3]), f2_pack(p.cap.a[2], p.cap.a[2]));
+        uint64_t t = f2_fma(u, f2_pack(p.cap.a[4], p.cap.a[4]), f2_pack(p.cap.a[3], p.cap.a[3]));
+        t = f2_fma(u, t, f2_pack(p.cap.a[2], p.cap.a[2]));
         t = f2_fma(u, t, f2_pack(p.cap.a[1], p.cap.a[1]));
         t = f2_mul(x[h], f2_fma(u, t, f2_pack(p.cap.a[0], p.cap.a[0])));
         w = f2_fma(f2_mul(t, t), f2_pack(p.cap.slope, p.cap.slope), f2_pack(0.25f, 0.25f));
@@ -772,14 +773,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* other = nullptr;
       bool finish = true;
       if (split >= 0) {
-        float* own = p.part + (((size_t)split * parts + half) * BN + r) * (HD + HDV);
-        write_partial<HDV>(T_DV + lane_base + wg * (HDV / 2), own + wg * (HDV / 2), T > 0);
-        write_partial<HD>(T_DK + lane_base + wg * (HD / 2), own + HDV + wg * (HD / 2), T > 0);
-        __threadfence();
-        named_bar_sync(3, 256);
-        if (warp == 4 && lane == 0) *split_seen = atomicAdd(&p.split_counters[split], 1u);
-        named_bar_sync(3, 256);
-        finish = *split_seen == (unsigned)parts - 1u;
+        // (modified scores: a part that finds all others counted in is the last, and
+        // need not write its own sums)
+        bool last = false;
+        if constexpr (MODS) {
+          if (warp == 4 && lane == 0) *split_seen = __ldcg(&p.split_counters[split]);
+          named_bar_sync(3, 256);
+          last = *split_seen == (unsigned)parts - 1u;
+          named_bar_sync(3, 256);  // all have read it
+        }
+        if (last) {
+          finish = true;
+        } else {
+          float* own = p.part + (((size_t)split * parts + half) * BN + r) * (HD + HDV);
+          write_partial<HDV>(T_DV + lane_base + wg * (HDV / 2), own + wg * (HDV / 2), T > 0);
+          write_partial<HD>(T_DK + lane_base + wg * (HD / 2), own + HDV + wg * (HD / 2), T > 0);
+          __threadfence();
+          named_bar_sync(3, 256);
+          if (warp == 4 && lane == 0) *split_seen = atomicAdd(&p.split_counters[split], 1u);
+          named_bar_sync(3, 256);
+          finish = *split_seen == (unsigned)parts - 1u;
+        }
         if (finish) {
           __threadfence();
           other = p.part + ((size_t)split * parts * BN + r) * (HD + HDV);

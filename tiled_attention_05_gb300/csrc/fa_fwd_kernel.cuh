@@ -309,7 +309,8 @@ __device__ __forceinline__ bool fwd_item(const FwdParamsOf<SCORE>& p, int n, Fwd
 
 // The polynomial of fa::CapParams without its leading factor s, of u = s^2.
 __device__ __forceinline__ uint64_t cap_poly(const fa::CapParams& c, uint64_t u) {
-  uint64_t t = f2_fma(u, f2_pack(c.a[3], c.a[3]), f2_pack(c.a[2], c.a[2]));
+  uint64_t t = f2_fma(u, f2_pack(c.a[4], c.a[4]), f2_pack(c.a[3], c.a[3]));
+  t = f2_fma(u, t, f2_pack(c.a[2], c.a[2]));
   t = f2_fma(u, t, f2_pack(c.a[1], c.a[1]));
   return f2_fma(u, t, f2_pack(c.a[0], c.a[0]));
 }
@@ -849,40 +850,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ns = 0, no = 0;  // s_full / o_done phases waited for
     int base = 0;        // ring position of the current item's first key tile
     bool ok = run;
-    FwdItem it;
-    for (int n = 0; ok && fwd_item<CAUSAL, WINDOW, SCORE>(p, n, &it); ++n) {
+    // What a row's mask and bias need (SCORE >= 0), read from the plan or worked out.
+    struct Row {
+      int lo = 0, hi = 0;  // the keys it sees
+      int doc = 0;         // its document, where the plan wants documents compared key by key
+      int pos = 0, batch = 0;  // its position among Tq, its batch entry
+      bool by_key = false;
+      float slope2 = 0.f;  // bias per step of the distance, log2 units
+    };
+    auto row_of = [&](const FwdItem& it) -> Row {
+      Row w;
+      if constexpr (SCORE >= 0) {
+        const int i = it.q0 + x * BM + r;
+        w.pos = i;
+        w.batch = it.bh / p.Hq;
+        // (packed heads: the row's position, and its head, within the group)
+        int head = 0;
+        if (kIsFew<SCORE> && p.row_mod) {
+          const int row = min(i, p.Tq - 1);
+          head = row / p.row_mod;
+          w.pos = row - head * p.row_mod;
+        }
+        if (p.plan.kv_beg) {
+          const size_t at = (size_t)w.batch * p.q_tiles * BM + (i < p.Tq ? w.pos : 0);
+          w.lo = p.plan.row_lo[at];
+          w.hi = i < p.Tq ? min(p.plan.row_hi[at], p.Tk) : 0;
+          w.doc = p.plan.q_doc[at];
+          w.by_key = fa::plan_flag(p.plan.by_key, w.batch);
+        } else {
+          w.lo = max(0, w.pos + p.lo_off);
+          w.hi = min(p.Tk, w.pos + p.hi_off);
+        }
+        if (SLOPES)
+          w.slope2 = p.slopes[(it.bh - w.batch * p.Hq) * (kIsFew<SCORE> ? p.group : 1) + head] * 1.4426950408889634f;
+      }
+      return w;
+    };
+    FwdItem it, next;
+    bool more = fwd_item<CAUSAL, WINDOW, SCORE>(p, 0, &it);
+    Row row, next_row;
+    if (more) row = row_of(it);
+    for (int n = 0; ok && more; ++n, it = next, row = next_row) {
       const int item_base = base;
       base += it.ue - it.ub;
       const int kbx = x ? it.kb[1] : it.kb[0];  // first key tile of this tile's range
       const int nkv = (x ? it.ke[1] : it.ke[0]) - kbx;
       const int qx0 = it.q0 + x * BM;
       const int i = qx0 + r;  // query row
-      int row_lo = 0, row_hi = 0;  // the keys row i sees (SCORE >= 0)
-      int my_doc = 0;              // its document, where the plan wants documents compared key by key
-      bool by_key = false;
-      float slope2 = 0.f;
-      int batch = 0, pos = i;  // the row's position among Tq
-      if constexpr (SCORE >= 0) {
-        batch = it.bh / p.Hq;
-        // (packed heads: the row's position, and its head, within the group)
-        int head = 0;
-        if (kIsFew<SCORE> && p.row_mod) {
-          const int row = min(i, p.Tq - 1);
-          head = row / p.row_mod;
-          pos = row - head * p.row_mod;
-        }
-        if (p.plan.kv_beg) {
-          const size_t at = (size_t)batch * p.q_tiles * BM + (i < p.Tq ? pos : 0);
-          row_lo = p.plan.row_lo[at];
-          row_hi = i < p.Tq ? min(p.plan.row_hi[at], p.Tk) : 0;
-          by_key = fa::plan_flag(p.plan.by_key, batch);
-          if (by_key) my_doc = p.plan.q_doc[at];
-        } else {
-          row_lo = max(0, pos + p.lo_off);
-          row_hi = min(p.Tk, pos + p.hi_off);
-        }
-        if (SLOPES) slope2 = p.slopes[(it.bh - batch * p.Hq) * (kIsFew<SCORE> ? p.group : 1) + head] * 1.4426950408889634f;
-      }
+      const int row_lo = row.lo, row_hi = row.hi, my_doc = row.doc, pos = row.pos, batch = row.batch;
+      const bool by_key = row.by_key;
+      const float slope2 = row.slope2;
+      // reference max (log2 units) the P values are taken against
       float m_ref = NEG_INF;
       if (BOUNDED && !(SLOPES && by_key)) {
         m_ref = 0.f;
@@ -1041,6 +1059,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&p_full[x]);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       }
+      // The next item is looked up here, where few registers are live and its loads
+      // overlap the wait and the epilogue: the epilogue and the start of an item
+      // are all that the MMA thread waits for between items.
+      more = ok && fwd_item<CAUSAL, WINDOW, SCORE>(p, n + 1, &next);
+      if (more) next_row = row_of(next);
       // ---- epilogue: O / l -> bf16 -> global (one row per thread); L -> global
       if (ok && nkv > 0) {
         if (!__all_sync(0xffffffffu, fwd_wait(&o_done[x], no & 1, abort_flag))) ok = false;

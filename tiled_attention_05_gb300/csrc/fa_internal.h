@@ -84,28 +84,31 @@ inline int row_lo_off(const Problem& p) { return p.causal && p.window ? p.Tk - p
 // The cap, for the kernels.  c * tanh(s * scale / c) in log2 units of a raw score s:
 //   everywhere  log2c - 2 log2c / (1 + exp2(in * s));
 //   for s^2 <= small2, i.e. arguments y = s * scale / c up to 1/2, where scores
-//   mostly are (a cap of 50 and scores up to 25):  s * (a0 + u (a1 + u (a2 + u a3))),
-//   u = s^2.  The odd polynomial of degree 7 has the least greatest error there,
-//   1.3e-7 of c (fitted to tanh(y) / y in y^2 by reweighted least squares); in fp32
-//   1.6e-7.  It needs no special function, of which the other form takes 1 1/4.
+//   mostly are (a cap of 50 and scores up to 25):  s * (a0 + u (a1 + ... + u a4)),
+//   u = s^2.  The odd polynomial of degree 9 has the least greatest error there,
+//   3.1e-9 of c (fitted to tanh(y) / y in y^2 by reweighted least squares); in fp32
+//   3.6e-8.  (Degree 7: 1.3e-7, of which 2.3e-6 of a small score, which L shows; one
+//   FMA less.)  It needs no special function, of which the other form takes 1 1/4.
 // slope: with the polynomial's x (log2 units), a quarter of the derivative
 // 1 - (x / log2c)^2 is 1/4 + slope x^2.
 struct CapParams {
-  float log2c, in, small2, a[4], slope;
+  float log2c, in, small2, a[5], slope;
 };
 inline CapParams cap_params(float softcap, float scale) {
   CapParams c = {};
   if (!(softcap > 0.f)) return c;
-  const double b[4] = {0.9999976761926945, -0.33320655218172035, 0.13145145656354004, -0.04337248367772688};
+  const double b[5] = {0.9999999316224369, -0.3333277617751536, 0.13320570677476742, -0.05276213076364388,
+                       0.016737567205032073};
   const double log2e = 1.4426950408889634, k = (double)scale / softcap;
   c.log2c = (float)(softcap * log2e);
   c.in = (float)(2.0 * scale * log2e / softcap);
   c.slope = (float)(-0.25 / ((double)softcap * log2e * softcap * log2e));
-  // (past k = 1000 the coefficients could leave fp32: the first form then serves all)
-  const bool fits = k < 1000.0;
+  // (past k = 1000, or with a scale past 2^20, the coefficients could leave fp32: the
+  // first form then serves all)
+  const bool fits = k < 1000.0 && scale < 0x1p20f;
   c.small2 = fits ? (float)(0.25 / (k * k)) : -1.f;
   double f = scale * log2e;
-  for (int i = 0; i < 4; ++i, f *= k * k) c.a[i] = fits ? (float)(b[i] * f) : 0.f;
+  for (int i = 0; i < 5; ++i, f *= k * k) c.a[i] = fits ? (float)(b[i] * f) : 0.f;
   return c;
 }
 
@@ -333,7 +336,8 @@ BwdWorkspace backward_workspace_layout(const Problem& p, long long slots = -1, i
 // above the mean per SM, the first of the order, run in parts; four tiles are
 // left to a part, whose set-up and fp32 partial sums cost about as much as two.
 // (B 2, 16 / 4 heads of 128, T 2001, prefixes: 142 us whole, 114 with every item in
-// four parts, 105 with the heavier half of the items in two.)  A plan's documents are not known here: its items count as without
+// four parts, 105 with the heavier half of the items in two; with all of them in two
+// 97 out of L2, but the step's time on cold data rises by 7 for the partial sums.)  A plan's documents are not known here: its items count as without
 // it.  With more than two items per SM the plain rule holds (equal work: a short
 // last round in halves).
 struct ScoredSplit {
@@ -360,8 +364,6 @@ inline ScoredSplit scored_split(const Problem& p, int sms) {
   if (parts > 8) parts = 8;
   long long items = 0;
   for (int k = 0; k < p.kv_tiles() && (double)work(k) > target; ++k) items += groups;
-  // (few enough: all of them, so that no whole item starts after the others' parts)
-  if (items > 0 && n <= kMaxSplitItems) items = n;
   if (items > kMaxSplitItems) items = kMaxSplitItems;
   return parts < 2 || items < 1 ? ScoredSplit{0, 1} : ScoredSplit{(int)items, parts};
 }
