@@ -444,6 +444,10 @@ def test_few_rows(shape):
         compare(Q, K, V, dO, False, 0, cap, slopes, docs=(some[:, :Tq].contiguous(), some), tag=name + " any order")
         compare(Q, K, V, dO, True, 0, cap, slopes, prefix=prefix, tag=name + " prefix")
     compare(Q, K, V, dO, False, 0, 0.0, None, docs=(rows, doc_k), tag="documents alone")
+    # heads of one tile with gentle, steep and negative slopes
+    mixed = torch.tensor([0.05, 20.0, -0.01, 7.0], device="cuda").repeat(-(-Hq // 4))[:Hq].contiguous()
+    for cap in (0.0, 30.0, 200.0):
+        compare(Q, K, V, dO, True, 0, cap, mixed, tag=f"mixed slopes, cap {cap}")
 
 
 @gpu

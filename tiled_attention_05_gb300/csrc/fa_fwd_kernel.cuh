@@ -944,11 +944,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool masked = false;
           float mt2;  // row max, in log2 units
           if constexpr (LINE) {
+            // (the warp takes one way: the ways load TMEM, and packed rows' slopes differ)
+            const bool steep = __any_sync(0xffffffffu, fabsf(slope2) > 8.f);
             masked = crossing || __any_sync(0xffffffffu, lim < BN || lo > 0);
-            if (masked || by_key || fabsf(slope2) > 8.f) {
+            if (masked || by_key || steep) {
               interval_bits(lo, lim, vis);
               if (by_key) masked = document_bits(vis, p, batch, kv0, my_doc) || masked;
-              masked = masked || fabsf(slope2) > 8.f;
+              masked = masked || steep;
             }
             mt2 = masked ? line_max<true>(tS, sl2, vis, rel0, slope2) : line_max<false>(tS, sl2, vis, rel0, slope2);
           } else {
