@@ -221,3 +221,21 @@ def test_other_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     check(out, Q, pos.view(1, 1, T), f, (64,), False)
+
+
+@pytest.mark.gpu
+def test_gradient_of_the_gradient():
+    """The rotation is linear: the gradient (R^T g) has the gradient R u in g, by the same kernels exactly."""
+    B, Hq, Hk, T, d, sections = 2, 3, 1, 21, 64, (8, 12, 12)
+    g = torch.Generator("cuda").manual_seed(5)
+    Q, K, gq, gk = (torch.randn(B, H, T, d, device="cuda", dtype=bf, generator=g).requires_grad_() for H in (Hq, Hk, Hq, Hk))
+    pos = torch.randint(0, 5000, (3, B, T), device="cuda", dtype=torch.int32, generator=g)
+    f = freqs(32)
+    Qr, Kr = fa.rotary(Q, K, pos, f, sections)
+    dQ, dK = torch.autograd.grad((Qr, Kr), (Q, K), (gq, gk), create_graph=True)
+    for got, want in zip((dQ, dK), fa.fa_rotary_backward(gq.detach(), gk.detach(), pos, f, sections)):
+        assert torch.equal(got, want)
+    uq, uk = torch.randn_like(dQ), torch.randn_like(dK)
+    ddq, ddk = torch.autograd.grad((dQ, dK), (gq, gk), (uq, uk))
+    for got, want in zip((ddq, ddk), fa.fa_rotary(uq, uk, pos, f, sections)):
+        assert torch.equal(got, want)

@@ -600,3 +600,11 @@ def test_other_stream():
     dQ, dK, dV = fa.fa_backward(Q, K, V, O, dO, L, True, stream=s, mask=mask)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(O, want[0]) and torch.equal(L, want[1]) and torch.equal(dK, want[3]) and torch.equal(dV, want[4])
+
+
+@pytest.mark.gpu
+def test_no_cap_by_none():
+    Q, K, V, _ = inputs(1, 4, 2, 70, 70, 64, 64, 3)
+    for got, want in zip(fa.fa_forward(Q, K, V, True, softcap=None, slopes=alibi(4)),
+                         fa.fa_forward(Q, K, V, True, slopes=alibi(4))):
+        assert torch.equal(got, want)

@@ -278,7 +278,7 @@ def _scores(dims: FaDims, device, softcap, slopes, mask, stream):
             raise ValueError(f"mask is on {mask.buffer.device}, expected {device} (all tensors on one GPU)")
         if stream is not None:
             mask.buffer.record_stream(stream)
-    return FaScores(float(softcap), _ptr(slopes), None if mask is None else mask.buffer.data_ptr())
+    return FaScores(float(softcap or 0.0), _ptr(slopes), None if mask is None else mask.buffer.data_ptr())
 
 
 def fa_forward(Q, K, V, causal: bool, scale: float | None = None, O=None, L=None, stream=None, window: int = 0,

@@ -114,20 +114,27 @@ def fa_rotary_backward(dQr, dKr, positions, inv_freq, sections=None, interleaved
 
 
 class _Rotary(torch.autograd.Function):
-    """Saves the positions and frequencies only."""
+    """Saves the positions and frequencies only.  Its gradient is the rotation back,
+    which is differentiated in turn where a graph of the gradient is asked for."""
 
     @staticmethod
-    def forward(ctx, Q, K, positions, inv_freq, sections, interleaved):
-        Qr, Kr = fa_rotary(Q, K, positions, inv_freq, sections, interleaved)
+    def forward(ctx, Q, K, positions, inv_freq, sections, interleaved, inverse=0):
+        turn = fa_rotary_backward if inverse else fa_rotary
+        Qr, Kr = turn(Q, K, positions, inv_freq, sections, interleaved)
         ctx.save_for_backward(positions, inv_freq)
-        ctx.sections, ctx.interleaved = sections, interleaved
+        ctx.sections, ctx.interleaved, ctx.inverse = sections, interleaved, inverse
         return Qr, Kr
 
     @staticmethod
     def backward(ctx, dQr, dKr):
         positions, inv_freq = ctx.saved_tensors
-        dQ, dK = fa_rotary_backward(_dense(dQr), _dense(dKr), positions, inv_freq, ctx.sections, ctx.interleaved)
-        return dQ, dK, None, None, None, None
+        dQr, dKr = _dense(dQr), _dense(dKr)
+        if torch.is_grad_enabled():
+            dQ, dK = _Rotary.apply(dQr, dKr, positions, inv_freq, ctx.sections, ctx.interleaved, 1 - ctx.inverse)
+        else:
+            turn = fa_rotary if ctx.inverse else fa_rotary_backward
+            dQ, dK = turn(dQr, dKr, positions, inv_freq, ctx.sections, ctx.interleaved)
+        return dQ, dK, None, None, None, None, None
 
 
 def _dense(g):
