@@ -19,6 +19,8 @@ __global__ void __launch_bounds__(256) fa_bwd_pre(const uint16_t* __restrict__ O
                                                   float* __restrict__ delta, float* __restrict__ dq_acc,
                                                   unsigned int* __restrict__ split_counters, int n_counters,
                                                   long long rows_pad, int Tq, long long Tq_pad) {
+  grid_next();
+  grid_previous();
   if (blockIdx.x == 0)
     for (int c = threadIdx.x; c < n_counters; c += blockDim.x) split_counters[c] = 0u;
   constexpr int LPR = HDV / 8;   // lanes per row
@@ -77,6 +79,8 @@ __global__ void __launch_bounds__(256) fa_bwd_pre(const uint16_t* __restrict__ O
 template <int HD>
 __global__ void __launch_bounds__(256) fa_dq_cast(const float* __restrict__ dq_acc, uint16_t* __restrict__ dQ,
                                                   long long q_rows, int Tq, long long Tq_pad, float scale) {
+  grid_next();
+  grid_previous();
   constexpr int LPR = HD / 8;
   constexpr int RPG = 32 / LPR;
   constexpr int UNR = 2;
@@ -221,10 +225,9 @@ cudaError_t launch_backward(const Problem& pr, const ScoreMods& mods, const void
   if (stages & FA_BWD_PRE) {
   auto pre = pr.d == 64 ? (pr.dv == 64 ? fa_bwd_pre<64, 64> : fa_bwd_pre<64, 128>)
                         : (pr.dv == 64 ? fa_bwd_pre<128, 64> : fa_bwd_pre<128, 128>);
-  pre<<<grid_for(rows_pad, 8 * 2 * (32 / (pr.dv / 8))), 256, 0, stream>>>(static_cast<const uint16_t*>(O), static_cast<const uint16_t*>(dO), L,
-                                                 lse2, delta, dq_acc, split_counters, split_cap, rows_pad, pr.Tq,
-                                                 pr.Tq_pad());
-  e = cudaGetLastError();
+  e = launch_next(pre, grid_for(rows_pad, 8 * 2 * (32 / (pr.dv / 8))), 256, 0, stream, static_cast<const uint16_t*>(O),
+                  static_cast<const uint16_t*>(dO), L, lse2, delta, dq_acc, split_counters, split_cap, rows_pad, pr.Tq,
+                  pr.Tq_pad());
   if (e != cudaSuccess) return e;
   ++*launches;
   }
@@ -289,14 +292,9 @@ cudaError_t launch_backward(const Problem& pr, const ScoreMods& mods, const void
   // 3. dQ cast
   if (!(stages & FA_BWD_CAST)) return cudaSuccess;
   const int rows_per_block = 8 * 2 * (32 / (pr.d / 8));  // 8 warps, two row groups each
-  if (pr.d == 64)
-    fa_dq_cast<64><<<grid_for(q_rows, rows_per_block), 256, 0, stream>>>(dq_acc, static_cast<uint16_t*>(dQ), q_rows,
-                                                                         pr.Tq, pr.Tq_pad(), scale_grad(pr, mods));
-  else
-    fa_dq_cast<128><<<grid_for(q_rows, rows_per_block), 256, 0, stream>>>(dq_acc, static_cast<uint16_t*>(dQ),
-                                                                          q_rows, pr.Tq, pr.Tq_pad(),
-                                                                          scale_grad(pr, mods));
-  e = cudaGetLastError();
+  auto cast = pr.d == 64 ? fa_dq_cast<64> : fa_dq_cast<128>;
+  e = launch_next(cast, grid_for(q_rows, rows_per_block), 256, 0, stream, dq_acc, static_cast<uint16_t*>(dQ), q_rows, pr.Tq,
+                  pr.Tq_pad(), scale_grad(pr, mods));
   if (e == cudaSuccess) ++*launches;
   return e;
 }

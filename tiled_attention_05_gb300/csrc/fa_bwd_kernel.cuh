@@ -314,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ CUtensorMap tmdK, const __grid_constant__ CUtensorMap tmdV,
                 const __grid_constant__ CUtensorMap tmAcc, const BwdParamsOf<SCORE> p) {
   using C = BwdCfg<HD, HDV>;
+  if constexpr (SCORE >= 0) grid_next();
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int NQ = C::NQ, NDO = C::NDO;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);

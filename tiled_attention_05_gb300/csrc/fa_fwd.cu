@@ -22,6 +22,8 @@ template <int HDV>
 __global__ void __launch_bounds__(256) fa_fwd_join(const float* __restrict__ part, uint16_t* __restrict__ O,
                                                    float* __restrict__ L, long long rows, int rows_per_head,
                                                    int pairs, int n_bh, int split, long long n_parts) {
+  grid_next();
+  grid_previous();
   constexpr int W = HDV / 32;
   const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
@@ -108,9 +110,8 @@ cudaError_t launch_forward(const Problem& pr, const ScoreMods& mods, const void*
   if (shape.split > 1) {
     auto join = pr.dv == 64 ? fa_fwd_join<64> : fa_fwd_join<128>;
     const int pairs = (shape.rows + 2 * BM - 1) / (2 * BM);
-    join<<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(part, static_cast<uint16_t*>(O), L, rows, shape.rows, pairs,
-                                                         pr.B * shape.heads, shape.split, shape.items * shape.split);
-    e = cudaGetLastError();
+    e = launch_next(join, (unsigned)((rows + 7) / 8), 256, 0, stream, part, static_cast<uint16_t*>(O), L, rows, shape.rows,
+                    pairs, pr.B * shape.heads, shape.split, shape.items * shape.split);
     if (e == cudaSuccess) ++*launches;
   }
   return e;

@@ -603,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap tmV, const FwdParamsOf<SCORE> p) {
   using C = FwdCfg<HD, HDV>;
   constexpr int NS = C::NS;
+  if constexpr (SCORE >= 0) grid_next();
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_full = bars;           // [2] per tile

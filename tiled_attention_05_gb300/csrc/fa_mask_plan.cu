@@ -26,6 +26,7 @@
 #include <cstdint>
 
 #include "fa_internal.h"
+#include "sm103_ptx.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -77,6 +78,8 @@ __device__ __forceinline__ bool any_flag(const int* flags) {
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) fa_mask_plan_kernel(const PlanParams p) {
   extern __shared__ int buf[];
+  fa_ptx::grid_next();
+  fa_ptx::grid_previous();
   cg::cluster_group cluster = cg::this_cluster();
   const int b = blockIdx.x / kCtas, cta = blockIdx.x % kCtas;
   const int lane = threadIdx.x & 31;
@@ -313,8 +316,7 @@ cudaError_t launch_mask_plan(const Problem& pr, const MaskInputs& in, void* plan
   p.room = smem / 4;
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(fa_mask_plan_kernel), kMaxSmem);
   if (e != cudaSuccess) return e;
-  fa_mask_plan_kernel<<<(unsigned)pr.B * kCtas, kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_next(fa_mask_plan_kernel, (unsigned)pr.B * kCtas, kThreads, smem, stream, p);
 }
 
 }  // namespace fa

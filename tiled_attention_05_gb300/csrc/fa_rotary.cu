@@ -85,6 +85,8 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 // UNITS: threads per token (d / 16).
 template <int UNITS, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, 6) fa_rotary_kernel(const RotaryParams p) {
+  grid_next();
+  grid_previous();
   const long long n = (long long)blockIdx.x * (kThreads / UNITS) + threadIdx.x / UNITS;
   if (n >= p.tokens) return;
   const int unit = threadIdx.x % UNITS;
@@ -226,19 +228,9 @@ fa_status fa_rotary(const fa_rotary_dims* dims, const void* Q, const void* K, co
   p.heads_per_block = (int)((heads + split - 1) / split);
   p.heads_per_block = (p.heads_per_block + kUnroll - 1) / kUnroll * kUnroll;
   const dim3 grid((unsigned)xb, (unsigned)((heads + p.heads_per_block - 1) / p.heads_per_block));
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (z.d == 64) {
-    if (z.interleaved)
-      fa_rotary_kernel<4, true><<<grid, kThreads, 0, st>>>(p);
-    else
-      fa_rotary_kernel<4, false><<<grid, kThreads, 0, st>>>(p);
-  } else {
-    if (z.interleaved)
-      fa_rotary_kernel<8, true><<<grid, kThreads, 0, st>>>(p);
-    else
-      fa_rotary_kernel<8, false><<<grid, kThreads, 0, st>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  auto kernel = z.d == 64 ? (z.interleaved ? fa_rotary_kernel<4, true> : fa_rotary_kernel<4, false>)
+                          : (z.interleaved ? fa_rotary_kernel<8, true> : fa_rotary_kernel<8, false>);
+  return fa::launch_next(kernel, grid, kThreads, 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"
