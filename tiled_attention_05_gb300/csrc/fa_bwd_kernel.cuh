@@ -506,13 +506,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id_q = idesc_bf16(BM, HD, 1, 1);    // dQ: M = queries (A MN-major), N = d
       const uint32_t k_base = smem_u32(smem + C::OFF_K), v_base = smem_u32(smem + C::OFF_V);
       const uint32_t ds_base = smem_u32(smem + C::OFF_DS);
+      const uint64_t k_desc = desc_kmajor(k_base), v_desc = desc_kmajor(v_base);
+      const uint64_t k_desc_mn = desc_mnmajor(k_base, BN * 128), ds_desc = desc_mnmajor(ds_base, BN * 128);
       // S^T(t) = K Q_t^T into T_S
       auto mma_s = [&](int t) {
-        const uint32_t q_base = smem_u32(smem + C::OFF_Q + (t % NQ) * C::QK_TILE);
+        const uint64_t q_desc = desc_kmajor(smem_u32(smem + C::OFF_Q + (t % NQ) * C::QK_TILE));
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k)
-          mma_ss(T_S, desc_kmajor(k_base + (k >> 2) * (BN * 128) + (k & 3) * 32),
-                 desc_kmajor(q_base + (k >> 2) * (BM * 128) + (k & 3) * 32), id_sdp, k > 0 ? 1u : 0u);
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t step = (k >> 2) * (BM * 128) + (k & 3) * 32;
+          mma_ss(T_S, desc_at(k_desc, step), desc_at(q_desc, step), id_sdp, k > 0 ? 1u : 0u);
+        }
         mma_commit(s_full);
       };
       // Issue order per tile t: dP^T(t), dV(t), S^T(t+1), dK(t), dQ(t).  S^T(t+1)
@@ -538,19 +541,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // dP^T shares its TMEM columns with dQ (d = 128): the previous tile's dQ must be drained
         if (!kOwnDQ && t > 0 && !mbar_wait(dq_empty, (t - 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
+        const uint64_t do_desc = desc_kmajor(do_base);
 #pragma unroll
-        for (int k = 0; k < HDV / 16; ++k)
-          mma_ss(T_DP, desc_kmajor(v_base + (k >> 2) * (BN * 128) + (k & 3) * 32),
-                 desc_kmajor(do_base + (k >> 2) * (BM * 128) + (k & 3) * 32), id_sdp, k > 0 ? 1u : 0u);
+        for (int k = 0; k < HDV / 16; ++k) {
+          const uint32_t step = (k >> 2) * (BM * 128) + (k & 3) * 32;
+          mma_ss(T_DP, desc_at(v_desc, step), desc_at(do_desc, step), id_sdp, k > 0 ? 1u : 0u);
+        }
         mma_commit(dp_full);
         if (!mbar_wait(p_ready, t & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         // P^T lives in TMEM as packed bf16 over S^T: query columns [0,64) at TMEM
         // columns [0,32), query columns [64,128) at [64,96) (each elementwise
         // warpgroup overwrote its own half of S^T).
+        const uint64_t do_desc_mn = desc_mnmajor(do_base, BM * 128);
 #pragma unroll
         for (int k = 0; k < BM / 16; ++k)
-          mma_ts(T_DV, T_S + (k >> 2) * 64 + (k & 3) * 8, desc_mnmajor(do_base + k * 2048, BM * 128), id_dv,
+          mma_ts(T_DV, T_S + (k >> 2) * 64 + (k & 3) * 8, desc_at(do_desc_mn, k * 2048), id_dv,
                  (t > 0 || k > 0) ? 1u : 0u);
         mma_commit(&do_empty[so]);
         if (t + 1 < T) {
@@ -568,9 +574,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // shared-memory round trip.)
         if (!mbar_wait(ds_ready, t & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
+        const uint64_t q_desc_mn = desc_mnmajor(q_base, BM * 128);
 #pragma unroll
         for (int k = 0; k < BM / 16; ++k)
-          mma_ts(T_DK, T_DP + (k >> 2) * 64 + (k & 3) * 8, desc_mnmajor(q_base + k * 2048, BM * 128), id_dk,
+          mma_ts(T_DK, T_DP + (k >> 2) * 64 + (k & 3) * 8, desc_at(q_desc_mn, k * 2048), id_dk,
                  (t > 0 || k > 0) ? 1u : 0u);
         mma_commit(&q_empty[st]);
         if (kOwnDQ && !C::VOUCH && t > 0) {  // dQ(t-1) drained from its columns
@@ -579,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < BN / 16; ++k)
-          mma_ss(T_DQ, desc_mnmajor(ds_base + k * 2048, BN * 128), desc_mnmajor(k_base + k * 2048, BN * 128), id_q,
+          mma_ss(T_DQ, desc_at(ds_desc, k * 2048), desc_at(k_desc_mn, k * 2048), id_q,
                  k > 0 ? 1u : 0u);
         mma_commit(dq_full);
       }
