@@ -642,7 +642,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // which of this warpgroup's 64 queries see this thread's key, by bits
         const int c0 = q0 + wg * 64;  // first of them
         uint32_t vis[2] = {~0u, ~0u};
-        const bool masked = by_row || __any_sync(0xffffffffu, row_from > c0 || row_to < c0 + 63);
+        const int rel0 = c0 + p.causal_off - key;  // of query c0 to the key
+        // (chunks that cross the key's position go with the masked ones: they are rare)
+        const bool masked = by_row || __any_sync(0xffffffffu, row_from > c0 || row_to < c0 + 63 ||
+                                                                  (SLOPES && p.two_sided && rel0 < 0 && rel0 + 64 > 1));
         if (masked) {
           if (by_row)
             rows_that_see(p, b, c0, key, vis);
@@ -651,13 +654,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float slope2 = 0.f;
         if (SLOPES) slope2 = p.slopes[hk * p.G + g] * 1.4426950408889634f;
-        const int rel0 = c0 + p.causal_off - key;  // of query c0 to the key
-        auto chunk = [&](auto ch_, auto masked_, auto both_) {
+        auto chunk = [&](auto ch_, auto masked_) {
           constexpr int ch = decltype(ch_)::value;
           uint32_t sr[32], pk[16];
           tmem_ld32(T_S + lane_base + wg * 64 + ch * 32, sr);
           tmem_wait_ld();
-          constexpr bool M = decltype(masked_)::value, B = decltype(both_)::value;
+          constexpr bool M = decltype(masked_)::value, B = M && SLOPES;
           // (with slopes the masked chunks go by the general form alone: less code and
           // fewer registers, 1322 -> 1283 us at T 8192, 32 heads of 128)
           if (!modified_chunk<CAP, SLOPES, M, B, CAP && !(SLOPES && M)>(p, sr, lse4 + ch * 8, rel0 + ch * 32, slope2, vis[ch],
@@ -673,16 +675,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         using zero = std::integral_constant<int, 0>;
         using one = std::integral_constant<int, 1>;
         if (!masked) {
-          if (SLOPES && p.two_sided && __any_sync(0xffffffffu, rel0 < 0 && rel0 + 64 > 1)) {
-            chunk(zero{}, std::false_type{}, std::bool_constant<SLOPES>{});
-            chunk(one{}, std::false_type{}, std::bool_constant<SLOPES>{});
-          } else {
-            chunk(zero{}, std::false_type{}, std::false_type{});
-            chunk(one{}, std::false_type{}, std::false_type{});
-          }
-        } else {  // (rare enough to take the two-sided form at once)
-          chunk(zero{}, std::true_type{}, std::bool_constant<SLOPES>{});
-          chunk(one{}, std::true_type{}, std::bool_constant<SLOPES>{});
+          chunk(zero{}, std::false_type{});
+          chunk(one{}, std::false_type{});
+        } else {
+          chunk(zero{}, std::true_type{});
+          chunk(one{}, std::true_type{});
         }
       } else {
         const bool need_mask = !key_valid || (CAUSAL && k0 + BN - 1 > q0 + p.causal_off) ||
