@@ -70,8 +70,8 @@
 // causal mask and window; a plan whose intervals are not in order is looked up
 // row by row instead.  Where there are few key tiles of unequal work, the
 // heaviest run in parts (fa::scored_split).  Bounded as the plain form is, with
-// a longer elementwise phase: 32 / 8 heads of 128, T 8192, causal, 990 us plain,
-// 1030 with slopes, 1185 with a cap, 1283 with both.
+// a longer elementwise phase: 32 / 8 heads of 128, T 8192, causal, 985 us plain,
+// 1012 with slopes, 1195 with a cap, 1220 with both.
 #pragma once
 #include <cstdint>
 #include <type_traits>
