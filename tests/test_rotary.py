@@ -239,3 +239,21 @@ def test_gradient_of_the_gradient():
     ddq, ddk = torch.autograd.grad((dQ, dK), (gq, gk), (uq, uk))
     for got, want in zip((ddq, ddk), fa.fa_rotary(uq, uk, pos, f, sections)):
         assert torch.equal(got, want)
+
+
+@pytest.mark.gpu
+def test_turns_in_a_row_in_place():
+    """Turned in place forth and back, with no wait in between: each call reads what the one before it wrote."""
+    B, H, T, d = 2, 4, 1200, 64
+    g = torch.Generator("cuda").manual_seed(9)
+    Q, K = (torch.randn(B, H, T, d, device="cuda", dtype=bf, generator=g) for _ in range(2))
+    pos, f = torch.arange(T, device="cuda", dtype=torch.int32), freqs(32)
+    want_q, want_k = Q.clone(), K.clone()
+    for _ in range(20):
+        fa.fa_rotary(Q, K, pos, f, Qo=Q, Ko=K)
+        fa.fa_rotary_backward(Q, K, pos, f, dQ=Q, dK=K)
+        torch.cuda.synchronize()
+    for _ in range(20):
+        fa.fa_rotary(want_q, want_k, pos, f, Qo=want_q, Ko=want_k)
+        fa.fa_rotary_backward(want_q, want_k, pos, f, dQ=want_q, dK=want_k)
+    assert torch.equal(Q, want_q) and torch.equal(K, want_k)

@@ -608,3 +608,67 @@ def test_no_cap_by_none():
     for got, want in zip(fa.fa_forward(Q, K, V, True, softcap=None, slopes=alibi(4)),
                          fa.fa_forward(Q, K, V, True, slopes=alibi(4))):
         assert torch.equal(got, want)
+
+
+@gpu
+def test_calls_in_a_row_share_plan_results_and_workspace():
+    """Kernels that start while the one before them ends must neither read nor
+    overwrite early: two batches' steps take turns in the same plan, L, workspace
+    and gradient buffers without a wait between them."""
+    B, H, Hkv, T, d = 2, 8, 2, 1000, 128
+    lib, stream = fa.load(), torch.cuda.current_stream().cuda_stream
+    dims = fa.make_dims(B, H, Hkv, T, T, d, d, True, None)
+    plan = fa.fa_mask_plan(B, T, T, True, 0, packed(B, T, 1), packed(B, T, 1))
+    scores = fa.FaScores(40.0, None, plan.buffer.data_ptr())
+    ref = ctypes.byref(dims)
+    L = torch.empty(B, H, T, device="cuda")
+    ws = torch.empty(lib.fa_backward_scored_workspace_bytes(ref, scores), dtype=torch.uint8, device="cuda")
+    batches = []
+    for seed in (1, 2):
+        Q, K, V, dO = inputs(B, H, Hkv, T, T, d, d, seed=seed)
+        batches.append((Q, K, V, dO, packed(B, T, seed + 10), torch.empty_like(Q), [torch.empty_like(t) for t in (Q, K, V)]))
+
+    def step(Q, K, V, dO, ids, O, grads):
+        assert lib.fa_mask_plan(ref, ids.data_ptr(), ids.data_ptr(), None, 0, plan.buffer.data_ptr(),
+                                plan.buffer.numel() * 4, stream) == fa.FA_OK
+        fa.fa_forward(Q, K, V, True, O=O, L=L, softcap=40.0, mask=plan)
+        fa.fa_backward(Q, K, V, O, dO, L, True, None, *grads, workspace=ws, softcap=40.0, mask=plan)
+
+    want = []
+    for b in batches:
+        step(*b)
+        torch.cuda.synchronize()
+        want.append([b[5].clone()] + [g.clone() for g in b[6]])
+        b[5].zero_()
+    for turn in range(30):
+        for b in batches:
+            step(*b)
+    torch.cuda.synchronize()
+    for b, (O, *grads) in zip(batches, want):
+        assert torch.equal(b[5], O)
+        for got, g in zip(b[6], grads):  # fp32 sums meet in any order: one bf16 step
+            assert_close("in a row", got, g.double().cpu().numpy(), rel_l2=2.0 ** -8)
+
+
+@gpu
+def test_two_streams_at_once():
+    B, H, Hkv, T, d = 1, 8, 2, 900, 64
+    sets = [inputs(B, H, Hkv, T, T, d, d, seed=s) + (packed(B, T, s),) for s in (31, 32)]
+
+    def step(Q, K, V, dO, ids):
+        mask = fa.fa_mask_plan(B, T, T, True, 0, ids, ids)
+        O, L = fa.fa_forward(Q, K, V, True, softcap=20.0, slopes=alibi(H), mask=mask)
+        return (O, L) + fa.fa_backward(Q, K, V, O, dO, L, True, softcap=20.0, slopes=alibi(H), mask=mask)
+
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in sets], [None, None]
+    for turn in range(10):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k] = step(*sets[k])
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+        for a, b in zip(g[2:], w[2:]):
+            assert_close("two streams", a, b.double().cpu().numpy(), rel_l2=2.0 ** -8)
