@@ -257,3 +257,21 @@ def test_turns_in_a_row_in_place():
         fa.fa_rotary(want_q, want_k, pos, f, Qo=want_q, Ko=want_k)
         fa.fa_rotary_backward(want_q, want_k, pos, f, dQ=want_q, dK=want_k)
     assert torch.equal(Q, want_q) and torch.equal(K, want_k)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Three rows of 2^23 tokens are 3 * 2^30 elements in and out: the last row is that of a call on it alone."""
+    B, T, d = 3, 1 << 23, 128
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    x = torch.empty(B, T, 1, d, device="cuda", dtype=bf)
+    x.view(-1, 1 << 20).copy_(torch.randn(1 << 20, device="cuda", generator=torch.Generator("cuda").manual_seed(3)))
+    x = x.transpose(1, 2)
+    none = torch.empty(B, 0, T, d, device="cuda", dtype=bf)
+    pos, f = torch.arange(B * T, device="cuda", dtype=torch.int64).view(1, B, T), freqs(64)
+    y, _ = fa.fa_rotary(x, none, pos, f)
+    one, _ = fa.fa_rotary(x[2:], none[2:], pos[:, 2:], f)
+    assert torch.equal(y[2:], one)
+    tail = slice(T - 64, T)
+    check(one[:, :, tail], x[2:, :, tail], pos[:, 2:, tail], f, (64,), False)

@@ -672,3 +672,30 @@ def test_two_streams_at_once():
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
         for a, b in zip(g[2:], w[2:]):
             assert_close("two streams", a, b.double().cpu().numpy(), rel_l2=2.0 ** -8)
+
+
+@gpu
+def test_offsets_past_32_bits():
+    """40 * 8 * 65536 * 128 elements are more than 2^31: the last batch entry's results are those of a call on it
+    alone (a window keeps the work small).  dQ is added up in fp32 in any order: one bf16 step."""
+    B, H, T, d, W = 40, 8, 65536, 128, 70
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB")
+    g = torch.Generator("cuda").manual_seed(4)
+    Q, K, V, dO = (torch.empty(B, H, T, d, device="cuda", dtype=bf) for _ in range(4))
+    for t in (Q, K, V, dO):
+        for b in range(B):
+            t[b].copy_(torch.randn(H, T, d, device="cuda", generator=g))
+    ids = (torch.arange(T, device="cuda") // 1000).int().expand(B, T).contiguous()
+    kw = dict(window=W, softcap=25.0, slopes=alibi(H))
+    mask = fa.fa_mask_plan(B, T, T, True, W, ids, ids)
+    O, L = fa.fa_forward(Q, K, V, True, mask=mask, **kw)
+    grads = fa.fa_backward(Q, K, V, O, dO, L, True, mask=mask, **kw)
+    one = [t[B - 1:].contiguous() for t in (Q, K, V, dO)]
+    mask1 = fa.fa_mask_plan(1, T, T, True, W, ids[:1], ids[:1])
+    O1, L1 = fa.fa_forward(*one[:3], True, mask=mask1, **kw)
+    grads1 = fa.fa_backward(*one[:3], O1, one[3], L1, True, mask=mask1, **kw)
+    assert torch.equal(O[B - 1:], O1) and torch.equal(L[B - 1:], L1)
+    for a, b in zip(grads, grads1):
+        off = (a[B - 1:].float() - b.float()).norm() / b.float().norm()
+        assert float(off) <= 2.0 ** -8
