@@ -506,32 +506,38 @@ __device__ __forceinline__ float line_exp(uint32_t tS, float scale, const uint32
   uint64_t rs[2] = {0ull, 0ull};
   const BiasLine line(rel0, slope2);
   const uint64_t scale2 = f2_pack(scale, scale);
+  constexpr int W = MASKED ? 32 : 64;  // columns at a time
 #pragma unroll 1
-  for (int ch = 0; ch < BN / 32; ++ch) {
+  for (int ch = 0; ch < BN / W; ++ch) {
     const uint32_t vis = MASKED ? (ch < 2 ? (ch == 0 ? vis4[0] : vis4[1]) : (ch == 2 ? vis4[2] : vis4[3])) : 0u;
-    const float relc = line.rel + (float)(32 * ch);
-    uint32_t s[32], pk[16];
-    tmem_ld32(tS + ch * 32, s);
+    const float relc = line.rel + (float)(W * ch);
+    uint32_t s[W];
+#pragma unroll
+    for (int w = 0; w < W / 32; ++w) tmem_ld32(tS + ch * W + w * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[w * 32]));
     tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      uint64_t bias;
-      if (MASKED) {
-        bias = f2_pack(fmaf(fabsf(relc + (float)c), -slope2, -base), fmaf(fabsf(relc + (float)(c + 1)), -slope2, -base));
-      } else {
-        const float g = fmaf(relc + (float)(c & ~7), line.s2, -base);
-        bias = f2_add(line.step[(c & 7) / 2], f2_pack(g, g));
+    for (int w = 0; w < W; w += 32) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int c = w; c < w + 32; c += 2) {
+        uint64_t bias;
+        if (MASKED) {
+          bias = f2_pack(fmaf(fabsf(relc + (float)c), -slope2, -base), fmaf(fabsf(relc + (float)(c + 1)), -slope2, -base));
+        } else {
+          const float g = fmaf(relc + (float)(c & ~7), line.s2, -base);
+          bias = f2_add(line.step[(c & 7) / 2], f2_pack(g, g));
+        }
+        const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, bias);
+        float v0 = ex2(f2_lo(x)), v1 = ex2(f2_hi(x));
+        if (MASKED) {
+          if (!((vis >> c) & 1u)) v0 = 0.f;
+          if (!((vis >> (c + 1)) & 1u)) v1 = 0.f;
+        }
+        rs[(c >> 1) & 1] = f2_add(rs[(c >> 1) & 1], f2_pack(v0, v1));
+        pk[(c - w) / 2] = pack_bf16x2(v0, v1);
       }
-      const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, bias);
-      float v0 = ex2(f2_lo(x)), v1 = ex2(f2_hi(x));
-      if (MASKED) {
-        if (!((vis >> c) & 1u)) v0 = 0.f;
-        if (!((vis >> (c + 1)) & 1u)) v1 = 0.f;
-      }
-      rs[(c >> 1) & 1] = f2_add(rs[(c >> 1) & 1], f2_pack(v0, v1));
-      pk[c / 2] = pack_bf16x2(v0, v1);
+      tmem_st16(tS + (W * ch + w) / 2, pk);
     }
-    tmem_st16(tS + 16 * ch, pk);
   }
   const uint64_t rs2 = f2_add(rs[0], rs[1]);
   return f2_lo(rs2) + f2_hi(rs2);
