@@ -163,7 +163,8 @@ FA_API fa_status fa_backward_noalloc(const fa_dims* dims, const void* Q, const v
  *
  * softcap is 0 (none) or between 2^-10 and 2^10; a capped score is off by at
  * most 2^-20 of the cap (fp32 arithmetic with one reciprocal for four scores),
- * which at 2^10 is half a step of a bf16 weight.  Slopes may have any sign.  With
+ * which at 2^10 is half a step of a bf16 weight.  Slopes may have any sign; biases
+ * are off by a few of fp32's roundings of their size, and L with them.  With
  * slopes, Tq and Tk are at most 2^24 (distances stay exact in fp32).  Everything
  * else is as for fa_forward / fa_backward: layouts, head sizes, empty rows,
  * workspace, errors.  Values at masked places have to be finite too (a masked

@@ -70,8 +70,8 @@
 // the softmax: the more its warps issue, the longer each group of MMAs takes to
 // issue (PV 602 cycles a group plain, 731 with a cap, 774 with both; the softmax
 // 1050, 1800 and 2100 cycles a tile).  B 2, 32 / 8 heads of 128, T 8192, causal:
-// 758 us plain, 960 with a cap of 50, 992 with slopes, 1084 with both; 4 batches of 16
-// heads of 64, T 2048: 54, 77 (98 where scores are past half of the cap), 76 and 89.
+// 758 us plain, 960 with a cap of 50 or slopes, 1084 with both; 4 batches of 16 heads of
+// 64, T 2048: 54, 78 with a cap (98 where scores are past half of it), 74 and 89.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -455,9 +455,10 @@ __device__ __forceinline__ float2 bounded_tile(uint32_t tS, const ScoredFwdParam
   return make_float2(sum, MASKED ? f2_lo(rounded) + f2_hi(rounded) : sum);
 }
 
-// Slopes without a cap: two passes over the scores in TMEM, which keep few
-// registers and little code (see bounded_tile on code; one pass over a row held in
-// registers: 76 us against 65 at T 2048, d 64).
+// Slopes without a cap: two passes over the scores in TMEM.  Held in registers from one
+// pass to the other they save nothing (T 8192, d 128: 959 us both ways; T 2048, d 64: 75.3
+// against 74.4), and the masked tiles' passes, 32 columns at a time, stay short (see
+// bounded_tile on code).
 //
 // First pass: the greatest score with its bias in one row and key tile (log2 units),
 // or a little more: of eight columns, the greatest score with the greatest bias,
@@ -499,14 +500,15 @@ __device__ __forceinline__ float line_max(uint32_t tS, float scale, const uint32
   return fmaxf(top[0], top[1]);
 }
 // Second pass: P = 2^(score + bias - base) as bf16 over the scores; returns the row's
-// sum of P.
+// sum of P.  Whole tiles take all columns at once, so that one wait for TMEM serves
+// them (32 / 64 / 128 columns: T 8192 991, 967, 960 us; T 2048, d 64 75.6, 75.9, 74.4).
 template <bool MASKED>
 __device__ __forceinline__ float line_exp(uint32_t tS, float scale, const uint32_t (&vis4)[BN / 32], int rel0,
                                           float slope2, float base) {
   uint64_t rs[2] = {0ull, 0ull};
   const BiasLine line(rel0, slope2);
   const uint64_t scale2 = f2_pack(scale, scale);
-  constexpr int W = MASKED ? 32 : 64;  // columns at a time
+  constexpr int W = MASKED ? 32 : BN;  // columns at a time
 #pragma unroll 1
   for (int ch = 0; ch < BN / W; ++ch) {
     const uint32_t vis = MASKED ? (ch < 2 ? (ch == 0 ? vis4[0] : vis4[1]) : (ch == 2 ? vis4[2] : vis4[3])) : 0u;
