@@ -70,8 +70,8 @@
 // the softmax: the more its warps issue, the longer each group of MMAs takes to
 // issue (PV 602 cycles a group plain, 731 with a cap, 774 with both; the softmax
 // 1050, 1800 and 2100 cycles a tile).  B 2, 32 / 8 heads of 128, T 8192, causal:
-// 758 us plain, 960 with a cap of 50 or slopes, 1084 with both; 4 batches of 16 heads of
-// 64, T 2048: 54, 78 with a cap (98 where scores are past half of it), 74 and 89.
+// 758 us plain, 960 with a cap of 50 or slopes, 1060 with both; 4 batches of 16 heads of
+// 64, T 2048: 54, 78 with a cap (98 where scores are past half of it), 74 and 85.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -364,7 +364,7 @@ __device__ __forceinline__ uint64_t pair_of(const uint32_t (&s)[32], int c) {
 
 // One key tile of a capped row whose cap bounds every score (kBounded).  P = 2^x,
 // with slopes 2^(x + bias - m_ref), needs no running maximum: m_ref is the
-// greatest bias of a key the row sees.  So the scores stream through 32 columns
+// greatest bias of a key the row sees.  So the scores stream through 32 or 64 columns
 // at a time, each written back as bf16 P over scores already read.  The cap is
 // taken by its polynomial; from the first score beyond it on (in any row of the
 // warp), the rest of the tile goes by the form that holds everywhere (the scores
@@ -375,6 +375,8 @@ __device__ __forceinline__ uint64_t pair_of(const uint32_t (&s)[32], int c) {
 // to bf16, so that a row of few keys is divided by the weights that its O was made
 // of (with one key O is V exactly, as where a maximum makes its P 1).  In other
 // tiles the roundings of 128 keys and more even out, and the two sums are one.
+// Steps of 64 columns suit slopes (T 8192, d 128: 1090 -> 1060 us; T 2048, d 64: 89.6 ->
+// 84.8) and not the cap alone (968 -> 1052).
 // The loop stays rolled: unrolled, its instructions crowd the MMA thread's out of
 // the instruction cache (T 8192, d 128: 925 us rolled, 1005 unrolled; two
 // warpgroups of 64 columns each per tile: 980 and 1025).
@@ -384,11 +386,18 @@ __device__ __forceinline__ float2 bounded_tile(uint32_t tS, const ScoredFwdParam
   uint64_t rs[2] = {0ull, 0ull}, rounded = 0ull;
   bool small = true;
   BiasLine line(rel0, slope2);
+  constexpr int W = SLOPES && !MASKED ? 64 : 32;  // columns at a time
 #pragma unroll 1
-  for (int ch = 0; ch < BN / 32; ++ch) {
+  for (int ch = 0; ch < BN / W; ++ch) {
     const uint32_t vis = MASKED ? (ch < 2 ? (ch == 0 ? vis4[0] : vis4[1]) : (ch == 2 ? vis4[2] : vis4[3])) : 0u;
-    const float relc = line.rel + (float)(32 * ch);
-    uint32_t s[32], pk[16];
+    const float relc = line.rel + (float)(W * ch);
+    uint32_t s[W], pk[W / 2];
+    auto load = [&]() {
+#pragma unroll
+      for (int w = 0; w < W; w += 32) tmem_ld32(tS + ch * W + w, *reinterpret_cast<uint32_t(*)[32]>(&s[w]));
+      tmem_wait_ld();
+    };
+    auto two = [&](int c) { return f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])); };
     uint64_t part[2] = {0ull, 0ull};
     auto take = [&](int c, uint64_t x01, uint64_t x23) {  // four capped scores -> P and the sums
       float v0 = ex2(f2_lo(x01)), v1 = ex2(f2_hi(x01)), v2 = ex2(f2_lo(x23)), v3 = ex2(f2_hi(x23));
@@ -414,30 +423,28 @@ __device__ __forceinline__ float2 bounded_tile(uint32_t tS, const ScoredFwdParam
       return f2_add(line.step[(c & 7) / 2], f2_pack(g, g));
     };
     if (small) {
-      tmem_ld32(tS + ch * 32, s);
-      tmem_wait_ld();
+      load();
       float top = 0.f;  // greatest s^2
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const uint64_t u01 = f2_mul(pair_of(s, c), pair_of(s, c)), u23 = f2_mul(pair_of(s, c + 2), pair_of(s, c + 2));
+      for (int c = 0; c < W; c += 4) {
+        const uint64_t u01 = f2_mul(two(c), two(c)), u23 = f2_mul(two(c + 2), two(c + 2));
         top = fmax3(fmax3(top, f2_lo(u01), f2_hi(u01)), f2_lo(u23), f2_hi(u23));
         const uint64_t t01 = cap_poly(p.cap, u01), t23 = cap_poly(p.cap, u23);
         if (SLOPES)
-          take(c, f2_fma(pair_of(s, c), t01, bias(c, 0.f)), f2_fma(pair_of(s, c + 2), t23, bias(c + 2, 0.f)));
+          take(c, f2_fma(two(c), t01, bias(c, 0.f)), f2_fma(two(c + 2), t23, bias(c + 2, 0.f)));
         else
-          take(c, f2_mul(pair_of(s, c), t01), f2_mul(pair_of(s, c + 2), t23));
+          take(c, f2_mul(two(c), t01), f2_mul(two(c + 2), t23));
       }
       small = !__any_sync(0xffffffffu, top > p.cap.small2);
     }
     if (!small) {
       const uint64_t in2 = f2_pack(p.cap.in, p.cap.in), m2cap2 = f2_pack(-2.f * p.cap.log2c, -2.f * p.cap.log2c);
       part[0] = part[1] = 0ull;
-      tmem_ld32(tS + ch * 32, s);
-      tmem_wait_ld();
+      load();
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
+      for (int c = 0; c < W; c += 4) {
         uint64_t r01, r23, e01, e23;
-        cap_quad(f2_mul(pair_of(s, c), in2), f2_mul(pair_of(s, c + 2), in2), r01, r23, e01, e23);
+        cap_quad(f2_mul(two(c), in2), f2_mul(two(c + 2), in2), r01, r23, e01, e23);
         take(c, f2_fma(r01, m2cap2, bias(c, p.cap.log2c)), f2_fma(r23, m2cap2, bias(c + 2, p.cap.log2c)));
       }
     }
@@ -445,10 +452,11 @@ __device__ __forceinline__ float2 bounded_tile(uint32_t tS, const ScoredFwdParam
     rs[1] = f2_add(rs[1], part[1]);
     if (MASKED) {
 #pragma unroll
-      for (int c = 0; c < 16; ++c)
+      for (int c = 0; c < W / 2; ++c)
         rounded = f2_add(rounded, f2_pack(__uint_as_float(pk[c] << 16), __uint_as_float(pk[c] & 0xffff0000u)));
     }
-    tmem_st16(tS + 16 * ch, pk);
+#pragma unroll
+    for (int w = 0; w < W / 2; w += 16) tmem_st16(tS + W / 2 * ch + w, *reinterpret_cast<uint32_t(*)[16]>(&pk[w]));
   }
   const uint64_t rs2 = f2_add(rs[0], rs[1]);
   const float sum = f2_lo(rs2) + f2_hi(rs2);
