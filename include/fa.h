@@ -32,7 +32,7 @@
  * Uncertainties", item 3, which attend to a bounded number of keys) further
  * requires j > i + (Tk - Tq) - W: each row sees at most its last W keys.
  * A query row that sees no key gets O = 0, L = -inf, dQ = 0 and contributes
- * nothing to dK, dV.
+ * nothing to dK, dV.  A row with a NaN among the scores it sees gets O = L = NaN.
  *
  * Supported: d and dv each in {64, 128} (dv may differ from d).  Any B, Hq, Hkv, Tq, Tk >= 0 (ragged tails
  * are handled; a zero-sized problem is a no-op; Tk == 0 yields O = 0 and

@@ -1,0 +1,112 @@
+"""NaN in Q, K and V.
+
+A NaN in a query row, or in a key that a row sees, makes that row's weights NaN, and
+so its O and its L; other rows are what they are without it, bit for bit.  A NaN in V reaches the channel it is in, of
+every row that sees its key.  (Masked places have to hold finite values.)"""
+import ctypes
+
+import pytest
+import torch
+
+import tiled_attention_05_gb300 as fa
+from tests.test_scored_attention import alibi, inputs
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+# name, cap, slopes, mask: every form of the scores (a cap of 200 is past the bounded form)
+FORMS = [("plain", 0.0, False, False), ("mask", 0.0, False, True), ("cap", 20.0, False, False), ("slopes", 0.0, True, False),
+         ("both", 50.0, True, False), ("wide cap", 200.0, True, False), ("capped documents", 30.0, False, True)]
+# B, Hq, Hkv, Tq, Tk, d, dv: packed and split, split, one item per head (split by nothing)
+SHAPES = [(1, 8, 2, 32, 4000, 128, 128), (1, 8, 8, 2048, 2048, 64, 64), (2, 4, 2, 300, 300, 128, 64)]
+
+
+def forward(Q, K, V, cap, slopes, mask, workspace):
+    """O, L of the causal call, with or without the workspace that lets it split."""
+    if workspace:
+        return fa.fa_forward(Q, K, V, True, softcap=cap, slopes=slopes, mask=mask)
+    B, Hq, Tq, d = Q.shape
+    dims = fa.make_dims(B, Hq, K.shape[1], Tq, K.shape[2], d, V.shape[3], True, None)
+    scores = fa.FaScores(cap, slopes.data_ptr() if slopes is not None else None,
+                         mask.buffer.data_ptr() if mask is not None else None)
+    O, L = Q.new_empty(B, Hq, Tq, V.shape[3]), torch.empty(B, Hq, Tq, device=Q.device)
+    code = fa.load().fa_forward_scored(ctypes.byref(dims), ctypes.byref(scores), Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+                                       O.data_ptr(), L.data_ptr(), None, 0, torch.cuda.current_stream().cuda_stream)
+    assert code == fa.FA_OK
+    return O, L
+
+
+def problem(shape, form):
+    B, Hq, Hkv, Tq, Tk, d, dv = shape
+    _, cap, slopes, masked = form
+    Q, K, V, dO = inputs(B, Hq, Hkv, Tq, Tk, d, dv, seed=Tk + d)
+    slopes = alibi(Hq) / 64 if slopes else None  # (gentle: no weight of a row of this length underflows)
+    mask = None
+    if masked:  # one document: rows see what the causal mask shows
+        ids = torch.zeros(B, max(Tq, Tk), dtype=torch.int32, device="cuda")
+        mask = fa.fa_mask_plan(B, Tq, Tk, True, 0, ids[:, :Tq].contiguous(), ids[:, :Tk].contiguous())
+    return Q, K, V, dO, cap, slopes, mask
+
+
+@pytest.mark.parametrize("workspace", [False])
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: f[0])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_a_nan_reaches_the_rows_that_see_it(shape, form, workspace):
+    B, Hq, Hkv, Tq, Tk, d, dv = shape
+    Q, K, V, dO, cap, slopes, mask = problem(shape, form)
+    O0, L0 = forward(Q, K, V, cap, slopes, mask, workspace)
+    assert bool(torch.isfinite(O0).all()) and bool(torch.isfinite(L0).all())
+    b, hk, j = B - 1, Hkv - 1, Tk // 3
+    heads = slice(hk * (Hq // Hkv), Hq)
+    first = max(0, j - (Tk - Tq))  # first row that sees key j
+    behind = 128 * (first // 128)  # rows before it in its tile have the NaN at a masked place
+
+    def others(t):
+        t = t.clone()
+        t[b, heads, behind:] = 0
+        return t
+
+    bad = K.clone()
+    bad[b, hk, j, 5] = NAN
+    O, L = forward(Q, bad, V, cap, slopes, mask, workspace)
+    assert bool(O[b, heads, first:].isnan().all()) and bool(L[b, heads, first:].isnan().all())
+    assert torch.equal(others(O), others(O0)) and torch.equal(others(L), others(L0))
+
+    bad = V.clone()
+    bad[b, hk, j, 7] = NAN
+    O, L = forward(Q, K, bad, cap, slopes, mask, workspace)
+    assert bool(O[b, heads, first:, 7].isnan().all())
+    keep = torch.arange(dv, device="cuda") != 7
+    assert torch.equal(O[b, heads, first:][..., keep], O0[b, heads, first:][..., keep]) and torch.equal(L, L0)
+
+    bad = Q.clone()
+    h, i = heads.start, Tq - 3
+    bad[b, h, i, 1] = NAN
+    O, L = forward(bad, K, V, cap, slopes, mask, workspace)
+    assert bool(O[b, h, i].isnan().all()) and bool(L[b, h, i].isnan())
+    O[b, h, i], L[b, h, i] = O0[b, h, i], L0[b, h, i]
+    assert torch.equal(O, O0) and torch.equal(L, L0)
+
+
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: f[0])
+def test_a_nan_reaches_the_gradients(form):
+    """A row of NaN weights gives NaN to its dQ and to dK and dV of every key it sees."""
+    shape = B, Hq, Hkv, Tq, Tk, d, dv = SHAPES[2]
+    Q, K, V, dO, cap, slopes, mask = problem(shape, form)
+    i = 140
+    Q[0, 1, i, 3] = NAN
+    mods = dict(softcap=cap, slopes=slopes, mask=mask)
+    O, L = fa.fa_forward(Q, K, V, True, **mods)
+    dQ, dK, dV = fa.fa_backward(Q, K, V, O, dO, L, True, **mods)
+    assert bool(dQ[0, 1, i].isnan().all())
+    assert bool(dK[0, 0, :i + 1].isnan().all()) and bool(dV[0, 0, :i + 1].isnan().all())
+    for t in (dQ[1], dK[1], dV[1], dK[0, 1], dV[0, 1], dQ[0, 0]):
+        assert bool(torch.isfinite(t).all())
+    # a key: every row from it on has NaN weights, and every key is seen by one of them
+    Q, K, V, dO, cap, slopes, mask = problem(shape, form)
+    K[0, 1, 100, 0] = NAN
+    O, L = fa.fa_forward(Q, K, V, True, **mods)
+    dQ, dK, dV = fa.fa_backward(Q, K, V, O, dO, L, True, **mods)
+    assert bool(dQ[0, 2:, 100:].isnan().all()) and bool(dV[0, 1].isnan().all()) and bool(dK[0, 1].isnan().all())
+    for t in (dQ[1], dK[1], dV[1], dK[0, 0], dV[0, 0], dQ[0, :2]):
+        assert bool(torch.isfinite(t).all())

@@ -1117,8 +1117,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
       }
-      if (row_ok) p.L[(size_t)it.bh * p.Tq + i] = l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : NEG_INF;
-      const float inv_l = l > 0.f ? 1.f / l_o : 0.f;
+      // (l is 0 where the row saw no key, and NaN where one of its scores is: so are L and O then)
+      if (row_ok) p.L[(size_t)it.bh * p.Tq + i] = l == 0.f ? NEG_INF : (m_ref + __log2f(l)) * 0.69314718055994531f;
+      const float inv_l = l == 0.f ? 0.f : 1.f / l_o;
       uint4* orow = reinterpret_cast<uint4*>(p.O + ((size_t)it.bh * p.Tq + (row_ok ? i : 0)) * HDV);
 #pragma unroll
       for (int c = 0; c < HDV / 32; ++c) {
