@@ -1,15 +1,20 @@
-"""NaN in Q, K and V.
+"""NaN and infinity in Q, K and V.
 
 A NaN in a query row, or in a key that a row sees, makes that row's weights NaN, and
-so its O and its L; other rows are what they are without it, bit for bit.  A NaN in V reaches the channel it is in, of
-every row that sees its key.  (Masked places have to hold finite values.)"""
+so its O and its L, whether the call is split over its keys or not; other rows are
+what they are without it, bit for bit.  A NaN in V reaches the channel it is in, of
+every row that sees its key.  (Masked places have to hold finite values.)
+
+Under a cap a score of any size counts as the cap; the tolerances are those of
+test_scored_attention: O off by r |O| + sum_j (r + e) P_ij |V_j| with r = 2^-8 and
+e = 2^-12 + 2^-20 c, L by 1e-4 + 2^-20 c."""
 import ctypes
 
 import pytest
 import torch
 
 import tiled_attention_05_gb300 as fa
-from tests.test_scored_attention import alibi, inputs
+from tests.test_scored_attention import alibi, definition, inputs, visible
 
 pytestmark = pytest.mark.gpu
 
@@ -48,7 +53,7 @@ def problem(shape, form):
     return Q, K, V, dO, cap, slopes, mask
 
 
-@pytest.mark.parametrize("workspace", [False])
+@pytest.mark.parametrize("workspace", [True, False])
 @pytest.mark.parametrize("form", FORMS, ids=lambda f: f[0])
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
 def test_a_nan_reaches_the_rows_that_see_it(shape, form, workspace):
@@ -110,3 +115,20 @@ def test_a_nan_reaches_the_gradients(form):
     assert bool(dQ[0, 2:, 100:].isnan().all()) and bool(dV[0, 1].isnan().all()) and bool(dK[0, 1].isnan().all())
     for t in (dQ[1], dK[1], dV[1], dK[0, 0], dV[0, 0], dQ[0, :2]):
         assert bool(torch.isfinite(t).all())
+
+
+@pytest.mark.parametrize("cap, slopes", [(20.0, False), (50.0, True), (200.0, True)])
+@pytest.mark.parametrize("Tq, Tk", [(32, 4000), (300, 300)])
+def test_infinite_scores_count_as_the_cap(Tq, Tk, cap, slopes):
+    B, Hq, Hkv, d = 1, 4, 2, 64
+    Q, K, V, _ = inputs(B, Hq, Hkv, Tq, Tk, d, d, seed=Tk)
+    Q[0, 0, 20], Q[0, 1, 21] = 2.0 ** 100, -2.0 ** 100
+    K[0, 0, 9] = 2.0 ** 100  # q.k = +-2^206, past fp32
+    slopes = alibi(Hq) if slopes else None
+    O, L = fa.fa_forward(Q, K, V, True, softcap=cap, slopes=slopes)
+    vis = visible(B, Tq, Tk, True, device="cuda")
+    Or, Lr, P, _ = definition(Q.double(), K.double(), V.double(), vis, cap, slopes, more=True)
+    r, e = 2.0 ** -8, 2.0 ** -12 + 2.0 ** -20 * cap
+    bound = r * Or.abs() + (r + e) * torch.matmul(P, V.double().abs().repeat_interleave(Hq // Hkv, 1))
+    assert bool(((O.double() - Or).abs() <= bound).all())
+    assert float((L - Lr).abs().max()) <= 1e-4 + 2.0 ** -20 * cap

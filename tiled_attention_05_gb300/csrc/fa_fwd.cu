@@ -16,8 +16,10 @@ cudaError_t launch_fwd_dims(const fa::Problem& pr, const fa::FwdShape& shape, co
 
 // Joins the parts of a split forward: with reference m_s and sum l_s of part s and
 // M = max m_s, O = sum 2^(m_s - M) O_s over the same sum of what each O is divided by,
-// and L = ln2 (M + log2 sum 2^(m_s - M) l_s).  A part that saw no key has l = 0 and no O.  One warp a row, HDV / 32
-// columns a lane.  Bound by HBM / L2 (the parts, fp32) and by its launch.
+// and L = ln2 (M + log2 sum 2^(m_s - M) l_s).  A part without a key tile has l = -1 and
+// no O.  One whose weights are all 0 counts with factor 0 (its O is 0, or NaN from a NaN
+// in V), and a NaN sum makes O and L NaN, both as in an unsplit row.  One warp a row,
+// HDV / 32 columns a lane.  Bound by HBM / L2 (the parts, fp32) and by its launch.
 template <int HDV>
 __global__ void __launch_bounds__(256) fa_fwd_join(const float* __restrict__ part, uint16_t* __restrict__ O,
                                                    float* __restrict__ L, long long rows, int rows_per_head,
@@ -37,7 +39,7 @@ __global__ void __launch_bounds__(256) fa_fwd_join(const float* __restrict__ par
   float top = -__int_as_float(0x7f800000);
   for (int s = lane; s < split; s += 32) {
     const float4 v = ml[(first + s) * 2 * BM + at];
-    if (v.y > 0.f) top = fmaxf(top, v.x);
+    if (v.y > 0.f || v.y != v.y) top = fmaxf(top, v.x);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -47,19 +49,19 @@ __global__ void __launch_bounds__(256) fa_fwd_join(const float* __restrict__ par
 #pragma unroll 4
   for (int s = 0; s < split; ++s) {
     const float4 v = ml[(first + s) * 2 * BM + at];
-    if (!(v.y > 0.f)) continue;
-    const float w = exp2f(v.x - top);
+    if (v.y < 0.f) continue;
+    const float w = v.y == 0.f ? 0.f : exp2f(v.x - top);
     const float* o = part + ((first + s) * 2 * BM + at) * HDV + lane * W;
     sum += w * v.y;
     sum_o += w * v.z;
 #pragma unroll
     for (int e = 0; e < W; ++e) acc[e] += w * o[e];
   }
-  const float inv = sum > 0.f ? 1.f / sum_o : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum_o;
   uint32_t* out = reinterpret_cast<uint32_t*>(O + row * HDV + lane * W);
 #pragma unroll
   for (int e = 0; e < W; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0) L[row] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -__int_as_float(0x7f800000);
+  if (lane == 0) L[row] = sum == 0.f ? -__int_as_float(0x7f800000) : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 __global__ void fa_fwd_empty_keys(uint32_t* O_words, size_t n_words, float* L, size_t n_rows) {

@@ -1098,7 +1098,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.split > 1) {  // the unnormalised row, its reference and sum, for fa_fwd_join
           const size_t row = ((size_t)fwd_index(n) * 2 + x) * BM + r;
           if (row_ok)
-            reinterpret_cast<float4*>(p.part + (size_t)p.n_items * 2 * BM * HDV)[row] = make_float4(m_ref, l, l_o, 0.f);
+            reinterpret_cast<float4*>(p.part + (size_t)p.n_items * 2 * BM * HDV)[row] =
+                make_float4(m_ref, nkv > 0 ? l : -1.f, l_o, 0.f);
           float4* out = reinterpret_cast<float4*>(p.part + row * HDV);
           if (nkv > 0) {
 #pragma unroll

@@ -175,7 +175,7 @@ inline FwdShape fwd_shape(const Problem& p, const ScoreMods& m, int sms) {
   return s;
 }
 // fp32 workspace of a split forward: per item, part and row the O row, its reference
-// m, its sum l and the sum that O is divided by.
+// m, its sum l (-1: no key tile, no O) and the sum that O is divided by.
 inline size_t fwd_workspace_bytes(const Problem& p, const FwdShape& s) {
   return s.split > 1 ? (size_t)s.items * s.split * 2 * kTile * (p.dv + 4) * sizeof(float) : 0;
 }
