@@ -196,6 +196,12 @@ def _on(device):
     return _HERE if device.index == _current_device() else torch.cuda.device(device)
 
 
+def _under(stream, device):
+    """Makes ``device`` and the stream of a call current (nothing to do for the
+    current one): what the call copies is then ordered with its kernels."""
+    return _on(device) if stream is None else torch.cuda.stream(stream)
+
+
 def _raise(code: int, where: str):
     if code != FA_OK:
         raise FAError(code, where)

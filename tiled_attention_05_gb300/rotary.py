@@ -80,9 +80,9 @@ def _call(Q, K, positions, inv_freq, sections, interleaved, inverse, Qo, Ko, str
     k_strides = _heads(K, "K", B, T, d, device)
     if inv_freq.dtype != torch.float32 or inv_freq.get_device() != device.index or not inv_freq.is_contiguous():
         raise ValueError(f"inv_freq must be a contiguous CUDA {torch.float32} tensor on {device}")
-    pos, pos_axis, pos_batch = _rows_positions(positions, axes, B, T, device)
-    if pos is not positions and stream is not None:
-        pos.record_stream(stream)
+    handle = _fa._stream_ptr(stream, device)
+    with _fa._under(stream, device):  # (a copy is made on the stream that reads it)
+        pos, pos_axis, pos_batch = _rows_positions(positions, axes, B, T, device)
     Hk = K.shape[1]
     if Qo is None:
         Qo = torch.empty((B, Hq, T, d), dtype=torch.bfloat16, device=device)
@@ -97,7 +97,7 @@ def _call(Q, K, positions, inv_freq, sections, interleaved, inverse, Qo, Ko, str
     lib = _fa.load()
     with _fa._on(device):
         code = lib.fa_rotary(ctypes.byref(dims), Q.data_ptr(), K.data_ptr(), pos.data_ptr(), inv_freq.data_ptr(),
-                             Qo.data_ptr(), Ko.data_ptr(), inverse, _fa._stream_ptr(stream, device))
+                             Qo.data_ptr(), Ko.data_ptr(), inverse, handle)
     _fa._raise(code, where)
     return Qo, Ko
 
