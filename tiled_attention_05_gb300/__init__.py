@@ -19,6 +19,10 @@ and L for the backward pass) and ``attention`` (its functional form), and
 
 Tensors are CUDA bf16, contiguous, [B, H, T, d]; L is fp32 [B, Hq, Tq].  The
 rotary calls also take strided Q and K (views of a packed projection).
+
+Calls run on the current stream, or on ``stream=``.  Inputs have to be ready there,
+and the caller orders its use of the results; what the call allocates belongs to
+that stream.
 """
 from __future__ import annotations
 
@@ -198,8 +202,18 @@ def _on(device):
 
 def _under(stream, device):
     """Makes ``device`` and the stream of a call current (nothing to do for the
-    current one): what the call copies is then ordered with its kernels."""
+    current one): what the call allocates and copies is then ordered with its
+    kernels.  (A block from another stream's pool may still be in use there.)"""
     return _on(device) if stream is None else torch.cuda.stream(stream)
+
+
+def _hand_over(device, results, given=()):
+    """Results that a call made (were not given to it) under an explicit stream go to
+    the caller, whose current stream may still use them when they are freed."""
+    here = torch.cuda.current_stream(device)
+    for n, t in enumerate(results):
+        if n >= len(given) or given[n] is None:
+            t.record_stream(here)
 
 
 def _raise(code: int, where: str):
@@ -247,13 +261,13 @@ def fa_mask_plan(B, Tq, Tk, causal: bool, window: int = 0, doc_q=None, doc_k=Non
     _check_all(device, specs)
     lib = load()
     nbytes = int(lib.fa_mask_plan_bytes(ctypes.byref(dims)))
-    buffer = torch.empty(max(nbytes // 4, 4), dtype=torch.int32, device=device)
-    if stream is not None:
-        buffer.record_stream(stream)
-    with _on(device):
+    handle = _stream_ptr(stream, device)
+    with _under(stream, device):
+        buffer = torch.empty(max(nbytes // 4, 4), dtype=torch.int32, device=device)
         code = lib.fa_mask_plan(ctypes.byref(dims), _ptr(doc_q), _ptr(doc_k), _ptr(prefix),
-                                int(prefix is not None and prefix.dim() == 2), buffer.data_ptr(), nbytes,
-                                _stream_ptr(stream, device))
+                                int(prefix is not None and prefix.dim() == 2), buffer.data_ptr(), nbytes, handle)
+    if stream is not None:
+        _hand_over(device, (buffer,))
     _raise(code, "fa_mask_plan")
     return MaskPlan(_plan_key(dims), buffer)
 
@@ -305,21 +319,21 @@ def fa_forward(Q, K, V, causal: bool, scale: float | None = None, O=None, L=None
         specs.append((L, "L", (dims.B, dims.Hq, dims.Tq), f32))
     _check_all(Q.device, specs)
     device = Q.device
-    if O is None:
-        O = torch.empty_like(Q) if dims.dv == dims.d else torch.empty(dims.B, dims.Hq, dims.Tq, dims.dv, dtype=bf,
-                                                                      device=device)
-    if L is None:
-        L = torch.empty((dims.B, dims.Hq, dims.Tq), dtype=f32, device=device)
-    lib = load()
+    lib, ref = load(), ctypes.byref(dims)
     scores = _scores(dims, device, softcap, slopes, mask, stream)
-    ref = ctypes.byref(dims)
-    with _on(device):
+    handle, given = _stream_ptr(stream, device), (O, L)
+    with _under(stream, device):
+        if O is None:
+            O = torch.empty_like(Q) if dims.dv == dims.d else torch.empty(dims.B, dims.Hq, dims.Tq, dims.dv, dtype=bf,
+                                                                          device=device)
+        if L is None:
+            L = torch.empty((dims.B, dims.Hq, dims.Tq), dtype=f32, device=device)
         nbytes = lib.fa_forward_scored_workspace_bytes(ref, scores) if scores is not None else 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-        if stream is not None and workspace is not None:  # freed on return, while the other stream still uses it
-            workspace.record_stream(stream)
         code = lib.fa_forward_scored(ref, scores, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
-                                     L.data_ptr(), _ptr(workspace), nbytes, _stream_ptr(stream, device))
+                                     L.data_ptr(), _ptr(workspace), nbytes, handle)
+    if stream is not None:
+        _hand_over(device, (O, L), given)
     _raise(code, "fa_forward")
     return O, L
 
@@ -333,29 +347,26 @@ def fa_backward(Q, K, V, O, dO, L, causal: bool, scale: float | None = None, dQ=
     ``stages`` selects which of the three backward kernels to launch (see
     fa_backward_stages in include/fa.h); the default runs all of them.
     """
-    dims, dQ, dK, dV = _backward_operands(Q, K, V, O, dO, L, causal, scale, window, dQ, dK, dV)
+    dims, handle, dQ, dK, dV = _backward_operands(Q, K, V, O, dO, L, causal, scale, window, dQ, dK, dV, stream)
     lib, device, ref = load(), Q.device, ctypes.byref(dims)
     scores = _scores(dims, device, softcap, slopes, mask, stream)
-    with _on(device):
+    with _under(stream, device):
         if workspace is None:
             need = lib.fa_backward_scored_workspace_bytes(ref, scores)
             workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-            if stream is not None:  # freed on return, while the other stream still uses it
-                workspace.record_stream(stream)
         elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
         nbytes = workspace.numel() * workspace.element_size()
         code = lib.fa_backward_scored(ref, scores, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
                                       O.data_ptr(), dO.data_ptr(), L.data_ptr(), dQ.data_ptr(), dK.data_ptr(),
-                                      dV.data_ptr(), workspace.data_ptr(), nbytes, int(stages),
-                                      _stream_ptr(stream, device))
+                                      dV.data_ptr(), workspace.data_ptr(), nbytes, int(stages), handle)
     _raise(code, "fa_backward")
     return dQ, dK, dV
 
 
-def _backward_operands(Q, K, V, O, dO, L, causal, scale, window, dQ, dK, dV):
-    """Dims of a backward call, its gradient buffers (allocated when not given)
-    and the shape / dtype / device checks of all eleven tensors."""
+def _backward_operands(Q, K, V, O, dO, L, causal, scale, window, dQ, dK, dV, stream):
+    """Dims and stream of a backward call, its gradient buffers (allocated when not
+    given) and the shape / dtype / device checks of all eleven tensors."""
     dims = _dims_of(Q, K, V, causal, scale, window)
     bf, f32 = torch.bfloat16, torch.float32
     qv, rows = (dims.B, dims.Hq, dims.Tq, dims.dv), (dims.B, dims.Hq, dims.Tq)
@@ -364,10 +375,14 @@ def _backward_operands(Q, K, V, O, dO, L, causal, scale, window, dQ, dK, dV):
     specs += [(t, n, like.shape, bf) for t, n, like in ((dQ, "dQ", Q), (dK, "dK", K), (dV, "dV", V))
               if t is not None]
     _check_all(Q.device, specs)
-    dQ = torch.empty_like(Q) if dQ is None else dQ
-    dK = torch.empty_like(K) if dK is None else dK
-    dV = torch.empty_like(V) if dV is None else dV
-    return dims, dQ, dK, dV
+    handle, given = _stream_ptr(stream, Q.device), (dQ, dK, dV)
+    with _under(stream, Q.device):
+        dQ = torch.empty_like(Q) if dQ is None else dQ
+        dK = torch.empty_like(K) if dK is None else dK
+        dV = torch.empty_like(V) if dV is None else dV
+    if stream is not None:
+        _hand_over(Q.device, (dQ, dK, dV), given)
+    return dims, handle, dQ, dK, dV
 
 
 def fa_backward_noalloc(Q, K, V, O, dO, L, causal: bool, scale: float | None = None, dQ=None, dK=None, dV=None,
@@ -376,12 +391,12 @@ def fa_backward_noalloc(Q, K, V, O, dO, L, causal: bool, scale: float | None = N
     memory: the library's fixed scratch array (FA_NOALLOC_SCRATCH_BYTES per
     GPU) is used instead.  Pass preallocated dQ / dK / dV to allocate nothing
     at all; calls that could overlap on the GPU must be ordered by the caller."""
-    dims, dQ, dK, dV = _backward_operands(Q, K, V, O, dO, L, causal, scale, window, dQ, dK, dV)
+    dims, handle, dQ, dK, dV = _backward_operands(Q, K, V, O, dO, L, causal, scale, window, dQ, dK, dV, stream)
     lib = load()
     with torch.cuda.device(Q.device):
         code = lib.fa_backward_noalloc(ctypes.byref(dims), Q.data_ptr(), K.data_ptr(), V.data_ptr(),
                                        O.data_ptr(), dO.data_ptr(), L.data_ptr(), dQ.data_ptr(), dK.data_ptr(),
-                                       dV.data_ptr(), _stream_ptr(stream, Q.device))
+                                       dV.data_ptr(), handle)
     _raise(code, "fa_backward_noalloc")
     return dQ, dK, dV
 

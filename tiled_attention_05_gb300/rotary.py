@@ -80,24 +80,25 @@ def _call(Q, K, positions, inv_freq, sections, interleaved, inverse, Qo, Ko, str
     k_strides = _heads(K, "K", B, T, d, device)
     if inv_freq.dtype != torch.float32 or inv_freq.get_device() != device.index or not inv_freq.is_contiguous():
         raise ValueError(f"inv_freq must be a contiguous CUDA {torch.float32} tensor on {device}")
-    handle = _fa._stream_ptr(stream, device)
-    with _fa._under(stream, device):  # (a copy is made on the stream that reads it)
-        pos, pos_axis, pos_batch = _rows_positions(positions, axes, B, T, device)
-    Hk = K.shape[1]
-    if Qo is None:
-        Qo = torch.empty((B, Hq, T, d), dtype=torch.bfloat16, device=device)
-    else:
-        _fa._check_all(device, [(Qo, "Qo", Q.shape, torch.bfloat16)])
-    if Ko is None:
-        Ko = torch.empty((B, Hk, T, d), dtype=torch.bfloat16, device=device)
-    else:
-        _fa._check_all(device, [(Ko, "Ko", K.shape, torch.bfloat16)])
-    dims = _fa.FaRotaryDims(B, Hq, Hk, T, d, 2 * half, axes, 1 if interleaved else 0, pos.element_size(), sections,
-                            q_strides, k_strides, (Hq * T * d, T * d, d), (Hk * T * d, T * d, d), pos_axis, pos_batch)
+    Hk, bf = K.shape[1], torch.bfloat16
+    if Qo is not None:
+        _fa._check_all(device, [(Qo, "Qo", Q.shape, bf)])
+    if Ko is not None:
+        _fa._check_all(device, [(Ko, "Ko", K.shape, bf)])
+    handle, given = _fa._stream_ptr(stream, device), (Qo, Ko)
     lib = _fa.load()
-    with _fa._on(device):
+    with _fa._under(stream, device):  # (copied positions belong to the stream that reads them)
+        pos, pos_axis, pos_batch = _rows_positions(positions, axes, B, T, device)
+        if Qo is None:
+            Qo = torch.empty((B, Hq, T, d), dtype=bf, device=device)
+        if Ko is None:
+            Ko = torch.empty((B, Hk, T, d), dtype=bf, device=device)
+        dims = _fa.FaRotaryDims(B, Hq, Hk, T, d, 2 * half, axes, 1 if interleaved else 0, pos.element_size(), sections,
+                                q_strides, k_strides, (Hq * T * d, T * d, d), (Hk * T * d, T * d, d), pos_axis, pos_batch)
         code = lib.fa_rotary(ctypes.byref(dims), Q.data_ptr(), K.data_ptr(), pos.data_ptr(), inv_freq.data_ptr(),
                              Qo.data_ptr(), Ko.data_ptr(), inverse, handle)
+    if stream is not None:
+        _fa._hand_over(device, (Qo, Ko), given)
     _fa._raise(code, where)
     return Qo, Ko
 
