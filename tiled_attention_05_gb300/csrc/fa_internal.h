@@ -25,7 +25,7 @@ struct Problem {
   int causal;
   int window;   // causal sliding window in keys, 0 = none
   float scale;  // resolved (> 0)
-  int G() const { return Hq / Hkv; }
+  int G() const { return Hkv ? Hq / Hkv : 0; }  // (no heads at all are allowed)
   int q_tiles() const { return (Tq + kTile - 1) / kTile; }
   int kv_tiles() const { return (Tk + kTile - 1) / kTile; }
   long long Tq_pad() const { return (long long)q_tiles() * kTile; }
