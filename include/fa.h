@@ -169,8 +169,8 @@ FA_API fa_status fa_backward_noalloc(const fa_dims* dims, const void* Q, const v
  * else is as for fa_forward / fa_backward: layouts, head sizes, empty rows,
  * workspace, errors.  Values at masked places have to be finite too (a masked
  * pair has weight 0, and 0 * NaN is NaN), and with a cap those of V are taken to be
- * below 2^20 in magnitude (the weights of a capped row are summed before they are
- * normalised, up to 2^90).  fa_backward_noalloc has no form with modified scores. */
+ * below 2^20 in magnitude (the weights of a capped row, up to 2^90, are summed before
+ * they are normalised).  fa_backward_noalloc has no form with modified scores. */
 typedef struct {
   float softcap;
   const float* slopes; /* device, [Hq], or NULL */

@@ -1,4 +1,4 @@
-"""NaN and infinity in Q, K and V.
+"""NaN and infinity in Q, K and V, and the largest values that a capped call takes.
 
 A NaN in a query row, or in a key that a row sees, makes that row's weights NaN, and
 so its O and its L, whether the call is split over its keys or not; other rows are
@@ -9,6 +9,7 @@ Under a cap a score of any size counts as the cap; the tolerances are those of
 test_scored_attention: O off by r |O| + sum_j (r + e) P_ij |V_j| with r = 2^-8 and
 e = 2^-12 + 2^-20 c, L by 1e-4 + 2^-20 c."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -132,3 +133,25 @@ def test_infinite_scores_count_as_the_cap(Tq, Tk, cap, slopes):
     bound = r * Or.abs() + (r + e) * torch.matmul(P, V.double().abs().repeat_interleave(Hq // Hkv, 1))
     assert bool(((O.double() - Or).abs() <= bound).all())
     assert float((L - Lr).abs().max()) <= 1e-4 + 2.0 ** -20 * cap
+
+
+@pytest.mark.parametrize("cap", [62.0, 60.0, 55.0])
+@pytest.mark.parametrize("Tq", [1, 100])
+def test_large_values_of_many_capped_keys(cap, Tq):
+    """Values just below 2^20 under weights of 2^90, over 2^19 keys: the unnormalised sums stay inside fp32.
+    Scores are saturated at both ends, so O is the mean of the values of the keys at the upper one.  Each of the
+    sums of O and L (at most 2^12 terms one after the other, of one sign, each addition off by 2^-23 of the sum so far
+    at most) is off by 2^-11 of itself; O is rounded once, 2^-8, and P before it, 2^-8."""
+    Tk, d = 1 << 19, 64
+    g = torch.Generator("cuda").manual_seed(6)
+    sign = torch.where(torch.rand(Tk, generator=g, device="cuda") < 0.9, 8.0, -8.0)
+    Q = torch.full((1, 1, Tq, d), 8.0, device="cuda").bfloat16()
+    K = sign[:, None].expand(Tk, d).bfloat16()[None, None].contiguous()
+    V = (2.0 ** 20 * (1 - 2.0 ** -8) * (1 - 0.1 * torch.rand(Tk, d, generator=g, device="cuda"))).bfloat16()[None, None]
+    assert float(V.max()) < 2.0 ** 20
+    O, L = fa.fa_forward(Q, K, V, False, softcap=cap)
+    up = sign > 0
+    want = V[0, 0][up].double().mean(0)
+    off = (O[0, 0].double() - want).abs() / want
+    assert float(off.max()) <= 2 * 2.0 ** -8 + 2 * 2.0 ** -11, float(off.max())
+    assert float((L - (cap + math.log(int(up.sum())))).abs().max()) <= 1e-4 + 2.0 ** -20 * cap + 2.0 ** -11

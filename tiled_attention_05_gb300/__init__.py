@@ -309,7 +309,8 @@ def fa_forward(Q, K, V, causal: bool, scale: float | None = None, O=None, L=None
     ``softcap=c`` replaces each scaled score x by c tanh(x / c); ``slopes`` (fp32
     [Hq]) then subtracts slopes[h] |i + Tk - Tq - j|; ``mask`` (a MaskPlan of the
     same sizes, causal and window) hides other documents' keys and shows a
-    prefix.  The backward takes the same three."""
+    prefix.  The backward takes the same three.  With a cap, values of V are to
+    be below 2^20 in magnitude."""
     dims = _dims_of(Q, K, V, causal, scale, window)
     bf, f32 = torch.bfloat16, torch.float32
     specs = [(Q, "Q", Q.shape, bf), (K, "K", K.shape, bf), (V, "V", V.shape, bf)]
@@ -435,7 +436,7 @@ class FlashAttention(torch.autograd.Function):
 def attention(Q, K, V, causal=False, scale=None, window=0, softcap=0.0, slopes=None, mask=None, docs=None,
               prefix=None):
     """Differentiable attention; ``softcap``, ``slopes`` and ``mask`` as in
-    fa_forward.  ``docs`` (int32 ids [B, T] of rows and keys, or a pair for
+    fa_forward (with its limit on V under a cap).  ``docs`` (int32 ids [B, T] of rows and keys, or a pair for
     each) and ``prefix`` plan the mask here, for this call and its backward;
     a program with several layers plans once (fa_mask_plan) and passes ``mask``."""
     if docs is not None or prefix is not None:

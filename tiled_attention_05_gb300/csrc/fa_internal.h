@@ -81,10 +81,17 @@ int sm_count();
 // bookkeeping cost the large calls 4%: T 8192, cap 50, 938 -> 978 us.)
 enum ScoreBits : int { kPlain = -1, kCap = 1, kSlopes = 2, kBounded = 4, kFew = 8 };
 
-// Largest cap (log2 units) of the bounded form: 2^-90 <= P <= 2^90, so that P, its
-// sums over 2^30 keys and its products with values down to 2^-36 are normal
-// numbers of bf16 and fp32.  In natural units a cap of 62.
-constexpr float kBoundedCapLog2 = 90.f;
+// Largest cap (log2 units) of the bounded form over Tk keys.  P is between 2^-90 and
+// 2^90, a normal number of bf16 and fp32 (as are its products with values down to
+// 2^-36), and a row's unnormalised O, at most 2^cap times the values' size times Tk,
+// stays below 2^127 with values below 2^20: 2^90 up to 2^17 keys (in natural units a cap
+// of 62), half as much for each further doubling.
+constexpr int kBoundedCapLog2 = 90, kBoundedKeysLog2 = 127 - 20 - kBoundedCapLog2;
+inline float bounded_cap_log2(int Tk) {
+  int more = 0;
+  while (((long long)Tk - 1) >> (kBoundedKeysLog2 + more) > 0) ++more;
+  return (float)(kBoundedCapLog2 - more);
+}
 
 struct ScoreMods {
   float softcap = 0.f;            // c > 0: x = c tanh(x / c)
@@ -92,8 +99,8 @@ struct ScoreMods {
   const void* plan = nullptr;     // mask plan (documents, prefixes) for the same dims
   bool any() const { return softcap > 0.f || slopes || plan; }
   int bits() const { return (softcap > 0.f ? kCap : 0) | (slopes ? kSlopes : 0); }
-  int fwd_bits() const {
-    return softcap > 0.f && softcap * 1.4426950408889634f <= kBoundedCapLog2 ? bits() | kBounded : bits();
+  int fwd_bits(int Tk) const {
+    return softcap > 0.f && softcap * 1.4426950408889634f <= bounded_cap_log2(Tk) ? bits() | kBounded : bits();
   }
 };
 

@@ -24,5 +24,5 @@ fa::FwdLauncher launcher(int bits) {
 }  // namespace
 
 fa::FwdLauncher fa::fwd_scored_few_128(const Problem& p, const ScoreMods& m) {
-  return p.dv == 64 ? launcher<64>(m.fwd_bits()) : launcher<128>(m.fwd_bits());
+  return p.dv == 64 ? launcher<64>(m.fwd_bits(p.Tk)) : launcher<128>(m.fwd_bits(p.Tk));
 }
