@@ -35,3 +35,22 @@ def test_calls_without_heads_or_batch(B, Hq, Hkv):
     torch.cuda.synchronize()
     assert O.shape == Q.shape and L.shape == (B, Hq, 9) and dQ.shape == Q.shape
     assert not dK.any() and not dV.any()
+
+
+def test_a_gradient_of_the_gradient_is_refused(monkeypatch):
+    """The backward kernels have no gradient: a gradient penalty through attention raises, and does not lose its term.
+    (On the CPU, with the two calls replaced by sums that have one.)"""
+    monkeypatch.setattr(fa, "fa_forward", lambda Q, K, V, *a, **kw: (Q * K + V, Q.sum(-1)))
+    monkeypatch.setattr(fa, "fa_backward", lambda Q, K, V, O, dO, L, *a, **kw: (dO * K, dO * Q, dO * 1))
+    Q, K, V = (torch.randn(1, 2, 3, 4, requires_grad=True) for _ in range(3))
+    O = fa.attention(Q, K, V, softcap=20.0)
+    dQ, = torch.autograd.grad(O.sum(), Q, create_graph=True)
+    assert torch.equal(dQ, K)
+    with pytest.raises(RuntimeError, match="differentiated again"):
+        (O.sum() + dQ.square().sum()).backward()
+    w = torch.randn_like(O).requires_grad_()  # also through the gradient that comes in
+    dV, = torch.autograd.grad((w * fa.attention(Q, K, V)).sum(), V, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiated again"):
+        dV.square().sum().backward()
+    fa.attention(Q, K, V, softcap=20.0).sum().backward()  # the first gradient is what it was
+    assert torch.equal(Q.grad, K) and torch.equal(K.grad, Q) and torch.equal(V.grad, torch.ones_like(V))

@@ -410,9 +410,23 @@ def last_launch_count() -> int:
     return int(load().fa_last_launch_count())
 
 
+class _LastGradient(torch.autograd.Function):
+    """Hands gradients on as a function of what they were made of, with no derivative
+    (torch's once_differentiable looks at dO alone)."""
+
+    @staticmethod
+    def forward(ctx, Q, K, V, dO, dQ, dK, dV):
+        return dQ, dK, dV
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the gradient of attention cannot be differentiated again")
+
+
 class FlashAttention(torch.autograd.Function):
     """Autograd wrapper: saves Q, K, V (inputs) plus O and L -- nothing quadratic
-    (and with modified scores the slopes and the mask plan)."""
+    (and with modified scores the slopes and the mask plan).  Its gradient has no
+    gradient: asking for one raises."""
 
     @staticmethod
     def forward(ctx, Q, K, V, causal=False, scale=None, window=0, softcap=0.0, slopes=None, mask=None):
@@ -430,6 +444,8 @@ class FlashAttention(torch.autograd.Function):
         mask = None if ctx.plan_key is None else MaskPlan(ctx.plan_key, more[0])
         dQ, dK, dV = fa_backward(Q, K, V, O, dO.contiguous(), L, ctx.causal, ctx.scale, window=ctx.window,
                                  softcap=ctx.softcap, slopes=slopes, mask=mask)
+        if torch.is_grad_enabled():  # a graph of the gradient is asked for (create_graph)
+            dQ, dK, dV = _LastGradient.apply(Q, K, V, dO, dQ, dK, dV)
         return dQ, dK, dV, None, None, None, None, None, None
 
 
