@@ -137,32 +137,50 @@ struct BwdCfg {
 // `have` is false when the CTA saw no query tile: the rows are zero.
 // `add` (optional): the same row's partial sums from the other half of a
 // split item, this warpgroup's columns, added before the scaling; or those of
-// n_add parts, add_stride floats apart, of which the skip-th is the CTA's own.
+// n_add parts, add_stride floats apart, of which the own-th is this CTA's (its sums are
+// those in TMEM).  The parts are added in their order, whichever of them is the last,
+// so that the sum is the same every time.
 template <int W>
 __device__ __forceinline__ void stage_rows_bf16(uint32_t src, uint8_t* stage, int r, int wg, float mul, bool have,
                                                 const float* add = nullptr, int n_add = 1, size_t add_stride = 0,
-                                                int skip = -1) {
+                                                int own = -1) {
   constexpr int HALF = W / 2;
 #pragma unroll
   for (int c = 0; c < HALF / 32; ++c) {
-    uint32_t v[32];
-    if (have) {
-      tmem_ld32(src + c * 32, v);
-      tmem_wait_ld();
-    } else {
+    auto load_own = [&](uint32_t (&t)[32]) {
+      if (have) {
+        tmem_ld32(src + c * 32, t);
+        tmem_wait_ld();
+      } else {
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = 0u;
-    }
-    for (int n = 0; add && n < n_add; ++n) {
-      if (n == skip) continue;
+        for (int e = 0; e < 32; ++e) t[e] = 0u;
+      }
+    };
+    auto load_part = [&](uint32_t (&t)[32], const float* from) {
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(add + n * add_stride + c * 32) + q);
-        v[4 * q] = __float_as_uint(__uint_as_float(v[4 * q]) + a.x);
-        v[4 * q + 1] = __float_as_uint(__uint_as_float(v[4 * q + 1]) + a.y);
-        v[4 * q + 2] = __float_as_uint(__uint_as_float(v[4 * q + 2]) + a.z);
-        v[4 * q + 3] = __float_as_uint(__uint_as_float(v[4 * q + 3]) + a.w);
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(from + c * 32) + q);
+        t[4 * q] = __float_as_uint(a.x);
+        t[4 * q + 1] = __float_as_uint(a.y);
+        t[4 * q + 2] = __float_as_uint(a.z);
+        t[4 * q + 3] = __float_as_uint(a.w);
       }
+    };
+    uint32_t v[32];
+    if (own >= 0) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = 0u;
+    } else {
+      load_own(v);
+    }
+    for (int n = 0; add && n < n_add; ++n) {
+      uint32_t t[32];
+      if (n == own)
+        load_own(t);
+      else
+        load_part(t, add + n * add_stride);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(t[e]));
     }
     const int col0 = wg * HALF + c * 32;  // first column of this chunk
 #pragma unroll
@@ -802,16 +820,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (finish) {
           __threadfence();
           other = p.part + ((size_t)split * parts * BN + r) * (HD + HDV);
-          if (!MODS) other += (size_t)(half ^ 1) * BN * (HD + HDV);
+          if (parts == 2) other += (size_t)(half ^ 1) * BN * (HD + HDV);
         }
       }
-      const int n_other = MODS ? parts : 1, skip = MODS ? half : -1;
+      // (two sums are the same in either order; more are added in theirs)
+      const int n_other = parts > 2 ? parts : 1, own_part = parts > 2 && other ? half : -1;
       constexpr size_t kPartStride = (size_t)BN * (HD + HDV);
       if (!finish) goto epilogue_done;
       stage_rows_bf16<HDV>(T_DV + lane_base + wg * (HDV / 2), smem + C::OFF_DV_STAGE, r, wg, 1.f, T > 0,
-                           other ? other + wg * (HDV / 2) : nullptr, n_other, kPartStride, skip);
+                           other ? other + wg * (HDV / 2) : nullptr, n_other, kPartStride, own_part);
       stage_rows_bf16<HD>(T_DK + lane_base + wg * (HD / 2), smem + C::OFF_DK_STAGE, r, wg, p.scale_grad, T > 0,
-                          other ? other + HDV + wg * (HD / 2) : nullptr, n_other, kPartStride, skip);
+                          other ? other + HDV + wg * (HD / 2) : nullptr, n_other, kPartStride, own_part);
       fence_async_smem();
       named_bar_sync(2, 256);
       if (warp == 4 && lane == 0) {
