@@ -129,13 +129,12 @@ cudaError_t launch_main_dims(const fa::Problem& pr, const CUtensorMap* maps, con
 // Groups per super-batch of fa_bwd_main's grid order: the smallest divisor of
 // the group count whose super-batch holds at least 1.5 CTAs per SM, so that
 // one super-batch fills the GPU with a heaviest-first queue of its own while
-// few groups' data is live in L2.  0 if the SM count cannot be read.
-int backward_super_batch(int n_groups, int kv_tiles) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) !=
-                                                 cudaSuccess)
-    return 0;
-  return fa::super_batch_groups(n_groups, kv_tiles, sms);
+// few groups' data is live in L2 (with a plan: see planned_super_batch_groups).
+// 0 if the SM count cannot be read.
+int backward_super_batch(int n_groups, int kv_tiles, bool planned) {
+  const int sms = fa::sm_count();
+  if (sms <= 0) return 0;
+  return planned ? fa::planned_super_batch_groups(n_groups, kv_tiles, sms) : fa::super_batch_groups(n_groups, kv_tiles, sms);
 }
 
 inline int grid_for(long long work, int per_block) {
@@ -256,11 +255,8 @@ cudaError_t launch_backward(const Problem& pr, const ScoreMods& mods, const void
   bp.window = pr.causal ? pr.window : 0;
   bp.q_tiles = pr.q_tiles();
   bp.kv_tiles = pr.kv_tiles();
-  // Items in parts, and a plan's, which are in order of their work: one super-batch,
-  // so that the heaviest are the first of all.  (Packed documents of T 8192, 32 / 8
-  // heads: by position in super-batches 393 us, by work in super-batches 403, by work in
-  // one 349.)
-  bp.sb_groups = parts.items || mods.plan ? pr.B * pr.Hkv : backward_super_batch(pr.B * pr.Hkv, pr.kv_tiles());
+  // (items in parts: the heaviest of all first)
+  bp.sb_groups = parts.items ? pr.B * pr.Hkv : backward_super_batch(pr.B * pr.Hkv, pr.kv_tiles(), mods.plan != nullptr);
   if (bp.sb_groups < 1) return cudaErrorInvalidValue;
   bp.Tq_pad = pr.Tq_pad();
   bp.scale_grad = scale_grad(pr, mods);

@@ -343,6 +343,22 @@ inline int super_batch_groups(int n_groups, int kv_tiles, int sms) {
   return n_groups;
 }
 
+// The same with a mask plan, which knows each key tile's work.  Up to eight groups go as
+// one super-batch, so that the heaviest tiles are the first of all; more groups' fp32 dQ
+// and dO would no longer stay in L2, and within super-batches the tiles still go by work.
+// Main kernel, one super-batch / the plain rule's, us, heads of 128 (query / kv heads),
+// packed documents:
+//   4 x T 8192, 8 / 2 of 64    238 / 270      B 1, T 8192, 40 / 10    393 / 371
+//   B 1, T 16384, 32 / 4      1231 / 1286     B 1, T 8192, 48 / 12    465 / 471
+//   B 1, T 8192, 32 / 8        303 / 330      B 2, T 4096, 32 / 8     211 / 195
+//   B 1, T 32768, 32 / 8      4182 / 4196     B 4, T 8192, 32 / 8    1565 / 1243
+//   B 1, T 8192, 64 / 8        715 / 678      B 8, T 8192, 32 / 8    3702 / 2438
+// (one document: B 8 12082 / 8011, where the unmodified call takes 8100).
+constexpr int kPlannedGroups = 8;
+inline int planned_super_batch_groups(int n_groups, int kv_tiles, int sms) {
+  return n_groups <= kPlannedGroups ? n_groups : super_batch_groups(n_groups, kv_tiles, sms);
+}
+
 // Work items of the backward main kernel that may be split in two (see
 // backward_split_items); the workspace holds their fp32 partial dK / dV.
 constexpr int kMaxSplitItems = 128;
