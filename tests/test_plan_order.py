@@ -1,6 +1,7 @@
 """The order in which the planned backward takes its key tiles: one super-batch for few
 (batch, kv head) groups, the plain rule's super-batches for many, whose live data would not
-stay in L2 together; the results are the definition's either way."""
+stay in L2 together; and the parts that they run in where there are few, as many as the
+plan leaves work for.  The results are the definition's either way."""
 import os
 import shutil
 import subprocess
@@ -68,3 +69,25 @@ def test_planned_backward_in_super_batches(B, Hq, Hkv, T, d, dv, causal):
         for got, want, s in zip((O, *grads), (O1, *grads1), (h, h, slice(hk, hk + 1), slice(hk, hk + 1))):
             off = (got[b:b + 1, s].float() - want.float()).norm() / want.float().norm()
             assert float(off) <= 2.0 ** -7, float(off)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["short", "one", "a long one among short ones", "prefix"])
+@pytest.mark.parametrize("B, Hq, Hkv, T, d, dv", [(1, 8, 2, 1900, 128, 64), (1, 16, 1, 1300, 64, 128), (2, 8, 4, 1000, 64, 64)])
+def test_planned_items_in_as_many_parts_as_they_have_work_for(B, Hq, Hkv, T, d, dv, kind):
+    """Of 15, 11 and 64 key tiles: some whole, some in two parts, some in up to eight, in one launch."""
+    t = torch.arange(T, device="cuda")
+    ids = {"short": t // 70, "one": t * 0, "a long one among short ones": torch.where((t > 400) & (t < T - 300), 400, t // 50)}
+    Q, K, V, dO = inputs(B, Hq, Hkv, T, T, d, dv, seed=T + len(kind))
+    docs = prefix = None
+    if kind == "prefix":
+        prefix = torch.tensor([T - 100, 30][:B], dtype=torch.int32, device="cuda")
+    else:
+        ids = ids[kind].int().expand(B, T).contiguous()
+        docs = (ids, ids)
+    first = compare(Q, K, V, dO, True, softcap=30.0, docs=docs, prefix=prefix, tag=kind)
+    again = compare(Q, K, V, dO, True, softcap=30.0, docs=docs, prefix=prefix, tag=kind)
+    for a, b in zip(first[3:], again[3:]):  # dK, dV: the parts are added in their order
+        assert torch.equal(a, b)
+    if docs:
+        compare(Q, K, V, dO, False, softcap=30.0, slopes=alibi(Hq), docs=docs, tag=kind + " both ways")

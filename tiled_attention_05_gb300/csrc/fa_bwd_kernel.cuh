@@ -415,6 +415,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int n_m = max(0, m_end - m_begin);
   const int T_item = p.G * n_m;  // the item's tiles
+  if constexpr (MODS) {
+    if (split >= 0 && p.plan.m_beg) {
+      // The launcher counts without the plan: an item of few tiles after all runs in
+      // fewer parts, or whole (part 0), and the CTAs of the rest leave.
+      parts = min(parts, max(1, T_item / fa::kPlannedPartTiles));
+      if (half >= parts) return;
+      if (parts == 1) split = -1;
+    }
+  }
   // this CTA's tiles: [t0, t0 + T) of the item's
   int t0 = split >= 0 && half ? T_item / 2 : 0;
   int T = split >= 0 ? (half ? T_item - T_item / 2 : T_item / 2) : T_item;
@@ -795,6 +804,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // to its own and stores the item's dV and dK.  Neither waits for the other.
       const float* other = nullptr;
       bool finish = true;
+      size_t slot0 = (size_t)split * 2;  // the item's first slot of the partial area
+      if constexpr (MODS) slot0 = (size_t)split * p.parts;
       if (split >= 0) {
         // (modified scores: a part that finds all others counted in is the last, and
         // need not write its own sums)
@@ -808,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (last) {
           finish = true;
         } else {
-          float* own = p.part + (((size_t)split * parts + half) * BN + r) * (HD + HDV);
+          float* own = p.part + ((slot0 + half) * BN + r) * (HD + HDV);
           write_partial<HDV>(T_DV + lane_base + wg * (HDV / 2), own + wg * (HDV / 2), T > 0);
           write_partial<HD>(T_DK + lane_base + wg * (HD / 2), own + HDV + wg * (HD / 2), T > 0);
           __threadfence();
@@ -819,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (finish) {
           __threadfence();
-          other = p.part + ((size_t)split * parts * BN + r) * (HD + HDV);
+          other = p.part + (slot0 * BN + r) * (HD + HDV);
           if (parts == 2) other += (size_t)(half ^ 1) * BN * (HD + HDV);
         }
       }

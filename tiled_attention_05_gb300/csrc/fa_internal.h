@@ -382,9 +382,19 @@ BwdWorkspace backward_workspace_layout(const Problem& p, long long slots = -1, i
 // left to a part, whose set-up and fp32 partial sums cost about as much as two.
 // (B 2, 16 / 4 heads of 128, T 2001, prefixes: 142 us whole, 114 with every item in
 // four parts, 105 with the heavier half of the items in two; with all of them in two
-// 97 out of L2, but the step's time on cold data rises by 7 for the partial sums.)  A plan's documents are not known here: its items count as without
-// it.  With more than two items per SM the plain rule holds (equal work: a short
-// last round in halves).
+// 97 out of L2, but the step's time on cold data rises by 7 for the partial sums.)
+// With more than two items per SM the plain rule holds (equal work: a short last round
+// in halves).
+// What a plan hides is not known here; its items are split as they are without it, and
+// in the kernel an item takes as many of its parts as have kPlannedPartTiles tiles: the
+// mean is lower than was counted, so a part has to be worth more.  Backward, us, all
+// parts / 4 tiles a part / 8 / 12 / 16 / nothing split; heads of 128:
+//   4096 tokens in documents of 64, 8 / 2 heads        80   37   37   37   37   37
+//   2048 in documents of 300, 16 / 4                   88   76   61   60   59   59
+//   2 x 2001 in documents of 700, 16 / 4               90   92   92   80   86   87
+//   2048 in documents of 1000, 8 / 1                  123  124  124  106   98  168
+//   2048 in one document, 16 / 4                      109  111  104   99   99  158
+constexpr int kPartTiles = 4, kPlannedPartTiles = 12;
 struct ScoredSplit {
   int items, parts;  // 0: none
 };
@@ -404,7 +414,7 @@ inline ScoredSplit scored_split(const Problem& p, int sms) {
     total += w * groups;
     if (w > most) most = w;
   }
-  const double mean = (double)total / sms, target = mean > 4.0 ? mean : 4.0;
+  const double mean = (double)total / sms, target = mean > kPartTiles ? mean : kPartTiles;
   int parts = (int)(most / (1.2 * target)) + (most > 1.2 * target);
   if (parts > 8) parts = 8;
   long long items = 0;
