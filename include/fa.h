@@ -248,8 +248,8 @@ FA_API const char* fa_status_string(fa_status s);
  * if the stream holds an asynchronous CUDA error, FA_OK otherwise. */
 FA_API fa_status fa_last_device_status(void* stream);
 
-/* Number of kernel launches the last fa_forward / fa_backward call on this
- * host thread enqueued (for launch accounting). */
+/* Number of kernel launches the last call of fa_forward, fa_backward (any form of
+ * them) or fa_mask_plan on this host thread enqueued (for launch accounting). */
 FA_API int fa_last_launch_count(void);
 
 #ifdef __cplusplus

@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = s_full + 7;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile unsigned int* split_seen = reinterpret_cast<volatile unsigned int*>(tmem_slot + 2);  // halves counted before
+  volatile unsigned int* split_seen = reinterpret_cast<volatile unsigned int*>(tmem_slot + 2);  // parts counted before
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // One linear grid in super-batches of sb_groups (batch, kv head) groups;
@@ -362,8 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // groups' Q, dO and fp32 dQ accumulator are live at a time, so they stay in
   // L2.  (One group at a time keeps even less live, but its late heavy CTAs
   // make the causal step ~12% longer.)
-  // Split items exist only without a causal mask (equal-work items); the
-  // causal instances compile none of their code.
+  // Plain calls have split items only without a causal mask (equal-work items): a
+  // short last round, in two halves; the causal instances compile none of their
+  // code.  Scored calls have them there too, and where there are few items of any
+  // mask: the first ones, in `parts` parts (fa::BwdParams).
   constexpr bool MODS = SCORE >= 0, CAP = MODS && (SCORE & fa::kCap), SLOPES = MODS && (SCORE & fa::kSlopes);
   constexpr bool SPLIT = MODS || !CAUSAL;
   int item = blockIdx.x, split = -1, half = 0;
@@ -799,9 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const bool mine = (T == 0 || ok) && *abort_flag == 0;
     if (named_bar_and(1, 256, mine)) {
-      // A split item's halves: each writes its fp32 sums to the partial area
-      // and counts itself in; the one that comes second adds the other's sums
-      // to its own and stores the item's dV and dK.  Neither waits for the other.
+      // A split item's parts (or halves): each writes its fp32 sums to the partial
+      // area and counts itself in; the one that comes last adds the others' sums and
+      // its own and stores the item's dV and dK.  None waits for another.
       const float* other = nullptr;
       bool finish = true;
       size_t slot0 = (size_t)split * 2;  // the item's first slot of the partial area

@@ -70,8 +70,9 @@
 // the softmax: the more its warps issue, the longer each group of MMAs takes to
 // issue (PV 602 cycles a group plain, 731 with a cap, 774 with both; the softmax
 // 1050, 1800 and 2100 cycles a tile).  B 2, 32 / 8 heads of 128, T 8192, causal:
-// 758 us plain, 960 with a cap of 50 or slopes, 1060 with both; 4 batches of 16 heads of
-// 64, T 2048: 54, 78 with a cap (98 where scores are past half of it), 74 and 85.
+// 758 us plain, 960 with a cap of 50 or slopes, 1060 with both; 1249 with a cap whose half
+// the scores pass; 4 batches of 16 heads of 64, T 2048: 54, 78 with a cap (98 past its
+// half), 74 and 85.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -378,8 +379,10 @@ __device__ __forceinline__ uint64_t pair_of(const uint32_t (&s)[32], int c) {
 // Steps of 64 columns suit slopes (T 8192, d 128: 1090 -> 1060 us; T 2048, d 64: 89.6 ->
 // 84.8) and not the cap alone (968 -> 1052).
 // The loop stays rolled: unrolled, its instructions crowd the MMA thread's out of
-// the instruction cache (T 8192, d 128: 925 us rolled, 1005 unrolled; two
-// warpgroups of 64 columns each per tile: 980 and 1025).
+// the instruction cache (T 8192, d 128: 964 us rolled, 997 unrolled; scores past the
+// polynomial 1249 and 1403; T 2048, d 64: 82 and 96).  Two warpgroups of 64 columns
+// each per tile were slower too (with the polynomial of degree 7, 925 us for one, 980
+// to 1025 for two).
 template <bool SLOPES, bool MASKED>
 __device__ __forceinline__ float2 bounded_tile(uint32_t tS, const ScoredFwdParams& p, const uint32_t (&vis4)[BN / 32],
                                                int rel0, float slope2, float m_ref) {
@@ -562,8 +565,11 @@ __device__ __forceinline__ void turn_over(uint32_t (&sr)[BN], int rel0, float pe
 }
 
 // Capped scores of one row and key tile, in place: raw q.k -> log2 units with the
-// cap and the distance bias (caps too wide for the bounded form, and plans that
-// compare documents key by key).  crossing: keys on both sides of the row's
+// cap and the distance bias (caps too wide for the bounded form, and slopes with plans
+// that compare documents key by key).  The form that holds everywhere serves all
+// scores, off by at most 2^-20 of the cap (L: 2e-4 under a cap of 1000), where the
+// backward takes the polynomial on small ones: by 32 columns at a time here it cost
+// 1309 -> 1387 us (T 8192, d 128, cap 100), and 1385 -> 1753 where scores pass it.  crossing: keys on both sides of the row's
 // position may be visible; the rising line is then turned over past it.  (Two
 // forms of the whole, each in a branch of its own, cost a move per score where
 // the branches meet: 1870 against 2550 cycles a tile with slopes alone.)

@@ -78,7 +78,8 @@ int sm_count();
 // kBounded (forward, with kCap): the cap keeps 2^score inside fp32, so the
 // softmax needs no running maximum.
 // kFew (forward): packed heads and split items (FwdShape).  (In every instance their
-// bookkeeping cost the large calls 4%: T 8192, cap 50, 938 -> 978 us.)
+// bookkeeping cost the large calls 4%: T 8192, cap 50, with the polynomial of degree 7
+// that was taken then, 938 -> 978 us.)
 enum ScoreBits : int { kPlain = -1, kCap = 1, kSlopes = 2, kBounded = 4, kFew = 8 };
 
 // Largest cap (log2 units) of the bounded form over Tk keys.  P is between 2^-90 and
@@ -288,13 +289,17 @@ struct BwdParams {
   long long Tq_pad;
   float scale_log2, scale_grad;  // scale_grad: of dK (scale, times 4 with a cap)
   int test_withhold_do;  // test build only: never issue the dO loads (the CTA's waits then time out)
-  // Split items: the last n_split items of the grid order run as two CTAs
-  // each (CTAs n_whole + 2 s and n_whole + 2 s + 1 for item n_whole + s),
-  // each walking half of the item's query tiles; the halves' fp32 dK / dV
-  // meet in `part`, and whichever half finishes second adds the other's and
-  // stores them (split_counters, zeroed by fa_bwd_pre, tell them apart).
+  // Split items.  Plain rule: the last n_split items of the grid order run as two
+  // CTAs each (CTAs n_whole + 2 s and n_whole + 2 s + 1 for item n_whole + s), each
+  // walking half of the item's query tiles.  Scored calls of few items
+  // (ScoredBwdParams::split_first): the first n_split items run as `parts` CTAs each
+  // (CTAs parts * s ... for item s), each walking its share; with a plan as many of
+  // them as there is work for.  The CTAs' fp32 dK / dV meet in `part`, and whichever
+  // finishes last adds the others' and stores the sum.  split_counters, zeroed by
+  // fa_bwd_pre, count those that have written theirs; in scored calls a CTA that finds
+  // all others counted before it writes is the last, and neither writes nor counts.
   int n_whole, n_split;
-  float* part;                    // [n_split][2 halves][128 key rows][d + dv]
+  float* part;                    // [n_split][2, or parts][128 key rows][d + dv]
   unsigned int* split_counters;   // [n_split]
 };
 // What the score-modified instances need besides (see ScoreMods).
@@ -303,7 +308,7 @@ struct ScoredBwdParams : BwdParams {
   const float* slopes;     // [Hq]
   int hi_off, lo_off;      // row i sees keys [i + lo_off, i + hi_off) (no plan)
   int two_sided;           // a row may see keys on both sides of its own position
-  int parts, split_first;  // CTAs per split item; the split items are the order's first (see scored_split)
+  int parts, split_first;  // CTAs per split item (2 by the plain rule); whether those are the order's first (scored_split)
   PlanView plan;
 };
 
@@ -359,14 +364,15 @@ inline int planned_super_batch_groups(int n_groups, int kv_tiles, int sms) {
   return n_groups <= kPlannedGroups ? n_groups : super_batch_groups(n_groups, kv_tiles, sms);
 }
 
-// Work items of the backward main kernel that may be split in two (see
-// backward_split_items); the workspace holds their fp32 partial dK / dV.
+// Work items of the backward main kernel that may be split (in two: see
+// backward_split_items; in parts: scored_split); the workspace holds their fp32
+// partial dK / dV.
 constexpr int kMaxSplitItems = 128;
 
 // Workspace carve-up of fa_backward (byte offsets, 256-aligned).  `part` and
 // `counters` (the split items' partial dK / dV and their finish counters)
-// are empty when no item can be split (with a causal mask).  The backward
-// needs `total_min` bytes (up to `part`); it splits items only when the
+// are empty when no item can be split (a plain call with a causal mask, or a
+// scored one of many items).  The backward needs `total_min` bytes (up to `part`); it splits items only when the
 // workspace also holds the split area (`total`).
 struct BwdWorkspace {
   size_t dq_acc, lse2, delta, part, counters, total_min, total;
