@@ -70,8 +70,8 @@
 // causal mask and window; a plan whose intervals are not in order is looked up
 // row by row instead.  Where there are few key tiles of unequal work, the
 // heaviest run in parts (fa::scored_split).  Bounded as the plain form is, with
-// a longer elementwise phase: 32 / 8 heads of 128, T 8192, causal, 985 us plain,
-// 1012 with slopes, 1195 with a cap, 1220 with both.
+// a longer elementwise phase: 32 / 8 heads of 128, T 8192, causal, 970 us plain,
+// 977 with slopes, 1152 with a cap, 1228 with both.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -136,51 +136,37 @@ struct BwdCfg {
 // as bf16 into a 128-row, 128B-swizzled staging tile for the TMA store.
 // `have` is false when the CTA saw no query tile: the rows are zero.
 // `add` (optional): the same row's partial sums from the other half of a
-// split item, this warpgroup's columns, added before the scaling; or those of
-// n_add parts, add_stride floats apart, of which the own-th is this CTA's (its sums are
-// those in TMEM).  The parts are added in their order, whichever of them is the last,
-// so that the sum is the same every time.
+// split item, this warpgroup's columns, added before the scaling; or, with `all`, those
+// of all n_add parts (its own among them), add_stride floats apart, added in their
+// order, whichever of them is the last to finish, so that the sum is the same every time.
+// The loops stay rolled: what this code takes up moves the main loop's (cap and slopes,
+// T 8192, 32 / 8 heads of 128: 1278 us unrolled, 1225 rolled; 64-wide heads with values of
+// 128: 1077 and 1094; a cap alone 1165 and 1152).
 template <int W>
 __device__ __forceinline__ void stage_rows_bf16(uint32_t src, uint8_t* stage, int r, int wg, float mul, bool have,
                                                 const float* add = nullptr, int n_add = 1, size_t add_stride = 0,
-                                                int own = -1) {
+                                                bool all = false) {
   constexpr int HALF = W / 2;
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < HALF / 32; ++c) {
-    auto load_own = [&](uint32_t (&t)[32]) {
-      if (have) {
-        tmem_ld32(src + c * 32, t);
-        tmem_wait_ld();
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) t[e] = 0u;
-      }
-    };
-    auto load_part = [&](uint32_t (&t)[32], const float* from) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(from + c * 32) + q);
-        t[4 * q] = __float_as_uint(a.x);
-        t[4 * q + 1] = __float_as_uint(a.y);
-        t[4 * q + 2] = __float_as_uint(a.z);
-        t[4 * q + 3] = __float_as_uint(a.w);
-      }
-    };
     uint32_t v[32];
-    if (own >= 0) {
+    if (have && !all) {
+      tmem_ld32(src + c * 32, v);
+      tmem_wait_ld();
+    } else {
 #pragma unroll
       for (int e = 0; e < 32; ++e) v[e] = 0u;
-    } else {
-      load_own(v);
     }
+#pragma unroll 1
     for (int n = 0; add && n < n_add; ++n) {
-      uint32_t t[32];
-      if (n == own)
-        load_own(t);
-      else
-        load_part(t, add + n * add_stride);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(t[e]));
+      for (int q = 0; q < 8; ++q) {
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(add + n * add_stride + c * 32) + q);
+        v[4 * q] = __float_as_uint(__uint_as_float(v[4 * q]) + a.x);
+        v[4 * q + 1] = __float_as_uint(__uint_as_float(v[4 * q + 1]) + a.y);
+        v[4 * q + 2] = __float_as_uint(__uint_as_float(v[4 * q + 2]) + a.z);
+        v[4 * q + 3] = __float_as_uint(__uint_as_float(v[4 * q + 3]) + a.w);
+      }
     }
     const int col0 = wg * HALF + c * 32;  // first column of this chunk
 #pragma unroll
@@ -202,7 +188,7 @@ __device__ __forceinline__ void stage_rows_bf16(uint32_t src, uint8_t* stage, in
 template <int W>
 __device__ __forceinline__ void write_partial(uint32_t src, float* dst, bool have) {
   constexpr int HALF = W / 2;
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < HALF / 32; ++c) {
     uint32_t v[32];
     if (have) {
@@ -809,13 +795,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       size_t slot0 = (size_t)split * 2;  // the item's first slot of the partial area
       if constexpr (MODS) slot0 = (size_t)split * p.parts;
       if (split >= 0) {
-        // (modified scores: a part that finds all others counted in is the last, and
+        // (modified scores: the half that finds the other counted in is the last, and
         // need not write its own sums)
         bool last = false;
-        if constexpr (MODS) {
+        if (MODS && parts == 2) {
           if (warp == 4 && lane == 0) *split_seen = __ldcg(&p.split_counters[split]);
           named_bar_sync(3, 256);
-          last = *split_seen == (unsigned)parts - 1u;
+          last = *split_seen == 1u;
           named_bar_sync(3, 256);  // all have read it
         }
         if (last) {
@@ -836,14 +822,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (parts == 2) other += (size_t)(half ^ 1) * BN * (HD + HDV);
         }
       }
-      // (two sums are the same in either order; more are added in theirs)
-      const int n_other = parts > 2 ? parts : 1, own_part = parts > 2 && other ? half : -1;
+      // (two sums are the same in either order)
+      const bool all = parts > 2 && other;
+      const int n_other = all ? parts : 1;
       constexpr size_t kPartStride = (size_t)BN * (HD + HDV);
       if (!finish) goto epilogue_done;
       stage_rows_bf16<HDV>(T_DV + lane_base + wg * (HDV / 2), smem + C::OFF_DV_STAGE, r, wg, 1.f, T > 0,
-                           other ? other + wg * (HDV / 2) : nullptr, n_other, kPartStride, own_part);
+                           other ? other + wg * (HDV / 2) : nullptr, n_other, kPartStride, all);
       stage_rows_bf16<HD>(T_DK + lane_base + wg * (HD / 2), smem + C::OFF_DK_STAGE, r, wg, p.scale_grad, T > 0,
-                          other ? other + HDV + wg * (HD / 2) : nullptr, n_other, kPartStride, own_part);
+                          other ? other + HDV + wg * (HD / 2) : nullptr, n_other, kPartStride, all);
       fence_async_smem();
       named_bar_sync(2, 256);
       if (warp == 4 && lane == 0) {

@@ -295,9 +295,10 @@ struct BwdParams {
   // (ScoredBwdParams::split_first): the first n_split items run as `parts` CTAs each
   // (CTAs parts * s ... for item s), each walking its share; with a plan as many of
   // them as there is work for.  The CTAs' fp32 dK / dV meet in `part`, and whichever
-  // finishes last adds the others' and stores the sum.  split_counters, zeroed by
-  // fa_bwd_pre, count those that have written theirs; in scored calls a CTA that finds
-  // all others counted before it writes is the last, and neither writes nor counts.
+  // finishes last adds them up (more than two: in their order) and stores the sum.
+  // split_counters, zeroed by fa_bwd_pre, count those that have written theirs; in
+  // scored calls the second of two that finds the first counted before it writes
+  // neither writes nor counts.
   int n_whole, n_split;
   float* part;                    // [n_split][2, or parts][128 key rows][d + dv]
   unsigned int* split_counters;   // [n_split]
@@ -395,11 +396,11 @@ BwdWorkspace backward_workspace_layout(const Problem& p, long long slots = -1, i
 // in the kernel an item takes as many of its parts as have kPlannedPartTiles tiles: the
 // mean is lower than was counted, so a part has to be worth more.  Backward, us, all
 // parts / 4 tiles a part / 8 / 12 / 16 / nothing split; heads of 128:
-//   4096 tokens in documents of 64, 8 / 2 heads        80   37   37   37   37   37
-//   2048 in documents of 300, 16 / 4                   88   76   61   60   59   59
-//   2 x 2001 in documents of 700, 16 / 4               90   92   92   80   86   87
-//   2048 in documents of 1000, 8 / 1                  123  124  124  106   98  168
-//   2048 in one document, 16 / 4                      109  111  104   99   99  158
+//   4096 tokens in documents of 64, 8 / 2 heads        81   37   37   37   37   37
+//   2048 in documents of 300, 16 / 4                   90   84   61   61   61   61
+//   2 x 2001 in documents of 700, 16 / 4               92   92   91   84   86   87
+//   2048 in documents of 1000, 8 / 1                  125  137  135  117  111  170
+//   2048 in one document, 16 / 4                      109  119  115  109  109  158
 constexpr int kPartTiles = 4, kPlannedPartTiles = 12;
 struct ScoredSplit {
   int items, parts;  // 0: none
