@@ -118,6 +118,29 @@ def test_a_nan_reaches_the_gradients(form):
         assert bool(torch.isfinite(t).all())
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("cap, slopes", [(5.0, False), (5.0, True), (100.0, True)])
+def test_a_nan_row_leaves_the_other_rows_gradients(cap, slopes, causal):
+    """dQ of the rows beside a NaN row is what it is without it, also where one reciprocal serves four rows' capped
+    scores (past half the cap).  dQ is added up in fp32 in any order and rounded once: 2^-8 of the whole."""
+    B, Hq, Hkv, T, d = 1, 4, 2, 300, 64
+    Q, K, V, dO = inputs(B, Hq, Hkv, T, T, d, d, seed=5, std=8.0 * cap / 5)
+    mods = dict(softcap=cap, slopes=alibi(Hq) if slopes else None)
+
+    def dq(Q):
+        O, L = fa.fa_forward(Q, K, V, causal, **mods)
+        return fa.fa_backward(Q, K, V, O, dO, L, causal, **mods)[0]
+
+    want = dq(Q)
+    bad = Q.clone()
+    bad[0, 1, 141, 3] = bad[0, 3, 10, 0] = NAN
+    got = dq(bad)
+    assert bool(got[0, 1, 141].isnan().all()) and bool(got[0, 3, 10].isnan().all())
+    got[0, 1, 141], got[0, 3, 10] = want[0, 1, 141], want[0, 3, 10]
+    assert bool(torch.isfinite(got).all())
+    assert float((got.float() - want.float()).norm()) <= 2.0 ** -8 * float(want.float().norm())
+
+
 @pytest.mark.parametrize("cap, slopes", [(20.0, False), (50.0, True), (200.0, True)])
 @pytest.mark.parametrize("Tq, Tk", [(32, 4000), (300, 300)])
 def test_infinite_scores_count_as_the_cap(Tq, Tk, cap, slopes):

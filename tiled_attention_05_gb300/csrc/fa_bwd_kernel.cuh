@@ -237,7 +237,7 @@ __device__ __forceinline__ bool modified_chunk(const ScoredBwdParams& p, const u
     uint64_t x[2] = {f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
                      f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]))};
     uint64_t r[2], e[2];
-    if (CAP && !SMALL) cap_quad(f2_mul(x[0], in2), f2_mul(x[1], in2), r[0], r[1], e[0], e[1]);
+    if (CAP && !SMALL) cap_quad<false>(f2_mul(x[0], in2), f2_mul(x[1], in2), r[0], r[1], e[0], e[1]);
     const float gb = fmaf(rel + (float)c, side, log2c);  // (the sum is exact)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {

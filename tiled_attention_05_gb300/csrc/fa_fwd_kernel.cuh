@@ -447,7 +447,7 @@ __device__ __forceinline__ float2 bounded_tile(uint32_t tS, const ScoredFwdParam
 #pragma unroll
       for (int c = 0; c < W; c += 4) {
         uint64_t r01, r23, e01, e23;
-        cap_quad(f2_mul(two(c), in2), f2_mul(two(c + 2), in2), r01, r23, e01, e23);
+        cap_quad<true>(f2_mul(two(c), in2), f2_mul(two(c + 2), in2), r01, r23, e01, e23);
         take(c, f2_fma(r01, m2cap2, bias(c, p.cap.log2c)), f2_fma(r23, m2cap2, bias(c + 2, p.cap.log2c)));
       }
     }
@@ -584,7 +584,7 @@ __device__ __forceinline__ void cap_scores(uint32_t (&sr)[BN], const ScoredFwdPa
     const uint64_t s01 = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
     const uint64_t s23 = f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
     uint64_t r01, r23, e01, e23, b01 = cap2, b23 = cap2;
-    cap_quad(f2_mul(s01, in2), f2_mul(s23, in2), r01, r23, e01, e23);
+    cap_quad<true>(f2_mul(s01, in2), f2_mul(s23, in2), r01, r23, e01, e23);
     if (SLOPES) {
       const float g = line.at(c & ~7, p.cap.log2c);
       b01 = f2_add(line.step[(c & 7) / 2], f2_pack(g, g));

@@ -345,12 +345,20 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // and the derivative 1 - tanh^2 = 4 e r^2.  One reciprocal serves all four: the
 // product of the four sums stays below 2^121 because z is held at 30, where
 // tanh is 1 to 2^-29.  (A reciprocal for each is the slower part: the special
-// function unit gives 16 a clock and SM, against 32 of ex2.)
+// function unit gives 16 a clock and SM, against 32 of ex2.)  One NaN among the four
+// reaches all of them with KEEP_NAN, as it must where the four are one row's scores; the
+// backward's are four rows', whose statistic L brings each its own NaN, and a score of
+// NaN counts as one past the cap there.
+template <bool KEEP_NAN>
+__device__ __forceinline__ float cap_top(float z) {
+  constexpr float kTop = 30.f;
+  return KEEP_NAN ? min_nan(z, kTop) : fminf(z, kTop);
+}
+template <bool KEEP_NAN>
 __device__ __forceinline__ void cap_quad(uint64_t z01, uint64_t z23, uint64_t& r01, uint64_t& r23, uint64_t& e01,
                                          uint64_t& e23) {
-  constexpr float kTop = 30.f;
-  e01 = f2_pack(ex2(min_nan(f2_lo(z01), kTop)), ex2(min_nan(f2_hi(z01), kTop)));
-  e23 = f2_pack(ex2(min_nan(f2_lo(z23), kTop)), ex2(min_nan(f2_hi(z23), kTop)));
+  e01 = f2_pack(ex2(cap_top<KEEP_NAN>(f2_lo(z01))), ex2(cap_top<KEEP_NAN>(f2_hi(z01))));
+  e23 = f2_pack(ex2(cap_top<KEEP_NAN>(f2_lo(z23))), ex2(cap_top<KEEP_NAN>(f2_hi(z23))));
   const uint64_t one = f2_pack(1.f, 1.f);
   const uint64_t d01 = f2_add(e01, one), d23 = f2_add(e23, one);
   const uint64_t d02_13 = f2_mul(d01, d23);                 // (d0 d2, d1 d3)
