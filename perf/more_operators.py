@@ -5,7 +5,7 @@ Cache.  K [pages, Hkv, page, d] and V [pages, Hkv, page, dv], bf16, or e4m3 with
 fp32 scale for each row of d (dv) values.  tables[b] lists the pages of sequence b:
 its position p is row p % page of page tables[b][p / page].
 Write.  Token t < counts[b] of sequence b goes to position starts[b] + t:
-    a = max(|x|) (2^-100 at least), code = e4m3(x * (448 / a)), scale = a * (1 / 448)
+    a = max(|x|) (2^-60 at least), code = e4m3(x * (448 / a)), scale = a * (1 / 448)
 Read back.  bf16(code * scale) of positions 0 .. lengths[b] - 1, zeros after them.
 Attention.  Row t (of Tq) of sequence b stands at its position p = lengths[b] - Tq + t,
 behind P tokens of a prefix that a group of sequences shares (P = 0 without one); it
@@ -25,7 +25,7 @@ import torch
 own = False
 
 E4M3_MAX = 448.0
-LEAST = 2.0 ** -100
+LEAST = 2.0 ** -60
 
 
 def _write(name, B, Hkv, T, d, dv=0, quant=True, page=64, lo=0, start=0, packed=False):
