@@ -146,7 +146,8 @@ def work(case):
 # ---------------------------------------------------------------- inputs
 def _quantise(x):
     a = x.float().abs().amax(-1, keepdim=True).clamp_min(LEAST)
-    return (x.float() * (E4M3_MAX / a)).to(torch.float8_e4m3fn), (a * (1.0 / E4M3_MAX)).squeeze(-1)
+    f = torch.full_like(a, E4M3_MAX) / a  # (a number divided by a tensor would be its product with a reciprocal)
+    return (x.float() * f).to(torch.float8_e4m3fn), (a * (1.0 / E4M3_MAX)).squeeze(-1)
 
 
 def _tables(g, dev, rows, n, first):
