@@ -73,7 +73,8 @@ typedef enum {
   FA_ERR_UNSUPPORTED = 2,
   FA_ERR_CUDA = 3,
   FA_ERR_TIMEOUT = 4,
-  FA_ERR_SCRATCH_TOO_SMALL = 5
+  FA_ERR_SCRATCH_TOO_SMALL = 5,
+  FA_ERR_BAD_TABLE = 6
 } fa_status;
 
 typedef struct {
@@ -240,12 +241,89 @@ typedef struct {
 FA_API fa_status fa_rotary(const fa_rotary_dims* dims, const void* Q, const void* K, const void* positions,
                            const float* inv_freq, void* Qo, void* Ko, int inverse, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A paged key/value cache, and attention of the newest tokens over it (the steps
+ * after training: sampling from and evaluating a model token by token).
+ *
+ * Pools: K [pages, Hkv, page, d] and V [pages, Hkv, page, dv], bf16, or with
+ * quantised = 1 e4m3 with one fp32 scale for each row of a key or value,
+ * k_scale / v_scale [pages, Hkv, page]; contiguous, 16-byte aligned.  page is 16, 32, 64,
+ * 128 or 256 positions.  tables (int32 [B, table_pages]) lists the pages of each
+ * sequence: its position p is row p % page of page tables[b][p / page].
+ *
+ * Tables, lengths, starts and counts are read on the GPU.  A negative length or count
+ * counts as 0.  An index that does not
+ * fit (a page outside of the pool that is needed, a length beyond the table, starts
+ * of groups that are no list of disjoint runs) reaches no memory: a row to write is
+ * dropped, a row to read is zero, results of the attention for that sequence or
+ * prefix are undefined, and fa_last_device_status reports FA_ERR_BAD_TABLE. */
+typedef struct {
+  int B, Hq, Hkv;  /* Hq: fa_cache_attention only */
+  int T;           /* write: new tokens a sequence; read: positions; attention: query rows */
+  int d, dv;       /* each 64 or 128 */
+  int pages, page; /* pages of the pool, positions of a page */
+  int table_pages; /* columns of tables; table_pages * page <= 2^30 */
+  int quantised;   /* 0: bf16, 1: e4m3 and scales */
+} fa_cache_dims;
+typedef struct {
+  void *K, *V;
+  float *k_scale, *v_scale; /* quantised only */
+} fa_kv_cache;
+
+/* Writes new tokens: K (bf16, [B, Hkv, T, d] with the strides k_stride in elements over
+ * batch, head and token, multiples of 8; channels contiguous) and V go to positions starts[b] ..
+ * starts[b] + counts[b] - 1 of each sequence (counts NULL: T tokens each; tokens from
+ * counts[b] on are padding).  Rows at other positions stay as they are.  Each position
+ * is written once: sequences whose tables share a page must not write the same row of it.
+ * Quantised: with a = max |x| of the row (2^-60 at least), code = e4m3(x * (448 / a)),
+ * scale = a * (1 / 448).  A row with a NaN or an infinity reads back as NaN throughout. */
+FA_API fa_status fa_cache_write(const fa_cache_dims* dims, const fa_kv_cache* cache, const void* K, const void* V,
+                                const long long* k_stride, const long long* v_stride, const int* tables,
+                                const int* starts, const int* counts, void* stream);
+
+/* Reads positions 0 .. T - 1 of each sequence back as contiguous bf16 K [B, Hkv, T, d] and
+ * V [B, Hkv, T, dv], code * scale rounded once; positions from lengths[b] on are zero. */
+FA_API fa_status fa_cache_read(const fa_cache_dims* dims, const fa_kv_cache* cache, const int* tables,
+                               const int* lengths, void* K, void* V, void* stream);
+
+/* Attention of the last T tokens of each sequence, which the cache holds already (any T;
+ * meant for few: a whole prompt goes through fa_forward).  Q [B, Hq, T, d], O [B, Hq, T, dv],
+ * L [B, Hq, T] as in fa_forward.  Row t stands at position p = lengths[b] - T + t and sees
+ * positions 0 .. p; a row with p < 0 is padding and sees nothing (O = 0, L = -inf).
+ *
+ * prefix (NULL: none): groups of sequences that share their first tokens.  Sequences
+ * starts[s] .. starts[s + 1] - 1 (int32 [groups + 1]; NULL for one group of all) see the
+ * lengths[s] positions of tables[s] ([groups, table_pages]) before their own, which
+ * then stand behind them.  A prefix's keys are read once for all its sequences.
+ *
+ * scores as for fa_scores (distances and window count over prefix and own keys
+ * together); scale <= 0 selects 1/sqrt(d).  With a cache of e4m3, weights are rounded to
+ * fp16 and values are taken to be below 2^60 in magnitude; values at masked places
+ * may be anything.  With bf16 weights are rounded to bf16, and values that one of a
+ * sequence's rows sees have to be finite for its other rows too.
+ *
+ * workspace: fa_cache_attention_workspace_bytes (it asks the current device for its
+ * SMs), 256-byte aligned, contents ignored. */
+typedef struct {
+  float scale, softcap;
+  const float* slopes; /* device, [Hq], or NULL */
+  int window;          /* 0: none */
+} fa_cache_scores;
+typedef struct {
+  int groups, table_pages;
+  const int *tables, *lengths, *starts;
+} fa_cache_prefix;
+FA_API size_t fa_cache_attention_workspace_bytes(const fa_cache_dims* dims, const fa_cache_prefix* prefix);
+FA_API fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache, const fa_cache_scores* scores,
+                                    const fa_cache_prefix* prefix, const void* Q, const int* tables, const int* lengths,
+                                    void* O, float* L, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 FA_API const char* fa_status_string(fa_status s);
 
 /* Synchronises `stream`, then reports (and clears) the device status word:
- * FA_ERR_TIMEOUT if a kernel gave up waiting since the last call, FA_ERR_CUDA
- * if the stream holds an asynchronous CUDA error, FA_OK otherwise. */
+ * FA_ERR_TIMEOUT if a kernel gave up waiting since the last call, FA_ERR_BAD_TABLE
+ * if a cache call met an index that does not fit, FA_ERR_CUDA if the stream holds an asynchronous CUDA error, FA_OK otherwise. */
 FA_API fa_status fa_last_device_status(void* stream);
 
 /* Number of kernel launches the last call of fa_forward, fa_backward (any form of

@@ -13,6 +13,9 @@ Entry points mirror the C ABI:
     fa_last_device_status()
     fa_rotary(Q, K, positions, inv_freq, ...)                     -> (Qr, Kr)
     fa_rotary_backward(dQr, dKr, positions, inv_freq, ...)        -> (dQ, dK)
+    fa_cache_write(cache, K, V, tables, starts, counts=None)      (a KVCache: pages in bf16 or e4m3)
+    fa_cache_read(cache, tables, lengths, T)                      -> (K, V)
+    fa_cache_attention(Q, cache, tables, lengths, ...)            -> (O, L)
 plus ``FlashAttention`` (a torch.autograd.Function that keeps only Q, K, V, O
 and L for the backward pass) and ``attention`` (its functional form), and
 ``rotary`` (multi-axis rotary positions of Q and K, differentiable).
@@ -41,8 +44,9 @@ EXPORTED_SYMBOLS = ("fa_forward", "fa_backward", "fa_backward_stages", "fa_backw
                     "fa_backward_workspace_min_bytes", "fa_backward_noalloc", "fa_status_string",
                     "fa_last_device_status", "fa_last_launch_count", "fa_rotary", "fa_mask_plan_bytes", "fa_mask_plan",
                     "fa_forward_scored", "fa_backward_scored", "fa_forward_scored_workspace_bytes",
-                    "fa_backward_scored_workspace_bytes")
-FA_ERR_SCRATCH_TOO_SMALL = 5
+                    "fa_backward_scored_workspace_bytes", "fa_cache_write", "fa_cache_read", "fa_cache_attention",
+                    "fa_cache_attention_workspace_bytes")
+FA_ERR_SCRATCH_TOO_SMALL, FA_ERR_BAD_TABLE = 5, 6
 FA_NOALLOC_SCRATCH_BYTES = 32 << 20
 FA_BWD_PRE, FA_BWD_MAIN, FA_BWD_CAST, FA_BWD_ALL = 1, 2, 4, 7
 
@@ -68,6 +72,24 @@ class FaRotaryDims(ctypes.Structure):
         [("section", ctypes.c_int * 4)] + \
         [(n, ctypes.c_longlong * 3) for n in ("q_stride", "k_stride", "qo_stride", "ko_stride")] + \
         [("pos_axis_stride", ctypes.c_longlong), ("pos_batch_stride", ctypes.c_longlong)]
+
+
+class FaCacheDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "Hq", "Hkv", "T", "d", "dv", "pages", "page", "table_pages", "quantised")]
+
+
+class FaKVCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("K", "V", "k_scale", "v_scale")]
+
+
+class FaCacheScores(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("window", ctypes.c_int)]
+
+
+class FaCachePrefix(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int), ("table_pages", ctypes.c_int), ("tables", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("starts", ctypes.c_void_p)]
 
 
 _HERE = contextlib.nullcontext()
@@ -126,6 +148,17 @@ def load(path: str | None = None):
             lib.fa_backward_scored.restype = ctypes.c_int
             lib.fa_rotary.argtypes = [ctypes.POINTER(FaRotaryDims), vp, vp, vp, vp, vp, vp, ctypes.c_int, vp]
             lib.fa_rotary.restype = ctypes.c_int
+            cd, cc, cp = ctypes.POINTER(FaCacheDims), ctypes.POINTER(FaKVCache), ctypes.POINTER(FaCachePrefix)
+            strides = ctypes.POINTER(ctypes.c_longlong)
+            lib.fa_cache_write.argtypes = [cd, cc, vp, vp, strides, strides, vp, vp, vp, vp]
+            lib.fa_cache_write.restype = ctypes.c_int
+            lib.fa_cache_read.argtypes = [cd, cc, vp, vp, vp, vp, vp]
+            lib.fa_cache_read.restype = ctypes.c_int
+            lib.fa_cache_attention_workspace_bytes.argtypes = [cd, cp]
+            lib.fa_cache_attention_workspace_bytes.restype = ctypes.c_size_t
+            lib.fa_cache_attention.argtypes = [cd, cc, ctypes.POINTER(FaCacheScores), cp, vp, vp, vp, vp, vp, vp,
+                                               ctypes.c_size_t, vp]
+            lib.fa_cache_attention.restype = ctypes.c_int
             _lib = lib
     return _lib
 
@@ -465,4 +498,6 @@ def attention(Q, K, V, causal=False, scale=None, window=0, softcap=0.0, slopes=N
     return FlashAttention.apply(Q, K, V, causal, scale, window, softcap, slopes, mask)
 
 
+from .cache import (KVCache, fa_cache_attention, fa_cache_attention_workspace_bytes, fa_cache_read,  # noqa: E402
+                    fa_cache_write)
 from .rotary import fa_rotary, fa_rotary_backward, rotary  # noqa: E402

@@ -1,0 +1,220 @@
+"""The paged key/value cache and attention over it (fa_cache_* in include/fa.h):
+argument checks and marshalling.
+
+    KVCache(K, V, k_scale=None, v_scale=None), KVCache.empty(pages, Hkv, page, d, ...)
+    fa_cache_write(cache, K, V, tables, starts, counts=None)
+    fa_cache_read(cache, tables, lengths, T)                               -> (K, V)
+    fa_cache_attention(Q, cache, tables, lengths, ..., prefix=None)        -> (O, L)
+    fa_cache_attention_workspace_bytes(Q, cache, tables, prefix=None)
+
+A program keeps a pool of pages (KVCache) for each layer, and for all of them the
+tables: int32 [B, n], the pages of each sequence in their order.  After the rotary
+step the new tokens' K and V are written behind what is cached, and their Q
+attends over it:
+
+    fa_cache_write(cache, K, V, tables, lengths)           # K, V [B, Hkv, T, d]: T new tokens each
+    O, L = fa_cache_attention(Q, cache, tables, lengths + T)
+
+Tables, lengths, starts and counts stay on the GPU and are not looked at by the host;
+an index in them that does not fit reaches no memory, and fa_last_device_status
+reports FA_ERR_BAD_TABLE.  The calls have no gradient.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+import tiled_attention_05_gb300 as _fa
+
+PAGE_SIZES = (16, 32, 64, 128, 256)
+
+
+class KVCache:
+    """Pools of pages: K [pages, Hkv, page, d] and V [pages, Hkv, page, dv], both bf16 or both
+    float8_e4m3fn, the latter with fp32 scales [pages, Hkv, page].  Holds the tensors it is
+    given and copies nothing."""
+
+    def __init__(self, K, V, k_scale=None, v_scale=None):
+        if K.dim() != 4 or V.dim() != 4 or K.shape[:3] != V.shape[:3]:
+            raise ValueError(f"K and V must be [pages, Hkv, page, d] and [pages, Hkv, page, dv], got {tuple(K.shape)} and "
+                             f"{tuple(V.shape)}")
+        if K.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError("a cache is bfloat16 or float8_e4m3fn")
+        self.quantised = K.dtype == torch.float8_e4m3fn
+        if (k_scale is None) != (not self.quantised) or (v_scale is None) != (not self.quantised):
+            raise ValueError("float8_e4m3fn caches have k_scale and v_scale, bfloat16 caches have none")
+        pages, Hkv, page, _ = K.shape
+        if page not in PAGE_SIZES:
+            raise ValueError(f"a page has {PAGE_SIZES} positions, not {page}")
+        specs = [(K, "K", K.shape, K.dtype), (V, "V", V.shape, K.dtype)]
+        if self.quantised:
+            specs += [(k_scale, "k_scale", (pages, Hkv, page), torch.float32),
+                      (v_scale, "v_scale", (pages, Hkv, page), torch.float32)]
+        self.device = K.device
+        _fa._check_all(self.device, specs)
+        self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
+        self._pools = ctypes.byref(_fa.FaKVCache(K.data_ptr(), V.data_ptr(), _fa._ptr(k_scale), _fa._ptr(v_scale)))
+
+    @classmethod
+    def empty(cls, pages, Hkv, page, d, dv=None, dtype=torch.bfloat16, device="cuda"):
+        """A new cache of zeros."""
+        quantised = dtype == torch.float8_e4m3fn
+        K, V = (torch.zeros(pages, Hkv, page, w, dtype=torch.uint8 if quantised else dtype, device=device)
+                for w in (d, d if dv is None else dv))
+        if not quantised:
+            return cls(K, V)
+        scales = (torch.zeros(pages, Hkv, page, device=device) for _ in range(2))
+        return cls(K.view(dtype), V.view(dtype), *scales)
+
+    def _dims(self, B, Hq, T, table_pages):
+        pages, Hkv, page, d = self.K.shape
+        return _fa.FaCacheDims(B, Hq, Hkv, T, d, self.V.shape[3], pages, page, table_pages, self.quantised)
+
+
+def _index(t, name, shape, device):
+    if t.dim() != len(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {list(shape)}")
+    _fa._check_all(device, [(t, name, tuple(n if want is None else want for n, want in zip(t.shape, shape)), torch.int32)])
+
+
+def _new_rows(x, name, shape, device):
+    """Strides (batch, head, token) of a [B, Hkv, T, w] operand, checked."""
+    if tuple(x.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {shape}")
+    if not x.is_cuda or x.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a CUDA {torch.bfloat16} tensor")
+    if x.get_device() != device.index:
+        raise ValueError(f"{name} is on {x.device}, expected {device} (all tensors on one GPU)")
+    sb, sh, st, sd = x.stride()
+    if x.numel() and (sd != 1 or (sb | sh | st) & 7 or x.data_ptr() & 15):
+        raise ValueError(f"{name} needs contiguous channels, strides of a multiple of 8 elements and 16-byte alignment")
+    return (ctypes.c_longlong * 3)(*((sb, sh, st) if x.numel() else (0, 0, 0)))
+
+
+def fa_cache_write(cache: KVCache, K, V, tables, starts, counts=None, stream=None):
+    """Writes tokens K [B, Hkv, T, d] and V [B, Hkv, T, dv] (bf16; views as fa_rotary takes
+    them) to positions starts[b] .. starts[b] + T - 1 of each sequence, quantised if the
+    cache is; with counts [B] only the first counts[b] tokens of each."""
+    if K.dim() != 4:
+        raise ValueError("K, V must be [B, Hkv, T, d]")
+    B, _, T, _ = K.shape
+    _, Hkv, _, d = cache.K.shape
+    device = cache.device
+    ks = _new_rows(K, "K", (B, Hkv, T, d), device)
+    vs = _new_rows(V, "V", (B, Hkv, T, cache.V.shape[3]), device)
+    _index(tables, "tables", (B, None), device)
+    _index(starts, "starts", (B,), device)
+    if counts is not None:
+        _index(counts, "counts", (B,), device)
+    dims, handle = cache._dims(B, 0, T, tables.shape[1]), _fa._stream_ptr(stream, device)
+    with _fa._under(stream, device):
+        code = _fa.load().fa_cache_write(ctypes.byref(dims), cache._pools, K.data_ptr(), V.data_ptr(), ks, vs,
+                                         tables.data_ptr(), starts.data_ptr(), _fa._ptr(counts), handle)
+    _fa._raise(code, "fa_cache_write")
+
+
+def fa_cache_read(cache: KVCache, tables, lengths, T: int, K=None, V=None, stream=None):
+    """K [B, Hkv, T, d], V [B, Hkv, T, dv] (bf16) = positions 0 .. T - 1 of each sequence, zero
+    from lengths[b] on.  Optional preallocated K / V are written in place."""
+    device = cache.device
+    _index(tables, "tables", (None, None), device)
+    B, n = tables.shape
+    _index(lengths, "lengths", (B,), device)
+    _, Hkv, _, d = cache.K.shape
+    T, dv, bf, given = int(T), cache.V.shape[3], torch.bfloat16, (K, V)
+    if T < 0:
+        raise ValueError(f"T is {T}")
+    specs = [(t, name, (B, Hkv, T, w), bf) for t, name, w in ((K, "K", d), (V, "V", dv)) if t is not None]
+    _fa._check_all(device, specs)
+    dims, handle = cache._dims(B, 0, T, n), _fa._stream_ptr(stream, device)
+    with _fa._under(stream, device):
+        if K is None:
+            K = torch.empty((B, Hkv, T, d), dtype=bf, device=device)
+        if V is None:
+            V = torch.empty((B, Hkv, T, dv), dtype=bf, device=device)
+        code = _fa.load().fa_cache_read(ctypes.byref(dims), cache._pools, tables.data_ptr(), lengths.data_ptr(),
+                                        K.data_ptr(), V.data_ptr(), handle)
+    if stream is not None:
+        _fa._hand_over(device, (K, V), given)
+    _fa._raise(code, "fa_cache_read")
+    return K, V
+
+
+def _prefix_of(prefix, B, device):
+    """The fa_cache_prefix of a call (None without one), checked."""
+    if prefix is None:
+        return None
+    tables, lengths, starts = prefix if len(prefix) == 3 else (*prefix, None)
+    _index(tables, "prefix tables", (None, None), device)
+    groups, n = tables.shape
+    _index(lengths, "prefix lengths", (groups,), device)
+    if starts is not None:
+        _index(starts, "prefix starts", (groups + 1,), device)
+    elif groups != 1:
+        raise ValueError(f"{groups} prefixes need starts [{groups + 1}], the first sequence of each group")
+    return _fa.FaCachePrefix(groups, n, tables.data_ptr(), lengths.data_ptr(), _fa._ptr(starts))
+
+
+def _attention_dims(Q, cache, tables, prefix):
+    if Q.dim() != 4:
+        raise ValueError("Q must be [B, Hq, T, d]")
+    B, Hq, T, d = Q.shape
+    if d != cache.K.shape[3]:
+        raise ValueError(f"Q has shape {tuple(Q.shape)}, the cache's keys have {cache.K.shape[3]} channels")
+    _index(tables, "tables", (B, None), cache.device)
+    return cache._dims(B, Hq, T, tables.shape[1]), _prefix_of(prefix, B, cache.device)
+
+
+def fa_cache_attention_workspace_bytes(Q, cache: KVCache, tables, prefix=None) -> int:
+    """The workspace that fa_cache_attention needs (what it allocates without one)."""
+    dims, pre = _attention_dims(Q, cache, tables, prefix)
+    with _fa._on(cache.device):
+        return int(_fa.load().fa_cache_attention_workspace_bytes(ctypes.byref(dims), pre))
+
+
+def fa_cache_attention(Q, cache: KVCache, tables, lengths, scale: float | None = None, window: int = 0,
+                       softcap: float = 0.0, slopes=None, prefix=None, O=None, L=None, workspace=None, stream=None):
+    """O [B, Hq, T, dv], L [B, Hq, T] = attention of the last T tokens of each sequence, Q
+    [B, Hq, T, d], over the lengths[b] positions that the cache holds of it (theirs among
+    them): row t sees positions up to lengths[b] - T + t, and nothing where that is
+    negative (O = 0, L = -inf).  ``scale``, ``window``, ``softcap`` and ``slopes`` as in
+    fa_forward.
+
+    ``prefix=(tables [S, n], lengths [S], starts [S + 1])``: sequences starts[s] ..
+    starts[s + 1] - 1 share the lengths[s] positions of tables[s] in front of their own;
+    their keys are read once for all of them.  Without starts one prefix serves the
+    whole batch."""
+    dims, pre = _attention_dims(Q, cache, tables, prefix)
+    device, bf, f32 = cache.device, torch.bfloat16, torch.float32
+    B, Hq, T, dv = dims.B, dims.Hq, dims.T, dims.dv
+    specs = [(Q, "Q", Q.shape, bf), (lengths, "lengths", (B,), torch.int32)]
+    if O is not None:
+        specs.append((O, "O", (B, Hq, T, dv), bf))
+    if L is not None:
+        specs.append((L, "L", (B, Hq, T), f32))
+    if slopes is not None:
+        if slopes.requires_grad:
+            raise ValueError("slopes have no gradient here; detach them")
+        specs.append((slopes, "slopes", (Hq,), f32))
+    _fa._check_all(device, specs)
+    lib, ref, given = _fa.load(), ctypes.byref(dims), (O, L)
+    scores = _fa.FaCacheScores(float(scale or 0.0), float(softcap or 0.0), _fa._ptr(slopes), int(window))
+    handle = _fa._stream_ptr(stream, device)
+    with _fa._under(stream, device):
+        if O is None:
+            O = torch.empty((B, Hq, T, dv), dtype=bf, device=device)
+        if L is None:
+            L = torch.empty((B, Hq, T), dtype=f32, device=device)
+        if workspace is None:
+            nbytes = lib.fa_cache_attention_workspace_bytes(ref, pre)
+            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+        elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+        code = lib.fa_cache_attention(ref, cache._pools, ctypes.byref(scores), pre, Q.data_ptr(), tables.data_ptr(),
+                                      lengths.data_ptr(), O.data_ptr(), L.data_ptr(), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), handle)
+    if stream is not None:
+        _fa._hand_over(device, (O, L), given)
+    _fa._raise(code, "fa_cache_attention")
+    return O, L

@@ -9,6 +9,7 @@
 #include <utility>
 
 #include "fa_internal.h"
+#include "sm103_ptx.cuh"
 
 namespace {
 
@@ -296,16 +297,18 @@ const char* fa_status_string(fa_status s) {
       return "ok";
     case FA_ERR_INVALID_ARG:
       return "invalid argument (null or misaligned pointer, negative size, Hq not a multiple of Hkv, "
-             "bad causal flag, window, scale, cap or prefix, or workspace too small)";
+             "bad causal flag, window, scale, cap, prefix or stride, or workspace too small)";
     case FA_ERR_UNSUPPORTED:
-      return "unsupported shape (d and dv must each be 64 or 128, rotary channels a multiple of 16; sizes within the "
-             "grid limits)";
+      return "unsupported shape (d and dv must each be 64 or 128, rotary channels a multiple of 16, a cache's page "
+             "16 to 256 and a power of two; sizes within the grid limits)";
     case FA_ERR_CUDA:
       return "CUDA error while encoding tensor maps or launching kernels";
     case FA_ERR_TIMEOUT:
       return "a kernel gave up waiting on an on-chip barrier; outputs are undefined";
     case FA_ERR_SCRATCH_TOO_SMALL:
       return "problem needs more scratch than fa_backward_noalloc's fixed array holds; use fa_backward";
+    case FA_ERR_BAD_TABLE:
+      return "a cache call met a page, length or group that does not fit the pool or its tables";
   }
   return "unknown status";
 }
@@ -319,7 +322,7 @@ fa_status fa_last_device_status(void* stream) {
   if (cudaMemcpyAsync(&v, w, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess) return FA_ERR_CUDA;
   if (cudaMemsetAsync(w, 0, sizeof(int), st) != cudaSuccess) return FA_ERR_CUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return FA_ERR_CUDA;
-  return v == 0 ? FA_OK : FA_ERR_TIMEOUT;
+  return v == 0 ? FA_OK : v == fa_ptx::DEV_BAD_TABLE ? FA_ERR_BAD_TABLE : FA_ERR_TIMEOUT;
 }
 
 int fa_last_launch_count(void) { return t_last_launches; }

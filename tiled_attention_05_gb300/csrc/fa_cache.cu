@@ -1,0 +1,524 @@
+// The key/value cache: writing new rows into its pages, reading them back, the join of
+// the attention's parts, and the C ABI of all three (fa_cache_* in include/fa.h).
+//
+// Write.  A row x of d values becomes e4m3 codes and one scale: with a = max |x| (2^-60
+// at least), code = e4m3(x * (448 / a)), scale = a * (1 / 448): two fp32 roundings
+// before the one to e4m3.  A row with a NaN or an infinity gets codes 0 and scale NaN,
+// so that its bytes are finite wherever its weight is 0.  bf16 caches take the row as
+// it is.  Read back: bf16(code * scale).
+//
+// Mapping.  Both are bound by HBM: each byte is read once and written once.  A thread
+// owns 8 channels of a row (16 bytes in bf16, 8 in e4m3), the d / 8 lanes of a row agree
+// on its maximum by shuffles, and a thread has four rows in flight.
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "fa_cache_internal.h"
+#include "sm103_ptx.cuh"
+
+using namespace fa_ptx;
+using fa::CacheParams;
+using fa::CacheParts;
+using fa::kCacheRows;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;  // rows in flight per thread
+constexpr float kE4m3Max = 448.f, kLeast = 0x1p-60f;
+
+struct PageParams {
+  const int *tables, *lengths;  // (write: the counts, or NULL)
+  const int* starts;            // write
+  int B, H, T, cols, pages, page_log2;
+  int* status;
+  struct Side {  // K or V
+    uint8_t* pool;
+    float* scale;
+    uint16_t* rows;          // the new rows, or the result
+    long long sb, sh, st;    // their strides (elements)
+  } side[2];
+  long long units;  // B * H * T
+};
+
+// Row of the pools for position `pos` of sequence b and head h; -1 where the table has
+// none.  (T = 2^31 positions do not meet: the capacity is below 2^30.)
+__device__ __forceinline__ long long pool_row(const PageParams& p, int b, int h, long long pos) {
+  const long long col = pos >> p.page_log2;
+  int id = -1;
+  if (pos >= 0 && col < p.cols) id = __ldg(p.tables + (long long)b * p.cols + col);
+  if ((unsigned)id >= (unsigned)p.pages) {
+    fa::cache_bad(p.status);
+    return -1;
+  }
+  return (((long long)id * p.H + h) << p.page_log2) | (pos & ((1 << p.page_log2) - 1));
+}
+
+struct Unit {
+  int b, h, t;
+};
+__device__ __forceinline__ Unit unit_of(const PageParams& p, long long n) {
+  const long long bh = n / p.T;
+  Unit u;
+  u.t = (int)(n - bh * p.T);
+  u.b = (int)(bh / p.H);
+  u.h = (int)(bh - (long long)u.b * p.H);
+  return u;
+}
+
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 x, y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\t"
+      "mov.b32 %0, {x, y};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// LANES threads hold a row (d / 8).
+template <int LANES, bool Q8>
+__device__ __forceinline__ void write_rows(const PageParams& p, const PageParams::Side& s) {
+  constexpr int ROWS = kThreads / LANES;
+  const int lane = threadIdx.x % LANES;
+  const long long n0 = (long long)blockIdx.x * (ROWS * kUnroll) + threadIdx.x / LANES;
+  uint4 x[kUnroll];
+  long long to[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const long long n = n0 + u * ROWS;
+    to[u] = -1;
+    x[u] = make_uint4(0, 0, 0, 0);
+    if (n >= p.units) continue;
+    const Unit at = unit_of(p, n);
+    if (p.lengths && at.t >= __ldg(p.lengths + at.b)) continue;  // a padding token
+    to[u] = pool_row(p, at.b, at.h, (long long)__ldg(p.starts + at.b) + at.t);
+    x[u] = *reinterpret_cast<const uint4*>(s.rows + at.b * s.sb + at.h * s.sh + at.t * s.st + lane * 8);
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+    if constexpr (Q8) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+#pragma unroll
+      for (int o = LANES / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+      const bool finite = top < 0x7f80u;
+      const float a = fmaxf(__uint_as_float(top << 16), kLeast);
+      const float f = finite ? __fdiv_rn(kE4m3Max, a) : 0.f;
+      uint2 c;
+      c.x = codes4(bf_lo(w[0]) * f, bf_hi(w[0]) * f, bf_lo(w[1]) * f, bf_hi(w[1]) * f);
+      c.y = codes4(bf_lo(w[2]) * f, bf_hi(w[2]) * f, bf_lo(w[3]) * f, bf_hi(w[3]) * f);
+      if (!finite) c = make_uint2(0, 0);
+      if (to[u] >= 0) {
+        *reinterpret_cast<uint2*>(s.pool + to[u] * (LANES * 8) + lane * 8) = c;
+        if (lane == 0) s.scale[to[u]] = finite ? a * (1.f / kE4m3Max) : __uint_as_float(0x7fffffffu);
+      }
+    } else if (to[u] >= 0) {
+      *reinterpret_cast<uint4*>(s.pool + to[u] * (LANES * 16) + lane * 16) = x[u];
+    }
+  }
+}
+
+template <int KL, int VL, bool Q8>
+__global__ void __launch_bounds__(kThreads) fa_cache_write_kernel(const PageParams p) {
+  grid_next();
+  grid_previous();
+  if (blockIdx.y == 0)
+    write_rows<KL, Q8>(p, p.side[0]);
+  else
+    write_rows<VL, Q8>(p, p.side[1]);
+}
+
+template <int LANES, bool Q8>
+__device__ __forceinline__ void read_rows(const PageParams& p, const PageParams::Side& s) {
+  constexpr int ROWS = kThreads / LANES;
+  const int lane = threadIdx.x % LANES;
+  const long long n0 = (long long)blockIdx.x * (ROWS * kUnroll) + threadIdx.x / LANES;
+  uint4 x[kUnroll];
+  float f[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const long long n = n0 + u * ROWS;
+    x[u] = make_uint4(0, 0, 0, 0);
+    f[u] = 0.f;
+    if (n >= p.units) continue;
+    const Unit at = unit_of(p, n);
+    if (at.t >= __ldg(p.lengths + at.b)) continue;
+    const long long from = pool_row(p, at.b, at.h, at.t);
+    if (from < 0) continue;
+    if constexpr (Q8) {
+      const uint2 c = *reinterpret_cast<const uint2*>(s.pool + from * (LANES * 8) + lane * 8);
+      x[u].x = c.x, x[u].y = c.y;
+      f[u] = __ldg(s.scale + from);
+    } else {
+      x[u] = *reinterpret_cast<const uint4*>(s.pool + from * (LANES * 16) + lane * 16);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const long long n = n0 + u * ROWS;
+    if (n >= p.units) continue;
+    uint4 out = x[u];
+    if constexpr (Q8) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t two = (k < 2 ? x[u].x : x[u].y) >> (16 * (k & 1));
+        uint32_t h;
+        asm("{\n\t.reg .b16 c, u;\n\tmov.b32 {c, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(two));
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+            : "=f"(v[2 * k]), "=f"(v[2 * k + 1])
+            : "r"(h));
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= f[u];
+      out = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    }
+    *reinterpret_cast<uint4*>(s.rows + n * (LANES * 8) + lane * 8) = out;
+  }
+}
+
+template <int KL, int VL, bool Q8>
+__global__ void __launch_bounds__(kThreads) fa_cache_read_kernel(const PageParams p) {
+  grid_next();
+  grid_previous();
+  if (blockIdx.y == 0)
+    read_rows<KL, Q8>(p, p.side[0]);
+  else
+    read_rows<VL, Q8>(p, p.side[1]);
+}
+
+// ---------------------------------------------------------------- join
+// Adds up the parts of each output row, in their order: those of its own keys and those
+// of its group's prefix.  WARPS warps take a row (1, or 4 where there are few rows: a
+// long sequence alone has tens of parts).
+template <int DV, int WARPS>
+__global__ void __launch_bounds__(128) fa_cache_join_kernel(const CacheParams p) {
+  constexpr int CH = DV / 32;
+  __shared__ float s_o[4][DV], s_l[4];
+  grid_next();
+  grid_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long out = (long long)blockIdx.x * (4 / WARPS) + warp / WARPS, rows = (long long)p.B * p.Hq * p.T;
+  if (out >= rows) return;  // (with WARPS 4 a block has one row)
+  const int sub = warp % WARPS;
+  const int t = (int)(out % p.T), hq = (int)(out / p.T % p.Hq), b = (int)(out / p.T / p.Hq);
+  const int h = hq / p.G, g = hq - h * p.G;
+  const long long per = p.head[p.S + p.B].work;
+  const CacheParts own = fa::cache_parts(p.head[p.S + b], p.G * p.T, h, g * p.T + t, per);
+  CacheParts pre = {0, 0, 0};
+  if (p.S) {
+    int group = -1, first = 0, seqs = 0;
+    for (int s0 = 0; s0 < p.S; s0 += 32) {
+      const int s = s0 + lane;
+      bool in = false;
+      int a = 0, z = 0;
+      if (s < p.S) {
+        a = p.p_starts ? __ldg(p.p_starts + s) : 0;
+        z = p.p_starts ? __ldg(p.p_starts + s + 1) : p.B;
+        in = a <= b && b < z && p.head[s].chunks > 0;
+      }
+      const unsigned found = __ballot_sync(~0u, in);
+      if (found) {
+        const int src = __ffs(found) - 1;
+        group = s0 + src;
+        first = __shfl_sync(~0u, a, src);
+        seqs = __shfl_sync(~0u, z, src) - first;
+        break;
+      }
+    }
+    if (group >= 0)
+      pre = fa::cache_parts(p.head[group], seqs * p.G * p.T, h, (b - first) * p.G * p.T + g * p.T + t, per);
+  } else if (own.n == 1) {
+    return;  // a whole item, stored by its CTA
+  }
+  const int n = own.n + pre.n;
+  auto row_at = [&](int i) {
+    return i < pre.n ? (pre.slot + i) * kCacheRows + pre.row : (own.slot + i - pre.n) * kCacheRows + own.row;
+  };
+  float top = -INFINITY;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, p.ml[row_at(i) * 2]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  float sum = 0.f, acc[CH] = {};
+#pragma unroll 4
+  for (int i = sub; i < n; i += WARPS) {
+    const long long r = row_at(i);
+    const float2 ml = *reinterpret_cast<const float2*>(p.ml + r * 2);
+    float v[CH];
+    if constexpr (CH == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p.part + r * DV + lane * CH);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(p.part + r * DV + lane * CH);
+      v[0] = x.x, v[1] = x.y;
+    }
+    const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - top);  // (without a finite reference, O is 0 or NaN)
+    sum += ml.y * f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) acc[k] += v[k] * f;
+  }
+  if constexpr (WARPS > 1) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) s_o[sub][lane * CH + k] = acc[k];
+    if (lane == 0) s_l[sub] = sum;
+    __syncthreads();
+    if (sub) return;
+    sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) acc[k] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      sum += s_l[w];
+#pragma unroll
+      for (int k = 0; k < CH; ++k) acc[k] += s_o[w][lane * CH + k];
+    }
+  }
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t w[CH / 2];
+#pragma unroll
+  for (int k = 0; k < CH; k += 2) w[k / 2] = pack_bf16x2(acc[k] * f, acc[k + 1] * f);
+  uint16_t* dst = p.O + out * DV + lane * CH;
+  if constexpr (CH == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(dst) = w[0];
+  if (lane == 0) p.L[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// ---------------------------------------------------------------- host
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Sizes that all three calls share.
+fa_status check_cache_dims(const fa_cache_dims* dims) {
+  if (!dims) return FA_ERR_INVALID_ARG;
+  const fa_cache_dims& z = *dims;
+  if (z.B < 0 || z.Hkv < 0 || z.T < 0 || z.d < 1 || z.dv < 1 || z.pages < 0 || z.page < 1 || z.table_pages < 0)
+    return FA_ERR_INVALID_ARG;
+  if (z.quantised != 0 && z.quantised != 1) return FA_ERR_INVALID_ARG;
+  if ((z.d != 64 && z.d != 128) || (z.dv != 64 && z.dv != 128)) return FA_ERR_UNSUPPORTED;
+  if (z.page < 16 || z.page > 256 || (z.page & (z.page - 1))) return FA_ERR_UNSUPPORTED;
+  if ((long long)z.table_pages * z.page > (1 << 30) || z.T > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  if ((long long)z.B * z.Hkv > INT_MAX || (long long)z.pages * z.Hkv * z.page > (1LL << 48)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+fa_status check_pools(const fa_cache_dims& z, const fa_kv_cache* c) {
+  if (!c) return FA_ERR_INVALID_ARG;
+  if (z.pages == 0 || z.Hkv == 0) return FA_OK;
+  if (!c->K || !c->V || !aligned(c->K, 16) || !aligned(c->V, 16)) return FA_ERR_INVALID_ARG;
+  if (z.quantised && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+int log2_of(int page) {
+  int n = 0;
+  while ((1 << n) < page) ++n;
+  return n;
+}
+
+PageParams page_params(const fa_cache_dims& z, const fa_kv_cache& c, const int* tables, const int* lengths) {
+  PageParams p = {};
+  p.tables = tables;
+  p.lengths = lengths;
+  p.B = z.B;
+  p.H = z.Hkv;
+  p.T = z.T;
+  p.cols = z.table_pages;
+  p.pages = z.pages;
+  p.page_log2 = log2_of(z.page);
+  p.side[0].pool = static_cast<uint8_t*>(c.K);
+  p.side[1].pool = static_cast<uint8_t*>(c.V);
+  p.side[0].scale = c.k_scale;
+  p.side[1].scale = c.v_scale;
+  p.units = (long long)z.B * z.Hkv * z.T;
+  p.status = fa::device_status_word();
+  return p;
+}
+
+template <typename Kernel>
+fa_status launch_pages(Kernel kernel, const fa_cache_dims& z, const PageParams& p, void* stream) {
+  // blocks of the wider rows; the narrower side needs half as many
+  const int lanes = (z.d > z.dv ? z.d : z.dv) / 8;
+  const long long per = (long long)(kThreads / lanes) * kUnroll, blocks = (p.units + per - 1) / per;
+  if (blocks > INT_MAX) return FA_ERR_UNSUPPORTED;
+  return fa::launch_next(kernel, dim3((unsigned)blocks, 2), kThreads, 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+// Checks what the attention's sizes have to be besides; on success its shape.
+fa_status attn_shape(const fa_cache_dims& z, const fa_cache_prefix* pre, fa::CacheShape* s) {
+  if (z.Hq < 0 || (z.Hq > 0 && (z.Hkv < 1 || z.Hq % z.Hkv))) return FA_ERR_INVALID_ARG;
+  const int S = pre ? pre->groups : 0, p_cols = pre ? pre->table_pages : 0;
+  if (S < 0 || p_cols < 0) return FA_ERR_INVALID_ARG;
+  if ((long long)p_cols * z.page > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  // rows are counted in 32 bits, those of a whole group among them
+  const long long rows = z.Hkv ? (long long)(z.Hq / z.Hkv) * z.T : 0;
+  if ((long long)z.B * z.Hq > INT_MAX || rows * z.B > (1 << 30) || (long long)z.B * z.Hq * z.T > INT_MAX)
+    return FA_ERR_UNSUPPORTED;
+  const int sms = fa::sm_count() > 0 ? fa::sm_count() : 1;  // (without a device the launch fails)
+  *s = fa::cache_shape(z.B, z.Hkv, rows, z.dv, z.quantised, (long long)z.table_pages * z.page, S, (long long)p_cols * z.page, sms);
+  return s->items > (1 << 30) || (long long)S + z.B > (1 << 30) ? FA_ERR_UNSUPPORTED : FA_OK;
+}
+
+}  // namespace
+
+namespace fa {
+
+template <int DV>
+static cudaError_t launch_join(const CacheParams& p, cudaStream_t stream) {
+  const long long rows = (long long)p.B * p.Hq * p.T;
+  // Four warps a row as long as that fills the GPU at most a few times over.
+  if (rows <= 2048) return launch_next(fa_cache_join_kernel<DV, 4>, dim3((unsigned)rows), 128, 0, stream, p);
+  return launch_next(fa_cache_join_kernel<DV, 1>, dim3((unsigned)((rows + 3) / 4)), 128, 0, stream, p);
+}
+
+cudaError_t launch_cache_join(const CacheParams& p, int dv, cudaStream_t stream) {
+  return dv == 64 ? launch_join<64>(p, stream) : launch_join<128>(p, stream);
+}
+
+}  // namespace fa
+
+extern "C" {
+
+fa_status fa_cache_write(const fa_cache_dims* dims, const fa_kv_cache* cache, const void* K, const void* V,
+                         const long long* k_stride, const long long* v_stride, const int* tables, const int* starts,
+                         const int* counts, void* stream) {
+  fa_status e = check_cache_dims(dims);
+  if (e != FA_OK || (e = check_pools(*dims, cache)) != FA_OK) return e;
+  if (!k_stride || !v_stride) return FA_ERR_INVALID_ARG;
+  const fa_cache_dims& z = *dims;
+  if ((long long)z.B * z.Hkv * z.T == 0) return FA_OK;
+  for (int k = 0; k < 3; ++k)
+    if (k_stride[k] % 8 || v_stride[k] % 8) return FA_ERR_INVALID_ARG;
+  if (!K || !V || !aligned(K, 16) || !aligned(V, 16) || !starts || !aligned(starts, 4) || !aligned(counts, 4) ||
+      (z.table_pages && !tables) || !aligned(tables, 4))
+    return FA_ERR_INVALID_ARG;
+  PageParams p = page_params(z, *cache, tables, counts);
+  if (!p.status) return FA_ERR_CUDA;
+  p.starts = starts;
+  const void* rows[2] = {K, V};
+  const long long* strides[2] = {k_stride, v_stride};
+  for (int k = 0; k < 2; ++k) {
+    p.side[k].rows = static_cast<uint16_t*>(const_cast<void*>(rows[k]));
+    p.side[k].sb = strides[k][0];
+    p.side[k].sh = strides[k][1];
+    p.side[k].st = strides[k][2];
+  }
+  auto pick = [&](auto q8) {
+    constexpr bool Q = decltype(q8)::value;
+    return z.d == 64 ? (z.dv == 64 ? fa_cache_write_kernel<8, 8, Q> : fa_cache_write_kernel<8, 16, Q>)
+                     : (z.dv == 64 ? fa_cache_write_kernel<16, 8, Q> : fa_cache_write_kernel<16, 16, Q>);
+  };
+  return launch_pages(z.quantised ? pick(std::true_type{}) : pick(std::false_type{}), z, p, stream);
+}
+
+fa_status fa_cache_read(const fa_cache_dims* dims, const fa_kv_cache* cache, const int* tables, const int* lengths,
+                        void* K, void* V, void* stream) {
+  fa_status e = check_cache_dims(dims);
+  if (e != FA_OK || (e = check_pools(*dims, cache)) != FA_OK) return e;
+  const fa_cache_dims& z = *dims;
+  if ((long long)z.B * z.Hkv * z.T == 0) return FA_OK;
+  if (!K || !V || !aligned(K, 16) || !aligned(V, 16) || !lengths || !aligned(lengths, 4) || (z.table_pages && !tables) ||
+      !aligned(tables, 4))
+    return FA_ERR_INVALID_ARG;
+  PageParams p = page_params(z, *cache, tables, lengths);
+  if (!p.status) return FA_ERR_CUDA;
+  p.side[0].rows = static_cast<uint16_t*>(K);
+  p.side[1].rows = static_cast<uint16_t*>(V);
+  auto pick = [&](auto q8) {
+    constexpr bool Q = decltype(q8)::value;
+    return z.d == 64 ? (z.dv == 64 ? fa_cache_read_kernel<8, 8, Q> : fa_cache_read_kernel<8, 16, Q>)
+                     : (z.dv == 64 ? fa_cache_read_kernel<16, 8, Q> : fa_cache_read_kernel<16, 16, Q>);
+  };
+  return launch_pages(z.quantised ? pick(std::true_type{}) : pick(std::false_type{}), z, p, stream);
+}
+
+size_t fa_cache_attention_workspace_bytes(const fa_cache_dims* dims, const fa_cache_prefix* prefix) {
+  fa::CacheShape s;
+  if (check_cache_dims(dims) != FA_OK || attn_shape(*dims, prefix, &s) != FA_OK) return 0;
+  return (long long)dims->B * dims->Hq * dims->T == 0 ? 0 : s.total;
+}
+
+fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache, const fa_cache_scores* scores,
+                             const fa_cache_prefix* prefix, const void* Q, const int* tables, const int* lengths, void* O,
+                             float* L, void* workspace, size_t workspace_bytes, void* stream) {
+  fa_status e = check_cache_dims(dims);
+  if (e != FA_OK || (e = check_pools(*dims, cache)) != FA_OK) return e;
+  const fa_cache_dims& z = *dims;
+  fa::CacheShape s;
+  if ((e = attn_shape(z, prefix, &s)) != FA_OK) return e;
+  const int S = prefix ? prefix->groups : 0, p_cols = prefix ? prefix->table_pages : 0;
+  fa_cache_scores sc = {};
+  if (scores) sc = *scores;
+  if (!(sc.scale == sc.scale) || std::isinf(sc.scale) || sc.window < 0) return FA_ERR_INVALID_ARG;
+  if (sc.softcap != 0.f && !(sc.softcap >= 0x1p-10f && sc.softcap <= 0x1p10f)) return FA_ERR_INVALID_ARG;
+  if (!aligned(sc.slopes, 4)) return FA_ERR_INVALID_ARG;
+  // distances stay exact in fp32, as for fa_scores
+  if (sc.slopes && (long long)(z.table_pages + p_cols) * z.page > (1 << 24)) return FA_ERR_UNSUPPORTED;
+  if ((long long)z.B * z.Hq * z.T == 0) return FA_OK;
+  if (!Q || !O || !L || !lengths || !aligned(Q, 16) || !aligned(O, 16) || !aligned(L, 4) || !aligned(lengths, 4) ||
+      (z.table_pages && !tables) || !aligned(tables, 4))
+    return FA_ERR_INVALID_ARG;
+  if (S && (!prefix->lengths || (p_cols && !prefix->tables) || !aligned(prefix->tables, 4) || !aligned(prefix->lengths, 4) ||
+              !aligned(prefix->starts, 4) || (S > 1 && !prefix->starts)))
+    return FA_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < s.total) return FA_ERR_INVALID_ARG;
+  fa::CacheParams p = {};
+  p.status = fa::device_status_word();
+  if (!p.status) return FA_ERR_CUDA;
+  p.Q = static_cast<const uint16_t*>(Q);
+  // (a pool without pages may have no address; nothing is read of it, and Q's stands in)
+  const bool none = z.pages == 0;
+  p.K = static_cast<const uint8_t*>(none ? Q : cache->K);
+  p.V = static_cast<const uint8_t*>(none ? Q : cache->V);
+  p.k_scale = none ? static_cast<const float*>(Q) : cache->k_scale;
+  p.v_scale = none ? static_cast<const float*>(Q) : cache->v_scale;
+  p.tables = tables;
+  p.lengths = lengths;
+  if (S) {
+    p.p_tables = prefix->tables;
+    p.p_lengths = prefix->lengths;
+    p.p_starts = prefix->starts;
+  }
+  p.slopes = sc.slopes;
+  p.O = static_cast<uint16_t*>(O);
+  p.L = L;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.head = reinterpret_cast<fa::CacheHead*>(ws);
+  p.ml = reinterpret_cast<float*>(ws + s.ml);
+  p.part = reinterpret_cast<float*>(ws + s.part);
+  p.B = z.B;
+  p.Hq = z.Hq;
+  p.Hkv = z.Hkv;
+  p.G = z.Hq / z.Hkv;
+  p.T = z.T;
+  p.pages = z.pages;
+  p.page_log2 = log2_of(z.page);
+  p.cols = z.table_pages;
+  p.S = S;
+  p.p_cols = p_cols;
+  // a window of all keys and more hides nothing
+  p.window = sc.window >= ((long long)z.table_pages + p_cols) * z.page ? 0 : sc.window;
+  const float scale = sc.scale > 0.f ? sc.scale : 1.0f / std::sqrt((float)z.d);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.capped = sc.softcap > 0.f;
+  p.cap = fa::cap_params(sc.softcap, scale);
+  p.min_chunks = fa::kCacheMinChunks;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t err = z.quantised ? fa::launch_cache_attn_e4m3(p, z.d, z.dv, s.grid, st)
+                                : fa::launch_cache_attn_bf16(p, z.d, z.dv, s.grid, st);
+  if (err == cudaSuccess) err = fa::launch_cache_join(p, z.dv, st);
+  return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

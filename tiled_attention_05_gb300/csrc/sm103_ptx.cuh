@@ -60,7 +60,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // Error codes a kernel leaves in its device status word.
-enum : int { DEV_OK = 0, DEV_TIMEOUT = 1 };
+enum : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_BAD_TABLE = 2 };
 
 // Bounded wait for the phase with the given parity.  Gives up after
 // `timeout_ns` of wall time, or as soon as another role of the CTA raised
