@@ -20,7 +20,7 @@
 
 using namespace fa_ptx;
 using fa::CacheParams;
-using fa::CacheParts;
+using fa::CacheSlots;
 using fa::kCacheRows;
 
 namespace {
@@ -200,64 +200,67 @@ __global__ void __launch_bounds__(kThreads) fa_cache_read_kernel(const PageParam
 // of its group's prefix.  WARPS warps take a row (1, or 4 where there are few rows: a
 // long sequence alone has tens of parts).
 template <int DV, int WARPS>
-__global__ void __launch_bounds__(128) fa_cache_join_kernel(const CacheParams p) {
+__global__ void __launch_bounds__(128) fa_cache_join_kernel(const fa::CacheJoin j) {
   constexpr int CH = DV / 32;
   __shared__ float s_o[4][DV], s_l[4];
   grid_next();
   grid_previous();
+  const CacheParams& p = j.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long out = (long long)blockIdx.x * (4 / WARPS) + warp / WARPS, rows = (long long)p.B * p.Hq * p.T;
   if (out >= rows) return;  // (with WARPS 4 a block has one row)
   const int sub = warp % WARPS;
   const int t = (int)(out % p.T), hq = (int)(out / p.T % p.Hq), b = (int)(out / p.T / p.Hq);
   const int h = hq / p.G, g = hq - h * p.G;
-  const long long per = p.head[p.S + p.B].work;
-  const CacheParts own = fa::cache_parts(p.head[p.S + b], p.G * p.T, h, g * p.T + t, per);
-  CacheParts pre = {0, 0, 0};
+  const CacheSlots own = fa::cache_slots(p.parts.head[j.own + b], p.G * p.T, kCacheRows, h, g * p.T + t, p.parts.head[j.own_entries].work);
+  CacheSlots pre = {0, 0, 0};
   if (p.S) {
-    int group = -1, first = 0, seqs = 0;
     for (int s0 = 0; s0 < p.S; s0 += 32) {
       const int s = s0 + lane;
       bool in = false;
       int a = 0, z = 0;
       if (s < p.S) {
-        a = p.p_starts ? __ldg(p.p_starts + s) : 0;
-        z = p.p_starts ? __ldg(p.p_starts + s + 1) : p.B;
-        in = a <= b && b < z && p.head[s].chunks > 0;
+        a = fa::cache_group_start(p, s);
+        z = fa::cache_group_start(p, s + 1);
+        in = a <= b && b < z && j.pre.head[s].chunks > 0;
       }
       const unsigned found = __ballot_sync(~0u, in);
       if (found) {
         const int src = __ffs(found) - 1;
-        group = s0 + src;
-        first = __shfl_sync(~0u, a, src);
-        seqs = __shfl_sync(~0u, z, src) - first;
+        a = __shfl_sync(~0u, a, src);
+        z = __shfl_sync(~0u, z, src);
+        pre = fa::cache_slots(j.pre.head[s0 + src], (z - a) * p.G * p.T, j.pre_rows, h, (b - a) * p.G * p.T + g * p.T + t,
+                              j.pre.head[j.pre_entries].work);
         break;
       }
     }
-    if (group >= 0)
-      pre = fa::cache_parts(p.head[group], seqs * p.G * p.T, h, (b - first) * p.G * p.T + g * p.T + t, per);
   } else if (own.n == 1) {
     return;  // a whole item, stored by its CTA
   }
   const int n = own.n + pre.n;
-  auto row_at = [&](int i) {
-    return i < pre.n ? (pre.slot + i) * kCacheRows + pre.row : (own.slot + i - pre.n) * kCacheRows + own.row;
+  // (reference, sum) and O of part i
+  auto ml_at = [&](int i) {
+    return reinterpret_cast<const float2*>(i < pre.n ? j.pre.ml : p.parts.ml) +
+           (i < pre.n ? (pre.slot + i) * j.pre_rows + pre.row : (own.slot + i - pre.n) * kCacheRows + own.row);
+  };
+  auto o_at = [&](int i) {
+    return i < pre.n ? j.pre.part + ((pre.slot + i) * j.pre_rows + pre.row) * DV
+                     : p.parts.part + ((own.slot + i - pre.n) * kCacheRows + own.row) * DV;
   };
   float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, p.ml[row_at(i) * 2]);
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, ml_at(i)->x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   float sum = 0.f, acc[CH] = {};
 #pragma unroll 4
   for (int i = sub; i < n; i += WARPS) {
-    const long long r = row_at(i);
-    const float2 ml = *reinterpret_cast<const float2*>(p.ml + r * 2);
+    const float2 ml = *ml_at(i);
     float v[CH];
     if constexpr (CH == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(p.part + r * DV + lane * CH);
+      const float4 x = *reinterpret_cast<const float4*>(o_at(i) + lane * CH);
       v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
     } else {
-      const float2 x = *reinterpret_cast<const float2*>(p.part + r * DV + lane * CH);
+      const float2 x = *reinterpret_cast<const float2*>(o_at(i) + lane * CH);
       v[0] = x.x, v[1] = x.y;
     }
     const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - top);  // (without a finite reference, O is 0 or NaN)
@@ -367,7 +370,7 @@ fa_status attn_shape(const fa_cache_dims& z, const fa_cache_prefix* pre, fa::Cac
     return FA_ERR_UNSUPPORTED;
   const int sms = fa::sm_count() > 0 ? fa::sm_count() : 1;  // (without a device the launch fails)
   *s = fa::cache_shape(z.B, z.Hkv, rows, z.dv, z.quantised, (long long)z.table_pages * z.page, S, (long long)p_cols * z.page, sms);
-  return s->items > (1 << 30) || (long long)S + z.B > (1 << 30) ? FA_ERR_UNSUPPORTED : FA_OK;
+  return s->list.items > (1 << 30) || s->pre.items > (1 << 30) || (long long)S + z.B > (1 << 30) ? FA_ERR_UNSUPPORTED : FA_OK;
 }
 
 }  // namespace
@@ -375,15 +378,15 @@ fa_status attn_shape(const fa_cache_dims& z, const fa_cache_prefix* pre, fa::Cac
 namespace fa {
 
 template <int DV>
-static cudaError_t launch_join(const CacheParams& p, cudaStream_t stream) {
-  const long long rows = (long long)p.B * p.Hq * p.T;
+static cudaError_t launch_join(const CacheJoin& j, cudaStream_t stream) {
+  const long long rows = (long long)j.p.B * j.p.Hq * j.p.T;
   // Four warps a row as long as that fills the GPU at most a few times over.
-  if (rows <= 2048) return launch_next(fa_cache_join_kernel<DV, 4>, dim3((unsigned)rows), 128, 0, stream, p);
-  return launch_next(fa_cache_join_kernel<DV, 1>, dim3((unsigned)((rows + 3) / 4)), 128, 0, stream, p);
+  if (rows <= 2048) return launch_next(fa_cache_join_kernel<DV, 4>, dim3((unsigned)rows), 128, 0, stream, j);
+  return launch_next(fa_cache_join_kernel<DV, 1>, dim3((unsigned)((rows + 3) / 4)), 128, 0, stream, j);
 }
 
-cudaError_t launch_cache_join(const CacheParams& p, int dv, cudaStream_t stream) {
-  return dv == 64 ? launch_join<64>(p, stream) : launch_join<128>(p, stream);
+cudaError_t launch_cache_join(const CacheJoin& j, int dv, cudaStream_t stream) {
+  return dv == 64 ? launch_join<64>(j, stream) : launch_join<128>(j, stream);
 }
 
 }  // namespace fa
@@ -493,10 +496,6 @@ fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache
   p.slopes = sc.slopes;
   p.O = static_cast<uint16_t*>(O);
   p.L = L;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.head = reinterpret_cast<fa::CacheHead*>(ws);
-  p.ml = reinterpret_cast<float*>(ws + s.ml);
-  p.part = reinterpret_cast<float*>(ws + s.part);
   p.B = z.B;
   p.Hq = z.Hq;
   p.Hkv = z.Hkv;
@@ -513,11 +512,38 @@ fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache
   p.scale_log2 = scale * 1.4426950408889634f;
   p.capped = sc.softcap > 0.f;
   p.cap = fa::cap_params(sc.softcap, scale);
-  p.min_chunks = fa::kCacheMinChunks;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  auto parts_of = [ws](const fa::CacheList& l) {
+    return fa::CacheParts{reinterpret_cast<fa::CacheHead*>(ws + l.head), reinterpret_cast<float*>(ws + l.ml),
+                          reinterpret_cast<float*>(ws + l.part)};
+  };
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t err = z.quantised ? fa::launch_cache_attn_e4m3(p, z.d, z.dv, s.grid, st)
-                                : fa::launch_cache_attn_bf16(p, z.d, z.dv, s.grid, st);
-  if (err == cudaSuccess) err = fa::launch_cache_join(p, z.dv, st);
+  cudaError_t err = cudaSuccess;
+  p.joined = S > 0;
+  fa::CacheJoin j = {};
+  j.pre = parts_of(s.pre);
+  if (s.apart) {
+    fa::CacheParams pre = p;
+    pre.parts = j.pre;
+    pre.entries = S;
+    pre.min_chunks = fa::kPrefixMinChunks;
+    err = z.quantised ? fa::launch_cache_prefix_e4m3(pre, z.d, z.dv, s.pre.grid, st)
+                      : fa::launch_cache_prefix_bf16(pre, z.d, z.dv, s.pre.grid, st);
+    if (err != cudaSuccess) return FA_ERR_CUDA;
+    p.S = 0;
+  }
+  p.parts = parts_of(s.list);
+  p.entries = p.S + z.B;
+  p.min_chunks = fa::kCacheMinChunks;
+  err = z.quantised ? fa::launch_cache_attn_e4m3(p, z.d, z.dv, s.list.grid, st)
+                    : fa::launch_cache_attn_bf16(p, z.d, z.dv, s.list.grid, st);
+  j.p = p;
+  j.p.S = S;
+  j.own = p.S;
+  j.own_entries = p.entries;
+  j.pre_rows = s.apart ? fa::kPrefixRows : kCacheRows;
+  j.pre_entries = s.apart ? S : p.entries;
+  if (err == cudaSuccess) err = fa::launch_cache_join(j, z.dv, st);
   return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

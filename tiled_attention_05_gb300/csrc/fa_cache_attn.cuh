@@ -41,7 +41,6 @@
 namespace {
 
 using namespace fa_ptx;
-using fa::CacheCursor;
 using fa::CacheEntry;
 using fa::CacheParams;
 
@@ -131,126 +130,18 @@ __device__ __forceinline__ float capped(const fa::CapParams& c, float x) {
   return c.log2c - 2.f * c.log2c * rcp(1.f + ex2(cap_top<true>(c.in * x)));
 }
 
-// The CTA's share [begin, end) of the list, and its first place.  CTA 0 also writes
-// where each entry begins, for the join.
-struct Share {
-  long long begin, end;
-  CacheCursor start;
-  int item;  // ordinal of the first place's item
-};
-
-template <int KC>
-__device__ __forceinline__ Share find_share(const CacheParams& p, bool groups_ok) {
-  __shared__ long long s_work[fa::kCacheWarps], s_found_work;
-  __shared__ int s_item[fa::kCacheWarps], s_found_e, s_found_item;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, entries = p.S + p.B;
-  long long total = 0;
-  for (int e = threadIdx.x; e < entries; e += kThreads) {
-    const CacheEntry n = fa::cache_entry<KC>(p, e, groups_ok);
-    total += (long long)p.Hkv * n.tiles() * n.chunks;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
-  if (lane == 0) s_work[warp] = total;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < fa::kCacheWarps; ++w) total += s_work[w];
-  __syncthreads();
-  Share s;
-  long long per = (total + gridDim.x - 1) / gridDim.x;
-  per = per < p.min_chunks ? p.min_chunks : per;
-  s.begin = per * blockIdx.x;
-  s.end = s.begin + per < total ? s.begin + per : total;
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    p.head[entries].work = per;
-    bool bad = !groups_ok;
-    for (int e = 0; e < p.S && !bad; ++e) bad = __ldg(p.p_lengths + e) > (p.p_cols << p.page_log2);
-    if (bad) fa::cache_bad(p.status);
-  }
-  if (s.begin >= s.end && blockIdx.x) return s;
-  long long base = 0;
-  int item = 0;
-  for (int e0 = 0; e0 < entries; e0 += kThreads) {
-    const int e = e0 + threadIdx.x;
-    long long work = 0;
-    int items = 0;
-    CacheEntry n = {};
-    if (e < entries) {
-      n = fa::cache_entry<KC>(p, e, groups_ok);
-      items = p.Hkv * n.tiles();
-      work = (long long)items * n.chunks;
-      if (blockIdx.x == 0 && e >= p.S && __ldg(p.lengths + e - p.S) > (p.cols << p.page_log2)) fa::cache_bad(p.status);
-    }
-    long long w = work;
-    int i = items;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long wo = __shfl_up_sync(~0u, w, o);
-      const int io = __shfl_up_sync(~0u, i, o);
-      if (lane >= o) w += wo, i += io;
-    }
-    if (lane == 31) s_work[warp] = w, s_item[warp] = i;
-    __syncthreads();
-    long long all = 0;
-    int all_items = 0;
-#pragma unroll
-    for (int v = 0; v < fa::kCacheWarps; ++v) {
-      if (v < warp) w += s_work[v], i += s_item[v];
-      all += s_work[v];
-      all_items += s_item[v];
-    }
-    w += base - work;
-    i += item - items;
-    if (blockIdx.x == 0 && e < entries) p.head[e] = {w, i, n.chunks};
-    if (work && w <= s.begin && s.begin < w + work) s_found_e = e, s_found_work = w, s_found_item = i;
-    base += all;
-    item += all_items;
-    __syncthreads();
-    if (blockIdx.x && s.begin < base) break;
-  }
-  if (s.begin >= s.end) return s;
-  CacheCursor& c = s.start;
-  c.e = s_found_e;
-  c.n = fa::cache_entry<KC>(p, c.e, groups_ok);
-  const long long in = s.begin - s_found_work;
-  const int o = (int)(in / c.n.chunks), tiles = c.n.tiles();
-  c.at = s.begin;
-  c.c = (int)(in - (long long)o * c.n.chunks);
-  c.h = o / tiles;
-  c.r = o - c.h * tiles;
-  s.item = s_found_item + o;
-  return s;
-}
-
-// Position (counted within the own keys) of row t of sequence b; the row's sequence and
-// head for row `row` of an item.
-struct RowOf {
-  int b, g, t;
-  bool valid;
-};
-__device__ __forceinline__ RowOf row_of(const CacheParams& p, const CacheEntry& n, int row) {
-  RowOf r;
-  r.valid = row < n.rows;
-  if (!r.valid) row = 0;
-  const int per = p.G * p.T, s = row / per, left = row - s * per;
-  r.b = n.first + s;
-  r.g = left / p.T;
-  r.t = left - r.g * p.T;
-  return r;
-}
-
 // FEW: the items have at most 8 rows (the upper half of the MMA's rows is not looked at).
 template <int D, int DV, bool Q8, bool FEW>
 __global__ void __launch_bounds__(kThreads, fa::kCacheCtasPerSm) fa_cache_attn_kernel(const CacheParams p) {
   using C = CacheCfg<D, DV, Q8>;
+  using Cursor = fa::CacheCursor<C::KC, kRows>;
   constexpr int KC = C::KC, NT = KC / 8, HALVES = FEW ? 1 : 2, ON = DV / 8;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[2][fa::kCacheWarps][kRows];
   grid_next();
   grid_previous();
   const bool groups_ok = fa::cache_groups_ok(p);
-  const Share share = find_share<KC>(p, groups_ok);
+  const auto share = fa::cache_share<KC, kRows, kThreads>(p, groups_ok);
   if (share.begin >= share.end) return;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -260,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, fa::kCacheCtasPerSm) fa_cache_attn_k
   const int page_mask = (1 << p.page_log2) - 1;
 
   // ------------------------------------------------------------ loads, ahead of the use
-  CacheCursor ld = share.start;
+  Cursor ld = share.start;
   int id0 = 0, id1 = 0;
   // the pages of the next chunk to load: its keys lie in one page, or in two by halves of 16
   auto fetch_ids = [&]() {
@@ -307,19 +198,19 @@ __global__ void __launch_bounds__(kThreads, fa::kCacheCtasPerSm) fa_cache_attn_k
         cp4(dst + C::KBYTES + C::VBYTES + lane * 4, p.k_scale + at, ok);
         cp4(dst + C::KBYTES + C::VBYTES + KC * 4 + lane * 4, p.v_scale + at, ok);
       }
-      ld.advance<KC>(p, groups_ok, fa::kCacheWarps);
+      ld.advance(p, groups_ok, fa::kCacheWarps);
       fetch_ids();
     }
     cp_commit();
   };
-  if (warp) ld.advance<KC>(p, groups_ok, warp);
+  if (warp) ld.advance(p, groups_ok, warp);
   fetch_ids();
 #pragma unroll
   for (int s = 0; s < C::NS - 1; ++s) issue(s);
   int stage = 0, fill = C::NS - 1;
 
   // ------------------------------------------------------------ items
-  CacheCursor it = share.start;
+  Cursor it = share.start;
   int item = share.item, turn = 0;
   long long mine = share.begin + warp;  // this warp's next chunk
   while (it.at < share.end) {
@@ -336,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, fa::kCacheCtasPerSm) fa_cache_attn_k
     uint32_t q[HALVES][D / 8];
 #pragma unroll
     for (int u = 0; u < HALVES; ++u) {
-      const RowOf r = row_of(p, n, it.r * kRows + lr + 8 * u);
+      const fa::CacheRow r = fa::cache_row(p, n, it.r * kRows + lr + 8 * u);
       const int pos = fa::cache_length(p, r.b) - p.T + r.t;
       abs0[u] = is_prefix ? n.keys + pos : pos;
       last[u] = is_prefix ? n.keys - 1 : pos;
@@ -571,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, fa::kCacheCtasPerSm) fa_cache_attn_k
       l[u] += __shfl_xor_sync(~0u, l[u], 2);
       if (li == 0) s_ml[side][warp][lr + 8 * u] = make_float2(m[u], l[u]);
     }
-    const bool whole = it.c == 0 && c_end == n.chunks && p.S == 0;
+    const bool whole = it.c == 0 && c_end == n.chunks && !p.joined;
     const long long slot = (long long)item + blockIdx.x;
 #pragma unroll
     for (int u = 0; u < HALVES; ++u) {
@@ -605,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, fa::kCacheCtasPerSm) fa_cache_attn_k
         }
         const int at = it.r * kRows + row;
         if (at < n.rows) {
-          const RowOf r = row_of(p, n, at);
+          const fa::CacheRow r = fa::cache_row(p, n, at);
           if (fa::cache_length(p, r.b) - p.T + r.t < 0) {  // a padding row
             sum = 0.f;
 #pragma unroll
@@ -628,12 +519,12 @@ __global__ void __launch_bounds__(kThreads, fa::kCacheCtasPerSm) fa_cache_attn_k
                     make_uint4(w[0], w[1], w[2], w[3]);
               }
           } else {
-            if (li == 0) *reinterpret_cast<float2*>(p.ml + (slot * kRows + row) * 2) = make_float2(top, sum);
+            if (li == 0) *reinterpret_cast<float2*>(p.parts.ml + (slot * kRows + row) * 2) = make_float2(top, sum);
 #pragma unroll
             for (int y = 0; y < 2; ++y)
 #pragma unroll
               for (int k = 0; k < ON; k += 4)
-                *reinterpret_cast<float4*>(p.part + (slot * kRows + row) * DV + (k / RUN) * 64 + (2 * li + y) * RUN + k % RUN) =
+                *reinterpret_cast<float4*>(p.parts.part + (slot * kRows + row) * DV + (k / RUN) * 64 + (2 * li + y) * RUN + k % RUN) =
                     make_float4(o[k][2 * u + y], o[k + 1][2 * u + y], o[k + 2][2 * u + y], o[k + 3][2 * u + y]);
           }
         }
@@ -641,9 +532,9 @@ __global__ void __launch_bounds__(kThreads, fa::kCacheCtasPerSm) fa_cache_attn_k
     }
     item += c_end == n.chunks;
     const int old = it.e;
-    it.advance<KC>(p, groups_ok, c_end - it.c);
+    it.advance(p, groups_ok, c_end - it.c);
     // (entries without work have items of their own number too)
-    for (int e = old + 1; e < it.e && e < p.S + p.B; ++e) item += p.Hkv * fa::cache_entry<KC>(p, e, groups_ok).tiles();
+    for (int e = old + 1; e < it.e && e < p.entries; ++e) item += p.Hkv * fa::cache_entry<KC>(p, e, groups_ok).tiles(kRows);
   }
   cp_wait<0>();
 }
