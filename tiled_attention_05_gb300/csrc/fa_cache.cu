@@ -309,7 +309,7 @@ fa_status check_cache_dims(const fa_cache_dims* dims) {
   if ((z.d != 64 && z.d != 128) || (z.dv != 64 && z.dv != 128)) return FA_ERR_UNSUPPORTED;
   if (z.page < 16 || z.page > 256 || (z.page & (z.page - 1))) return FA_ERR_UNSUPPORTED;
   if ((long long)z.table_pages * z.page > (1 << 30) || z.T > (1 << 30)) return FA_ERR_UNSUPPORTED;
-  if ((long long)z.B * z.Hkv > INT_MAX || (long long)z.pages * z.Hkv * z.page > (1LL << 48)) return FA_ERR_UNSUPPORTED;
+  if ((long long)z.B * z.Hkv > INT_MAX || (long long)z.pages * z.Hkv > INT_MAX) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 

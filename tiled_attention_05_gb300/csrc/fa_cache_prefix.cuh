@@ -9,10 +9,10 @@
 //                O_X += P_X(j) V_j, so that the tensor pipe runs one tile's while the
 //                softmax works on the other's (the forward's order: those of one
 //                thread execute in issue order, so S_X(j + 1) may overwrite P_X(j))
-//   warps 1..3   bring K_j and V_j from their pages into the ring's slots, in the 128-byte
-//                swizzle that TMA would write: rows lie in pages of 16 and more, some
-//                of a tile past the prefix's end, and e4m3 codes become fp16 on the way
-//                (16 cp.async of a slot in flight while the one before it is converted)
+//   warps 1..3   bring K_j and V_j from their pages into the ring's slots: bf16 by TMA, a
+//                box a page (by cp.async of these warps, 16 bytes a lane, a tile took them
+//                4 us); e4m3 by bulk copies into raw buffers, which the three warps
+//                turn into fp16 in the swizzle that TMA writes
 //   warps 4..11  softmax of tile A and of tile B, a thread a row: scores from TMEM, exp2, P
 //                as 16-bit pairs over the scores, O rescaled in TMEM when the maximum grows
 //                by more than 2^8; before that the row of Q into shared memory, after
@@ -35,7 +35,7 @@ using namespace fa_ptx;
 using fa::CacheEntry;
 using fa::CacheParams;
 
-constexpr int kThreads = 384, kLoaders = 96;
+constexpr int kThreads = 384, kLoaders = 96;  // (three warps of them load)
 constexpr int BM = 128, BN = fa::kPrefixKeys;
 // Register split, as in the forward: 88 + 2 * 208 = 3 * 168.
 constexpr int kRegsLaunch = 168, kRegsLow = 88, kRegsHigh = 208;
@@ -45,7 +45,7 @@ template <int D, int DV, bool Q8>
 struct PrefixCfg {
   static constexpr int W = D > DV ? D : DV;
   static constexpr int Q_BYTES = BM * D * 2, SLOT = BN * W * 2;
-  static constexpr int RAW = Q8 ? BN * W : 0;  // a slot's codes, in the order of the copying threads
+  static constexpr int RAW = Q8 ? BN * W : 0;  // a slot's codes
   static constexpr int NRAW = Q8 ? 3 : 0;
   static constexpr int SCALES = Q8 ? 2 * 2 * 3 * BN * 4 : 0;  // [tile][buffer][k_scale, log2 v_scale, 1 / v_scale][key]
   static constexpr int OFF_SLOT = 2 * Q_BYTES;
@@ -55,22 +55,13 @@ struct PrefixCfg {
   static constexpr int OFF_SCALES = OFF_RAW + NRAW * RAW;
   static constexpr int OFF_BAR = OFF_SCALES + SCALES;
   static constexpr int SMEM = OFF_BAR + 512;
-  // V_j leaves its slot after S_A(j + 1), so a loader must not wait for that before K_{j+1}
-  // is handed over: two slots, and as many as copies it has in flight beyond (bf16).
-  static_assert(NS >= (Q8 ? 2 : 4) && SMEM <= (226 << 10), "shared memory");
+  // (V_j leaves its slot after S_A(j + 1): K_{j+1} needs another one)
+  static_assert(NS >= 3 && SMEM <= (226 << 10), "shared memory");
 };
 
 // Instruction descriptor, kind::f16 with fp32 D; A and B fp16 or bf16.
 __host__ __device__ constexpr uint32_t idesc(bool f16, int M, int N, int b_mn) {
   return f16 ? idesc_bf16(M, N, 0, b_mn) & ~((1u << 7) | (1u << 10)) : idesc_bf16(M, N, 0, b_mn);
-}
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -94,7 +85,8 @@ __device__ __forceinline__ float capped(const fa::CapParams& c, float x) {
 }
 
 template <int D, int DV, bool Q8, bool MODS>
-__global__ void __launch_bounds__(kThreads, 1) fa_cache_prefix_kernel(const CacheParams p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    fa_cache_prefix_kernel(const CacheParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = PrefixCfg<D, DV, Q8>;
   using Cursor = fa::CacheCursor<BN, fa::kPrefixRows>;
   constexpr int NS = C::NS;
@@ -111,15 +103,21 @@ __global__ void __launch_bounds__(kThreads, 1) fa_cache_prefix_kernel(const Cach
   uint64_t* s_full = q_full + 2;   // [2]
   uint64_t* p_full = s_full + 2;   // [2]
   uint64_t* o_done = p_full + 2;   // [2]
-  uint64_t* drain = o_done + 2;
+  uint64_t* raw_full = o_done + 2;    // [3] a raw buffer holds its codes (bf16: [0], a tile's last rows have come)
+  uint64_t* raw_empty = raw_full + 3;  // [3]
+  uint64_t* drain = raw_empty + 3;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     *abort_flag = (smem_u32(smem) & 1023u) ? 1 : 0;  // swizzled tiles need 1024 B alignment
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], kLoaders / 32);
+      mbar_init(&full[s], Q8 ? kLoaders / 32 : 1);
       mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], kLoaders / 32);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 128);
@@ -215,110 +213,148 @@ __global__ void __launch_bounds__(kThreads, 1) fa_cache_prefix_kernel(const Cach
       }
     } else {
       // ------------------------------------------------------------ loaders
+      // Units K_0, V_0, K_1, ... of all items; unit u goes to slot u % NS (e4m3: by way of the
+      // raw buffer u % NRAW).  Warp 1 issues the copies, a page (or 128 rows of it) a lane.
       const int tid = threadIdx.x - 32;
-      const uint32_t slots = smem_u32(smem + C::OFF_SLOT), raw = smem_u32(smem + C::OFF_RAW);
-      // Pieces of 16 bytes: a row has PK (PV) of them; thread tid takes piece tid % P of
-      // rows tid / P + k * (96 / P).
-      auto copy = [&](const Cursor& it, int c, bool v, uint32_t dst) {
-        const int key0 = (it.n.chunk0 + c) * BN;
-        const int* tab = p.p_tables + (long long)it.e * p.p_cols;
-        auto go = [&](auto row_bytes) {
-          constexpr int B = decltype(row_bytes)::value, P = B / 16, STEP = kLoaders / P;
-          const uint8_t* pool = v ? p.V : p.K;
-          const int piece = tid % P;
-          bool bad = false;
-#pragma unroll 4
-          for (int k = 0; k < (BN + STEP - 1) / STEP; ++k) {
-            const int row = tid / P + k * STEP, key = key0 + row;
-            if (row >= BN) break;
-            bool ok = key < it.n.keys;
-            int id = 0;
-            if (ok) {
-              id = __ldg(tab + (key >> p.page_log2));
-              ok = (unsigned)id < (unsigned)p.pages;
-              bad = bad || !ok;
-            }
-            const long long at = ok ? ((((long long)id * p.Hkv + it.h) << p.page_log2) | (key & page_mask)) * B + piece * 16 : 0;
-            const uint32_t to = Q8 ? (uint32_t)(k * kLoaders + tid) * 16
-                                   : (piece >> 3) * (BN * 128) + sw128_offset(row, piece & 7);
-            cp16(dst + to, pool + at, ok);
-          }
-          if (bad) fa::cache_bad(p.status);
-        };
-        if (v)
-          go(std::integral_constant<int, DV * (Q8 ? 1 : 2)>{});
-        else
-          go(std::integral_constant<int, D * (Q8 ? 1 : 2)>{});
+      uint8_t* slots = smem + C::OFF_SLOT;
+      const int box = p.page_log2 < 7 ? 1 << p.page_log2 : BN;  // rows of a copy
+      struct Units {
+        Cursor it;
+        Item m;
+        int c, u;
+        bool v;
       };
-      // e4m3: the thread's own pieces, 16 codes each, to fp16 in the slot
-      auto convert = [&](bool v, uint32_t src, uint32_t dst) {
-        auto go = [&](auto row_bytes) {
-          constexpr int P = decltype(row_bytes)::value / 16, STEP = kLoaders / P;
-          const int piece = tid % P;
-#pragma unroll 4
-          for (int k = 0; k < (BN + STEP - 1) / STEP; ++k) {
-            const int row = tid / P + k * STEP;
-            if (row >= BN) break;
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(src + (k * kLoaders + tid) * 16)
-                         : "memory");
-            const uint32_t block = dst + (piece >> 2) * (BN * 128);
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              st_shared_v4(block + sw128_offset(row, (piece & 3) * 2 + x), half2_of(w[2 * x]), half2_of(w[2 * x] >> 16),
-                           half2_of(w[2 * x + 1]), half2_of(w[2 * x + 1] >> 16));
-          }
-        };
-        if (v)
-          go(std::integral_constant<int, DV>{});
-        else
-          go(std::integral_constant<int, D>{});
+      auto step = [&](Units& n) {  // to the next unit; false at the share's end
+        ++n.u;
+        n.v = !n.v;
+        if (n.v || ++n.c < n.m.c1) return true;
+        n.it.advance(p, groups_ok, n.m.c1 - n.m.c0);
+        if (n.it.at >= share.end) return false;
+        n.m = item_of(n.it);
+        n.c = n.m.c0;
+        return true;
       };
-      // Units K_0, V_0, K_1, ... of all items; `ahead` copies in flight.  Unit u goes to slot
-      // u % NS (e4m3: by way of the raw buffer u % NRAW).
-      constexpr int AHEAD = 2;
-      Cursor ld = share.start;
-      Item m = item_of(ld);
-      int c = m.c0;
-      bool v = false, more = run, ok = run;
-      int issued = 0, done = 0;
-      uint32_t is_v = 0;  // bit i: unit i (mod 32) is a V
-      auto issue = [&]() {  // the next unit, if there is one (a group is committed all the same)
-        if (more && ok) {
-          if (!Q8 && !mbar_wait(&empty[issued % NS], ((issued / NS) & 1) ^ 1, abort_flag)) ok = false;
-          ok = __all_sync(~0u, ok);
-          if (ok) {
-            copy(ld, c, v, Q8 ? raw + (issued % (C::NRAW + !C::NRAW)) * C::RAW : slots + (issued % NS) * C::SLOT);
-            is_v = (is_v & ~(1u << (issued & 31))) | ((uint32_t)v << (issued & 31));
-            ++issued;
-            v = !v;
-            if (!v && ++c == m.c1) {
-              ld.advance(p, groups_ok, m.c1 - m.c0);
-              more = ld.at < share.end;
-              if (more) m = item_of(ld), c = m.c0;
-            }
-          }
-        }
-        cp_commit();
+      Units ld = {share.start, item_of(share.start), 0, 0, false};
+      ld.c = ld.m.c0;
+      bool ok = run;
+      // The page of this lane's 16 rows of a tile (-1: none is needed, or it does not fit).
+      int id = 0;
+      auto fetch_id = [&]() {
+        const int key = (ld.it.n.chunk0 + ld.c) * BN + (lane & 7) * 16;
+        id = -1;
+        if (key >= ld.it.n.keys) return;
+        id = __ldg(p.p_tables + (long long)ld.it.e * p.p_cols + (key >> p.page_log2));
+        if ((unsigned)id >= (unsigned)p.pages) fa::cache_bad(p.status), id = -1;
       };
-      for (int k = 0; k < AHEAD; ++k) issue();
-      while (ok && done < issued) {
-        issue();
-        cp_wait<AHEAD>();  // unit `done` has landed (this thread's pieces of it)
-        if (Q8) {
-          if (!mbar_wait(&empty[done % NS], ((done / NS) & 1) ^ 1, abort_flag)) ok = false;
-          ok = __all_sync(~0u, ok);
-          if (!ok) break;
-          convert((is_v >> (done & 31)) & 1u, raw + (done % (C::NRAW + !C::NRAW)) * C::RAW, slots + (done % NS) * C::SLOT);
-        }
-        fence_async_smem();
+      // Copies of unit ld; `bar` gets their bytes.
+      auto copy = [&](uint64_t* bar, uint8_t* dst) {
+        const int row = (lane & 7) * 16, width = ld.v ? DV : D;
+        const bool mine = lane < 8 && row % box == 0 && id >= 0;
+        const unsigned all = __ballot_sync(~0u, mine);
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(all) * box * width * (Q8 ? 1 : 2));
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[done % NS]);
-        ++done;
+        if (!mine) return;
+        const int at = ((ld.it.n.chunk0 + ld.c) * BN + row) & page_mask;
+        const int head = id * p.Hkv + ld.it.h;
+        if constexpr (Q8) {
+          bulk_load(dst + row * width, (ld.v ? p.V : p.K) + (((long long)head << p.page_log2) | at) * width, box * width, bar);
+        } else {
+          for (int cb = 0; cb < width / 64; ++cb)
+            tma_load_3d(dst + cb * (BN * 128) + row * 128, ld.v ? &tmV : &tmK, bar, cb * 64, at, head);
+        }
+      };
+      if constexpr (!Q8) {
+        if (warp == 1) {
+          int tails = 0;
+          bool more = true;
+          fetch_id();
+          while (ok && more) {
+            const int s = ld.u % NS, valid = ld.it.n.keys - (ld.it.n.chunk0 + ld.c) * BN;
+            if (!__all_sync(~0u, mbar_wait(&empty[s], ((ld.u / NS) & 1) ^ 1, abort_flag))) break;
+            // Rows past the prefix's end: whatever the pages hold there meets a score that is
+            // masked, and as a value a weight of 0, for which it has to be finite.
+            const bool tail = ld.v && valid < BN;
+            copy(tail ? raw_full : &full[s], slots + s * C::SLOT);
+            if (tail) {
+              ok = __all_sync(~0u, mbar_wait(raw_full, tails++ & 1, abort_flag));
+              for (int k = lane; k < (BN - valid) * (DV / 8); k += 32) {
+                const int row = valid + k / (DV / 8), chunk = k % (DV / 8);
+                st_shared_v4(smem_u32(slots + s * C::SLOT) + (chunk >> 3) * (BN * 128) + sw128_offset(row, chunk & 7), 0, 0, 0, 0);
+              }
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&full[s]);
+            }
+            more = step(ld);
+            if (more && !ld.v) fetch_id();
+          }
+          // Copies in flight have to land before the CTA leaves its shared memory.
+          for (int u = ld.u > NS ? ld.u - NS : 0; u < ld.u; ++u) mbar_wait_bounded(&full[u % NS], (u / NS) & 1);
+        }
+      } else {
+        // e4m3: all three warps turn the codes of a raw buffer into fp16, pieces of 16 codes.
+        auto convert = [&](auto w, int valid, const uint8_t* src, uint32_t dst) {
+          constexpr int P = decltype(w)::value / 16, N = (BN * P + kLoaders - 1) / kLoaders, HALF = (N + 1) / 2;
+#pragma unroll
+          for (int k0 = 0; k0 < N; k0 += HALF) {
+            uint4 c[HALF];
+#pragma unroll
+            for (int k = 0; k < HALF; ++k) {
+              const int i = (k0 + k) * kLoaders + tid;
+              c[k] = make_uint4(0, 0, 0, 0);
+              if (i < valid * P) c[k] = reinterpret_cast<const uint4*>(src)[i];
+            }
+#pragma unroll
+            for (int k = 0; k < HALF; ++k) {
+              const int i = (k0 + k) * kLoaders + tid, row = i / P, piece = i % P;
+              if (k0 + k >= N || row >= BN) continue;
+              const uint32_t block = dst + (piece >> 2) * (BN * 128);
+              st_shared_v4(block + sw128_offset(row, (piece & 3) * 2), half2_of(c[k].x), half2_of(c[k].x >> 16), half2_of(c[k].y),
+                           half2_of(c[k].y >> 16));
+              st_shared_v4(block + sw128_offset(row, (piece & 3) * 2 + 1), half2_of(c[k].z), half2_of(c[k].z >> 16),
+                           half2_of(c[k].w), half2_of(c[k].w >> 16));
+            }
+          }
+        };
+        constexpr int NR = C::NRAW + !Q8;
+        bool more_ld = true, more = true;
+        auto issue = [&]() {  // (warp 1) the next unit's codes into their raw buffer
+          if (warp != 1 || !more_ld || !ok) return;
+          const int s = ld.u % NR;
+          if (!__all_sync(~0u, mbar_wait(&raw_empty[s], ((ld.u / NR) & 1) ^ 1, abort_flag))) {
+            ok = false;
+            return;
+          }
+          copy(&raw_full[s], smem + C::OFF_RAW + s * C::RAW);
+          more_ld = step(ld);
+          if (more_ld && !ld.v) fetch_id();
+        };
+        fetch_id();
+        Units now = ld;
+        for (int k = 0; k < NR - 1; ++k) issue();
+        while (ok && more) {
+          issue();
+          const int s = now.u % NS, rs = now.u % NR, valid = min(now.it.n.keys - (now.it.n.chunk0 + now.c) * BN, BN);
+          const bool both = mbar_wait(&raw_full[rs], (now.u / NR) & 1, abort_flag) &&
+                            mbar_wait(&empty[s], ((now.u / NS) & 1) ^ 1, abort_flag);
+          if (!__all_sync(~0u, both)) break;
+          const uint8_t* src = smem + C::OFF_RAW + rs * C::RAW;
+          const uint32_t dst = smem_u32(slots + s * C::SLOT);
+          if (now.v)
+            convert(std::integral_constant<int, DV>{}, valid, src, dst);
+          else
+            convert(std::integral_constant<int, D>{}, valid, src, dst);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full[s]);
+            mbar_arrive(&raw_empty[rs]);
+          }
+          more = step(now);
+        }
+        if (warp == 1)
+          for (int u = ld.u > NR ? ld.u - NR : 0; u < ld.u; ++u) mbar_wait_bounded(&raw_full[u % NR], (u / NR) & 1);
       }
-      cp_wait<0>();
     }
   } else {
     // ------------------------------------------------------------ softmax of tile x
@@ -345,30 +381,35 @@ __global__ void __launch_bounds__(kThreads, 1) fa_cache_prefix_kernel(const Cach
         float unit = MODS && p.capped ? 1.f : p.scale_log2;
         const float slope = MODS && p.slopes ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
         const int abs0 = it.n.keys + pos;
-        {  // Q's row into shared memory (e4m3: as fp16, its largest value brought to [1, 2))
-          const uint4* src = reinterpret_cast<const uint4*>(p.Q + (((long long)w.b * p.Hq + head) * p.T + w.t) * D);
+        {  // the warp's 32 rows of Q into shared memory (e4m3: as fp16, a row's largest value brought to [1, 2))
+          constexpr int P = D / 8, STEP = 32 / P;  // lanes a row, rows at a time
+          const int mine = w.valid ? (w.b * p.Hq + head) * p.T + w.t : -1;
           const uint32_t dst = smem_u32(smem) + x * C::Q_BYTES;
-          uint4 q[D / 8];
-          uint32_t top = 0;
+          uint4 q[32 / STEP];
 #pragma unroll
-          for (int k = 0; k < D / 8; ++k) {
-            q[k] = w.valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-            const uint32_t a[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) top = max(top, max(a[y] & 0x7fffu, (a[y] >> 16) & 0x7fffu));
+          for (int k = 0; k < 32 / STEP; ++k) {
+            const int from = __shfl_sync(~0u, mine, k * STEP + lane / P);
+            q[k] = from >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.Q + (long long)from * D) + lane % P) : make_uint4(0, 0, 0, 0);
           }
-          const int ex = min(max((int)(top >> 7), 1), 253);
-          const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
-          if constexpr (Q8) unit *= __uint_as_float((uint32_t)ex << 23);
 #pragma unroll
-          for (int k = 0; k < D / 8; ++k) {
+          for (int k = 0; k < 32 / STEP; ++k) {
             uint32_t a[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
             if constexpr (Q8) {
+              uint32_t top = 0;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) top = max(top, max(a[y] & 0x7fffu, (a[y] >> 16) & 0x7fffu));
+#pragma unroll
+              for (int o = P / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+              const int ex = min(max((int)(top >> 7), 1), 253);
+              const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
 #pragma unroll
               for (int y = 0; y < 4; ++y)
                 a[y] = pack_f16x2(__uint_as_float(a[y] << 16) * down, __uint_as_float(a[y] & 0xffff0000u) * down);
+              const int theirs = __shfl_sync(~0u, ex, (lane % STEP) * P);  // row k * STEP + lane % STEP
+              if (lane / STEP == k) unit *= __uint_as_float((uint32_t)theirs << 23);
             }
-            st_shared_v4(dst + (k >> 3) * (BM * 128) + sw128_offset(r, k & 7), a[0], a[1], a[2], a[3]);
+            const int row = quad * 32 + k * STEP + lane / P, piece = lane % P;
+            st_shared_v4(dst + (piece >> 3) * (BM * 128) + sw128_offset(row, piece & 7), a[0], a[1], a[2], a[3]);
           }
           fence_async_smem();
           mbar_arrive(&q_full[x]);
@@ -506,19 +547,29 @@ __global__ void __launch_bounds__(kThreads, 1) fa_cache_prefix_kernel(const Cach
           const bool none = pos < 0;
           const long long at = ((long long)item + blockIdx.x) * fa::kPrefixRows + x * BM + r;
           if (w.valid) *reinterpret_cast<float2*>(p.parts.ml + at * 2) = none ? make_float2(NEG_INF, 0.f) : make_float2(m_ref, l);
-          float4* out = reinterpret_cast<float4*>(p.parts.part + at * DV);
-#pragma unroll
+          // 32 columns at a time through this warp's share of Q_X, which is free now, so that a
+          // row's 128 bytes leave together.
+          uint8_t* stage = smem + x * C::Q_BYTES + quad * 4096;
+          const unsigned valid = __ballot_sync(~0u, w.valid);
+          const long long first = at - lane;  // the warp's first row
+#pragma unroll 1
           for (int c = 0; c < DV / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(tO + c * 32, o);
             tmem_wait_ld();
-            if (w.valid) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                out[c * 8 + k] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                      : make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                                    __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                  none ? make_uint4(0, 0, 0, 0) : make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int row = k * 4 + lane / 8;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+              if ((valid >> row) & 1u)
+                *reinterpret_cast<uint4*>(p.parts.part + (first + row) * DV + c * 32 + (lane & 7) * 4) = v;
             }
+            __syncwarp();
           }
           tc_fence_before();  // (the next item's first P.V into O_X follows this warpgroup's next P)
         }
@@ -549,7 +600,13 @@ cudaError_t launch_mods(const CacheParams& p, int grid, cudaStream_t stream) {
   e = cudaFuncGetAttributes(&a, kernel);
   if (e != cudaSuccess) return e;
   if (a.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-  return fa::launch_next(kernel, dim3((unsigned)grid), kThreads, C::SMEM, stream, p);
+  CUtensorMap mk = {}, mv = {};
+  const int page = 1 << p.page_log2;
+  const long long heads = (long long)p.pages * p.Hkv;
+  if (!Q8 && (!fa::encode_pages_bf16(&mk, p.K, D, page, heads, page < BN ? page : BN) ||
+              !fa::encode_pages_bf16(&mv, p.V, DV, page, heads, page < BN ? page : BN)))
+    return cudaErrorInvalidValue;
+  return fa::launch_next(kernel, dim3((unsigned)grid), kThreads, C::SMEM, stream, p, mk, mv);
 }
 
 template <int D, int DV, bool Q8>

@@ -36,6 +36,9 @@ struct Problem {
 // Returns false if cuTensorMapEncodeTiled rejects it.
 bool encode_rows_bf16(CUtensorMap* map, const void* base, int inner, int rows, long long outer);
 
+// The same for a pool of cache pages viewed as [outer][page][inner], box = 64 x box_rows x 1.
+bool encode_pages_bf16(CUtensorMap* map, const void* base, int inner, int page, long long outer, int box_rows);
+
 // TMA descriptor for the fp32 dQ accumulator viewed as [outer][rows][inner]
 // (inner = d), box = 32 x box_rows x 1 (128 bytes x box_rows), 128-byte swizzle.
 bool encode_acc_f32(CUtensorMap* map, const void* base, int inner, long long rows, long long outer, int box_rows);
