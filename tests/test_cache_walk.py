@@ -29,7 +29,7 @@ using namespace fa;
 template <int KC, int ROWS>
 void follow(int call, std::mt19937& rng) {
   constexpr bool PRE = ROWS == kPrefixRows;
-  constexpr int kWarps = PRE ? 1 : 4, kMin = PRE ? kPrefixMinChunks : kCacheMinChunks;
+  constexpr int kWarps = PRE ? 1 : 4, kItem = PRE ? kPrefixItem : kCacheItem, kMin = PRE ? kPrefixMinChunks : kCacheMinChunks;
   auto in = [&](int a, int b) { return a + (int)(rng() % (unsigned)(b - a + 1)); };
   CacheParams p = {};
   p.B = in(1, call % 3 ? 6 : 300);
@@ -52,7 +52,7 @@ void follow(int call, std::mt19937& rng) {
   p.p_starts = starts.data();
   const int rows = p.G * p.T, entries = PRE ? p.S : p.S + p.B;
   p.entries = entries;
-  const CacheShape all = cache_shape(p.B, p.Hkv, rows, 64, KC == 32, (long long)p.cols << p.page_log2, p.S,
+  const CacheShape all = cache_shape(p.B, p.Hkv, rows, 64, call % 2, (long long)p.cols << p.page_log2, p.S,
                                        (long long)p.p_cols << p.page_log2, sms);
   if (PRE && !all.apart) return;
   const CacheList shape = PRE ? all.pre : all.list;
@@ -65,15 +65,16 @@ void follow(int call, std::mt19937& rng) {
   if (all.apart) CHECK(fits(all.pre, p.S, kPrefixRows, all.total));
   // the entries' places, as CTA 0 writes them
   std::vector<CacheHead> head(entries);
-  long long total = 0;
+  long long total = 0, chunks = 0;
   int items = 0;
   for (int e = 0; e < entries; ++e) {
-    const CacheEntry n = cache_entry<KC>(p, e, true);
-    head[e] = {total, items, n.chunks};
-    total += (long long)p.Hkv * n.tiles(ROWS) * n.chunks;
+    const CacheEntry n = cache_entry<KC>(p, e);
+    head[e] = {(int)total, items, n.chunks};
+    if (n.chunks) total += (long long)p.Hkv * n.tiles(ROWS) * (n.chunks + kItem);
+    chunks += (long long)p.Hkv * n.tiles(ROWS) * n.chunks;
     items += p.Hkv * n.tiles(ROWS);
   }
-  CHECK(items <= shape.items);
+  CHECK(all.fits && items <= shape.items);
   long long per = (total + shape.grid - 1) / shape.grid;
   if (per < kMin) per = kMin;
   CHECK(per * shape.grid >= total);
@@ -82,47 +83,58 @@ void follow(int call, std::mt19937& rng) {
   for (int cta = 0; cta < shape.grid; ++cta) {
     const long long begin = cta * per, end = begin + per < total ? begin + per : total;
     if (begin >= end) break;
-    CacheCursor<KC, ROWS> it;
-    it.e = 0;
-    while (!(head[it.e].chunks && begin < head[it.e].work + (long long)p.Hkv * cache_entry<KC>(p, it.e, true).tiles(ROWS) * head[it.e].chunks))
-      ++it.e;
-    it.n = cache_entry<KC>(p, it.e, true);
-    const long long into = begin - head[it.e].work;
-    const int o = (int)(into / it.n.chunks);
-    it.at = begin;
-    it.c = (int)(into % it.n.chunks);
-    it.h = o / it.n.tiles(ROWS);
-    it.r = o % it.n.tiles(ROWS);
-    int item = head[it.e].item + o;
-    CacheCursor<KC, ROWS> warp[4] = {it, it, it, it};
-    for (int w = 1; w < kWarps; ++w) warp[w].advance(p, true, w);
-    while (it.at < end) {
-      const long long left = end - it.at;
-      const int c_end = left < it.n.chunks - it.c ? it.c + (int)left : it.n.chunks;
-      CHECK(item == head[it.e].item + it.h * it.n.tiles(ROWS) + it.r);
-      CHECK(item + cta < shape.slots);
-      CHECK(slots.emplace((long long)item + cta, std::make_pair(item, cta)).second);
+    using Cursor = CacheCursor<KC, ROWS, kItem>;
+    int e = 0;
+    while (!(head[e].chunks && begin < head[e].work + (long long)p.Hkv * cache_entry<KC>(p, e).tiles(ROWS) * (head[e].chunks + kItem))) ++e;
+    Cursor it;
+    it.start(p, e, head[e].item, (int)begin, (int)(begin - head[e].work));
+    for (; it.at < end; it.next(p)) {
+      const int c_end = it.end((int)end);
+      CHECK(it.c < c_end);
+      CHECK(it.item == head[it.e].item + it.h * it.n.tiles(ROWS) + it.r);
+      CHECK(it.at == head[it.e].work + (it.h * it.n.tiles(ROWS) + it.r) * (it.n.chunks + kItem) + it.c);
+      CHECK(it.item + cta < shape.slots);
+      CHECK(slots.emplace((long long)it.item + cta, std::make_pair(it.item, cta)).second);
       for (int c = it.c; c < c_end; ++c) {
         CHECK(seen.insert({it.e, it.h, it.r, c}).second);
-        // the warp whose turn it is stands there
-        CacheCursor<KC, ROWS>& w = warp[(it.at + (c - it.c) - begin) % kWarps];
-        CHECK(w.e == it.e && w.h == it.h && w.r == it.r && w.c == c && w.at == it.at + (c - it.c));
-        const int key = (w.n.chunk0 + c) * KC;
-        CHECK(key >= 0 && key < w.n.keys && (key >> p.page_log2) < (w.e < p.S ? p.p_cols : p.cols));
-        w.advance(p, true, kWarps);
+        const int key = (it.n.chunk0 + c) * KC;
+        CHECK(key >= 0 && key < it.n.keys && (key >> p.page_log2) < (it.e < p.S ? p.p_cols : p.cols));
       }
-      item += c_end == it.n.chunks;
-      const int old = it.e;
-      it.advance(p, true, c_end - it.c);
-      for (int e = old + 1; e < it.e && e < entries; ++e) item += p.Hkv * cache_entry<KC>(p, e, true).tiles(ROWS);
     }
+    // each warp's chunks, as the loads walk ahead: the same that it meets item by item
+    if (!PRE)
+      for (int warp = 0; warp < kWarps; ++warp) {
+        Cursor ld;
+        ld.start(p, e, head[e].item, (int)begin, (int)(begin - head[e].work));
+        if (ld.at >= end) break;
+        Cursor use = ld;
+        int lc = ld.c + warp, lc_end = ld.end((int)end), turn = 0;
+        auto next_load = [&](int step) {
+          lc += step;
+          while (lc >= lc_end) {
+            ld.next(p);
+            if (ld.at >= end) return;
+            ++turn;
+            lc = ld.c + ((warp - turn) & 3);
+            lc_end = ld.end((int)end);
+          }
+        };
+        next_load(0);
+        int t = 0;
+        for (; use.at < end; use.next(p), ++t)
+          for (int c = use.c + ((warp - t) & 3); c < use.end((int)end); c += 4) {
+            CHECK(lc < lc_end && ld.item == use.item && lc == c);
+            next_load(4);
+          }
+        CHECK(lc >= lc_end);
+      }
   }
-  CHECK((long long)seen.size() == total);
+  CHECK((long long)seen.size() == chunks);
   for (int e = 0; e < entries; ++e) {
-    const CacheEntry n = cache_entry<KC>(p, e, true);
+    const CacheEntry n = cache_entry<KC>(p, e);
     for (int h = 0; h < p.Hkv; ++h)
       for (int row = 0; row < n.rows; ++row) {
-        const CacheSlots l = cache_slots(head[e], n.rows, ROWS, h, row, per);
+        const CacheSlots l = cache_slots(head[e], n.rows, ROWS, kItem, h, row, (int)per);
         CHECK((l.n > 0) == (n.chunks > 0) && l.row == row % ROWS);
         for (int i = 0; i < l.n; ++i) {
           CHECK(slots.count(l.slot + i));
@@ -140,9 +152,15 @@ void follow(int call, std::mt19937& rng) {
 
 int main() {
   std::mt19937 rng(7);
+  for (int by : {1, 2, 3, 5, 7, 16, 255, 1000003, (1 << 30) - 1, 1 << 30})
+    for (int k = 0; k < 2000; ++k) {
+      const int call = by, n = k < 100 ? k : (int)(rng() & ((1u << 30) - 1)), d = Divide::of(by)(n);
+      CHECK(d == n / by);
+      const int m = n / by * by;  // at a multiple, and before one
+      CHECK(Divide::of(by)(m) == m / by && (m == 0 || Divide::of(by)(m - 1) == (m - 1) / by));
+    }
   for (int call = 0; call < 400; ++call) {
-    follow<32, kCacheRows>(call, rng);
-    follow<16, kCacheRows>(call, rng);
+    follow<kCacheKeys, kCacheRows>(call, rng);
     follow<kPrefixKeys, kPrefixRows>(call, rng);
   }
   std::printf("ok\n");

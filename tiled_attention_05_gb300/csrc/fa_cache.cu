@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(128) fa_cache_join_kernel(const fa::CacheJoin 
   const int sub = warp % WARPS;
   const int t = (int)(out % p.T), hq = (int)(out / p.T % p.Hq), b = (int)(out / p.T / p.Hq);
   const int h = hq / p.G, g = hq - h * p.G;
-  const CacheSlots own = fa::cache_slots(p.parts.head[j.own + b], p.G * p.T, kCacheRows, h, g * p.T + t, p.parts.head[j.own_entries].work);
+  const CacheSlots own = fa::cache_slots(p.parts.head[j.own + b], p.G * p.T, kCacheRows, fa::kCacheItem, h, g * p.T + t, p.parts.head[j.own_entries].work);
   CacheSlots pre = {0, 0, 0};
   if (p.S) {
     for (int s0 = 0; s0 < p.S; s0 += 32) {
@@ -220,8 +220,7 @@ __global__ void __launch_bounds__(128) fa_cache_join_kernel(const fa::CacheJoin 
       bool in = false;
       int a = 0, z = 0;
       if (s < p.S) {
-        a = fa::cache_group_start(p, s);
-        z = fa::cache_group_start(p, s + 1);
+        fa::cache_group(p, s, &a, &z);
         in = a <= b && b < z && j.pre.head[s].chunks > 0;
       }
       const unsigned found = __ballot_sync(~0u, in);
@@ -229,7 +228,7 @@ __global__ void __launch_bounds__(128) fa_cache_join_kernel(const fa::CacheJoin 
         const int src = __ffs(found) - 1;
         a = __shfl_sync(~0u, a, src);
         z = __shfl_sync(~0u, z, src);
-        pre = fa::cache_slots(j.pre.head[s0 + src], (z - a) * p.G * p.T, j.pre_rows, h, (b - a) * p.G * p.T + g * p.T + t,
+        pre = fa::cache_slots(j.pre.head[s0 + src], (z - a) * p.G * p.T, j.pre_rows, j.pre_rows == kCacheRows ? fa::kCacheItem : fa::kPrefixItem, h, (b - a) * p.G * p.T + g * p.T + t,
                               j.pre.head[j.pre_entries].work);
         break;
       }
@@ -370,7 +369,7 @@ fa_status attn_shape(const fa_cache_dims& z, const fa_cache_prefix* pre, fa::Cac
     return FA_ERR_UNSUPPORTED;
   const int sms = fa::sm_count() > 0 ? fa::sm_count() : 1;  // (without a device the launch fails)
   *s = fa::cache_shape(z.B, z.Hkv, rows, z.dv, z.quantised, (long long)z.table_pages * z.page, S, (long long)p_cols * z.page, sms);
-  return s->list.items > (1 << 30) || s->pre.items > (1 << 30) || (long long)S + z.B > (1 << 30) ? FA_ERR_UNSUPPORTED : FA_OK;
+  return !s->fits || (long long)S + z.B > (1 << 30) ? FA_ERR_UNSUPPORTED : FA_OK;
 }
 
 }  // namespace
@@ -501,6 +500,8 @@ fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache
   p.Hkv = z.Hkv;
   p.G = z.Hq / z.Hkv;
   p.T = z.T;
+  p.by_T = fa::Divide::of(p.T);
+  p.by_GT = fa::Divide::of(p.G * p.T);
   p.pages = z.pages;
   p.page_log2 = log2_of(z.page);
   p.cols = z.table_pages;
@@ -527,6 +528,7 @@ fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache
     pre.parts = j.pre;
     pre.entries = S;
     pre.min_chunks = fa::kPrefixMinChunks;
+    pre.max_items = (int)s.pre.items;
     err = z.quantised ? fa::launch_cache_prefix_e4m3(pre, z.d, z.dv, s.pre.grid, st)
                       : fa::launch_cache_prefix_bf16(pre, z.d, z.dv, s.pre.grid, st);
     if (err != cudaSuccess) return FA_ERR_CUDA;
@@ -535,6 +537,7 @@ fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache
   p.parts = parts_of(s.list);
   p.entries = p.S + z.B;
   p.min_chunks = fa::kCacheMinChunks;
+  p.max_items = (int)s.list.items;
   err = z.quantised ? fa::launch_cache_attn_e4m3(p, z.d, z.dv, s.list.grid, st)
                     : fa::launch_cache_attn_bf16(p, z.d, z.dv, s.list.grid, st);
   j.p = p;

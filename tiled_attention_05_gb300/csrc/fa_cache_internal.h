@@ -19,22 +19,38 @@ namespace fa {
 // (entries S .. S + B - 1).
 constexpr int kCacheRows = 16;      // query rows of an item: one MMA's
 constexpr int kCacheWarps = 4;      // warps of a CTA; each walks every fourth chunk of its keys
-constexpr int kCacheCtasPerSm = 2;
-// A CTA gets this many chunks of keys at least: two a warp, which is what setting it up
-// and joining its part is worth.
-constexpr int kCacheMinChunks = 8;
+// CTAs an SM.  e4m3 takes about twice the instructions a byte (its codes become fp16), so
+// it needs the warps.
+constexpr int cache_ctas(bool quantised, bool few) { return quantised && few ? 3 : 2; }
+constexpr bool cache_few(long long rows, bool prefixes) { return rows <= 8 && !prefixes; }
+// A CTA gets this much work at least, in chunks of keys, and an item counts as so many
+// chunks more than it has, for its set-up and the joining of its parts.
+constexpr int kCacheMinChunks = 8, kCacheItem = 8;
 // Prefixes of many rows have a list of their own (fa_cache_prefix_kernel), with items of
 // two tiles of 128 rows and chunks of 128 keys.
-constexpr int kPrefixRows = 256, kPrefixKeys = 128, kPrefixMinChunks = 4;
+constexpr int kPrefixRows = 256, kPrefixKeys = 128, kPrefixMinChunks = 4, kPrefixItem = 2;
 
 struct CacheHead {
-  long long work;  // chunks of all entries before this one
-  int item;        // items of all entries before this one
-  int chunks;      // of one item of this entry
+  int work;    // work of all entries before this one
+  int item;    // items of all entries before this one
+  int chunks;  // of one item of this entry
+};
+// Division of numbers below 2^30 by a positive one, by its reciprocal (one short at most).
+struct Divide {
+  unsigned by, inverse;
+  static Divide of(int by) { return {(unsigned)by, by == 1 ? 0xffffffffu : (unsigned)((1ull << 32) / (unsigned)by)}; }
+  FA_WALK int operator()(int n) const {
+#ifdef __CUDA_ARCH__
+    unsigned q = __umulhi((unsigned)n, inverse);
+#else
+    unsigned q = (unsigned)(((unsigned long long)(unsigned)n * inverse) >> 32);
+#endif
+    return (int)(q + ((q + 1) * by <= (unsigned)n));
+  }
 };
 // Parts of items (of `rows` rows each) that a join adds up.
 struct CacheParts {
-  CacheHead* head;  // [entries + 1]; the last one's work: chunks a CTA
+  CacheHead* head;  // [entries + 1]; the last one's work: a CTA's share
   float *ml, *part; // [slots][rows][2]: reference and sum; [slots][rows][dv]: unnormalised O
 };
 
@@ -52,6 +68,8 @@ struct CacheParams {
   int B, Hq, Hkv, G, T, pages, page_log2, cols, S, p_cols, window;
   int entries;     // of the list: S + B, or S (prefixes alone)
   int joined;      // whole items too leave their part for the join
+  Divide by_T, by_GT;  // rows of a head, of a sequence
+  int max_items;   // that the workspace has slots for
   int capped, min_chunks;
   float scale_log2;
   CapParams cap;
@@ -72,9 +90,8 @@ cudaError_t launch_cache_prefix_e4m3(const CacheParams& p, int d, int dv, int gr
 cudaError_t launch_cache_prefix_bf16(const CacheParams& p, int d, int dv, int grid, cudaStream_t stream);
 cudaError_t launch_cache_join(const CacheJoin& j, int dv, cudaStream_t stream);
 
-// Keys of a chunk, the unit of the walk: what one warp holds in one stage of its ring
-// (8 KB at heads of 128).
-constexpr int cache_chunk_keys(bool quantised) { return quantised ? 32 : 16; }
+// Keys of a chunk, the unit of the walk: what one warp holds in one stage of its ring.
+constexpr int kCacheKeys = 16;
 
 // Whether the prefixes go through the kernel that takes 128 rows at a time (`rows`: those
 // of all sequences' kv heads).
@@ -89,6 +106,7 @@ struct CacheList {
   size_t head, ml, part;  // byte offsets
 };
 struct CacheShape {
+  bool fits;       // items and chunks can be counted in 32 bits
   bool apart;      // prefixes are a list of their own (`pre`); else one list holds all
   CacheList list;  // the own keys' (and the prefixes')
   CacheList pre;
@@ -100,30 +118,34 @@ inline CacheShape cache_shape(long long B, long long Hkv, long long rows, int dv
                               long long groups, long long prefix_capacity, int sms) {
   CacheShape s;
   s.apart = prefix_apart(groups, rows * B);
+  s.fits = true;
   size_t at = 0;
   auto take = [&at](size_t bytes) {
     const size_t o = at;
     at += (bytes + 255) / 256 * 256;
     return o;
   };
-  auto lay = [&](CacheList* l, long long entries, long long tiles, long long chunks, int item_rows, int min_chunks, long long ctas) {
+  auto lay = [&](CacheList* l, long long entries, long long tiles, double chunks, int item_rows, int min_chunks, int item, long long ctas) {
     l->items = Hkv * tiles;
-    const long long want = (Hkv * chunks + min_chunks - 1) / min_chunks;
-    l->grid = (int)(want < 1 ? 1 : want < ctas ? want : ctas);
+    chunks += (double)tiles * item;
+    s.fits = s.fits && l->items <= (1 << 30) && Hkv * (double)chunks < (double)(1 << 30);
+    const double want = Hkv * chunks / min_chunks + 1;
+    l->grid = (int)(want < ctas ? want : ctas);
     l->slots = l->items + l->grid;
     l->head = take((size_t)(entries + 1) * sizeof(CacheHead));
     l->ml = take((size_t)l->slots * item_rows * 2 * sizeof(float));
     l->part = take((size_t)l->slots * item_rows * dv * sizeof(float));
   };
-  const long long kc = cache_chunk_keys(quantised), own_tiles = B * ((rows + kCacheRows - 1) / kCacheRows);
+  const long long kc = kCacheKeys, own_tiles = B * ((rows + kCacheRows - 1) / kCacheRows);
   const long long pre_tiles = groups ? groups + rows * B / (s.apart ? kPrefixRows : kCacheRows) : 0;
-  const long long own = own_tiles * ((capacity + kc - 1) / kc);
+  const double own = (double)own_tiles * ((capacity + kc - 1) / kc);
+  const long long ctas = (long long)sms * cache_ctas(quantised, cache_few(rows, groups && !s.apart));
   if (s.apart) {
-    lay(&s.list, B, own_tiles, own, kCacheRows, kCacheMinChunks, (long long)kCacheCtasPerSm * sms);
-    lay(&s.pre, groups, pre_tiles, pre_tiles * ((prefix_capacity + kPrefixKeys - 1) / kPrefixKeys), kPrefixRows, kPrefixMinChunks, sms);
+    lay(&s.list, B, own_tiles, own, kCacheRows, kCacheMinChunks, kCacheItem, ctas);
+    lay(&s.pre, groups, pre_tiles, (double)pre_tiles * ((prefix_capacity + kPrefixKeys - 1) / kPrefixKeys), kPrefixRows, kPrefixMinChunks, kPrefixItem, sms);
   } else {
-    lay(&s.list, groups + B, own_tiles + pre_tiles, own + pre_tiles * ((prefix_capacity + kc - 1) / kc), kCacheRows,
-        kCacheMinChunks, (long long)kCacheCtasPerSm * sms);
+    lay(&s.list, groups + B, own_tiles + pre_tiles, own + (double)pre_tiles * ((prefix_capacity + kc - 1) / kc), kCacheRows,
+        kCacheMinChunks, kCacheItem, ctas);
     s.pre = s.list;
   }
   s.total = at;
@@ -151,17 +173,21 @@ struct CacheEntry {
 FA_WALK int cache_length(const CacheParams& p, int b) {
   return cache_clamp(cache_ld(p.lengths + b), p.cols << p.page_log2);
 }
-FA_WALK int cache_group_start(const CacheParams& p, int s) {
-  return p.p_starts ? cache_ld(p.p_starts + s) : s ? p.B : 0;
+// Sequences [first, end) of group s; none where the starts do not fit.
+FA_WALK void cache_group(const CacheParams& p, int s, int* first, int* end) {
+  *first = p.p_starts ? cache_ld(p.p_starts + s) : 0;
+  *end = p.p_starts ? cache_ld(p.p_starts + s + 1) : p.B;
+  if (*first < 0 || *end > p.B || *first > *end) *first = *end = 0;
 }
 
 template <int KC>
-FA_WALK CacheEntry cache_entry(const CacheParams& p, int e, bool groups_ok) {
+FA_WALK CacheEntry cache_entry(const CacheParams& p, int e) {
   CacheEntry n;
   int first_key;  // the first that a row may see, with a window
   if (e < p.S) {
-    n.first = cache_group_start(p, e);
-    n.rows = groups_ok ? (cache_group_start(p, e + 1) - n.first) * p.G * p.T : 0;
+    int end;
+    cache_group(p, e, &n.first, &end);
+    n.rows = (end - n.first) * p.G * p.T;
     n.keys = cache_clamp(cache_ld(p.p_lengths + e), p.p_cols << p.page_log2);
     first_key = n.keys - p.window + 1;  // (the first row of all stands behind the prefix)
   } else {
@@ -176,154 +202,150 @@ FA_WALK CacheEntry cache_entry(const CacheParams& p, int e, bool groups_ok) {
   return n;
 }
 
-// A place in the list of chunks: that of chunk c of the item of tile r, kv head h, entry e.
-template <int KC, int ROWS>
+// A place in the list: that of chunk c of the item of tile r, kv head h, entry e.  ITEM:
+// what an item counts beside its chunks, behind them.
+template <int KC, int ROWS, int ITEM>
 struct CacheCursor {
-  long long at;  // in the whole list
+  int at;  // in the whole list
   int e, h, r, c;
+  int item;  // ordinal of the item
   CacheEntry n;
-  FA_WALK void advance(const CacheParams& p, bool groups_ok, int k) {
-    at += k;
-    c += k;
-    while (c >= n.chunks) {
-      c -= n.chunks;
-      if (++r < n.tiles(ROWS)) continue;
-      r = 0;
-      if (++h < p.Hkv) continue;
-      h = 0;
-      do {
-        if (++e >= p.entries) {  // the list's end: stay there
-          n.chunks = 0x7fffffff;
-          return;
-        }
-        n = cache_entry<KC>(p, e, groups_ok);
-      } while (n.chunks == 0);
+  FA_WALK int end(int share_end) const { return c + share_end - at < n.chunks ? c + share_end - at : n.chunks; }
+  FA_WALK void next(const CacheParams& p) {  // the next item's first chunk
+    at += n.chunks + ITEM - c;
+    c = 0;
+    ++item;
+    if (++r < n.tiles(ROWS)) return;
+    r = 0;
+    if (++h < p.Hkv) return;
+    h = 0;
+    while (++e < p.entries) {
+      n = cache_entry<KC>(p, e);
+      if (n.chunks) return;
+      item += p.Hkv * n.tiles(ROWS);
     }
+    at = 0x3fffffff;  // the list's end
+  }
+  // To the share's start `in` units into entry e's items, the first of which is `first`.
+  FA_WALK void start(const CacheParams& p, int entry, int first, int begin, int in) {
+    e = entry;
+    n = cache_entry<KC>(p, e);
+    const int o = in / (n.chunks + ITEM), tiles = n.tiles(ROWS);
+    at = begin;
+    c = in - o * (n.chunks + ITEM);
+    h = o / tiles;
+    r = o - h * tiles;
+    item = first + o;
+    if (c >= n.chunks) next(p);
   }
 };
 
 // Where the join finds the parts of row `row` of an entry's kv head h: `n` slots from
-// `slot` on (`per`: chunks a CTA).
+// `slot` on (`per`: a CTA's share).
 struct CacheSlots {
   long long slot;
   int n, row;  // parts, row within the tile
 };
-FA_WALK CacheSlots cache_slots(const CacheHead& e, int rows, int item_rows, int h, int row, long long per) {
+FA_WALK CacheSlots cache_slots(const CacheHead& e, int rows, int item_rows, int item_work, int h, int row, int per) {
   CacheSlots l = {0, 0, row % item_rows};
   if (e.chunks == 0) return l;
   const int o = h * ((rows + item_rows - 1) / item_rows) + row / item_rows;
-  const long long at = e.work + (long long)o * e.chunks, c0 = at / per, c1 = (at + e.chunks - 1) / per;
+  const int at = e.work + o * (e.chunks + item_work), c0 = at / per, c1 = (at + e.chunks - 1) / per;
   l.slot = (long long)e.item + o + c0;
-  l.n = (int)(c1 - c0) + 1;
+  l.n = c1 - c0 + 1;
   return l;
 }
 
 #ifdef __CUDACC__
-// Whether the groups' starts are a list of disjoint runs of sequences.  Every thread of
-// the CTA gets the answer.
-__device__ __forceinline__ bool cache_groups_ok(const CacheParams& p) {
-  bool ok = true;
-  if (p.p_starts)
-    for (int s = threadIdx.x; s < p.S; s += blockDim.x) {
-      const int a = __ldg(p.p_starts + s), z = __ldg(p.p_starts + s + 1);
-      ok = ok && a >= 0 && a <= z && z <= p.B;
-    }
-  return p.S == 0 || __syncthreads_and(ok);
-}
-
 // An index that does not fit: the device status word says so (a timeout stays).
 __device__ __forceinline__ void cache_bad(int* status) { atomicCAS(status, 0, fa_ptx::DEV_BAD_TABLE); }
+
 // The CTA's share [begin, end) of the list, and its first place.  CTA 0 also writes
-// where each entry begins, for the join.
-template <int KC, int ROWS>
+// where each entry begins, for the join.  (Code that runs once is short rather than
+// fast: an instruction that no CTA has run yet costs some 10 to 20 cycles.)
+template <class Cursor>
 struct CacheShare {
-  long long begin, end;
-  CacheCursor<KC, ROWS> start;
-  int item;  // ordinal of the first place's item
+  int begin, end;
+  Cursor start;
 };
 
-template <int KC, int ROWS, int THREADS>
-__device__ __forceinline__ CacheShare<KC, ROWS> cache_share(const CacheParams& p, bool groups_ok) {
+template <int KC, int ROWS, int ITEM, int THREADS>
+__device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(const CacheParams& p) {
   constexpr int WARPS = THREADS / 32;
-  __shared__ long long s_work[WARPS], s_found_work;
-  __shared__ int s_item[WARPS], s_found_e, s_found_item;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, entries = p.entries;
-  long long total = 0;
-  for (int e = threadIdx.x; e < entries; e += THREADS) {
-    const CacheEntry n = cache_entry<KC>(p, e, groups_ok);
-    total += (long long)p.Hkv * n.tiles(ROWS) * n.chunks;
+  __shared__ long long s_sum[WARPS][2];
+  __shared__ int s_found[3];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int each = (p.entries + THREADS - 1) / THREADS;
+  const int e0 = min((int)threadIdx.x * each, p.entries), e1 = min(e0 + each, p.entries);
+  long long sum[2] = {0, 0};  // work and items of this thread's entries
+#pragma unroll 1
+  for (int e = e0; e < e1; ++e) {
+    const CacheEntry n = cache_entry<KC>(p, e);
+    const int items = p.Hkv * n.tiles(ROWS);
+    if (n.chunks) sum[0] += (long long)items * (n.chunks + ITEM);
+    sum[1] += items;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
-  if (lane == 0) s_work[warp] = total;
+  const long long mine = sum[0], my_items = sum[1];
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(~0u, sum[0], o), b = __shfl_up_sync(~0u, sum[1], o);
+    if (lane >= o) sum[0] += a, sum[1] += b;
+  }
+  if (lane == 31) s_sum[warp][0] = sum[0], s_sum[warp][1] = sum[1];
   __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) total += s_work[w];
-  __syncthreads();
-  CacheShare<KC, ROWS> s;
-  long long per = (total + gridDim.x - 1) / gridDim.x;
-  per = per < p.min_chunks ? p.min_chunks : per;
-  s.begin = per * blockIdx.x;
-  s.end = s.begin + per < total ? s.begin + per : total;
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    p.parts.head[entries].work = per;
-    bool bad = !groups_ok;
-    for (int e = 0; e < p.S && !bad; ++e) bad = __ldg(p.p_lengths + e) > (p.p_cols << p.page_log2);
+  long long total = 0, items = 0, base = sum[0] - mine, item = sum[1] - my_items;
+#pragma unroll 1
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) base += s_sum[w][0], item += s_sum[w][1];
+    total += s_sum[w][0];
+    items += s_sum[w][1];
+  }
+  // groups that overlap can ask for more than there is room for: then there is no work
+  const bool room = items <= p.max_items && total < (1 << 30);
+  CacheShare<CacheCursor<KC, ROWS, ITEM>> s;
+  const int all = room ? (int)total : 0;
+  const int per = max((int)(((unsigned)all + gridDim.x - 1) / gridDim.x), p.min_chunks);
+  s.begin = min(per * (int)blockIdx.x, all);
+  s.end = min(s.begin + per, all);
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) p.parts.head[p.entries].work = per;
+    bool bad = !room;
+    int w = (int)base, i = (int)item;
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+      const CacheEntry n = cache_entry<KC>(p, e);
+      const int own = p.Hkv * n.tiles(ROWS);
+      p.parts.head[e] = {w, i, room ? n.chunks : 0};
+      if (n.chunks) w += own * (n.chunks + ITEM);
+      i += own;
+      if (e < p.S) {  // (the runs are in order and disjoint)
+        bad = bad || __ldg(p.p_lengths + e) > (p.p_cols << p.page_log2);
+        if (p.p_starts) {
+          const int a = __ldg(p.p_starts + e), z = __ldg(p.p_starts + e + 1);
+          bad = bad || a < 0 || a > z || z > p.B;
+        }
+      } else {
+        bad = bad || __ldg(p.lengths + e - p.S) > (p.cols << p.page_log2);
+      }
+    }
     if (bad) cache_bad(p.status);
   }
-  if (s.begin >= s.end && blockIdx.x) return s;
-  long long base = 0;
-  int item = 0;
-  for (int e0 = 0; e0 < entries; e0 += THREADS) {
-    const int e = e0 + threadIdx.x;
-    long long work = 0;
-    int items = 0;
-    CacheEntry n = {};
-    if (e < entries) {
-      n = cache_entry<KC>(p, e, groups_ok);
-      items = p.Hkv * n.tiles(ROWS);
-      work = (long long)items * n.chunks;
-      if (blockIdx.x == 0 && e >= p.S && __ldg(p.lengths + e - p.S) > (p.cols << p.page_log2)) cache_bad(p.status);
+  if (base <= s.begin && s.begin < base + mine && room) {
+    int e = e0, w = (int)base, i = (int)item;
+#pragma unroll 1
+    for (;; ++e) {
+      const CacheEntry n = cache_entry<KC>(p, e);
+      const int own = p.Hkv * n.tiles(ROWS);
+      const int all = n.chunks ? own * (n.chunks + ITEM) : 0;
+      if (s.begin < w + all) break;
+      w += all;
+      i += own;
     }
-    long long w = work;
-    int i = items;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long wo = __shfl_up_sync(~0u, w, o);
-      const int io = __shfl_up_sync(~0u, i, o);
-      if (lane >= o) w += wo, i += io;
-    }
-    if (lane == 31) s_work[warp] = w, s_item[warp] = i;
-    __syncthreads();
-    long long all = 0;
-    int all_items = 0;
-#pragma unroll
-    for (int v = 0; v < WARPS; ++v) {
-      if (v < warp) w += s_work[v], i += s_item[v];
-      all += s_work[v];
-      all_items += s_item[v];
-    }
-    w += base - work;
-    i += item - items;
-    if (blockIdx.x == 0 && e < entries) p.parts.head[e] = {w, i, n.chunks};
-    if (work && w <= s.begin && s.begin < w + work) s_found_e = e, s_found_work = w, s_found_item = i;
-    base += all;
-    item += all_items;
-    __syncthreads();
-    if (blockIdx.x && s.begin < base) break;
+    s_found[0] = e, s_found[1] = w, s_found[2] = i;
   }
+  __syncthreads();
   if (s.begin >= s.end) return s;
-  CacheCursor<KC, ROWS>& c = s.start;
-  c.e = s_found_e;
-  c.n = cache_entry<KC>(p, c.e, groups_ok);
-  const long long in = s.begin - s_found_work;
-  const int o = (int)(in / c.n.chunks), tiles = c.n.tiles(ROWS);
-  c.at = s.begin;
-  c.c = (int)(in - (long long)o * c.n.chunks);
-  c.h = o / tiles;
-  c.r = o - c.h * tiles;
-  s.item = s_found_item + o;
+  s.start.start(p, s_found[0], s_found[2], s.begin, s.begin - s_found[1]);
   return s;
 }
 
@@ -337,9 +359,9 @@ __device__ __forceinline__ CacheRow cache_row(const CacheParams& p, const CacheE
   CacheRow r;
   r.valid = row < n.rows;
   if (!r.valid) row = 0;
-  const int per = p.G * p.T, s = row / per, left = row - s * per;
+  const int s = p.by_GT(row), left = row - s * p.G * p.T;
   r.b = n.first + s;
-  r.g = left / p.T;
+  r.g = p.by_T(left);
   r.t = left - r.g * p.T;
   return r;
 }

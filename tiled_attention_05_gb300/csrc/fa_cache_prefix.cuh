@@ -63,6 +63,14 @@ struct PrefixCfg {
 __host__ __device__ constexpr uint32_t idesc(bool f16, int M, int N, int b_mn) {
   return f16 ? idesc_bf16(M, N, 0, b_mn) & ~((1u << 7) | (1u << 10)) : idesc_bf16(M, N, 0, b_mn);
 }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -88,14 +96,13 @@ template <int D, int DV, bool Q8, bool MODS>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_cache_prefix_kernel(const CacheParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = PrefixCfg<D, DV, Q8>;
-  using Cursor = fa::CacheCursor<BN, fa::kPrefixRows>;
+  using Cursor = fa::CacheCursor<BN, fa::kPrefixRows, fa::kPrefixItem>;
   constexpr int NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
   grid_next();
   grid_previous();
-  const bool groups_ok = fa::cache_groups_ok(p);
-  const auto share = fa::cache_share<BN, fa::kPrefixRows, kThreads>(p, groups_ok);
-  if (share.begin >= share.end) return;
+  const auto share = fa::cache_share<BN, fa::kPrefixRows, fa::kPrefixItem, kThreads>(p);
+  if (share.begin >= share.end || share.start.at >= share.end) return;
 
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [NS] a slot holds its tile
   uint64_t* empty = full + NS;     // [NS]
@@ -144,8 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int c0, c1;
   };
   auto item_of = [&](const Cursor& it) {
-    const long long left = share.end - it.at;
-    return Item{it.c, left < it.n.chunks - it.c ? it.c + (int)left : it.n.chunks};
+    return Item{it.c, it.end(share.end)};
   };
   auto tile_active = [](const Cursor& it, int x) { return it.n.rows > it.r * fa::kPrefixRows + x * BM; };
 
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_commit(&o_done[x]);
             }
           u += 2 * tiles;
-          it.advance(p, groups_ok, tiles);
+          it.next(p);
         }
         // Let every MMA issued above finish before TMEM is released.
         mma_commit(drain);
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n.u;
         n.v = !n.v;
         if (n.v || ++n.c < n.m.c1) return true;
-        n.it.advance(p, groups_ok, n.m.c1 - n.m.c0);
+        n.it.next(p);
         if (n.it.at >= share.end) return false;
         n.m = item_of(n.it);
         n.c = n.m.c0;
@@ -364,7 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + x * 128 + lane_base, tO = tmem + 256 + x * 128 + lane_base;
     const float NEG_INF = -__int_as_float(0x7f800000);
     int ns = 0, no = 0, nb = 0;  // phases waited for; scale buffers written
-    int item = share.item;
     bool ok = run;
     // Loads from TMEM are a warp's, and the barrier that hands the scales round is the
     // tile's: those who meet there leave together when one of them gave up.
@@ -381,35 +386,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         float unit = MODS && p.capped ? 1.f : p.scale_log2;
         const float slope = MODS && p.slopes ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
         const int abs0 = it.n.keys + pos;
-        {  // the warp's 32 rows of Q into shared memory (e4m3: as fp16, a row's largest value brought to [1, 2))
+        {  // the warp's 32 rows of Q into shared memory
           constexpr int P = D / 8, STEP = 32 / P;  // lanes a row, rows at a time
-          const int mine = w.valid ? (w.b * p.Hq + head) * p.T + w.t : -1;
+          const int mine = w.valid ? (w.b * p.Hq + head) * p.T + w.t : -1, piece = lane % P;
           const uint32_t dst = smem_u32(smem) + x * C::Q_BYTES;
-          uint4 q[32 / STEP];
-#pragma unroll
-          for (int k = 0; k < 32 / STEP; ++k) {
-            const int from = __shfl_sync(~0u, mine, k * STEP + lane / P);
-            q[k] = from >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.Q + (long long)from * D) + lane % P) : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+          for (int k = 0; k < 32; k += STEP) {
+            const int from = __shfl_sync(~0u, mine, k + lane / P), row = quad * 32 + k + lane / P;
+            cp16(dst + (piece >> 3) * (BM * 128) + sw128_offset(row, piece & 7), p.Q + (from < 0 ? 0ll : (long long)from * D + piece * 8),
+                 from >= 0);
           }
+          cp_commit();
+          cp_wait<0>();
+          if constexpr (Q8) {  // as fp16, a row's largest value brought to [1, 2); a row a thread
+            __syncwarp();
+            uint32_t top = 0;
+#pragma unroll 1
+            for (int k = 0; k < P; ++k) {
+              const float4 v = ld_shared_f4(smem + x * C::Q_BYTES + (k >> 3) * (BM * 128) + sw128_offset(r, k & 7));
+              const float a[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int k = 0; k < 32 / STEP; ++k) {
-            uint32_t a[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
-            if constexpr (Q8) {
-              uint32_t top = 0;
-#pragma unroll
-              for (int y = 0; y < 4; ++y) top = max(top, max(a[y] & 0x7fffu, (a[y] >> 16) & 0x7fffu));
-#pragma unroll
-              for (int o = P / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-              const int ex = min(max((int)(top >> 7), 1), 253);
-              const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+              for (int y = 0; y < 4; ++y)
+                top = max(top, max(__float_as_uint(a[y]) & 0x7fffu, (__float_as_uint(a[y]) >> 16) & 0x7fffu));
+            }
+            const int ex = min(max((int)(top >> 7), 1), 253);
+            const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+            unit *= __uint_as_float((uint32_t)ex << 23);
+#pragma unroll 1
+            for (int k = 0; k < P; ++k) {
+              const uint32_t at = (k >> 3) * (BM * 128) + sw128_offset(r, k & 7);
+              const float4 v = ld_shared_f4(smem + x * C::Q_BYTES + at);
+              uint32_t a[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
 #pragma unroll
               for (int y = 0; y < 4; ++y)
                 a[y] = pack_f16x2(__uint_as_float(a[y] << 16) * down, __uint_as_float(a[y] & 0xffff0000u) * down);
-              const int theirs = __shfl_sync(~0u, ex, (lane % STEP) * P);  // row k * STEP + lane % STEP
-              if (lane / STEP == k) unit *= __uint_as_float((uint32_t)theirs << 23);
+              st_shared_v4(dst + at, a[0], a[1], a[2], a[3]);
             }
-            const int row = quad * 32 + k * STEP + lane / P, piece = lane % P;
-            st_shared_v4(dst + (piece >> 3) * (BM * 128) + sw128_offset(row, piece & 7), a[0], a[1], a[2], a[3]);
           }
           fence_async_smem();
           mbar_arrive(&q_full[x]);
@@ -446,85 +458,138 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++ns;
           tc_fence_after();
           const int kv0 = (it.n.chunk0 + m.c0 + j) * BN;
-          uint32_t sr[BN];
-#pragma unroll
-          for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-          tmem_wait_ld();
+          float mt = NEG_INF, m_new, base, sum;
+          bool rescale, warp_rescale;
+          auto refer = [&]() {  // the reference of this tile's weights, from its maximum
+            m_new = mt > m_ref + kRescaleThreshold ? mt : m_ref;  // also taken when m_ref == -inf
+            rescale = j > 0 && m_new != m_ref && m_ref != NEG_INF;
+            warp_rescale = __any_sync(~0u, rescale);
+            base = m_new == NEG_INF ? 0.f : m_new;
+          };
+          const int lim = it.n.keys - kv0;  // columns that are keys
           if constexpr (Q8 || MODS) {
+            // Two passes of 32 columns at a time: the scores in log2 units, back into TMEM, and
+            // their maximum; then the weights.  (With the row in registers the code is four
+            // times as long, and short calls run it cold.)
+            float top[2] = {NEG_INF, NEG_INF};
+#pragma unroll 1
+            for (int c = 0; c < BN; c += 32) {
+              uint32_t s[32];
+              tmem_ld32(tS + c, s);
+              tmem_wait_ld();
+              const uint64_t unit2 = f2_pack(unit, unit);
 #pragma unroll
-            for (int c = 0; c < BN; c += 4) {
-              float t[4];
-              float4 k4 = make_float4(1.f, 1.f, 1.f, 1.f), l4 = make_float4(0.f, 0.f, 0.f, 0.f);
-              if constexpr (Q8) k4 = ld_shared_f4(sc + c), l4 = ld_shared_f4(sc + BN + c);
-              const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, ll[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                t[y] = __uint_as_float(sr[c + y]) * unit;
+              for (int e = 0; e < 32; e += 4) {
+                uint64_t t[2] = {f2_mul(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), unit2),
+                                 f2_mul(f2_pack(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), unit2)};
+                float4 k4, l4;
+                if constexpr (Q8) k4 = ld_shared_f4(sc + c + e), l4 = ld_shared_f4(sc + BN + c + e);
                 if constexpr (!MODS) {
-                  t[y] = fmaf(t[y], kk[y], ll[y]);
+                  t[0] = f2_fma(t[0], f2_pack(k4.x, k4.y), f2_pack(l4.x, l4.y));
+                  t[1] = f2_fma(t[1], f2_pack(k4.z, k4.w), f2_pack(l4.z, l4.w));
                 } else {
-                  if constexpr (Q8) t[y] *= kk[y];
-                  if (p.capped) t[y] = capped(p.cap, t[y]);
-                  const int far = abs0 - (kv0 + c + y);
-                  t[y] -= slope * (float)far;
-                  if (p.window && far >= p.window) t[y] = NEG_INF;
-                  if constexpr (Q8) t[y] += ll[y];
+                  if constexpr (Q8) t[0] = f2_mul(t[0], f2_pack(k4.x, k4.y)), t[1] = f2_mul(t[1], f2_pack(k4.z, k4.w));
+                  float v[4] = {f2_lo(t[0]), f2_hi(t[0]), f2_lo(t[1]), f2_hi(t[1])};
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) {
+                    if (p.capped) v[y] = capped(p.cap, v[y]);
+                    const int far = abs0 - (kv0 + c + e + y);
+                    v[y] -= slope * (float)far;
+                    if (p.window && far >= p.window) v[y] = NEG_INF;
+                  }
+                  t[0] = f2_pack(v[0], v[1]), t[1] = f2_pack(v[2], v[3]);
+                  if constexpr (Q8) t[0] = f2_add(t[0], f2_pack(l4.x, l4.y)), t[1] = f2_add(t[1], f2_pack(l4.z, l4.w));
                 }
-                sr[c + y] = __float_as_uint(t[y]);
+                s[e] = __float_as_uint(f2_lo(t[0])), s[e + 1] = __float_as_uint(f2_hi(t[0]));
+                s[e + 2] = __float_as_uint(f2_lo(t[1])), s[e + 3] = __float_as_uint(f2_hi(t[1]));
               }
+              if (c + 32 > lim) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (c + e >= lim) s[e] = __float_as_uint(NEG_INF);
+              }
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                top[0] = fmax3(top[0], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                top[1] = fmax3(top[1], __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+              }
+              tmem_st32(tS + c, s);
             }
-          }
-          if (kv0 + BN > it.n.keys) {
+            tmem_wait_st();
+            mt = fmaxf(top[0], top[1]);
+            refer();
+            const uint64_t nbase2 = f2_pack(-base, -base);
+            uint64_t rs[2] = {0ull, 0ull};
+#pragma unroll 1
+            for (int c = 0; c < BN; c += 32) {
+              uint32_t s[32], pk[16];
+              tmem_ld32(tS + c, s);
+              tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < BN; ++c)
-              if (kv0 + c >= it.n.keys) sr[c] = __float_as_uint(NEG_INF);
-          }
-          float pm[8];
+              for (int e = 0; e < 32; e += 4) {
+                const uint64_t x0 = f2_add(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), nbase2);
+                const uint64_t x1 = f2_add(f2_pack(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), nbase2);
+                const float e0 = ex2(f2_lo(x0)), e1 = ex2(f2_hi(x0)), e2 = ex2(f2_lo(x1)), e3 = ex2(f2_hi(x1));
+                if constexpr (Q8) {
+                  const float4 i4 = ld_shared_f4(sc + 2 * BN + c + e);
+                  rs[0] = f2_fma(f2_pack(e0, e1), f2_pack(i4.x, i4.y), rs[0]);
+                  rs[1] = f2_fma(f2_pack(e2, e3), f2_pack(i4.z, i4.w), rs[1]);
+                } else {
+                  rs[0] = f2_add(rs[0], f2_pack(e0, e1));
+                  rs[1] = f2_add(rs[1], f2_pack(e2, e3));
+                }
+                pk[e / 2] = Q8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+                pk[e / 2 + 1] = Q8 ? pack_f16x2(e2, e3) : pack_bf16x2(e2, e3);
+              }
+              tmem_st16(tS + c / 2, pk);  // (over columns that have been read)
+            }
+            const uint64_t rs2 = f2_add(rs[0], rs[1]);
+            sum = f2_lo(rs2) + f2_hi(rs2);
+          } else {
+            uint32_t sr[BN];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) pm[k] = __uint_as_float(sr[k]);
+            for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+            tmem_wait_ld();
+            if (lim < BN) {
 #pragma unroll
-          for (int c = 8; c + 16 <= BN; c += 16)
+              for (int c = 0; c < BN; ++c)
+                if (c >= lim) sr[c] = __float_as_uint(NEG_INF);
+            }
+            float pm[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) pm[k] = fmax3(pm[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
+            for (int k = 0; k < 8; ++k) pm[k] = __uint_as_float(sr[k]);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], __uint_as_float(sr[BN - 8 + k]));
-          const float sl = Q8 || MODS ? 1.f : unit;  // what brings sr to log2 units
-          const float mt = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * sl;
-          float m_new = m_ref;
-          if (mt > m_ref + kRescaleThreshold) m_new = mt;  // also taken when m_ref == -inf
-          const bool rescale = j > 0 && m_new != m_ref && m_ref != NEG_INF;
-          const bool warp_rescale = __any_sync(~0u, rescale);
-          const float base = m_new == NEG_INF ? 0.f : m_new;
-          const uint64_t sl2 = f2_pack(sl, sl), nbase2 = f2_pack(-base, -base);
-          uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
+            for (int c = 8; c + 16 <= BN; c += 16)
 #pragma unroll
-          for (int c = 0; c < BN / 32; ++c) {
-            uint32_t pk[16];
+              for (int k = 0; k < 8; ++k) pm[k] = fmax3(pm[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              float4 i4 = make_float4(1.f, 1.f, 1.f, 1.f);
-              if constexpr (Q8) i4 = ld_shared_f4(sc + 2 * BN + 32 * c + 2 * e);
+            for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], __uint_as_float(sr[BN - 8 + k]));
+            mt = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * unit;
+            refer();
+            const uint64_t unit2 = f2_pack(unit, unit), nbase2 = f2_pack(-base, -base);
+            uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const uint64_t s2 = f2_pack(__uint_as_float(sr[32 * c + 2 * e + 2 * y]), __uint_as_float(sr[32 * c + 2 * e + 2 * y + 1]));
-                const uint64_t xv = Q8 || MODS ? f2_add(s2, nbase2) : f2_fma(s2, sl2, nbase2);
+            for (int c = 0; c < BN / 32; ++c) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const uint64_t xv = f2_fma(
+                    f2_pack(__uint_as_float(sr[32 * c + 2 * e]), __uint_as_float(sr[32 * c + 2 * e + 1])), unit2, nbase2);
                 const float e0 = ex2(f2_lo(xv)), e1 = ex2(f2_hi(xv));
-                if constexpr (Q8)
-                  rs[e / 2 & 3] = f2_fma(f2_pack(e0, e1), y ? f2_pack(i4.z, i4.w) : f2_pack(i4.x, i4.y), rs[e / 2 & 3]);
-                else
-                  rs[e / 2 & 3] = f2_add(rs[e / 2 & 3], f2_pack(e0, e1));
-                pk[e + y] = Q8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+                rs[e & 3] = f2_add(rs[e & 3], f2_pack(e0, e1));
+                pk[e] = pack_bf16x2(e0, e1);
               }
+              tmem_st16(tS + 16 * c, pk);
             }
-            tmem_st16(tS + 16 * c, pk);
+            const uint64_t rs2 = f2_add(f2_add(rs[0], rs[1]), f2_add(rs[2], rs[3]));
+            sum = f2_lo(rs2) + f2_hi(rs2);
           }
-          const uint64_t rs2 = f2_add(f2_add(rs[0], rs[1]), f2_add(rs[2], rs[3]));
           // O_X is idle here: the P.V of tile j - 1 completed before S_X(j) did.
           const float alpha = m_new == m_ref ? 1.f : m_ref == NEG_INF ? 0.f : ex2(m_ref - m_new);
-          l = l * alpha + f2_lo(rs2) + f2_hi(rs2);
+          l = l * alpha + sum;
           if (warp_rescale) {
             const float a = rescale ? alpha : 1.f;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DV / 32; ++c) {
               uint32_t o[32];
               tmem_ld32(tO + c * 32, o);
@@ -545,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           // A padding row's part is none.
           const bool none = pos < 0;
-          const long long at = ((long long)item + blockIdx.x) * fa::kPrefixRows + x * BM + r;
+          const long long at = ((long long)it.item + blockIdx.x) * fa::kPrefixRows + x * BM + r;
           if (w.valid) *reinterpret_cast<float2*>(p.parts.ml + at * 2) = none ? make_float2(NEG_INF, 0.f) : make_float2(m_ref, l);
           // 32 columns at a time through this warp's share of Q_X, which is free now, so that a
           // row's 128 bytes leave together.
@@ -574,10 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();  // (the next item's first P.V into O_X follows this warpgroup's next P)
         }
       }
-      item += m.c1 == it.n.chunks;
-      const int old = it.e;
-      it.advance(p, groups_ok, tiles);
-      for (int e = old + 1; e < it.e && e < p.entries; ++e) item += p.Hkv * fa::cache_entry<BN>(p, e, groups_ok).tiles(fa::kPrefixRows);
+      it.next(p);
     }
   }
   tc_fence_before();
