@@ -207,11 +207,10 @@ __global__ void __launch_bounds__(128) fa_cache_join_kernel(const fa::CacheJoin 
   grid_previous();
   const CacheParams& p = j.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long out = (long long)blockIdx.x * (4 / WARPS) + warp / WARPS, rows = (long long)p.B * p.Hq * p.T;
-  if (out >= rows) return;  // (with WARPS 4 a block has one row)
+  const int out = blockIdx.x * (4 / WARPS) + warp / WARPS;
+  if (out >= p.B * p.Hq * p.T) return;  // (with WARPS 4 a block has one row)
   const int sub = warp % WARPS;
-  const int t = (int)(out % p.T), hq = (int)(out / p.T % p.Hq), b = (int)(out / p.T / p.Hq);
-  const int h = hq / p.G, g = hq - h * p.G;
+  const int bh = p.by_T(out), t = out - bh * p.T, b = j.by_Hq(bh), hq = bh - b * p.Hq, h = j.by_G(hq), g = hq - h * p.G;
   const CacheSlots own = fa::cache_slots(p.parts.head[j.own + b], p.G * p.T, kCacheRows, fa::kCacheItem, h, g * p.T + t, p.parts.head[j.own_entries].work);
   CacheSlots pre = {0, 0, 0};
   if (p.S) {
@@ -287,7 +286,7 @@ __global__ void __launch_bounds__(128) fa_cache_join_kernel(const fa::CacheJoin 
   uint32_t w[CH / 2];
 #pragma unroll
   for (int k = 0; k < CH; k += 2) w[k / 2] = pack_bf16x2(acc[k] * f, acc[k + 1] * f);
-  uint16_t* dst = p.O + out * DV + lane * CH;
+  uint16_t* dst = p.O + (long long)out * DV + lane * CH;
   if constexpr (CH == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
   else
@@ -365,7 +364,7 @@ fa_status attn_shape(const fa_cache_dims& z, const fa_cache_prefix* pre, fa::Cac
   if ((long long)p_cols * z.page > (1 << 30)) return FA_ERR_UNSUPPORTED;
   // rows are counted in 32 bits, those of a whole group among them
   const long long rows = z.Hkv ? (long long)(z.Hq / z.Hkv) * z.T : 0;
-  if ((long long)z.B * z.Hq > INT_MAX || rows * z.B > (1 << 30) || (long long)z.B * z.Hq * z.T > INT_MAX)
+  if ((long long)z.B * z.Hq > INT_MAX || rows * z.B > (1 << 30) || (long long)z.B * z.Hq * z.T > (1 << 30))
     return FA_ERR_UNSUPPORTED;
   const int sms = fa::sm_count() > 0 ? fa::sm_count() : 1;  // (without a device the launch fails)
   *s = fa::cache_shape(z.B, z.Hkv, rows, z.dv, z.quantised, (long long)z.table_pages * z.page, S, (long long)p_cols * z.page, sms);
@@ -524,6 +523,10 @@ fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache
   fa::CacheJoin j = {};
   j.pre = parts_of(s.pre);
   if (s.apart) {
+    p.sms = fa::sm_count();
+    p.groups = S;
+    p.per_sm = fa::cache_ctas(z.quantised, fa::cache_few(p.G * p.T, false));
+    p.chunk_cost = fa::cache_chunk_cost(z.d, z.dv, z.quantised);
     fa::CacheParams pre = p;
     pre.parts = j.pre;
     pre.entries = S;
@@ -543,6 +546,8 @@ fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache
   j.p = p;
   j.p.S = S;
   j.own = p.S;
+  j.by_Hq = fa::Divide::of(z.Hq);
+  j.by_G = fa::Divide::of(p.G);
   j.own_entries = p.entries;
   j.pre_rows = s.apart ? fa::kPrefixRows : kCacheRows;
   j.pre_entries = s.apart ? S : p.entries;

@@ -67,6 +67,11 @@ struct CacheParams {
   int* status;
   int B, Hq, Hkv, G, T, pages, page_log2, cols, S, p_cols, window;
   int entries;     // of the list: S + B, or S (prefixes alone)
+  // Prefixes of many rows and the own keys run side by side, on SMs of their own: the two
+  // kernels divide `sms` between them by their work (0: a kernel has all).
+  int sms, groups;  // groups: S, also for the kernel of the own keys (whose S is 0)
+  int chunk_cost;   // of a chunk of own keys; of a prefix's 1024
+  int per_sm;       // CTAs of the own keys' kernel on an SM
   int joined;      // whole items too leave their part for the join
   Divide by_T, by_GT;  // rows of a head, of a sequence
   int max_items;   // that the workspace has slots for
@@ -81,6 +86,7 @@ struct CacheJoin {
   int own_entries;     // of that list
   CacheParts pre;      // parts of the prefixes, in items of pre_rows rows
   int pre_rows, pre_entries;
+  Divide by_Hq, by_G;
 };
 
 // The kernels, by the type of the cache, and the join of their parts.
@@ -93,9 +99,14 @@ cudaError_t launch_cache_join(const CacheJoin& j, int dv, cudaStream_t stream);
 // Keys of a chunk, the unit of the walk: what one warp holds in one stage of its ring.
 constexpr int kCacheKeys = 16;
 
+// What an SM takes for a chunk of own keys (its bytes at ~80 a ns), where a prefix's tile
+// pair of heads of 128, 1.5 us, is 1024.
+constexpr int cache_chunk_cost(int d, int dv, bool quantised) {
+  return kCacheKeys * (quantised ? d + dv + 8 : 2 * (d + dv)) * 1024 / (80 * 1500) * 256 / (d + dv);
+}
 // Whether the prefixes go through the kernel that takes 128 rows at a time (`rows`: those
 // of all sequences' kv heads).
-inline bool prefix_apart(long long groups, long long rows) { return groups > 0 && rows > 32 * groups; }
+inline bool prefix_apart(long long groups, long long rows) { return groups > 0 && rows > kCacheRows * groups; }
 
 // Slots of the workspace and CTAs of a call, from what the host knows.  A part's slot is
 // its item's ordinal + its CTA's: walking through the list, each next part raises one of
@@ -180,26 +191,33 @@ FA_WALK void cache_group(const CacheParams& p, int s, int* first, int* end) {
   if (*first < 0 || *end > p.B || *first > *end) *first = *end = 0;
 }
 
+FA_WALK void cache_span(CacheEntry* n, int first_key, int KC) {
+  n->chunk0 = first_key > 0 ? first_key / KC : 0;
+  n->chunks = n->rows > 0 ? (n->keys + KC - 1) / KC - n->chunk0 : 0;
+  if (n->chunks < 0) n->chunks = 0;
+}
+template <int KC>
+FA_WALK CacheEntry cache_prefix(const CacheParams& p, int s) {
+  CacheEntry n;
+  int end;
+  cache_group(p, s, &n.first, &end);
+  n.rows = (end - n.first) * p.G * p.T;
+  n.keys = cache_clamp(cache_ld(p.p_lengths + s), p.p_cols << p.page_log2);
+  cache_span(&n, p.window ? n.keys - p.window + 1 : 0, KC);  // (the first row of all stands behind the prefix)
+  return n;
+}
+template <int KC>
+FA_WALK CacheEntry cache_own(const CacheParams& p, int b) {
+  CacheEntry n;
+  n.first = b;
+  n.rows = p.G * p.T;
+  n.keys = cache_length(p, b);
+  cache_span(&n, p.window ? (n.keys > p.T ? n.keys - p.T : 0) - p.window + 1 : 0, KC);
+  return n;
+}
 template <int KC>
 FA_WALK CacheEntry cache_entry(const CacheParams& p, int e) {
-  CacheEntry n;
-  int first_key;  // the first that a row may see, with a window
-  if (e < p.S) {
-    int end;
-    cache_group(p, e, &n.first, &end);
-    n.rows = (end - n.first) * p.G * p.T;
-    n.keys = cache_clamp(cache_ld(p.p_lengths + e), p.p_cols << p.page_log2);
-    first_key = n.keys - p.window + 1;  // (the first row of all stands behind the prefix)
-  } else {
-    n.first = e - p.S;
-    n.rows = p.G * p.T;
-    n.keys = cache_length(p, n.first);
-    first_key = (n.keys > p.T ? n.keys - p.T : 0) - p.window + 1;
-  }
-  n.chunk0 = p.window && first_key > 0 ? first_key / KC : 0;
-  n.chunks = n.rows > 0 ? (n.keys + KC - 1) / KC - n.chunk0 : 0;
-  if (n.chunks < 0) n.chunks = 0;
-  return n;
+  return e < p.S ? cache_prefix<KC>(p, e) : cache_own<KC>(p, e - p.S);
 }
 
 // A place in the list: that of chunk c of the item of tile r, kv head h, entry e.  ITEM:
@@ -272,7 +290,7 @@ struct CacheShare {
 template <int KC, int ROWS, int ITEM, int THREADS>
 __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(const CacheParams& p) {
   constexpr int WARPS = THREADS / 32;
-  __shared__ long long s_sum[WARPS][2];
+  __shared__ long long s_sum[WARPS][3];
   __shared__ int s_found[3];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int each = (p.entries + THREADS - 1) / THREADS;
@@ -286,25 +304,43 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
     sum[1] += items;
   }
   const long long mine = sum[0], my_items = sum[1];
+  constexpr bool PRE = ROWS == kPrefixRows;
+  long long other = 0;  // work of the list that runs beside this one
+  if (p.sms) {
+#pragma unroll 1
+    for (int e = threadIdx.x; e < (PRE ? p.B : p.groups); e += THREADS) {
+      const CacheEntry n = PRE ? cache_own<kCacheKeys>(p, e) : cache_prefix<kPrefixKeys>(p, e);
+      if (n.chunks) other += (long long)p.Hkv * n.tiles(PRE ? kCacheRows : kPrefixRows) * (n.chunks + (PRE ? kCacheItem : kPrefixItem));
+    }
+  }
 #pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const long long a = __shfl_up_sync(~0u, sum[0], o), b = __shfl_up_sync(~0u, sum[1], o);
     if (lane >= o) sum[0] += a, sum[1] += b;
+    other += __shfl_xor_sync(~0u, other, o);
   }
-  if (lane == 31) s_sum[warp][0] = sum[0], s_sum[warp][1] = sum[1];
+  if (lane == 31) s_sum[warp][0] = sum[0], s_sum[warp][1] = sum[1], s_sum[warp][2] = other;
   __syncthreads();
+  other = 0;
   long long total = 0, items = 0, base = sum[0] - mine, item = sum[1] - my_items;
 #pragma unroll 1
   for (int w = 0; w < WARPS; ++w) {
     if (w < warp) base += s_sum[w][0], item += s_sum[w][1];
     total += s_sum[w][0];
     items += s_sum[w][1];
+    other += s_sum[w][2];
   }
   // groups that overlap can ask for more than there is room for: then there is no work
   const bool room = items <= p.max_items && total < (1 << 30);
   CacheShare<CacheCursor<KC, ROWS, ITEM>> s;
   const int all = room ? (int)total : 0;
-  const int per = max((int)(((unsigned)all + gridDim.x - 1) / gridDim.x), p.min_chunks);
+  unsigned ctas = gridDim.x;
+  if (p.sms) {  // as many SMs as its part of the cost, one at least (the CTAs from there on have nothing)
+    const float pre = 1024.f * (float)(PRE ? total : other), own = (float)p.chunk_cost * (float)(PRE ? other : total);
+    const int on_pre = own > 0.f ? min(max((int)((float)p.sms * pre / (pre + own) + 0.5f), 1), p.sms - 1) : p.sms;
+    ctas = min(ctas, (unsigned)(PRE ? on_pre : max(p.sms - on_pre, 1) * p.per_sm));
+  }
+  const int per = max((int)(((unsigned)all + ctas - 1) / ctas), p.min_chunks);
   s.begin = min(per * (int)blockIdx.x, all);
   s.end = min(s.begin + per, all);
   if (blockIdx.x == 0) {

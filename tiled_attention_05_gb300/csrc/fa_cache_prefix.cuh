@@ -99,8 +99,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   using Cursor = fa::CacheCursor<BN, fa::kPrefixRows, fa::kPrefixItem>;
   constexpr int NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
-  grid_next();
-  grid_previous();
+  __shared__ Cursor s_walk[9];
+  __shared__ uint8_t s_row[256];
+  grid_next();  // the own keys' kernel, on the SMs that this one leaves
   const auto share = fa::cache_share<BN, fa::kPrefixRows, fa::kPrefixItem, kThreads>(p);
   if (share.begin >= share.end || share.start.at >= share.end) return;
 
@@ -165,10 +166,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int u = 0;  // ring position of the item's first K (K_j at u + 2 j, V_j after it)
         int nq[2] = {0, 0}, np[2] = {0, 0};
         bool ok = true;
-        Cursor it = share.start;
-        while (ok && it.at < share.end) {
-          const Item m = item_of(it);
-          const int tiles = m.c1 - m.c0, last_x = tile_active(it, 1) ? 1 : 0;
+        Cursor* const walk = &s_walk[8];
+        *walk = share.start;
+        while (ok && walk->at < share.end) {
+          const int tiles = walk->end(share.end) - walk->c, last_x = tile_active(*walk, 1) ? 1 : 0;
           auto issue_s = [&](int x, int j) -> bool {
             if (j == 0) {
               if (!mbar_wait(&q_full[x], nq[x] & 1, abort_flag)) return false;
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_commit(&o_done[x]);
             }
           u += 2 * tiles;
-          it.next(p);
+          walk->next(p);
         }
         // Let every MMA issued above finish before TMEM is released.
         mma_commit(drain);
@@ -374,18 +375,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Loads from TMEM are a warp's, and the barrier that hands the scales round is the
     // tile's: those who meet there leave together when one of them gave up.
     auto agree = [&](bool fine) { return Q8 ? named_bar_and(1 + x, 128, fine) : (bool)__all_sync(~0u, fine); };
-    Cursor it = share.start;
-    while (ok && it.at < share.end) {
-      const Item m = item_of(it);
-      const int tiles = m.c1 - m.c0;
-      if (tile_active(it, x)) {
+    // Where the walk stands, and what is left to say of this thread's row at an item's end, lie
+    // in shared memory: the loop over an item's tiles needs the registers.
+    Cursor* const walk = &s_walk[warp - 4];
+    if (lane == 0) *walk = share.start;
+    __syncwarp();
+    while (ok && walk->at < share.end) {
+      if (tile_active(*walk, x)) {
+        const Cursor it = *walk;
+        const Item m = item_of(it);
+        const int tiles = m.c1 - m.c0;
         const int row = it.r * fa::kPrefixRows + x * BM + r;
         const fa::CacheRow w = fa::cache_row(p, it.n, row);
         const int pos = fa::cache_length(p, w.b) - p.T + w.t;  // among the own keys; negative: padding
         const int head = it.h * p.G + w.g;
         float unit = MODS && p.capped ? 1.f : p.scale_log2;
         const float slope = MODS && p.slopes ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
-        const int abs0 = it.n.keys + pos;
+        s_row[threadIdx.x - 128] = !w.valid ? 0 : pos < 0 ? 2 : 1;  // 2: a padding row, whose part is none
+        int lim = it.n.keys - (it.n.chunk0 + m.c0) * BN;  // columns of the next tile that are keys
         {  // the warp's 32 rows of Q into shared memory
           constexpr int P = D / 8, STEP = 32 / P;  // lanes a row, rows at a time
           const int mine = w.valid ? (w.b * p.Hq + head) * p.T + w.t : -1, piece = lane % P;
@@ -429,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The scales of a tile's keys, one key a thread, a tile ahead.
         float ks = 0.f, vs = 0.f;
         auto fetch_scales = [&](int c) {
+          const Cursor& it = *walk;
           const int key = (it.n.chunk0 + c) * BN + r;
           ks = 0.f, vs = 1.f;
           if (key >= it.n.keys) return;
@@ -457,7 +465,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           ++ns;
           tc_fence_after();
-          const int kv0 = (it.n.chunk0 + m.c0 + j) * BN;
           float mt = NEG_INF, m_new, base, sum;
           bool rescale, warp_rescale;
           auto refer = [&]() {  // the reference of this tile's weights, from its maximum
@@ -466,7 +473,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             warp_rescale = __any_sync(~0u, rescale);
             base = m_new == NEG_INF ? 0.f : m_new;
           };
-          const int lim = it.n.keys - kv0;  // columns that are keys
           if constexpr (Q8 || MODS) {
             // Two passes of 32 columns at a time: the scores in log2 units, back into TMEM, and
             // their maximum; then the weights.  (With the row in registers the code is four
@@ -493,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                   for (int y = 0; y < 4; ++y) {
                     if (p.capped) v[y] = capped(p.cap, v[y]);
-                    const int far = abs0 - (kv0 + c + e + y);
+                    const int far = pos + lim - (c + e + y);
                     v[y] -= slope * (float)far;
                     if (p.window && far >= p.window) v[y] = NEG_INF;
                   }
@@ -603,19 +609,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&p_full[x]);
+          lim -= BN;
         }
         if (ok) ok = agree(mbar_wait(&o_done[x], no & 1, abort_flag));
         ++no;
         if (ok) {
           tc_fence_after();
-          // A padding row's part is none.
-          const bool none = pos < 0;
-          const long long at = ((long long)it.item + blockIdx.x) * fa::kPrefixRows + x * BM + r;
-          if (w.valid) *reinterpret_cast<float2*>(p.parts.ml + at * 2) = none ? make_float2(NEG_INF, 0.f) : make_float2(m_ref, l);
+          const bool some = s_row[threadIdx.x - 128] != 0, none = s_row[threadIdx.x - 128] == 2;
+          const long long at = ((long long)walk->item + blockIdx.x) * fa::kPrefixRows + x * BM + r;
+          if (some) *reinterpret_cast<float2*>(p.parts.ml + at * 2) = none ? make_float2(NEG_INF, 0.f) : make_float2(m_ref, l);
           // 32 columns at a time through this warp's share of Q_X, which is free now, so that a
           // row's 128 bytes leave together.
           uint8_t* stage = smem + x * C::Q_BYTES + quad * 4096;
-          const unsigned valid = __ballot_sync(~0u, w.valid);
+          const unsigned valid = __ballot_sync(~0u, some);
           const long long first = at - lane;  // the warp's first row
 #pragma unroll 1
           for (int c = 0; c < DV / 32; ++c) {
@@ -639,7 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();  // (the next item's first P.V into O_X follows this warpgroup's next P)
         }
       }
-      it.next(p);
+      __syncwarp();
+      if (lane == 0) walk->next(p);
+      __syncwarp();
     }
   }
   tc_fence_before();
@@ -668,7 +676,8 @@ cudaError_t launch_mods(const CacheParams& p, int grid, cudaStream_t stream) {
   if (!Q8 && (!fa::encode_pages_bf16(&mk, p.K, D, page, heads, page < BN ? page : BN) ||
               !fa::encode_pages_bf16(&mv, p.V, DV, page, heads, page < BN ? page : BN)))
     return cudaErrorInvalidValue;
-  return fa::launch_next(kernel, dim3((unsigned)grid), kThreads, C::SMEM, stream, p, mk, mv);
+  kernel<<<grid, kThreads, C::SMEM, stream>>>(p, mk, mv);
+  return cudaGetLastError();
 }
 
 template <int D, int DV, bool Q8>
