@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
     }
     cp_commit();
   };
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < C::NS - 1; ++s) issue(s);
   int stage = 0, fill = C::NS - 1;
 

@@ -323,7 +323,7 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
   __syncthreads();
   other = 0;
   long long total = 0, items = 0, base = sum[0] - mine, item = sum[1] - my_items;
-#pragma unroll 1
+#pragma unroll 4
   for (int w = 0; w < WARPS; ++w) {
     if (w < warp) base += s_sum[w][0], item += s_sum[w][1];
     total += s_sum[w][0];

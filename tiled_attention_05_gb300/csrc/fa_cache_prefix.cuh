@@ -86,10 +86,24 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float capped(const fa::CapParams& c, float x) {
-  const float u = x * x;
-  if (u <= c.small2) return x * (c.a[0] + u * (c.a[1] + u * (c.a[2] + u * (c.a[3] + u * c.a[4]))));
-  return c.log2c - 2.f * c.log2c * rcp(1.f + ex2(cap_top<true>(c.in * x)));
+// Four capped scores in log2 units (see CapParams): by the polynomial where that serves all
+// of the warp's, else by the form for any.
+__device__ __forceinline__ void cap_quad_of(const fa::CapParams& c, uint64_t& a, uint64_t& b) {
+  const uint64_t ua = f2_mul(a, a), ub = f2_mul(b, b);
+  const float top = fmax3(fmaxf(f2_lo(ua), f2_hi(ua)), f2_lo(ub), f2_hi(ub));
+  if (__any_sync(~0u, !(top <= c.small2))) {
+    uint64_t r0, r1, e0, e1;
+    const uint64_t in = f2_pack(c.in, c.in), scale = f2_pack(-2.f * c.log2c, -2.f * c.log2c), top2 = f2_pack(c.log2c, c.log2c);
+    cap_quad<true>(f2_mul(a, in), f2_mul(b, in), r0, r1, e0, e1);
+    a = f2_fma(r0, scale, top2);
+    b = f2_fma(r1, scale, top2);
+    return;
+  }
+  uint64_t ta = f2_pack(c.a[4], c.a[4]), tb = ta;
+#pragma unroll
+  for (int k = 3; k >= 0; --k) ta = f2_fma(ta, ua, f2_pack(c.a[k], c.a[k])), tb = f2_fma(tb, ub, f2_pack(c.a[k], c.a[k]));
+  a = f2_mul(a, ta);
+  b = f2_mul(b, tb);
 }
 
 template <int D, int DV, bool Q8, bool MODS>
@@ -299,27 +313,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = ld.u > NS ? ld.u - NS : 0; u < ld.u; ++u) mbar_wait_bounded(&full[u % NS], (u / NS) & 1);
         }
       } else {
-        // e4m3: all three warps turn the codes of a raw buffer into fp16, pieces of 16 codes.
-        auto convert = [&](auto w, int valid, const uint8_t* src, uint32_t dst) {
-          constexpr int P = decltype(w)::value / 16, N = (BN * P + kLoaders - 1) / kLoaders, HALF = (N + 1) / 2;
+        // e4m3: all three warps turn the codes of a raw buffer into fp16, pieces of 16 codes, four at
+        // a time (a row has 1 << shift pieces).
+        auto convert = [&](int shift, int valid, const uint8_t* src, uint32_t dst) {
+#pragma unroll 1
+          for (int i0 = tid; i0 < BN << shift; i0 += 4 * kLoaders) {
+            uint4 c[4];
 #pragma unroll
-          for (int k0 = 0; k0 < N; k0 += HALF) {
-            uint4 c[HALF];
-#pragma unroll
-            for (int k = 0; k < HALF; ++k) {
-              const int i = (k0 + k) * kLoaders + tid;
+            for (int k = 0; k < 4; ++k) {
+              const int i = i0 + k * kLoaders;
               c[k] = make_uint4(0, 0, 0, 0);
-              if (i < valid * P) c[k] = reinterpret_cast<const uint4*>(src)[i];
+              if (i < valid << shift) c[k] = reinterpret_cast<const uint4*>(src)[i];
             }
 #pragma unroll
-            for (int k = 0; k < HALF; ++k) {
-              const int i = (k0 + k) * kLoaders + tid, row = i / P, piece = i % P;
-              if (k0 + k >= N || row >= BN) continue;
-              const uint32_t block = dst + (piece >> 2) * (BN * 128);
-              st_shared_v4(block + sw128_offset(row, (piece & 3) * 2), half2_of(c[k].x), half2_of(c[k].x >> 16), half2_of(c[k].y),
-                           half2_of(c[k].y >> 16));
-              st_shared_v4(block + sw128_offset(row, (piece & 3) * 2 + 1), half2_of(c[k].z), half2_of(c[k].z >> 16),
-                           half2_of(c[k].w), half2_of(c[k].w >> 16));
+            for (int k = 0; k < 4; ++k) {
+              const int i = i0 + k * kLoaders, row = i >> shift, piece = i - (row << shift);
+              if (row >= BN) break;
+              const uint32_t to = dst + (piece >> 2) * (BN * 128) + sw128_offset(row, (piece & 3) * 2);
+              st_shared_v4(to, half2_of(c[k].x), half2_of(c[k].x >> 16), half2_of(c[k].y), half2_of(c[k].y >> 16));
+              st_shared_v4(to ^ 16, half2_of(c[k].z), half2_of(c[k].z >> 16), half2_of(c[k].w), half2_of(c[k].w >> 16));
             }
           }
         };
@@ -338,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         fetch_id();
         Units now = ld;
+#pragma unroll 1
         for (int k = 0; k < NR - 1; ++k) issue();
         while (ok && more) {
           issue();
@@ -347,10 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!__all_sync(~0u, both)) break;
           const uint8_t* src = smem + C::OFF_RAW + rs * C::RAW;
           const uint32_t dst = smem_u32(slots + s * C::SLOT);
-          if (now.v)
-            convert(std::integral_constant<int, DV>{}, valid, src, dst);
-          else
-            convert(std::integral_constant<int, D>{}, valid, src, dst);
+          convert((now.v ? DV : D) == 128 ? 3 : 2, valid, src, dst);
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -387,28 +397,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tiles = m.c1 - m.c0;
         const int row = it.r * fa::kPrefixRows + x * BM + r;
         const fa::CacheRow w = fa::cache_row(p, it.n, row);
-        const int pos = fa::cache_length(p, w.b) - p.T + w.t;  // among the own keys; negative: padding
         const int head = it.h * p.G + w.g;
         float unit = MODS && p.capped ? 1.f : p.scale_log2;
-        const float slope = MODS && p.slopes ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
-        s_row[threadIdx.x - 128] = !w.valid ? 0 : pos < 0 ? 2 : 1;  // 2: a padding row, whose part is none
         int lim = it.n.keys - (it.n.chunk0 + m.c0) * BN;  // columns of the next tile that are keys
+        int pos;  // of this row among the own keys; negative: padding
+        float slope = 0.f;
         {  // the warp's 32 rows of Q into shared memory
           constexpr int P = D / 8, STEP = 32 / P;  // lanes a row, rows at a time
           const int mine = w.valid ? (w.b * p.Hq + head) * p.T + w.t : -1, piece = lane % P;
           const uint32_t dst = smem_u32(smem) + x * C::Q_BYTES;
-#pragma unroll 1
+#pragma unroll 4
           for (int k = 0; k < 32; k += STEP) {
             const int from = __shfl_sync(~0u, mine, k + lane / P), row = quad * 32 + k + lane / P;
             cp16(dst + (piece >> 3) * (BM * 128) + sw128_offset(row, piece & 7), p.Q + (from < 0 ? 0ll : (long long)from * D + piece * 8),
                  from >= 0);
           }
           cp_commit();
+          pos = fa::cache_length(p, w.b) - p.T + w.t;
+          if (MODS && p.slopes) slope = __ldg(p.slopes + head) * 1.4426950408889634f;
           cp_wait<0>();
           if constexpr (Q8) {  // as fp16, a row's largest value brought to [1, 2); a row a thread
             __syncwarp();
             uint32_t top = 0;
-#pragma unroll 1
+#pragma unroll 4
             for (int k = 0; k < P; ++k) {
               const float4 v = ld_shared_f4(smem + x * C::Q_BYTES + (k >> 3) * (BM * 128) + sw128_offset(r, k & 7));
               const float a[4] = {v.x, v.y, v.z, v.w};
@@ -419,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ex = min(max((int)(top >> 7), 1), 253);
             const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
             unit *= __uint_as_float((uint32_t)ex << 23);
-#pragma unroll 1
+#pragma unroll 4
             for (int k = 0; k < P; ++k) {
               const uint32_t at = (k >> 3) * (BM * 128) + sw128_offset(r, k & 7);
               const float4 v = ld_shared_f4(smem + x * C::Q_BYTES + at);
@@ -432,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_async_smem();
           mbar_arrive(&q_full[x]);
+          s_row[threadIdx.x - 128] = !w.valid ? 0 : pos < 0 ? 2 : 1;  // 2: a padding row, whose part is none
         }
         // The scales of a tile's keys, one key a thread, a tile ahead.
         float ks = 0.f, vs = 0.f;
@@ -484,6 +496,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld32(tS + c, s);
               tmem_wait_ld();
               const uint64_t unit2 = f2_pack(unit, unit);
+              const float far0 = (float)(pos + lim - c);  // of column c
+              // Of the columns only those from `from` on and before `to` count.
+              const int from = MODS && p.window ? pos + lim - c - p.window + 1 : 0, to = lim - c;
+              const bool some_hidden = from > 0 || to < 32;
+              if (MODS && some_hidden) {  // (a NaN there would reach the others of its four through the cap)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (e < from || e >= to) s[e] = 0u;
+              }
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
                 uint64_t t[2] = {f2_mul(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), unit2),
@@ -495,24 +516,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                   t[1] = f2_fma(t[1], f2_pack(k4.z, k4.w), f2_pack(l4.z, l4.w));
                 } else {
                   if constexpr (Q8) t[0] = f2_mul(t[0], f2_pack(k4.x, k4.y)), t[1] = f2_mul(t[1], f2_pack(k4.z, k4.w));
+                  if (p.capped) cap_quad_of(p.cap, t[0], t[1]);
                   float v[4] = {f2_lo(t[0]), f2_hi(t[0]), f2_lo(t[1]), f2_hi(t[1])};
 #pragma unroll
-                  for (int y = 0; y < 4; ++y) {
-                    if (p.capped) v[y] = capped(p.cap, v[y]);
-                    const int far = pos + lim - (c + e + y);
-                    v[y] -= slope * (float)far;
-                    if (p.window && far >= p.window) v[y] = NEG_INF;
-                  }
+                  for (int y = 0; y < 4; ++y) v[y] = fmaf(-slope, far0 - (float)(e + y), v[y]);
                   t[0] = f2_pack(v[0], v[1]), t[1] = f2_pack(v[2], v[3]);
                   if constexpr (Q8) t[0] = f2_add(t[0], f2_pack(l4.x, l4.y)), t[1] = f2_add(t[1], f2_pack(l4.z, l4.w));
                 }
                 s[e] = __float_as_uint(f2_lo(t[0])), s[e + 1] = __float_as_uint(f2_hi(t[0]));
                 s[e + 2] = __float_as_uint(f2_lo(t[1])), s[e + 3] = __float_as_uint(f2_hi(t[1]));
               }
-              if (c + 32 > lim) {
+              if (some_hidden) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                  if (c + e >= lim) s[e] = __float_as_uint(NEG_INF);
+                  if (e < from || e >= to) s[e] = __float_as_uint(NEG_INF);
               }
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
