@@ -300,6 +300,13 @@ PREFIXES = [
     ([20 + k for k in range(40)], [1500, 777], [0, 19, 40], 16, 2, 1, 128, 128, 128),
     ([3, 4, 0, 2], [6000], None, 12, 4, 5, 64, 64, 256),
     ([300] * 130, [257], None, 8, 1, 1, 128, 128, 64),    # 1040 rows over one prefix
+    # 128 rows and fewer of a group (two parts of an item), 129 to 256, and more; one key tile and many
+    ([17] * 32, [100], None, 4, 1, 1, 128, 64, 16),
+    ([17, 0] * 10, [129, 5000], [0, 9, 20], 8, 2, 1, 64, 128, 32),
+    ([5 + k for k in range(33)], [4000], None, 4, 1, 1, 128, 128, 256),
+    ([5 + k for k in range(64)], [3001], None, 16, 4, 1, 64, 64, 64),
+    ([40] * 97, [2000], None, 6, 1, 1, 64, 128, 128),
+    ([9, 2, 30, 4], [20000], None, 48, 2, 3, 128, 64, 64),
 ]
 
 
@@ -318,14 +325,39 @@ def test_shared_prefix(lens, prefix, starts, Hq, Hkv, T, d, dv, page, quant):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("quant", [False, True])
-@pytest.mark.parametrize("mods", [dict(softcap=30.0), dict(slopes=True), dict(window=40), dict(window=250, softcap=20.0, slopes=True)])
-def test_shared_prefix_modified(mods, quant):
-    s = Setup([30, 2, 0, 77, 20, 64, 3, 3], 2, 128, 128, quant, 32, [300, 200], [0, 5, 8])
+@pytest.mark.parametrize("heads", [(128, 128), (64, 64)])
+@pytest.mark.parametrize("mods", [dict(softcap=30.0), dict(softcap=2.0), dict(slopes=True), dict(window=40), dict(window=1),
+                                  dict(window=250, softcap=20.0, slopes=True)])
+def test_shared_prefix_modified(mods, quant, heads):
+    s = Setup([30, 2, 0, 77, 20, 64, 3, 3], 2, *heads, quant, 32, [300, 200], [0, 5, 8])
     Q, mods = query(s, 16, 3, std=1.5), dict(mods)
     if mods.get("slopes"):
         mods["slopes"] = slopes_of(16)
     O, L = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, **mods)
     check(s, Q, O, L, **mods)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("quant", [False, True])
+def test_nan_of_a_prefix(quant):
+    """A NaN key or value of a prefix reaches the rows that see it, in whatever place of a tile
+    it stands, and none that a window hides it from (values in bf16 have to be finite)."""
+    s = Setup([30] * 40, 1, 64, 64, quant, 16, [400, 400], [0, 20, 40])
+    Q = query(s, 4, 1)
+    NaN, one = (torch.full((1, 1, 1, 64), x, device="cuda").to(bf) for x in (math.nan, 1.0))
+    at = torch.tensor([130], dtype=torch.int32, device="cuda")
+    for K, V in ((NaN, one), (one, NaN)):
+        before = [x.clone() for x in bits(s.cache)]
+        fa.fa_cache_write(s.cache, K, V, s.p_tables[:1], at)
+        for mods in (dict(), dict(softcap=5.0)):
+            O, L = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, **mods)
+            assert torch.isnan(O[:20]).all() and torch.isfinite(O[20:]).all() and torch.isfinite(L[20:]).all()
+            assert torch.isnan(L[:20]).all() == (K is NaN or quant)
+            if quant or V is one:
+                O, L = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, window=250, **mods)
+                assert torch.isfinite(O).all() and torch.isfinite(L).all()
+        for x, y in zip(bits(s.cache), before):
+            x.copy_(y)
 
 
 @pytest.mark.gpu

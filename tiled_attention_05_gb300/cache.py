@@ -72,10 +72,11 @@ class KVCache:
         return _fa.FaCacheDims(B, Hq, Hkv, T, d, self.V.shape[3], pages, page, table_pages, self.quantised)
 
 
-def _index(t, name, shape, device):
-    if t.dim() != len(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {list(shape)}")
-    _fa._check_all(device, [(t, name, tuple(n if want is None else want for n, want in zip(t.shape, shape)), torch.int32)])
+def _table(t, name, rows):
+    """Columns of a table of ``rows`` rows (None: any), as far as its shape goes."""
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{'sequences' if rows is None else rows}, pages]")
+    return t.shape[1]
 
 
 def _new_rows(x, name, shape, device):
@@ -103,11 +104,12 @@ def fa_cache_write(cache: KVCache, K, V, tables, starts, counts=None, stream=Non
     device = cache.device
     ks = _new_rows(K, "K", (B, Hkv, T, d), device)
     vs = _new_rows(V, "V", (B, Hkv, T, cache.V.shape[3]), device)
-    _index(tables, "tables", (B, None), device)
-    _index(starts, "starts", (B,), device)
+    n, i32 = _table(tables, "tables", B), torch.int32
+    specs = [(tables, "tables", tables.shape, i32), (starts, "starts", (B,), i32)]
     if counts is not None:
-        _index(counts, "counts", (B,), device)
-    dims, handle = cache._dims(B, 0, T, tables.shape[1]), _fa._stream_ptr(stream, device)
+        specs.append((counts, "counts", (B,), i32))
+    _fa._check_all(device, specs)
+    dims, handle = cache._dims(B, 0, T, n), _fa._stream_ptr(stream, device)
     with _fa._under(stream, device):
         code = _fa.load().fa_cache_write(ctypes.byref(dims), cache._pools, K.data_ptr(), V.data_ptr(), ks, vs,
                                          tables.data_ptr(), starts.data_ptr(), _fa._ptr(counts), handle)
@@ -118,14 +120,13 @@ def fa_cache_read(cache: KVCache, tables, lengths, T: int, K=None, V=None, strea
     """K [B, Hkv, T, d], V [B, Hkv, T, dv] (bf16) = positions 0 .. T - 1 of each sequence, zero
     from lengths[b] on.  Optional preallocated K / V are written in place."""
     device = cache.device
-    _index(tables, "tables", (None, None), device)
-    B, n = tables.shape
-    _index(lengths, "lengths", (B,), device)
+    n, B = _table(tables, "tables", None), tables.shape[0]
     _, Hkv, _, d = cache.K.shape
     T, dv, bf, given = int(T), cache.V.shape[3], torch.bfloat16, (K, V)
     if T < 0:
         raise ValueError(f"T is {T}")
-    specs = [(t, name, (B, Hkv, T, w), bf) for t, name, w in ((K, "K", d), (V, "V", dv)) if t is not None]
+    specs = [(tables, "tables", tables.shape, torch.int32), (lengths, "lengths", (B,), torch.int32)]
+    specs += [(t, name, (B, Hkv, T, w), bf) for t, name, w in ((K, "K", d), (V, "V", dv)) if t is not None]
     _fa._check_all(device, specs)
     dims, handle = cache._dims(B, 0, T, n), _fa._stream_ptr(stream, device)
     with _fa._under(stream, device):
@@ -141,34 +142,32 @@ def fa_cache_read(cache: KVCache, tables, lengths, T: int, K=None, V=None, strea
     return K, V
 
 
-def _prefix_of(prefix, B, device):
-    """The fa_cache_prefix of a call (None without one), checked."""
-    if prefix is None:
-        return None
-    tables, lengths, starts = prefix if len(prefix) == 3 else (*prefix, None)
-    _index(tables, "prefix tables", (None, None), device)
-    groups, n = tables.shape
-    _index(lengths, "prefix lengths", (groups,), device)
-    if starts is not None:
-        _index(starts, "prefix starts", (groups + 1,), device)
-    elif groups != 1:
-        raise ValueError(f"{groups} prefixes need starts [{groups + 1}], the first sequence of each group")
-    return _fa.FaCachePrefix(groups, n, tables.data_ptr(), lengths.data_ptr(), _fa._ptr(starts))
-
-
-def _attention_dims(Q, cache, tables, prefix):
+def _attention_dims(Q, cache, tables, prefix, specs):
+    """Dims and fa_cache_prefix (None without one) of a call; the index arrays go to specs."""
     if Q.dim() != 4:
         raise ValueError("Q must be [B, Hq, T, d]")
     B, Hq, T, d = Q.shape
     if d != cache.K.shape[3]:
         raise ValueError(f"Q has shape {tuple(Q.shape)}, the cache's keys have {cache.K.shape[3]} channels")
-    _index(tables, "tables", (B, None), cache.device)
-    return cache._dims(B, Hq, T, tables.shape[1]), _prefix_of(prefix, B, cache.device)
+    dims, i32 = cache._dims(B, Hq, T, _table(tables, "tables", B)), torch.int32
+    specs.append((tables, "tables", tables.shape, i32))
+    if prefix is None:
+        return dims, None
+    p_tables, lengths, starts = prefix if len(prefix) == 3 else (*prefix, None)
+    n, groups = _table(p_tables, "prefix tables", None), p_tables.shape[0]
+    specs += [(p_tables, "prefix tables", p_tables.shape, i32), (lengths, "prefix lengths", (groups,), i32)]
+    if starts is not None:
+        specs.append((starts, "prefix starts", (groups + 1,), i32))
+    elif groups != 1:
+        raise ValueError(f"{groups} prefixes need starts [{groups + 1}], the first sequence of each group")
+    return dims, _fa.FaCachePrefix(groups, n, p_tables.data_ptr(), lengths.data_ptr(), _fa._ptr(starts))
 
 
 def fa_cache_attention_workspace_bytes(Q, cache: KVCache, tables, prefix=None) -> int:
     """The workspace that fa_cache_attention needs (what it allocates without one)."""
-    dims, pre = _attention_dims(Q, cache, tables, prefix)
+    specs = []
+    dims, pre = _attention_dims(Q, cache, tables, prefix, specs)
+    _fa._check_all(cache.device, specs)
     with _fa._on(cache.device):
         return int(_fa.load().fa_cache_attention_workspace_bytes(ctypes.byref(dims), pre))
 
@@ -185,10 +184,11 @@ def fa_cache_attention(Q, cache: KVCache, tables, lengths, scale: float | None =
     starts[s + 1] - 1 share the lengths[s] positions of tables[s] in front of their own;
     their keys are read once for all of them.  Without starts one prefix serves the
     whole batch."""
-    dims, pre = _attention_dims(Q, cache, tables, prefix)
     device, bf, f32 = cache.device, torch.bfloat16, torch.float32
-    B, Hq, T, dv = dims.B, dims.Hq, dims.T, dims.dv
-    specs = [(Q, "Q", Q.shape, bf), (lengths, "lengths", (B,), torch.int32)]
+    specs = [(Q, "Q", Q.shape, bf)]
+    dims, pre = _attention_dims(Q, cache, tables, prefix, specs)
+    (B, Hq, T, d), dv = Q.shape, cache.V.shape[3]
+    specs.append((lengths, "lengths", (B,), torch.int32))
     if O is not None:
         specs.append((O, "O", (B, Hq, T, dv), bf))
     if L is not None:
@@ -203,7 +203,7 @@ def fa_cache_attention(Q, cache: KVCache, tables, lengths, scale: float | None =
     handle = _fa._stream_ptr(stream, device)
     with _fa._under(stream, device):
         if O is None:
-            O = torch.empty((B, Hq, T, dv), dtype=bf, device=device)
+            O = torch.empty_like(Q) if dv == d else torch.empty((B, Hq, T, dv), dtype=bf, device=device)
         if L is None:
             L = torch.empty((B, Hq, T), dtype=f32, device=device)
         if workspace is None:

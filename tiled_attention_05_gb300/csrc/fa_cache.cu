@@ -199,10 +199,12 @@ __global__ void __launch_bounds__(kThreads) fa_cache_read_kernel(const PageParam
 // Adds up the parts of each output row, in their order: those of its own keys and those
 // of its group's prefix.  WARPS warps take a row (1, or 4 where there are few rows: a
 // long sequence alone has tens of parts).
+// All that does not depend on one another is loaded together: a row's time is that of its
+// chain of loads (heads and groups, then parts, four at a time).
 template <int DV, int WARPS>
 __global__ void __launch_bounds__(128) fa_cache_join_kernel(const fa::CacheJoin j) {
   constexpr int CH = DV / 32;
-  __shared__ float s_o[4][DV], s_l[4];
+  __shared__ float s_o[4][DV], s_ml[4][2];
   grid_next();
   grid_previous();
   const CacheParams& p = j.p;
@@ -211,75 +213,93 @@ __global__ void __launch_bounds__(128) fa_cache_join_kernel(const fa::CacheJoin 
   if (out >= p.B * p.Hq * p.T) return;  // (with WARPS 4 a block has one row)
   const int sub = warp % WARPS;
   const int bh = p.by_T(out), t = out - bh * p.T, b = j.by_Hq(bh), hq = bh - b * p.Hq, h = j.by_G(hq), g = hq - h * p.G;
-  const CacheSlots own = fa::cache_slots(p.parts.head[j.own + b], p.G * p.T, kCacheRows, fa::kCacheItem, h, g * p.T + t, p.parts.head[j.own_entries].work);
-  CacheSlots pre = {0, 0, 0};
+  const fa::CacheHead own_head = p.parts.head[j.own + b];
+  const int own_per = p.parts.head[j.own_entries].work;
+  // The group of this sequence, if it has a prefix.
+  fa::CacheHead pre_head = {0, 0, 0};
+  int pre_per = 1, first = 0, pre_rows = 0;
   if (p.S) {
+    pre_per = j.pre.head[j.pre_entries].work;
     for (int s0 = 0; s0 < p.S; s0 += 32) {
       const int s = s0 + lane;
-      bool in = false;
       int a = 0, z = 0;
+      fa::CacheHead head = {0, 0, 0};
       if (s < p.S) {
         fa::cache_group(p, s, &a, &z);
-        in = a <= b && b < z && j.pre.head[s].chunks > 0;
+        head = j.pre.head[s];
       }
-      const unsigned found = __ballot_sync(~0u, in);
+      const unsigned found = __ballot_sync(~0u, a <= b && b < z && head.chunks > 0);
       if (found) {
         const int src = __ffs(found) - 1;
-        a = __shfl_sync(~0u, a, src);
-        z = __shfl_sync(~0u, z, src);
-        pre = fa::cache_slots(j.pre.head[s0 + src], (z - a) * p.G * p.T, j.pre_rows, j.pre_rows == kCacheRows ? fa::kCacheItem : fa::kPrefixItem, h, (b - a) * p.G * p.T + g * p.T + t,
-                              j.pre.head[j.pre_entries].work);
+        first = __shfl_sync(~0u, a, src);
+        pre_rows = (__shfl_sync(~0u, z, src) - first) * p.G * p.T;
+        pre_head = {__shfl_sync(~0u, head.work, src), __shfl_sync(~0u, head.item, src), __shfl_sync(~0u, head.chunks, src)};
         break;
       }
     }
-  } else if (own.n == 1) {
-    return;  // a whole item, stored by its CTA
   }
-  const int n = own.n + pre.n;
-  // (reference, sum) and O of part i
-  auto ml_at = [&](int i) {
-    return reinterpret_cast<const float2*>(i < pre.n ? j.pre.ml : p.parts.ml) +
-           (i < pre.n ? (pre.slot + i) * j.pre_rows + pre.row : (own.slot + i - pre.n) * kCacheRows + own.row);
-  };
-  auto o_at = [&](int i) {
-    return i < pre.n ? j.pre.part + ((pre.slot + i) * j.pre_rows + pre.row) * DV
-                     : p.parts.part + ((own.slot + i - pre.n) * kCacheRows + own.row) * DV;
-  };
-  float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, ml_at(i)->x);
+  const CacheSlots own = fa::cache_slots(own_head, p.G * p.T, kCacheRows, fa::kCacheItem, h, g * p.T + t, own_per);
+  if (!p.S && own.n == 1) return;  // a whole item, stored by its CTA
+  const int pre_row = (b - first) * p.G * p.T + g * p.T + t;
+  const CacheSlots pre =
+      fa::cache_slots(pre_head, pre_rows, j.pre_rows, j.pre_rows == kCacheRows ? fa::kCacheItem : fa::kPrefixItem, h, pre_row, pre_per);
+  // A prefix's item of at most 128 rows leaves two parts, 128 rows apart.
+  const int halves = j.pre_rows == fa::kPrefixRows && pre_rows - (pre_row - pre.row) <= fa::kPrefixRows / 2 ? 1 : 0;
+  const int pre_n = pre.n << halves, n = own.n + pre_n;
+  float top = -INFINITY, sum = 0.f, acc[CH] = {};
+  for (int i0 = sub * 4; i0 < n; i0 += WARPS * 4) {
+    float2 ml[4];
+    float v[4][CH];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  float sum = 0.f, acc[CH] = {};
-#pragma unroll 4
-  for (int i = sub; i < n; i += WARPS) {
-    const float2 ml = *ml_at(i);
-    float v[CH];
-    if constexpr (CH == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(o_at(i) + lane * CH);
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(o_at(i) + lane * CH);
-      v[0] = x.x, v[1] = x.y;
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k;
+      ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int x = 0; x < CH; ++x) v[k][x] = 0.f;
+      if (i >= n) continue;
+      const bool is_pre = i < pre_n;
+      const long long row = is_pre ? (pre.slot + (i >> halves)) * j.pre_rows + pre.row + (i & halves) * 128
+                                   : (own.slot + i - pre_n) * kCacheRows + own.row;
+      ml[k] = reinterpret_cast<const float2*>(is_pre ? j.pre.ml : p.parts.ml)[row];
+      const float* o = (is_pre ? j.pre.part : p.parts.part) + row * DV + lane * CH;
+      if constexpr (CH == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(o);
+        v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(o);
+        v[k][0] = x.x, v[k][1] = x.y;
+      }
     }
-    const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - top);  // (without a finite reference, O is 0 or NaN)
-    sum += ml.y * f;
+    const float now = fmaxf(top, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+    const float a = top == now ? 1.f : ex2(top - now);
+    top = now;
+    sum *= a;
 #pragma unroll
-    for (int k = 0; k < CH; ++k) acc[k] += v[k] * f;
+    for (int x = 0; x < CH; ++x) acc[x] *= a;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = ml[k].x == -INFINITY ? 1.f : ex2(ml[k].x - top);  // (without a finite reference, O is 0 or NaN)
+      sum += ml[k].y * f;
+#pragma unroll
+      for (int x = 0; x < CH; ++x) acc[x] += v[k][x] * f;
+    }
   }
   if constexpr (WARPS > 1) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) s_o[sub][lane * CH + k] = acc[k];
-    if (lane == 0) s_l[sub] = sum;
+    if (lane == 0) s_ml[sub][0] = top, s_ml[sub][1] = sum;
     __syncthreads();
     if (sub) return;
+    top = fmaxf(fmaxf(s_ml[0][0], s_ml[1][0]), fmaxf(s_ml[2][0], s_ml[3][0]));
     sum = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) acc[k] = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      sum += s_l[w];
+      const float f = s_ml[w][0] == -INFINITY ? 1.f : ex2(s_ml[w][0] - top);
+      sum += s_ml[w][1] * f;
 #pragma unroll
-      for (int k = 0; k < CH; ++k) acc[k] += s_o[w][lane * CH + k];
+      for (int k = 0; k < CH; ++k) acc[k] += s_o[w][lane * CH + k] * f;
     }
   }
   const float f = sum == 0.f ? 0.f : 1.f / sum;
@@ -378,8 +398,8 @@ namespace fa {
 template <int DV>
 static cudaError_t launch_join(const CacheJoin& j, cudaStream_t stream) {
   const long long rows = (long long)j.p.B * j.p.Hq * j.p.T;
-  // Four warps a row as long as that fills the GPU at most a few times over.
-  if (rows <= 2048) return launch_next(fa_cache_join_kernel<DV, 4>, dim3((unsigned)rows), 128, 0, stream, j);
+  // Four warps a row where there are few: only a long sequence among few has many parts.
+  if (rows <= 512) return launch_next(fa_cache_join_kernel<DV, 4>, dim3((unsigned)rows), 128, 0, stream, j);
   return launch_next(fa_cache_join_kernel<DV, 1>, dim3((unsigned)((rows + 3) / 4)), 128, 0, stream, j);
 }
 

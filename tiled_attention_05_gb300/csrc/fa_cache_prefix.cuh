@@ -168,7 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto item_of = [&](const Cursor& it) {
     return Item{it.c, it.end(share.end)};
   };
-  auto tile_active = [](const Cursor& it, int x) { return it.n.rows > it.r * fa::kPrefixRows + x * BM; };
+  // Whether tile B has rows of its own.  Where it has none, it takes the same rows as tile A, A
+  // the item's even key tiles and B its odd ones; both leave a part.
+  auto two_tiles = [](const Cursor& it) { return it.n.rows > it.r * fa::kPrefixRows + BM; };
 
   if (warp < 4) {
     setmaxnreg_dec<kRegsLow>();
@@ -183,45 +185,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         Cursor* const walk = &s_walk[8];
         *walk = share.start;
         while (ok && walk->at < share.end) {
-          const int tiles = walk->end(share.end) - walk->c, last_x = tile_active(*walk, 1) ? 1 : 0;
+          const int tiles = walk->end(share.end) - walk->c;
+          const bool two = two_tiles(*walk);
+          // tile X's first key tile, and the distance of its next one
+          const int step = two ? 1 : 2, first_b = two ? 0 : 1;
           auto issue_s = [&](int x, int j) -> bool {
-            if (j == 0) {
+            if (j == (x ? first_b : 0)) {
               if (!mbar_wait(&q_full[x], nq[x] & 1, abort_flag)) return false;
               ++nq[x];
             }
             const int pos = u + 2 * j, s = pos % NS;
-            if (x == 0 && !mbar_wait(&full[s], (pos / NS) & 1, abort_flag)) return false;
+            if ((x == 0 || !two) && !mbar_wait(&full[s], (pos / NS) & 1, abort_flag)) return false;
             tc_fence_after();
             const uint64_t a0 = desc_kmajor(q_buf + x * C::Q_BYTES), b0 = desc_kmajor(slots + s * C::SLOT);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-              const uint32_t step = (k >> 2) * (BM * 128) + (k & 3) * 32;
-              mma_ss(tmem + x * 128, desc_at(a0, step), desc_at(b0, step), idS, k > 0 ? 1u : 0u);
+              const uint32_t off = (k >> 2) * (BM * 128) + (k & 3) * 32;
+              mma_ss(tmem + x * 128, desc_at(a0, off), desc_at(b0, off), idS, k > 0 ? 1u : 0u);
             }
             mma_commit(&s_full[x]);
-            if (x == last_x) mma_commit(&empty[s]);
+            if (x == 1 || !two) mma_commit(&empty[s]);
             return true;
           };
           auto issue_pv = [&](int x, int j) -> bool {
             const int pos = u + 2 * j + 1, s = pos % NS;
             if (!mbar_wait(&p_full[x], np[x] & 1, abort_flag)) return false;
             ++np[x];
-            if (x == 0 && !mbar_wait(&full[s], (pos / NS) & 1, abort_flag)) return false;
+            if ((x == 0 || !two) && !mbar_wait(&full[s], (pos / NS) & 1, abort_flag)) return false;
             tc_fence_after();
             const uint64_t v0 = desc_mnmajor(slots + s * C::SLOT, BN * 128);
 #pragma unroll
             for (int k = 0; k < BN / 16; ++k)
-              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, desc_at(v0, k * 2048), idPV, (j > 0 || k > 0) ? 1u : 0u);
-            if (x == last_x) mma_commit(&empty[s]);
+              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, desc_at(v0, k * 2048), idPV, (j >= step || k > 0) ? 1u : 0u);
+            if (x == 1 || !two) mma_commit(&empty[s]);
             return true;
           };
-          for (int x = 0; ok && x <= last_x; ++x) ok = issue_s(x, 0);
-          for (int j = 0; ok && j < tiles; ++j)
-            for (int x = 0; ok && x <= last_x; ++x) {
+          ok = issue_s(0, 0) && (first_b >= tiles || issue_s(1, first_b));
+          for (int j0 = 0; ok && j0 < tiles; j0 += step)
+            for (int x = 0; ok && x < 2; ++x) {
+              const int j = x ? j0 + first_b : j0;
+              if (j >= tiles) break;
               ok = issue_pv(x, j);
               if (!ok) break;
-              if (j + 1 < tiles)
-                ok = issue_s(x, j + 1);
+              if (j + step < tiles)
+                ok = issue_s(x, j + step);
               else
                 mma_commit(&o_done[x]);
             }
@@ -391,18 +398,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) *walk = share.start;
     __syncwarp();
     while (ok && walk->at < share.end) {
-      if (tile_active(*walk, x)) {
+      {
         const Cursor it = *walk;
+        const bool two = two_tiles(it);
         const Item m = item_of(it);
-        const int tiles = m.c1 - m.c0;
-        const int row = it.r * fa::kPrefixRows + x * BM + r;
+        const int step = two ? 1 : 2, c0 = two ? m.c0 : m.c0 + x;  // this tile's key tiles: every step-th from c0 on
+        const int tiles = (m.c1 - c0 + step - 1) / step;
+        const int row = it.r * fa::kPrefixRows + (two ? x * BM : 0) + r;
         const fa::CacheRow w = fa::cache_row(p, it.n, row);
         const int head = it.h * p.G + w.g;
         float unit = MODS && p.capped ? 1.f : p.scale_log2;
-        int lim = it.n.keys - (it.n.chunk0 + m.c0) * BN;  // columns of the next tile that are keys
-        int pos;  // of this row among the own keys; negative: padding
+        int lim = it.n.keys - (it.n.chunk0 + c0) * BN;  // columns of the next tile that are keys
+        int pos = 0;  // of this row among the own keys; negative: padding
         float slope = 0.f;
-        {  // the warp's 32 rows of Q into shared memory
+        if (tiles > 0) {  // the warp's 32 rows of Q into shared memory
           constexpr int P = D / 8, STEP = 32 / P;  // lanes a row, rows at a time
           const int mine = w.valid ? (w.b * p.Hq + head) * p.T + w.t : -1, piece = lane % P;
           const uint32_t dst = smem_u32(smem) + x * C::Q_BYTES;
@@ -443,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_async_smem();
           mbar_arrive(&q_full[x]);
+        }
+        {
           s_row[threadIdx.x - 128] = !w.valid ? 0 : pos < 0 ? 2 : 1;  // 2: a padding row, whose part is none
         }
         // The scales of a tile's keys, one key a thread, a tile ahead.
@@ -458,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ks = __ldg(p.k_scale + at);
           vs = __ldg(p.v_scale + at);
         };
-        if constexpr (Q8) fetch_scales(m.c0);
+        if (Q8 && tiles > 0) fetch_scales(c0);
         float m_ref = NEG_INF, l = 0.f;
         for (int j = 0; ok && j < tiles; ++j) {
           const float* sc = nullptr;
@@ -470,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             to[BN + r] = vs == vs ? a : vs;
             to[2 * BN + r] = ex2(-a);
             sc = to;
-            if (j + 1 < tiles) fetch_scales(m.c0 + j + 1);
+            if (j + 1 < tiles) fetch_scales(c0 + (j + 1) * step);
           }
           ok = mbar_wait(&s_full[x], ns & 1, abort_flag);
           ok = agree(ok);
@@ -626,13 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&p_full[x]);
-          lim -= BN;
+          lim -= step * BN;
         }
-        if (ok) ok = agree(mbar_wait(&o_done[x], no & 1, abort_flag));
-        ++no;
+        if (ok && tiles > 0) ok = agree(mbar_wait(&o_done[x], no++ & 1, abort_flag));
         if (ok) {
           tc_fence_after();
-          const bool some = s_row[threadIdx.x - 128] != 0, none = s_row[threadIdx.x - 128] == 2;
+          const bool some = s_row[threadIdx.x - 128] != 0, none = s_row[threadIdx.x - 128] == 2 || tiles <= 0;
           const long long at = ((long long)walk->item + blockIdx.x) * fa::kPrefixRows + x * BM + r;
           if (some) *reinterpret_cast<float2*>(p.parts.ml + at * 2) = none ? make_float2(NEG_INF, 0.f) : make_float2(m_ref, l);
           // 32 columns at a time through this warp's share of Q_X, which is free now, so that a
@@ -643,8 +653,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < DV / 32; ++c) {
             uint32_t o[32];
-            tmem_ld32(tO + c * 32, o);
-            tmem_wait_ld();
+            if (tiles > 0) {
+              tmem_ld32(tO + c * 32, o);
+              tmem_wait_ld();
+            }
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
