@@ -54,6 +54,7 @@ class KVCache:
         self.device = K.device
         _fa._check_all(self.device, specs)
         self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
+        self._sizes = {}  # dims and workspace of the attention calls by their sizes
         self._pools = ctypes.byref(_fa.FaKVCache(K.data_ptr(), V.data_ptr(), _fa._ptr(k_scale), _fa._ptr(v_scale)))
 
     @classmethod
@@ -143,33 +144,42 @@ def fa_cache_read(cache: KVCache, tables, lengths, T: int, K=None, V=None, strea
 
 
 def _attention_dims(Q, cache, tables, prefix, specs):
-    """Dims and fa_cache_prefix (None without one) of a call; the index arrays go to specs."""
+    """Dims, workspace bytes and fa_cache_prefix (None without one) of a call; the index
+    arrays go to specs."""
     if Q.dim() != 4:
         raise ValueError("Q must be [B, Hq, T, d]")
     B, Hq, T, d = Q.shape
     if d != cache.K.shape[3]:
         raise ValueError(f"Q has shape {tuple(Q.shape)}, the cache's keys have {cache.K.shape[3]} channels")
-    dims, i32 = cache._dims(B, Hq, T, _table(tables, "tables", B)), torch.int32
+    cols, i32, pre, groups, n = _table(tables, "tables", B), torch.int32, None, 0, 0
     specs.append((tables, "tables", tables.shape, i32))
-    if prefix is None:
-        return dims, None
-    p_tables, lengths, starts = prefix if len(prefix) == 3 else (*prefix, None)
-    n, groups = _table(p_tables, "prefix tables", None), p_tables.shape[0]
-    specs += [(p_tables, "prefix tables", p_tables.shape, i32), (lengths, "prefix lengths", (groups,), i32)]
-    if starts is not None:
-        specs.append((starts, "prefix starts", (groups + 1,), i32))
-    elif groups != 1:
-        raise ValueError(f"{groups} prefixes need starts [{groups + 1}], the first sequence of each group")
-    return dims, _fa.FaCachePrefix(groups, n, p_tables.data_ptr(), lengths.data_ptr(), _fa._ptr(starts))
+    if prefix is not None:
+        p_tables, lengths, starts = prefix if len(prefix) == 3 else (*prefix, None)
+        n, groups = _table(p_tables, "prefix tables", None), p_tables.shape[0]
+        specs += [(p_tables, "prefix tables", p_tables.shape, i32), (lengths, "prefix lengths", (groups,), i32)]
+        if starts is not None:
+            specs.append((starts, "prefix starts", (groups + 1,), i32))
+        elif groups != 1:
+            raise ValueError(f"{groups} prefixes need starts [{groups + 1}], the first sequence of each group")
+        pre = _fa.FaCachePrefix(groups, n, p_tables.data_ptr(), lengths.data_ptr(), _fa._ptr(starts))
+    key = (B, Hq, T, cols, groups, n)
+    sizes = cache._sizes.get(key)
+    if sizes is None:
+        ref = ctypes.byref(cache._dims(B, Hq, T, cols))
+        with _fa._on(cache.device):  # (it asks for the SMs)
+            nbytes = int(_fa.load().fa_cache_attention_workspace_bytes(ref, pre))
+        if len(cache._sizes) > 1000:
+            cache._sizes.clear()
+        sizes = cache._sizes[key] = (ref, nbytes)
+    return (*sizes, pre)
 
 
 def fa_cache_attention_workspace_bytes(Q, cache: KVCache, tables, prefix=None) -> int:
     """The workspace that fa_cache_attention needs (what it allocates without one)."""
     specs = []
-    dims, pre = _attention_dims(Q, cache, tables, prefix, specs)
+    nbytes = _attention_dims(Q, cache, tables, prefix, specs)[1]
     _fa._check_all(cache.device, specs)
-    with _fa._on(cache.device):
-        return int(_fa.load().fa_cache_attention_workspace_bytes(ctypes.byref(dims), pre))
+    return nbytes
 
 
 def fa_cache_attention(Q, cache: KVCache, tables, lengths, scale: float | None = None, window: int = 0,
@@ -186,7 +196,7 @@ def fa_cache_attention(Q, cache: KVCache, tables, lengths, scale: float | None =
     whole batch."""
     device, bf, f32 = cache.device, torch.bfloat16, torch.float32
     specs = [(Q, "Q", Q.shape, bf)]
-    dims, pre = _attention_dims(Q, cache, tables, prefix, specs)
+    ref, nbytes, pre = _attention_dims(Q, cache, tables, prefix, specs)
     (B, Hq, T, d), dv = Q.shape, cache.V.shape[3]
     specs.append((lengths, "lengths", (B,), torch.int32))
     if O is not None:
@@ -198,7 +208,7 @@ def fa_cache_attention(Q, cache: KVCache, tables, lengths, scale: float | None =
             raise ValueError("slopes have no gradient here; detach them")
         specs.append((slopes, "slopes", (Hq,), f32))
     _fa._check_all(device, specs)
-    lib, ref, given = _fa.load(), ctypes.byref(dims), (O, L)
+    lib, given = _fa.load(), (O, L)
     scores = _fa.FaCacheScores(float(scale or 0.0), float(softcap or 0.0), _fa._ptr(slopes), int(window))
     handle = _fa._stream_ptr(stream, device)
     with _fa._under(stream, device):
@@ -207,13 +217,12 @@ def fa_cache_attention(Q, cache: KVCache, tables, lengths, scale: float | None =
         if L is None:
             L = torch.empty((B, Hq, T), dtype=f32, device=device)
         if workspace is None:
-            nbytes = lib.fa_cache_attention_workspace_bytes(ref, pre)
             workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
         elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
         code = lib.fa_cache_attention(ref, cache._pools, ctypes.byref(scores), pre, Q.data_ptr(), tables.data_ptr(),
                                       lengths.data_ptr(), O.data_ptr(), L.data_ptr(), workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), handle)
+                                      workspace.nbytes, handle)
     if stream is not None:
         _fa._hand_over(device, (O, L), given)
     _fa._raise(code, "fa_cache_attention")

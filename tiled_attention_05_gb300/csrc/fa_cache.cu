@@ -8,8 +8,9 @@
 // it is.  Read back: bf16(code * scale).
 //
 // Mapping.  Both are bound by HBM: each byte is read once and written once.  A thread
-// owns 8 channels of a row (16 bytes in bf16, 8 in e4m3), the d / 8 lanes of a row agree
-// on its maximum by shuffles, and a thread has four rows in flight.
+// owns 8 channels of a position's key and value (16 bytes each in bf16, 8 in e4m3), the
+// lanes of a row agree on its maximum by shuffles, and a thread has several positions in
+// flight.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -25,14 +26,16 @@ using fa::kCacheRows;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // rows in flight per thread
+constexpr int kThreads = 128;
+constexpr int kUnroll = 2;  // positions in flight per thread (4, and blocks of 256, were slower: 21 -> 22 and 23 us)
 constexpr float kE4m3Max = 448.f, kLeast = 0x1p-60f;
 
 struct PageParams {
   const int *tables, *lengths;  // (write: the counts, or NULL)
   const int* starts;            // write
   int B, H, T, cols, pages, page_log2;
+  fa::Divide by_inner, by_outer;  // the rows' order: by T and H (token by token), or H and T (write, `heads_first`)
+  int heads_first;
   int* status;
   struct Side {  // K or V
     uint8_t* pool;
@@ -40,7 +43,7 @@ struct PageParams {
     uint16_t* rows;          // the new rows, or the result
     long long sb, sh, st;    // their strides (elements)
   } side[2];
-  long long units;  // B * H * T
+  int units;  // B * H * T
 };
 
 // Row of the pools for position `pos` of sequence b and head h; -1 where the table has
@@ -59,12 +62,13 @@ __device__ __forceinline__ long long pool_row(const PageParams& p, int b, int h,
 struct Unit {
   int b, h, t;
 };
-__device__ __forceinline__ Unit unit_of(const PageParams& p, long long n) {
-  const long long bh = n / p.T;
+__device__ __forceinline__ Unit unit_of(const PageParams& p, int n) {
+  const int outer = p.by_inner(n), inner = n - outer * (int)p.by_inner.by;
   Unit u;
-  u.t = (int)(n - bh * p.T);
-  u.b = (int)(bh / p.H);
-  u.h = (int)(bh - (long long)u.b * p.H);
+  u.b = p.by_outer(outer);
+  const int middle = outer - u.b * (int)p.by_outer.by;
+  u.h = p.heads_first ? inner : middle;
+  u.t = p.heads_first ? middle : inner;
   return u;
 }
 
@@ -81,48 +85,29 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// LANES threads hold a row (d / 8).
+// LANES threads hold a row of the wider of K and V, and the same positions' row of both:
+// where it goes is worked out once for the two (by itself for each, the write of T 8192,
+// B 2, 8 heads of 128 took 29 us, the read 20).  K_LANES, V_LANES: d / 8, dv / 8.
 template <int LANES, bool Q8>
-__device__ __forceinline__ void write_rows(const PageParams& p, const PageParams::Side& s) {
-  constexpr int ROWS = kThreads / LANES;
-  const int lane = threadIdx.x % LANES;
-  const long long n0 = (long long)blockIdx.x * (ROWS * kUnroll) + threadIdx.x / LANES;
-  uint4 x[kUnroll];
-  long long to[kUnroll];
+__device__ __forceinline__ void write_row(const PageParams::Side& s, uint4 x, long long to, int lane) {
+  if constexpr (Q8) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t two = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const long long n = n0 + u * ROWS;
-    to[u] = -1;
-    x[u] = make_uint4(0, 0, 0, 0);
-    if (n >= p.units) continue;
-    const Unit at = unit_of(p, n);
-    if (p.lengths && at.t >= __ldg(p.lengths + at.b)) continue;  // a padding token
-    to[u] = pool_row(p, at.b, at.h, (long long)__ldg(p.starts + at.b) + at.t);
-    x[u] = *reinterpret_cast<const uint4*>(s.rows + at.b * s.sb + at.h * s.sh + at.t * s.st + lane * 8);
-  }
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-    if constexpr (Q8) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-#pragma unroll
-      for (int o = LANES / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-      const bool finite = top < 0x7f80u;
-      const float a = fmaxf(__uint_as_float(top << 16), kLeast);
-      const float f = finite ? __fdiv_rn(kE4m3Max, a) : 0.f;
-      uint2 c;
-      c.x = codes4(bf_lo(w[0]) * f, bf_hi(w[0]) * f, bf_lo(w[1]) * f, bf_hi(w[1]) * f);
-      c.y = codes4(bf_lo(w[2]) * f, bf_hi(w[2]) * f, bf_lo(w[3]) * f, bf_hi(w[3]) * f);
-      if (!finite) c = make_uint2(0, 0);
-      if (to[u] >= 0) {
-        *reinterpret_cast<uint2*>(s.pool + to[u] * (LANES * 8) + lane * 8) = c;
-        if (lane == 0) s.scale[to[u]] = finite ? a * (1.f / kE4m3Max) : __uint_as_float(0x7fffffffu);
-      }
-    } else if (to[u] >= 0) {
-      *reinterpret_cast<uint4*>(s.pool + to[u] * (LANES * 16) + lane * 16) = x[u];
-    }
+    for (int o = LANES / 2; o; o >>= 1) two = __vmaxu2(two, __shfl_xor_sync(~0u, two, o));
+    const uint32_t top = max(two & 0xffffu, two >> 16);
+    const bool finite = top < 0x7f80u;
+    const float a = fmaxf(__uint_as_float(top << 16), kLeast);
+    const float f = finite ? __fdiv_rn(kE4m3Max, a) : 0.f;
+    uint2 c;
+    c.x = codes4(bf_lo(w[0]) * f, bf_hi(w[0]) * f, bf_lo(w[1]) * f, bf_hi(w[1]) * f);
+    c.y = codes4(bf_lo(w[2]) * f, bf_hi(w[2]) * f, bf_lo(w[3]) * f, bf_hi(w[3]) * f);
+    if (!finite) c = make_uint2(0, 0);
+    if (to < 0 || lane >= LANES) return;
+    *reinterpret_cast<uint2*>(s.pool + to * (LANES * 8) + lane * 8) = c;
+    if (lane == 0) s.scale[to] = finite ? a * (1.f / kE4m3Max) : __uint_as_float(0x7fffffffu);
+  } else if (to >= 0 && lane < LANES) {
+    *reinterpret_cast<uint4*>(s.pool + to * (LANES * 16) + lane * 16) = x;
   }
 }
 
@@ -130,69 +115,84 @@ template <int KL, int VL, bool Q8>
 __global__ void __launch_bounds__(kThreads) fa_cache_write_kernel(const PageParams p) {
   grid_next();
   grid_previous();
-  if (blockIdx.y == 0)
-    write_rows<KL, Q8>(p, p.side[0]);
-  else
-    write_rows<VL, Q8>(p, p.side[1]);
-}
-
-template <int LANES, bool Q8>
-__device__ __forceinline__ void read_rows(const PageParams& p, const PageParams::Side& s) {
-  constexpr int ROWS = kThreads / LANES;
-  const int lane = threadIdx.x % LANES;
-  const long long n0 = (long long)blockIdx.x * (ROWS * kUnroll) + threadIdx.x / LANES;
-  uint4 x[kUnroll];
-  float f[kUnroll];
+  constexpr int LANES = KL > VL ? KL : VL, ROWS = kThreads / LANES;
+  const int lane = threadIdx.x % LANES, n0 = blockIdx.x * (ROWS * kUnroll) + threadIdx.x / LANES;
+  uint4 k[kUnroll], v[kUnroll];
+  long long to[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const long long n = n0 + u * ROWS;
-    x[u] = make_uint4(0, 0, 0, 0);
-    f[u] = 0.f;
+    const int n = n0 + u * ROWS;
+    to[u] = -1;
+    k[u] = v[u] = make_uint4(0, 0, 0, 0);
     if (n >= p.units) continue;
     const Unit at = unit_of(p, n);
-    if (at.t >= __ldg(p.lengths + at.b)) continue;
-    const long long from = pool_row(p, at.b, at.h, at.t);
-    if (from < 0) continue;
-    if constexpr (Q8) {
-      const uint2 c = *reinterpret_cast<const uint2*>(s.pool + from * (LANES * 8) + lane * 8);
-      x[u].x = c.x, x[u].y = c.y;
-      f[u] = __ldg(s.scale + from);
-    } else {
-      x[u] = *reinterpret_cast<const uint4*>(s.pool + from * (LANES * 16) + lane * 16);
-    }
+    if (p.lengths && at.t >= __ldg(p.lengths + at.b)) continue;  // a padding token
+    const PageParams::Side &ks = p.side[0], &vs = p.side[1];
+    if (lane < KL) k[u] = *reinterpret_cast<const uint4*>(ks.rows + at.b * ks.sb + at.h * ks.sh + at.t * ks.st + lane * 8);
+    if (lane < VL) v[u] = *reinterpret_cast<const uint4*>(vs.rows + at.b * vs.sb + at.h * vs.sh + at.t * vs.st + lane * 8);
+    to[u] = pool_row(p, at.b, at.h, (long long)__ldg(p.starts + at.b) + at.t);
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const long long n = n0 + u * ROWS;
-    if (n >= p.units) continue;
-    uint4 out = x[u];
-    if constexpr (Q8) {
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t two = (k < 2 ? x[u].x : x[u].y) >> (16 * (k & 1));
-        uint32_t h;
-        asm("{\n\t.reg .b16 c, u;\n\tmov.b32 {c, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(two));
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-            : "=f"(v[2 * k]), "=f"(v[2 * k + 1])
-            : "r"(h));
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] *= f[u];
-      out = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    }
-    *reinterpret_cast<uint4*>(s.rows + n * (LANES * 8) + lane * 8) = out;
+    write_row<KL, Q8>(p.side[0], k[u], to[u], lane);
+    write_row<VL, Q8>(p.side[1], v[u], to[u], lane);
   }
+}
+
+// A lane's 8 values of a row, as bf16.
+template <int LANES, bool Q8>
+__device__ __forceinline__ uint4 load_row(const PageParams::Side& s, long long from, int lane) {
+  if constexpr (!Q8) return *reinterpret_cast<const uint4*>(s.pool + from * (LANES * 16) + lane * 16);
+  const uint2 c = *reinterpret_cast<const uint2*>(s.pool + from * (LANES * 8) + lane * 8);
+  return make_uint4(c.x, c.y, __float_as_uint(__ldg(s.scale + from)), 0);
+}
+__device__ __forceinline__ uint2 bf16_of(uint32_t codes, float f) {  // four codes
+  uint32_t a, b;
+  float v[4];
+  asm("{\n\t.reg .b16 c, u;\n\tmov.b32 {c, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(codes));
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}" : "=f"(v[0]), "=f"(v[1]) : "r"(a));
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}" : "=f"(v[2]), "=f"(v[3]) : "r"(b));
+  return make_uint2(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f));
+}
+template <int LANES, bool Q8>
+__device__ __forceinline__ void store_row(const PageParams::Side& s, int n, uint4 x, int lane) {
+  if (lane >= LANES) return;
+  if constexpr (Q8) {
+    const float f = __uint_as_float(x.z);
+    const uint2 a = bf16_of(x.x, f), b = bf16_of(x.y, f);
+    x = make_uint4(a.x, a.y, b.x, b.y);
+  }
+  *reinterpret_cast<uint4*>(s.rows + (long long)n * (LANES * 8) + lane * 8) = x;
 }
 
 template <int KL, int VL, bool Q8>
 __global__ void __launch_bounds__(kThreads) fa_cache_read_kernel(const PageParams p) {
   grid_next();
   grid_previous();
-  if (blockIdx.y == 0)
-    read_rows<KL, Q8>(p, p.side[0]);
-  else
-    read_rows<VL, Q8>(p, p.side[1]);
+  constexpr int LANES = KL > VL ? KL : VL, ROWS = kThreads / LANES;
+  const int lane = threadIdx.x % LANES, n0 = blockIdx.x * (ROWS * kUnroll) + threadIdx.x / LANES;
+  uint4 k[kUnroll], v[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int n = n0 + u * ROWS;
+    k[u] = v[u] = make_uint4(0, 0, 0, 0);
+    if (n >= p.units) continue;
+    const Unit at = unit_of(p, n);
+    if (at.t >= __ldg(p.lengths + at.b)) continue;
+    const long long from = pool_row(p, at.b, at.h, at.t);
+    if (from < 0) continue;
+    if (lane < KL) k[u] = load_row<KL, Q8>(p.side[0], from, lane);
+    if (lane < VL) v[u] = load_row<VL, Q8>(p.side[1], from, lane);
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int n = n0 + u * ROWS;
+    if (n >= p.units) continue;
+    store_row<KL, Q8>(p.side[0], n, k[u], lane);
+    store_row<VL, Q8>(p.side[1], n, v[u], lane);
+  }
 }
 
 // ---------------------------------------------------------------- join
@@ -327,7 +327,8 @@ fa_status check_cache_dims(const fa_cache_dims* dims) {
   if ((z.d != 64 && z.d != 128) || (z.dv != 64 && z.dv != 128)) return FA_ERR_UNSUPPORTED;
   if (z.page < 16 || z.page > 256 || (z.page & (z.page - 1))) return FA_ERR_UNSUPPORTED;
   if ((long long)z.table_pages * z.page > (1 << 30) || z.T > (1 << 30)) return FA_ERR_UNSUPPORTED;
-  if ((long long)z.B * z.Hkv > INT_MAX || (long long)z.pages * z.Hkv > INT_MAX) return FA_ERR_UNSUPPORTED;
+  if ((long long)z.B * z.Hkv > INT_MAX || (long long)z.B * z.Hkv * z.T > (1 << 30) || (long long)z.pages * z.Hkv > INT_MAX)
+    return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
@@ -360,18 +361,18 @@ PageParams page_params(const fa_cache_dims& z, const fa_kv_cache& c, const int* 
   p.side[1].pool = static_cast<uint8_t*>(c.V);
   p.side[0].scale = c.k_scale;
   p.side[1].scale = c.v_scale;
-  p.units = (long long)z.B * z.Hkv * z.T;
+  p.units = z.B * z.Hkv * z.T;
+  p.by_inner = fa::Divide::of(z.T);
+  p.by_outer = fa::Divide::of(z.Hkv);
   p.status = fa::device_status_word();
   return p;
 }
 
 template <typename Kernel>
 fa_status launch_pages(Kernel kernel, const fa_cache_dims& z, const PageParams& p, void* stream) {
-  // blocks of the wider rows; the narrower side needs half as many
   const int lanes = (z.d > z.dv ? z.d : z.dv) / 8;
-  const long long per = (long long)(kThreads / lanes) * kUnroll, blocks = (p.units + per - 1) / per;
-  if (blocks > INT_MAX) return FA_ERR_UNSUPPORTED;
-  return fa::launch_next(kernel, dim3((unsigned)blocks, 2), kThreads, 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess
+  const int per = kThreads / lanes * kUnroll, blocks = (p.units + per - 1) / per;
+  return fa::launch_next(kernel, dim3((unsigned)blocks), kThreads, 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
 }
@@ -427,6 +428,12 @@ fa_status fa_cache_write(const fa_cache_dims* dims, const fa_kv_cache* cache, co
   PageParams p = page_params(z, *cache, tables, counts);
   if (!p.status) return FA_ERR_CUDA;
   p.starts = starts;
+  // The rows as they lie: of a packed projection a token's heads are neighbours.
+  if (z.Hkv > 1 && k_stride[1] < k_stride[2]) {
+    p.heads_first = 1;
+    p.by_inner = fa::Divide::of(z.Hkv);
+    p.by_outer = fa::Divide::of(z.T);
+  }
   const void* rows[2] = {K, V};
   const long long* strides[2] = {k_stride, v_stride};
   for (int k = 0; k < 2; ++k) {

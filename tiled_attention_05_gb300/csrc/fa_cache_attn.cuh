@@ -63,7 +63,7 @@ struct CacheCfg {
   static constexpr int ROWS8 = 8 * DV * 4;
   static constexpr bool IN_STAGE = STAGE >= ROWS8;
   static constexpr int JOIN = IN_STAGE ? 0 : fa::kCacheWarps * ROWS8;
-  static constexpr int ROOM = ((228 << 10) / CTAS - 1024 - 1536 - JOIN) / fa::kCacheWarps / STAGE;
+  static constexpr int ROOM = ((228 << 10) / CTAS - 1024 - 2560 - JOIN) / fa::kCacheWarps / STAGE;
   static constexpr int NS = ROOM > 6 ? 6 : ROOM;
   static constexpr int RING = NS * STAGE;  // per warp
   static constexpr int SMEM = fa::kCacheWarps * RING + JOIN;
@@ -167,6 +167,11 @@ __device__ __forceinline__ void cap_scores(const fa::CapParams& c, float (&t)[RT
     for (int x = 0; x < 4; ++x) t[u][x] = y[u][x];
 }
 
+struct __align__(16) Row {
+  int at, last;  // position among the entry's keys (key j is at - j behind it), last key it may see
+  int out;       // row of the result; -1: none; padding: -2 - row
+  float slope;
+};
 // The softmax's reference follows a row's maximum when that has grown by more than this
 // (log2 units: weights stay <= 256).
 constexpr float kGrown = 8.f;
@@ -180,6 +185,8 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[fa::kCacheWarps][kRows];
   __shared__ int s_free[fa::kCacheWarps];
+  __shared__ Row s_row[fa::kCacheWarps][kRows];
+  __shared__ Cursor s_load[fa::kCacheWarps];
   // Beside the prefixes' kernel (launched so that it may start with that): what comes before
   // both has completed; the end waits for that one, as the join waits for this one only.
   const auto share = fa::cache_share<KC, kRows, fa::kCacheItem, kThreads>(p);
@@ -195,12 +202,16 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
 
   // ------------------------------------------------------------ loads, ahead of the use
   // An item's chunks go round the warps, from another one on for each item of the share.
-  Cursor ld = share.start;
+  Cursor& ld = s_load[warp];  // (in shared memory: registers are short)
+  if (lane == 0) ld = share.start;
+  __syncwarp();
   int lc = ld.c + warp, lc_end = ld.end(share.end), l_turn = 0;
   auto next_load = [&](int step) {  // to this warp's next chunk (lc >= lc_end: there is none)
     lc += step;
     while (lc >= lc_end) {
-      ld.next(p);
+      __syncwarp();
+      if (lane == 0) ld.next(p);
+      __syncwarp();
       if (ld.at >= share.end) return;
       ++l_turn;
       lc = ld.c + ((warp - l_turn) & 3);
@@ -303,21 +314,23 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
           q[u][k] = pack_f16x2(__uint_as_float(q[u][k] << 16) * down, __uint_as_float(q[u][k] & 0xffff0000u) * down);
       }
     }
-    // The rows whose scores this lane has: 2 li and 2 li + 1 of each tile of 8.
-    int at0[2 * RT], last[2 * RT];  // position among the entry's keys (key j is at0 - j behind it), last key it may see
-    int out[2 * RT];  // row of the result; -1: none; padding: ~row - 1
-    float slope[2 * RT], unit[2 * RT];
-#pragma unroll
-    for (int y = 0; y < 2 * RT; ++y) {
-      const fa::CacheRow r = fa::cache_row(p, n, it.r * kRows + 2 * li + (y & 1) + 8 * (y >> 1));
-      const int pos = (is_prefix ? fa::cache_length(p, r.b) : n.keys) - p.T + r.t;
-      out[y] = (r.b * p.Hq + it.h * p.G + r.g) * p.T + r.t;
-      out[y] = !r.valid ? -1 : pos < 0 ? -2 - out[y] : out[y];
-      at0[y] = is_prefix ? n.keys + pos : pos;
-      last[y] = is_prefix ? n.keys - 1 : pos;
-      slope[y] = p.slopes ? __ldg(p.slopes + it.h * p.G + r.g) * 1.4426950408889634f : 0.f;
-      unit[y] = __shfl_sync(~0u, scale[y >> 1], (2 * li + (y & 1)) * 4);
+    // The rows whose scores this lane has: 2 li and 2 li + 1 of each tile of 8.  What is seldom
+    // asked of a row lies in shared memory.
+    __syncwarp();
+    if (lane < kRows) {
+      const fa::CacheRow r = fa::cache_row(p, n, it.r * kRows + lane);
+      const int pos = (is_prefix ? fa::cache_length(p, r.b) : n.keys) - p.T + r.t, out = (r.b * p.Hq + it.h * p.G + r.g) * p.T + r.t;
+      Row& row = s_row[warp][lane];
+      row.at = is_prefix ? n.keys + pos : pos;
+      row.last = is_prefix ? n.keys - 1 : pos;
+      row.out = !r.valid ? -1 : pos < 0 ? -2 - out : out;
+      row.slope = p.slopes ? __ldg(p.slopes + it.h * p.G + r.g) * 1.4426950408889634f : 0.f;
     }
+    __syncwarp();
+    auto row_of = [&](int y) -> const Row& { return s_row[warp][2 * li + (y & 1) + 8 * (y >> 1)]; };
+    float unit[2 * RT];
+#pragma unroll
+    for (int y = 0; y < 2 * RT; ++y) unit[y] = __shfl_sync(~0u, scale[y >> 1], (2 * li + (y & 1)) * 4);
     float m[2 * RT], l[2 * RT], o[RT][MT][4];
 #pragma unroll
     for (int y = 0; y < 2 * RT; ++y) m[y] = -INFINITY, l[y] = 0.f;
@@ -394,19 +407,22 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
       if (p.capped) cap_scores(p.cap, t);
       if (p.slopes) {
 #pragma unroll
-        for (int u = 0; u < RT; ++u)
+        for (int y = 0; y < 2 * RT; ++y) {
+          const Row row = row_of(y);
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            t[u][x] -= slope[2 * u + (x & 1)] * (float)(at0[2 * u + (x & 1)] - (key0 + lr + 8 * (x >> 1)));
+          for (int x = y & 1; x < 4; x += 2) t[y >> 1][x] -= row.slope * (float)(row.at - (key0 + lr + 8 * (x >> 1)));
+        }
       }
       if (key0 + KC > all_to || key0 < all_from) {
 #pragma unroll
-        for (int u = 0; u < RT; ++u)
+        for (int y = 0; y < 2 * RT; ++y) {
+          const Row row = row_of(y);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = key0 + lr + 8 * (x >> 1), y = 2 * u + (x & 1);
-            if (key > last[y] || (p.window && at0[y] - key >= p.window)) t[u][x] = -INFINITY;
+          for (int x = y & 1; x < 4; x += 2) {
+            const int key = key0 + lr + 8 * (x >> 1);
+            if (key > row.last || (p.window && row.at - key >= p.window)) t[y >> 1][x] = -INFINITY;
           }
+        }
       }
       bool grown = false;
 #pragma unroll
@@ -544,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int to = out[2 * u + y];
+        const int to = row_of(2 * u + y).out;
         if (to == -1) continue;
         const bool none = to < 0;  // a padding row
         if (none) sum[y] = 0.f;

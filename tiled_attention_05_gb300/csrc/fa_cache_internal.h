@@ -21,7 +21,7 @@ constexpr int kCacheRows = 16;      // query rows of an item: one MMA's
 constexpr int kCacheWarps = 4;      // warps of a CTA; each walks every fourth chunk of its keys
 // CTAs an SM.  e4m3 takes about twice the instructions a byte (its codes become fp16), so
 // it needs the warps.
-constexpr int cache_ctas(bool quantised, bool few) { return quantised && few ? 3 : 2; }
+constexpr int cache_ctas(bool quantised, bool few) { return quantised ? 3 : 2; }
 constexpr bool cache_few(long long rows, bool prefixes) { return rows <= 8 && !prefixes; }
 // A CTA gets this much work at least, in chunks of keys, and an item counts as so many
 // chunks more than it has, for its set-up and the joining of its parts.
