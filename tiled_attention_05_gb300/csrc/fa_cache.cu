@@ -8,9 +8,8 @@
 // it is.  Read back: bf16(code * scale).
 //
 // Mapping.  Both are bound by HBM: each byte is read once and written once.  A thread
-// owns 8 channels of a position's key and value (16 bytes each in bf16, 8 in e4m3), the
-// lanes of a row agree on its maximum by shuffles, and a thread has several positions in
-// flight.
+// owns some channels of a position's key and value, the lanes of a row agree on its maximum
+// by shuffles, and a thread has several positions in flight.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -27,7 +26,10 @@ using fa::kCacheRows;
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 2;  // positions in flight per thread (4, and blocks of 256, were slower: 21 -> 22 and 23 us)
+// Positions in flight per thread.  Blocks of 256 and more in flight were slower (write of
+// T 8192, B 2, 8 heads of 128: 17.5, 19.3 and 22.9 us with 1, 2 and 4).
+template <bool WRITE, bool Q8>
+constexpr int kUnroll = WRITE && Q8 ? 1 : 2;
 constexpr float kE4m3Max = 448.f, kLeast = 0x1p-60f;
 
 struct PageParams {
@@ -85,61 +87,81 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// LANES threads hold a row of the wider of K and V, and the same positions' row of both:
-// where it goes is worked out once for the two (by itself for each, the write of T 8192,
-// B 2, 8 heads of 128 took 29 us, the read 20).  K_LANES, V_LANES: d / 8, dv / 8.
+// The lanes of a row hold some channels each, for the same position's row of both K and V:
+// where it goes is worked out once for the two.  A lane that quantises has 16 (its
+// instructions are the bound then: a thread for each of K and V 29 us, 8 channels 21, 16
+// channels 17.5, of T 8192 as above); one that reads back has 8, since its two halves of 32 bytes
+// would leave by two stores (17.7 us, 16 channels 20.8).  LANES: of this row; the wider
+// of the two decides the group's size.
+template <bool Q8>
+constexpr int kChannels = Q8 ? 16 : 8;  // write
+template <bool Q8>
+struct Piece {
+  uint4 x[Q8 ? 2 : 1];
+};
+
 template <int LANES, bool Q8>
-__device__ __forceinline__ void write_row(const PageParams::Side& s, uint4 x, long long to, int lane) {
+__device__ __forceinline__ void write_row(const PageParams::Side& s, const Piece<Q8>& piece, long long to, int lane) {
   if constexpr (Q8) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t two = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    const uint32_t w[8] = {piece.x[0].x, piece.x[0].y, piece.x[0].z, piece.x[0].w, piece.x[1].x, piece.x[1].y, piece.x[1].z, piece.x[1].w};
+    uint32_t two = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) two = __vmaxu2(two, w[k] & 0x7fff7fffu);
 #pragma unroll
     for (int o = LANES / 2; o; o >>= 1) two = __vmaxu2(two, __shfl_xor_sync(~0u, two, o));
     const uint32_t top = max(two & 0xffffu, two >> 16);
     const bool finite = top < 0x7f80u;
     const float a = fmaxf(__uint_as_float(top << 16), kLeast);
     const float f = finite ? __fdiv_rn(kE4m3Max, a) : 0.f;
-    uint2 c;
-    c.x = codes4(bf_lo(w[0]) * f, bf_hi(w[0]) * f, bf_lo(w[1]) * f, bf_hi(w[1]) * f);
-    c.y = codes4(bf_lo(w[2]) * f, bf_hi(w[2]) * f, bf_lo(w[3]) * f, bf_hi(w[3]) * f);
-    if (!finite) c = make_uint2(0, 0);
+    const uint64_t f2 = f2_pack(f, f);
+    uint32_t c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t u = f2_mul(f2_pack(bf_lo(w[2 * k]), bf_hi(w[2 * k])), f2), v = f2_mul(f2_pack(bf_lo(w[2 * k + 1]), bf_hi(w[2 * k + 1])), f2);
+      c[k] = finite ? codes4(f2_lo(u), f2_hi(u), f2_lo(v), f2_hi(v)) : 0u;
+    }
     if (to < 0 || lane >= LANES) return;
-    *reinterpret_cast<uint2*>(s.pool + to * (LANES * 8) + lane * 8) = c;
+    *reinterpret_cast<uint4*>(s.pool + to * (LANES * 16) + lane * 16) = make_uint4(c[0], c[1], c[2], c[3]);
     if (lane == 0) s.scale[to] = finite ? a * (1.f / kE4m3Max) : __uint_as_float(0x7fffffffu);
   } else if (to >= 0 && lane < LANES) {
-    *reinterpret_cast<uint4*>(s.pool + to * (LANES * 16) + lane * 16) = x;
+    *reinterpret_cast<uint4*>(s.pool + to * (LANES * 16) + lane * 16) = piece.x[0];
   }
 }
+template <bool Q8>
+__device__ __forceinline__ void load_new(const PageParams::Side& s, const Unit& at, int lane, Piece<Q8>& piece) {
+  const uint4* src = reinterpret_cast<const uint4*>(s.rows + at.b * s.sb + at.h * s.sh + at.t * s.st + lane * kChannels<Q8>);
+  piece.x[0] = src[0];
+  if constexpr (Q8) piece.x[1] = src[1];
+}
 
-template <int KL, int VL, bool Q8>
+template <int D, int DV, bool Q8>
 __global__ void __launch_bounds__(kThreads) fa_cache_write_kernel(const PageParams p) {
   grid_next();
   grid_previous();
-  constexpr int LANES = KL > VL ? KL : VL, ROWS = kThreads / LANES;
-  const int lane = threadIdx.x % LANES, n0 = blockIdx.x * (ROWS * kUnroll) + threadIdx.x / LANES;
-  uint4 k[kUnroll], v[kUnroll];
-  long long to[kUnroll];
+  constexpr int N = kUnroll<true, Q8>, KL = D / kChannels<Q8>, VL = DV / kChannels<Q8>, LANES = KL > VL ? KL : VL,
+                ROWS = kThreads / LANES;
+  const int lane = threadIdx.x % LANES, n0 = blockIdx.x * (ROWS * N) + threadIdx.x / LANES;
+  Piece<Q8> k[N] = {}, v[N] = {};
+  long long to[N];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < N; ++u) {
     const int n = n0 + u * ROWS;
     to[u] = -1;
-    k[u] = v[u] = make_uint4(0, 0, 0, 0);
     if (n >= p.units) continue;
     const Unit at = unit_of(p, n);
     if (p.lengths && at.t >= __ldg(p.lengths + at.b)) continue;  // a padding token
-    const PageParams::Side &ks = p.side[0], &vs = p.side[1];
-    if (lane < KL) k[u] = *reinterpret_cast<const uint4*>(ks.rows + at.b * ks.sb + at.h * ks.sh + at.t * ks.st + lane * 8);
-    if (lane < VL) v[u] = *reinterpret_cast<const uint4*>(vs.rows + at.b * vs.sb + at.h * vs.sh + at.t * vs.st + lane * 8);
+    if (lane < KL) load_new<Q8>(p.side[0], at, lane, k[u]);
+    if (lane < VL) load_new<Q8>(p.side[1], at, lane, v[u]);
     to[u] = pool_row(p, at.b, at.h, (long long)__ldg(p.starts + at.b) + at.t);
   }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < N; ++u) {
     write_row<KL, Q8>(p.side[0], k[u], to[u], lane);
     write_row<VL, Q8>(p.side[1], v[u], to[u], lane);
   }
 }
 
-// A lane's 8 values of a row, as bf16.
+// A lane's 8 values of a row (e4m3: the codes, and the scale in z).
 template <int LANES, bool Q8>
 __device__ __forceinline__ uint4 load_row(const PageParams::Side& s, long long from, int lane) {
   if constexpr (!Q8) return *reinterpret_cast<const uint4*>(s.pool + from * (LANES * 16) + lane * 16);
@@ -167,15 +189,15 @@ __device__ __forceinline__ void store_row(const PageParams::Side& s, int n, uint
   *reinterpret_cast<uint4*>(s.rows + (long long)n * (LANES * 8) + lane * 8) = x;
 }
 
-template <int KL, int VL, bool Q8>
+template <int D, int DV, bool Q8>
 __global__ void __launch_bounds__(kThreads) fa_cache_read_kernel(const PageParams p) {
   grid_next();
   grid_previous();
-  constexpr int LANES = KL > VL ? KL : VL, ROWS = kThreads / LANES;
-  const int lane = threadIdx.x % LANES, n0 = blockIdx.x * (ROWS * kUnroll) + threadIdx.x / LANES;
-  uint4 k[kUnroll], v[kUnroll];
+  constexpr int N = kUnroll<false, Q8>, KL = D / 8, VL = DV / 8, LANES = KL > VL ? KL : VL, ROWS = kThreads / LANES;
+  const int lane = threadIdx.x % LANES, n0 = blockIdx.x * (ROWS * N) + threadIdx.x / LANES;
+  uint4 k[N], v[N];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < N; ++u) {
     const int n = n0 + u * ROWS;
     k[u] = v[u] = make_uint4(0, 0, 0, 0);
     if (n >= p.units) continue;
@@ -187,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) fa_cache_read_kernel(const PageParam
     if (lane < VL) v[u] = load_row<VL, Q8>(p.side[1], from, lane);
   }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < N; ++u) {
     const int n = n0 + u * ROWS;
     if (n >= p.units) continue;
     store_row<KL, Q8>(p.side[0], n, k[u], lane);
@@ -369,9 +391,9 @@ PageParams page_params(const fa_cache_dims& z, const fa_kv_cache& c, const int* 
 }
 
 template <typename Kernel>
-fa_status launch_pages(Kernel kernel, const fa_cache_dims& z, const PageParams& p, void* stream) {
-  const int lanes = (z.d > z.dv ? z.d : z.dv) / 8;
-  const int per = kThreads / lanes * kUnroll, blocks = (p.units + per - 1) / per;
+fa_status launch_pages(Kernel kernel, const fa_cache_dims& z, const PageParams& p, int channels, int unroll, void* stream) {
+  const int lanes = (z.d > z.dv ? z.d : z.dv) / channels;
+  const int per = kThreads / lanes * unroll, blocks = (p.units + per - 1) / per;
   return fa::launch_next(kernel, dim3((unsigned)blocks), kThreads, 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
@@ -444,10 +466,11 @@ fa_status fa_cache_write(const fa_cache_dims* dims, const fa_kv_cache* cache, co
   }
   auto pick = [&](auto q8) {
     constexpr bool Q = decltype(q8)::value;
-    return z.d == 64 ? (z.dv == 64 ? fa_cache_write_kernel<8, 8, Q> : fa_cache_write_kernel<8, 16, Q>)
-                     : (z.dv == 64 ? fa_cache_write_kernel<16, 8, Q> : fa_cache_write_kernel<16, 16, Q>);
+    return z.d == 64 ? (z.dv == 64 ? fa_cache_write_kernel<64, 64, Q> : fa_cache_write_kernel<64, 128, Q>)
+                     : (z.dv == 64 ? fa_cache_write_kernel<128, 64, Q> : fa_cache_write_kernel<128, 128, Q>);
   };
-  return launch_pages(z.quantised ? pick(std::true_type{}) : pick(std::false_type{}), z, p, stream);
+  return z.quantised ? launch_pages(pick(std::true_type{}), z, p, kChannels<true>, kUnroll<true, true>, stream)
+                     : launch_pages(pick(std::false_type{}), z, p, kChannels<false>, kUnroll<true, false>, stream);
 }
 
 fa_status fa_cache_read(const fa_cache_dims* dims, const fa_kv_cache* cache, const int* tables, const int* lengths,
@@ -465,10 +488,10 @@ fa_status fa_cache_read(const fa_cache_dims* dims, const fa_kv_cache* cache, con
   p.side[1].rows = static_cast<uint16_t*>(V);
   auto pick = [&](auto q8) {
     constexpr bool Q = decltype(q8)::value;
-    return z.d == 64 ? (z.dv == 64 ? fa_cache_read_kernel<8, 8, Q> : fa_cache_read_kernel<8, 16, Q>)
-                     : (z.dv == 64 ? fa_cache_read_kernel<16, 8, Q> : fa_cache_read_kernel<16, 16, Q>);
+    return z.d == 64 ? (z.dv == 64 ? fa_cache_read_kernel<64, 64, Q> : fa_cache_read_kernel<64, 128, Q>)
+                     : (z.dv == 64 ? fa_cache_read_kernel<128, 64, Q> : fa_cache_read_kernel<128, 128, Q>);
   };
-  return launch_pages(z.quantised ? pick(std::true_type{}) : pick(std::false_type{}), z, p, stream);
+  return launch_pages(z.quantised ? pick(std::true_type{}) : pick(std::false_type{}), z, p, 8, kUnroll<false, false>, stream);
 }
 
 size_t fa_cache_attention_workspace_bytes(const fa_cache_dims* dims, const fa_cache_prefix* prefix) {

@@ -99,10 +99,10 @@ cudaError_t launch_cache_join(const CacheJoin& j, int dv, cudaStream_t stream);
 // Keys of a chunk, the unit of the walk: what one warp holds in one stage of its ring.
 constexpr int kCacheKeys = 16;
 
-// What an SM takes for a chunk of own keys (its bytes at ~110 a ns), where a prefix's tile
+// What an SM takes for a chunk of own keys (its bytes at ~100 a ns), where a prefix's tile
 // pair of heads of 128, 1.5 us, is 1024.
 constexpr int cache_chunk_cost(int d, int dv, bool quantised) {
-  return kCacheKeys * (quantised ? d + dv + 8 : 2 * (d + dv)) * 1024 / (110 * 1500) * 256 / (d + dv);
+  return kCacheKeys * (quantised ? d + dv + 8 : 2 * (d + dv)) * 1024 / (100 * 1500) * 256 / (d + dv);
 }
 // Whether the prefixes go through the kernel that takes 128 rows at a time (`rows`: those
 // of all sequences' kv heads).
