@@ -303,7 +303,7 @@ FA_API fa_status fa_cache_read(const fa_cache_dims* dims, const fa_kv_cache* cac
  * sequence's rows sees have to be finite for its other rows too.
  *
  * workspace: fa_cache_attention_workspace_bytes (it asks the current device for its
- * SMs), 256-byte aligned, contents ignored. */
+ * SMs; 0 where the tables hold few positions), 256-byte aligned, contents ignored. */
 typedef struct {
   float scale, softcap;
   const float* slopes; /* device, [Hq], or NULL */

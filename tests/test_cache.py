@@ -101,8 +101,9 @@ def test_abi_read_refuses_the_rest():
 
 def test_abi_attention_refuses_the_rest():
     S, P = fa.FaCacheScores, fa.FaCachePrefix
-    for bad in (dict(q=0), dict(q=0x5008), dict(o=0), dict(o=0x9008), dict(l=0xa002), dict(lengths=0), dict(ws=0), dict(ws=0x100010),
-                dict(nbytes=0), dict(scores=S(math.nan, 0, None, 0)), dict(scores=S(math.inf, 0, None, 0)),
+    for bad in (dict(ws=0), dict(ws=0x100010), dict(nbytes=0)):
+        assert abi_attention(dims(table_pages=100), **bad) == fa.FA_ERR_INVALID_ARG, bad
+    for bad in (dict(q=0), dict(q=0x5008), dict(o=0), dict(o=0x9008), dict(l=0xa002), dict(lengths=0), dict(scores=S(math.nan, 0, None, 0)), dict(scores=S(math.inf, 0, None, 0)),
                 dict(scores=S(0, -1.0, None, 0)), dict(scores=S(0, 2000.0, None, 0)), dict(scores=S(0, math.nan, None, 0)),
                 dict(scores=S(0, 0, 0x10002, 0)), dict(scores=S(0, 0, None, -1)), dict(prefix=P(-1, 4, 0x7000, 0x8000, None)),
                 dict(prefix=P(1, -4, 0x7000, 0x8000, None)), dict(prefix=P(1, 4, None, 0x8000, None)),
@@ -116,7 +117,9 @@ def test_abi_attention_refuses_the_rest():
     # distances past 2^24 are not exact in fp32
     far = dims(table_pages=(1 << 20) + 1)
     assert abi_attention(far, scores=S(0, 0, 0x10000, 0)) == fa.FA_ERR_UNSUPPORTED
-    z = dims()
+    # few positions: no workspace is asked for
+    assert fa.load().fa_cache_attention_workspace_bytes(ctypes.byref(dims()), None) == 0
+    z = dims(table_pages=100)
     need = fa.load().fa_cache_attention_workspace_bytes(ctypes.byref(z), None)
     assert need > 0 and abi_attention(z, nbytes=need - 1) == fa.FA_ERR_INVALID_ARG
     assert fa.load().fa_cache_attention_workspace_bytes(ctypes.byref(dims(Hq=3)), None) == 0
@@ -266,9 +269,10 @@ SHAPES = [
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("long_tables", [False, True])  # (whole items where they hold few positions)
 @pytest.mark.parametrize("lens, Hq, Hkv, T, d, dv, page", SHAPES)
-def test_attention(lens, Hq, Hkv, T, d, dv, page, quant):
-    s = Setup(lens, Hkv, d, dv, quant, page)
+def test_attention(lens, Hq, Hkv, T, d, dv, page, quant, long_tables):
+    s = Setup(lens, Hkv, d, dv, quant, page, extra_cols=70 if long_tables else 1)
     Q = query(s, Hq, T, std=1.5)
     O, L = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths)
     check(s, Q, O, L)
@@ -625,7 +629,7 @@ def test_shared_prefix_is_the_same_as_a_copy_for_each():
 def test_captured_step_is_replayed_with_other_lengths():
     """Write and attention in one graph: the next tokens, lengths and pages are what the
     buffers hold at the replay; two graphs with one workspace, replayed in turn."""
-    s = Setup([102, 32, 61], 2, 64, 64, True, 16)  # (all that a replay sees is held: the rest is NaN)
+    s = Setup([102, 32, 61], 2, 64, 64, True, 16, extra_cols=60)  # (all that a replay sees is held: the rest is NaN)
     K, V = (torch.randn(3, 2, 1, 64, device="cuda").to(bf) for _ in range(2))
     Q, starts = query(s, 4, 1), torch.tensor([100, 30, 7], dtype=torch.int32, device="cuda")
     lengths = starts + 1

@@ -26,6 +26,7 @@ using namespace fa;
 #define CHECK(x) do { if (!(x)) { std::printf("failed: %s (call %d)\n", #x, call); std::exit(1); } } while (0)
 
 // ROWS 16: own keys and prefixes in one list; 256: the prefixes' own list
+int wholes = 0;
 template <int KC, int ROWS>
 void follow(int call, std::mt19937& rng) {
   constexpr bool PRE = ROWS == kPrefixRows;
@@ -55,13 +56,16 @@ void follow(int call, std::mt19937& rng) {
   const CacheShape all = cache_shape(p.B, p.Hkv, rows, 64, call % 2, (long long)p.cols << p.page_log2, p.S,
                                        (long long)p.p_cols << p.page_log2, sms);
   if (PRE && !all.apart) return;
+  p.whole = all.whole;
+  wholes += all.whole;
   const CacheList shape = PRE ? all.pre : all.list;
   // the lists' areas follow one another
   auto fits = [&](const CacheList& l, long long n, int item_rows, size_t end) {
     return l.head + (n + 1) * sizeof(CacheHead) <= l.ml && l.ml + l.slots * item_rows * 8 <= l.part &&
            l.part + l.slots * item_rows * 64 * 4 <= end;
   };
-  CHECK(fits(all.list, all.apart ? p.B : p.S + p.B, kCacheRows, all.apart ? all.pre.head : all.total));
+  if (all.whole) CHECK(all.total == 0 && p.S == 0);
+  else CHECK(fits(all.list, all.apart ? p.B : p.S + p.B, kCacheRows, all.apart ? all.pre.head : all.total));
   if (all.apart) CHECK(fits(all.pre, p.S, kPrefixRows, all.total));
   // the entries' places, as CTA 0 writes them
   std::vector<CacheHead> head(entries);
@@ -70,7 +74,7 @@ void follow(int call, std::mt19937& rng) {
   for (int e = 0; e < entries; ++e) {
     const CacheEntry n = cache_entry<KC>(p, e);
     head[e] = {(int)total, items, n.chunks};
-    if (n.chunks) total += (long long)p.Hkv * n.tiles(ROWS) * (n.chunks + kItem);
+    if (n.chunks || p.whole) total += (long long)p.Hkv * n.tiles(ROWS) * (n.chunks + kItem);
     chunks += (long long)p.Hkv * n.tiles(ROWS) * n.chunks;
     items += p.Hkv * n.tiles(ROWS);
   }
@@ -80,17 +84,19 @@ void follow(int call, std::mt19937& rng) {
   CHECK(per * shape.grid >= total);
   std::set<std::tuple<int, int, int, int>> seen;
   std::map<long long, std::pair<int, int>> slots;  // slot -> item, CTA
+  std::set<int> items_seen;
   for (int cta = 0; cta < shape.grid; ++cta) {
     const long long begin = cta * per, end = begin + per < total ? begin + per : total;
     if (begin >= end) break;
     using Cursor = CacheCursor<KC, ROWS, kItem>;
     int e = 0;
-    while (!(head[e].chunks && begin < head[e].work + (long long)p.Hkv * cache_entry<KC>(p, e).tiles(ROWS) * (head[e].chunks + kItem))) ++e;
+    while (!((head[e].chunks || p.whole) && begin < head[e].work + (long long)p.Hkv * cache_entry<KC>(p, e).tiles(ROWS) * (head[e].chunks + kItem))) ++e;
     Cursor it;
     it.start(p, e, head[e].item, (int)begin, (int)(begin - head[e].work));
     for (; it.at < end; it.next(p)) {
-      const int c_end = it.end((int)end);
-      CHECK(it.c < c_end);
+      const int c_end = it.end(p, (int)end);
+      CHECK(p.whole ? it.c == 0 && c_end == it.n.chunks : it.c < c_end);
+      if (p.whole) CHECK(items_seen.insert(it.item).second);
       CHECK(it.item == head[it.e].item + it.h * it.n.tiles(ROWS) + it.r);
       CHECK(it.at == head[it.e].work + (it.h * it.n.tiles(ROWS) + it.r) * (it.n.chunks + kItem) + it.c);
       CHECK(it.item + cta < shape.slots);
@@ -108,7 +114,7 @@ void follow(int call, std::mt19937& rng) {
         ld.start(p, e, head[e].item, (int)begin, (int)(begin - head[e].work));
         if (ld.at >= end) break;
         Cursor use = ld;
-        int lc = ld.c + warp, lc_end = ld.end((int)end), turn = 0;
+        int lc = ld.c + warp, lc_end = ld.end(p, (int)end), turn = 0;
         auto next_load = [&](int step) {
           lc += step;
           while (lc >= lc_end) {
@@ -116,13 +122,13 @@ void follow(int call, std::mt19937& rng) {
             if (ld.at >= end) return;
             ++turn;
             lc = ld.c + ((warp - turn) & 3);
-            lc_end = ld.end((int)end);
+            lc_end = ld.end(p, (int)end);
           }
         };
         next_load(0);
         int t = 0;
         for (; use.at < end; use.next(p), ++t)
-          for (int c = use.c + ((warp - t) & 3); c < use.end((int)end); c += 4) {
+          for (int c = use.c + ((warp - t) & 3); c < use.end(p, (int)end); c += 4) {
             CHECK(lc < lc_end && ld.item == use.item && lc == c);
             next_load(4);
           }
@@ -130,6 +136,10 @@ void follow(int call, std::mt19937& rng) {
       }
   }
   CHECK((long long)seen.size() == chunks);
+  if (p.whole) {
+    CHECK((int)items_seen.size() == items);
+    return;
+  }
   for (int e = 0; e < entries; ++e) {
     const CacheEntry n = cache_entry<KC>(p, e);
     for (int h = 0; h < p.Hkv; ++h)
@@ -163,6 +173,8 @@ int main() {
     follow<kCacheKeys, kCacheRows>(call, rng);
     follow<kPrefixKeys, kPrefixRows>(call, rng);
   }
+  const int call = -1;
+  CHECK(wholes > 10);
   std::printf("ok\n");
 }
 """

@@ -175,7 +175,8 @@ def _attention_dims(Q, cache, tables, prefix, specs):
 
 
 def fa_cache_attention_workspace_bytes(Q, cache: KVCache, tables, prefix=None) -> int:
-    """The workspace that fa_cache_attention needs (what it allocates without one)."""
+    """The workspace that fa_cache_attention needs (what it allocates without one); 0 where
+    the tables hold few positions."""
     specs = []
     nbytes = _attention_dims(Q, cache, tables, prefix, specs)[1]
     _fa._check_all(cache.device, specs)
@@ -217,12 +218,12 @@ def fa_cache_attention(Q, cache: KVCache, tables, lengths, scale: float | None =
         if L is None:
             L = torch.empty((B, Hq, T), dtype=f32, device=device)
         if workspace is None:
-            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
         elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
         code = lib.fa_cache_attention(ref, cache._pools, ctypes.byref(scores), pre, Q.data_ptr(), tables.data_ptr(),
-                                      lengths.data_ptr(), O.data_ptr(), L.data_ptr(), workspace.data_ptr(),
-                                      workspace.nbytes, handle)
+                                      lengths.data_ptr(), O.data_ptr(), L.data_ptr(), _fa._ptr(workspace),
+                                      0 if workspace is None else workspace.nbytes, handle)
     if stream is not None:
         _fa._hand_over(device, (O, L), given)
     _fa._raise(code, "fa_cache_attention")

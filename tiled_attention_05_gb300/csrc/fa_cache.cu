@@ -523,7 +523,7 @@ fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache
   if (S && (!prefix->lengths || (p_cols && !prefix->tables) || !aligned(prefix->tables, 4) || !aligned(prefix->lengths, 4) ||
               !aligned(prefix->starts, 4) || (S > 1 && !prefix->starts)))
     return FA_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < s.total) return FA_ERR_INVALID_ARG;
+  if (s.total && (!workspace || !aligned(workspace, 256) || workspace_bytes < s.total)) return FA_ERR_INVALID_ARG;
   fa::CacheParams p = {};
   p.status = fa::device_status_word();
   if (!p.status) return FA_ERR_CUDA;
@@ -570,6 +570,7 @@ fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t err = cudaSuccess;
   p.joined = S > 0;
+  p.whole = s.whole;
   fa::CacheJoin j = {};
   j.pre = parts_of(s.pre);
   if (s.apart) {
@@ -593,6 +594,7 @@ fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache
   p.max_items = (int)s.list.items;
   err = z.quantised ? fa::launch_cache_attn_e4m3(p, z.d, z.dv, s.list.grid, st)
                     : fa::launch_cache_attn_bf16(p, z.d, z.dv, s.list.grid, st);
+  if (s.whole) return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
   j.p = p;
   j.p.S = S;
   j.own = p.S;

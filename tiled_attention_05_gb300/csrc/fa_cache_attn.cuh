@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
   Cursor& ld = s_load[warp];  // (in shared memory: registers are short)
   if (lane == 0) ld = share.start;
   __syncwarp();
-  int lc = ld.c + warp, lc_end = ld.end(share.end), l_turn = 0;
+  int lc = ld.c + warp, lc_end = ld.end(p, share.end), l_turn = 0;
   auto next_load = [&](int step) {  // to this warp's next chunk (lc >= lc_end: there is none)
     lc += step;
     while (lc >= lc_end) {
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
       if (ld.at >= share.end) return;
       ++l_turn;
       lc = ld.c + ((warp - l_turn) & 3);
-      lc_end = ld.end(share.end);
+      lc_end = ld.end(p, share.end);
     }
   };
   auto page_of = [&]() {  // of the next chunk to load (its 16 keys lie in one)
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
   for (; it.at < share.end; it.next(p), ++turn) {
     const CacheEntry n = it.n;
     const bool is_prefix = it.e < p.S;
-    const int c_end = it.end(share.end);
+    const int c_end = it.end(p, share.end);
 
     // Q of rows lr and lr + 8 of the tile: the lane's pieces (16 channels in e4m3 calls, 8 in
     // bf16 ones)

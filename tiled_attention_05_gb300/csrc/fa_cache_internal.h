@@ -26,6 +26,12 @@ constexpr bool cache_few(long long rows, bool prefixes) { return rows <= 8 && !p
 // A CTA gets this much work at least, in chunks of keys, and an item counts as so many
 // chunks more than it has, for its set-up and the joining of its parts.
 constexpr int kCacheMinChunks = 8, kCacheItem = 8;
+// Where no item can have more chunks than this (and there are no prefixes), a CTA takes its
+// items whole: those that begin in its share.  Then there are no parts, no workspace and
+// no join.  (On the GPU, whole / in parts, us, heads of 128, bf16: 1 sequence of 100, 256, 500
+// keys 5.7 / 7.2, 7.1 / 7.1, 9.7 / 7.4; 64 of 100, 256, 500 10.2 / 12.6, 13.0 / 15.2,
+// 26.1 / 25.4; on the host it is one launch and allocation less, 6 us.)
+constexpr int kCacheWhole = 16;
 // Prefixes of many rows have a list of their own (fa_cache_prefix_kernel), with items of
 // two tiles of 128 rows and chunks of 128 keys.
 constexpr int kPrefixRows = 256, kPrefixKeys = 128, kPrefixMinChunks = 4, kPrefixItem = 2;
@@ -73,6 +79,7 @@ struct CacheParams {
   int chunk_cost;   // of a chunk of own keys; of a prefix's 1024
   int per_sm;       // CTAs of the own keys' kernel on an SM
   int joined;      // whole items too leave their part for the join
+  int whole;       // items are not split (kCacheWhole)
   Divide by_T, by_GT;  // rows of a head, of a sequence
   int max_items;   // that the workspace has slots for
   int capped, min_chunks;
@@ -118,6 +125,7 @@ struct CacheList {
 };
 struct CacheShape {
   bool fits;       // items and chunks can be counted in 32 bits
+  bool whole;      // no item is split: no workspace
   bool apart;      // prefixes are a list of their own (`pre`); else one list holds all
   CacheList list;  // the own keys' (and the prefixes')
   CacheList pre;
@@ -129,6 +137,7 @@ inline CacheShape cache_shape(long long B, long long Hkv, long long rows, int dv
                               long long groups, long long prefix_capacity, int sms) {
   CacheShape s;
   s.apart = prefix_apart(groups, rows * B);
+  s.whole = groups == 0 && capacity <= kCacheWhole * kCacheKeys;
   s.fits = true;
   size_t at = 0;
   auto take = [&at](size_t bytes) {
@@ -159,7 +168,7 @@ inline CacheShape cache_shape(long long B, long long Hkv, long long rows, int dv
         kCacheMinChunks, kCacheItem, ctas);
     s.pre = s.list;
   }
-  s.total = at;
+  s.total = s.whole ? 0 : at;
   return s;
 }
 
@@ -228,7 +237,9 @@ struct CacheCursor {
   int e, h, r, c;
   int item;  // ordinal of the item
   CacheEntry n;
-  FA_WALK int end(int share_end) const { return c + share_end - at < n.chunks ? c + share_end - at : n.chunks; }
+  FA_WALK int end(const CacheParams& p, int share_end) const {
+    return p.whole || c + share_end - at >= n.chunks ? n.chunks : c + share_end - at;
+  }
   FA_WALK void next(const CacheParams& p) {  // the next item's first chunk
     at += n.chunks + ITEM - c;
     c = 0;
@@ -239,7 +250,7 @@ struct CacheCursor {
     h = 0;
     while (++e < p.entries) {
       n = cache_entry<KC>(p, e);
-      if (n.chunks) return;
+      if (n.chunks || p.whole) return;  // (whole: a row that sees nothing is written by its item)
       item += p.Hkv * n.tiles(ROWS);
     }
     at = 0x3fffffff;  // the list's end
@@ -254,7 +265,7 @@ struct CacheCursor {
     h = o / tiles;
     r = o - h * tiles;
     item = first + o;
-    if (c >= n.chunks) next(p);
+    if (p.whole ? c > 0 : c >= n.chunks) next(p);
   }
 };
 
@@ -300,7 +311,7 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
   for (int e = e0; e < e1; ++e) {
     const CacheEntry n = cache_entry<KC>(p, e);
     const int items = p.Hkv * n.tiles(ROWS);
-    if (n.chunks) sum[0] += (long long)items * (n.chunks + ITEM);
+    if (n.chunks || p.whole) sum[0] += (long long)items * (n.chunks + ITEM);
     sum[1] += items;
   }
   const long long mine = sum[0], my_items = sum[1];
@@ -344,14 +355,14 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
   s.begin = min(per * (int)blockIdx.x, all);
   s.end = min(s.begin + per, all);
   if (blockIdx.x == 0) {
-    if (threadIdx.x == 0) p.parts.head[p.entries].work = per;
+    if (threadIdx.x == 0 && !p.whole) p.parts.head[p.entries].work = per;
     bool bad = !room;
     int w = (int)base, i = (int)item;
 #pragma unroll 1
     for (int e = e0; e < e1; ++e) {
       const CacheEntry n = cache_entry<KC>(p, e);
       const int own = p.Hkv * n.tiles(ROWS);
-      p.parts.head[e] = {w, i, room ? n.chunks : 0};
+      if (!p.whole) p.parts.head[e] = {w, i, room ? n.chunks : 0};
       if (n.chunks) w += own * (n.chunks + ITEM);
       i += own;
       if (e < p.S) {  // (the runs are in order and disjoint)
@@ -372,7 +383,7 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
     for (;; ++e) {
       const CacheEntry n = cache_entry<KC>(p, e);
       const int own = p.Hkv * n.tiles(ROWS);
-      const int all = n.chunks ? own * (n.chunks + ITEM) : 0;
+      const int all = n.chunks || p.whole ? own * (n.chunks + ITEM) : 0;
       if (s.begin < w + all) break;
       w += all;
       i += own;

@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int c0, c1;
   };
   auto item_of = [&](const Cursor& it) {
-    return Item{it.c, it.end(share.end)};
+    return Item{it.c, it.end(p, share.end)};
   };
   // Whether tile B has rows of its own.  Where it has none, it takes the same rows as tile A, A
   // the item's even key tiles and B its odd ones; both leave a part.
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Cursor* const walk = &s_walk[8];
         *walk = share.start;
         while (ok && walk->at < share.end) {
-          const int tiles = walk->end(share.end) - walk->c;
+          const int tiles = walk->end(p, share.end) - walk->c;
           const bool two = two_tiles(*walk);
           // tile X's first key tile, and the distance of its next one
           const int step = two ? 1 : 2, first_b = two ? 0 : 1;
