@@ -299,8 +299,9 @@ FA_API fa_status fa_cache_read(const fa_cache_dims* dims, const fa_kv_cache* cac
  * scores as for fa_scores (distances and window count over prefix and own keys
  * together); scale <= 0 selects 1/sqrt(d).  With a cache of e4m3, weights are rounded to
  * fp16 and values are taken to be below 2^60 in magnitude; values at masked places
- * may be anything.  With bf16 weights are rounded to bf16, and values that one of a
- * sequence's rows sees have to be finite for its other rows too.
+ * may be anything.  With bf16 the weights of a prefix's keys are rounded to bf16 (where it
+ * goes through the tensor cores: many rows), and values that one of a sequence's rows sees
+ * have to be finite for its other rows too.
  *
  * workspace: fa_cache_attention_workspace_bytes (it asks the current device for its
  * SMs; 0 where the tables hold few positions), 256-byte aligned, contents ignored. */

@@ -33,8 +33,8 @@
 // the exponent, t = score + log2(v_scale), and the softmax's reference follows the
 // maximum of t: the weights w = 2^(t - m) that meet the codes in fp16 (rounded to 11 bits)
 // are at most 2^8 whatever the scales' sizes are, and the sum takes w / v_scale in fp32.
-// bf16 caches: w is rounded to bf16, half a step being 2^-8 of a weight, as in the
-// unmodified forward; the sum takes it unrounded.
+// bf16 caches: w is the sum of two bf16 (16 bits of it; the second product takes no time
+// that HBM leaves).
 #pragma once
 #include <cstdint>
 
@@ -448,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
         }
       }
       uint32_t w[RT][2];  // P^T: keys 2 li, 2 li + 1 (+ 8) of row lr
+      [[maybe_unused]] uint32_t rest[RT][2];  // (bf16) what their rounding left
 #pragma unroll
       for (int u = 0; u < RT; ++u) {
         float e[4];
@@ -457,13 +458,21 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
           e[x] = ex2(t[u][x] - (ref == -INFINITY ? 0.f : ref));
           l[2 * u + (x & 1)] += Q8 ? e[x] * inv[x >> 1] : e[x];
         }
-        w[u][0] = turned(pack2<Q8>(e[0], e[1]));
-        w[u][1] = turned(pack2<Q8>(e[2], e[3]));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t pair = pack2<Q8>(e[2 * j], e[2 * j + 1]);
+          if constexpr (!Q8)
+            rest[u][j] = turned(pack_bf16x2(e[2 * j] - __uint_as_float(pair << 16), e[2 * j + 1] - __uint_as_float(pair & 0xffff0000u)));
+          w[u][j] = turned(pair);
+        }
       }
       // O^T += V^T P^T: this lane's value rows 2 li, 2 li + 1, 8 + 2 li, 9 + 2 li
       auto mma_o = [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-        for (int u = 0; u < RT; ++u) mma16<Q8>(o[u][k], a0, a1, a2, a3, w[u][0], w[u][1]);
+        for (int u = 0; u < RT; ++u) {
+          mma16<Q8>(o[u][k], a0, a1, a2, a3, w[u][0], w[u][1]);
+          if constexpr (!Q8) mma16<Q8>(o[u][k], a0, a1, a2, a3, rest[u][0], rest[u][1]);
+        }
       };
       // four channels of four rows
       auto four = [&](int k, uint32_t r0, uint32_t r1, uint32_t r8, uint32_t r9) {
