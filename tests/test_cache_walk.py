@@ -26,7 +26,7 @@ using namespace fa;
 #define CHECK(x) do { if (!(x)) { std::printf("failed: %s (call %d)\n", #x, call); std::exit(1); } } while (0)
 
 // ROWS 16: own keys and prefixes in one list; 256: the prefixes' own list
-int wholes = 0;
+int wholes = 0, bundles = 0;
 template <int KC, int ROWS>
 void follow(int call, std::mt19937& rng) {
   constexpr bool PRE = ROWS == kPrefixRows;
@@ -43,7 +43,7 @@ void follow(int call, std::mt19937& rng) {
   if (!PRE && p.S && prefix_apart(p.S, (long long)p.G * p.T * p.B)) p.S = 0;
   p.p_cols = in(0, 30);
   p.window = in(0, 2) ? 0 : in(1, 400);
-  const int sms = in(1, 8);
+  const int sms = in(1, call % 2 ? 8 : 60);
   std::vector<int> lengths(p.B), plens(p.S + 1), starts(p.S + 1);
   for (int& n : lengths) n = in(-3, (p.cols << p.page_log2) + 5);
   for (int& n : plens) n = in(-3, (p.p_cols << p.page_log2) + 5);
@@ -67,40 +67,46 @@ void follow(int call, std::mt19937& rng) {
   if (all.whole) CHECK(all.total == 0 && p.S == 0);
   else CHECK(fits(all.list, all.apart ? p.B : p.S + p.B, kCacheRows, all.apart ? all.pre.head : all.total));
   if (all.apart) CHECK(fits(all.pre, p.S, kPrefixRows, all.total));
-  // the entries' places, as CTA 0 writes them
+  // the entries' places, as CTA 0 writes them (in bundles of tiles)
+  const int bundle = PRE ? cache_bundle(p.S, cache_prefix<kPrefixKeys>(p, 0).tiles(kPrefixRows), shape.grid) : 1;
+  bundles += bundle > 1;
   std::vector<CacheHead> head(entries);
   long long total = 0, chunks = 0;
   int items = 0;
   for (int e = 0; e < entries; ++e) {
     const CacheEntry n = cache_entry<KC>(p, e);
     head[e] = {(int)total, items, n.chunks};
-    if (n.chunks || p.whole) total += (long long)p.Hkv * n.tiles(ROWS) * (n.chunks + kItem);
-    chunks += (long long)p.Hkv * n.tiles(ROWS) * n.chunks;
-    items += p.Hkv * n.tiles(ROWS);
+    if (n.chunks || p.whole) total += (long long)p.Hkv * (n.tiles(ROWS) / bundle) * (n.chunks + kItem);
+    chunks += (long long)p.Hkv * (n.tiles(ROWS) / bundle) * n.chunks;
+    items += p.Hkv * (n.tiles(ROWS) / bundle);
   }
   CHECK(all.fits && items <= shape.items);
-  long long per = (total + shape.grid - 1) / shape.grid;
+  const int ctas = shape.grid / bundle;
+  long long per = (total + ctas - 1) / ctas;
   if (per < kMin) per = kMin;
-  CHECK(per * shape.grid >= total);
+  CHECK(per * ctas >= total);
   std::set<std::tuple<int, int, int, int>> seen;
   std::map<long long, std::pair<int, int>> slots;  // slot -> item, CTA
   std::set<int> items_seen;
-  for (int cta = 0; cta < shape.grid; ++cta) {
+  for (int cta = 0; cta < ctas; ++cta) {
     const long long begin = cta * per, end = begin + per < total ? begin + per : total;
     if (begin >= end) break;
     using Cursor = CacheCursor<KC, ROWS, kItem>;
     int e = 0;
-    while (!((head[e].chunks || p.whole) && begin < head[e].work + (long long)p.Hkv * cache_entry<KC>(p, e).tiles(ROWS) * (head[e].chunks + kItem))) ++e;
+    while (!((head[e].chunks || p.whole) && begin < head[e].work + (long long)p.Hkv * (cache_entry<KC>(p, e).tiles(ROWS) / bundle) * (head[e].chunks + kItem))) ++e;
     Cursor it;
-    it.start(p, e, head[e].item, (int)begin, (int)(begin - head[e].work));
+    it.start(p, bundle, e, head[e].item, (int)begin, (int)(begin - head[e].work));
     for (; it.at < end; it.next(p)) {
       const int c_end = it.end(p, (int)end);
       CHECK(p.whole ? it.c == 0 && c_end == it.n.chunks : it.c < c_end);
       if (p.whole) CHECK(items_seen.insert(it.item).second);
-      CHECK(it.item == head[it.e].item + it.h * it.n.tiles(ROWS) + it.r);
-      CHECK(it.at == head[it.e].work + (it.h * it.n.tiles(ROWS) + it.r) * (it.n.chunks + kItem) + it.c);
-      CHECK(it.item + cta < shape.slots);
-      CHECK(slots.emplace((long long)it.item + cta, std::make_pair(it.item, cta)).second);
+      CHECK(it.item == head[it.e].item + it.h * it.tiles() + it.r);
+      CHECK(it.at == head[it.e].work + (it.h * it.tiles() + it.r) * (it.n.chunks + kItem) + it.c);
+      for (int tile = 0; tile < bundle; ++tile) {
+        const long long slot = ((long long)it.item + cta) * bundle + tile;
+        CHECK(slot < shape.slots);
+        CHECK(slots.emplace(slot, std::make_pair(it.item * bundle + tile, cta)).second);
+      }
       for (int c = it.c; c < c_end; ++c) {
         CHECK(seen.insert({it.e, it.h, it.r, c}).second);
         const int key = (it.n.chunk0 + c) * KC;
@@ -111,7 +117,7 @@ void follow(int call, std::mt19937& rng) {
     if (!PRE)
       for (int warp = 0; warp < kWarps; ++warp) {
         Cursor ld;
-        ld.start(p, e, head[e].item, (int)begin, (int)(begin - head[e].work));
+        ld.start(p, bundle, e, head[e].item, (int)begin, (int)(begin - head[e].work));
         if (ld.at >= end) break;
         Cursor use = ld;
         int lc = ld.c + warp, lc_end = ld.end(p, (int)end), turn = 0;
@@ -144,17 +150,19 @@ void follow(int call, std::mt19937& rng) {
     const CacheEntry n = cache_entry<KC>(p, e);
     for (int h = 0; h < p.Hkv; ++h)
       for (int row = 0; row < n.rows; ++row) {
-        const CacheSlots l = cache_slots(head[e], n.rows, ROWS, kItem, h, row, (int)per);
+        const CacheSlots l = cache_slots(head[e], n.rows, ROWS, kItem, bundle, h, row, (int)per);
         CHECK((l.n > 0) == (n.chunks > 0) && l.row == row % ROWS);
         for (int i = 0; i < l.n; ++i) {
-          CHECK(slots.count(l.slot + i));
-          CHECK(slots[l.slot + i].first == head[e].item + h * n.tiles(ROWS) + row / ROWS);
-          if (i) CHECK(slots[l.slot + i].second == slots[l.slot + i - 1].second + 1);
+          const long long at = l.slot + (long long)i * l.step;
+          CHECK(slots.count(at));
+          CHECK(slots[at].first == head[e].item * bundle + h * n.tiles(ROWS) + row / ROWS);
+          if (i) CHECK(slots[at].second == slots[at - l.step].second + 1);
         }
         if (l.n) {  // no part before the first or after the last
           const int item = slots[l.slot].first;
-          CHECK(!slots.count(l.slot - 1) || slots[l.slot - 1].first != item);
-          CHECK(!slots.count(l.slot + l.n) || slots[l.slot + l.n].first != item);
+          const long long after = l.slot + (long long)l.n * l.step, before = l.slot - l.step;
+          CHECK(!slots.count(before) || slots[before].first != item);
+          CHECK(!slots.count(after) || slots[after].first != item);
         }
       }
   }
@@ -174,7 +182,7 @@ int main() {
     follow<kPrefixKeys, kPrefixRows>(call, rng);
   }
   const int call = -1;
-  CHECK(wholes > 10);
+  CHECK(wholes > 10 && bundles > 10);
   std::printf("ok\n");
 }
 """

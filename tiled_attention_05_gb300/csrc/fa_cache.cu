@@ -239,9 +239,10 @@ __global__ void __launch_bounds__(128) fa_cache_join_kernel(const fa::CacheJoin 
   const int own_per = p.parts.head[j.own_entries].work;
   // The group of this sequence, if it has a prefix.
   fa::CacheHead pre_head = {0, 0, 0};
-  int pre_per = 1, first = 0, pre_rows = 0;
+  int pre_per = 1, bundle = 1, first = 0, pre_rows = 0;
   if (p.S) {
     pre_per = j.pre.head[j.pre_entries].work;
+    bundle = j.pre.head[j.pre_entries].item;
     for (int s0 = 0; s0 < p.S; s0 += 32) {
       const int s = s0 + lane;
       int a = 0, z = 0;
@@ -260,11 +261,11 @@ __global__ void __launch_bounds__(128) fa_cache_join_kernel(const fa::CacheJoin 
       }
     }
   }
-  const CacheSlots own = fa::cache_slots(own_head, p.G * p.T, kCacheRows, fa::kCacheItem, h, g * p.T + t, own_per);
+  const CacheSlots own = fa::cache_slots(own_head, p.G * p.T, kCacheRows, fa::kCacheItem, 1, h, g * p.T + t, own_per);
   if (!p.S && own.n == 1) return;  // a whole item, stored by its CTA
   const int pre_row = (b - first) * p.G * p.T + g * p.T + t;
   const CacheSlots pre =
-      fa::cache_slots(pre_head, pre_rows, j.pre_rows, j.pre_rows == kCacheRows ? fa::kCacheItem : fa::kPrefixItem, h, pre_row, pre_per);
+      fa::cache_slots(pre_head, pre_rows, j.pre_rows, j.pre_rows == kCacheRows ? fa::kCacheItem : fa::kPrefixItem, bundle, h, pre_row, pre_per);
   // A prefix's item of at most 128 rows leaves two parts, 128 rows apart.
   const int halves = j.pre_rows == fa::kPrefixRows && pre_rows - (pre_row - pre.row) <= fa::kPrefixRows / 2 ? 1 : 0;
   const int pre_n = pre.n << halves, n = own.n + pre_n;
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(128) fa_cache_join_kernel(const fa::CacheJoin 
       for (int x = 0; x < CH; ++x) v[k][x] = 0.f;
       if (i >= n) continue;
       const bool is_pre = i < pre_n;
-      const long long row = is_pre ? (pre.slot + (i >> halves)) * j.pre_rows + pre.row + (i & halves) * 128
+      const long long row = is_pre ? (pre.slot + (i >> halves) * pre.step) * j.pre_rows + pre.row + (i & halves) * 128
                                    : (own.slot + i - pre_n) * kCacheRows + own.row;
       ml[k] = reinterpret_cast<const float2*>(is_pre ? j.pre.ml : p.parts.ml)[row];
       const float* o = (is_pre ? j.pre.part : p.parts.part) + row * DV + lane * CH;

@@ -56,7 +56,7 @@ struct Divide {
 };
 // Parts of items (of `rows` rows each) that a join adds up.
 struct CacheParts {
-  CacheHead* head;  // [entries + 1]; the last one's work: a CTA's share
+  CacheHead* head;  // [entries + 1]; the last one's work: a CTA's share; its item: the bundle
   float *ml, *part; // [slots][rows][2]: reference and sum; [slots][rows][dv]: unnormalised O
 };
 
@@ -86,6 +86,12 @@ struct CacheParams {
   float scale_log2;
   CapParams cap;
 };
+// A prefix of several tiles of rows, the only one of a call, is walked by so many CTAs side
+// by side, each with a tile of its own: they meet the same keys at about the same time, and
+// HBM gives them once (walked one after the other, 1024 rows over 32768 keys of bf16 read
+// 402 MB where there are 134).  1: each CTA walks all of an entry's tiles.
+FA_WALK int cache_bundle(int groups, int tiles, int ctas) { return groups == 1 && tiles > 1 && tiles <= ctas ? tiles : 1; }
+
 // What the join adds to the own keys' parts: those of the prefixes.
 struct CacheJoin {
   CacheParams p;       // p.S = 0: no prefixes; parts: of the own keys
@@ -119,7 +125,7 @@ constexpr int cache_chunk_cost(int d, int dv, bool quantised) {
 inline bool prefix_apart(long long groups, long long rows) { return groups > 0 && rows > kCacheRows * groups; }
 
 // Slots of the workspace and CTAs of a call, from what the host knows.  A part's slot is
-// its item's ordinal + its CTA's: walking through the list, each next part raises one of
+// its item's ordinal + its CTA's (both of bundles, times the bundle, + the tile): walking through the list, each next part raises one of
 // the two, so that no two parts share one.
 struct CacheList {
   long long items, slots;  // at most
@@ -238,8 +244,10 @@ template <int KC, int ROWS, int ITEM>
 struct CacheCursor {
   int at;  // in the whole list
   int e, h, r, c;
-  int item;  // ordinal of the item
+  int item;  // ordinal of the item (of a bundle's)
+  int bundle;
   CacheEntry n;
+  FA_WALK int tiles() const { return n.tiles(ROWS) / bundle; }
   FA_WALK int end(const CacheParams& p, int share_end) const {
     return p.whole || c + share_end - at >= n.chunks ? n.chunks : c + share_end - at;
   }
@@ -247,26 +255,27 @@ struct CacheCursor {
     at += n.chunks + ITEM - c;
     c = 0;
     ++item;
-    if (++r < n.tiles(ROWS)) return;
+    if (++r < tiles()) return;
     r = 0;
     if (++h < p.Hkv) return;
     h = 0;
     while (++e < p.entries) {
       n = cache_entry<KC>(p, e);
       if (n.chunks || p.whole) return;  // (whole: a row that sees nothing is written by its item)
-      item += p.Hkv * n.tiles(ROWS);
+      item += p.Hkv * tiles();
     }
     at = 0x3fffffff;  // the list's end
   }
   // To the share's start `in` units into entry e's items, the first of which is `first`.
-  FA_WALK void start(const CacheParams& p, int entry, int first, int begin, int in) {
+  FA_WALK void start(const CacheParams& p, int side_by_side, int entry, int first, int begin, int in) {
+    bundle = side_by_side;
     e = entry;
     n = cache_entry<KC>(p, e);
-    const int o = in / (n.chunks + ITEM), tiles = n.tiles(ROWS);
+    const int o = in / (n.chunks + ITEM);
     at = begin;
     c = in - o * (n.chunks + ITEM);
-    h = o / tiles;
-    r = o - h * tiles;
+    h = o / tiles();
+    r = o - h * tiles();
     item = first + o;
     if (p.whole ? c > 0 : c >= n.chunks) next(p);
   }
@@ -275,15 +284,15 @@ struct CacheCursor {
 // Where the join finds the parts of row `row` of an entry's kv head h: `n` slots from
 // `slot` on (`per`: a CTA's share).
 struct CacheSlots {
-  long long slot;
-  int n, row;  // parts, row within the tile
+  long long slot;    // of the first part; the next ones are `step` apart
+  int n, row, step;  // parts, row within the tile
 };
-FA_WALK CacheSlots cache_slots(const CacheHead& e, int rows, int item_rows, int item_work, int h, int row, int per) {
-  CacheSlots l = {0, 0, row % item_rows};
+FA_WALK CacheSlots cache_slots(const CacheHead& e, int rows, int item_rows, int item_work, int bundle, int h, int row, int per) {
+  CacheSlots l = {0, 0, row % item_rows, bundle};
   if (e.chunks == 0) return l;
-  const int o = h * ((rows + item_rows - 1) / item_rows) + row / item_rows;
+  const int tile = row / item_rows, o = h * ((rows + item_rows - 1) / item_rows / bundle) + tile / bundle;
   const int at = e.work + o * (e.chunks + item_work), c0 = at / per, c1 = (at + e.chunks - 1) / per;
-  l.slot = (long long)e.item + o + c0;
+  l.slot = ((long long)e.item + o + c0) * bundle + tile % bundle;
   l.n = c1 - c0 + 1;
   return l;
 }
@@ -298,6 +307,7 @@ __device__ __forceinline__ void cache_bad(int* status) { atomicCAS(status, 0, fa
 template <class Cursor>
 struct CacheShare {
   int begin, end;
+  int cta, tile;  // place among the bundles, tile within its own
   Cursor start;
 };
 
@@ -307,18 +317,21 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
   __shared__ long long s_sum[WARPS][3];
   __shared__ int s_found[3];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr bool PRE = ROWS == kPrefixRows;
+  // CTAs side by side (see cache_bundle); the other list's kernel has to know, too
+  const int pre_tiles = (PRE || p.sms) && p.groups == 1 ? cache_prefix<kPrefixKeys>(p, 0).tiles(kPrefixRows) : 1;
+  const int pre_bundle = cache_bundle(p.groups, pre_tiles, PRE ? (int)gridDim.x : p.sms), bundle = PRE ? pre_bundle : 1;
   const int each = (p.entries + THREADS - 1) / THREADS;
   const int e0 = min((int)threadIdx.x * each, p.entries), e1 = min(e0 + each, p.entries);
   long long sum[2] = {0, 0};  // work and items of this thread's entries
 #pragma unroll 1
   for (int e = e0; e < e1; ++e) {
     const CacheEntry n = cache_entry<KC>(p, e);
-    const int items = p.Hkv * n.tiles(ROWS);
+    const int items = p.Hkv * (n.tiles(ROWS) / bundle);
     if (n.chunks || p.whole) sum[0] += (long long)items * (n.chunks + ITEM);
     sum[1] += items;
   }
   const long long mine = sum[0], my_items = sum[1];
-  constexpr bool PRE = ROWS == kPrefixRows;
   long long other = 0;  // work of the list that runs beside this one
   if (p.sms) {
 #pragma unroll 1
@@ -350,21 +363,24 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
   const int all = room ? (int)total : 0;
   unsigned ctas = gridDim.x;
   if (p.sms) {  // as many SMs as its part of the cost, one at least (the CTAs from there on have nothing)
-    const float pre = 1024.f * (float)(PRE ? total : other), own = (float)p.chunk_cost * (float)(PRE ? other : total);
-    const int on_pre = own > 0.f ? min(max((int)((float)p.sms * pre / (pre + own) + 0.5f), 1), p.sms - 1) : p.sms;
-    ctas = min(ctas, (unsigned)(PRE ? on_pre : max(p.sms - on_pre, 1) * p.per_sm));
+    const float pre = 1024.f * (float)(PRE ? total * bundle : other), own = (float)p.chunk_cost * (float)(PRE ? other : total);
+    int on_pre = own > 0.f ? min(max((int)((float)p.sms * pre / (pre + own) + 0.5f), 1), p.sms - 1) : p.sms;
+    on_pre = max(on_pre - on_pre % pre_bundle, min(pre_bundle, p.sms));  // whole bundles, one at least
+    ctas = min(ctas / bundle, (unsigned)(PRE ? on_pre / bundle : max(p.sms - on_pre, 1) * p.per_sm));
   }
   const int per = max((int)(((unsigned)all + ctas - 1) / ctas), p.min_chunks);
-  s.begin = min(per * (int)blockIdx.x, all);
+  s.tile = (int)blockIdx.x % bundle;
+  s.cta = (int)blockIdx.x / bundle;
+  s.begin = min(per * s.cta, all);
   s.end = min(s.begin + per, all);
   if (blockIdx.x == 0) {
-    if (threadIdx.x == 0 && !p.whole) p.parts.head[p.entries].work = per;
+    if (threadIdx.x == 0 && !p.whole) p.parts.head[p.entries].work = per, p.parts.head[p.entries].item = bundle;
     bool bad = !room;
     int w = (int)base, i = (int)item;
 #pragma unroll 1
     for (int e = e0; e < e1; ++e) {
       const CacheEntry n = cache_entry<KC>(p, e);
-      const int own = p.Hkv * n.tiles(ROWS);
+      const int own = p.Hkv * (n.tiles(ROWS) / bundle);
       if (!p.whole) p.parts.head[e] = {w, i, room ? n.chunks : 0};
       if (n.chunks) w += own * (n.chunks + ITEM);
       i += own;
@@ -385,7 +401,7 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
 #pragma unroll 1
     for (;; ++e) {
       const CacheEntry n = cache_entry<KC>(p, e);
-      const int own = p.Hkv * n.tiles(ROWS);
+      const int own = p.Hkv * (n.tiles(ROWS) / bundle);
       const int all = n.chunks || p.whole ? own * (n.chunks + ITEM) : 0;
       if (s.begin < w + all) break;
       w += all;
@@ -395,7 +411,7 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
   }
   __syncthreads();
   if (s.begin >= s.end) return s;
-  s.start.start(p, s_found[0], s_found[2], s.begin, s.begin - s_found[1]);
+  s.start.start(p, bundle, s_found[0], s_found[2], s.begin, s.begin - s_found[1]);
   return s;
 }
 

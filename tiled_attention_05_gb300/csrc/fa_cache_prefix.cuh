@@ -59,6 +59,31 @@ struct PrefixCfg {
   static_assert(NS >= 3 && SMEM <= (226 << 10), "shared memory");
 };
 
+// mbar_wait with a suspend-time hint: a thread that finds the phase incomplete sleeps until it
+// completes (or the hint runs out), mostly in the first try.
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > 2000000000ull) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
 // Instruction descriptor, kind::f16 with fp32 D; A and B fp16 or bf16.
 __host__ __device__ constexpr uint32_t idesc(bool f16, int M, int N, int b_mn) {
   return f16 ? idesc_bf16(M, N, 0, b_mn) & ~((1u << 7) | (1u << 10)) : idesc_bf16(M, N, 0, b_mn);
@@ -170,7 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // Whether tile B has rows of its own.  Where it has none, it takes the same rows as tile A, A
   // the item's even key tiles and B its odd ones; both leave a part.
-  auto two_tiles = [](const Cursor& it) { return it.n.rows > it.r * fa::kPrefixRows + BM; };
+  auto first_row = [&](const Cursor& it) { return (it.r * it.bundle + share.tile) * fa::kPrefixRows; };
+  auto two_tiles = [&](const Cursor& it) { return it.n.rows > first_row(it) + BM; };
 
   if (warp < 4) {
     setmaxnreg_dec<kRegsLow>();
@@ -179,60 +205,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && run) {
         constexpr uint32_t idS = idesc(Q8, BM, BN, 0), idPV = idesc(Q8, BM, DV, 1);
         const uint32_t q_buf = smem_u32(smem), slots = smem_u32(smem + C::OFF_SLOT);
-        int u = 0;  // ring position of the item's first K (K_j at u + 2 j, V_j after it)
-        int nq[2] = {0, 0}, np[2] = {0, 0};
+        // Slots and phases of the next K and the next V to read: every other unit of the ring.
+        int sk = 0, sv = 1;
+        uint32_t pk = 0, pv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+        auto pass = [](int& s, uint32_t& phase) {
+          s += 2;
+          if (s >= NS) s -= NS, phase ^= 1;
+        };
+        const uint64_t q_desc = desc_kmajor(q_buf), k_desc = desc_kmajor(slots), v_desc = desc_mnmajor(slots, BN * 128);
         bool ok = true;
+        // S_X of the next K; `first`: of the item, whose Q has to be there; `wait`: the K is not
+        // known to be there yet; `last`: this tile is the last to read it.
+        auto issue_s = [&](int x, bool first, bool wait, bool last) -> bool {
+          if (first) {
+            if (!wait_for(&q_full[x], nq[x], abort_flag)) return false;
+            nq[x] ^= 1;
+          }
+          if (wait && !wait_for(&full[sk], pk, abort_flag)) return false;
+          tc_fence_after();
+          const uint64_t a0 = desc_at(q_desc, x * C::Q_BYTES), b0 = desc_at(k_desc, sk * C::SLOT);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * (BM * 128) + (k & 3) * 32;
+            mma_ss(tmem + x * 128, desc_at(a0, off), desc_at(b0, off), idS, k > 0 ? 1u : 0u);
+          }
+          mma_commit(&s_full[x]);
+          if (last) {
+            mma_commit(&empty[sk]);
+            pass(sk, pk);
+          }
+          return true;
+        };
+        auto issue_pv = [&](int x, bool first, bool wait, bool last) -> bool {
+          if (!wait_for(&p_full[x], np[x], abort_flag)) return false;
+          np[x] ^= 1;
+          if (wait && !wait_for(&full[sv], pv, abort_flag)) return false;
+          tc_fence_after();
+          const uint64_t v0 = desc_at(v_desc, sv * C::SLOT);
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            mma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, desc_at(v0, k * 2048), idPV, !first || k > 0 ? 1u : 0u);
+          if (last) {
+            mma_commit(&empty[sv]);
+            pass(sv, pv);
+          }
+          return true;
+        };
         Cursor* const walk = &s_walk[8];
         *walk = share.start;
         while (ok && walk->at < share.end) {
           const int tiles = walk->end(p, share.end) - walk->c;
           const bool two = two_tiles(*walk);
-          // tile X's first key tile, and the distance of its next one
+          // tile B's first key tile, and the distance of a tile's next one
           const int step = two ? 1 : 2, first_b = two ? 0 : 1;
-          auto issue_s = [&](int x, int j) -> bool {
-            if (j == (x ? first_b : 0)) {
-              if (!mbar_wait(&q_full[x], nq[x] & 1, abort_flag)) return false;
-              ++nq[x];
-            }
-            const int pos = u + 2 * j, s = pos % NS;
-            if ((x == 0 || !two) && !mbar_wait(&full[s], (pos / NS) & 1, abort_flag)) return false;
-            tc_fence_after();
-            const uint64_t a0 = desc_kmajor(q_buf + x * C::Q_BYTES), b0 = desc_kmajor(slots + s * C::SLOT);
+          ok = issue_s(0, true, true, !two) && (first_b >= tiles || issue_s(1, true, !two, true));
+          for (int j0 = 0; ok && j0 < tiles; j0 += step) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k >> 2) * (BM * 128) + (k & 3) * 32;
-              mma_ss(tmem + x * 128, desc_at(a0, off), desc_at(b0, off), idS, k > 0 ? 1u : 0u);
-            }
-            mma_commit(&s_full[x]);
-            if (x == 1 || !two) mma_commit(&empty[s]);
-            return true;
-          };
-          auto issue_pv = [&](int x, int j) -> bool {
-            const int pos = u + 2 * j + 1, s = pos % NS;
-            if (!mbar_wait(&p_full[x], np[x] & 1, abort_flag)) return false;
-            ++np[x];
-            if ((x == 0 || !two) && !mbar_wait(&full[s], (pos / NS) & 1, abort_flag)) return false;
-            tc_fence_after();
-            const uint64_t v0 = desc_mnmajor(slots + s * C::SLOT, BN * 128);
-#pragma unroll
-            for (int k = 0; k < BN / 16; ++k)
-              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, desc_at(v0, k * 2048), idPV, (j >= step || k > 0) ? 1u : 0u);
-            if (x == 1 || !two) mma_commit(&empty[s]);
-            return true;
-          };
-          ok = issue_s(0, 0) && (first_b >= tiles || issue_s(1, first_b));
-          for (int j0 = 0; ok && j0 < tiles; j0 += step)
-            for (int x = 0; ok && x < 2; ++x) {
+            for (int x = 0; x < 2; ++x) {
               const int j = x ? j0 + first_b : j0;
-              if (j >= tiles) break;
-              ok = issue_pv(x, j);
+              if (j >= tiles || !ok) break;
+              const bool wait = x == 0 || !two, last = x == 1 || !two;
+              ok = issue_pv(x, j0 == 0, wait, last);
               if (!ok) break;
               if (j + step < tiles)
-                ok = issue_s(x, j + step);
+                ok = issue_s(x, false, wait, last);
               else
                 mma_commit(&o_done[x]);
             }
-          u += 2 * tiles;
+          }
           walk->next(p);
         }
         // Let every MMA issued above finish before TMEM is released.
@@ -298,13 +338,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           fetch_id();
           while (ok && more) {
             const int s = ld.u % NS, valid = ld.it.n.keys - (ld.it.n.chunk0 + ld.c) * BN;
-            if (!__all_sync(~0u, mbar_wait(&empty[s], ((ld.u / NS) & 1) ^ 1, abort_flag))) break;
+            if (!__all_sync(~0u, wait_for(&empty[s], ((ld.u / NS) & 1) ^ 1, abort_flag))) break;
             // Rows past the prefix's end: whatever the pages hold there meets a score that is
             // masked, and as a value a weight of 0, for which it has to be finite.
             const bool tail = ld.v && valid < BN;
             copy(tail ? raw_full : &full[s], slots + s * C::SLOT);
             if (tail) {
-              ok = __all_sync(~0u, mbar_wait(raw_full, tails++ & 1, abort_flag));
+              ok = __all_sync(~0u, wait_for(raw_full, tails++ & 1, abort_flag));
               for (int k = lane; k < (BN - valid) * (DV / 8); k += 32) {
                 const int row = valid + k / (DV / 8), chunk = k % (DV / 8);
                 st_shared_v4(smem_u32(slots + s * C::SLOT) + (chunk >> 3) * (BN * 128) + sw128_offset(row, chunk & 7), 0, 0, 0, 0);
@@ -347,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto issue = [&]() {  // (warp 1) the next unit's codes into their raw buffer
           if (warp != 1 || !more_ld || !ok) return;
           const int s = ld.u % NR;
-          if (!__all_sync(~0u, mbar_wait(&raw_empty[s], ((ld.u / NR) & 1) ^ 1, abort_flag))) {
+          if (!__all_sync(~0u, wait_for(&raw_empty[s], ((ld.u / NR) & 1) ^ 1, abort_flag))) {
             ok = false;
             return;
           }
@@ -362,8 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && more) {
           issue();
           const int s = now.u % NS, rs = now.u % NR, valid = min(now.it.n.keys - (now.it.n.chunk0 + now.c) * BN, BN);
-          const bool both = mbar_wait(&raw_full[rs], (now.u / NR) & 1, abort_flag) &&
-                            mbar_wait(&empty[s], ((now.u / NS) & 1) ^ 1, abort_flag);
+          const bool both = wait_for(&raw_full[rs], (now.u / NR) & 1, abort_flag) &&
+                            wait_for(&empty[s], ((now.u / NS) & 1) ^ 1, abort_flag);
           if (!__all_sync(~0u, both)) break;
           const uint8_t* src = smem + C::OFF_RAW + rs * C::RAW;
           const uint32_t dst = smem_u32(slots + s * C::SLOT);
@@ -404,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item m = item_of(it);
         const int step = two ? 1 : 2, c0 = two ? m.c0 : m.c0 + x;  // this tile's key tiles: every step-th from c0 on
         const int tiles = (m.c1 - c0 + step - 1) / step;
-        const int row = it.r * fa::kPrefixRows + (two ? x * BM : 0) + r;
+        const int row = first_row(it) + (two ? x * BM : 0) + r;
         const fa::CacheRow w = fa::cache_row(p, it.n, row);
         const int head = it.h * p.G + w.g;
         float unit = MODS && p.capped ? 1.f : p.scale_log2;
@@ -483,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sc = to;
             if (j + 1 < tiles) fetch_scales(c0 + (j + 1) * step);
           }
-          ok = mbar_wait(&s_full[x], ns & 1, abort_flag);
+          ok = wait_for(&s_full[x], ns & 1, abort_flag);
           ok = agree(ok);
           if (!ok) break;
           ++ns;
@@ -639,11 +679,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&p_full[x]);
           lim -= step * BN;
         }
-        if (ok && tiles > 0) ok = agree(mbar_wait(&o_done[x], no++ & 1, abort_flag));
+        if (ok && tiles > 0) ok = agree(wait_for(&o_done[x], no++ & 1, abort_flag));
         if (ok) {
           tc_fence_after();
           const bool some = s_row[threadIdx.x - 128] != 0, none = s_row[threadIdx.x - 128] == 2 || tiles <= 0;
-          const long long at = ((long long)walk->item + blockIdx.x) * fa::kPrefixRows + x * BM + r;
+          const long long at = (((long long)walk->item + share.cta) * walk->bundle + share.tile) * fa::kPrefixRows + x * BM + r;
           if (some) *reinterpret_cast<float2*>(p.parts.ml + at * 2) = none ? make_float2(NEG_INF, 0.f) : make_float2(m_ref, l);
           // 32 columns at a time through this warp's share of Q_X, which is free now, so that a
           // row's 128 bytes leave together.
