@@ -55,6 +55,9 @@ struct PrefixCfg {
   static constexpr int OFF_SCALES = OFF_RAW + NRAW * RAW;
   static constexpr int OFF_BAR = OFF_SCALES + SCALES;
   static constexpr int SMEM = OFF_BAR + 512;
+  // The softmax looks for V_j and K_{j+1} on the MMA thread's behalf (142 us of 256 rows x 4 over
+  // 32768 keys, 151 without), unless slots are few: then it would wait for a K that is late.
+  static constexpr bool VOUCHED = NS > 4;
   // (V_j leaves its slot after S_A(j + 1): K_{j+1} needs another one)
   static_assert(NS >= 3 && SMEM <= (226 << 10), "shared memory");
 };
@@ -214,8 +217,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const uint64_t q_desc = desc_kmajor(q_buf), k_desc = desc_kmajor(slots), v_desc = desc_mnmajor(slots, BN * 128);
         bool ok = true;
-        // S_X of the next K; `first`: of the item, whose Q has to be there; `wait`: the K is not
-        // known to be there yet; `last`: this tile is the last to read it.
+        // S_X of the next K; `first`: of the item, whose Q has to be there; `wait`: nobody has
+        // looked for the K (or V); `last`: this tile is the last to read it.  Every check of a
+        // barrier costs the tensor pipe a round trip (see VOUCHED).
         auto issue_s = [&](int x, bool first, bool wait, bool last) -> bool {
           if (first) {
             if (!wait_for(&q_full[x], nq[x], abort_flag)) return false;
@@ -264,11 +268,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 2; ++x) {
               const int j = x ? j0 + first_b : j0;
               if (j >= tiles || !ok) break;
-              const bool wait = x == 0 || !two, last = x == 1 || !two;
-              ok = issue_pv(x, j0 == 0, wait, last);
+              const bool mine = x == 0 || !two, last = x == 1 || !two;
+              ok = issue_pv(x, j0 == 0, !C::VOUCHED && mine, last);
               if (!ok) break;
               if (j + step < tiles)
-                ok = issue_s(x, false, wait, last);
+                ok = issue_s(x, false, C::VOUCHED ? !two : mine, last);
               else
                 mma_commit(&o_done[x]);
             }
@@ -428,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + x * 128 + lane_base, tO = tmem + 256 + x * 128 + lane_base;
     const float NEG_INF = -__int_as_float(0x7f800000);
     int ns = 0, no = 0, nb = 0;  // phases waited for; scale buffers written
+    int units = 0;               // ring position of the item's first K
     bool ok = run;
     // Loads from TMEM are a warp's, and the barrier that hands the scales round is the
     // tile's: those who meet there leave together when one of them gave up.
@@ -528,6 +533,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           ++ns;
           tc_fence_after();
+          // V_j and K_{j+1}, on behalf of the MMA thread: tile A looks for both.  (Not for a K where
+          // the tiles have key tiles of their own: the next one may need the slot of V_j, which
+          // this tile's P has to free first.)
+          bool there = true;
+          if (C::VOUCHED && r == 0 && (x == 0 || step == 2)) {
+            const int at = units + 2 * ((step == 2 ? x : 0) + j * step);
+            there = wait_for(&full[(at + 1) % NS], ((at + 1) / NS) & 1, abort_flag) &&
+                    (step == 2 || j + 1 >= tiles || wait_for(&full[(at + 2) % NS], ((at + 2) / NS) & 1, abort_flag));
+          }
+          __syncwarp();
           float mt = NEG_INF, m_new, base, sum;
           bool rescale, warp_rescale;
           auto refer = [&]() {  // the reference of this tile's weights, from its maximum
@@ -676,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_ref = m_new;
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(&p_full[x]);
+          if (there) mbar_arrive(&p_full[x]);
           lim -= step * BN;
         }
         if (ok && tiles > 0) ok = agree(wait_for(&o_done[x], no++ & 1, abort_flag));
@@ -714,6 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();  // (the next item's first P.V into O_X follows this warpgroup's next P)
         }
       }
+      units += 2 * (walk->end(p, share.end) - walk->c);
       __syncwarp();
       if (lane == 0) walk->next(p);
       __syncwarp();
