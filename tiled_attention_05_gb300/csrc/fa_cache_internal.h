@@ -112,13 +112,13 @@ cudaError_t launch_cache_join(const CacheJoin& j, int dv, cudaStream_t stream);
 // Keys of a chunk, the unit of the walk: what one warp holds in one stage of its ring.
 constexpr int kCacheKeys = 16;
 
-// What an SM takes for a chunk of own keys (its bytes at ~100 a ns) over a prefix's two tiles
+// What an SM takes for a chunk of own keys (its bytes at ~90 a ns) over a prefix's two tiles
 // of 128 keys (1.5 us at heads of 128; in e4m3, where the softmax reads three values a key from
-// shared memory, 10% more), in 1024ths.  (64 answers to 8192 tokens, e4m3, at 80, 100, 110, 130,
-// 170 a ns: 47, 44, 40, 43, 49 us; 256 to 32768, bf16, at 60, 80, 100, 130: 192, 175, 172, 200.)
+// shared memory, 20% more), in 1024ths.  (64 answers to 8192 tokens, e4m3, at 80, 100, 110, 130,
+// 170 a ns: 47, 44, 40, 43, 49 us; 256 to 32768, bf16, at 70, 80, 90, 100: 166, 164, 165, 177.)
 constexpr int cache_chunk_cost(int d, int dv, bool quantised) {
   return quantised ? kCacheKeys * (d + dv + 8) * 1024 / (110 * 1500) * 256 / (d + dv)
-                   : kCacheKeys * 2 * 256 * 1024 / (100 * 1500);
+                   : kCacheKeys * 2 * 256 * 1024 / (90 * 1500);
 }
 // Whether the prefixes go through the kernel that takes 128 rows at a time (`rows`: those
 // of all sequences' kv heads).

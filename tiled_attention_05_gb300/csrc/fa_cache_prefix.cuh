@@ -21,7 +21,9 @@
 // multiplies the score, the value's goes into the exponent.  (Codes could feed the fp8
 // pipe as they are, but then the weights would be e4m3 too: a sum of two has a weight's
 // 8 bits, and ends at 2^-18 of the largest, which a long flat tail falls below.)
-// MODS: cap, slopes and window.
+// MODS: kLines, slopes or a window (bf16), or kCapped, a cap, with or without these.  (With the cap
+// in the registers' form too, its code for each four columns made a prefix with slopes alone
+// take 70 us for 39.)
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -37,6 +39,7 @@ using fa::CacheParams;
 
 constexpr int kThreads = 384, kLoaders = 96;  // (three warps of them load)
 constexpr int BM = 128, BN = fa::kPrefixKeys;
+enum : int { kUnmodified = 0, kLines = 1, kCapped = 2 };
 // Register split, as in the forward: 88 + 2 * 208 = 3 * 168.
 constexpr int kRegsLaunch = 168, kRegsLow = 88, kRegsHigh = 208;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: weights stay <= 256
@@ -134,7 +137,7 @@ __device__ __forceinline__ void cap_quad_of(const fa::CapParams& c, uint64_t& a,
   b = f2_mul(b, tb);
 }
 
-template <int D, int DV, bool Q8, bool MODS>
+template <int D, int DV, bool Q8, int MODS>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_cache_prefix_kernel(const CacheParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = PrefixCfg<D, DV, Q8>;
@@ -551,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             warp_rescale = __any_sync(~0u, rescale);
             base = m_new == NEG_INF ? 0.f : m_new;
           };
-          if constexpr (Q8 || MODS) {
+          if constexpr (Q8 || MODS == kCapped) {
             // Two passes of 32 columns at a time: the scores in log2 units, back into TMEM, and
             // their maximum; then the weights.  (With the row in registers the code is four
             // times as long, and short calls run it cold.)
@@ -639,11 +642,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
             tmem_wait_ld();
-            if (lim < BN) {
+            // Of the columns only those from `from` on and before `lim` count.
+            const int from = MODS && p.window ? pos + lim - p.window + 1 : 0;
+            const bool some_hidden = __any_sync(~0u, from > 0 || lim < BN);
+            auto hide = [&](uint32_t with) {
 #pragma unroll
               for (int c = 0; c < BN; ++c)
-                if (c >= lim) sr[c] = __float_as_uint(NEG_INF);
+                if (c < from || c >= lim) sr[c] = with;
+            };
+            if constexpr (MODS) {
+              const uint64_t unit2 = f2_pack(unit, unit), nslope2 = f2_pack(-slope, -slope);
+              const uint64_t far2 = f2_pack((float)(pos + lim), (float)(pos + lim));  // of column 0
+#pragma unroll
+              for (int c = 0; c < BN; c += 4) {
+                uint64_t a = f2_mul(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), unit2);
+                uint64_t b = f2_mul(f2_pack(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), unit2);
+                a = f2_fma(nslope2, f2_add(far2, f2_pack((float)-c, (float)(-c - 1))), a);
+                b = f2_fma(nslope2, f2_add(far2, f2_pack((float)(-c - 2), (float)(-c - 3))), b);
+                sr[c] = __float_as_uint(f2_lo(a)), sr[c + 1] = __float_as_uint(f2_hi(a));
+                sr[c + 2] = __float_as_uint(f2_lo(b)), sr[c + 3] = __float_as_uint(f2_hi(b));
+              }
             }
+            if (some_hidden) hide(__float_as_uint(NEG_INF));
+            const float sl = MODS ? 1.f : unit;  // what brings sr to log2 units
             float pm[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) pm[k] = __uint_as_float(sr[k]);
@@ -653,9 +674,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 0; k < 8; ++k) pm[k] = fmax3(pm[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
 #pragma unroll
             for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], __uint_as_float(sr[BN - 8 + k]));
-            mt = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * unit;
+            mt = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * sl;
             refer();
-            const uint64_t unit2 = f2_pack(unit, unit), nbase2 = f2_pack(-base, -base);
+            const uint64_t sl2 = f2_pack(sl, sl), nbase2 = f2_pack(-base, -base);
             uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
             for (int c = 0; c < BN / 32; ++c) {
@@ -663,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const uint64_t xv = f2_fma(
-                    f2_pack(__uint_as_float(sr[32 * c + 2 * e]), __uint_as_float(sr[32 * c + 2 * e + 1])), unit2, nbase2);
+                    f2_pack(__uint_as_float(sr[32 * c + 2 * e]), __uint_as_float(sr[32 * c + 2 * e + 1])), sl2, nbase2);
                 const float e0 = ex2(f2_lo(xv)), e1 = ex2(f2_hi(xv));
                 rs[e & 3] = f2_add(rs[e & 3], f2_pack(e0, e1));
                 pk[e] = pack_bf16x2(e0, e1);
@@ -744,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && *abort_flag) atomicExch(p.status, DEV_TIMEOUT);
 }
 
-template <int D, int DV, bool Q8, bool MODS>
+template <int D, int DV, bool Q8, int MODS>
 cudaError_t launch_mods(const CacheParams& p, int grid, cudaStream_t stream) {
   using C = PrefixCfg<D, DV, Q8>;
   auto kernel = fa_cache_prefix_kernel<D, DV, Q8, MODS>;
@@ -767,8 +788,9 @@ cudaError_t launch_mods(const CacheParams& p, int grid, cudaStream_t stream) {
 
 template <int D, int DV, bool Q8>
 cudaError_t launch_dims(const CacheParams& p, int grid, cudaStream_t stream) {
-  return p.capped || p.slopes || p.window ? launch_mods<D, DV, Q8, true>(p, grid, stream)
-                                          : launch_mods<D, DV, Q8, false>(p, grid, stream);
+  const bool lines = p.slopes || p.window;
+  if (p.capped || (Q8 && lines)) return launch_mods<D, DV, Q8, kCapped>(p, grid, stream);
+  return lines ? launch_mods<D, DV, Q8, Q8 ? kCapped : kLines>(p, grid, stream) : launch_mods<D, DV, Q8, kUnmodified>(p, grid, stream);
 }
 
 template <bool Q8>
