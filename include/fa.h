@@ -262,7 +262,7 @@ typedef struct {
   int T;           /* write: new tokens a sequence; read: positions; attention: query rows */
   int d, dv;       /* each 64 or 128 */
   int pages, page; /* pages of the pool, positions of a page */
-  int table_pages; /* columns of tables; table_pages * page <= 2^30 */
+  int table_pages; /* columns of tables; table_pages * page <= 2^30 (and B * Hkv * T, B * Hq * T) */
   int quantised;   /* 0: bf16, 1: e4m3 and scales */
 } fa_cache_dims;
 typedef struct {
@@ -297,7 +297,7 @@ FA_API fa_status fa_cache_read(const fa_cache_dims* dims, const fa_kv_cache* cac
  * then stand behind them.  A prefix's keys are read once for all its sequences.
  *
  * scores as for fa_scores (distances and window count over prefix and own keys
- * together); scale <= 0 selects 1/sqrt(d).  With a cache of e4m3, weights are rounded to
+ * together; with slopes the tables hold at most 2^24 positions); scale <= 0 selects 1/sqrt(d).  With a cache of e4m3, weights are rounded to
  * fp16 and values are taken to be below 2^60 in magnitude; values at masked places
  * may be anything.  With bf16 the weights of a prefix's keys are rounded to bf16 (where it
  * goes through the tensor cores: many rows), and values that one of a sequence's rows sees
