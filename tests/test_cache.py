@@ -410,6 +410,25 @@ def test_nan_reaches_the_rows_that_see_it(quant):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("mods", [dict(), dict(softcap=5.0), dict(window=3)])
+def test_nan_value_of_a_hidden_key(mods):
+    """In e4m3 a value that a row does not see may be anything, its scale NaN too."""
+    s = Setup([300, 17], 2, 64, 128, True, 16)
+    K = torch.ones(2, 2, 1, 64, device="cuda").to(bf)
+    V = torch.full((2, 2, 1, 128), math.nan, device="cuda").to(bf)
+    fa.fa_cache_write(s.cache, K, V, s.tables, s.lengths - 1)
+    Q = query(s, 4, 5)
+    O, L = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, **mods)
+    assert torch.isnan(O[:, :, 4]).all() and torch.isnan(L[:, :, 4]).all()
+    assert torch.isfinite(O[:, :, :4]).all() and torch.isfinite(L[:, :, :4]).all()
+    # hidden by a window: from the rows after it
+    more = torch.ones(2, 2, 4, 64, device="cuda").to(bf), torch.ones(2, 2, 4, 128, device="cuda").to(bf)
+    fa.fa_cache_write(s.cache, *more, s.tables, s.lengths)
+    O, L = fa.fa_cache_attention(Q[:, :, :2].contiguous(), s.cache, s.tables, s.lengths + 4, window=4)
+    assert torch.isnan(O[:, :, 0]).all() and torch.isfinite(O[:, :, 1]).all() and torch.isfinite(L[:, :, 1]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("quant", [False, True])
 def test_workspace_and_results_of_the_caller(quant):
     s = Setup([500, 40, 3], 2, 128, 64, quant, 16, [100], None)

@@ -413,6 +413,12 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
           for (int x = y & 1; x < 4; x += 2) t[y >> 1][x] -= row.slope * (float)(row.at - (key0 + lr + 8 * (x >> 1)));
         }
       }
+      if constexpr (Q8) {  // before the mask: a hidden value's scale may be NaN
+#pragma unroll
+        for (int u = 0; u < RT; ++u)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) t[u][x] += lv[x >> 1];
+      }
       if (key0 + KC > all_to || key0 < all_from) {
 #pragma unroll
         for (int y = 0; y < 2 * RT; ++y) {
@@ -428,10 +434,7 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
 #pragma unroll
       for (int u = 0; u < RT; ++u)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if constexpr (Q8) t[u][x] += lv[x >> 1];
-          grown = grown || t[u][x] > m[2 * u + (x & 1)] + kGrown;  // (-inf + 8: the first keys)
-        }
+        for (int x = 0; x < 4; ++x) grown = grown || t[u][x] > m[2 * u + (x & 1)] + kGrown;  // (-inf + 8: the first keys)
       if (__any_sync(~0u, grown)) {
 #pragma unroll
         for (int y = 0; y < 2 * RT; ++y) {
