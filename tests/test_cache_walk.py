@@ -182,6 +182,22 @@ int main() {
     follow<kPrefixKeys, kPrefixRows>(call, rng);
   }
   const int call = -1;
+  // shares of lists of any size, for fewer CTAs than the grid has, too
+  for (int k = 0; k < 3000; ++k) {
+    const int all = k < 50 ? k : (int)(rng() % (1u << (10 + k % 21))), grid = 1 + (int)(rng() % 600), least = 1 + k % 8;
+    const unsigned ctas = 1 + rng() % (unsigned)(k % 3 ? grid : k % 5 + 1);
+    long long at = 0, size = 0;
+    for (int cta = 0; cta < (grid > (int)ctas ? grid : (int)ctas); ++cta) {
+      int begin, end;
+      const int per = cache_cut(all, ctas, least, cta, &begin, &end);
+      CHECK(begin == at && begin <= end && end <= all && end - begin <= per && per >= least);
+      CHECK(end == all || end - begin == per);
+      CHECK(cta == 0 || per == size);
+      at = end;
+      size = per;
+    }
+    CHECK(at == all);
+  }
   CHECK(wholes > 10 && bundles > 10);
   std::printf("ok\n");
 }

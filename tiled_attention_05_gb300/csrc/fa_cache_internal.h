@@ -297,6 +297,16 @@ FA_WALK CacheSlots cache_slots(const CacheHead& e, int rows, int item_rows, int 
   return l;
 }
 
+// CTA `cta`'s share of a list of `all` (below 2^30) cut for `ctas`; those from there on have
+// nothing (their number times the share may pass 32 bits).  Returns the share's size.
+FA_WALK int cache_cut(int all, unsigned ctas, int min_chunks, int cta, int* begin, int* end) {
+  const int even = (int)(((unsigned)all + ctas - 1) / ctas), per = even > min_chunks ? even : min_chunks;
+  const bool some = (unsigned)cta < ctas && (unsigned)per * (unsigned)cta < (unsigned)all;
+  *begin = some ? per * cta : all;
+  *end = all - *begin > per ? *begin + per : all;
+  return per;
+}
+
 #ifdef __CUDACC__
 // An index that does not fit: the device status word says so (a timeout stays).
 __device__ __forceinline__ void cache_bad(int* status) { atomicCAS(status, 0, fa_ptx::DEV_BAD_TABLE); }
@@ -368,11 +378,9 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
     on_pre = max(on_pre - on_pre % pre_bundle, min(pre_bundle, p.sms));  // whole bundles, one at least
     ctas = min(ctas / bundle, (unsigned)(PRE ? on_pre / bundle : max(p.sms - on_pre, 1) * p.per_sm));
   }
-  const int per = max((int)(((unsigned)all + ctas - 1) / ctas), p.min_chunks);
   s.tile = (int)blockIdx.x % bundle;
   s.cta = (int)blockIdx.x / bundle;
-  s.begin = min(per * s.cta, all);
-  s.end = min(s.begin + per, all);
+  const int per = cache_cut(all, ctas, p.min_chunks, s.cta, &s.begin, &s.end);
   if (blockIdx.x == 0) {
     if (threadIdx.x == 0 && !p.whole) p.parts.head[p.entries].work = per, p.parts.head[p.entries].item = bundle;
     bool bad = !room;
