@@ -460,6 +460,8 @@ def test_attention_checks_its_operands():
     for bad in (dict(window=-1), dict(softcap=1e9), dict(scale=math.nan)):
         with pytest.raises(fa.FAError):
             call(**bad)
+    with pytest.raises(AttributeError):
+        s.cache.K = s.cache.K.clone()
 
 
 # ---------------------------------------------------------------- write and read (GPU)

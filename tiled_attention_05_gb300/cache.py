@@ -33,7 +33,7 @@ PAGE_SIZES = (16, 32, 64, 128, 256)
 class KVCache:
     """Pools of pages: K [pages, Hkv, page, d] and V [pages, Hkv, page, dv], both bf16 or both
     float8_e4m3fn, the latter with fp32 scales [pages, Hkv, page].  Holds the tensors it is
-    given and copies nothing."""
+    given and copies nothing; another tensor is another cache."""
 
     def __init__(self, K, V, k_scale=None, v_scale=None):
         if K.dim() != 4 or V.dim() != 4 or K.shape[:3] != V.shape[:3]:
@@ -56,6 +56,11 @@ class KVCache:
         self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
         self._sizes = {}  # dims and workspace of the attention calls by their sizes
         self._pools = ctypes.byref(_fa.FaKVCache(K.data_ptr(), V.data_ptr(), _fa._ptr(k_scale), _fa._ptr(v_scale)))
+
+    def __setattr__(self, name, value):
+        if name in ("K", "V", "k_scale", "v_scale") and "_pools" in self.__dict__:
+            raise AttributeError(f"a KVCache keeps the {name} that it was made of")
+        object.__setattr__(self, name, value)
 
     @classmethod
     def empty(cls, pages, Hkv, page, d, dv=None, dtype=torch.bfloat16, device="cuda"):
