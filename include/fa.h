@@ -298,8 +298,8 @@ FA_API fa_status fa_cache_read(const fa_cache_dims* dims, const fa_kv_cache* cac
  *
  * scores as for fa_scores (distances and window count over prefix and own keys
  * together; with slopes the tables hold at most 2^24 positions); scale <= 0 selects 1/sqrt(d).  With a cache of e4m3, weights are rounded to
- * fp16 and values are taken to be below 2^60 in magnitude; values at masked places
- * may be anything.  With bf16 the weights of a prefix's keys are rounded to bf16 (where it
+ * fp16 and values are taken to be below 2^40 in magnitude (beyond, a key whose value is zero may
+ * be lost from L); a row at a masked place may be anything that fa_cache_write leaves.  With bf16 the weights of a prefix's keys are rounded to bf16 (where it
  * goes through the tensor cores: many rows), and values that one of a sequence's rows sees
  * have to be finite for its other rows too.
  *

@@ -4,7 +4,10 @@
 // of the sequences' own keys.
 //
 // An item is (group, kv head, up to 256 rows), two tiles of 128; the list of items times
-// key tiles of 128 is cut into equal shares, one CTA an SM each.  Roles:
+// key tiles of 128 is cut into equal shares, one CTA an SM each.  The chain of S, softmax and
+// P V bounds it, two tiles of rows and 128 keys in ~3300 cycles where the MMAs alone take
+// ~2200.  Measured (32 / 8 heads of 128): 1024 rows over 32768 keys of bf16, on the ~105 SMs that
+// the own keys leave, 145 us; 256 over 8192 in e4m3, 32 us, some 7 of them its start.  Roles:
 //   warp 0       issues the MMAs of both tiles in turn, S_X(j) = Q_X K_j^T and
 //                O_X += P_X(j) V_j, so that the tensor pipe runs one tile's while the
 //                softmax works on the other's (the forward's order: those of one
@@ -16,7 +19,11 @@
 //   warps 4..11  softmax of tile A and of tile B, a thread a row: scores from TMEM, exp2, P
 //                as 16-bit pairs over the scores, O rescaled in TMEM when the maximum grows
 //                by more than 2^8; before that the row of Q into shared memory, after
-//                it the part to the workspace
+//                it the part to the workspace.  bf16: the row's scores in registers.
+//                e4m3 and capped: two passes of 32 columns over TMEM, whose code is a
+//                quarter as long (short calls run it cold)
+//   dual         an item of at most 128 rows: both tiles are its rows, A over the even key tiles
+//                and B over the odd ones, with a part each
 // e4m3: as in fa_cache_attn.cuh, codes and weights meet in fp16, the key's scale
 // multiplies the score, the value's goes into the exponent.  (Codes could feed the fp8
 // pipe as they are, but then the weights would be e4m3 too: a sum of two has a weight's
