@@ -26,11 +26,11 @@ using namespace fa;
 #define CHECK(x) do { if (!(x)) { std::printf("failed: %s (call %d)\n", #x, call); std::exit(1); } } while (0)
 
 // ROWS 16: own keys and prefixes in one list; 256: the prefixes' own list
-int wholes = 0, bundles = 0;
-template <int KC, int ROWS>
+int wholes = 0, bundles = 0, calls[2];
+template <int KC, int ROWS, bool FEW>
 void follow(int call, std::mt19937& rng) {
   constexpr bool PRE = ROWS == kPrefixRows;
-  constexpr int kWarps = PRE ? 1 : 4, kItem = PRE ? kPrefixItem : kCacheItem, kMin = PRE ? kPrefixMinChunks : kCacheMinChunks;
+  constexpr int kWarps = PRE ? 1 : 4, kItem = PRE ? kPrefixItem : cache_item(FEW), kMin = PRE ? kPrefixMinChunks : kCacheMinChunks;
   auto in = [&](int a, int b) { return a + (int)(rng() % (unsigned)(b - a + 1)); };
   CacheParams p = {};
   p.B = in(1, call % 3 ? 6 : 300);
@@ -56,6 +56,8 @@ void follow(int call, std::mt19937& rng) {
   const CacheShape all = cache_shape(p.B, p.Hkv, rows, 64, call % 2, (long long)p.cols << p.page_log2, p.S,
                                        (long long)p.p_cols << p.page_log2, sms);
   if (PRE && !all.apart) return;
+  if (!PRE && cache_few(rows, p.S > 0) != FEW) return;
+  ++calls[FEW];
   p.whole = all.whole;
   wholes += all.whole;
   const CacheList shape = PRE ? all.pre : all.list;
@@ -177,9 +179,10 @@ int main() {
       const int m = n / by * by;  // at a multiple, and before one
       CHECK(Divide::of(by)(m) == m / by && (m == 0 || Divide::of(by)(m - 1) == (m - 1) / by));
     }
-  for (int call = 0; call < 400; ++call) {
-    follow<kCacheKeys, kCacheRows>(call, rng);
-    follow<kPrefixKeys, kPrefixRows>(call, rng);
+  for (int call = 0; call < 600; ++call) {
+    follow<kCacheKeys, kCacheRows, true>(call, rng);
+    follow<kCacheKeys, kCacheRows, false>(call, rng);
+    follow<kPrefixKeys, kPrefixRows, false>(call, rng);
   }
   const int call = -1;
   // shares of lists of any size, for fewer CTAs than the grid has, too
@@ -198,7 +201,7 @@ int main() {
     }
     CHECK(at == all);
   }
-  CHECK(wholes > 10 && bundles > 10);
+  CHECK(wholes > 10 && bundles > 10 && calls[0] > 100 && calls[1] > 100);
   std::printf("ok\n");
 }
 """

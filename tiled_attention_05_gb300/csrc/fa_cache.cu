@@ -261,11 +261,11 @@ __global__ void __launch_bounds__(128) fa_cache_join_kernel(const fa::CacheJoin 
       }
     }
   }
-  const CacheSlots own = fa::cache_slots(own_head, p.G * p.T, kCacheRows, fa::kCacheItem, 1, h, g * p.T + t, own_per);
+  const CacheSlots own = fa::cache_slots(own_head, p.G * p.T, kCacheRows, p.own_item, 1, h, g * p.T + t, own_per);
   if (!p.S && own.n == 1) return;  // a whole item, stored by its CTA
   const int pre_row = (b - first) * p.G * p.T + g * p.T + t;
   const CacheSlots pre =
-      fa::cache_slots(pre_head, pre_rows, j.pre_rows, j.pre_rows == kCacheRows ? fa::kCacheItem : fa::kPrefixItem, bundle, h, pre_row, pre_per);
+      fa::cache_slots(pre_head, pre_rows, j.pre_rows, j.pre_rows == kCacheRows ? p.own_item : fa::kPrefixItem, bundle, h, pre_row, pre_per);
   // A prefix's item of at most 128 rows leaves two parts, 128 rows apart.
   const int halves = j.pre_rows == fa::kPrefixRows && pre_rows - (pre_row - pre.row) <= fa::kPrefixRows / 2 ? 1 : 0;
   const int pre_n = pre.n << halves, n = own.n + pre_n;
@@ -571,6 +571,7 @@ fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t err = cudaSuccess;
   p.joined = S > 0;
+  p.own_item = fa::cache_item(fa::cache_few((long long)p.G * p.T, S > 0 && !s.apart));
   p.whole = s.whole;
   fa::CacheJoin j = {};
   j.pre = parts_of(s.pre);

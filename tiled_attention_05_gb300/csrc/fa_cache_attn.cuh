@@ -5,7 +5,7 @@
 // operations, so HBM bounds it; the kernel's work is to keep enough loads in flight.
 // Measured, 32 / 8 heads of 128, one row each: 4 x 50000 to 65536 keys in bf16, 146 us (6.7 TB/s);
 // 32 x 8192 in e4m3, 91 us (6.1 TB/s; its start of 3 to 4 us is the rest); 4 rows each of
-// 48 x 3 to 7000, capped, 16 / 4 heads, 46 us (3.2 TB/s: items of 1 to 4 us have their
+// 48 x 3 to 7000, capped, 16 / 4 heads, 37 us (3.9 TB/s: items of 1 to 4 us have their
 // starts and ends beside them).
 //
 // Split.  The keys of all items (sequence or shared prefix, kv head, tile of 16 rows)
@@ -184,7 +184,7 @@ constexpr float kGrown = 8.f;
 template <int D, int DV, bool Q8, bool FEW>
 __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_cache_attn_kernel(const CacheParams p) {
   using C = CacheCfg<D, DV, Q8, FEW>;
-  using Cursor = fa::CacheCursor<C::KC, kRows, fa::kCacheItem>;
+  using Cursor = fa::CacheCursor<C::KC, kRows, fa::cache_item(FEW)>;
   constexpr int KC = C::KC, RT = FEW ? 1 : 2, MT = DV / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[fa::kCacheWarps][kRows];
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
   __shared__ Cursor s_load[fa::kCacheWarps];
   // Beside the prefixes' kernel (launched so that it may start with that): what comes before
   // both has completed; the end waits for that one, as the join waits for this one only.
-  const auto share = fa::cache_share<KC, kRows, fa::kCacheItem, kThreads>(p);
+  const auto share = fa::cache_share<KC, kRows, fa::cache_item(FEW), kThreads>(p);
   if (share.begin >= share.end || share.start.at >= share.end) {
     if (blockIdx.x == 0) grid_previous();
     return;

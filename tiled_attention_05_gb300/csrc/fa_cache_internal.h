@@ -24,8 +24,12 @@ constexpr int kCacheWarps = 4;      // warps of a CTA; each walks every fourth c
 constexpr int cache_ctas(bool quantised, bool few) { return quantised ? 3 : 2; }
 constexpr bool cache_few(long long rows, bool prefixes) { return rows <= 8 && !prefixes; }
 // A CTA gets this much work at least, in chunks of keys, and an item counts as so many
-// chunks more than it has, for its set-up and the joining of its parts.
-constexpr int kCacheMinChunks = 8, kCacheItem = 8;
+// chunks more than it has, for its set-up and the joining of its parts: 16 where there are two
+// tiles of 8 rows, which are joined one after the other (4 rows each of 48 sequences, 16 / 4 heads,
+// e4m3, at 8, 12, 16, 24: 50, 46, 41.5, 43 us; 16 / 8 heads of 64, one row each of 128, beside
+// prefixes, at 8, 16, 24: 48.2, 48.5, 54.2).
+constexpr int kCacheMinChunks = 8;
+constexpr int cache_item(bool few) { return few ? 8 : 16; }
 // Where no item can have more chunks than this (and there are no prefixes), a CTA takes its
 // items whole: those that begin in its share.  Then there are no parts, no workspace and
 // no join.  (On the GPU, whole / in parts, us, heads of 128, bf16: 1 sequence of 100, 256, 500
@@ -78,6 +82,7 @@ struct CacheParams {
   int sms, groups;  // groups: S, also for the kernel of the own keys (whose S is 0)
   int chunk_cost;   // of a chunk of own keys; of a prefix's 1024
   int per_sm;       // CTAs of the own keys' kernel on an SM
+  int own_item;    // what an item of the own keys' list counts (cache_item)
   int joined;      // whole items too leave their part for the join
   int whole;       // items are not split (kCacheWhole)
   Divide by_T, by_GT;  // rows of a head, of a sequence
@@ -168,13 +173,14 @@ inline CacheShape cache_shape(long long B, long long Hkv, long long rows, int dv
   const long long kc = kCacheKeys, own_tiles = B * ((rows + kCacheRows - 1) / kCacheRows);
   const long long pre_tiles = groups ? groups + rows * B / (s.apart ? kPrefixRows : kCacheRows) : 0;
   const double own = (double)own_tiles * ((capacity + kc - 1) / kc);
-  const long long ctas = (long long)sms * cache_ctas(quantised, cache_few(rows, groups && !s.apart));
+  const bool few = cache_few(rows, groups && !s.apart);
+  const long long ctas = (long long)sms * cache_ctas(quantised, few);
   if (s.apart) {
-    lay(&s.list, B, own_tiles, own, kCacheRows, kCacheMinChunks, kCacheItem, ctas);
+    lay(&s.list, B, own_tiles, own, kCacheRows, kCacheMinChunks, cache_item(few), ctas);
     lay(&s.pre, groups, pre_tiles, (double)pre_tiles * ((prefix_capacity + kPrefixKeys - 1) / kPrefixKeys), kPrefixRows, kPrefixMinChunks, kPrefixItem, sms);
   } else {
     lay(&s.list, groups + B, own_tiles + pre_tiles, own + (double)pre_tiles * ((prefix_capacity + kc - 1) / kc), kCacheRows,
-        kCacheMinChunks, kCacheItem, ctas);
+        kCacheMinChunks, cache_item(few), ctas);
     s.pre = s.list;
   }
   s.total = s.whole ? 0 : at;
@@ -347,7 +353,7 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
 #pragma unroll 1
     for (int e = threadIdx.x; e < (PRE ? p.B : p.groups); e += THREADS) {
       const CacheEntry n = PRE ? cache_own<kCacheKeys>(p, e) : cache_prefix<kPrefixKeys>(p, e);
-      if (n.chunks) other += (long long)p.Hkv * n.tiles(PRE ? kCacheRows : kPrefixRows) * (n.chunks + (PRE ? kCacheItem : kPrefixItem));
+      if (n.chunks) other += (long long)p.Hkv * n.tiles(PRE ? kCacheRows : kPrefixRows) * (n.chunks + (PRE ? p.own_item : kPrefixItem));
     }
   }
 #pragma unroll 1
