@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int P = D / 8, STEP = 32 / P;  // lanes a row, rows at a time
           const int mine = w.valid ? (w.b * p.Hq + head) * p.T + w.t : -1, piece = lane % P;
           const uint32_t dst = smem_u32(smem) + x * C::Q_BYTES;
-#pragma unroll 4
+#pragma unroll 2
           for (int k = 0; k < 32; k += STEP) {
             const int from = __shfl_sync(~0u, mine, k + lane / P), row = quad * 32 + k + lane / P;
             cp16(dst + (piece >> 3) * (BM * 128) + sw128_offset(row, piece & 7), p.Q + (from < 0 ? 0ll : (long long)from * D + piece * 8),
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (Q8) {  // as fp16, a row's largest value brought to [1, 2); a row a thread
             __syncwarp();
             uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll 2
             for (int k = 0; k < P; ++k) {
               const float4 v = ld_shared_f4(smem + x * C::Q_BYTES + (k >> 3) * (BM * 128) + sw128_offset(r, k & 7));
               const float a[4] = {v.x, v.y, v.z, v.w};
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ex = min(max((int)(top >> 7), 1), 253);
             const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
             unit *= __uint_as_float((uint32_t)ex << 23);
-#pragma unroll 4
+#pragma unroll 2
             for (int k = 0; k < P; ++k) {
               const uint32_t at = (k >> 3) * (BM * 128) + sw128_offset(r, k & 7);
               const float4 v = ld_shared_f4(smem + x * C::Q_BYTES + at);
