@@ -40,7 +40,7 @@ void follow(int call, std::mt19937& rng) {
   p.page_log2 = in(4, 8);
   p.cols = in(0, call % 4 ? 12 : 200);
   p.S = in(PRE, 3);
-  if (!PRE && p.S && prefix_apart(p.S, (long long)p.G * p.T * p.B)) p.S = 0;
+  if (!PRE && p.S && prefix_apart(p.S, (long long)p.G * p.T * p.B, call % 2, 64)) p.S = 0;
   p.p_cols = in(0, 30);
   p.window = in(0, 2) ? 0 : in(1, 400);
   const int sms = in(1, call % 2 ? 8 : 60);

@@ -13,7 +13,7 @@
 // for each CTA, whatever the lengths are.  A share that begins or ends inside an item
 // leaves that item's part (unnormalised O, its reference and sum, in fp32) in the
 // workspace, and a second kernel joins the parts in their order.  A prefix's rows are those
-// of all its sequences; with more than 16 of them it goes through fa_cache_prefix.cuh.
+// of all its sequences; where they are many it goes through fa_cache_prefix.cuh.
 //
 // Warps.  Each of the CTA's four takes every fourth chunk of the share, through a ring
 // of its own in shared memory (cp.async, no barrier between warps), and carries its own

@@ -126,8 +126,15 @@ constexpr int cache_chunk_cost(int d, int dv, bool quantised) {
                    : kCacheKeys * 2 * 256 * 1024 / (90 * 1500);
 }
 // Whether the prefixes go through the kernel that takes 128 rows at a time (`rows`: those
-// of all sequences' kv heads).
-inline bool prefix_apart(long long groups, long long rows) { return groups > 0 && rows > kCacheRows * groups; }
+// of all sequences' kv heads): from so many rows a group on, as the decode kernel reads a
+// prefix's keys, out of L2, once for each 16 rows, and spends as many instructions on a key
+// of 64 channels as on one of 128, and e4m3 costs the other kernel a conversion.  (Decode kernel / apart, us,
+// at that number of rows: bf16, heads of 128, 32 rows a group: 8 groups of 4000 keys 40 / 42, one of 40000 53 / 60;
+// 48 rows: 4 of 4000 50 / 46; heads of 64, 32 rows, slopes, 8 of 2001 51 / 48.  e4m3, 32 rows: one of 40000 46 / 81;
+// 64 rows: 4 of 4000 51 / 53, 8 of 2001 with heads of 64 67 / 81; 96: 8 of 2000 81 / 71.)
+inline bool prefix_apart(long long groups, long long rows, bool quantised, int dv) {
+  return groups > 0 && rows > (quantised ? 64 : dv == 64 ? 16 : 32) * groups;
+}
 
 // Slots of the workspace and CTAs of a call, from what the host knows.  A part's slot is
 // its item's ordinal + its CTA's (both of bundles, times the bundle, + the tile): walking through the list, each next part raises one of
@@ -150,7 +157,7 @@ struct CacheShape {
 inline CacheShape cache_shape(long long B, long long Hkv, long long rows, int dv, bool quantised, long long capacity,
                               long long groups, long long prefix_capacity, int sms) {
   CacheShape s;
-  s.apart = prefix_apart(groups, rows * B);
+  s.apart = prefix_apart(groups, rows * B, quantised, dv);
   s.whole = groups == 0 && capacity <= kCacheWhole * kCacheKeys;
   s.fits = true;
   size_t at = 0;
