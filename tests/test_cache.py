@@ -343,6 +343,20 @@ def test_shared_prefix_modified(mods, quant, heads):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("mods", [dict(softcap=30.0), dict(softcap=2.0), dict(slopes=True), dict(window=40), dict(window=1),
+                                  dict(window=250, softcap=20.0, slopes=True)])
+@pytest.mark.parametrize("T, d, dv", [(1, 128, 128), (3, 64, 64), (2, 128, 64)])
+def test_shared_prefix_of_few_rows_modified(T, d, dv, mods, quant):
+    s = Setup([30, 2, 0, 77, 20], 2, d, dv, quant, 64, [700, 90, 5], [0, 2, 3, 5])
+    Q, mods = query(s, 8, T, std=1.5), dict(mods)
+    if mods.get("slopes"):
+        mods["slopes"] = slopes_of(8)
+    O, L = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, **mods)
+    check(s, Q, O, L, **mods)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("quant", [False, True])
 def test_nan_of_a_prefix(quant):
     """A NaN key or value of a prefix reaches the rows that see it, in whatever place of a tile
     it stands, and none that a window hides it from (values in bf16 have to be finite)."""
