@@ -118,8 +118,8 @@ cudaError_t launch_cache_join(const CacheJoin& j, int dv, cudaStream_t stream);
 constexpr int kCacheKeys = 16;
 
 // What an SM takes for a chunk of own keys (its bytes at ~90 a ns) over a prefix's two tiles
-// of 128 keys (1.5 us at heads of 128; in e4m3, where the softmax reads three values a key from
-// shared memory, 20% more), in 1024ths.  (64 answers to 8192 tokens, e4m3, at 80, 100, 110, 130,
+// of 128 keys (1.5 us at heads of 128; in e4m3 they take longer, and the own keys' rate that
+// divides best is higher), in 1024ths.  (64 answers to 8192 tokens, e4m3, at 80, 100, 110, 130,
 // 170 a ns: 47, 44, 40, 43, 49 us; 256 to 32768, bf16, at 70, 80, 90, 100: 166, 164, 165, 177.)
 constexpr int cache_chunk_cost(int d, int dv, bool quantised) {
   return quantised ? kCacheKeys * (d + dv + 8) * 1024 / (110 * 1500) * 256 / (d + dv)

@@ -4,10 +4,12 @@
 // of the sequences' own keys.
 //
 // An item is (group, kv head, up to 256 rows), two tiles of 128; the list of items times
-// key tiles of 128 is cut into equal shares, one CTA an SM each.  The chain of S, softmax and
-// P V bounds it, two tiles of rows and 128 keys in ~3300 cycles where the MMAs alone take
-// ~2200.  Measured (32 / 8 heads of 128): 1024 rows over 32768 keys of bf16, on the ~105 SMs that
-// the own keys leave, 145 us; 256 over 8192 in e4m3, 32 us, some 7 of them its start.  Roles:
+// key tiles of 128 is cut into equal shares, one CTA an SM each.  Two tiles of rows and 128
+// keys take ~3300 cycles, where the MMAs alone take ~2200: the MMA thread bounds it (an MMA
+// takes it some 70 cycles, a commit 150).  In e4m3 they take ~5400: the chain of a tile's softmax
+// (2400) and of its turn on the MMA thread.  Measured (32 / 8 heads of 128): 1024 rows over 32768
+// keys of bf16, on the ~105 SMs that the own keys leave, 147 us; 256 over 8192 in e4m3, 33 us,
+// some 10 of them until the first scores.  Roles:
 //   warp 0       issues the MMAs of both tiles in turn, S_X(j) = Q_X K_j^T and
 //                O_X += P_X(j) V_j, so that the tensor pipe runs one tile's while the
 //                softmax works on the other's (the forward's order: those of one
