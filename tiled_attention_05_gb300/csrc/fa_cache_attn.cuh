@@ -578,8 +578,8 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
       for (int y = 0; y < 2; ++y) {
         const int to = row_of(2 * u + y).out;
         if (to == -1) continue;
-        const bool none = to < 0;  // a padding row
-        if (none) sum[y] = 0.f;
+        const bool none = to < 0;  // a padding row: its part is none, whatever it scored a prefix's keys
+        if (none) top[y] = -INFINITY, sum[y] = 0.f;
         const float g = none || (whole && sum[y] == 0.f) ? 0.f : whole ? 1.f / sum[y] : 1.f;
 #pragma unroll
         for (int k = 0; k < PER; ++k) c[y][k] = g == 0.f ? 0.f : c[y][k] * g;
