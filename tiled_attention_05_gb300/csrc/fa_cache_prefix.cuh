@@ -534,8 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* to = reinterpret_cast<float*>(smem + C::OFF_SCALES) + (x * 2 + (nb & 1)) * 3 * BN;
             ++nb;
             const float a = lg2(fmaxf(vs, 0x1p-69f));  // (see fa_cache_attn.cuh)
-            to[r] = ks;
-            to[BN + r] = vs == vs ? a : vs;
+            // A key's scale of NaN comes in with the value's, behind the cap and before the mask: the
+            // cap would give it to the other keys of its four, hidden or not.
+            const bool fine = fabsf(ks) < INFINITY;
+            to[r] = fine ? ks : 0.f;
+            to[BN + r] = fine && vs == vs ? a : __int_as_float(0x7fffffff);
             to[2 * BN + r] = ex2(-a);
             sc = to;
             if (j + 1 < tiles) fetch_scales(c0 + (j + 1) * step);
