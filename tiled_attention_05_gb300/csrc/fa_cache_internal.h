@@ -222,19 +222,50 @@ FA_WALK void cache_group(const CacheParams& p, int s, int* first, int* end) {
   if (*first < 0 || *end > p.B || *first > *end) *first = *end = 0;
 }
 
+// The least position among the own keys that a row has which sees anything, of sequence b and of
+// sequences [first, end), group s; 2^31 - 1 where there is none.  With a window the first key
+// of the prefix that any row sees hangs on it.
+FA_WALK int cache_least_of(const CacheParams& p, int b) {
+  const int n = cache_length(p, b);
+  return n <= 0 ? 0x7fffffff : n > p.T ? n - p.T : 0;
+}
+#ifdef __CUDACC__
+// A CTA works it out once for the first groups (cache_share); for those behind them whoever asks does.
+constexpr int kCacheLeast = 32;
+__device__ __forceinline__ int* cache_leasts() {
+  __shared__ int least[kCacheLeast];
+  return least;
+}
+#endif
+FA_WALK int cache_least(const CacheParams& p, int s, int first, int end) {
+#ifdef __CUDACC__
+  if (s < kCacheLeast) return cache_leasts()[s];
+#endif
+  int least = 0x7fffffff;
+#pragma unroll 1
+  for (int b = first; b < end; ++b) {
+    const int at = cache_least_of(p, b);
+    least = at < least ? at : least;
+  }
+  return least;
+}
+
 FA_WALK void cache_span(CacheEntry* n, int first_key, int KC) {
   n->chunk0 = first_key > 0 ? first_key / KC : 0;
-  n->chunks = n->rows > 0 ? (n->keys + KC - 1) / KC - n->chunk0 : 0;
-  if (n->chunks < 0) n->chunks = 0;
+  n->chunks = n->rows > 0 && first_key < n->keys ? (n->keys + KC - 1) / KC - n->chunk0 : 0;
 }
 template <int KC>
 FA_WALK CacheEntry cache_prefix(const CacheParams& p, int s) {
   CacheEntry n;
-  int end;
+  int end, first_key = 0;
   cache_group(p, s, &n.first, &end);
   n.rows = (end - n.first) * p.G * p.T;
   n.keys = cache_clamp(cache_ld(p.p_lengths + s), p.p_cols << p.page_log2);
-  cache_span(&n, p.window ? n.keys - p.window + 1 : 0, KC);  // (the first row of all stands behind the prefix)
+  if (p.window) {
+    const int least = cache_least(p, s, n.first, end);
+    first_key = least == 0x7fffffff ? n.keys : n.keys - p.window + 1 + least;  // (both lengths are 2^30 at most)
+  }
+  cache_span(&n, first_key, KC);
   return n;
 }
 template <int KC>
@@ -341,6 +372,19 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
   __shared__ int s_found[3];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr bool PRE = ROWS == kPrefixRows;
+  const int groups = p.S > p.groups ? p.S : p.groups;
+  if (p.window && groups) {
+#pragma unroll 1
+    for (int s = warp; s < min(groups, kCacheLeast); s += WARPS) {
+      int first, end, least = 0x7fffffff;
+      cache_group(p, s, &first, &end);
+#pragma unroll 1
+      for (int b = first + lane; b < end; b += 32) least = min(least, cache_least_of(p, b));
+      least = __reduce_min_sync(~0u, least);
+      if (lane == 0) cache_leasts()[s] = least;
+    }
+    __syncthreads();
+  }
   // CTAs side by side (see cache_bundle); the other list's kernel has to know, too
   const int pre_tiles = (PRE || p.sms) && p.groups == 1 ? cache_prefix<kPrefixKeys>(p, 0).tiles(kPrefixRows) : 1;
   const int pre_bundle = cache_bundle(p.groups, pre_tiles, PRE ? (int)gridDim.x : p.sms), bundle = PRE ? pre_bundle : 1;

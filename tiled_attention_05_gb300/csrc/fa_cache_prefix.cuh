@@ -66,12 +66,13 @@ struct PrefixCfg {
   static constexpr int OFF_RAW = OFF_SLOT + NS * SLOT;
   static constexpr int OFF_SCALES = OFF_RAW + NRAW * RAW;
   static constexpr int OFF_BAR = OFF_SCALES + SCALES;
-  static constexpr int SMEM = OFF_BAR + 512;
+  static constexpr int OFF_ROW = OFF_BAR + 256;  // (the barriers take 8 (2 NS + 15) + 8 bytes)
+  static constexpr int SMEM = OFF_ROW + 256;
   // The softmax looks for V_j and K_{j+1} on the MMA thread's behalf (142 us of 256 rows x 4 over
   // 32768 keys, 151 without), unless slots are few: then it would wait for a K that is late.
   static constexpr bool VOUCHED = NS > 4;
   // (V_j leaves its slot after S_A(j + 1): K_{j+1} needs another one)
-  static_assert(NS >= 3 && SMEM <= (226 << 10), "shared memory");
+  static_assert(NS >= 3 && NS <= 8 && SMEM <= (226 << 10), "shared memory");
 };
 
 // mbar_wait with a suspend-time hint: a thread that finds the phase incomplete sleeps until it
@@ -154,7 +155,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Cursor s_walk[9];
-  __shared__ uint8_t s_row[256];
   grid_next();  // the own keys' kernel, on the SMs that this one leaves
   const auto share = fa::cache_share<BN, fa::kPrefixRows, fa::kPrefixItem, kThreads>(p);
   if (share.begin >= share.end || share.start.at >= share.end) return;
@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = raw_empty + 3;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint8_t* s_row = smem + C::OFF_ROW;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     *abort_flag = (smem_u32(smem) & 1023u) ? 1 : 0;  // swizzled tiles need 1024 B alignment
