@@ -24,3 +24,45 @@ def test_nan_key_beside_the_first_visible_one(lens, softcap):
     for first in range(201, 209):  # the first key that is seen
         mods = dict(window=400 + 29 - first + 1, softcap=softcap)
         check(s, Q, *fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, **mods), **mods)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("lens", [[1, 2, 3, 17] * 8, [1, 3]])
+@pytest.mark.parametrize("page, window", [(16, 100), (32, 1), (16, 205), (256, 300)])
+def test_pages_before_the_window_may_be_dropped(lens, quant, page, window):
+    """Pages of a prefix that the window hides from every row are no longer the cache's: their
+    places in the table hold -1, and what lay in shared memory before is not taken for them."""
+    s = Setup(lens, 2, 64, 64, quant, page, [700])
+    Q = query(s, 8, 1)
+    other = Setup(lens, 2, 64, 64, quant, page, [700])
+    for x in (other.cache.K, other.cache.V):
+        x.view(torch.uint8).fill_(0x7f)  # NaN in both types
+    dropped = s.p_tables.clone()
+    dropped[:, :(700 - window + 1) // page] = -1  # (a row at its first position sees the furthest)
+    prefix = (dropped, *s.prefix[1:])
+    for mods in (dict(), dict(softcap=20.0, slopes=slopes_of(8))):
+        fa.fa_cache_attention(Q, other.cache, other.tables, other.lengths, prefix=other.prefix)
+        O, L = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=prefix, window=window, **mods)
+        assert fa.fa_last_device_status() == fa.FA_OK
+        check(s, Q, O, L, window=window, **mods)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_a_bad_page_of_a_prefix_is_its_groups_alone(page, quant):
+    s = Setup([30] * 40, 1, 64, 64, quant, page, [700, 690], [0, 20, 40])
+    Q = query(s, 4, 1)
+    want = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix)
+    for bad in (-1, 10 ** 6):
+        tables = s.p_tables.clone()
+        tables[0, 1] = bad
+        for mods in (dict(), dict(window=720)):
+            O, L = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=(tables, *s.prefix[1:]), **mods)
+            assert fa.fa_last_device_status() == fa.FA_ERR_BAD_TABLE
+            if not mods:
+                assert torch.equal(O[20:], want[0][20:]) and torch.equal(L[20:], want[1][20:])
+    again = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+    assert fa.fa_last_device_status() == fa.FA_OK

@@ -113,9 +113,13 @@ def test_the_span_is_what_some_row_sees(tmp_path):
 @pytest.mark.parametrize("quant", [False, True])
 @pytest.mark.parametrize("lens, starts, T, window", [
     ([50, 61], None, 1, 120),                        # the window begins inside the prefix
+    ([50, 61, 77] * 10, None, 1, 120),
+    ([50, 61], None, 3, 120),
     ([150, 161, 300] * 10, None, 1, 120),            # ... and behind it
     ([150, 161, 300], None, 5, 120),
     ([0, 150, 0, 131], None, 2, 100),                # (an empty sequence has no rows that see anything)
+    ([0, 90, 200, 61] * 8, None, 2, 100),
+    ([70, 300, 70, 90, 0, 0] * 8, [0, 1, 2, 4, 6, 20, 33, 48], 1, 100),
     ([30 + 3 * k for k in range(80)], list(range(0, 81, 2)), 1, 100),  # many groups
 ])
 def test_pages_behind_all_rows_may_be_dropped(lens, starts, T, window, quant):

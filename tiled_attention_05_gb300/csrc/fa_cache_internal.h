@@ -207,7 +207,8 @@ struct CacheEntry {
   int first;   // first sequence of the group, or the sequence
   int rows;    // query rows of one kv head
   int keys;    // keys of the entry
-  int chunk0;  // first chunk that any row may see
+  int from;    // first key that any row sees
+  int chunk0;  // its chunk
   int chunks;  // from there on
   FA_WALK int tiles(int item_rows) const { return (rows + item_rows - 1) / item_rows; }
 };
@@ -251,7 +252,8 @@ FA_WALK int cache_least(const CacheParams& p, int s, int first, int end) {
 }
 
 FA_WALK void cache_span(CacheEntry* n, int first_key, int KC) {
-  n->chunk0 = first_key > 0 ? first_key / KC : 0;
+  n->from = first_key > 0 ? first_key : 0;
+  n->chunk0 = n->from / KC;
   n->chunks = n->rows > 0 && first_key < n->keys ? (n->keys + KC - 1) / KC - n->chunk0 : 0;
 }
 template <int KC>

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = q_full + 2;   // [2]
   uint64_t* p_full = s_full + 2;   // [2]
   uint64_t* o_done = p_full + 2;   // [2]
-  uint64_t* raw_full = o_done + 2;    // [3] a raw buffer holds its codes (bf16: [0], a tile's last rows have come)
+  uint64_t* raw_full = o_done + 2;    // [3] a raw buffer holds its codes (bf16: [0], a tile's rows have come, before zeros go to some)
   uint64_t* raw_empty = raw_full + 3;  // [3]
   uint64_t* drain = raw_empty + 3;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -322,20 +322,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       Units ld = {share.start, item_of(share.start), 0, 0, false};
       ld.c = ld.m.c0;
       bool ok = run;
-      // The page of this lane's 16 rows of a tile (-1: none is needed, or it does not fit).
+      // The page of this lane's 16 rows of a tile: -1 if no row of it is needed (it ends before the
+      // first key that is seen, or begins behind the last), -2 if it does not fit.
       int id = 0;
       auto fetch_id = [&]() {
         const int key = (ld.it.n.chunk0 + ld.c) * BN + (lane & 7) * 16;
         id = -1;
-        if (key >= ld.it.n.keys) return;
+        if (key >= ld.it.n.keys || (key | page_mask) < ld.it.n.from) return;
         id = __ldg(p.p_tables + (long long)ld.it.e * p.p_cols + (key >> p.page_log2));
-        if ((unsigned)id >= (unsigned)p.pages) fa::cache_bad(p.status), id = -1;
+        if ((unsigned)id >= (unsigned)p.pages) fa::cache_bad(p.status), id = -2;
       };
       // Copies of unit ld; `bar` gets their bytes.
       auto copy = [&](uint64_t* bar, uint8_t* dst) {
         const int row = (lane & 7) * 16, width = ld.v ? DV : D;
         const bool mine = lane < 8 && row % box == 0 && id >= 0;
         const unsigned all = __ballot_sync(~0u, mine);
+        if constexpr (Q8) {  // codes that a bad page leaves out are 0
+          if (lane < 8 && id == -2) {
+            for (int k = 0; k < width; ++k) st_shared_v4(smem_u32(dst + row * width) + k * 16, 0, 0, 0, 0);
+            fence_async_smem();
+          }
+          __syncwarp();
+        }
         if (lane == 0) mbar_arrive_expect_tx(bar, __popc(all) * box * width * (Q8 ? 1 : 2));
         __syncwarp();
         if (!mine) return;
@@ -350,22 +358,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if constexpr (!Q8) {
         if (warp == 1) {
-          int tails = 0;
+          int zeroed = 0;  // tiles of values, in whose rows zeros are written
           bool more = true;
           fetch_id();
           while (ok && more) {
             const int s = ld.u % NS, valid = ld.it.n.keys - (ld.it.n.chunk0 + ld.c) * BN;
             if (!__all_sync(~0u, wait_for(&empty[s], ((ld.u / NS) & 1) ^ 1, abort_flag))) break;
-            // Rows past the prefix's end: whatever the pages hold there meets a score that is
-            // masked, and as a value a weight of 0, for which it has to be finite.
-            const bool tail = ld.v && valid < BN;
-            copy(tail ? raw_full : &full[s], slots + s * C::SLOT);
-            if (tail) {
-              ok = __all_sync(~0u, wait_for(raw_full, tails++ & 1, abort_flag));
-              for (int k = lane; k < (BN - valid) * (DV / 8); k += 32) {
-                const int row = valid + k / (DV / 8), chunk = k % (DV / 8);
-                st_shared_v4(smem_u32(slots + s * C::SLOT) + (chunk >> 3) * (BN * 128) + sw128_offset(row, chunk & 7), 0, 0, 0, 0);
-              }
+            // Rows past the prefix's end or before the first key that is seen, whatever the pages hold
+            // there, and what a page that was not copied leaves from an earlier tile: as keys they
+            // meet a score that is masked, as values a weight of 0, for which they have to be finite.
+            const int first = ld.it.n.from - (ld.it.n.chunk0 + ld.c) * BN;
+            const unsigned bad = __ballot_sync(~0u, lane < 8 && id == -2);  // blocks of 16 rows
+            const bool some_zero = ld.v && (valid < BN || first > 0 || bad);
+            copy(some_zero ? raw_full : &full[s], slots + s * C::SLOT);
+            if (some_zero) {
+              ok = __all_sync(~0u, wait_for(raw_full, zeroed++ & 1, abort_flag));
+              auto zero = [&](int row0, int row1) {
+                for (int k = lane; k < (row1 - row0) * (DV / 8); k += 32) {
+                  const int row = row0 + k / (DV / 8), chunk = k % (DV / 8);
+                  st_shared_v4(smem_u32(slots + s * C::SLOT) + (chunk >> 3) * (BN * 128) + sw128_offset(row, chunk & 7), 0, 0, 0, 0);
+                }
+              };
+              zero(0, first);
+              zero(valid, BN);
+#pragma unroll 1
+              for (unsigned b = bad; b; b &= b - 1) zero((__ffs(b) - 1) * 16, __ffs(b) * 16);
               fence_async_smem();
               __syncwarp();
               if (lane == 0) mbar_arrive(&full[s]);
@@ -379,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // e4m3: all three warps turn the codes of a raw buffer into fp16, pieces of 16 codes, four at
         // a time (a row has 1 << shift pieces).
-        auto convert = [&](int shift, int valid, const uint8_t* src, uint32_t dst) {
+        auto convert = [&](int shift, int first, int valid, const uint8_t* src, uint32_t dst) {
 #pragma unroll 1
           for (int i0 = tid; i0 < BN << shift; i0 += 4 * kLoaders) {
             uint4 c[4];
@@ -387,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) {
               const int i = i0 + k * kLoaders;
               c[k] = make_uint4(0, 0, 0, 0);
-              if (i < valid << shift) c[k] = reinterpret_cast<const uint4*>(src)[i];
+              if (i >= first << shift && i < valid << shift) c[k] = reinterpret_cast<const uint4*>(src)[i];
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -424,7 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!__all_sync(~0u, both)) break;
           const uint8_t* src = smem + C::OFF_RAW + rs * C::RAW;
           const uint32_t dst = smem_u32(slots + s * C::SLOT);
-          convert((now.v ? DV : D) == 128 ? 3 : 2, valid, src, dst);
+          const int first = max(now.it.n.from - (now.it.n.chunk0 + now.c) * BN, 0);
+          convert((now.v ? DV : D) == 128 ? 3 : 2, first, valid, src, dst);
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -520,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Cursor& it = *walk;
           const int key = (it.n.chunk0 + c) * BN + r;
           ks = 0.f, vs = 1.f;
-          if (key >= it.n.keys) return;
+          if (key >= it.n.keys || key < it.n.from) return;
           const int id = __ldg(p.p_tables + (long long)it.e * p.p_cols + (key >> p.page_log2));
           if ((unsigned)id >= (unsigned)p.pages) return;
           const long long at = (((long long)id * p.Hkv + it.h) << p.page_log2) | (key & page_mask);
