@@ -256,14 +256,16 @@ FA_WALK void cache_span(CacheEntry* n, int first_key, int KC) {
   n->chunk0 = n->from / KC;
   n->chunks = n->rows > 0 && first_key < n->keys ? (n->keys + KC - 1) / KC - n->chunk0 : 0;
 }
-template <int KC>
+// WINDOW (here and below): the call may have one.  (Code that is jumped over costs a kernel's start
+// too: 64 answers to 8192 tokens in e4m3 took 44.6 us with it, 43.2 without.)
+template <int KC, bool WINDOW = true>
 FA_WALK CacheEntry cache_prefix(const CacheParams& p, int s) {
   CacheEntry n;
   int end, first_key = 0;
   cache_group(p, s, &n.first, &end);
   n.rows = (end - n.first) * p.G * p.T;
   n.keys = cache_clamp(cache_ld(p.p_lengths + s), p.p_cols << p.page_log2);
-  if (p.window) {
+  if (WINDOW && p.window) {
     const int least = cache_least(p, s, n.first, end);
     first_key = least == 0x7fffffff ? n.keys : n.keys - p.window + 1 + least;  // (both lengths are 2^30 at most)
   }
@@ -279,14 +281,14 @@ FA_WALK CacheEntry cache_own(const CacheParams& p, int b) {
   cache_span(&n, p.window ? (n.keys > p.T ? n.keys - p.T : 0) - p.window + 1 : 0, KC);
   return n;
 }
-template <int KC>
+template <int KC, bool WINDOW = true>
 FA_WALK CacheEntry cache_entry(const CacheParams& p, int e) {
-  return e < p.S ? cache_prefix<KC>(p, e) : cache_own<KC>(p, e - p.S);
+  return e < p.S ? cache_prefix<KC, WINDOW>(p, e) : cache_own<KC>(p, e - p.S);
 }
 
 // A place in the list: that of chunk c of the item of tile r, kv head h, entry e.  ITEM:
 // what an item counts beside its chunks, behind them.
-template <int KC, int ROWS, int ITEM>
+template <int KC, int ROWS, int ITEM, bool WINDOW = true>
 struct CacheCursor {
   int at;  // in the whole list
   int e, h, r, c;
@@ -306,7 +308,7 @@ struct CacheCursor {
     if (++h < p.Hkv) return;
     h = 0;
     while (++e < p.entries) {
-      n = cache_entry<KC>(p, e);
+      n = cache_entry<KC, WINDOW>(p, e);
       if (n.chunks || p.whole) return;  // (whole: a row that sees nothing is written by its item)
       item += p.Hkv * tiles();
     }
@@ -316,7 +318,7 @@ struct CacheCursor {
   FA_WALK void start(const CacheParams& p, int side_by_side, int entry, int first, int begin, int in) {
     bundle = side_by_side;
     e = entry;
-    n = cache_entry<KC>(p, e);
+    n = cache_entry<KC, WINDOW>(p, e);
     const int o = in / (n.chunks + ITEM);
     at = begin;
     c = in - o * (n.chunks + ITEM);
@@ -367,15 +369,15 @@ struct CacheShare {
   Cursor start;
 };
 
-template <int KC, int ROWS, int ITEM, int THREADS>
-__device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(const CacheParams& p) {
+template <int KC, int ROWS, int ITEM, int THREADS, bool WINDOW = true>
+__device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM, WINDOW>> cache_share(const CacheParams& p) {
   constexpr int WARPS = THREADS / 32;
   __shared__ long long s_sum[WARPS][3];
   __shared__ int s_found[3];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr bool PRE = ROWS == kPrefixRows;
   const int groups = p.S > p.groups ? p.S : p.groups;
-  if (p.window && groups) {
+  if (WINDOW && p.window && groups) {
 #pragma unroll 1
     for (int s = warp; s < min(groups, kCacheLeast); s += WARPS) {
       int first, end, least = 0x7fffffff;
@@ -388,14 +390,14 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
     __syncthreads();
   }
   // CTAs side by side (see cache_bundle); the other list's kernel has to know, too
-  const int pre_tiles = (PRE || p.sms) && p.groups == 1 ? cache_prefix<kPrefixKeys>(p, 0).tiles(kPrefixRows) : 1;
+  const int pre_tiles = (PRE || p.sms) && p.groups == 1 ? cache_prefix<kPrefixKeys, WINDOW>(p, 0).tiles(kPrefixRows) : 1;
   const int pre_bundle = cache_bundle(p.groups, pre_tiles, PRE ? (int)gridDim.x : p.sms), bundle = PRE ? pre_bundle : 1;
   const int each = (p.entries + THREADS - 1) / THREADS;
   const int e0 = min((int)threadIdx.x * each, p.entries), e1 = min(e0 + each, p.entries);
   long long sum[2] = {0, 0};  // work and items of this thread's entries
 #pragma unroll 1
   for (int e = e0; e < e1; ++e) {
-    const CacheEntry n = cache_entry<KC>(p, e);
+    const CacheEntry n = cache_entry<KC, WINDOW>(p, e);
     const int items = p.Hkv * (n.tiles(ROWS) / bundle);
     if (n.chunks || p.whole) sum[0] += (long long)items * (n.chunks + ITEM);
     sum[1] += items;
@@ -405,7 +407,7 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
   if (p.sms) {
 #pragma unroll 1
     for (int e = threadIdx.x; e < (PRE ? p.B : p.groups); e += THREADS) {
-      const CacheEntry n = PRE ? cache_own<kCacheKeys>(p, e) : cache_prefix<kPrefixKeys>(p, e);
+      const CacheEntry n = PRE ? cache_own<kCacheKeys>(p, e) : cache_prefix<kPrefixKeys, WINDOW>(p, e);
       if (n.chunks) other += (long long)p.Hkv * n.tiles(PRE ? kCacheRows : kPrefixRows) * (n.chunks + (PRE ? p.own_item : kPrefixItem));
     }
   }
@@ -428,7 +430,7 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
   }
   // groups that overlap can ask for more than there is room for: then there is no work
   const bool room = items <= p.max_items && total < (1 << 30);
-  CacheShare<CacheCursor<KC, ROWS, ITEM>> s;
+  CacheShare<CacheCursor<KC, ROWS, ITEM, WINDOW>> s;
   const int all = room ? (int)total : 0;
   unsigned ctas = gridDim.x;
   if (p.sms) {  // as many SMs as its part of the cost, one at least (the CTAs from there on have nothing)
@@ -446,7 +448,7 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
     int w = (int)base, i = (int)item;
 #pragma unroll 1
     for (int e = e0; e < e1; ++e) {
-      const CacheEntry n = cache_entry<KC>(p, e);
+      const CacheEntry n = cache_entry<KC, WINDOW>(p, e);
       const int own = p.Hkv * (n.tiles(ROWS) / bundle);
       if (!p.whole) p.parts.head[e] = {w, i, room ? n.chunks : 0};
       if (n.chunks) w += own * (n.chunks + ITEM);
@@ -467,7 +469,7 @@ __device__ __forceinline__ CacheShare<CacheCursor<KC, ROWS, ITEM>> cache_share(c
     int e = e0, w = (int)base, i = (int)item;
 #pragma unroll 1
     for (;; ++e) {
-      const CacheEntry n = cache_entry<KC>(p, e);
+      const CacheEntry n = cache_entry<KC, WINDOW>(p, e);
       const int own = p.Hkv * (n.tiles(ROWS) / bundle);
       const int all = n.chunks || p.whole ? own * (n.chunks + ITEM) : 0;
       if (s.begin < w + all) break;

@@ -151,12 +151,12 @@ template <int D, int DV, bool Q8, int MODS>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_cache_prefix_kernel(const CacheParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = PrefixCfg<D, DV, Q8>;
-  using Cursor = fa::CacheCursor<BN, fa::kPrefixRows, fa::kPrefixItem>;
+  using Cursor = fa::CacheCursor<BN, fa::kPrefixRows, fa::kPrefixItem, MODS != kUnmodified>;
   constexpr int NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Cursor s_walk[9];
   grid_next();  // the own keys' kernel, on the SMs that this one leaves
-  const auto share = fa::cache_share<BN, fa::kPrefixRows, fa::kPrefixItem, kThreads>(p);
+  const auto share = fa::cache_share<BN, fa::kPrefixRows, fa::kPrefixItem, kThreads, MODS != kUnmodified>(p);
   if (share.begin >= share.end || share.start.at >= share.end) return;
 
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [NS] a slot holds its tile
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto fetch_id = [&]() {
         const int key = (ld.it.n.chunk0 + ld.c) * BN + (lane & 7) * 16;
         id = -1;
-        if (key >= ld.it.n.keys || (key | page_mask) < ld.it.n.from) return;
+        if (key >= ld.it.n.keys || (MODS && (key | page_mask) < ld.it.n.from)) return;
         id = __ldg(p.p_tables + (long long)ld.it.e * p.p_cols + (key >> p.page_log2));
         if ((unsigned)id >= (unsigned)p.pages) fa::cache_bad(p.status), id = -2;
       };
@@ -339,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned all = __ballot_sync(~0u, mine);
         if constexpr (Q8) {  // codes that a bad page leaves out are 0
           if (lane < 8 && id == -2) {
+#pragma unroll 1
             for (int k = 0; k < width; ++k) st_shared_v4(smem_u32(dst + row * width) + k * 16, 0, 0, 0, 0);
             fence_async_smem();
           }
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Rows past the prefix's end or before the first key that is seen, whatever the pages hold
             // there, and what a page that was not copied leaves from an earlier tile: as keys they
             // meet a score that is masked, as values a weight of 0, for which they have to be finite.
-            const int first = ld.it.n.from - (ld.it.n.chunk0 + ld.c) * BN;
+            const int first = MODS ? ld.it.n.from - (ld.it.n.chunk0 + ld.c) * BN : 0;
             const unsigned bad = __ballot_sync(~0u, lane < 8 && id == -2);  // blocks of 16 rows
             const bool some_zero = ld.v && (valid < BN || first > 0 || bad);
             copy(some_zero ? raw_full : &full[s], slots + s * C::SLOT);
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!__all_sync(~0u, both)) break;
           const uint8_t* src = smem + C::OFF_RAW + rs * C::RAW;
           const uint32_t dst = smem_u32(slots + s * C::SLOT);
-          const int first = max(now.it.n.from - (now.it.n.chunk0 + now.c) * BN, 0);
+          const int first = MODS ? max(now.it.n.from - (now.it.n.chunk0 + now.c) * BN, 0) : 0;
           convert((now.v ? DV : D) == 128 ? 3 : 2, first, valid, src, dst);
           fence_async_smem();
           __syncwarp();
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Cursor& it = *walk;
           const int key = (it.n.chunk0 + c) * BN + r;
           ks = 0.f, vs = 1.f;
-          if (key >= it.n.keys || key < it.n.from) return;
+          if (key >= it.n.keys || (MODS && key < it.n.from)) return;
           const int id = __ldg(p.p_tables + (long long)it.e * p.p_cols + (key >> p.page_log2));
           if ((unsigned)id >= (unsigned)p.pages) return;
           const long long at = (((long long)id * p.Hkv + it.h) << p.page_log2) | (key & page_mask);
