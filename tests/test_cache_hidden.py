@@ -66,3 +66,47 @@ def test_a_bad_page_of_a_prefix_is_its_groups_alone(page, quant):
     again = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix)
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
     assert fa.fa_last_device_status() == fa.FA_OK
+
+
+def spoil(x, table, page, keys, value):
+    """``value`` in the rows of positions ``keys`` of one table."""
+    p = torch.as_tensor(keys, device="cuda")
+    x.view(torch.int16)[table.long()[p // page], :, p % page] = torch.tensor(value).to(bf).view(torch.int16).item()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("dv", [64, 128])
+def test_values_before_the_window(dv, T, value):
+    """bf16: what a window hides from all rows may be anything, wherever the window begins in a
+    chunk or a tile of keys."""
+    s = Setup([90, 41, 300], 2, 64, dv, False, 16)
+    Q = query(s, 8, T)
+    clean = s.cache.V.clone()
+    for window in (20, 21, 27, 36):
+        want = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, window=window)
+        check(s, Q, *want, window=window)
+        for table, n in zip(s.tables, s.lens):
+            spoil(s.cache.V, table, 16, list(range(n - T - window + 1)), value)
+        got = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, window=window)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        s.cache.V.copy_(clean)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("lens", [MANY, FEW])
+@pytest.mark.parametrize("dv", [64, 128])
+def test_values_of_a_prefix_before_the_window(dv, lens, value):
+    s = Setup(lens, 2, 64, dv, False, 16, [700])
+    Q = query(s, 8, 2)
+    clean = s.cache.V.clone()
+    for window, softcap in ((60, 0.0), (133, 0.0), (501, 0.0), (95, 20.0)):
+        mods = dict(window=window, softcap=softcap)
+        want = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, **mods)
+        check(s, Q, *want, **mods)
+        spoil(s.cache.V, s.p_tables[0], 16, list(range(700 + 28 - window + 1)), value)
+        got = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, **mods)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        s.cache.V.copy_(clean)

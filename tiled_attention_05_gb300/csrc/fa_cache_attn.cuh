@@ -236,7 +236,9 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
       const bool in_pool = (unsigned)id < (unsigned)p.pages;
       if (!in_pool) fa::cache_bad(p.status);
       const long long first = in_pool ? (((long long)id * p.Hkv + ld.h) << p.page_log2) | (key & page_mask) : 0;  // row in the pools
-      const int rows = in_pool ? ld.n.keys - key : 0;  // to load; the others are zero
+      // Rows [skip, rows) are loaded, the others are zero: those past the entry's end, and those before
+      // the first key that any row sees, where a value may be anything.
+      const int rows = in_pool ? ld.n.keys - key : 0, skip = ld.n.from - key;
       constexpr int KP = C::KROW / 16, VP = C::VROW / 16;  // pieces of a row
       const int kr = lane / KP, kp = lane % KP, vr = lane / VP, vp = lane % VP;  // this lane's row and piece of the first copy
       const uint8_t* ks = p.K + (first + kr) * C::KROW + kp * 16;
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
         // (rows of 64 bytes: two to a line of 128, which is what the swizzle permutes)
         return dst + C::KBYTES + (VP >= 8 ? row * C::VROW + (vp ^ sw) * 16 : (row >> 1) * 128 + ((((row & 1) << 2) | vp) ^ sw) * 16);
       };
-      if (rows >= KC) {
+      if (rows >= KC && skip <= 0) {
 #pragma unroll
         for (int k = 0; k < C::KBYTES / 512; ++k) cp16(kd + k * 512, ks + k * 512, true);
 #pragma unroll
@@ -258,16 +260,18 @@ __global__ void __launch_bounds__(kThreads, CacheCfg<D, DV, Q8, FEW>::CTAS) fa_c
       } else {
 #pragma unroll 1
         for (int k = 0; k < C::KBYTES / 512; ++k) {
-          const bool ok = kr + k * (32 / KP) < rows;
+          const int row = kr + k * (32 / KP);
+          const bool ok = row >= skip && row < rows;
           cp16(kd + k * 512, ok ? ks + k * 512 : p.K, ok);
         }
 #pragma unroll 1
         for (int k = 0; k < C::VBYTES / 512; ++k) {
-          const bool ok = vr + k * (32 / VP) < rows;
+          const int row = vr + k * (32 / VP);
+          const bool ok = row >= skip && row < rows;
           cp16(vd(k), ok ? vs + k * 512 : p.V, ok);
         }
         if constexpr (Q8) {
-          const bool ok = (lane & 15) < rows;
+          const bool ok = (lane & 15) >= skip && (lane & 15) < rows;
           cp4(dst + C::KBYTES + C::VBYTES + lane * 4, ok ? ss : p.k_scale, ok);
         }
       }
