@@ -299,9 +299,11 @@ FA_API fa_status fa_cache_read(const fa_cache_dims* dims, const fa_kv_cache* cac
  * scores as for fa_scores (distances and window count over prefix and own keys
  * together; with slopes the tables hold at most 2^24 positions); scale <= 0 selects 1/sqrt(d).  With a cache of e4m3, weights are rounded to
  * fp16 and values are taken to be below 2^40 in magnitude (beyond, a key whose value is zero may
- * be lost from L); a row at a masked place may be anything that fa_cache_write leaves.  With bf16 the weights of a prefix's keys are rounded to bf16 (where it
- * goes through the tensor cores: many rows), and values that one of a sequence's rows sees
- * have to be finite for its other rows too.
+ * be lost from L); a row at a masked place may be anything that fa_cache_write leaves.
+ * With bf16 the weights of a prefix's keys are rounded to bf16 where it goes through the
+ * tensor cores (many rows).  A NaN or an infinity among the keys and values reaches the rows
+ * that see it, and no others; but where a window hides a key of such a prefix from some of
+ * its sequences only, its value (bf16) has to be finite for all of them.
  *
  * workspace: fa_cache_attention_workspace_bytes (it asks the current device for its
  * SMs; 0 where the tables hold few positions), 256-byte aligned, contents ignored. */

@@ -110,3 +110,52 @@ def test_values_of_a_prefix_before_the_window(dv, lens, value):
         got = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, **mods)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         s.cache.V.copy_(clean)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("d, dv", [(64, 64), (128, 128), (64, 128)])
+@pytest.mark.parametrize("Hq, T", [(2, 3), (8, 4), (6, 17)])
+def test_values_that_some_rows_see(Hq, T, d, dv, value):
+    """bf16: a value of the newest tokens, or one at the window's edge, reaches those rows that see
+    it, in its channel; the others' results are as if it was not there."""
+    s = Setup([90, 41, 300, 7], 2, d, dv, False, 16)
+    Q = query(s, Hq, T)
+    clean = s.cache.V.clone()
+    for window, back in ((0, 1), (0, 2), (20, 1), (20, 20 + T // 2), (33, 34)):  # the key is the back-th from the end
+        want = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, window=window)
+        for b, n in enumerate(s.lens):
+            if n >= back:
+                spoil(s.cache.V[..., 5:6], s.tables[b], 16, [n - back], value)
+                spoil(s.cache.V[..., dv - 3:dv - 2], s.tables[b], 16, [n - back], math.nan)
+        got = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, window=window)
+        assert torch.equal(got[1], want[1])
+        for b, n in enumerate(s.lens):
+            for t in range(T):
+                far = n - T + t - (n - back)
+                sees = n >= back and n - T + t >= 0 and far >= 0 and (not window or far < window)
+                hit = torch.zeros(dv, dtype=torch.bool, device="cuda")
+                hit[[5, dv - 3]] = sees
+                assert torch.equal(got[0][b, :, t, ~hit], want[0][b, :, t, ~hit]), (window, back, b, t)
+                assert not torch.isfinite(got[0][b, :, t, hit]).any()
+        s.cache.V.copy_(clean)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("dv", [64, 128])
+def test_values_of_a_prefix_that_some_sequences_see(dv, value):
+    """bf16, a prefix of few rows: the window hides its key 650 from some sequences."""
+    lens, window = [30, 41, 42, 70, 2], 92
+    s = Setup(lens, 2, 128, dv, False, 16, [700])
+    Q = query(s, 4, 1)
+    want = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, window=window)
+    check(s, Q, *want, window=window)
+    spoil(s.cache.V[..., 7:8], s.p_tables[0], 16, [650], value)
+    got = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, window=window)
+    hit = torch.zeros(dv, dtype=torch.bool, device="cuda")
+    hit[7] = True
+    assert torch.equal(got[1], want[1]) and torch.equal(got[0][..., ~hit], want[0][..., ~hit])
+    for b, n in enumerate(lens):
+        sees = 700 + n - 1 - 650 < window
+        assert (~torch.isfinite(got[0][b, :, 0, 7]) if sees else got[0][b, :, 0, 7] == want[0][b, :, 0, 7]).all(), b
