@@ -302,8 +302,7 @@ FA_API fa_status fa_cache_read(const fa_cache_dims* dims, const fa_kv_cache* cac
  * be lost from L); a row at a masked place may be anything that fa_cache_write leaves.
  * With bf16 the weights of a prefix's keys are rounded to bf16 where it goes through the
  * tensor cores (many rows).  A NaN or an infinity among the keys and values reaches the rows
- * that see it, and no others; but where a window hides a key of such a prefix from some of
- * its sequences only, its value (bf16) has to be finite for all of them.
+ * that see it, and no others.
  *
  * workspace: fa_cache_attention_workspace_bytes (it asks the current device for its
  * SMs; 0 where the tables hold few positions), 256-byte aligned, contents ignored. */

@@ -159,3 +159,38 @@ def test_values_of_a_prefix_that_some_sequences_see(dv, value):
     for b, n in enumerate(lens):
         sees = 700 + n - 1 - 650 < window
         assert (~torch.isfinite(got[0][b, :, 0, 7]) if sees else got[0][b, :, 0, 7] == want[0][b, :, 0, 7]).all(), b
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("lens, starts, Hq, Hkv, T, d, dv, page", [
+    ([30, 41, 42, 70, 2, 300] * 8, None, 8, 2, 1, 128, 128, 16),    # several tiles of rows
+    ([30, 41, 42, 70, 2, 300], None, 8, 1, 1, 64, 128, 256),        # one: two parts of even and odd key tiles
+    ([38, 45], None, 32, 2, 9, 128, 64, 64),                        # rows of one sequence differ, too
+    ([30, 45, 300] * 60, list(range(0, 181, 3)), 64, 8, 1, 64, 64, 32),  # several items a CTA
+    ([30, 45, 300] * 60, list(range(0, 181, 3)), 128, 8, 1, 128, 128, 32),
+])
+def test_values_of_a_prefix_that_some_rows_see(lens, starts, Hq, Hkv, T, d, dv, page, softcap, value):
+    """bf16, prefixes of many rows: keys at the edges of the rows' windows, in several tiles."""
+    window, groups = 292, len(starts) - 1 if starts else 1
+    s = Setup(lens, Hkv, d, dv, False, page, [700] * groups, starts)
+    Q = query(s, Hq, T)
+    mods = dict(window=window, softcap=softcap)
+    want = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, **mods)
+    check(s, Q, *want, **mods)
+    keys = {5: 409, 8: 450, dv - 1: 450, 0: 511, 33: 512, 40: 699}  # channel: key
+    hurt = [g for g in range(groups) if groups == 1 or g % 7 == 3]
+    for g in hurt:
+        for c, key in keys.items():
+            spoil(s.cache.V[..., c:c + 1], s.p_tables[g], page, [key], value)
+    got = fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, **mods)
+    assert torch.equal(got[1], want[1])
+    hit = torch.zeros(len(lens), T, dv, dtype=torch.bool, device="cuda")
+    for b, n in enumerate(lens):
+        for t in range(T):
+            for c, key in keys.items():
+                hit[b, t, c] = s.group(b) in hurt and n - T + t >= 0 and 700 + n - T + t - key < window
+    hit = hit[:, None].expand_as(got[0])
+    assert hit.any() and torch.equal(got[0][~hit], want[0][~hit])
+    assert not torch.isfinite(got[0][hit]).any()

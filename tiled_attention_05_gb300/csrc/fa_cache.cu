@@ -575,16 +575,18 @@ fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache
   p.whole = s.whole;
   fa::CacheJoin j = {};
   j.pre = parts_of(s.pre);
+  fa::CacheParams pre = {};
   if (s.apart) {
     p.sms = fa::sm_count();
     p.groups = S;
     p.per_sm = fa::cache_ctas(z.quantised, fa::cache_few(p.G * p.T, false));
     p.chunk_cost = fa::cache_chunk_cost(z.d, z.dv, z.quantised);
-    fa::CacheParams pre = p;
+    pre = p;
     pre.parts = j.pre;
     pre.entries = S;
     pre.min_chunks = fa::kPrefixMinChunks;
     pre.max_items = (int)s.pre.items;
+    pre.look = reinterpret_cast<int*>(ws + s.look);
     err = z.quantised ? fa::launch_cache_prefix_e4m3(pre, z.d, z.dv, s.pre.grid, st)
                       : fa::launch_cache_prefix_bf16(pre, z.d, z.dv, s.pre.grid, st);
     if (err != cudaSuccess) return FA_ERR_CUDA;
@@ -596,6 +598,8 @@ fa_status fa_cache_attention(const fa_cache_dims* dims, const fa_kv_cache* cache
   p.max_items = (int)s.list.items;
   err = z.quantised ? fa::launch_cache_attn_e4m3(p, z.d, z.dv, s.list.grid, st)
                     : fa::launch_cache_attn_bf16(p, z.d, z.dv, s.list.grid, st);
+  if (err == cudaSuccess && s.apart && !z.quantised && p.window)
+    err = fa::launch_cache_prefix_careful(pre, z.d, z.dv, s.pre.grid, st);
   if (s.whole) return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
   j.p = p;
   j.p.S = S;

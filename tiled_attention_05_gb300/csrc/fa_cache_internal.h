@@ -87,6 +87,7 @@ struct CacheParams {
   int whole;       // items are not split (kCacheWhole)
   Divide by_T, by_GT;  // rows of a head, of a sequence
   int max_items;   // that the workspace has slots for
+  int* look;       // [CTAs] prefixes in bf16 with a window: whether the results hold a NaN or an infinity
   int capped, min_chunks;
   float scale_log2;
   CapParams cap;
@@ -112,6 +113,8 @@ cudaError_t launch_cache_attn_e4m3(const CacheParams& p, int d, int dv, int grid
 cudaError_t launch_cache_attn_bf16(const CacheParams& p, int d, int dv, int grid, cudaStream_t stream);
 cudaError_t launch_cache_prefix_e4m3(const CacheParams& p, int d, int dv, int grid, cudaStream_t stream);
 cudaError_t launch_cache_prefix_bf16(const CacheParams& p, int d, int dv, int grid, cudaStream_t stream);
+// After the prefixes' kernel, with a window: the shares that it marked in `look` again (bf16).
+cudaError_t launch_cache_prefix_careful(const CacheParams& p, int d, int dv, int grid, cudaStream_t stream);
 cudaError_t launch_cache_join(const CacheJoin& j, int dv, cudaStream_t stream);
 
 // Keys of a chunk, the unit of the walk: what one warp holds in one stage of its ring.
@@ -150,6 +153,7 @@ struct CacheShape {
   bool apart;      // prefixes are a list of their own (`pre`); else one list holds all
   CacheList list;  // the own keys' (and the prefixes')
   CacheList pre;
+  size_t look;     // byte offset
   size_t total;    // bytes
 };
 // A prefix's tiles of `rows` rows: those of its sequences' rows, and one a group for the
@@ -190,6 +194,7 @@ inline CacheShape cache_shape(long long B, long long Hkv, long long rows, int dv
         kCacheMinChunks, cache_item(few), ctas);
     s.pre = s.list;
   }
+  s.look = take(s.apart && !quantised ? s.pre.grid * sizeof(int) : 0);
   s.total = s.whole ? 0 : at;
   return s;
 }

@@ -34,6 +34,7 @@
 // in the registers' form too, its code for each four columns made a prefix with slopes alone
 // take 70 us for 39.)
 #pragma once
+#include <climits>
 #include <cstdint>
 #include <type_traits>
 
@@ -66,13 +67,14 @@ struct PrefixCfg {
   static constexpr int OFF_RAW = OFF_SLOT + NS * SLOT;
   static constexpr int OFF_SCALES = OFF_RAW + NRAW * RAW;
   static constexpr int OFF_BAR = OFF_SCALES + SCALES;
-  static constexpr int OFF_ROW = OFF_BAR + 256;  // (the barriers take 8 (2 NS + 15) + 8 bytes)
-  static constexpr int SMEM = OFF_ROW + 256;
+  static constexpr int OFF_ROW = OFF_BAR + 256;  // (the barriers take 8 (2 NS + 19) + 8 bytes)
+  static constexpr int OFF_SEEN = OFF_ROW + 256;
+  static constexpr int SMEM = OFF_SEEN + (Q8 ? 0 : 2 * (DV + 1) * 4);
   // The softmax looks for V_j and K_{j+1} on the MMA thread's behalf (142 us of 256 rows x 4 over
   // 32768 keys, 151 without), unless slots are few: then it would wait for a K that is late.
   static constexpr bool VOUCHED = NS > 4;
   // (V_j leaves its slot after S_A(j + 1): K_{j+1} needs another one)
-  static_assert(NS >= 3 && NS <= 8 && SMEM <= (226 << 10), "shared memory");
+  static_assert(NS >= 3 && NS <= 6 && SMEM <= (226 << 10), "shared memory");
 };
 
 // mbar_wait with a suspend-time hint: a thread that finds the phase incomplete sleeps until it
@@ -147,7 +149,15 @@ __device__ __forceinline__ void cap_quad_of(const fa::CapParams& c, uint64_t& a,
   b = f2_mul(b, tb);
 }
 
-template <int D, int DV, bool Q8, int MODS>
+// bf16 with a window: a NaN or an infinity among the values of a tile reaches rows that do not see it,
+// through their weights of 0.  A CTA in whose results is one says so in the workspace, and the kernel
+// after it (CAREFUL), whose other CTAs end at once, goes through that share again: in
+// tiles that not all rows see whole it replaces such values by 0, and notes the last key with one
+// in each channel.  A row sees a prefix from some key on to its end, so that this key says
+// whether it saw any: then its result there is NaN.  (64 answers of 16 to 1000 to 8192 tokens,
+// window 4096: 66 us, 101 with the loader looking for them at once, 68 without any of this; 16 to each of
+// 8 prompts of 2001, heads of 64, window 1000: 59, 94 and 56.)
+template <int D, int DV, bool Q8, int MODS, bool CAREFUL>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_cache_prefix_kernel(const CacheParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = PrefixCfg<D, DV, Q8>;
@@ -155,9 +165,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Cursor s_walk[9];
+  constexpr bool kLooks = !Q8 && MODS != kUnmodified && !CAREFUL;
   grid_next();  // the own keys' kernel, on the SMs that this one leaves
+  if constexpr (CAREFUL) {
+    grid_previous();
+    if (p.look[blockIdx.x] == 0) return;
+  }
   const auto share = fa::cache_share<BN, fa::kPrefixRows, fa::kPrefixItem, kThreads, MODS != kUnmodified>(p);
-  if (share.begin >= share.end || share.start.at >= share.end) return;
+  if (share.begin >= share.end || share.start.at >= share.end) {
+    if (kLooks && p.window && threadIdx.x == 0) p.look[blockIdx.x] = 0;
+    return;
+  }
 
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [NS] a slot holds its tile
   uint64_t* empty = full + NS;     // [NS]
@@ -167,13 +185,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* o_done = p_full + 2;   // [2]
   uint64_t* raw_full = o_done + 2;    // [3] a raw buffer holds its codes (bf16: [0], a tile's rows have come, before zeros go to some)
   uint64_t* raw_empty = raw_full + 3;  // [3]
-  uint64_t* drain = raw_empty + 3;
+  uint64_t* found_full = raw_empty + 3;    // [2] see found_of
+  uint64_t* found_free = found_full + 2;   // [2]
+  uint64_t* drain = found_free + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t* s_row = smem + C::OFF_ROW;
+  // CAREFUL: two buffers, for items in turn, of the last key with a NaN or an infinity in each channel,
+  // and behind the channels the number of them.
+  auto found_of = [&](int item) { return reinterpret_cast<int*>(smem + C::OFF_SEEN) + (item & 1) * (DV + 1); };
+  volatile int* not_finite = found_of(0);  // (not CAREFUL) a row's result has a NaN or an infinity
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     *abort_flag = (smem_u32(smem) & 1023u) ? 1 : 0;  // swizzled tiles need 1024 B alignment
+    if (kLooks) *not_finite = 0;
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], Q8 ? kLoaders / 32 : 1);
       mbar_init(&empty[s], 1);
@@ -187,6 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 128);
       mbar_init(&o_done[x], 1);
+      mbar_init(&found_full[x], 1);
+      mbar_init(&found_free[x], 256);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -360,9 +387,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (!Q8) {
         if (warp == 1) {
           int zeroed = 0;  // tiles of values, in whose rows zeros are written
+          int items = 0, all_from = 0;  // of the share so far; first key that all rows of the item's group see
           bool more = true;
+          auto begin_item = [&]() {
+            if (!__all_sync(~0u, wait_for(&found_free[items & 1], ((items >> 1) & 1) ^ 1, abort_flag))) return false;
+            int* found = found_of(items);
+            for (int k = lane; k <= DV; k += 32) found[k] = k < DV ? -1 : 0;
+            int first, end, most = 0;
+            fa::cache_group(p, ld.it.e, &first, &end);
+            for (int b = first + lane; b < end; b += 32) most = max(most, fa::cache_length(p, b));
+            all_from = ld.it.n.keys + __reduce_max_sync(~0u, most) - p.window;  // (the furthest row is the last of the longest)
+            __syncwarp();
+            return true;
+          };
           fetch_id();
           while (ok && more) {
+            if (CAREFUL && !ld.v && ld.c == ld.m.c0 && !begin_item()) break;
             const int s = ld.u % NS, valid = ld.it.n.keys - (ld.it.n.chunk0 + ld.c) * BN;
             if (!__all_sync(~0u, wait_for(&empty[s], ((ld.u / NS) & 1) ^ 1, abort_flag))) break;
             // Rows past the prefix's end or before the first key that is seen, whatever the pages hold
@@ -370,9 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // meet a score that is masked, as values a weight of 0, for which they have to be finite.
             const int first = MODS ? ld.it.n.from - (ld.it.n.chunk0 + ld.c) * BN : 0;
             const unsigned bad = __ballot_sync(~0u, lane < 8 && id == -2);  // blocks of 16 rows
-            const bool some_zero = ld.v && (valid < BN || first > 0 || bad);
-            copy(some_zero ? raw_full : &full[s], slots + s * C::SLOT);
-            if (some_zero) {
+            const int all = CAREFUL ? min(all_from - (ld.it.n.chunk0 + ld.c) * BN, min(valid, BN)) : 0;
+            const bool look = ld.v && (valid < BN || first > 0 || bad || all > 0);
+            copy(look ? raw_full : &full[s], slots + s * C::SLOT);
+            if (look) {
               ok = __all_sync(~0u, wait_for(raw_full, zeroed++ & 1, abort_flag));
               auto zero = [&](int row0, int row1) {
                 for (int k = lane; k < (row1 - row0) * (DV / 8); k += 32) {
@@ -384,9 +425,34 @@ __global__ void __launch_bounds__(kThreads, 1)
               zero(valid, BN);
 #pragma unroll 1
               for (unsigned b = bad; b; b &= b - 1) zero((__ffs(b) - 1) * 16, __ffs(b) * 16);
+              if constexpr (CAREFUL) {  // rows that some of the item's do not see
+                __syncwarp();
+                int* found = found_of(items);
+#pragma unroll 4
+                for (int k = max(first, 0) * (DV / 8) + lane; k < all * (DV / 8); k += 32) {
+                  const int row = k / (DV / 8), chunk = k % (DV / 8);
+                  const uint32_t at = (chunk >> 3) * (BN * 128) + sw128_offset(row, chunk & 7);
+                  const float4 v = ld_shared_f4(slots + s * C::SLOT + at);
+                  const uint32_t w[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
+                  uint32_t b[4];
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) b[y] = __vcmpeq2(w[y] & 0x7f807f80u, 0x7f807f80u);
+                  if (!(b[0] | b[1] | b[2] | b[3])) continue;
+                  st_shared_v4(smem_u32(slots + s * C::SLOT) + at, w[0] & ~b[0], w[1] & ~b[1], w[2] & ~b[2], w[3] & ~b[3]);
+                  atomicAdd(&found[DV], 1);
+#pragma unroll 1
+                  for (int y = 0; y < 8; ++y)
+                    if ((b[y >> 1] >> (16 * (y & 1))) & 1u) atomicMax(&found[chunk * 8 + y], (ld.it.n.chunk0 + ld.c) * BN + row);
+                }
+              }
               fence_async_smem();
               __syncwarp();
               if (lane == 0) mbar_arrive(&full[s]);
+            }
+            if (CAREFUL && ld.v && ld.c + 1 == ld.m.c1) {  // all of the item's values have been looked at
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&found_full[items & 1]);
+              ++items;
             }
             more = step(ld);
             if (more && !ld.v) fetch_id();
@@ -465,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float NEG_INF = -__int_as_float(0x7f800000);
     int ns = 0, no = 0, nb = 0;  // phases waited for; scale buffers written
     int units = 0;               // ring position of the item's first K
+    [[maybe_unused]] int items = 0;  // of the share so far
     bool ok = run;
     // Loads from TMEM are a warp's, and the barrier that hands the scales round is the
     // tile's: those who meet there leave together when one of them gave up.
@@ -556,9 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float a = lg2(fmaxf(vs, 0x1p-69f));  // (see fa_cache_attn.cuh)
             // A key's scale of NaN comes in with the value's, behind the cap and before the mask: the
             // cap would give it to the other keys of its four, hidden or not.
-            const bool fine = fabsf(ks) < INFINITY;
-            to[r] = fine ? ks : 0.f;
-            to[BN + r] = fine && vs == vs ? a : __int_as_float(0x7fffffff);
+            const bool finite = fabsf(ks) < INFINITY;
+            to[r] = finite ? ks : 0.f;
+            to[BN + r] = finite && vs == vs ? a : __int_as_float(0x7fffffff);
             to[2 * BN + r] = ex2(-a);
             sc = to;
             if (j + 1 < tiles) fetch_scales(c0 + (j + 1) * step);
@@ -748,8 +815,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           lim -= step * BN;
         }
         if (ok && tiles > 0) ok = agree(wait_for(&o_done[x], no++ & 1, abort_flag));
+        if (CAREFUL && ok) ok = agree(wait_for(&found_full[items & 1], (items >> 1) & 1, abort_flag));
         if (ok) {
           tc_fence_after();
+          [[maybe_unused]] int last_hidden = INT_MAX;
+          [[maybe_unused]] const int* found = found_of(items);
+          [[maybe_unused]] const bool some_found = CAREFUL && found[DV] > 0;
+          if (some_found) {
+            const Cursor it = *walk;
+            const fa::CacheRow w = fa::cache_row(p, it.n, first_row(it) + (two_tiles(it) ? x * BM : 0) + r);
+            last_hidden = it.n.keys + fa::cache_length(p, w.b) - p.T + w.t - p.window;
+          }
           const bool some = s_row[threadIdx.x - 128] != 0, none = s_row[threadIdx.x - 128] == 2 || tiles <= 0;
           const long long at = (((long long)walk->item + share.cta) * walk->bundle + share.tile) * fa::kPrefixRows + x * BM + r;
           if (some) *reinterpret_cast<float2*>(p.parts.ml + at * 2) = none ? make_float2(NEG_INF, 0.f) : make_float2(m_ref, l);
@@ -764,6 +840,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (tiles > 0) {
               tmem_ld32(tO + c * 32, o);
               tmem_wait_ld();
+            }
+            if (kLooks && p.window && tiles > 0) {
+              uint64_t none2 = 0ull;  // 0 times each: 0, or NaN
+#pragma unroll
+              for (int k = 0; k < 32; k += 2)
+                none2 = f2_fma(f2_pack(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), 0ull, none2);
+              if (f2_lo(none2) + f2_hi(none2) != 0.f && s_row[threadIdx.x - 128] == 1) *not_finite = 1;
+            }
+            if (some_found) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (found[c * 32 + k] > last_hidden) o[k] = 0x7fffffffu;
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -780,6 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           tc_fence_before();  // (the next item's first P.V into O_X follows this warpgroup's next P)
+          if (CAREFUL) mbar_arrive(&found_free[items++ & 1]);
         }
       }
       units += 2 * (walk->end(p, share.end) - walk->c);
@@ -788,19 +877,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   }
+  __syncwarp();  // (the MMA thread and the rest of its warp)
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
+    __syncwarp();
     tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0 && *abort_flag) atomicExch(p.status, DEV_TIMEOUT);
+  // (Not before the deallocation, which warp 0 does as a whole: thread 0 would come to it apart.)
+  if (kLooks && p.window && threadIdx.x == 0) p.look[blockIdx.x] = *not_finite;
 }
 
-template <int D, int DV, bool Q8, int MODS>
+template <int D, int DV, bool Q8, int MODS, bool CAREFUL>
 cudaError_t launch_mods(const CacheParams& p, int grid, cudaStream_t stream) {
   using C = PrefixCfg<D, DV, Q8>;
-  auto kernel = fa_cache_prefix_kernel<D, DV, Q8, MODS>;
+  auto kernel = fa_cache_prefix_kernel<D, DV, Q8, MODS, CAREFUL>;
   cudaError_t e = fa::allow_dynamic_smem(reinterpret_cast<const void*>(kernel), C::SMEM);
   if (e != cudaSuccess) return e;
   // The register split only balances if every thread was launched with kRegsLaunch.
@@ -814,21 +907,26 @@ cudaError_t launch_mods(const CacheParams& p, int grid, cudaStream_t stream) {
   if (!Q8 && (!fa::encode_pages_bf16(&mk, p.K, D, page, heads, page < BN ? page : BN) ||
               !fa::encode_pages_bf16(&mv, p.V, DV, page, heads, page < BN ? page : BN)))
     return cudaErrorInvalidValue;
+  if (CAREFUL) return fa::launch_next(kernel, dim3((unsigned)grid), kThreads, C::SMEM, stream, p, mk, mv);
   kernel<<<grid, kThreads, C::SMEM, stream>>>(p, mk, mv);
   return cudaGetLastError();
 }
 
-template <int D, int DV, bool Q8>
+template <int D, int DV, bool Q8, bool CAREFUL>
 cudaError_t launch_dims(const CacheParams& p, int grid, cudaStream_t stream) {
   const bool lines = p.slopes || p.window;
-  if (p.capped || (Q8 && lines)) return launch_mods<D, DV, Q8, kCapped>(p, grid, stream);
-  return lines ? launch_mods<D, DV, Q8, Q8 ? kCapped : kLines>(p, grid, stream) : launch_mods<D, DV, Q8, kUnmodified>(p, grid, stream);
+  if (p.capped || (Q8 && lines)) return launch_mods<D, DV, Q8, kCapped, CAREFUL>(p, grid, stream);
+  if constexpr (CAREFUL)
+    return launch_mods<D, DV, Q8, kLines, CAREFUL>(p, grid, stream);
+  else
+    return lines ? launch_mods<D, DV, Q8, Q8 ? kCapped : kLines, CAREFUL>(p, grid, stream)
+                 : launch_mods<D, DV, Q8, kUnmodified, CAREFUL>(p, grid, stream);
 }
 
-template <bool Q8>
+template <bool Q8, bool CAREFUL>
 cudaError_t launch_prefix(const CacheParams& p, int d, int dv, int grid, cudaStream_t stream) {
-  if (d == 64) return dv == 64 ? launch_dims<64, 64, Q8>(p, grid, stream) : launch_dims<64, 128, Q8>(p, grid, stream);
-  return dv == 64 ? launch_dims<128, 64, Q8>(p, grid, stream) : launch_dims<128, 128, Q8>(p, grid, stream);
+  if (d == 64) return dv == 64 ? launch_dims<64, 64, Q8, CAREFUL>(p, grid, stream) : launch_dims<64, 128, Q8, CAREFUL>(p, grid, stream);
+  return dv == 64 ? launch_dims<128, 64, Q8, CAREFUL>(p, grid, stream) : launch_dims<128, 128, Q8, CAREFUL>(p, grid, stream);
 }
 
 }  // namespace
