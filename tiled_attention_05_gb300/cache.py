@@ -215,7 +215,8 @@ def fa_cache_attention(Q, cache: KVCache, tables, lengths, scale: float | None =
         specs.append((slopes, "slopes", (Hq,), f32))
     _fa._check_all(device, specs)
     lib, given = _fa.load(), (O, L)
-    scores = _fa.FaCacheScores(float(scale or 0.0), float(softcap or 0.0), _fa._ptr(slopes), int(window))
+    window = max(-1, min(int(window), 2 ** 31 - 1))  # (ctypes would cut it to 32 bits)
+    scores = _fa.FaCacheScores(float(scale or 0.0), float(softcap or 0.0), _fa._ptr(slopes), window)
     handle = _fa._stream_ptr(stream, device)
     with _fa._under(stream, device):
         if O is None:
