@@ -55,7 +55,16 @@ class KVCache:
         _fa._check_all(self.device, specs)
         self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
         self._sizes = {}  # dims and workspace of the attention calls by their sizes
+        self._shape, self._dv = tuple(K.shape), V.shape[3]
+        self._where = [f for t in (K, V, k_scale, v_scale) if t is not None for f in (t.data_ptr, t.numel)]
+        self._at = [f() for f in self._where]
         self._pools = ctypes.byref(_fa.FaKVCache(K.data_ptr(), V.data_ptr(), _fa._ptr(k_scale), _fa._ptr(v_scale)))
+
+    def _struct(self):
+        """The library's fa_kv_cache.  Refused if a tensor was given other memory since."""
+        if [f() for f in self._where] != self._at:
+            raise ValueError("a pool of the cache has moved since; make another KVCache of it")
+        return self._pools
 
     def __setattr__(self, name, value):
         if name in ("K", "V", "k_scale", "v_scale") and "_pools" in self.__dict__:
@@ -74,8 +83,8 @@ class KVCache:
         return cls(K.view(dtype), V.view(dtype), *scales)
 
     def _dims(self, B, Hq, T, table_pages):
-        pages, Hkv, page, d = self.K.shape
-        return _fa.FaCacheDims(B, Hq, Hkv, T, d, self.V.shape[3], pages, page, table_pages, self.quantised)
+        pages, Hkv, page, d = self._shape
+        return _fa.FaCacheDims(B, Hq, Hkv, T, d, self._dv, pages, page, table_pages, self.quantised)
 
 
 def _table(t, name, rows):
@@ -106,10 +115,10 @@ def fa_cache_write(cache: KVCache, K, V, tables, starts, counts=None, stream=Non
     if K.dim() != 4:
         raise ValueError("K, V must be [B, Hkv, T, d]")
     B, _, T, _ = K.shape
-    _, Hkv, _, d = cache.K.shape
+    _, Hkv, _, d = cache._shape
     device = cache.device
     ks = _new_rows(K, "K", (B, Hkv, T, d), device)
-    vs = _new_rows(V, "V", (B, Hkv, T, cache.V.shape[3]), device)
+    vs = _new_rows(V, "V", (B, Hkv, T, cache._dv), device)
     n, i32 = _table(tables, "tables", B), torch.int32
     specs = [(tables, "tables", tables.shape, i32), (starts, "starts", (B,), i32)]
     if counts is not None:
@@ -117,7 +126,7 @@ def fa_cache_write(cache: KVCache, K, V, tables, starts, counts=None, stream=Non
     _fa._check_all(device, specs)
     dims, handle = cache._dims(B, 0, T, n), _fa._stream_ptr(stream, device)
     with _fa._under(stream, device):
-        code = _fa.load().fa_cache_write(ctypes.byref(dims), cache._pools, K.data_ptr(), V.data_ptr(), ks, vs,
+        code = _fa.load().fa_cache_write(ctypes.byref(dims), cache._struct(), K.data_ptr(), V.data_ptr(), ks, vs,
                                          tables.data_ptr(), starts.data_ptr(), _fa._ptr(counts), handle)
     _fa._raise(code, "fa_cache_write")
 
@@ -127,8 +136,8 @@ def fa_cache_read(cache: KVCache, tables, lengths, T: int, K=None, V=None, strea
     from lengths[b] on.  Optional preallocated K / V are written in place."""
     device = cache.device
     n, B = _table(tables, "tables", None), tables.shape[0]
-    _, Hkv, _, d = cache.K.shape
-    T, dv, bf, given = int(T), cache.V.shape[3], torch.bfloat16, (K, V)
+    _, Hkv, _, d = cache._shape
+    T, dv, bf, given = int(T), cache._dv, torch.bfloat16, (K, V)
     if T < 0:
         raise ValueError(f"T is {T}")
     specs = [(tables, "tables", tables.shape, torch.int32), (lengths, "lengths", (B,), torch.int32)]
@@ -140,7 +149,7 @@ def fa_cache_read(cache: KVCache, tables, lengths, T: int, K=None, V=None, strea
             K = torch.empty((B, Hkv, T, d), dtype=bf, device=device)
         if V is None:
             V = torch.empty((B, Hkv, T, dv), dtype=bf, device=device)
-        code = _fa.load().fa_cache_read(ctypes.byref(dims), cache._pools, tables.data_ptr(), lengths.data_ptr(),
+        code = _fa.load().fa_cache_read(ctypes.byref(dims), cache._struct(), tables.data_ptr(), lengths.data_ptr(),
                                         K.data_ptr(), V.data_ptr(), handle)
     if stream is not None:
         _fa._hand_over(device, (K, V), given)
@@ -154,8 +163,8 @@ def _attention_dims(Q, cache, tables, prefix, specs):
     if Q.dim() != 4:
         raise ValueError("Q must be [B, Hq, T, d]")
     B, Hq, T, d = Q.shape
-    if d != cache.K.shape[3]:
-        raise ValueError(f"Q has shape {tuple(Q.shape)}, the cache's keys have {cache.K.shape[3]} channels")
+    if d != cache._shape[3]:
+        raise ValueError(f"Q has shape {tuple(Q.shape)}, the cache's keys have {cache._shape[3]} channels")
     cols, i32, pre, groups, n = _table(tables, "tables", B), torch.int32, None, 0, 0
     specs.append((tables, "tables", tables.shape, i32))
     if prefix is not None:
@@ -203,7 +212,7 @@ def fa_cache_attention(Q, cache: KVCache, tables, lengths, scale: float | None =
     device, bf, f32 = cache.device, torch.bfloat16, torch.float32
     specs = [(Q, "Q", Q.shape, bf)]
     ref, nbytes, pre = _attention_dims(Q, cache, tables, prefix, specs)
-    (B, Hq, T, d), dv = Q.shape, cache.V.shape[3]
+    (B, Hq, T, d), dv = Q.shape, cache._dv
     specs.append((lengths, "lengths", (B,), torch.int32))
     if O is not None:
         specs.append((O, "O", (B, Hq, T, dv), bf))
@@ -227,7 +236,7 @@ def fa_cache_attention(Q, cache: KVCache, tables, lengths, scale: float | None =
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
         elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
-        code = lib.fa_cache_attention(ref, cache._pools, ctypes.byref(scores), pre, Q.data_ptr(), tables.data_ptr(),
+        code = lib.fa_cache_attention(ref, cache._struct(), ctypes.byref(scores), pre, Q.data_ptr(), tables.data_ptr(),
                                       lengths.data_ptr(), O.data_ptr(), L.data_ptr(), _fa._ptr(workspace),
                                       0 if workspace is None else workspace.nbytes, handle)
     if stream is not None:
