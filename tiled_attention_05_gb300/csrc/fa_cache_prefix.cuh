@@ -458,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more && !ld.v) fetch_id();
           }
           // Copies in flight have to land before the CTA leaves its shared memory.
+          if (zeroed) mbar_wait_bounded(raw_full, (zeroed - 1) & 1);  // (its slot's barrier was passed on by hand)
           for (int u = ld.u > NS ? ld.u - NS : 0; u < ld.u; ++u) mbar_wait_bounded(&full[u % NS], (u / NS) & 1);
         }
       } else {
