@@ -113,7 +113,8 @@ cudaError_t launch_cache_attn_e4m3(const CacheParams& p, int d, int dv, int grid
 cudaError_t launch_cache_attn_bf16(const CacheParams& p, int d, int dv, int grid, cudaStream_t stream);
 cudaError_t launch_cache_prefix_e4m3(const CacheParams& p, int d, int dv, int grid, cudaStream_t stream);
 cudaError_t launch_cache_prefix_bf16(const CacheParams& p, int d, int dv, int grid, cudaStream_t stream);
-// After the prefixes' kernel, with a window: the shares that it marked in `look` again (bf16).
+// bf16 with a window: the kernel, and after it, for the shares that it marked in `look`, again.
+cudaError_t launch_cache_prefix_window(const CacheParams& p, int d, int dv, int grid, cudaStream_t stream);
 cudaError_t launch_cache_prefix_careful(const CacheParams& p, int d, int dv, int grid, cudaStream_t stream);
 cudaError_t launch_cache_join(const CacheJoin& j, int dv, cudaStream_t stream);
 

@@ -33,6 +33,8 @@
 // MODS: kLines, slopes or a window (bf16), or kCapped, a cap, with or without these.  (With the cap
 // in the registers' form too, its code for each four columns made a prefix with slopes alone
 // take 70 us for 39.)
+// WINDOW: the call has one.  (Its code in all of them, though jumped over, made a prefix with slopes
+// alone take 48.5 us for 47.2: 16 answers to each of 8 prompts.)
 #pragma once
 #include <climits>
 #include <cstdint>
@@ -157,23 +159,23 @@ __device__ __forceinline__ void cap_quad_of(const fa::CapParams& c, uint64_t& a,
 // whether it saw any: then its result there is NaN.  (64 answers of 16 to 1000 to 8192 tokens,
 // window 4096: 66 us, 101 with the loader looking for them at once, 68 without any of this; 16 to each of
 // 8 prompts of 2001, heads of 64, window 1000: 59, 94 and 56.)
-template <int D, int DV, bool Q8, int MODS, bool CAREFUL>
+template <int D, int DV, bool Q8, int MODS, bool WINDOW, bool CAREFUL>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_cache_prefix_kernel(const CacheParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = PrefixCfg<D, DV, Q8>;
-  using Cursor = fa::CacheCursor<BN, fa::kPrefixRows, fa::kPrefixItem, MODS != kUnmodified>;
+  using Cursor = fa::CacheCursor<BN, fa::kPrefixRows, fa::kPrefixItem, WINDOW>;
   constexpr int NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Cursor s_walk[9];
-  constexpr bool kLooks = !Q8 && MODS != kUnmodified && !CAREFUL;
+  constexpr bool kLooks = !Q8 && WINDOW && !CAREFUL;
   grid_next();  // the own keys' kernel, on the SMs that this one leaves
   if constexpr (CAREFUL) {
     grid_previous();
     if (p.look[blockIdx.x] == 0) return;
   }
-  const auto share = fa::cache_share<BN, fa::kPrefixRows, fa::kPrefixItem, kThreads, MODS != kUnmodified>(p);
+  const auto share = fa::cache_share<BN, fa::kPrefixRows, fa::kPrefixItem, kThreads, WINDOW>(p);
   if (share.begin >= share.end || share.start.at >= share.end) {
-    if (kLooks && p.window && threadIdx.x == 0) p.look[blockIdx.x] = 0;
+    if (kLooks && threadIdx.x == 0) p.look[blockIdx.x] = 0;
     return;
   }
 
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto fetch_id = [&]() {
         const int key = (ld.it.n.chunk0 + ld.c) * BN + (lane & 7) * 16;
         id = -1;
-        if (key >= ld.it.n.keys || (MODS && (key | page_mask) < ld.it.n.from)) return;
+        if (key >= ld.it.n.keys || (WINDOW && (key | page_mask) < ld.it.n.from)) return;
         id = __ldg(p.p_tables + (long long)ld.it.e * p.p_cols + (key >> p.page_log2));
         if ((unsigned)id >= (unsigned)p.pages) fa::cache_bad(p.status), id = -2;
       };
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Rows past the prefix's end or before the first key that is seen, whatever the pages hold
             // there, and what a page that was not copied leaves from an earlier tile: as keys they
             // meet a score that is masked, as values a weight of 0, for which they have to be finite.
-            const int first = MODS ? ld.it.n.from - (ld.it.n.chunk0 + ld.c) * BN : 0;
+            const int first = WINDOW ? ld.it.n.from - (ld.it.n.chunk0 + ld.c) * BN : 0;
             const unsigned bad = __ballot_sync(~0u, lane < 8 && id == -2);  // blocks of 16 rows
             const int all = CAREFUL ? min(all_from - (ld.it.n.chunk0 + ld.c) * BN, min(valid, BN)) : 0;
             const bool look = ld.v && (valid < BN || first > 0 || bad || all > 0);
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!__all_sync(~0u, both)) break;
           const uint8_t* src = smem + C::OFF_RAW + rs * C::RAW;
           const uint32_t dst = smem_u32(slots + s * C::SLOT);
-          const int first = MODS ? max(now.it.n.from - (now.it.n.chunk0 + now.c) * BN, 0) : 0;
+          const int first = WINDOW ? max(now.it.n.from - (now.it.n.chunk0 + now.c) * BN, 0) : 0;
           convert((now.v ? DV : D) == 128 ? 3 : 2, first, valid, src, dst);
           fence_async_smem();
           __syncwarp();
@@ -607,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Cursor& it = *walk;
           const int key = (it.n.chunk0 + c) * BN + r;
           ks = 0.f, vs = 1.f;
-          if (key >= it.n.keys || (MODS && key < it.n.from)) return;
+          if (key >= it.n.keys || (WINDOW && key < it.n.from)) return;
           const int id = __ldg(p.p_tables + (long long)it.e * p.p_cols + (key >> p.page_log2));
           if ((unsigned)id >= (unsigned)p.pages) return;
           const long long at = (((long long)id * p.Hkv + it.h) << p.page_log2) | (key & page_mask);
@@ -667,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t unit2 = f2_pack(unit, unit);
               const float far0 = (float)(pos + lim - c);  // of column c
               // Of the columns only those from `from` on and before `to` count.
-              const int from = MODS && p.window ? pos + lim - c - p.window + 1 : 0, to = lim - c;
+              const int from = WINDOW ? pos + lim - c - p.window + 1 : 0, to = lim - c;
               const bool some_hidden = from > 0 || to < 32;
               if (MODS && some_hidden) {  // (a NaN there would reach the others of its four through the cap)
 #pragma unroll
@@ -743,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
             tmem_wait_ld();
             // Of the columns only those from `from` on and before `lim` count.
-            const int from = MODS && p.window ? pos + lim - p.window + 1 : 0;
+            const int from = WINDOW ? pos + lim - p.window + 1 : 0;
             const bool some_hidden = __any_sync(~0u, from > 0 || lim < BN);
             auto hide = [&](uint32_t with) {
 #pragma unroll
@@ -842,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld32(tO + c * 32, o);
               tmem_wait_ld();
             }
-            if (kLooks && p.window && tiles > 0) {
+            if (kLooks && tiles > 0) {
               uint64_t none2 = 0ull;  // 0 times each: 0, or NaN
 #pragma unroll
               for (int k = 0; k < 32; k += 2)
@@ -888,13 +890,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0 && *abort_flag) atomicExch(p.status, DEV_TIMEOUT);
   // (Not before the deallocation, which warp 0 does as a whole: thread 0 would come to it apart.)
-  if (kLooks && p.window && threadIdx.x == 0) p.look[blockIdx.x] = *not_finite;
+  if (kLooks && threadIdx.x == 0) p.look[blockIdx.x] = *not_finite;
 }
 
-template <int D, int DV, bool Q8, int MODS, bool CAREFUL>
+template <int D, int DV, bool Q8, int MODS, bool WINDOW, bool CAREFUL>
 cudaError_t launch_mods(const CacheParams& p, int grid, cudaStream_t stream) {
   using C = PrefixCfg<D, DV, Q8>;
-  auto kernel = fa_cache_prefix_kernel<D, DV, Q8, MODS, CAREFUL>;
+  auto kernel = fa_cache_prefix_kernel<D, DV, Q8, MODS, WINDOW, CAREFUL>;
   cudaError_t e = fa::allow_dynamic_smem(reinterpret_cast<const void*>(kernel), C::SMEM);
   if (e != cudaSuccess) return e;
   // The register split only balances if every thread was launched with kRegsLaunch.
@@ -913,21 +915,20 @@ cudaError_t launch_mods(const CacheParams& p, int grid, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <int D, int DV, bool Q8, bool CAREFUL>
+template <int D, int DV, bool Q8, bool WINDOW, bool CAREFUL>
 cudaError_t launch_dims(const CacheParams& p, int grid, cudaStream_t stream) {
-  const bool lines = p.slopes || p.window;
-  if (p.capped || (Q8 && lines)) return launch_mods<D, DV, Q8, kCapped, CAREFUL>(p, grid, stream);
-  if constexpr (CAREFUL)
-    return launch_mods<D, DV, Q8, kLines, CAREFUL>(p, grid, stream);
-  else
-    return lines ? launch_mods<D, DV, Q8, Q8 ? kCapped : kLines, CAREFUL>(p, grid, stream)
-                 : launch_mods<D, DV, Q8, kUnmodified, CAREFUL>(p, grid, stream);
+  constexpr int kLine = Q8 ? kCapped : kLines;
+  if (p.capped) return launch_mods<D, DV, Q8, kCapped, WINDOW, CAREFUL>(p, grid, stream);
+  if (WINDOW || p.slopes) return launch_mods<D, DV, Q8, kLine, WINDOW, CAREFUL>(p, grid, stream);
+  return launch_mods<D, DV, Q8, WINDOW ? kLine : kUnmodified, WINDOW, CAREFUL>(p, grid, stream);
 }
 
-template <bool Q8, bool CAREFUL>
+// WINDOW: p.window is not 0.
+template <bool Q8, bool WINDOW, bool CAREFUL>
 cudaError_t launch_prefix(const CacheParams& p, int d, int dv, int grid, cudaStream_t stream) {
-  if (d == 64) return dv == 64 ? launch_dims<64, 64, Q8, CAREFUL>(p, grid, stream) : launch_dims<64, 128, Q8, CAREFUL>(p, grid, stream);
-  return dv == 64 ? launch_dims<128, 64, Q8, CAREFUL>(p, grid, stream) : launch_dims<128, 128, Q8, CAREFUL>(p, grid, stream);
+  if (d == 64)
+    return dv == 64 ? launch_dims<64, 64, Q8, WINDOW, CAREFUL>(p, grid, stream) : launch_dims<64, 128, Q8, WINDOW, CAREFUL>(p, grid, stream);
+  return dv == 64 ? launch_dims<128, 64, Q8, WINDOW, CAREFUL>(p, grid, stream) : launch_dims<128, 128, Q8, WINDOW, CAREFUL>(p, grid, stream);
 }
 
 }  // namespace
