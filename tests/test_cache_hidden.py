@@ -194,3 +194,70 @@ def test_values_of_a_prefix_that_some_rows_see(lens, starts, Hq, Hkv, T, d, dv, 
     hit = hit[:, None].expand_as(got[0])
     assert hit.any() and torch.equal(got[0][~hit], want[0][~hit])
     assert not torch.isfinite(got[0][hit]).any()
+
+
+@pytest.mark.gpu
+def test_captured_windowed_prefix_is_replayed_with_other_values():
+    """Two graphs with one workspace, bf16, many rows, a window: replayed with values that are finite
+    and not, with other lengths, and the workspace's neighbours left alone."""
+    s = Setup([30, 41, 42, 70, 2, 300] * 8, 2, 128, 128, False, 16, [700])
+    Q, window = query(s, 8, 1), 292
+    lengths = s.lengths.clone()
+    need = fa.fa_cache_attention_workspace_bytes(Q, s.cache, s.tables, s.prefix)
+    ws = torch.full((need + 4096,), 0xff, dtype=torch.uint8, device="cuda")
+
+    def step():
+        return fa.fa_cache_attention(Q, s.cache, s.tables, lengths, prefix=s.prefix, window=window, workspace=ws[:need])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        graphs.append((graph, out))
+    clean, lens = s.cache.V.clone(), list(s.lens)
+    for k in range(6):
+        graph, (O, L) = graphs[k % 2]
+        s.lens = [max(n - 3 * k, 0) for n in lens]
+        lengths.copy_(torch.tensor(s.lens, dtype=torch.int32))
+        s.cache.V.copy_(clean)
+        if k % 3 == 1:
+            spoil(s.cache.V[..., 9:10], s.p_tables[0], 16, [450], math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        sees = torch.tensor([k % 3 == 1 and n > 0 and 700 + n - 1 - 450 < window for n in s.lens], device="cuda")
+        assert (torch.isfinite(O[..., 9]) != sees[:, None, None]).all()
+        O[..., 9] = O[..., 9].nan_to_num(0.0)
+        s.cache.V.copy_(clean)
+        if k % 3 != 1:
+            check(s, Q, O, L, window=window)
+        else:
+            want = fa.fa_cache_attention(Q, s.cache, s.tables, lengths, prefix=s.prefix, window=window)
+            keep = ~sees[:, None, None, None].expand_as(O) | (torch.arange(128, device="cuda") != 9)
+            assert torch.equal(O[keep], want[0][keep]) and torch.equal(L, want[1])
+    assert (ws[need:] == 0xff).all()
+    assert fa.fa_last_device_status() == fa.FA_OK
+
+
+@pytest.mark.gpu
+def test_windowed_prefixes_on_two_streams():
+    sets = [Setup([30 + k, 41, 70, 2, 300] * 8, 2, 64, 128, False, 16, [700], seed=k) for k in range(2)]
+    Qs, window = [query(s, 8, 1) for s in sets], 292
+    for s in sets:
+        spoil(s.cache.V[..., 3:4], s.p_tables[0], 16, [450], math.nan)
+    want = [fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, window=window) for s, Q in zip(sets, Qs)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [fa.fa_cache_attention(Q, s.cache, s.tables, s.lengths, prefix=s.prefix, window=window, stream=t)
+               for s, Q, t in zip(sets, Qs, streams)]
+    torch.cuda.synchronize()
+    for (O, L), (Ow, Lw), s in zip(got, want, sets):
+        assert torch.equal(O.view(torch.int16), Ow.view(torch.int16)) and torch.equal(L, Lw)
+        seen = torch.tensor([700 + n - 1 - 450 < window for n in s.lens], device="cuda")
+        assert (torch.isfinite(O[:, :, 0, 3]) != seen[:, None]).all()
