@@ -75,16 +75,8 @@ struct CacheCfg {
   static_assert(NS >= 3 && STAGE % 16 == 0);
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
@@ -107,11 +99,6 @@ __device__ __forceinline__ uint2 half4_of(uint32_t codes) {
   asm("{\n\t.reg .b16 c, u;\n\tmov.b32 {c, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
       : "=r"(r.x), "=r"(r.y)
       : "r"(codes));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 template <bool Q8>
@@ -137,14 +124,6 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Which of two bf16 are NaN or infinite: all bits of such a half.
-__device__ __forceinline__ uint32_t not_finite2(uint32_t x) { return __vcmpeq2(x & 0x7f807f80u, 0x7f807f80u); }
 
 // c * tanh(x / c) in log2 units of scores x without the softmax scale (see CapParams): by
 // the polynomial where that serves all of the warp's, else by the form for any x.

@@ -79,57 +79,14 @@ struct PrefixCfg {
   static_assert(NS >= 3 && NS <= 6 && SMEM <= (226 << 10), "shared memory");
 };
 
-// mbar_wait with a suspend-time hint: a thread that finds the phase incomplete sleeps until it
-// completes (or the hint runs out), mostly in the first try.
-__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!try_wait(bar, parity)) {
-    if (*abort) return false;
-    if (globaltimer_ns() - t0 > 2000000000ull) {
-      *abort = 1;
-      return false;
-    }
-  }
-  return true;
-}
 // Instruction descriptor, kind::f16 with fp32 D; A and B fp16 or bf16.
 __host__ __device__ constexpr uint32_t idesc(bool f16, int M, int N, int b_mn) {
   return f16 ? idesc_bf16(M, N, 0, b_mn) & ~((1u << 7) | (1u << 10)) : idesc_bf16(M, N, 0, b_mn);
-}
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 __device__ __forceinline__ uint32_t half2_of(uint32_t codes) {
   uint32_t r;
   asm("{\n\t.reg .b16 c, u;\n\tmov.b32 {c, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(codes));
   return r;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 // Four capped scores in log2 units (see CapParams): by the polynomial where that serves all
 // of the warp's, else by the form for any.
@@ -264,10 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // barrier costs the tensor pipe a round trip (see VOUCHED).
         auto issue_s = [&](int x, bool first, bool wait, bool last) -> bool {
           if (first) {
-            if (!wait_for(&q_full[x], nq[x], abort_flag)) return false;
+            if (!mbar_wait_for(&q_full[x], nq[x], abort_flag)) return false;
             nq[x] ^= 1;
           }
-          if (wait && !wait_for(&full[sk], pk, abort_flag)) return false;
+          if (wait && !mbar_wait_for(&full[sk], pk, abort_flag)) return false;
           tc_fence_after();
           const uint64_t a0 = desc_at(q_desc, x * C::Q_BYTES), b0 = desc_at(k_desc, sk * C::SLOT);
 #pragma unroll
@@ -283,9 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         };
         auto issue_pv = [&](int x, bool first, bool wait, bool last) -> bool {
-          if (!wait_for(&p_full[x], np[x], abort_flag)) return false;
+          if (!mbar_wait_for(&p_full[x], np[x], abort_flag)) return false;
           np[x] ^= 1;
-          if (wait && !wait_for(&full[sv], pv, abort_flag)) return false;
+          if (wait && !mbar_wait_for(&full[sv], pv, abort_flag)) return false;
           tc_fence_after();
           const uint64_t v0 = desc_at(v_desc, sv * C::SLOT);
 #pragma unroll
@@ -392,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int items = 0, all_from = 0;  // of the share so far; first key that all rows of the item's group see
           bool more = true;
           auto begin_item = [&]() {
-            if (!__all_sync(~0u, wait_for(&found_free[items & 1], ((items >> 1) & 1) ^ 1, abort_flag))) return false;
+            if (!__all_sync(~0u, mbar_wait_for(&found_free[items & 1], ((items >> 1) & 1) ^ 1, abort_flag))) return false;
             int* found = found_of(items);
             for (int k = lane; k <= DV; k += 32) found[k] = k < DV ? -1 : 0;
             int first, end, most = 0;
@@ -406,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           while (ok && more) {
             if (CAREFUL && !ld.v && ld.c == ld.m.c0 && !begin_item()) break;
             const int s = ld.u % NS, valid = ld.it.n.keys - (ld.it.n.chunk0 + ld.c) * BN;
-            if (!__all_sync(~0u, wait_for(&empty[s], ((ld.u / NS) & 1) ^ 1, abort_flag))) break;
+            if (!__all_sync(~0u, mbar_wait_for(&empty[s], ((ld.u / NS) & 1) ^ 1, abort_flag))) break;
             // Rows past the prefix's end or before the first key that is seen, whatever the pages hold
             // there, and what a page that was not copied leaves from an earlier tile: as keys they
             // meet a score that is masked, as values a weight of 0, for which they have to be finite.
@@ -416,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool look = ld.v && (valid < BN || first > 0 || bad || all > 0);
             copy(look ? raw_full : &full[s], slots + s * C::SLOT);
             if (look) {
-              ok = __all_sync(~0u, wait_for(raw_full, zeroed++ & 1, abort_flag));
+              ok = __all_sync(~0u, mbar_wait_for(raw_full, zeroed++ & 1, abort_flag));
               auto zero = [&](int row0, int row1) {
                 for (int k = lane; k < (row1 - row0) * (DV / 8); k += 32) {
                   const int row = row0 + k / (DV / 8), chunk = k % (DV / 8);
@@ -438,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const uint32_t w[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
                   uint32_t b[4];
 #pragma unroll
-                  for (int y = 0; y < 4; ++y) b[y] = __vcmpeq2(w[y] & 0x7f807f80u, 0x7f807f80u);
+                  for (int y = 0; y < 4; ++y) b[y] = not_finite2(w[y]);
                   if (!(b[0] | b[1] | b[2] | b[3])) continue;
                   st_shared_v4(smem_u32(slots + s * C::SLOT) + at, w[0] & ~b[0], w[1] & ~b[1], w[2] & ~b[2], w[3] & ~b[3]);
                   atomicAdd(&found[DV], 1);
@@ -491,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto issue = [&]() {  // (warp 1) the next unit's codes into their raw buffer
           if (warp != 1 || !more_ld || !ok) return;
           const int s = ld.u % NR;
-          if (!__all_sync(~0u, wait_for(&raw_empty[s], ((ld.u / NR) & 1) ^ 1, abort_flag))) {
+          if (!__all_sync(~0u, mbar_wait_for(&raw_empty[s], ((ld.u / NR) & 1) ^ 1, abort_flag))) {
             ok = false;
             return;
           }
@@ -506,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && more) {
           issue();
           const int s = now.u % NS, rs = now.u % NR, valid = min(now.it.n.keys - (now.it.n.chunk0 + now.c) * BN, BN);
-          const bool both = wait_for(&raw_full[rs], (now.u / NR) & 1, abort_flag) &&
-                            wait_for(&empty[s], ((now.u / NS) & 1) ^ 1, abort_flag);
+          const bool both = mbar_wait_for(&raw_full[rs], (now.u / NR) & 1, abort_flag) &&
+                            mbar_wait_for(&empty[s], ((now.u / NS) & 1) ^ 1, abort_flag);
           if (!__all_sync(~0u, both)) break;
           const uint8_t* src = smem + C::OFF_RAW + rs * C::RAW;
           const uint32_t dst = smem_u32(slots + s * C::SLOT);
@@ -633,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sc = to;
             if (j + 1 < tiles) fetch_scales(c0 + (j + 1) * step);
           }
-          ok = wait_for(&s_full[x], ns & 1, abort_flag);
+          ok = mbar_wait_for(&s_full[x], ns & 1, abort_flag);
           ok = agree(ok);
           if (!ok) break;
           ++ns;
@@ -644,8 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool there = true;
           if (C::VOUCHED && r == 0 && (x == 0 || step == 2)) {
             const int at = units + 2 * ((step == 2 ? x : 0) + j * step);
-            there = wait_for(&full[(at + 1) % NS], ((at + 1) / NS) & 1, abort_flag) &&
-                    (step == 2 || j + 1 >= tiles || wait_for(&full[(at + 2) % NS], ((at + 2) / NS) & 1, abort_flag));
+            there = mbar_wait_for(&full[(at + 1) % NS], ((at + 1) / NS) & 1, abort_flag) &&
+                    (step == 2 || j + 1 >= tiles || mbar_wait_for(&full[(at + 2) % NS], ((at + 2) / NS) & 1, abort_flag));
           }
           __syncwarp();
           float mt = NEG_INF, m_new, base, sum;
@@ -817,8 +774,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (there) mbar_arrive(&p_full[x]);
           lim -= step * BN;
         }
-        if (ok && tiles > 0) ok = agree(wait_for(&o_done[x], no++ & 1, abort_flag));
-        if (CAREFUL && ok) ok = agree(wait_for(&found_full[items & 1], (items >> 1) & 1, abort_flag));
+        if (ok && tiles > 0) ok = agree(mbar_wait_for(&o_done[x], no++ & 1, abort_flag));
+        if (CAREFUL && ok) ok = agree(mbar_wait_for(&found_full[items & 1], (items >> 1) & 1, abort_flag));
         if (ok) {
           tc_fence_after();
           [[maybe_unused]] int last_hidden = INT_MAX;
