@@ -256,7 +256,9 @@ FA_API fa_status fa_rotary(const fa_rotary_dims* dims, const void* Q, const void
  * fit (a page outside of the pool that is needed, a length beyond the table, starts
  * of groups that are no list of disjoint runs) reaches no memory: a row to write is
  * dropped, a row to read is zero, results of the attention for that sequence or
- * prefix are undefined, and fa_last_device_status reports FA_ERR_BAD_TABLE. */
+ * prefix are undefined, and fa_last_device_status reports FA_ERR_BAD_TABLE.  Pages that a
+ * window hides from all rows of a call are not needed: their places may hold anything.  Without
+ * a window a prefix's pages are needed as far as its length goes. */
 typedef struct {
   int B, Hq, Hkv;  /* Hq: fa_cache_attention only */
   int T;           /* write: new tokens a sequence; read: positions; attention: query rows */
@@ -297,10 +299,10 @@ FA_API fa_status fa_cache_read(const fa_cache_dims* dims, const fa_kv_cache* cac
  * then stand behind them.  A prefix's keys are read once for all its sequences.
  *
  * scores as for fa_scores (distances and window count over prefix and own keys
- * together; with slopes the tables hold at most 2^24 positions); scale <= 0 selects 1/sqrt(d).  With a cache of e4m3, weights are rounded to
- * fp16 and values are taken to be below 2^40 in magnitude (beyond, a key whose value is zero may
- * be lost from L); a row at a masked place may be anything that fa_cache_write leaves.
- * With bf16 the weights of a prefix's keys are rounded to bf16 where it goes through the
+ * together; with slopes the tables hold at most 2^24 positions); scale <= 0 selects
+ * 1/sqrt(d).  With a cache of e4m3, weights are rounded to fp16 and values are taken to be
+ * below 2^40 in magnitude (beyond, a key whose value is zero may be lost from L); a row at
+ * a masked place may be anything that fa_cache_write leaves.  With bf16 the weights of a prefix's keys are rounded to bf16 where it goes through the
  * tensor cores (many rows).  A NaN or an infinity among the keys and values reaches the rows
  * that see it, and no others.
  *

@@ -261,3 +261,17 @@ def test_windowed_prefixes_on_two_streams():
         assert torch.equal(O.view(torch.int16), Ow.view(torch.int16)) and torch.equal(L, Lw)
         seen = torch.tensor([700 + n - 1 - 450 < window for n in s.lens], device="cuda")
         assert (torch.isfinite(O[:, :, 0, 3]) != seen[:, None]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("page, window, T", [(16, 1, 1), (16, 40, 3), (128, 130, 1), (32, 31, 5)])
+def test_own_pages_before_the_window_may_be_dropped(page, window, T, quant):
+    s = Setup([300, 41, 1, 129, 700], 2, 64, 64, quant, page)
+    Q = query(s, 8, T)
+    tables = s.tables.clone()
+    for b, n in enumerate(s.lens):
+        tables[b, :max(max(n - T, 0) - window + 1, 0) // page] = -1
+    O, L = fa.fa_cache_attention(Q, s.cache, tables, s.lengths, window=window)
+    assert fa.fa_last_device_status() == fa.FA_OK
+    check(s, Q, O, L, window=window)

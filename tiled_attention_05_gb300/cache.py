@@ -208,7 +208,7 @@ def fa_cache_attention(Q, cache: KVCache, tables, lengths, scale: float | None =
     ``prefix=(tables [S, n], lengths [S], starts [S + 1])``: sequences starts[s] ..
     starts[s + 1] - 1 share the lengths[s] positions of tables[s] in front of their own;
     their keys are read once for all of them.  Without starts one prefix serves the
-    whole batch."""
+    whole batch.  Pages that the window hides from all rows may be gone from the tables."""
     device, bf, f32 = cache.device, torch.bfloat16, torch.float32
     specs = [(Q, "Q", Q.shape, bf)]
     ref, nbytes, pre = _attention_dims(Q, cache, tables, prefix, specs)

@@ -5,7 +5,7 @@
 // operations, so HBM bounds it; the kernel's work is to keep enough loads in flight.
 // Measured, 32 / 8 heads of 128, one row each: 4 x 50000 to 65536 keys in bf16, 146 us (6.7 TB/s);
 // 32 x 8192 in e4m3, 91 us (6.1 TB/s; its start of 3 to 4 us is the rest); 4 rows each of
-// 48 x 3 to 7000, capped, 16 / 4 heads, 37 us (3.9 TB/s: items of 1 to 4 us have their
+// 48 x 3 to 7000, capped, 16 / 4 heads, 38 us (3.8 TB/s: items of 1 to 4 us have their
 // starts and ends beside them).
 //
 // Split.  The keys of all items (sequence or shared prefix, kv head, tile of 16 rows)

@@ -31,7 +31,8 @@ constexpr bool cache_few(long long rows, bool prefixes) { return rows <= 8 && !p
 constexpr int kCacheMinChunks = 8;
 constexpr int cache_item(bool few) { return few ? 8 : 16; }
 // Where no item can have more chunks than this (and there are no prefixes), a CTA takes its
-// items whole: those that begin in its share.  Then there are no parts, no workspace and
+// items whole: those that begin in its share.  What can be is what the tables hold, which the host
+// knows, not the lengths: a table kept for the longest answer is not among these.  Then there are no parts, no workspace and
 // no join.  (On the GPU, whole / in parts, us, heads of 128, bf16: 1 sequence of 100, 256, 500
 // keys 5.7 / 7.2, 7.1 / 7.1, 9.7 / 7.4; 64 of 100, 256, 500 10.2 / 12.6, 13.0 / 15.2,
 // 26.1 / 25.4; on the host it is one launch and allocation less, 6 us.)
@@ -123,8 +124,9 @@ constexpr int kCacheKeys = 16;
 
 // What an SM takes for a chunk of own keys (its bytes at ~90 a ns) over a prefix's two tiles
 // of 128 keys (1.5 us at heads of 128; in e4m3 they take longer, and the own keys' rate that
-// divides best is higher), in 1024ths.  (64 answers to 8192 tokens, e4m3, at 80, 100, 110, 130,
-// 170 a ns: 47, 44, 40, 43, 49 us; 256 to 32768, bf16, at 70, 80, 90, 100: 166, 164, 165, 177.)
+// divides best is higher), in 1024ths.  One rate for each type, whatever the items' lengths: the
+// own keys' own rate falls where those are short.  (64 answers to 8192 tokens, e4m3, at 80, 100,
+// 110, 130, 170 a ns: 49, 47, 43, 43, 49 us; 256 to 32768, bf16, at 70, 80, 90, 100: 165, 164, 165, 178.)
 constexpr int cache_chunk_cost(int d, int dv, bool quantised) {
   return quantised ? kCacheKeys * (d + dv + 8) * 1024 / (110 * 1500) * 256 / (d + dv)
                    : kCacheKeys * 2 * 256 * 1024 / (90 * 1500);

@@ -5,11 +5,11 @@
 //
 // An item is (group, kv head, up to 256 rows), two tiles of 128; the list of items times
 // key tiles of 128 is cut into equal shares, one CTA an SM each.  Two tiles of rows and 128
-// keys take ~3300 cycles, where the MMAs alone take ~2200: the MMA thread bounds it (an MMA
-// takes it some 70 cycles, a commit 150).  In e4m3 they take ~5400: the chain of a tile's softmax
-// (2400) and of its turn on the MMA thread.  Measured (32 / 8 heads of 128): 1024 rows over 32768
-// keys of bf16, on the ~105 SMs that the own keys leave, 147 us; 256 over 8192 in e4m3, 33 us,
-// some 10 of them until the first scores.  Roles:
+// keys take ~3300 cycles, where the MMAs alone take ~2200 (some 64 each, the tensor pipe's own
+// time): the MMA thread bounds it, by its commits (some 150 each) and waits.  In e4m3 they take
+// ~5400: the chain of a tile's softmax (2400) and of its turn on the MMA thread.  Measured (32 / 8
+// heads of 128): 1024 rows over 32768 keys of bf16, on the ~105 SMs that the own keys leave, 151 us;
+// 256 over 8192 in e4m3, 34 us, some 10 of them until the first scores.  Roles:
 //   warp 0       issues the MMAs of both tiles in turn, S_X(j) = Q_X K_j^T and
 //                O_X += P_X(j) V_j, so that the tensor pipe runs one tile's while the
 //                softmax works on the other's (the forward's order: those of one
@@ -26,6 +26,9 @@
 //                quarter as long (short calls run it cold)
 //   dual         an item of at most 128 rows: both tiles are its rows, A over the even key tiles
 //                and B over the odd ones, with a part each
+// bf16: a weight is one bf16, as in the forward: O is 2.3e-3 from 64 bits over 32768 keys, where the
+// result's own rounding is 1.7e-3.  (Two of them, as in fa_cache_attn.cuh, where HBM leaves the
+// time, would be half as many MMAs again for the thread that bounds this kernel.)
 // e4m3: as in fa_cache_attn.cuh, codes and weights meet in fp16, the key's scale
 // multiplies the score, the value's goes into the exponent.  (Codes could feed the fp8
 // pipe as they are, but then the weights would be e4m3 too: a sum of two has a weight's
@@ -72,8 +75,8 @@ struct PrefixCfg {
   static constexpr int OFF_ROW = OFF_BAR + 256;  // (the barriers take 8 (2 NS + 19) + 8 bytes)
   static constexpr int OFF_SEEN = OFF_ROW + 256;
   static constexpr int SMEM = OFF_SEEN + (Q8 ? 0 : 2 * (DV + 1) * 4);
-  // The softmax looks for V_j and K_{j+1} on the MMA thread's behalf (142 us of 256 rows x 4 over
-  // 32768 keys, 151 without), unless slots are few: then it would wait for a K that is late.
+  // The softmax looks for V_j and K_{j+1} on the MMA thread's behalf (256 answers to 32768 tokens
+  // 165 us, 168 without), unless slots are few: then it would wait for a K that is late.
   static constexpr bool VOUCHED = NS > 4;
   // (V_j leaves its slot after S_A(j + 1): K_{j+1} needs another one)
   static_assert(NS >= 3 && NS <= 6 && SMEM <= (226 << 10), "shared memory");
