@@ -34,9 +34,9 @@ METRIC = "attention fwd+bwd TFLOP/s (bf16, 1×GB300) and % of dense BF16 tensor 
 # capture of it on each workload listed.  Valid only for the kernel code it was
 # taken on (comments aside): reported as null once that changes.
 NCU_TRAFFIC = {
-    "gqa_B2_H32x8_T8192_d128_causal": {"bytes": 728187648 + 348864768, "source_sha256_16": "e97adf2d6ec1c42b"},
-    "swa_B1_H32x8_T8192_W2080_d128": {"bytes": 335203072 + 139809536, "source_sha256_16": "e97adf2d6ec1c42b"},
-    "gqa_B1_H32x8_Tq4096_Tk8032_d128": {"bytes": 288700672 + 130297856, "source_sha256_16": "e97adf2d6ec1c42b"},
+    "gqa_B2_H32x8_T8192_d128_causal": {"bytes": 723874304 + 347893504, "source_sha256_16": "3eb684ce039995af"},
+    "swa_B1_H32x8_T8192_W2080_d128": {"bytes": 332034816 + 137523456, "source_sha256_16": "3eb684ce039995af"},
+    "gqa_B1_H32x8_Tq4096_Tk8032_d128": {"bytes": 288274432 + 129947136, "source_sha256_16": "3eb684ce039995af"},
 }
 TRAFFIC_SOURCES = ("tiled_attention_05_gb300/csrc/fa_bwd.cu", "tiled_attention_05_gb300/csrc/fa_bwd_kernel.cuh",
                    "tiled_attention_05_gb300/csrc/sm103_ptx.cuh", "tiled_attention_05_gb300/csrc/fa_internal.h")
