@@ -31,11 +31,11 @@ constexpr bool cache_few(long long rows, bool prefixes) { return rows <= 8 && !p
 constexpr int kCacheMinChunks = 8;
 constexpr int cache_item(bool few) { return few ? 8 : 16; }
 // Where no item can have more chunks than this (and there are no prefixes), a CTA takes its
-// items whole: those that begin in its share.  What can be is what the tables hold, which the host
-// knows, not the lengths: a table kept for the longest answer is not among these.  Then there are no parts, no workspace and
-// no join.  (On the GPU, whole / in parts, us, heads of 128, bf16: 1 sequence of 100, 256, 500
-// keys 5.7 / 7.2, 7.1 / 7.1, 9.7 / 7.4; 64 of 100, 256, 500 10.2 / 12.6, 13.0 / 15.2,
-// 26.1 / 25.4; on the host it is one launch and allocation less, 6 us.)
+// items whole: those that begin in its share.  What can be is what the tables hold, which the
+// host knows, not the lengths: a table kept for the longest answer is not among these.  Then
+// there are no parts, no workspace and no join.  (On the GPU, whole / in parts, us, heads of 128,
+// bf16: 1 sequence of 100, 256, 500 keys 5.7 / 7.2, 7.1 / 7.1, 9.7 / 7.4; 64 of 100, 256, 500
+// 10.2 / 12.6, 13.0 / 15.2, 26.1 / 25.4; on the host it is one launch and allocation less, 6 us.)
 constexpr int kCacheWhole = 16;
 // Prefixes of many rows have a list of their own (fa_cache_prefix_kernel), with items of
 // two tiles of 128 rows and chunks of 128 keys.
